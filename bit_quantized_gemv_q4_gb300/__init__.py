@@ -17,6 +17,8 @@ __all__ = [
     "LayerTable", "q4_decode_step", "q4_decode_workspace_bytes", "q4_decode_buffers",
     "q4_layer_table_release", "q4_decode_path", "q4_moe_route", "q4_moe_route_workspace_bytes",
     "q4_moe_gather", "q4_moe_gemm", "q4_moe_combine",
+    "PagedCache", "q4_rope_frequencies", "q4_paged_append", "q4_tree_attention", "q4_tree_attention_workspace_bytes",
+    "q4_tree_accept", "q4_sample", "Q4_ROPE_HALF", "Q4_ROPE_INTERLEAVED",
     "Q4_F32", "Q4_F16", "Q4_GEMV_PLAIN", "Q4_GEMV_GLU", "Q4_DECODE_NO_GRAPH", "Q4_DECODE_NO_PDL",
     "Q4_DECODE_TAGGED",
     "Q4_DECODE_PERSISTENT", "Q4_DECODE_CLUSTERED", "Q4_GEMV_EARLY_WEIGHTS",
@@ -32,6 +34,7 @@ Q4_DECODE_ATTENTION = 16
 Q4_DECODE_CLUSTERED = 32
 Q4_GEMV_EARLY_WEIGHTS = 1
 Q4_MAX_SEGMENTS = 4
+Q4_ROPE_HALF, Q4_ROPE_INTERLEAVED = 0, 1
 
 STATUS = {0: "Q4_OK", -1: "Q4_ERR_INVALID_ARG", -2: "Q4_ERR_UNSUPPORTED", -3: "Q4_ERR_MISALIGNED",
           -4: "Q4_ERR_CUDA", -5: "Q4_ERR_TIMEOUT", -6: "Q4_ERR_NO_DEVICE", -7: "Q4_ERR_DEVICE_CHECK"}
@@ -44,7 +47,8 @@ EXPORTS = ["q4_last_error", "q4_status_string", "q4_version", "q4_device_status"
            "q4_moe_route_noalloc",
            "q4_moe_gather", "q4_moe_gemm", "q4_moe_combine", "q4_gemm", "q4_prefill_workspace_bytes",
            "q4_prefill", "q4_attention_workspace_bytes", "q4_attention", "q4_gemm_workspace_bytes",
-           "q4_prefill_buffers"]
+           "q4_prefill_buffers", "q4_rope_frequencies", "q4_paged_append", "q4_tree_attention_workspace_bytes",
+           "q4_tree_attention", "q4_tree_accept", "q4_sample"]
 
 
 class Q4Error(RuntimeError):
@@ -107,6 +111,40 @@ class q4_prefill_buffers_t(ctypes.Structure):
 class q4_gemm_desc(ctypes.Structure):
     _fields_ = [("M", i32), ("X", vp), ("w", q4_linear), ("up", q4_linear), ("mode", i32), ("out_dtype", i32),
                 ("Y", vp), ("residual", vp), ("workspace", vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class q4_paged_cache(ctypes.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("page_table", vp), ("n_pages", i32), ("page_size", i32), ("n_kv_heads", i32),
+                ("head_dim", i32), ("n_seqs", i32), ("max_pages", i32)]
+
+
+class q4_rope_desc(ctypes.Structure):
+    _fields_ = [("rot_dim", i32), ("orig_len", i32)] + [(n, ctypes.c_double)
+                                                        for n in ("theta", "factor", "alpha", "beta")]
+
+
+class q4_paged_append_desc(ctypes.Structure):
+    _fields_ = [("cache", q4_paged_cache), ("ctx_len", vp), ("row_start", vp), ("rows", i32), ("positions", vp),
+                ("k", vp), ("v", vp), ("ldk", i32), ("ldv", i32), ("q", vp), ("q_out", vp), ("ldq", i32),
+                ("ldqo", i32), ("n_q_heads", i32), ("freqs", vp), ("rot_dim", i32), ("layout", i32),
+                ("amplitude", ctypes.c_float)]
+
+
+class q4_tree_attention_desc(ctypes.Structure):
+    _fields_ = [("cache", q4_paged_cache), ("ctx_len", vp), ("row_start", vp), ("rows", i32), ("mask", vp),
+                ("mask_words", i32), ("q", vp), ("out", vp), ("ldq", i32), ("ldo", i32), ("n_q_heads", i32),
+                ("scale", ctypes.c_float), ("workspace", vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class q4_tree_accept_desc(ctypes.Structure):
+    _fields_ = [("cache", q4_paged_cache), ("ctx_len", vp), ("row_start", vp), ("rows", i32), ("draft", vp),
+                ("parents", vp), ("sampled", vp), ("accepted", vp), ("path", vp), ("next_token", vp),
+                ("ctx_out", vp), ("n_layers", i32), ("layer_stride", ctypes.c_size_t)]
+
+
+class q4_sample_desc(ctypes.Structure):
+    _fields_ = [("logits", vp), ("dtype", i32), ("rows", i32), ("vocab", i32), ("ld", i32), ("temperature", vp),
+                ("top_k", vp), ("top_p", vp), ("min_p", vp), ("u", vp), ("tokens", vp), ("probs", vp)]
 
 
 _lib = None
@@ -173,6 +211,18 @@ def lib() -> ctypes.CDLL:
         L.q4_attention_workspace_bytes.argtypes = [i32, i32, i32]
         L.q4_attention.restype = st
         L.q4_attention.argtypes = [ctypes.POINTER(q4_attention_desc), vp]
+        L.q4_rope_frequencies.restype = st
+        L.q4_rope_frequencies.argtypes = [ctypes.POINTER(q4_rope_desc), vp, vp]
+        L.q4_paged_append.restype = st
+        L.q4_paged_append.argtypes = [ctypes.POINTER(q4_paged_append_desc), vp]
+        L.q4_tree_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.q4_tree_attention_workspace_bytes.argtypes = [i32]
+        L.q4_tree_attention.restype = st
+        L.q4_tree_attention.argtypes = [ctypes.POINTER(q4_tree_attention_desc), vp]
+        L.q4_tree_accept.restype = st
+        L.q4_tree_accept.argtypes = [ctypes.POINTER(q4_tree_accept_desc), vp]
+        L.q4_sample.restype = st
+        L.q4_sample.argtypes = [ctypes.POINTER(q4_sample_desc), vp]
         _lib = L
     return _lib
 
@@ -423,3 +473,146 @@ def q4_prefill_buffers(table: LayerTable, chunk: int, workspace) -> dict:
     _check(lib().q4_prefill_buffers(ctypes.byref(table.t), chunk, _ptr(workspace), ctypes.byref(b)),
            "q4_prefill_buffers")
     return {n: getattr(b, n) for n in ("n", "q", "k", "v", "act", "a")}
+
+
+# ----------------------------------------- paged cache, trees, sampling ---
+
+def _typed(t, name: str, kind: str, *, count: int = 0, stride: int = 0, width: int = 0):
+    """Device pointer of an argument of the calls below.  A tensor is checked:
+    element type, device (the current one), last dimension contiguous, and,
+    where the call says how much it reads or writes, that it holds that much.
+    ints and None pass as in _ptr."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    p = _ptr(t)
+    kinds = {"f16": (torch.float16,), "f32": (torch.float32,), "i32": (torch.int32,),
+             "w32": (torch.int32, torch.uint32), "w64": (torch.int64, torch.uint64), "raw": (t.dtype,)}[kind]
+    if t.dtype not in kinds:
+        raise ValueError(f"{name}: expected {kinds[0]}, got {t.dtype}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.dim() and t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # elements that the call can reach: rows `stride` apart, the last one `width` wide
+    need = (count - 1) * stride + width if stride else count
+    if count and need > 0:
+        have = 1 + sum((n - 1) * abs(st) for n, st in zip(t.shape, t.stride())) if t.numel() else 0
+        if have < need:
+            raise ValueError(f"{name}: holds {have} elements, the call needs {need}")
+    return p
+
+
+class PagedCache:
+    """Key / value pools fp16 [n_pages][n_kv_heads][page_size][head_dim] (for
+    q4_tree_accept one such pool per layer, layer_stride elements apart) and
+    the sequences' page table int32 [n_seqs][max_pages]; keeps the tensors."""
+
+    def __init__(self, k, v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, page_table, n_seqs: int,
+                 max_pages: int):
+        self.k, self.v, self.page_table = k, v, page_table
+        self.c = q4_paged_cache(None, None, None, n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages)
+
+    def _desc(self, n_layers: int = 1, layer_stride: int = 0) -> q4_paged_cache:
+        c = self.c
+        pool = c.n_pages * c.n_kv_heads * c.page_size * c.head_dim
+        n = (n_layers - 1) * layer_stride + pool if n_layers > 0 else 0
+        for t, name in ((self.k, "cache.k"), (self.v, "cache.v"), (self.page_table, "cache.page_table")):
+            if t is not None and not isinstance(t, int) and not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        c.k, c.v = _typed(self.k, "cache.k", "f16", count=n), _typed(self.v, "cache.v", "f16", count=n)
+        c.page_table = _typed(self.page_table, "cache.page_table", "i32", count=c.n_seqs * c.max_pages)
+        return c
+
+
+def _row_stride(t, given: int, name: str) -> int:
+    """A matrix argument's row stride: the given one, else the tensor's own (0: packed)."""
+    if given or t is None or isinstance(t, int) or t.dim() < 2:
+        return given
+    if t.dim() > 2:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: give a [rows][width] view or its row stride")
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def q4_rope_frequencies(freqs, rot_dim: int, theta: float = 1.0e6, factor: float = 1.0, orig_len: int = 0,
+                        alpha: float = 1.0, beta: float = 32.0, stream=None):
+    """freqs: int64 (or uint64) [rot_dim / 2] out, turns per position in units of 2^-64."""
+    d = q4_rope_desc(rot_dim, orig_len, theta, factor, alpha, beta)
+    _check(lib().q4_rope_frequencies(ctypes.byref(d), _typed(freqs, "freqs", "w64", count=rot_dim // 2),
+                                     _stream(stream)), "q4_rope_frequencies")
+
+
+def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=None, q_out=None, n_q_heads: int = 0,
+                    positions=None, freqs=None, rot_dim: int = 0, layout=Q4_ROPE_HALF, amplitude: float = 1.0,
+                    ldq: int = 0, ldk: int = 0, ldv: int = 0, ldqo: int = 0, stream=None):
+    """New rows' keys (rotated) and values into the paged cache, queries (rotated) into q_out."""
+    d = q4_paged_append_desc()
+    c = d.cache = cache._desc()
+    wk, wq = c.n_kv_heads * c.head_dim, n_q_heads * c.head_dim
+    ldq, ldk = _row_stride(q, ldq, "q"), _row_stride(k, ldk, "k")
+    ldv, ldqo = _row_stride(v, ldv, "v"), _row_stride(q_out, ldqo, "q_out")
+    d.ctx_len = _typed(ctx_len, "ctx_len", "i32", count=c.n_seqs)
+    d.row_start = _typed(row_start, "row_start", "i32", count=c.n_seqs + 1)
+    d.rows, d.positions = rows, _typed(positions, "positions", "i32", count=rows)
+    d.k = _typed(k, "k", "f16", count=rows, stride=ldk or wk, width=wk)
+    d.v = _typed(v, "v", "f16", count=rows, stride=ldv or wk, width=wk)
+    d.q = _typed(q, "q", "f16", count=rows, stride=ldq or wq, width=wq)
+    d.q_out = _typed(q_out, "q_out", "f16", count=rows, stride=ldqo or wq, width=wq)
+    d.ldk, d.ldv, d.ldq, d.ldqo, d.n_q_heads = ldk, ldv, ldq, ldqo, n_q_heads
+    d.freqs = _typed(freqs, "freqs", "w64", count=rot_dim // 2)
+    d.rot_dim, d.layout, d.amplitude = rot_dim, layout, amplitude
+    _check(lib().q4_paged_append(ctypes.byref(d), _stream(stream)), "q4_paged_append")
+
+
+def q4_tree_attention_workspace_bytes(head_dim: int) -> int:
+    return lib().q4_tree_attention_workspace_bytes(head_dim)
+
+
+def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_heads: int, out, workspace,
+                      workspace_bytes: int, mask=None, mask_words: int = 0, scale: float = 0.0, ldq: int = 0,
+                      ldo: int = 0, stream=None):
+    """Attention of the new rows over the cached positions and, by the mask (NULL: causal), their own."""
+    d = q4_tree_attention_desc()
+    c = d.cache = cache._desc()
+    w = n_q_heads * c.head_dim
+    ldq, ldo = _row_stride(q, ldq, "q"), _row_stride(out, ldo, "out")
+    if mask is not None and not isinstance(mask, int) and not mask.is_contiguous():
+        raise ValueError("mask must be contiguous")
+    d.ctx_len = _typed(ctx_len, "ctx_len", "i32", count=c.n_seqs)
+    d.row_start = _typed(row_start, "row_start", "i32", count=c.n_seqs + 1)
+    d.rows, d.mask, d.mask_words = rows, _typed(mask, "mask", "w32", count=rows * mask_words), mask_words
+    d.q = _typed(q, "q", "f16", count=rows, stride=ldq or w, width=w)
+    d.out = _typed(out, "out", "f16", count=rows, stride=ldo or w, width=w)
+    d.ldq, d.ldo, d.n_q_heads, d.scale = ldq, ldo, n_q_heads, scale
+    d.workspace, d.workspace_bytes = _typed(workspace, "workspace", "raw"), workspace_bytes
+    _check(lib().q4_tree_attention(ctypes.byref(d), _stream(stream)), "q4_tree_attention")
+
+
+def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, parents, sampled, accepted, path,
+                   next_token, ctx_out, n_layers: int = 1, layer_stride: int = 0, stream=None):
+    """Walks each sequence's drafted tree along the sampled tokens and moves the path's cache rows into place."""
+    d = q4_tree_accept_desc()
+    c = d.cache = cache._desc(n_layers, layer_stride)
+    d.ctx_len = _typed(ctx_len, "ctx_len", "i32", count=c.n_seqs)
+    d.row_start = _typed(row_start, "row_start", "i32", count=c.n_seqs + 1)
+    d.rows = rows
+    for n, t in (("draft", draft), ("parents", parents), ("sampled", sampled), ("path", path)):
+        setattr(d, n, _typed(t, n, "i32", count=rows))
+    for n, t in (("accepted", accepted), ("next_token", next_token), ("ctx_out", ctx_out)):
+        setattr(d, n, _typed(t, n, "i32", count=c.n_seqs))
+    d.n_layers, d.layer_stride = n_layers, layer_stride
+    _check(lib().q4_tree_accept(ctypes.byref(d), _stream(stream)), "q4_tree_accept")
+
+
+def q4_sample(logits, dtype, rows: int, vocab: int, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
+              u=None, probs=None, ld: int = 0, stream=None):
+    """One token per row of logits (see q4.h section 8); u: fp32 random numbers of [0, 1), None = greedy."""
+    ld = _row_stride(logits, ld, "logits")
+    d = q4_sample_desc(_typed(logits, "logits", "f16" if dtype == Q4_F16 else "f32", count=rows, stride=ld or vocab,
+                              width=vocab), dtype, rows, vocab, ld)
+    for n, t in (("temperature", temperature), ("top_p", top_p), ("min_p", min_p), ("u", u), ("probs", probs)):
+        setattr(d, n, _typed(t, n, "f32", count=rows))
+    d.top_k, d.tokens = _typed(top_k, "top_k", "i32", count=rows), _typed(tokens, "tokens", "i32", count=rows)
+    _check(lib().q4_sample(ctypes.byref(d), _stream(stream)), "q4_sample")

@@ -1,0 +1,396 @@
+// The paged key / value cache: rotary frequencies, the append that rotates,
+// and the acceptance of a drafted tree (q4.h 7a, 7b, 7d).
+//
+// BaseRT: optimal LLM inference on Apple Silicon with native Metal, §3.3
+// lists RoPE among the decode kernels and §3.2 preallocates the cache; the
+// pages describe neither a cache of pages nor drafted tokens.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "q4_paged.cuh"
+
+namespace q4p {
+
+// ------------------------------------------------------------- frequencies ---
+// Once per model, so plain fp64: turns f / 2 pi < 1, scaled to 2^64.  The
+// relative error of the fp64 power (a few 2^-53) times a position stays below
+// 2^-20 turns up to position 2^31.
+__global__ void rope_freq_kernel(q4_rope_desc d, uint64_t* __restrict__ out) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= d.rot_dim / 2) return;
+    double f = pow(d.theta, -2.0 * i / d.rot_dim) * 0.15915494309189533577;  // / 2 pi
+    if (d.factor > 1.0) {
+        double c = 0.0;
+        if (d.orig_len > 0) c = fmin(1.0, fmax(0.0, (d.orig_len * f - d.alpha) / (d.beta - d.alpha)));
+        f = f * c + f / d.factor * (1.0 - c);
+    }
+    out[i] = (uint64_t)rint(f * 18446744073709551616.0);
+}
+
+// ------------------------------------------------------------------ append ---
+// One block per row.  The angle of pair i is the fraction of a turn
+// (position * freqs[i]) mod 2^64, exact in integers; its upper 32 bits, signed,
+// are x 2^-31 half turns in [-1, 1), which sincospif takes without any
+// reduction (an error of 2^-32 turns = 1.5e-9 rad from the bits left off).
+// The table of a row's (cos, sin) is built once in shared memory and used by
+// every head.
+constexpr int kAppendThreads = 256;
+
+struct AppendArgs {
+    View w;
+    const int32_t* positions;
+    const uint16_t *k, *v, *q;
+    uint16_t* q_out;
+    long long ldk, ldv, ldq, ldqo;
+    int Hq;
+    const uint64_t* freqs;
+    int rot;
+    float amplitude;
+};
+
+// Sequence of a row: the number of sequences whose end is at or before it, by
+// a search 32 ways wide (one load per lane and level).  All lanes get it.
+__device__ __forceinline__ int seq_of_row(const View& w, int row, int lane) {
+    int lo = 0, len = w.S;
+    while (len > 0) {
+        const int stride = (len + 31) / 32;
+        const int i = lane * stride + stride - 1;
+        const bool before = i < len && w.row_start[lo + i + 1] <= row;
+        const int c = __popc(__ballot_sync(0xffffffffu, before));
+        lo += c * stride;
+        len = min(stride - 1, len - c * stride);
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float h2f(uint32_t w, int hi) {
+    return __half2float(__ushort_as_half((uint16_t)(hi ? w >> 16 : w)));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// kPairs: how a 16-byte chunk finds its partners.  0: neighbours (the chunk
+// holds whole pairs); 1: the halves of the rotated part are whole chunks, a
+// thread turns a chunk of each; 2: halves of any even length, element by
+// element.
+template <int D, int kPairs>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs p) {
+    __shared__ __align__(16) float2 cs[D / 2];
+    __shared__ int slot_s[2];  // sequence (-1: nobody's row), position
+    const int row = blockIdx.x, tid = threadIdx.x;
+    constexpr int NC = D / 8;
+    if (tid < 32) {
+        const int s = seq_of_row(p.w, row, tid);
+        if (tid == 0) {
+            int slot = -1, live = -1;
+            if (s < p.w.S) {
+                bool bad;
+                const Seq q = seq_of(p.w, s, bad);
+                if (bad || row < q.start || row >= q.start + q.n) {
+                    atomicOr(p.w.err, q4d::kErrDeviceCheck);
+                } else {
+                    live = s;
+                    slot = q.ctx + (row - q.start);
+                }
+            }
+            slot_s[0] = live;
+            slot_s[1] = slot;
+        }
+    }
+    const int half = p.rot / 2;
+    __syncthreads();
+    const int s = slot_s[0], slot = slot_s[1];
+    if (s < 0) return;
+    {
+        const long long pos = p.positions ? p.positions[row] : slot;
+        for (int i = tid; i < half; i += kAppendThreads) {
+            const uint64_t turn = (uint64_t)pos * p.freqs[i];
+            float sn, cn;
+            sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f, &sn, &cn);
+            cs[i] = make_float2(cn * p.amplitude, sn * p.amplitude);
+        }
+    }
+    const long long base = row_at(p.w, s, slot, 0, D);  // head 0's row
+    if (base < 0 && tid == 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
+    __syncthreads();
+    const long long head_step = (long long)p.w.div.d * D;
+    const int rc = half / 8;  // kPairs 1: chunks of a half
+    const int per = kPairs == 1 ? NC - rc : NC;  // items of a rotated head
+    const int nq = p.Hq * per, nk = p.w.H * per, nv = p.w.H * NC;
+    for (int x = tid; x < nq + nk + nv; x += kAppendThreads) {
+        if (x >= nq + nk) {  // values
+            const int y = x - nq - nk, h = y / NC, c = y % NC;
+            if (base >= 0)
+                *reinterpret_cast<uint4*>(p.w.v + base + h * head_step + 8 * c) =
+                    *reinterpret_cast<const uint4*>(p.v + row * p.ldv + (long long)h * D + 8 * c);
+            continue;
+        }
+        const bool isq = x < nq;
+        const int y = isq ? x : x - nq;
+        const int h = y / per, c = y - h * per;
+        const uint16_t* src = isq ? p.q + row * p.ldq + (long long)h * D : p.k + row * p.ldk + (long long)h * D;
+        uint16_t* dst = isq ? p.q_out + row * p.ldqo + (long long)h * D : p.w.k + base + h * head_step;
+        const bool store = isq || base >= 0;
+        if constexpr (kPairs == 1) {
+            if (c >= rc) {  // behind the rotated part
+                const int e = c + rc;
+                const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * e);
+                if (store) *reinterpret_cast<uint4*>(dst + 8 * e) = a;
+                continue;
+            }
+            const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * c);
+            const uint4 b = *reinterpret_cast<const uint4*>(src + 8 * (c + rc));
+            const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+            uint32_t oa[4], ob[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 t = *reinterpret_cast<const float4*>(&cs[8 * c + 2 * e]);
+                const float a0 = h2f(wa[e], 0), a1 = h2f(wa[e], 1), b0 = h2f(wb[e], 0), b1 = h2f(wb[e], 1);
+                oa[e] = pack2(a0 * t.x - b0 * t.y, a1 * t.z - b1 * t.w);
+                ob[e] = pack2(b0 * t.x + a0 * t.y, b1 * t.z + a1 * t.w);
+            }
+            if (store) {
+                *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+                *reinterpret_cast<uint4*>(dst + 8 * (c + rc)) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+            }
+        } else if constexpr (kPairs == 0) {
+            const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * c);
+            uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 4 * c + e;  // pair
+                if (i < half) {
+                    const float2 t = cs[i];
+                    const float x0 = h2f(w[e], 0), x1 = h2f(w[e], 1);
+                    w[e] = pack2(x0 * t.x - x1 * t.y, x1 * t.x + x0 * t.y);
+                }
+            }
+            if (store) *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            // pairs (i, i + half) cross the chunks; in place (q_out == q) a
+            // thread must own both elements of a pair, so the items are pairs
+            // here: 8 c .. 8 c + 7 of the first half, then the rest copied
+            for (int i = c; i < half; i += NC) {
+                const float a = __half2float(__ushort_as_half(src[i]));
+                const float b = __half2float(__ushort_as_half(src[i + half]));
+                const float2 t = cs[i];
+                if (store) {
+                    dst[i] = __half_as_ushort(__float2half_rn(a * t.x - b * t.y));
+                    dst[i + half] = __half_as_ushort(__float2half_rn(b * t.x + a * t.y));
+                }
+            }
+            for (int i = p.rot + c; i < D; i += NC) {
+                const uint16_t a = src[i];
+                if (store) dst[i] = a;
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------- acceptance ---
+// A cluster of 8 blocks per sequence.  Each block finds the path for itself:
+// every row in parallel looks whether it continues its parent (its token is
+// the one sampled there) and the smallest such row of a parent wins (an
+// integer minimum, the same in any order), then one thread follows the
+// pointers.  The blocks share the columns (layer, keys or values, head,
+// 16-byte chunk) to move: a thread moves its column's rows of the whole path,
+// and as paths ascend (path[i] >= i, path[j] > path[i] for j > i) no row is
+// written before the same column's later sources are past it.  ctx_out may be
+// ctx_len, so it is written after every block of the cluster has read it.
+constexpr int kAcceptThreads = 512;
+constexpr int kAcceptCluster = 8;
+constexpr int kMaxTree = 4096;
+constexpr int kMoves = 8;  // rows whose addresses are staged, and whose copies are in flight, together
+
+struct AcceptArgs {
+    View w;
+    const int32_t *draft, *parents, *sampled;
+    int32_t *accepted, *path, *next_token;
+    int32_t* ctx_out;
+    int layers, D;
+    long long layer_stride;
+};
+
+__global__ void __cluster_dims__(kAcceptCluster, 1, 1) __launch_bounds__(kAcceptThreads)
+    accept_kernel(const AcceptArgs p) {
+    __shared__ int32_t next[kMaxTree];
+    __shared__ int32_t path[kMaxTree];
+    __shared__ int len_s;
+    __shared__ long long src_s[kMoves], dst_s[kMoves];
+    const int s = blockIdx.x / kAcceptCluster, rank = blockIdx.x % kAcceptCluster, tid = threadIdx.x;
+    bool bad;
+    Seq q = seq_of(p.w, s, bad);
+    if (q.n > kMaxTree) {
+        bad = true;
+        q.n = -1;
+    }
+    if (bad && rank == 0 && tid == 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
+    const int n = q.n;
+    for (int i = tid; i < n; i += kAcceptThreads) next[i] = 0x7fffffff;
+    __syncthreads();
+    for (int i = 1 + tid; i < n; i += kAcceptThreads) {
+        const int up = p.parents[q.start + i];
+        if (up >= 0 && up < i) {
+            const int t = p.sampled[q.start + up];
+            if (t >= 0 && t == p.draft[q.start + i]) atomicMin(&next[up], i);
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int len = 0;
+        for (int at = 0; at < n; at = next[at]) path[len++] = at;  // ascending: next[at] > at
+        len_s = len;
+    }
+    __syncthreads();
+    const int len = len_s;
+    // what is moved: path[i] -> i for the rows that are not in place
+    const int cols = p.D / 8, per_layer = 2 * p.w.H * cols;
+    const long long total = (long long)p.layers * per_layer;
+    const long long head_step = (long long)p.w.div.d * p.D;
+    int first = 1;
+    while (first < len && path[first] == first) ++first;
+    for (int i0 = first; i0 < len && total > 0; i0 += kMoves) {
+        const int m = min(kMoves, len - i0);
+        __syncthreads();
+        if (tid < m) {
+            const long long a = row_at(p.w, s, q.ctx + path[i0 + tid], 0, p.D);
+            const long long b = row_at(p.w, s, q.ctx + i0 + tid, 0, p.D);
+            if (a < 0 || b < 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
+            src_s[tid] = a;
+            dst_s[tid] = a < 0 ? -1 : b;
+        }
+        __syncthreads();
+        for (long long x = (long long)rank * kAcceptThreads + tid; x < total; x += kAcceptCluster * kAcceptThreads) {
+            const long long l = x / per_layer;
+            const int y = (int)(x - l * per_layer), c = y % cols, h = y / cols % p.w.H;
+            uint16_t* pool = (y >= p.w.H * cols ? p.w.v : p.w.k) + l * p.layer_stride + h * head_step + 8 * c;
+            uint4 r[kMoves];
+#pragma unroll
+            for (int i = 0; i < kMoves; ++i)
+                if (i < m && dst_s[i] >= 0) r[i] = *reinterpret_cast<const uint4*>(pool + src_s[i]);
+#pragma unroll
+            for (int i = 0; i < kMoves; ++i)
+                if (i < m && dst_s[i] >= 0) *reinterpret_cast<uint4*>(pool + dst_s[i]) = r[i];
+        }
+    }
+    if (rank == 0 && n >= 0)
+        for (int i = tid; i < n; i += kAcceptThreads) p.path[q.start + i] = i < len ? path[i] : -1;
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (rank == 0 && tid == 0 && n >= 0) {
+        p.accepted[s] = len;
+        p.next_token[s] = len > 0 ? p.sampled[q.start + path[len - 1]] : -1;
+        p.ctx_out[s] = q.ctx + len;
+    }
+}
+
+}  // namespace q4p
+
+using namespace q4i;
+
+extern "C" q4_status q4_rope_frequencies(const q4_rope_desc* desc, uint64_t* freqs, q4_stream_t stream) {
+    clear_error();
+    if (!desc || !freqs) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    const q4_rope_desc& d = *desc;
+    if (d.rot_dim < 2 || d.rot_dim > 1024 || d.rot_dim % 2)
+        return fail(Q4_ERR_INVALID_ARG, "rot_dim=%d (even, 2 .. 1024)", d.rot_dim);
+    if (!(d.theta > 1.0) || !(d.theta < INFINITY) || !(d.factor >= 1.0) || !(d.factor < INFINITY) || d.orig_len < 0)
+        return fail(Q4_ERR_INVALID_ARG, "theta=%g factor=%g orig_len=%d", d.theta, d.factor, d.orig_len);
+    if (d.factor > 1.0 && d.orig_len > 0 && !(d.alpha >= 0.0 && d.beta > d.alpha && d.beta < INFINITY))
+        return fail(Q4_ERR_INVALID_ARG, "alpha=%g beta=%g (0 <= alpha < beta)", d.alpha, d.beta);
+    if (reinterpret_cast<uintptr_t>(freqs) & 7u) return fail(Q4_ERR_MISALIGNED, "freqs must be 8-byte aligned");
+    const DeviceInfo* dev = nullptr;
+    const q4_status st = current_device(&dev);
+    if (st != Q4_OK) return st;
+    const int n = d.rot_dim / 2;
+    q4p::rope_freq_kernel<<<(n + 63) / 64, 64, 0, reinterpret_cast<cudaStream_t>(stream)>>>(d, freqs);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e, "q4_rope_frequencies launch");
+}
+
+extern "C" q4_status q4_paged_append(const q4_paged_append_desc* desc, q4_stream_t stream) {
+    clear_error();
+    if (!desc) return fail(Q4_ERR_INVALID_ARG, "desc is NULL");
+    q4_paged_append_desc d = *desc;
+    q4p::AppendArgs a;
+    q4_status st = paged_view(d.cache, d.ctx_len, d.row_start, d.rows, &a.w);
+    if (st != Q4_OK) return st;
+    const int D = d.cache.head_dim;
+    if (!d.k || !d.v || (d.q && !d.q_out) || (d.q_out && !d.q)) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (d.q ? d.n_q_heads < 1 : d.n_q_heads < 0) return fail(Q4_ERR_INVALID_ARG, "n_q_heads=%d", d.n_q_heads);
+    if ((long long)d.n_q_heads * D > (1 << 24) || (long long)d.cache.n_kv_heads * D > (1 << 24))
+        return fail(Q4_ERR_UNSUPPORTED, "%d query and %d kv heads", d.n_q_heads, d.cache.n_kv_heads);
+    if (d.rot_dim < 0 || d.rot_dim > D || d.rot_dim % 2) return fail(Q4_ERR_INVALID_ARG, "rot_dim=%d of %d", d.rot_dim, D);
+    if ((d.rot_dim > 0) != (d.freqs != nullptr)) return fail(Q4_ERR_INVALID_ARG, "freqs and rot_dim go together");
+    if (d.layout != Q4_ROPE_HALF && d.layout != Q4_ROPE_INTERLEAVED) return fail(Q4_ERR_INVALID_ARG, "layout=%d", (int)d.layout);
+    if (!(d.amplitude >= 0.f) || !(d.amplitude < INFINITY)) return fail(Q4_ERR_INVALID_ARG, "amplitude=%g", d.amplitude);
+    if (reinterpret_cast<uintptr_t>(d.freqs) & 7u) return fail(Q4_ERR_MISALIGNED, "freqs must be 8-byte aligned");
+    const int wk = d.cache.n_kv_heads * D, wq = d.n_q_heads * D;
+    if ((st = row_matrix("k", d.k, wk, &d.ldk)) != Q4_OK || (st = row_matrix("v", d.v, wk, &d.ldv)) != Q4_OK) return st;
+    if (d.q && ((st = row_matrix("q", d.q, wq, &d.ldq)) != Q4_OK || (st = row_matrix("q_out", d.q_out, wq, &d.ldqo)) != Q4_OK))
+        return st;
+    if (d.q == d.q_out && d.q && d.ldq != d.ldqo) return fail(Q4_ERR_INVALID_ARG, "q_out is q with another row stride");
+    const DeviceInfo* dev = nullptr;
+    if ((st = current_device(&dev)) != Q4_OK) return st;
+    if (d.rows == 0) return Q4_OK;
+    a.w.err = dev->err_word;
+    a.positions = d.positions;
+    a.k = d.k;
+    a.v = d.v;
+    a.q = d.q;
+    a.q_out = d.q_out;
+    a.ldk = d.ldk;
+    a.ldv = d.ldv;
+    a.ldq = d.ldq;
+    a.ldqo = d.ldqo;
+    a.Hq = d.q ? d.n_q_heads : 0;
+    a.freqs = d.freqs;
+    a.rot = d.rot_dim;
+    a.amplitude = d.amplitude == 0.f ? 1.f : d.amplitude;
+    // chunks of 8: neighbours always pair up within one; halves do where they
+    // are whole chunks (rot_dim a multiple of 16)
+    const int pairs = d.layout == Q4_ROPE_INTERLEAVED ? 0 : d.rot_dim % 16 == 0 ? 1 : 2;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    void (*kern)(q4p::AppendArgs) =
+        D == 128 ? (pairs == 0 ? q4p::append_kernel<128, 0> : pairs == 1 ? q4p::append_kernel<128, 1> : q4p::append_kernel<128, 2>)
+                 : (pairs == 0 ? q4p::append_kernel<64, 0> : pairs == 1 ? q4p::append_kernel<64, 1> : q4p::append_kernel<64, 2>);
+    kern<<<d.rows, q4p::kAppendThreads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e, "q4_paged_append launch");
+}
+
+extern "C" q4_status q4_tree_accept(const q4_tree_accept_desc* desc, q4_stream_t stream) {
+    clear_error();
+    if (!desc) return fail(Q4_ERR_INVALID_ARG, "desc is NULL");
+    const q4_tree_accept_desc& d = *desc;
+    q4p::AcceptArgs a;
+    q4_status st = paged_view(d.cache, d.ctx_len, d.row_start, d.rows, &a.w);
+    if (st != Q4_OK) return st;
+    if (!d.accepted || !d.next_token || !d.ctx_out || (d.rows > 0 && (!d.draft || !d.parents || !d.sampled || !d.path)))
+        return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (d.n_layers < 0 || d.n_layers > (1 << 16)) return fail(Q4_ERR_INVALID_ARG, "n_layers=%d", d.n_layers);
+    if (d.layer_stride % 8) return fail(Q4_ERR_MISALIGNED, "layer_stride must be a multiple of 8");
+    const unsigned long long pool =
+        (unsigned long long)d.cache.n_pages * d.cache.page_size * d.cache.n_kv_heads * d.cache.head_dim;
+    if (d.n_layers > 1 && d.layer_stride < pool)
+        return fail(Q4_ERR_INVALID_ARG, "layer_stride=%zu, a layer's pool has %llu elements", d.layer_stride, pool);
+    if (d.cache.n_seqs > (1 << 27)) return fail(Q4_ERR_UNSUPPORTED, "n_seqs=%d", d.cache.n_seqs);
+    const DeviceInfo* dev = nullptr;
+    if ((st = current_device(&dev)) != Q4_OK) return st;
+    a.w.err = dev->err_word;
+    a.draft = d.draft;
+    a.parents = d.parents;
+    a.sampled = d.sampled;
+    a.accepted = d.accepted;
+    a.path = d.path;
+    a.next_token = d.next_token;
+    a.ctx_out = d.ctx_out;
+    a.layers = d.n_layers;
+    a.D = d.cache.head_dim;
+    a.layer_stride = (long long)d.layer_stride;
+    q4p::accept_kernel<<<d.cache.n_seqs * q4p::kAcceptCluster, q4p::kAcceptThreads, 0,
+                         reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? Q4_OK : cuda_fail(e, "q4_tree_accept launch");
+}

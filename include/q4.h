@@ -556,6 +556,194 @@ size_t q4_attention_workspace_bytes(int n_q_heads, int head_dim, int max_seq);
  * most 8 query heads per kv head (else Q4_ERR_UNSUPPORTED). */
 q4_status q4_attention(const q4_attention_desc *desc, q4_stream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * 7. A key / value cache in pages, for several sequences at once.
+ *
+ * BaseRT §3.2 preallocates the KV cache for one sequence; the pages describe
+ * no batch.  Here the rows of all sequences live in pools of equal pages:
+ *
+ *   k, v: fp16 [n_pages][n_kv_heads][page_size][head_dim]
+ *   page_table: int32 [n_seqs][max_pages], DEVICE; position j of sequence s
+ *     is row j % page_size of page page_table[s][j / page_size].
+ *
+ * page_size is any number of positions.  A cache of q4_attention, q4_prefill
+ * or q4_decode_step ([n_kv_heads][max_seq][head_dim]) is a pool of one page
+ * of max_seq positions, so a prompt that q4_prefill cached can be attended
+ * here.  Sequences may share pages that nobody writes.
+ *
+ * The calls below work on `rows` rows of new tokens, the sequences' one after
+ * another: sequence s has rows row_start[s] .. row_start[s+1]-1 (row_start:
+ * int32 [n_seqs+1], DEVICE; a sequence may have none), and ctx_len[s] (int32,
+ * DEVICE) positions are cached before them; row i of a sequence takes
+ * position ctx_len[s] + i.  The sizes are read on the device, so a captured
+ * graph can be replayed as they change.  Rows from row_start[n_seqs] up to
+ * `rows` belong to nobody: they are neither read nor written.  A sequence
+ * whose sizes do not fit (row_start not ascending within 0..rows, ctx_len
+ * negative, more positions than max_pages * page_size) is left out, its
+ * outputs untouched, and a page number outside [0, n_pages) stands for no
+ * memory: nothing is written there and its rows read as zeros.  Both latch
+ * Q4_ERR_DEVICE_CHECK.  max_pages * page_size must stay below 2^31.
+ * ------------------------------------------------------------------------ */
+typedef struct q4_paged_cache {
+    uint16_t *k;               /* both 16-byte aligned */
+    uint16_t *v;
+    const int32_t *page_table;
+    int n_pages, page_size;
+    int n_kv_heads, head_dim;  /* head_dim 64 or 128 */
+    int n_seqs, max_pages;
+} q4_paged_cache;
+
+/* 7a. Rotary frequencies, once per model (no counterpart in the pages, which
+ * name RoPE only: BaseRT §3.3).  Pair i of the rot_dim / 2 rotated pairs turns
+ * by f_i per position, f_i = theta^(-2i/rot_dim).  For contexts longer than
+ * the trained one, factor > 1 slows the turns: with orig_len 0 all of them
+ * (f_i / factor: positions interpolated), else by parts: a pair that makes
+ * r_i = orig_len f_i / 2 pi turns over the trained context keeps f_i where
+ * r_i >= beta, takes f_i / factor where r_i <= alpha, and between them
+ * f_i (c + (1 - c) / factor) with c = (r_i - alpha) / (beta - alpha).
+ * freqs (DEVICE, uint64 [rot_dim/2], 8-byte aligned) receives f_i / 2 pi in
+ * units of 2^-64 turns: a position times that, modulo 2^64, is the angle's
+ * fraction of a turn, exact however far the position. */
+typedef struct q4_rope_desc {
+    int rot_dim;        /* 2 .. 1024, even */
+    int orig_len;       /* >= 0 */
+    double theta;       /* > 1 */
+    double factor;      /* >= 1; 1 = as trained */
+    double alpha, beta; /* 0 <= alpha < beta; read where factor > 1 and orig_len > 0 */
+} q4_rope_desc;
+
+q4_status q4_rope_frequencies(const q4_rope_desc *desc, uint64_t *freqs, q4_stream_t stream);
+
+/* 7b. q4_paged_append -- the new rows' keys, rotated, and values into the
+ * cache, and their queries, rotated, into q_out; one kernel.  For a pair
+ * (x, y) of a head and its angle a = positions[row] * f_i the rotated pair is
+ * amplitude * (x cos a - y sin a, y cos a + x sin a), in fp32 with one fp16
+ * rounding; elements rot_dim .. head_dim-1 pass through.  Pair i is elements
+ * (i, i + rot_dim/2) with Q4_ROPE_HALF (for rot_dim = head_dim the form of
+ * section 6), (2i, 2i + 1) with Q4_ROPE_INTERLEAVED.  Row strides ld* count
+ * elements, 0 = packed, multiples of 8; q, k, v, q_out 16-byte aligned.  Two
+ * rows must not meet in one place of the cache (two sequences appending to a
+ * shared page): which of them stays is not defined. */
+typedef enum q4_rope_layout { Q4_ROPE_HALF = 0, Q4_ROPE_INTERLEAVED = 1 } q4_rope_layout;
+
+typedef struct q4_paged_append_desc {
+    q4_paged_cache cache;
+    const int32_t *ctx_len;    /* [n_seqs] */
+    const int32_t *row_start;  /* [n_seqs + 1] */
+    int rows;                  /* rows of k, v, q, q_out and positions; >= 0 */
+    const int32_t *positions;  /* [rows] rotary positions, any int32; NULL = the cache position.  A drafted
+                                  tree's rows of one depth share a position */
+    const uint16_t *k, *v;     /* fp16 [rows][n_kv_heads * head_dim] */
+    int ldk, ldv;
+    const uint16_t *q;         /* fp16 [rows][n_q_heads * head_dim]; NULL = no queries */
+    uint16_t *q_out;           /* likewise; may be q itself (same stride), must not overlap it otherwise */
+    int ldq, ldqo;
+    int n_q_heads;
+    const uint64_t *freqs;     /* q4_rope_frequencies' output; NULL (with rot_dim 0) = no rotation */
+    int rot_dim;               /* even, 0 .. head_dim */
+    q4_rope_layout layout;
+    float amplitude;           /* factor on the rotated pairs (long-context scalings use one); 0 = 1 */
+} q4_paged_append_desc;
+
+q4_status q4_paged_append(const q4_paged_append_desc *desc, q4_stream_t stream);
+
+/* 7c. q4_tree_attention -- attention of the new rows over the cache, which
+ * holds their own keys and values already (7b).  Row i of sequence s sees the
+ * ctx_len[s] cached positions, and of the sequence's own rows j those whose
+ * bit j is set in its mask: bit j % 32 of mask[row * mask_words + j / 32].
+ * For a drafted tree that is the row itself and its ancestors.  mask NULL:
+ * rows 0 .. i, which is a prompt's chunk, and with one row per sequence the
+ * decoding of a batch.  a = sum_j softmax_j(scale q . k_j) v_j with the heads
+ * paired as in section 6 (any number of query heads per kv head), fp32
+ * scores, statistics and sums; the probabilities enter the value product as
+ * fp16 (error below 5e-4 * sum_j p_j |v_j|).  A row that sees nothing gets
+ * zeros.  What a row does not see never reaches it, NaN and infinities
+ * included.  q and out: fp16 [rows][n_q_heads * head_dim], strides as in 7b,
+ * 16-byte aligned; they must not overlap.  The workspace is written and read
+ * by the call's kernels; calls that can overlap need one each. */
+typedef struct q4_tree_attention_desc {
+    q4_paged_cache cache;
+    const int32_t *ctx_len, *row_start;
+    int rows;                  /* >= 0 */
+    const uint32_t *mask;      /* [rows][mask_words]; NULL = causal */
+    int mask_words;            /* >= 1 with a mask; a row j >= 32 * mask_words is seen by nobody */
+    const uint16_t *q;
+    uint16_t *out;
+    int ldq, ldo;
+    int n_q_heads;
+    float scale;               /* 0 = 1 / sqrt(head_dim) */
+    void *workspace;           /* 256-byte aligned, >= q4_tree_attention_workspace_bytes */
+    size_t workspace_bytes;
+} q4_tree_attention_desc;
+
+/* Workspace bytes for any sizes of any call with this head_dim (0 for a bad
+ * one): the partial results of the CTAs that share a row's positions. */
+size_t q4_tree_attention_workspace_bytes(int head_dim);
+
+q4_status q4_tree_attention(const q4_tree_attention_desc *desc, q4_stream_t stream);
+
+/* 7d. q4_tree_accept -- commits a drafted tree: row 0 of a sequence is its
+ * last certain token, draft[row] the token of each row, parents[row] the row
+ * (within the sequence) that it continues (-1 for row 0), and sampled[row]
+ * the token that the model chose after that row (q4_sample).  From row 0 on,
+ * the path goes to the first later row whose parent is the path's end and
+ * whose token is the one sampled there, as long as there is one (a sampled
+ * token below 0 ends it).  accepted[s] = rows on the path (>= 1; 0 for a
+ * sequence without rows), path[row_start[s] + i] = its i-th row, -1 behind
+ * it, next_token[s] = the token sampled at its end (-1 without rows),
+ * ctx_out[s] = ctx_len[s] + accepted[s] (may be ctx_len itself).  Key and
+ * value of the path's i-th row move to position ctx_len[s] + i in each of
+ * n_layers pools, layer l's at k + l * layer_stride and v + l * layer_stride
+ * (elements, a multiple of 8); n_layers 0 moves nothing.  Keys keep their
+ * rotation, which goes by depth (7b's positions).  A sequence of more than
+ * 4096 rows is left out and latches Q4_ERR_DEVICE_CHECK. */
+typedef struct q4_tree_accept_desc {
+    q4_paged_cache cache;
+    const int32_t *ctx_len, *row_start;
+    int rows;
+    const int32_t *draft, *parents, *sampled; /* [rows] */
+    int32_t *accepted;         /* [n_seqs] */
+    int32_t *path;             /* [rows] */
+    int32_t *next_token;       /* [n_seqs] */
+    int32_t *ctx_out;          /* [n_seqs] */
+    int n_layers;
+    size_t layer_stride;
+} q4_tree_accept_desc;
+
+q4_status q4_tree_accept(const q4_tree_accept_desc *desc, q4_stream_t stream);
+
+/* ------------------------------------------------------------------------ *
+ * 8. Sampling a token per row of logits (BaseRT §3.3 lists sampling among
+ *    the decode kernels; the pages print no formula).
+ *
+ * Row r orders its tokens by logit, the greater first, equal ones by index.
+ * With w_i = exp((l_i - max l) / temperature) it keeps the first top_k of
+ * them; of these the shortest beginning whose weights come to top_p of
+ * theirs together (at least one token); of these the ones with
+ * w_i >= min_p (1 is the greatest weight).  The token is the first, in that
+ * order, at which the kept weights' running sum exceeds u times their sum.
+ * prob = its share of the kept weights.  -inf and NaN logits take no part; if
+ * the greatest logit is +inf, the tokens that have it weigh 1 and all others
+ * 0; a row without any other logit gives token -1 and prob 0.  Sums are exact
+ * 64-bit integers of weights rounded to 2^-44, whatever the order.
+ * ------------------------------------------------------------------------ */
+typedef struct q4_sample_desc {
+    const void *logits;       /* [rows][vocab] of `dtype`, rows ld elements apart */
+    q4_dtype dtype;
+    int rows, vocab;          /* rows >= 0, 1 <= vocab <= 2^19 */
+    int ld;                   /* 0 = vocab */
+    const float *temperature; /* [rows]; not above 0: the greatest logit; NULL = 1 for every row */
+    const int32_t *top_k;     /* [rows]; below 1: no limit; NULL = no limit */
+    const float *top_p;       /* [rows]; 1 and above, or NaN: no limit; NULL = no limit */
+    const float *min_p;       /* [rows]; not above 0: no limit, above 1 counts as 1; NULL = no limit */
+    const float *u;           /* [rows] random numbers of [0, 1) (outside it they count as its ends);
+                                 NULL = the greatest logit of every row */
+    int32_t *tokens;          /* [rows] out */
+    float *probs;             /* [rows] out, or NULL */
+} q4_sample_desc;
+
+q4_status q4_sample(const q4_sample_desc *desc, q4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

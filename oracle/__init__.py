@@ -664,3 +664,108 @@ def moe_combine(Y, pos, weights):
             out[t] += weights[t, k] * Y[pos[t, k]]
             mag[t] += np.abs(weights[t, k] * Y[pos[t, k]])
     return out, mag
+
+
+# ------------------------------------- paged cache, drafted trees, sampling ---
+# The pages name RoPE, attention and sampling among the decode kernels (BaseRT
+# §3.3) and print no formula; the readings are the ones of include/q4.h,
+# sections 7 and 8.
+
+def rope_turns(rot_dim: int, theta: float = DEFAULT_ROPE_THETA, factor: float = 1.0, orig_len: int = 0,
+               alpha: float = 1.0, beta: float = 32.0) -> np.ndarray:
+    """Turns per position of each pair, fp64 [rot_dim / 2]."""
+    f = theta ** (-2.0 * np.arange(rot_dim // 2) / rot_dim) / (2 * np.pi)
+    if factor == 1.0:
+        return f
+    keep = np.clip((orig_len * f - alpha) / (beta - alpha), 0.0, 1.0) if orig_len else np.zeros_like(f)
+    return f * (keep + (1 - keep) / factor)
+
+
+def rope_pairs(x, positions, turns, interleaved: bool = False, amplitude: float = 1.0) -> np.ndarray:
+    """x [rows, heads, d] with the first 2 len(turns) elements of every head turned, fp64."""
+    x = np.asarray(x, np.float64)
+    rot = 2 * len(turns)
+    i = np.arange(rot // 2)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+    ang = 2 * np.pi * np.mod(np.asarray(positions, np.float64)[:, None] * turns, 1.0)
+    c, s = amplitude * np.cos(ang)[:, None], amplitude * np.sin(ang)[:, None]
+    out = x.copy()
+    out[..., a] = x[..., a] * c - x[..., b] * s
+    out[..., b] = x[..., b] * c + x[..., a] * s
+    return out
+
+
+def paged_rows(pool, table, positions) -> np.ndarray:
+    """Rows of one sequence's positions, [len(positions), heads, d], from pool [pages, heads, page_size, d]."""
+    positions = np.asarray(positions)
+    size = pool.shape[2]
+    return pool[np.asarray(table)[positions // size], :, positions % size]
+
+
+def tree_attention(q, k, v, sees, scale=None):
+    """q [n, Hq, d] over k, v [L, Hkv, d]; sees bool [n, L].  Returns (a, A)
+    with A = sum_j p_j |v_j|; rows that see nothing are zeros.  Only what a row
+    sees enters its sums."""
+    q, k, v = (np.asarray(t, np.float64) for t in (q, k, v))
+    n, Hq, d = q.shape
+    G = Hq // k.shape[1]
+    scale = 1 / np.sqrt(d) if scale is None else scale
+    a, A = np.zeros((n, Hq, d)), np.zeros((n, Hq, d))
+    for i in range(n):
+        at = np.flatnonzero(sees[i])
+        if not at.size:
+            continue
+        for h in range(Hq):
+            s = scale * (k[at, h // G] @ q[i, h])
+            p = np.exp(s - s.max())
+            p /= p.sum()
+            a[i, h], A[i, h] = p @ v[at, h // G], p @ np.abs(v[at, h // G])
+    return a, A
+
+
+def tree_sees(parents) -> np.ndarray:
+    """bool [n, n]: row i sees itself and its ancestors."""
+    n = len(parents)
+    s = np.zeros((n, n), bool)
+    for i, p in enumerate(parents):
+        if p >= 0:
+            s[i] = s[p]
+        s[i, i] = True
+    return s
+
+
+def sample(logits, temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0, min_p: float = 0.0, u=None):
+    """(token, probability) for one row; u None or temperature <= 0: the greatest logit."""
+    x = np.asarray(logits, np.float64)
+    order = [int(i) for i in np.argsort(np.where(np.isnan(x), np.inf, -x), kind="stable")
+             if not np.isnan(x[i]) and x[i] != -np.inf]
+    if not order:
+        return -1, 0.0
+    if u is None or not temperature > 0:
+        return order[0], 1.0
+    top = x[order[0]]
+    w = [1.0 if x[i] == top else 0.0 if top == np.inf else float(np.exp((x[i] - top) / temperature)) for i in order]
+    if top_k > 0:
+        w = w[:top_k]
+    if top_p < 1:
+        run = np.cumsum(w)
+        w = w[:max(1, int(np.searchsorted(run, max(0.0, top_p) * run[-1])) + 1)]
+    if min_p > 0:
+        w = [t for t in w if t >= min(1.0, min_p)]
+    run = np.cumsum(w)
+    at = min(int(np.searchsorted(run, min(max(u, 0.0), 1.0) * run[-1], side="right")),
+             len(w) - 1)
+    return order[at], w[at] / run[-1]
+
+
+def tree_path(draft, parents, sampled):
+    """Rows of the accepted path of one sequence."""
+    path = [0] if len(draft) else []
+    while path:
+        at = path[-1]
+        nxt = [j for j in range(at + 1, len(draft))
+               if parents[j] == at and draft[j] == sampled[at] and sampled[at] >= 0]
+        if not nxt:
+            break
+        path.append(nxt[0])
+    return path

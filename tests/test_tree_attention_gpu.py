@@ -1,0 +1,301 @@
+"""GPU parity of the attention over a paged cache against the fp64 oracle:
+trees, random masks, rows that see nothing, prompt chunks, batched decoding;
+groups of query heads, page sizes that end inside a tile, empty sequences and
+contexts, splits over many CTAs, strides; NaN and infinities where a row does
+not look; graphs, streams and the cache that q4_prefill's layout makes."""
+import numpy as np
+import pytest
+
+import oracle
+from helpers import torch_dev, ulp16
+from serving_helpers import Batch, mask_words, rand16, random_tree
+
+torch = pytest.importorskip("torch")
+import bit_quantized_gemv_q4_gb300 as q4  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    from bit_quantized_gemv_q4_gb300 import build
+    build.build()
+
+
+def workspace(d):
+    n = q4.q4_tree_attention_workspace_bytes(d)
+    return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"), n  # NaN where nobody wrote
+
+
+def seen_by(b, kind, g):
+    """Per sequence, bool [n][n] over its own rows."""
+    out = []
+    for n in b.n:
+        if kind == "causal":
+            out.append(np.tril(np.ones((n, n), bool)))
+        elif kind == "tree":
+            out.append(oracle.tree_sees(random_tree(g, n)) if n else np.zeros((0, 0), bool))
+        elif kind == "random":
+            m = g.random((n, n)) < 0.3
+            m[::3] = False
+            out.append(m)
+        else:  # nothing
+            out.append(np.zeros((n, n), bool))
+    return out
+
+
+def expected(b, q, sees, scale=None):
+    a, A = [], []
+    for s in range(b.S):
+        L = b.ctx[s] + b.n[s]
+        full = np.concatenate([np.ones((b.n[s], b.ctx[s]), bool), sees[s]], 1)
+        x, y = oracle.tree_attention(q[b.start[s]:b.start[s + 1]], b.rows_of(b.k[0], s, np.arange(L)),
+                                     b.rows_of(b.v[0], s, np.arange(L)), full, scale)
+        a.append(x)
+        A.append(y)
+    return np.concatenate(a), np.concatenate(A)
+
+
+# A probability enters the product as fp16: 2^-11 of it; the scores (fp32, up
+# to 128 terms of |q k| / sqrt(d) about 7 in sum) and exp2 add under 2e-5 of
+# it; the sums' fp32 roundings 1e-6.  Then one fp16 rounding of the output.
+def close(got, a, A):
+    return np.abs(np.asarray(got, np.float64) - a) <= (2.0 ** -11 + 4e-5) * A + ulp16(a) / 2 + 1e-12
+
+
+def attend(b, c, q, kind, sees, words=None, scale=0.0, ld=0, stream=None, tail=2):
+    T, Hq, d = q.shape
+    mask, w = None, 0
+    if kind != "causal":
+        w = words or max(1, -(-max(b.n) // 32))
+        mask = mask_words([r for m in sees for r in m] + [np.zeros(1, bool)] * tail, w)
+        mask = torch_dev(mask.view(np.int32))
+    width = ld or Hq * d
+    dq = torch.full((T + tail, width), float("nan"), dtype=torch.float16, device="cuda")
+    dq[:T, :Hq * d] = torch_dev(q.reshape(T, -1))
+    out = torch.full((T + tail, width), -5.0, dtype=torch.float16, device="cuda")
+    ws, n = workspace(d)
+    q4.q4_tree_attention(c, b.dctx, b.dstart, T + tail, dq, Hq, out, ws, n, mask=mask, mask_words=w, scale=scale,
+                         ldq=width, ldo=width, stream=stream)
+    return out
+
+
+def check(out, b, q, a, A):
+    T, Hq, d = q.shape
+    got = out.cpu().numpy()
+    ok = close(got[:T, :Hq * d].reshape(a.shape), a, A)
+    assert ok.all(), (np.argwhere(~ok)[:5], np.abs(got[:T, :Hq * d].reshape(a.shape) - a)[~ok][:5])
+    assert np.all(got[T:] == -5.0) and np.all(got[:, Hq * d:] == -5.0)
+
+
+CASES = [
+    # d, Hkv, G, page, ctx, n
+    (128, 2, 2, 16, [5, 0, 130], [1, 1, 1]),
+    (128, 1, 8, 64, [63, 64, 65, 1], [1, 1, 1, 1]),
+    (128, 2, 1, 7, [0, 700], [5, 12]),
+    (128, 2, 4, 24, [200, 31, 0], [9, 33, 64]),
+    (128, 1, 5, 1, [90], [40]),
+    (64, 2, 4, 16, [0, 1, 300], [8, 0, 17]),
+    (64, 1, 16, 100, [129, 77], [3, 70]),
+    (64, 4, 1, 64, [2000], [1]),
+    (64, 3, 2, 33, [10, 20, 30, 0, 0], [0, 1, 2, 3, 0]),
+    (128, 8, 2, 128, [9000], [2]),
+    (128, 1, 7, 256, [513], [100]),
+]
+
+
+@pytest.mark.parametrize("kind", ["causal", "tree", "random", "nothing"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention(case, kind):
+    d, Hkv, G, page, ctx, n = CASES[case]
+    g = np.random.default_rng(100 + case)
+    b = Batch(g, ctx, n, Hkv, d, page)
+    q = rand16(g, b.rows, Hkv * G, d)
+    sees = seen_by(b, kind, g)
+    a, A = expected(b, q, sees)
+    out = attend(b, b.to_device(q4), q, kind, sees)
+    assert q4.q4_device_status() == 0
+    check(out, b, q, a, A)
+
+
+def test_attention_scale_stride_and_more_mask_words_than_rows():
+    g = np.random.default_rng(3)
+    b = Batch(g, [100, 3], [20, 7], 2, 64, 16)
+    q = rand16(g, b.rows, 6, 64)
+    sees = seen_by(b, "tree", g)
+    a, A = expected(b, q, sees, scale=0.37)
+    out = attend(b, b.to_device(q4), q, "tree", sees, words=3, scale=0.37, ld=6 * 64 + 40)
+    assert q4.q4_device_status() == 0
+    assert np.all(np.abs(out.cpu().numpy()[:27, :384].reshape(a.shape) - a) <= (2.0 ** -11 + 2e-4) * A + ulp16(a) / 2)
+
+
+def test_rows_past_the_mask_are_seen_by_nobody():
+    g = np.random.default_rng(4)
+    b = Batch(g, [10], [40], 1, 64, 16)
+    q = rand16(g, 40, 2, 64)
+    sees = [np.tril(np.ones((40, 40), bool))]
+    sees[0][:, 32:] = False
+    a, A = expected(b, q, sees)
+    out = attend(b, b.to_device(q4), q, "tree", [s[:, :32] for s in sees], words=1)
+    assert q4.q4_device_status() == 0
+    check(out, b, q, a, A)
+
+
+@pytest.mark.parametrize("d,G", [(128, 2), (64, 8), (128, 16)])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan, 65504.0])
+def test_values_that_a_row_does_not_see_do_not_reach_it(d, G, value):
+    # one branch of a tree holds infinities or NaN in its keys and values
+    g = np.random.default_rng(5)
+    b = Batch(g, [70, 0], [24, 11], 1, d, 16)
+    for s, j in ((0, 7), (1, 4), (0, 23)):
+        p = b.ctx[s] + j
+        b.v[0, b.table[s, p // 16], 0, p % 16, ::5] = value
+        b.k[0, b.table[s, p // 16], 0, p % 16, 3] = value
+    q = rand16(g, b.rows, G, d)
+    sees = seen_by(b, "tree", g)
+    with np.errstate(all="ignore"):
+        a, A = expected(b, q, sees)
+    got = attend(b, b.to_device(q4), q, "tree", sees).cpu().numpy()[:b.rows].reshape(a.shape)
+    assert q4.q4_device_status() == 0
+    clean = np.concatenate([~sees[0][:, [7, 23]].any(1), ~sees[1][:, 4]])
+    assert clean.any() and not clean.all()
+    assert close(got[clean], a[clean], A[clean]).all()
+    if value != 65504.0:  # what sees them is not finite, as in the formula
+        odd = ~np.isfinite(a[~clean])
+        assert (~np.isfinite(got[~clean]))[odd].all()
+
+
+def test_uniform_and_dominant_scores():
+    # equal keys average the values; a dominant one takes all, and probabilities
+    # 2^-30 of it still count where 4000 of them stand against it
+    g = np.random.default_rng(6)
+    d = 128
+    b = Batch(g, [4000], [1], 1, d, 64)
+    b.k[np.isfinite(b.k)] = 0
+    q = np.ones((1, 1, d), np.float16)
+    sees = [np.ones((1, 1), bool)]
+    a, A = expected(b, q, sees)
+    check(attend(b, b.to_device(q4), q, "causal", sees), b, q, a, A)
+    b.k[0, b.table[0, 0], 0, 0] = 1.625  # score 18.4: e^-18.4 = 2^-26.5
+    a, A = expected(b, q, sees)
+    check(attend(b, b.to_device(q4), q, "causal", sees), b, q, a, A)
+    assert q4.q4_device_status() == 0
+
+
+def test_prefill_cache_is_a_pool_of_one_page():
+    g = np.random.default_rng(7)
+    Hkv, d, max_seq = 4, 64, 300
+    kc, vc = rand16(g, Hkv, max_seq, d), rand16(g, Hkv, max_seq, d)
+    q = rand16(g, 3, 8, d)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    c = q4.PagedCache(torch_dev(kc), torch_dev(vc), 1, max_seq, Hkv, d, ints(0), 1, 1)
+    out = torch.empty(3, 8 * d, dtype=torch.float16, device="cuda")
+    ws, n = workspace(d)
+    q4.q4_tree_attention(c, ints(250), ints(0, 3), 3, torch_dev(q.reshape(3, -1)), 8, out, ws, n)
+    assert q4.q4_device_status() == 0
+    sees = np.tril(np.ones((3, 253), bool), 250)
+    a, A = oracle.tree_attention(q, kc[:, :253].transpose(1, 0, 2), vc[:, :253].transpose(1, 0, 2), sees)
+    assert close(out.cpu().numpy().reshape(a.shape), a, A).all()
+
+
+def test_bits_do_not_depend_on_the_run_or_the_stream():
+    g = np.random.default_rng(8)
+    b = Batch(g, [3000, 10, 777], [5, 64, 1], 2, 128, 16)
+    q = rand16(g, b.rows, 8, 128)
+    sees = seen_by(b, "tree", g)
+    c = b.to_device(q4)
+    first = attend(b, c, q, "tree", sees)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            again = attend(b, c, q, "tree", sees, stream=s)
+        s.synchronize()
+        assert torch.equal(first.view(torch.int16), again.view(torch.int16))
+
+
+def test_graph_replays_as_the_sequences_grow():
+    g = np.random.default_rng(9)
+    b = Batch(g, [500, 40, 0], [4, 4, 4], 2, 64, 16)
+    q = rand16(g, 12, 4, 64)
+    c = b.to_device(q4)
+    dq, out = torch_dev(q.reshape(12, -1)), torch.empty(12, 256, dtype=torch.float16, device="cuda")
+    ws, n = workspace(64)
+    run = lambda: q4.q4_tree_attention(c, b.dctx, b.dstart, 12, dq, 4, out, ws, n)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for ctx, start in (([500, 40, 0], [0, 4, 8, 12]), ([100, 3, 0], [0, 1, 9, 12]), ([30, 30, 0], [0, 12, 12, 12])):
+        use = [min(c0 + n0, x + (start[i + 1] - start[i])) for i, (c0, n0, x) in enumerate(zip([500, 40, 0], [4, 4, 4], ctx))]
+        rows = [start[i + 1] - start[i] for i in range(3)]
+        ctx = [u - r for u, r in zip(use, rows)]
+        if min(ctx) < 0:
+            continue
+        b.dctx.copy_(torch.tensor(ctx, dtype=torch.int32))
+        b.dstart.copy_(torch.tensor(start, dtype=torch.int32))
+        out.fill_(float("nan"))
+        graph.replay()
+        assert q4.q4_device_status() == 0
+        b.ctx, b.n, b.start = ctx, rows, np.array(start)
+        a, A = expected(b, q, seen_by(b, "causal", g))
+        assert close(out.cpu().numpy().reshape(a.shape), a, A).all()
+
+
+def test_bad_sizes_and_pages():
+    g = np.random.default_rng(10)
+    for what in ("page", "ctx", "room", "order"):
+        b = Batch(g, [40, 20, 9], [2, 3, 2], 1, 64, 16)
+        q = rand16(g, 7, 2, 64)
+        sees = seen_by(b, "causal", g)
+        a, A = expected(b, q, sees)
+        c = b.to_device(q4)
+        keep = [0, 1, 5, 6]  # rows of the other sequences
+        if what == "page":
+            b.dtable[1, 0] = b.n_pages
+        elif what == "ctx":
+            b.dctx[1] = -1
+        elif what == "room":
+            b.dctx[1] = 16 * b.max_pages
+        else:
+            b.dstart[2] = 1  # the second sequence ends before it starts; the third would start at 1
+            keep = [0, 1]
+        out = attend(b, c, q, "causal", sees)
+        assert q4.q4_device_status() == -7, what
+        got = out.cpu().numpy()[:7].reshape(a.shape)
+        if what == "order":
+            assert close(got[:1], a[:1], A[:1]).all()
+        else:
+            assert close(got[keep], a[keep], A[keep]).all(), what
+        if what in ("ctx", "room"):
+            assert np.all(got[2:5] == -5.0)
+        assert q4.q4_device_status() == 0
+
+
+def test_many_sequences():
+    g = np.random.default_rng(11)
+    S = 700
+    n = [int(x) for x in g.integers(0, 3, S)]
+    b = Batch(g, [int(x) for x in g.integers(0, 90, S)], n, 1, 64, 16)
+    q = rand16(g, b.rows, 4, 64)
+    sees = seen_by(b, "causal", g)
+    a, A = expected(b, q, sees)
+    out = attend(b, b.to_device(q4), q, "causal", sees)
+    assert q4.q4_device_status() == 0
+    check(out, b, q, a, A)
+
+
+def test_no_rows():
+    g = np.random.default_rng(12)
+    b = Batch(g, [5, 6], [1, 1], 1, 64, 16)
+    c = b.to_device(q4)
+    b.dstart.zero_()
+    out = torch.full((2, 64), -5.0, dtype=torch.float16, device="cuda")
+    ws, n = workspace(64)
+    for rows in (0, 2):
+        q4.q4_tree_attention(c, b.dctx, b.dstart, rows, torch.zeros_like(out), 1, out, ws, n)
+        assert q4.q4_device_status() == 0
+    assert bool((out == -5.0).all())
