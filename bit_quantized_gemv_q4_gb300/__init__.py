@@ -476,31 +476,83 @@ def q4_prefill_buffers(table: LayerTable, chunk: int, workspace) -> dict:
 
 
 # ----------------------------------------- paged cache, trees, sampling ---
+#
+# A call here takes a dozen tensors and its kernel a few microseconds, so the
+# checks of a plain argument (element type, current device, contiguous, large
+# enough) are four attribute reads in _arg / _rows; whatever does not pass them
+# goes to the functions behind, which say what is wrong or find the stride.
 
-def _typed(t, name: str, kind: str, *, count: int = 0, stride: int = 0, width: int = 0):
-    """Device pointer of an argument of the calls below.  A tensor is checked:
-    element type, device (the current one), last dimension contiguous, and,
-    where the call says how much it reads or writes, that it holds that much.
-    ints and None pass as in _ptr."""
-    if t is None or isinstance(t, int):
-        return t
-    import torch
+_torch = None
+
+
+def _get_torch():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _stream_of(torch, dev: int, stream):
+    """_stream without building a torch Stream object, which costs as much as a launch."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _arg_other(t, dtype, need: int, dev: int, name: str):
+    """Pointer of an argument that is not a plain contiguous tensor of its type, or the error."""
+    torch = _get_torch()
     p = _ptr(t)
-    kinds = {"f16": (torch.float16,), "f32": (torch.float32,), "i32": (torch.int32,),
-             "w32": (torch.int32, torch.uint32), "w64": (torch.int64, torch.uint64), "raw": (t.dtype,)}[kind]
-    if t.dtype not in kinds:
-        raise ValueError(f"{name}: expected {kinds[0]}, got {t.dtype}")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if t.dim() and t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    # elements that the call can reach: rows `stride` apart, the last one `width` wide
-    need = (count - 1) * stride + width if stride else count
-    if count and need > 0:
-        have = 1 + sum((n - 1) * abs(st) for n, st in zip(t.shape, t.stride())) if t.numel() else 0
-        if have < need:
-            raise ValueError(f"{name}: holds {have} elements, the call needs {need}")
+    same = {torch.int32: (torch.int32, torch.uint32), torch.int64: (torch.int64, torch.uint64)}
+    # words: the signed type of the same width holds the same bits
+    kinds = same[dtype] if name in ("mask", "freqs") else (dtype,)
+    if dtype is not None and t.dtype not in kinds:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < need:
+        raise ValueError(f"{name}: holds {t.numel()} elements, the call needs {need}")
     return p
+
+
+def _arg(t, dtype, need: int, dev: int, name: str):
+    """Device pointer of a packed argument of at least `need` elements; ints and None pass as in _ptr."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= need and t.is_contiguous():
+        return t.data_ptr()
+    return _arg_other(t, dtype, need, dev, name)
+
+
+def _rows_other(t, dtype, rows: int, width: int, ld: int, dev: int, name: str):
+    p = _ptr(t)
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if t.dim() == 2 and not ld:
+        ld = t.stride(0) if t.size(0) > 1 else max(width, t.size(1))
+    elif t.dim() != 2 and not t.is_contiguous():
+        raise ValueError(f"{name}: give a [rows][width] view or a contiguous tensor")
+    if t.numel() and t.size(-1) != 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    need = (rows - 1) * (ld or width) + width if rows > 0 else 0
+    have = 1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride())) if t.numel() else 0
+    if have < need:
+        raise ValueError(f"{name}: reaches over {have} elements, the call needs {need}")
+    return p, ld
+
+
+def _rows(t, dtype, rows: int, width: int, ld: int, dev: int, name: str):
+    """(device pointer, row stride) of a matrix argument; a 2-D tensor's own stride unless one is given."""
+    if t is None or t.__class__ is int:
+        return t, ld
+    if (not ld and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.size(-1) == width
+            and t.numel() >= rows * width):
+        return t.data_ptr(), width
+    return _rows_other(t, dtype, rows, width, ld, dev, name)
 
 
 class PagedCache:
@@ -508,62 +560,49 @@ class PagedCache:
     q4_tree_accept one such pool per layer, layer_stride elements apart) and
     the sequences' page table int32 [n_seqs][max_pages]; keeps the tensors."""
 
+    __slots__ = ("k", "v", "page_table", "sizes", "pool")
+
     def __init__(self, k, v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, page_table, n_seqs: int,
                  max_pages: int):
         self.k, self.v, self.page_table = k, v, page_table
-        self.c = q4_paged_cache(None, None, None, n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages)
+        self.sizes = (n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages)
+        self.pool = n_pages * page_size * n_kv_heads * head_dim  # elements of one layer's keys
 
-    def _desc(self, n_layers: int = 1, layer_stride: int = 0) -> q4_paged_cache:
-        c = self.c
-        pool = c.n_pages * c.n_kv_heads * c.page_size * c.head_dim
-        n = (n_layers - 1) * layer_stride + pool if n_layers > 0 else 0
-        for t, name in ((self.k, "cache.k"), (self.v, "cache.v"), (self.page_table, "cache.page_table")):
-            if t is not None and not isinstance(t, int) and not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-        c.k, c.v = _typed(self.k, "cache.k", "f16", count=n), _typed(self.v, "cache.v", "f16", count=n)
-        c.page_table = _typed(self.page_table, "cache.page_table", "i32", count=c.n_seqs * c.max_pages)
-        return c
-
-
-def _row_stride(t, given: int, name: str) -> int:
-    """A matrix argument's row stride: the given one, else the tensor's own (0: packed)."""
-    if given or t is None or isinstance(t, int) or t.dim() < 2:
-        return given
-    if t.dim() > 2:
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: give a [rows][width] view or its row stride")
-        return 0
-    return t.stride(0) if t.shape[0] > 1 else 0
+    def _desc(self, torch, dev: int, elements: int) -> q4_paged_cache:
+        s = self.sizes
+        return q4_paged_cache(_arg(self.k, torch.float16, elements, dev, "cache.k"),
+                              _arg(self.v, torch.float16, elements, dev, "cache.v"),
+                              _arg(self.page_table, torch.int32, s[4] * s[5], dev, "cache.page_table"), *s)
 
 
 def q4_rope_frequencies(freqs, rot_dim: int, theta: float = 1.0e6, factor: float = 1.0, orig_len: int = 0,
                         alpha: float = 1.0, beta: float = 32.0, stream=None):
     """freqs: int64 (or uint64) [rot_dim / 2] out, turns per position in units of 2^-64."""
+    torch = _get_torch()
     d = q4_rope_desc(rot_dim, orig_len, theta, factor, alpha, beta)
-    _check(lib().q4_rope_frequencies(ctypes.byref(d), _typed(freqs, "freqs", "w64", count=rot_dim // 2),
-                                     _stream(stream)), "q4_rope_frequencies")
+    dev = torch.cuda.current_device()
+    p = _arg(freqs, torch.int64, rot_dim // 2, dev, "freqs")
+    _check(lib().q4_rope_frequencies(ctypes.byref(d), p, _stream_of(torch, dev, stream)), "q4_rope_frequencies")
 
 
 def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=None, q_out=None, n_q_heads: int = 0,
                     positions=None, freqs=None, rot_dim: int = 0, layout=Q4_ROPE_HALF, amplitude: float = 1.0,
                     ldq: int = 0, ldk: int = 0, ldv: int = 0, ldqo: int = 0, stream=None):
     """New rows' keys (rotated) and values into the paged cache, queries (rotated) into q_out."""
-    d = q4_paged_append_desc()
-    c = d.cache = cache._desc()
-    wk, wq = c.n_kv_heads * c.head_dim, n_q_heads * c.head_dim
-    ldq, ldk = _row_stride(q, ldq, "q"), _row_stride(k, ldk, "k")
-    ldv, ldqo = _row_stride(v, ldv, "v"), _row_stride(q_out, ldqo, "q_out")
-    d.ctx_len = _typed(ctx_len, "ctx_len", "i32", count=c.n_seqs)
-    d.row_start = _typed(row_start, "row_start", "i32", count=c.n_seqs + 1)
-    d.rows, d.positions = rows, _typed(positions, "positions", "i32", count=rows)
-    d.k = _typed(k, "k", "f16", count=rows, stride=ldk or wk, width=wk)
-    d.v = _typed(v, "v", "f16", count=rows, stride=ldv or wk, width=wk)
-    d.q = _typed(q, "q", "f16", count=rows, stride=ldq or wq, width=wq)
-    d.q_out = _typed(q_out, "q_out", "f16", count=rows, stride=ldqo or wq, width=wq)
-    d.ldk, d.ldv, d.ldq, d.ldqo, d.n_q_heads = ldk, ldv, ldq, ldqo, n_q_heads
-    d.freqs = _typed(freqs, "freqs", "w64", count=rot_dim // 2)
-    d.rot_dim, d.layout, d.amplitude = rot_dim, layout, amplitude
-    _check(lib().q4_paged_append(ctypes.byref(d), _stream(stream)), "q4_paged_append")
+    torch = _get_torch()
+    dev = torch.cuda.current_device()
+    f16, i32_ = torch.float16, torch.int32
+    _, _, heads, hd, n_seqs, _ = cache.sizes
+    pk, ldk = _rows(k, f16, rows, heads * hd, ldk, dev, "k")
+    pv, ldv = _rows(v, f16, rows, heads * hd, ldv, dev, "v")
+    pq, ldq = _rows(q, f16, rows, n_q_heads * hd, ldq, dev, "q")
+    po, ldqo = _rows(q_out, f16, rows, n_q_heads * hd, ldqo, dev, "q_out")
+    d = q4_paged_append_desc(
+        cache._desc(torch, dev, cache.pool), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
+        _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(positions, i32_, rows, dev, "positions"), pk, pv,
+        ldk, ldv, pq, po, ldq, ldqo, n_q_heads, _arg(freqs, torch.int64, rot_dim // 2, dev, "freqs"), rot_dim, layout,
+        amplitude)
+    _check(lib().q4_paged_append(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_paged_append")
 
 
 def q4_tree_attention_workspace_bytes(head_dim: int) -> int:
@@ -573,46 +612,50 @@ def q4_tree_attention_workspace_bytes(head_dim: int) -> int:
 def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_heads: int, out, workspace,
                       workspace_bytes: int, mask=None, mask_words: int = 0, scale: float = 0.0, ldq: int = 0,
                       ldo: int = 0, stream=None):
-    """Attention of the new rows over the cached positions and, by the mask (NULL: causal), their own."""
-    d = q4_tree_attention_desc()
-    c = d.cache = cache._desc()
-    w = n_q_heads * c.head_dim
-    ldq, ldo = _row_stride(q, ldq, "q"), _row_stride(out, ldo, "out")
-    if mask is not None and not isinstance(mask, int) and not mask.is_contiguous():
-        raise ValueError("mask must be contiguous")
-    d.ctx_len = _typed(ctx_len, "ctx_len", "i32", count=c.n_seqs)
-    d.row_start = _typed(row_start, "row_start", "i32", count=c.n_seqs + 1)
-    d.rows, d.mask, d.mask_words = rows, _typed(mask, "mask", "w32", count=rows * mask_words), mask_words
-    d.q = _typed(q, "q", "f16", count=rows, stride=ldq or w, width=w)
-    d.out = _typed(out, "out", "f16", count=rows, stride=ldo or w, width=w)
-    d.ldq, d.ldo, d.n_q_heads, d.scale = ldq, ldo, n_q_heads, scale
-    d.workspace, d.workspace_bytes = _typed(workspace, "workspace", "raw"), workspace_bytes
-    _check(lib().q4_tree_attention(ctypes.byref(d), _stream(stream)), "q4_tree_attention")
+    """Attention of the new rows over the cached positions and, by the mask (None: causal), their own."""
+    torch = _get_torch()
+    dev = torch.cuda.current_device()
+    f16, i32_ = torch.float16, torch.int32
+    w, n_seqs = n_q_heads * cache.sizes[3], cache.sizes[4]
+    pq, ldq = _rows(q, f16, rows, w, ldq, dev, "q")
+    po, ldo = _rows(out, f16, rows, w, ldo, dev, "out")
+    if workspace is not None and workspace.__class__ is not int:
+        if workspace.numel() * workspace.element_size() < workspace_bytes:
+            raise ValueError(f"workspace: smaller than {workspace_bytes} bytes")
+        workspace = _arg(workspace, workspace.dtype, 0, dev, "workspace")
+    d = q4_tree_attention_desc(
+        cache._desc(torch, dev, cache.pool), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
+        _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(mask, i32_, rows * mask_words, dev, "mask"),
+        mask_words, pq, po, ldq, ldo, n_q_heads, scale, workspace, workspace_bytes)
+    _check(lib().q4_tree_attention(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_attention")
 
 
 def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, parents, sampled, accepted, path,
                    next_token, ctx_out, n_layers: int = 1, layer_stride: int = 0, stream=None):
     """Walks each sequence's drafted tree along the sampled tokens and moves the path's cache rows into place."""
-    d = q4_tree_accept_desc()
-    c = d.cache = cache._desc(n_layers, layer_stride)
-    d.ctx_len = _typed(ctx_len, "ctx_len", "i32", count=c.n_seqs)
-    d.row_start = _typed(row_start, "row_start", "i32", count=c.n_seqs + 1)
-    d.rows = rows
-    for n, t in (("draft", draft), ("parents", parents), ("sampled", sampled), ("path", path)):
-        setattr(d, n, _typed(t, n, "i32", count=rows))
-    for n, t in (("accepted", accepted), ("next_token", next_token), ("ctx_out", ctx_out)):
-        setattr(d, n, _typed(t, n, "i32", count=c.n_seqs))
-    d.n_layers, d.layer_stride = n_layers, layer_stride
-    _check(lib().q4_tree_accept(ctypes.byref(d), _stream(stream)), "q4_tree_accept")
+    torch = _get_torch()
+    dev = torch.cuda.current_device()
+    i32_, n_seqs = torch.int32, cache.sizes[4]
+    elements = (n_layers - 1) * layer_stride + cache.pool if n_layers > 0 else 0
+    d = q4_tree_accept_desc(
+        cache._desc(torch, dev, elements), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
+        _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(draft, i32_, rows, dev, "draft"),
+        _arg(parents, i32_, rows, dev, "parents"), _arg(sampled, i32_, rows, dev, "sampled"),
+        _arg(accepted, i32_, n_seqs, dev, "accepted"), _arg(path, i32_, rows, dev, "path"),
+        _arg(next_token, i32_, n_seqs, dev, "next_token"), _arg(ctx_out, i32_, n_seqs, dev, "ctx_out"), n_layers,
+        layer_stride)
+    _check(lib().q4_tree_accept(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_accept")
 
 
 def q4_sample(logits, dtype, rows: int, vocab: int, tokens, temperature=None, top_k=None, top_p=None, min_p=None,
               u=None, probs=None, ld: int = 0, stream=None):
-    """One token per row of logits (see q4.h section 8); u: fp32 random numbers of [0, 1), None = greedy."""
-    ld = _row_stride(logits, ld, "logits")
-    d = q4_sample_desc(_typed(logits, "logits", "f16" if dtype == Q4_F16 else "f32", count=rows, stride=ld or vocab,
-                              width=vocab), dtype, rows, vocab, ld)
-    for n, t in (("temperature", temperature), ("top_p", top_p), ("min_p", min_p), ("u", u), ("probs", probs)):
-        setattr(d, n, _typed(t, n, "f32", count=rows))
-    d.top_k, d.tokens = _typed(top_k, "top_k", "i32", count=rows), _typed(tokens, "tokens", "i32", count=rows)
-    _check(lib().q4_sample(ctypes.byref(d), _stream(stream)), "q4_sample")
+    """One token per row of logits (q4.h section 8); u: fp32 random numbers of [0, 1), None = the greatest logit."""
+    torch = _get_torch()
+    dev = torch.cuda.current_device()
+    f32, i32_ = torch.float32, torch.int32
+    p, ld = _rows(logits, torch.float16 if dtype == Q4_F16 else f32, rows, vocab, ld, dev, "logits")
+    d = q4_sample_desc(p, dtype, rows, vocab, ld, _arg(temperature, f32, rows, dev, "temperature"),
+                       _arg(top_k, i32_, rows, dev, "top_k"), _arg(top_p, f32, rows, dev, "top_p"),
+                       _arg(min_p, f32, rows, dev, "min_p"), _arg(u, f32, rows, dev, "u"),
+                       _arg(tokens, i32_, rows, dev, "tokens"), _arg(probs, f32, rows, dev, "probs"))
+    _check(lib().q4_sample(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_sample")
