@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include "q4_paged.cuh"
+#include "q4_tc.cuh"
 
 namespace q4x {
 
@@ -35,6 +36,7 @@ constexpr int kThreads = 128;  // 4 warps: WM of them along the rows, 4 / WM alo
 constexpr int kStages = 3;
 constexpr int kMaxRows = 64;   // rows of a job
 constexpr int kMaxCtas = 512;
+constexpr int kTcRows = 256, kMaxTcCtas = 160;
 // P = 2^(s - m + kShift): fp16 keeps 11 bits of a probability down to 2^-26
 // of the row's greatest, and O / l is the same quotient.
 constexpr float kShift = 12.f;
@@ -48,35 +50,34 @@ struct Args {
     long long ldq, ldo;
     int G;       // query heads per kv head
     float c;     // scale * log2(e)
-    float* part; // workspace: [2 CTAs][kMaxRows][D] outputs, then [2 CTAs][kMaxRows] (m, l)
-    int ctas;
+    int ctas;    // CTAs that share the line
+    int BM, KT;  // rows of a job, positions of a tile
+    float* po;   // workspace: [2 CTAs][BM][D] outputs
+    float2* pml; // [2 CTAs][BM] (m, l)
 };
 
 template <int D>
 __device__ __forceinline__ float* part_o(const Args& a, int slot) {
-    return a.part + (size_t)slot * kMaxRows * D;
+    return a.po + (size_t)slot * a.BM * D;
 }
-template <int D>
-__device__ __forceinline__ float2* part_ml(const Args& a, int slot) {
-    return reinterpret_cast<float2*>(a.part + (size_t)2 * kMaxCtas * kMaxRows * D) + (size_t)slot * kMaxRows;
-}
+__device__ __forceinline__ float2* part_ml(const Args& a, int slot) { return a.pml + (size_t)slot * a.BM; }
 
 // ---------------------------------------------------------------- schedule ---
-// Tiles of a sequence's row block `rb` (BM rows): with a mask every row may
-// see every new row; causally the block's last token is the last key.
-__device__ __forceinline__ int block_tiles(const Args& a, const Seq& q, int rb, int BM) {
-    const int last = min(((rb + 1) * BM - 1) / a.G, q.n - 1);
+// Tiles of a sequence's row block `rb`: with a mask every row may see every
+// new row; causally the block's last token is the last key.
+__device__ __forceinline__ int block_tiles(const Args& a, const Seq& q, int rb) {
+    const int last = min(((rb + 1) * a.BM - 1) / a.G, q.n - 1);
     const int keys = q.ctx + (a.mask ? q.n : last + 1);
-    return (keys + kKeys - 1) / kKeys;
+    return (keys + a.KT - 1) / a.KT;
 }
 
 // Tiles of one head of a sequence (all row blocks).
-__device__ __forceinline__ long long head_tiles(const Args& a, const Seq& q, int BM) {
+__device__ __forceinline__ long long head_tiles(const Args& a, const Seq& q) {
     if (q.n <= 0) return 0;
-    const int blocks = (int)(((long long)q.n * a.G + BM - 1) / BM);
-    if (a.mask) return (long long)blocks * block_tiles(a, q, 0, BM);
+    const int blocks = (int)(((long long)q.n * a.G + a.BM - 1) / a.BM);
+    if (a.mask || blocks == 1) return (long long)blocks * block_tiles(a, q, blocks - 1);
     long long t = 0;
-    for (int b = 0; b < blocks; ++b) t += block_tiles(a, q, b, BM);
+    for (int b = 0; b < blocks; ++b) t += block_tiles(a, q, b);
     return t;
 }
 
@@ -86,10 +87,9 @@ struct Place {
     Seq q;
 };
 
-// The job line's length, and the place of tile x (by every thread; `sums`
-// holds the threads' shares).  Each thread adds up a contiguous share of the
-// sequences; the share that holds x is then walked.
-__device__ __forceinline__ long long line_scan(const Args& a, int BM, long long* sums, int threads) {
+// The line's length; `sums` gets the threads' running shares: each thread adds
+// up a contiguous share of the sequences.
+__device__ __forceinline__ long long line_scan(const Args& a, long long* sums, int threads) {
     const int per = (a.w.S + threads - 1) / threads;
     const int lo = min(a.w.S, (int)threadIdx.x * per), hi = min(a.w.S, lo + per);
     long long t = 0;
@@ -97,10 +97,9 @@ __device__ __forceinline__ long long line_scan(const Args& a, int BM, long long*
         bool bad;
         const Seq q = q4p::seq_of(a.w, s, bad);
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
-        t += head_tiles(a, q, BM);
+        t += head_tiles(a, q);
     }
     t *= a.w.H;
-    // inclusive scan over the threads
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -116,9 +115,15 @@ __device__ __forceinline__ long long line_scan(const Args& a, int BM, long long*
     return sums[threads - 1];
 }
 
+// A CTA's share of the line: as even as whole tiles allow.
+__device__ __forceinline__ long long line_share(const Args& a, long long line) {
+    if (line < (1ll << 31)) return ((unsigned)line + (unsigned)a.ctas - 1) / (unsigned)a.ctas;
+    return (line + a.ctas - 1) / a.ctas;
+}
+
 // Place of tile x (x < the line's length).
-__device__ __forceinline__ Place line_find(const Args& a, int BM, const long long* sums, int threads, long long x) {
-    int lo = 0, hi = threads - 1;  // first thread whose inclusive sum exceeds x
+__device__ __forceinline__ Place line_find(const Args& a, const long long* sums, int threads, long long x) {
+    int lo = 0, hi = threads - 1;  // first thread whose running sum exceeds x
     while (lo < hi) {
         const int mid = (lo + hi) / 2;
         if (sums[mid] > x) hi = mid;
@@ -131,14 +136,14 @@ __device__ __forceinline__ Place line_find(const Args& a, int BM, const long lon
     long long head = 0;
     for (p.s = lo * per;; ++p.s) {
         p.q = q4p::seq_of(a.w, p.s, bad);
-        head = head_tiles(a, p.q, BM);
+        head = head_tiles(a, p.q);
         if (x < head * a.w.H) break;
         x -= head * a.w.H;
     }
-    p.h = (int)(x / head);
+    p.h = x < (1ll << 31) && head < (1ll << 31) ? (int)((unsigned)x / (unsigned)head) : (int)(x / head);
     x -= p.h * head;
     for (p.rb = 0;; ++p.rb) {
-        p.tiles = block_tiles(a, p.q, p.rb, BM);
+        p.tiles = block_tiles(a, p.q, p.rb);
         if (x < p.tiles) break;
         x -= p.tiles;
     }
@@ -146,11 +151,10 @@ __device__ __forceinline__ Place line_find(const Args& a, int BM, const long lon
     return p;
 }
 
-// The next tile's place (there is one).
-__device__ __forceinline__ void step(const Args& a, int BM, Place& p) {
-    if (++p.tile < p.tiles) return;
+// The next job's first tile (there is one).
+__device__ __forceinline__ void next_job(const Args& a, Place& p) {
     p.tile = 0;
-    if ((long long)++p.rb * BM >= (long long)p.q.n * a.G) {
+    if ((long long)++p.rb * a.BM >= (long long)p.q.n * a.G) {
         p.rb = 0;
         if (++p.h == a.w.H) {
             p.h = 0;
@@ -160,7 +164,12 @@ __device__ __forceinline__ void step(const Args& a, int BM, Place& p) {
             } while (p.q.n <= 0);
         }
     }
-    p.tiles = block_tiles(a, p.q, p.rb, BM);
+    p.tiles = block_tiles(a, p.q, p.rb);
+}
+
+// The next tile's place (there is one).
+__device__ __forceinline__ void step(const Args& a, Place& p) {
+    if (++p.tile == p.tiles) next_job(a, p);
 }
 
 // ----------------------------------------------------------------- devices ---
@@ -226,10 +235,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
     constexpr uint32_t TB = kKeys * D * 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, u = lane & 3;
     const int wm = warp / WN, wn = warp % WN;
-    const long long line = line_scan(a, BM, sums, kThreads);
-    const long long x0 = line * blockIdx.x / a.ctas, x1 = line * (blockIdx.x + 1) / a.ctas;
+    const long long line = line_scan(a, sums, kThreads);
+    const long long share = line_share(a, line), x0 = share * blockIdx.x, x1 = min(line, x0 + share);
+    q4d::pdl_trigger();  // the joining kernel's blocks may start; they wait for this grid's end
     if (x0 >= x1) return;
-    Place cur = line_find(a, BM, sums, kThreads, x0);
+    Place cur = line_find(a, sums, kThreads, x0);
     Place ld = cur;
     const uint32_t sm0 = q4d::smem_addr(smem);
 
@@ -260,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
     for (int i = 0; i < kStages - 1; ++i) {
         if (loaded < x1) {
             load(i);
-            if (++loaded < x1) step(a, BM, ld);
+            if (++loaded < x1) step(a, ld);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
         __syncthreads();
         if (loaded < x1) {
             load((int)((loaded - x0) % kStages));
-            if (++loaded < x1) step(a, BM, ld);
+            if (++loaded < x1) step(a, ld);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         const uint32_t kb = sm0 + (uint32_t)st * 2u * TB, vb = kb + TB;
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
                 } else {
                     const int slot = 2 * blockIdx.x + (begun ? 1 : 0);
                     float* po = part_o<D>(a, slot);
-                    float2* pm = part_ml<D>(a, slot);
+                    float2* pm = part_ml(a, slot);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = row0 + 8 * e;
@@ -490,68 +500,649 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             fresh = true;
             begun = true;
         }
-        if (x + 1 < x1) step(a, BM, cur);
+        if (x + 1 < x1) step(a, cur);
     }
 }
 
 // Joins the parts of the jobs that several CTAs shared.  Block b looks at the
 // border between CTAs b and b + 1; it works if that is the first border inside
-// its job.  A warp per row; grid.y covers the rows.
-template <int D>
-__global__ void __launch_bounds__(256) tree_join_kernel(const Args a, int BM) {
-    __shared__ long long sums[256];
-    const long long line = line_scan(a, BM, sums, 256);
-    const int b = blockIdx.x;
-    const long long x = line * (b + 1) / a.ctas, xb = line * b / a.ctas;
-    if (x <= xb || x >= line) return;  // CTA b has no tiles, or the line ends
-    const Place p = line_find(a, BM, sums, 256, x);
-    const long long j0 = x - p.tile, j1 = j0 + p.tiles;  // the job's tiles
-    if (p.tile == 0 || xb > j0) return;                   // no job across this border, or an earlier border's
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const long long rr = (long long)p.rb * BM + r;
-    if (r >= BM || rr >= (long long)p.q.n * a.G) return;
-    // CTA b has the job's beginning (slot 2 b + 1), later CTAs their slot 2 c
-    constexpr int E = D / 32;
-    float m = -INFINITY;
-    int last = b;
-    for (int c = b; c < a.ctas && line * c / a.ctas < j1; ++c) {
-        if (line * (c + 1) / a.ctas == line * c / a.ctas) continue;
-        m = fmaxf(m, part_ml<D>(a, 2 * c + (c == b))[r].x);
-        last = c;
-    }
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[E] = {};
-    for (int c = b; c <= last; ++c) {
-        if (line * (c + 1) / a.ctas == line * c / a.ctas) continue;
-        const int slot = 2 * c + (c == b);
-        const float2 t = part_ml<D>(a, slot)[r];
-        const float f = exp2f(t.x - ms);
-        l = fmaf(t.y, f, l);
-        const float* src = part_o<D>(a, slot) + (size_t)r * D + E * lane;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(src[e], f, o[e]);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* dst = a.out + (p.q.start + rr / a.G) * a.ldo + (p.h * a.G + rr % a.G) * D + E * lane;
-#pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack2(o[e] * inv, o[e + 1] * inv);
-}
+// its job.  A warp per row; a lane holds (m, l) of every 32nd part, so the
+// loads are in flight together.
+constexpr int kJoinThreads = 256;
 
 template <int D>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Args a) {
+    __shared__ long long sums[kJoinThreads];
+    const long long line = line_scan(a, sums, kJoinThreads);
+    const long long share = line_share(a, line);
+    const int b = blockIdx.x;
+    const long long xb = share * b, x = xb + share;
+    Place p;
+    long long j0 = 0;  // the job's first tile
+    bool work = x < line;
+    if (work) {
+        p = line_find(a, sums, kJoinThreads, x);
+        j0 = x - p.tile;
+        work = p.tile != 0 && xb <= j0;  // a job across this border, and no earlier border in it
+    }
+    // the parts are written (and no grid that follows this one starts before
+    // the attention's end, so blocks without work wait as well)
+    q4d::pdl_wait();
+    if (!work) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM);
+    // CTA b has the job's beginning (slot 2 b + 1), later CTAs their slot 2 c
+    const int last = (int)((j0 + p.tiles - 1) / share);  // CTA of the job's last tile
+    const auto slot_of = [&](int c) { return 2 * c + (c == b); };
+    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += gridDim.y * (kJoinThreads / 32)) {
+        const long long rr = (long long)p.rb * a.BM + r;
+        float m = -INFINITY;
+        for (int c = b + lane; c <= last; c += 32) m = fmaxf(m, part_ml(a, slot_of(c))[r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float ms = m == -INFINITY ? 0.f : m;
+        constexpr int E = D / 32;
+        float l = 0.f, o[E] = {};
+        for (int c0 = b; c0 <= last; c0 += 32) {
+            float f = 0.f;
+            if (c0 + lane <= last) {
+                const float2 t = part_ml(a, slot_of(c0 + lane))[r];
+                f = exp2f(t.x - ms);
+                l = fmaf(t.y, f, l);
+            }
+            const int n = min(32, last - c0 + 1);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                const float* src = part_o<D>(a, slot_of(c0 + i)) + (size_t)r * D + E * lane;
+                float v[E];
+                if constexpr (E == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(src);
+                    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(src);
+                    v[0] = t.x, v[1] = t.y;
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], fi, o[e]);
+            }
+        }
+#pragma unroll
+        for (int o2 = 16; o2 > 0; o2 >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* dst = a.out + (p.q.start + rr / a.G) * a.ldo + (p.h * a.G + rr % a.G) * D + E * lane;
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) w[e / 2] = pack2(o[e] * inv, o[e + 1] * inv);
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = w[0];
+    }
+}
+
+// The parts' places in the workspace.
+template <int D>
+size_t parts_bytes(int ctas, int BM) {
+    return (size_t)2 * ctas * BM * (D + 2) * 4;
+}
+template <int D>
+void place_parts(Args& a, void* workspace) {
+    a.po = static_cast<float*>(workspace);
+    a.pml = reinterpret_cast<float2*>(a.po + (size_t)2 * a.ctas * a.BM * D);
+}
+template <int D>
 size_t workspace_bytes() {
-    return (size_t)2 * kMaxCtas * kMaxRows * (D + 2) * 4;
+    const size_t x = parts_bytes<D>(kMaxCtas, kMaxRows), y = parts_bytes<D>(kMaxTcCtas, kTcRows);
+    return x > y ? x : y;
+}
+
+// The joining kernel starts while the attention's last CTAs run (programmatic
+// dependent launch) and has its place in the line by the time they end.
+template <int D>
+cudaError_t launch_join(const Args& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.ctas - 1, (unsigned)(a.BM <= 32 ? 1 : a.BM <= 64 ? 2 : 4));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a);
 }
 
 template <int D, int WM>
-cudaError_t launch(Args& a, int sms, cudaStream_t s) {
+cudaError_t launch(Args& a, void* workspace, int sms, cudaStream_t s) {
     static std::atomic<int> marks[64];
     cudaError_t e = q4i::ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_kernel<D, WM>), marks, (int)attn_smem<D>());
     if (e != cudaSuccess) return e;
     a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    a.BM = 16 * WM;
+    a.KT = kKeys;
+    place_parts<D>(a, workspace);
     tree_attn_kernel<D, WM><<<a.ctas, kThreads, attn_smem<D>(), s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    tree_join_kernel<D><<<dim3(a.ctas - 1, 2 * WM), 256, 0, s>>>(a, 16 * WM);
-    return cudaGetLastError();
+    return launch_join<D>(a, s);
+}
+
+// ------------------------------------------------- tcgen05: many rows per job ---
+// From a few dozen rows per kv head on the products bound the work, and they
+// belong to the 5th-generation tensor cores.  A CTA takes a job of up to 256
+// rows and 128-position tiles as two streams of 128 rows (the MMA's M):
+//   more than 128 rows: stream i has rows 128 i .. and every tile, so a tile
+//     of keys and values is read once for 256 rows;
+//   else: both streams have the same rows and alternate tiles, and their
+//     (m, l, O) are joined at the end.
+// Per stream a warpgroup computes the softmax (thread = row = TMEM lane) while
+// the tensor cores work for the other stream; one thread issues, in order,
+//   S(0) S(1) | P V(0) S(2) | P V(1) S(3) | ...   (numbers: steps, stream = step % 2)
+// S = Q K^T (128 x 128, Q and K from shared memory) and O += P V (P, fp16,
+// from tensor memory over the scores it came from, V read MN-major).  MMAs of
+// one thread run in order, so S(k + 2) may overwrite what P V(k) reads, and
+// the commit behind S(k + 2) tells the softmax that O holds step k's product.
+// Tensor memory (512 columns): S 0 and 1 (128 each), O 0 and 1.
+// The reference maximum of a row moves only when its maximum exceeds it by
+// more than 8 (a factor 2^8); then O and l are rescaled.  With kTcShift P
+// reaches 2^15 and keeps 11 bits down to 2^-29 of the row's greatest at worst.
+// Key and value tiles come by TMA as boxes of `box` rows (the greatest power
+// of two, 8 .. 128, that divides the page): a box lies in one page.  A page
+// that does not exist is read outside the map, where TMA fills in zeros.
+constexpr int kTcKeys = 128;
+constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10: MMA, 11: TMEM
+constexpr float kTcShift = 7.f;
+
+template <int D>
+struct TcShape {
+    static constexpr uint32_t kTile = 128 * D * 2;      // a 128 x D fp16 tile: D / 64 swizzled slabs of 16 KB
+    static constexpr int kStages = D == 128 ? 2 : 4;    // of keys, and of values
+    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * (size_t)kTile + 512;
+};
+
+struct TcBars {
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], p_full[2], q_full, o_full, x_full, x_empty, drain;
+    uint32_t tmem_base;
+    volatile int abort;
+    volatile int odd[2];  // last segment (by parity) that met infinities or NaN among its new rows' values
+};
+
+__device__ __forceinline__ bool tc_wait(TcBars& B, uint64_t& bar, uint32_t parity, int* err) {
+    if (B.abort) return false;
+    if (!q4d::mbar_wait(q4d::smem_addr(&bar), parity, err)) {
+        B.abort = 1;
+        return false;
+    }
+    return true;
+}
+
+__device__ __forceinline__ uint32_t sw_off(int r, int c) {  // row r, 16-byte chunk c < 8 of a swizzled slab
+    return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bits 0 .. 31: which of the positions behind new row j0 (negative: cached)
+// row `tok` of a sequence sees.
+__device__ __forceinline__ uint32_t sees_word(const Args& a, const Seq& q, int tok, int j0) {
+    if (j0 >= q.n) return 0u;
+    if (j0 + 32 <= 0) return 0xffffffffu;
+    uint32_t bits;
+    const int lo = j0 < 0 ? 0 : j0;
+    if (!a.mask) {
+        const int n = tok - lo + 1;  // rows lo .. tok
+        bits = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+    } else {
+        const uint32_t* m = a.mask + (size_t)(q.start + tok) * a.mask_words;
+        const int w = lo >> 5, s = lo & 31;
+        const uint32_t w0 = w < a.mask_words ? m[w] : 0u, w1 = s && w + 1 < a.mask_words ? m[w + 1] : 0u;
+        bits = s ? (w0 >> s) | (w1 << (32 - s)) : w0;
+    }
+    if (q.n - lo < 32) bits &= (1u << (q.n - lo)) - 1u;
+    return j0 < 0 ? (bits << -j0) | ((1u << -j0) - 1u) : bits;
+}
+
+struct TcArgs {
+    Args a;
+    int box;            // rows per TMA box
+    int zero_row;       // a row outside the maps
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TcArgs t) {
+    using Sh = TcShape<D>;
+    constexpr uint32_t kTile = Sh::kTile;
+    constexpr int NST = Sh::kStages, SLABS = D / 64;
+    constexpr uint32_t kColS = 0, kColO = 256;
+    const Args& a = t.a;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ long long sums[kTcThreads];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* q_s = base;                              // two tiles; between segments, stream 1's O (fp32)
+    uint8_t* k_s = base + 2 * kTile;
+    uint8_t* v_s = k_s + NST * kTile;
+    TcBars& B = *reinterpret_cast<TcBars*>(v_s + NST * kTile);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* err = a.w.err;
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            q4d::mbar_init(q4d::smem_addr(&B.k_full[i]), 1);
+            q4d::mbar_init(q4d::smem_addr(&B.k_empty[i]), 1);
+            q4d::mbar_init(q4d::smem_addr(&B.v_full[i]), 1);
+            q4d::mbar_init(q4d::smem_addr(&B.v_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            q4d::mbar_init(q4d::smem_addr(&B.s_full[i]), 1);
+            q4d::mbar_init(q4d::smem_addr(&B.p_full[i]), 4);
+            B.odd[i] = 0;
+        }
+        q4d::mbar_init(q4d::smem_addr(&B.q_full), 8);
+        q4d::mbar_init(q4d::smem_addr(&B.o_full), 1);
+        q4d::mbar_init(q4d::smem_addr(&B.x_full), 4);
+        q4d::mbar_init(q4d::smem_addr(&B.x_empty), 4);
+        q4d::mbar_init(q4d::smem_addr(&B.drain), 1);
+        B.abort = 0;
+        q4d::fence_mbar_init();
+    }
+    if (warp == 11) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         q4d::smem_addr(&B.tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const long long line = line_scan(a, sums, kTcThreads);
+    const long long share = line_share(a, line), x0 = share * blockIdx.x, x1 = min(line, x0 + share);
+    q4t::fence_before();
+    __syncthreads();
+    q4t::fence_after();
+    q4d::pdl_trigger();
+    const uint32_t tmem = B.tmem_base;
+
+    if (x0 < x1) {
+        // Every role walks the same segments: the part of each job that lies
+        // in x0 .. x1 - 1.
+        Place p = line_find(a, sums, kTcThreads, x0);
+        long long x = x0;
+        uint32_t seg = 0;   // segments done
+        uint32_t tiles0 = 0;  // tiles before this segment
+
+        if (warp == 8 || warp == 9) {
+            // --------------------------------------------- key / value tiles
+            const bool keys = warp == 8;
+            uint64_t* full = keys ? B.k_full : B.v_full;
+            uint64_t* empty = keys ? B.k_empty : B.v_empty;
+            uint8_t* dst0 = keys ? k_s : v_s;
+            const CUtensorMap* map = keys ? &tmK : &tmV;
+            const int boxes = kTcKeys / t.box;
+            bool ok = true;
+            uint32_t kt = 0;
+            while (x < x1 && ok) {
+                const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
+                const int len = p.q.ctx + p.q.n;
+                for (int j = 0; j < T && ok; ++j, ++kt) {
+                    const uint32_t st = kt % NST;
+                    if (kt >= (uint32_t)NST) ok = __all_sync(0xffffffffu, tc_wait(B, empty[st], (kt / NST - 1) & 1, err));
+                    if (!ok) break;
+                    const uint32_t fb = q4d::smem_addr(&full[st]);
+                    if (lane == 0) q4d::mbar_arrive_expect_tx(fb, kTile);
+                    __syncwarp();
+                    for (int b = lane; b < boxes; b += 32) {
+                        const int key = (p.tile + j) * kTcKeys + b * t.box;
+                        int y = t.zero_row;
+                        if (key < len) {
+                            const long long at = q4p::row_at(a.w, p.s, key, p.h, 1);
+                            if (at >= 0) y = (int)at;
+                            else atomicOr(err, q4d::kErrDeviceCheck);
+                        }
+                        const uint32_t dst = q4d::smem_addr(dst0 + st * kTile) + (uint32_t)(b * t.box) * 128u;
+#pragma unroll
+                        for (int sl = 0; sl < SLABS; ++sl) q4t::tma_load_2d(dst + sl * 16384, map, 64 * sl, y, fb);
+                    }
+                }
+                x += T;
+                if (x < x1 && ok) next_job(a, p);
+            }
+            if (!ok) {  // copies still in flight land before the CTA can exit
+                for (uint32_t i = kt > (uint32_t)NST ? kt - NST : 0; i < kt; ++i)
+                    q4d::mbar_wait(q4d::smem_addr(&full[i % NST]), (i / NST) & 1, nullptr);
+            }
+        } else if (warp == 10) {
+            // ------------------------------------------------- MMA issue
+            if (lane == 0) {
+                const uint32_t id_s = q4t::idesc_f16_m128(kTcKeys, 0), id_o = q4t::idesc_f16_m128(D, 1);
+                const uint64_t dq = q4t::sw128_desc(q4d::smem_addr(q_s), 16, 1024);
+                const uint64_t dk = q4t::sw128_desc(q4d::smem_addr(k_s), 16, 1024);
+                const uint64_t dv = q4t::sw128_desc(q4d::smem_addr(v_s), 16384, 1024);
+                bool ok = true;
+                uint32_t n_p[2] = {0, 0};  // p_full phases passed
+                while (x < x1 && ok) {
+                    const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
+                    const bool two = (long long)p.q.n * a.G - (long long)p.rb * a.BM > 128;
+                    const int K = two ? 2 * T : T;
+                    ok = tc_wait(B, B.q_full, seg & 1, err);
+                    const auto issue_s = [&](int k) -> bool {
+                        const int i = k & 1, j = two ? k >> 1 : k;
+                        const uint32_t kt = tiles0 + j, st = kt % NST;
+                        if (!(two && i == 1) && !tc_wait(B, B.k_full[st], (kt / NST) & 1, err)) return false;
+                        q4t::fence_after();
+                        const uint64_t ad = dq + (uint64_t)((two ? i : 0) * (kTile / 16)), bd = dk + (uint64_t)(st * (kTile / 16));
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) / 16);
+                            q4t::mma_ss(tmem + kColS + 128 * i, ad + off, bd + off, id_s, kk > 0 ? 1u : 0u);
+                        }
+                        if (!two || i == 1) q4t::commit(q4d::smem_addr(&B.k_empty[st]));
+                        q4t::commit(q4d::smem_addr(&B.s_full[i]));
+                        return true;
+                    };
+                    if (ok) ok = issue_s(0);
+                    if (ok && K > 1) ok = issue_s(1);
+                    for (int k = 0; k < K && ok; ++k) {
+                        const int i = k & 1, j = two ? k >> 1 : k;
+                        const uint32_t kt = tiles0 + j, st = kt % NST;
+                        if (!tc_wait(B, B.p_full[i], n_p[i] & 1, err) ||
+                            (!(two && i == 1) && !tc_wait(B, B.v_full[st], (kt / NST) & 1, err))) {
+                            ok = false;
+                            break;
+                        }
+                        ++n_p[i];
+                        q4t::fence_after();
+                        const uint64_t bd = dv + (uint64_t)(st * (kTile / 16));
+                        const uint32_t pa = tmem + kColS + 128 * i, od = tmem + kColO + 128 * i;
+#pragma unroll
+                        for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                            q4t::mma_ts(od, pa + 8 * kk, bd + (uint64_t)(kk * 2048 / 16), id_o, (k >= 2 || kk > 0) ? 1u : 0u);
+                        if (!two || i == 1) q4t::commit(q4d::smem_addr(&B.v_empty[st]));
+                        if (k + 2 < K) ok = issue_s(k + 2);
+                    }
+                    if (ok) q4t::commit(q4d::smem_addr(&B.o_full));
+                    tiles0 += T;
+                    ++seg;
+                    x += T;
+                    if (x < x1 && ok) next_job(a, p);
+                }
+                if (!ok) B.abort = 1;
+                // every MMA this thread issued has finished before the CTA winds down
+                q4t::commit(q4d::smem_addr(&B.drain));
+                q4d::mbar_wait(q4d::smem_addr(&B.drain), 0, nullptr);
+            }
+        } else if (warp < 8) {
+            // ------------------------------------------------- softmax
+            const int i = warp >> 2, wr = warp & 3;  // stream, TMEM lane quarter
+            const int row = wr * 32 + lane;
+            const uint32_t lt = tmem + ((uint32_t)(wr * 32) << 16);
+            const uint32_t ts = lt + kColS + 128 * i, to = lt + kColO + 128 * i;
+            const float2 cc = make_float2(a.c, a.c);
+            uint32_t n_s = 0;      // s_full phases passed
+            uint32_t joins = 0;    // joined segments so far
+            bool ok = true;
+            while (x < x1) {
+                const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
+                const int R = (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM);
+                const bool two = R > 128;
+                const int r = (two ? 128 * i : 0) + row;  // row of the job
+                const bool live = r < R;  // the others run along with queries of zero
+                const int rr = p.rb * a.BM + (live ? r : 0), tok = rr / a.G;
+                const size_t q_row = (size_t)(p.q.start + tok), q_col = (size_t)(p.h * a.G + rr % a.G) * D;
+                const int steps = two ? T : (T - i + 1) / 2;
+                const bool join = !two && T > 1;
+                // the row's query into the stream's tile (both streams share stream
+                // 0's), once every warp of stream 0 has read the last join's part there
+                if (joins > 0) ok = __all_sync(0xffffffffu, ok && tc_wait(B, B.x_empty, (joins - 1) & 1, err));
+                if (!ok) break;
+                if (two || i == 0) {
+                    uint8_t* dst = q_s + (two ? i : 0) * kTile;
+                    const uint4* src = reinterpret_cast<const uint4*>(a.q + q_row * a.ldq + q_col);
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 w = live ? src[c] : make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw_off(row, c & 7)) = w;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.q_full));
+
+                float m = -INFINITY, l = 0.f;
+                for (int j = 0; j < steps; ++j) {
+                    const int tj = two ? j : 2 * j + i;  // tile of the segment
+                    const int key0 = (p.tile + tj) * kTcKeys;
+                    const uint32_t kt = tiles0 + tj, st = kt % NST;
+                    ok = __all_sync(0xffffffffu, tc_wait(B, B.s_full[i], n_s & 1, err));
+                    if (!ok) break;
+                    ++n_s;
+                    q4t::fence_after();
+                    uint32_t s[128];
+#pragma unroll
+                    for (int c = 0; c < 128; c += 16) q4t::ld16(ts + c, s + c);
+                    q4t::ld_wait();
+                    const bool tail = key0 + kTcKeys > p.q.ctx;  // the tile holds new rows, or the end
+                    if (tail) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t bits = sees_word(a, p.q, tok, key0 + 32 * w - p.q.ctx);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(bits >> e & 1u)) s[32 * w + e] = 0xff800000u;
+                        }
+                    }
+                    float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < 128; e += 8)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f)
+                            x4[f] = fmaxf(x4[f], fmaxf(__uint_as_float(s[e + f]), __uint_as_float(s[e + 4 + f])));
+                    const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * a.c;
+                    float corr = 1.f;
+                    if (mx > m + 8.f) {
+                        corr = m == -INFINITY ? 1.f : ex2(m - mx);  // nothing seen yet: O and l are zero
+                        m = mx;
+                    }
+                    if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+#pragma unroll
+                        for (int c0 = 0; c0 < D; c0 += 16) {
+                            uint32_t o[16];
+                            q4t::ld16(to + c0, o);
+                            q4t::ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                            q4t::st16(to + c0, o);
+                        }
+                    }
+                    const float sub = kTcShift - (m == -INFINITY ? 0.f : m);
+                    const float2 ss = make_float2(sub, sub);
+                    float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        float2 v = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, ss);
+                        v.x = ex2(v.x);
+                        v.y = ex2(v.y);
+                        if (e & 1) sum2 = __fadd2_rn(sum2, v);
+                        else sum = __fadd2_rn(sum, v);
+                        s[e] = pack2(v.x, v.y);
+                    }
+                    l = fmaf(l, corr, (sum.x + sum2.x) + (sum.y + sum2.y));
+#pragma unroll
+                    for (int c = 0; c < 64; c += 16) q4t::st16(ts + c, s + c);
+                    // A new row's value reaches only the rows that see it, and
+                    // what lies behind the sequence nobody: this thread clears
+                    // its row of the value tile there, or its infinities and
+                    // NaN, which the epilogue adds back where they are seen.
+                    if (tail && !(two && i == 1)) {
+                        ok = __all_sync(0xffffffffu, tc_wait(B, B.v_full[st], (kt / NST) & 1, err));
+                        if (!ok) break;
+                        const int nj = key0 + row - p.q.ctx;
+                        if (nj >= 0) {
+                            uint8_t* vt = v_s + st * kTile;
+                            bool found = false;
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c) {
+                                uint4* at = reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + sw_off(row, c & 7));
+                                if (nj >= p.q.n) {
+                                    *at = make_uint4(0, 0, 0, 0);
+                                    continue;
+                                }
+                                uint4 w = *at;
+                                uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                                bool bad = false;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if (!finite16((uint16_t)ws[e])) ws[e] &= 0xffff0000u, bad = true;
+                                    if (!finite16((uint16_t)(ws[e] >> 16))) ws[e] &= 0x0000ffffu, bad = true;
+                                }
+                                if (bad) *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+                                found |= bad;
+                            }
+                            if (found) B.odd[seg & 1] = (int)seg + 1;
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    }
+                    q4t::st_wait();
+                    q4t::fence_before();
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.p_full[i]));
+                }
+                if (!ok) break;
+                ok = __all_sync(0xffffffffu, tc_wait(B, B.o_full, seg & 1, err));
+                if (!ok) break;
+                q4t::fence_after();
+                const bool job_begin = p.tile == 0, job_end = p.tile + T == p.tiles;
+                const bool odd = B.odd[seg & 1] == (int)seg + 1;
+                if (join && i == 1) {
+                    // stream 1's part, fp32, into the query tiles' place (16-byte
+                    // chunks of a row spread over the banks); (m, l) into sums, done with
+                    float* ob = reinterpret_cast<float*>(q_s);
+                    constexpr int NC = D / 4;
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t o[16];
+                        q4t::ld16(to + c0, o);
+                        q4t::ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            *reinterpret_cast<uint4*>(ob + row * D + (((c0 / 4 + c) ^ (row & (NC - 1))) * 4)) =
+                                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    }
+                    sums[2 * row] = __float_as_int(m);
+                    sums[2 * row + 1] = __float_as_int(l);
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_full));
+                } else if (two || i == 0) {
+                    float f0 = 1.f, f1 = 0.f;
+                    if (join) {
+                        ok = __all_sync(0xffffffffu, tc_wait(B, B.x_full, joins & 1, err));
+                        if (!ok) break;
+                        const float m1 = __int_as_float((int)sums[2 * row]), l1 = __int_as_float((int)sums[2 * row + 1]);
+                        const float mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
+                        f0 = ex2(m - ms);
+                        f1 = ex2(m1 - ms);
+                        l = l * f0 + l1 * f1;
+                        m = mm;
+                    }
+                    const bool whole = job_begin && job_end;
+                    const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                    const int slot = 2 * blockIdx.x + (job_begin ? 1 : 0);
+                    const float* ob = reinterpret_cast<const float*>(q_s);
+                    constexpr int NC = D / 4;
+                    if (!whole && live) part_ml(a, slot)[r] = make_float2(m, l);
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t w[16];
+                        float o[16];
+                        q4t::ld16(to + c0, w);
+                        q4t::ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(w[e]);
+                        if (join) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const float4 v = *reinterpret_cast<const float4*>(
+                                    ob + row * D + (((c0 / 4 + c) ^ (row & (NC - 1))) * 4));
+                                o[4 * c] = fmaf(v.x, f1, o[4 * c] * f0);
+                                o[4 * c + 1] = fmaf(v.y, f1, o[4 * c + 1] * f0);
+                                o[4 * c + 2] = fmaf(v.z, f1, o[4 * c + 2] * f0);
+                                o[4 * c + 3] = fmaf(v.w, f1, o[4 * c + 3] * f0);
+                            }
+                        }
+                        if (odd && live) {
+                            const int n0 = max(0, p.tile * kTcKeys - p.q.ctx), n1 = min(p.q.n, (p.tile + T) * kTcKeys - p.q.ctx);
+                            for (int nj = n0; nj < n1; ++nj) {
+                                if (!sees(a, p.q.start, tok, nj)) continue;
+                                const long long at = q4p::row_at(a.w, p.s, p.q.ctx + nj, p.h, D);
+                                if (at < 0) continue;
+                                for (int e = 0; e < 16; ++e) {
+                                    const uint16_t v = a.w.v[at + c0 + e];
+                                    if (!finite16(v)) o[e] += __half2float(__ushort_as_half(v));
+                                }
+                            }
+                        }
+                        if (!live) continue;
+                        if (whole) {
+                            uint32_t y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
+                            uint4* dst = reinterpret_cast<uint4*>(a.out + q_row * a.ldo + q_col + c0);
+                            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(part_o<D>(a, slot) + (size_t)r * D + c0);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                    if (join) {
+                        __syncwarp();
+                        if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_empty));
+                    }
+                }
+                q4t::fence_before();  // O is read before the next segment's queries release its MMAs
+                if (join) ++joins;
+                tiles0 += T;
+                ++seg;
+                x += T;
+                if (x < x1) next_job(a, p);
+            }
+        }
+    }
+    q4t::fence_before();
+    __syncthreads();
+    if (warp == 11) {
+        q4t::fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <int D>
+q4_status launch_tc(Args& a, const q4_paged_cache& c, void* workspace, int sms, int box, cudaStream_t s) {
+    TcArgs t;
+    a.ctas = sms < kMaxTcCtas ? sms : kMaxTcCtas;
+    a.BM = kTcRows;
+    a.KT = kTcKeys;
+    place_parts<D>(a, workspace);
+    t.a = a;
+    t.box = box;
+    const uint64_t rows = (uint64_t)c.n_pages * c.n_kv_heads * c.page_size;
+    t.zero_row = (int)rows;
+    CUtensorMap tmK, tmV;
+    q4_status st;
+    if ((st = q4i::make_map(&tmK, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.k, D, rows, D * 2, 64, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_128B)) != Q4_OK)
+        return st;
+    if ((st = q4i::make_map(&tmV, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.v, D, rows, D * 2, 64, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_128B)) != Q4_OK)
+        return st;
+    static std::atomic<int> marks[64];
+    cudaError_t e = q4i::ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_tc_kernel<D>), marks, (int)TcShape<D>::kSmem);
+    if (e == cudaSuccess) {
+        tree_attn_tc_kernel<D><<<a.ctas, kTcThreads, TcShape<D>::kSmem, s>>>(tmK, tmV, t);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) e = launch_join<D>(a, s);
+    return e == cudaSuccess ? Q4_OK : q4i::cuda_fail(e, "q4_tree_attention launch");
 }
 
 }  // namespace q4x
@@ -601,14 +1192,18 @@ extern "C" q4_status q4_tree_attention(const q4_tree_attention_desc* desc, q4_st
     a.ldq = d.ldq;
     a.ldo = d.ldo;
     a.G = G;
-    a.part = static_cast<float*>(d.workspace);
     // rows per job: the average sequence's, by 16, 32 or 64
     const long long avg = ((long long)d.rows * G + d.cache.n_seqs - 1) / d.cache.n_seqs;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int box = d.cache.page_size % 128 == 0 ? 128 : d.cache.page_size & -d.cache.page_size;
+    const long long pool_rows = (long long)d.cache.n_pages * d.cache.n_kv_heads * d.cache.page_size;
+    if (avg > 32 && box >= 8 && pool_rows < (1ll << 31) - 1)
+        return D == 128 ? q4x::launch_tc<128>(a, d.cache, d.workspace, dev->sms, box, s)
+                        : q4x::launch_tc<64>(a, d.cache, d.workspace, dev->sms, box, s);
     cudaError_t e;
     if (D == 128)
-        e = avg <= 16 ? q4x::launch<128, 1>(a, dev->sms, s) : avg <= 32 ? q4x::launch<128, 2>(a, dev->sms, s) : q4x::launch<128, 4>(a, dev->sms, s);
+        e = avg <= 16 ? q4x::launch<128, 1>(a, d.workspace, dev->sms, s) : avg <= 32 ? q4x::launch<128, 2>(a, d.workspace, dev->sms, s) : q4x::launch<128, 4>(a, d.workspace, dev->sms, s);
     else
-        e = avg <= 16 ? q4x::launch<64, 1>(a, dev->sms, s) : avg <= 32 ? q4x::launch<64, 2>(a, dev->sms, s) : q4x::launch<64, 4>(a, dev->sms, s);
+        e = avg <= 16 ? q4x::launch<64, 1>(a, d.workspace, dev->sms, s) : avg <= 32 ? q4x::launch<64, 2>(a, d.workspace, dev->sms, s) : q4x::launch<64, 4>(a, d.workspace, dev->sms, s);
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "q4_tree_attention launch");
 }

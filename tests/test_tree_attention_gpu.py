@@ -104,6 +104,19 @@ CASES = [
 ]
 
 
+# rows per kv head around the job sizes of both kernels, pages around its boxes
+CASES += [
+    (128, 2, 4, 64, [260, 127, 128], [32, 32, 32]),
+    (128, 1, 3, 128, [129], [43]),
+    (128, 1, 1, 8, [40, 0, 900], [128, 129, 64]),
+    (64, 1, 1, 32, [300, 1], [256, 257]),
+    (64, 2, 8, 16, [5000], [16]),
+    (128, 8, 2, 256, [3000, 20], [33, 70]),
+    (128, 2, 2, 40, [1000, 255], [65, 64]),
+    (64, 1, 5, 384, [11], [300]),
+]
+
+
 @pytest.mark.parametrize("kind", ["causal", "tree", "random", "nothing"])
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_attention(case, kind):
@@ -141,7 +154,7 @@ def test_rows_past_the_mask_are_seen_by_nobody():
     check(out, b, q, a, A)
 
 
-@pytest.mark.parametrize("d,G", [(128, 2), (64, 8), (128, 16)])
+@pytest.mark.parametrize("d,G", [(128, 1), (128, 2), (64, 8), (128, 16), (64, 1)])
 @pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan, 65504.0])
 def test_values_that_a_row_does_not_see_do_not_reach_it(d, G, value):
     # one branch of a tree holds infinities or NaN in its keys and values
