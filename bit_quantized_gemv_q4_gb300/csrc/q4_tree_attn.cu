@@ -634,12 +634,12 @@ cudaError_t launch(Args& a, void* workspace, int sms, cudaStream_t s) {
 //   else: both streams have the same rows and alternate tiles, and their
 //     (m, l, O) are joined at the end.
 // Per stream a warpgroup computes the softmax (thread = row = TMEM lane) while
-// the tensor cores work for the other stream; one thread issues, in order,
-//   S(0) S(1) | P V(0) S(2) | P V(1) S(3) | ...   (numbers: steps, stream = step % 2)
+// the tensor cores work for the other stream, and one thread issues, in order,
+//   S(0) | P V(0) S(1) | P V(1) S(2) | ...
 // S = Q K^T (128 x 128, Q and K from shared memory) and O += P V (P, fp16,
 // from tensor memory over the scores it came from, V read MN-major).  MMAs of
-// one thread run in order, so S(k + 2) may overwrite what P V(k) reads, and
-// the commit behind S(k + 2) tells the softmax that O holds step k's product.
+// one thread run in order, so S(k + 1) may overwrite what P V(k) reads, and
+// the commit behind S(k + 1) tells the softmax that O holds step k's product.
 // Tensor memory (512 columns): S 0 and 1 (128 each), O 0 and 1.
 // The reference maximum of a row moves only when its maximum exceeds it by
 // more than 8 (a factor 2^8); then O and l are rescaled.  With kTcShift P
@@ -648,7 +648,7 @@ cudaError_t launch(Args& a, void* workspace, int sms, cudaStream_t s) {
 // of two, 8 .. 128, that divides the page): a box lies in one page.  A page
 // that does not exist is read outside the map, where TMA fills in zeros.
 constexpr int kTcKeys = 128;
-constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10: MMA, 11: TMEM
+constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1
 constexpr float kTcShift = 7.f;
 
 template <int D>
@@ -660,7 +660,8 @@ struct TcShape {
 
 struct TcBars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], p_full[2], q_full, o_full, x_full, x_empty, drain;
+    uint64_t v_clean[4];  // two row streams: stream 0 has cleared what stream 1's products must not meet
+    uint64_t s_full[2], p_full[2], q_full, o_full, x_full, x_empty, drain[2];
     uint32_t tmem_base;
     volatile int abort;
     volatile int odd[2];  // last segment (by parity) that met infinities or NaN among its new rows' values
@@ -677,6 +678,12 @@ __device__ __forceinline__ bool tc_wait(TcBars& B, uint64_t& bar, uint32_t parit
 
 __device__ __forceinline__ uint32_t sw_off(int r, int c) {  // row r, 16-byte chunk c < 8 of a swizzled slab
     return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -732,20 +739,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             q4d::mbar_init(q4d::smem_addr(&B.k_full[i]), 1);
-            q4d::mbar_init(q4d::smem_addr(&B.k_empty[i]), 1);
+            q4d::mbar_init(q4d::smem_addr(&B.k_empty[i]), 2);  // both streams' MMAs
             q4d::mbar_init(q4d::smem_addr(&B.v_full[i]), 1);
-            q4d::mbar_init(q4d::smem_addr(&B.v_empty[i]), 1);
+            q4d::mbar_init(q4d::smem_addr(&B.v_empty[i]), 2);
+            q4d::mbar_init(q4d::smem_addr(&B.v_clean[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             q4d::mbar_init(q4d::smem_addr(&B.s_full[i]), 1);
             q4d::mbar_init(q4d::smem_addr(&B.p_full[i]), 4);
+            q4d::mbar_init(q4d::smem_addr(&B.drain[i]), 1);
             B.odd[i] = 0;
         }
         q4d::mbar_init(q4d::smem_addr(&B.q_full), 8);
-        q4d::mbar_init(q4d::smem_addr(&B.o_full), 1);
+        q4d::mbar_init(q4d::smem_addr(&B.o_full), 2);
         q4d::mbar_init(q4d::smem_addr(&B.x_full), 4);
         q4d::mbar_init(q4d::smem_addr(&B.x_empty), 4);
-        q4d::mbar_init(q4d::smem_addr(&B.drain), 1);
         B.abort = 0;
         q4d::fence_mbar_init();
     }
@@ -811,66 +819,91 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (uint32_t i = kt > (uint32_t)NST ? kt - NST : 0; i < kt; ++i)
                     q4d::mbar_wait(q4d::smem_addr(&full[i % NST]), (i / NST) & 1, nullptr);
             }
-        } else if (warp == 10) {
+        } else if (warp >= 10) {
             // ------------------------------------------------- MMA issue
-            if (lane == 0) {
-                const uint32_t id_s = q4t::idesc_f16_m128(kTcKeys, 0), id_o = q4t::idesc_f16_m128(D, 1);
-                const uint64_t dq = q4t::sw128_desc(q4d::smem_addr(q_s), 16, 1024);
-                const uint64_t dk = q4t::sw128_desc(q4d::smem_addr(k_s), 16, 1024);
-                const uint64_t dv = q4t::sw128_desc(q4d::smem_addr(v_s), 16384, 1024);
-                bool ok = true;
-                uint32_t n_p[2] = {0, 0};  // p_full phases passed
-                while (x < x1 && ok) {
-                    const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
-                    const bool two = (long long)p.q.n * a.G - (long long)p.rb * a.BM > 128;
-                    const int K = two ? 2 * T : T;
-                    ok = tc_wait(B, B.q_full, seg & 1, err);
-                    const auto issue_s = [&](int k) -> bool {
-                        const int i = k & 1, j = two ? k >> 1 : k;
-                        const uint32_t kt = tiles0 + j, st = kt % NST;
-                        if (!(two && i == 1) && !tc_wait(B, B.k_full[st], (kt / NST) & 1, err)) return false;
-                        q4t::fence_after();
-                        const uint64_t ad = dq + (uint64_t)((two ? i : 0) * (kTile / 16)), bd = dk + (uint64_t)(st * (kTile / 16));
+            // One warp per stream (a completed wait costs an issuing thread
+            // about as much as four MMAs, so the streams' waits run side by
+            // side), one elected lane issuing.
+            const int i = warp - 10;
+            const bool leader = elect_one();
+            const uint32_t id_s = q4t::idesc_f16_m128(kTcKeys, 0), id_o = q4t::idesc_f16_m128(D, 1);
+            const uint64_t dq = q4t::sw128_desc(q4d::smem_addr(q_s), 16, 1024);
+            const uint64_t dk = q4t::sw128_desc(q4d::smem_addr(k_s), 16, 1024);
+            const uint64_t dv = q4t::sw128_desc(q4d::smem_addr(v_s), 16384, 1024);
+            const uint32_t sd = tmem + kColS + 128 * i, od = tmem + kColO + 128 * i;
+            bool ok = true;
+            uint32_t n_p = 0;    // p_full phases passed
+            uint32_t cleans = 0;  // parity of the v_clean phases passed, a bit per stage
+            while (x < x1 && ok) {
+                const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
+                const bool two = (long long)p.q.n * a.G - (long long)p.rb * a.BM > 128;
+                const int steps = two ? T : (T - i + 1) / 2;
+                const uint64_t ad = dq + (uint64_t)((two ? i : 0) * (kTile / 16));
+                const auto tile_of = [&](int k) { return tiles0 + (two ? k : 2 * k + i); };
+                // S of step k (its keys have landed)
+                const auto issue_s = [&](int k) {
+                    const uint32_t st = tile_of(k) % NST;
+                    const uint64_t bd = dk + (uint64_t)(st * (kTile / 16));
+                    if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk) {
                             const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) / 16);
-                            q4t::mma_ss(tmem + kColS + 128 * i, ad + off, bd + off, id_s, kk > 0 ? 1u : 0u);
+                            q4t::mma_ss(sd, ad + off, bd + off, id_s, kk > 0 ? 1u : 0u);
                         }
-                        if (!two || i == 1) q4t::commit(q4d::smem_addr(&B.k_empty[st]));
                         q4t::commit(q4d::smem_addr(&B.s_full[i]));
-                        return true;
-                    };
-                    if (ok) ok = issue_s(0);
-                    if (ok && K > 1) ok = issue_s(1);
-                    for (int k = 0; k < K && ok; ++k) {
-                        const int i = k & 1, j = two ? k >> 1 : k;
-                        const uint32_t kt = tiles0 + j, st = kt % NST;
-                        if (!tc_wait(B, B.p_full[i], n_p[i] & 1, err) ||
-                            (!(two && i == 1) && !tc_wait(B, B.v_full[st], (kt / NST) & 1, err))) {
-                            ok = false;
-                            break;
-                        }
-                        ++n_p[i];
-                        q4t::fence_after();
-                        const uint64_t bd = dv + (uint64_t)(st * (kTile / 16));
-                        const uint32_t pa = tmem + kColS + 128 * i, od = tmem + kColO + 128 * i;
+                        q4t::commit(q4d::smem_addr(&B.k_empty[st]));
+                        if (!two) q4t::commit(q4d::smem_addr(&B.k_empty[st]));  // the other stream's share
+                    }
+                    __syncwarp();
+                };
+                const auto wait_k = [&](int k) {
+                    const uint32_t kt = tile_of(k);
+                    return tc_wait(B, B.k_full[kt % NST], (kt / NST) & 1, err);
+                };
+                ok = tc_wait(B, B.q_full, seg & 1, err);
+                if (ok && steps > 0) {
+                    ok = wait_k(0);
+                    q4t::fence_after();
+                    if (ok) issue_s(0);
+                }
+                for (int k = 0; k < steps && ok; ++k) {
+                    const uint32_t kt = tile_of(k), st = kt % NST;
+                    const bool more = k + 1 < steps;
+                    ok = tc_wait(B, B.v_full[st], (kt / NST) & 1, err) && (!more || wait_k(k + 1)) &&
+                         tc_wait(B, B.p_full[i], n_p & 1, err);
+                    if (ok && two && i == 1 && (int)(p.tile + k + 1) * kTcKeys > p.q.ctx) {
+                        ok = tc_wait(B, B.v_clean[st], cleans >> st & 1, err);
+                        cleans ^= 1u << st;
+                    }
+                    if (!ok) break;
+                    ++n_p;
+                    q4t::fence_after();
+                    const uint64_t bd = dv + (uint64_t)(st * (kTile / 16));
+                    if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                            q4t::mma_ts(od, pa + 8 * kk, bd + (uint64_t)(kk * 2048 / 16), id_o, (k >= 2 || kk > 0) ? 1u : 0u);
-                        if (!two || i == 1) q4t::commit(q4d::smem_addr(&B.v_empty[st]));
-                        if (k + 2 < K) ok = issue_s(k + 2);
+                            q4t::mma_ts(od, sd + 8 * kk, bd + (uint64_t)(kk * 2048 / 16), id_o, (k > 0 || kk > 0) ? 1u : 0u);
                     }
-                    if (ok) q4t::commit(q4d::smem_addr(&B.o_full));
-                    tiles0 += T;
-                    ++seg;
-                    x += T;
-                    if (x < x1 && ok) next_job(a, p);
+                    __syncwarp();
+                    if (more) issue_s(k + 1);
+                    if (leader) {
+                        q4t::commit(q4d::smem_addr(&B.v_empty[st]));
+                        if (!two) q4t::commit(q4d::smem_addr(&B.v_empty[st]));
+                        if (!more) q4t::commit(q4d::smem_addr(&B.o_full));
+                    }
+                    __syncwarp();
                 }
-                if (!ok) B.abort = 1;
-                // every MMA this thread issued has finished before the CTA winds down
-                q4t::commit(q4d::smem_addr(&B.drain));
-                q4d::mbar_wait(q4d::smem_addr(&B.drain), 0, nullptr);
+                if (steps == 0 && leader) q4d::mbar_arrive(q4d::smem_addr(&B.o_full));
+                tiles0 += T;
+                ++seg;
+                x += T;
+                if (x < x1 && ok) next_job(a, p);
             }
+            if (!ok) B.abort = 1;
+            // every MMA this warp issued has finished before the CTA winds down
+            if (leader) q4t::commit(q4d::smem_addr(&B.drain[i]));
+            __syncwarp();
+            q4d::mbar_wait(q4d::smem_addr(&B.drain[i]), 0, nullptr);
         } else if (warp < 8) {
             // ------------------------------------------------- softmax
             const int i = warp >> 2, wr = warp & 3;  // stream, TMEM lane quarter
@@ -1001,6 +1034,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             if (found) B.odd[seg & 1] = (int)seg + 1;
                         }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        if (two) {
+                            __syncwarp();
+                            if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.v_clean[st]));
+                        }
                     }
                     q4t::st_wait();
                     q4t::fence_before();
