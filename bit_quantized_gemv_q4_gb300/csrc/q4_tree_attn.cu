@@ -686,6 +686,28 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// 32 consecutive 32-bit columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -871,7 +893,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const bool more = k + 1 < steps;
                     ok = tc_wait(B, B.v_full[st], (kt / NST) & 1, err) && (!more || wait_k(k + 1)) &&
                          tc_wait(B, B.p_full[i], n_p & 1, err);
-                    if (ok && two && i == 1 && (int)(p.tile + k + 1) * kTcKeys > p.q.ctx) {
+                    if (ok && two && i == 1 && (p.tile + k + 1) * kTcKeys > p.q.ctx + (a.mask ? 0 : p.rb * a.BM / a.G + 1)) {
                         ok = tc_wait(B, B.v_clean[st], cleans >> st & 1, err);
                         cleans ^= 1u << st;
                     }
@@ -924,6 +946,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const size_t q_row = (size_t)(p.q.start + tok), q_col = (size_t)(p.h * a.G + rr % a.G) * D;
                 const int steps = two ? T : (T - i + 1) / 2;
                 const bool join = !two && T > 1;
+                // new rows that every row of the job sees
+                const int all_see = a.mask ? 0 : p.rb * a.BM / a.G + 1;
                 // the row's query into the stream's tile (both streams share stream
                 // 0's), once every warp of stream 0 has read the last join's part there
                 if (joins > 0) ok = __all_sync(0xffffffffu, ok && tc_wait(B, B.x_empty, (joins - 1) & 1, err));
@@ -950,58 +974,74 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!ok) break;
                     ++n_s;
                     q4t::fence_after();
-                    uint32_t s[128];
-#pragma unroll
-                    for (int c = 0; c < 128; c += 16) q4t::ld16(ts + c, s + c);
-                    q4t::ld_wait();
-                    const bool tail = key0 + kTcKeys > p.q.ctx;  // the tile holds new rows, or the end
-                    if (tail) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t bits = sees_word(a, p.q, tok, key0 + 32 * w - p.q.ctx);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(bits >> e & 1u)) s[32 * w + e] = 0xff800000u;
-                        }
-                    }
+                    // The row in halves, so that it fits the registers: the
+                    // second one's maximum, the first one's, P of the first
+                    // (over scores that are read), the second one again.
+                    // Some row of the job does not see some position of the tile:
+                    const bool tail = key0 + kTcKeys > p.q.ctx + all_see;
+                    uint32_t s[64];
                     float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    const auto load_half = [&](int h) {
+                        ld32(ts + 64 * h, s);
+                        ld32(ts + 64 * h + 32, s + 32);
+                        q4t::ld_wait();
+                        if (tail) {
 #pragma unroll
-                    for (int e = 0; e < 128; e += 8)
+                            for (int w = 0; w < 2; ++w) {
+                                const uint32_t bits = sees_word(a, p.q, tok, key0 + 64 * h + 32 * w - p.q.ctx);
+                                if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
 #pragma unroll
-                        for (int f = 0; f < 4; ++f)
-                            x4[f] = fmaxf(x4[f], fmaxf(__uint_as_float(s[e + f]), __uint_as_float(s[e + 4 + f])));
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(bits >> e & 1u)) s[32 * w + e] = 0xff800000u;
+                            }
+                        }
+                    };
+                    const auto max_half = [&]() {
+#pragma unroll
+                        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f)
+                                x4[f] = fmaxf(x4[f], fmaxf(__uint_as_float(s[e + f]), __uint_as_float(s[e + 4 + f])));
+                    };
+                    load_half(1);
+                    max_half();
+                    load_half(0);
+                    max_half();
                     const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * a.c;
                     float corr = 1.f;
                     if (mx > m + 8.f) {
                         corr = m == -INFINITY ? 1.f : ex2(m - mx);  // nothing seen yet: O and l are zero
                         m = mx;
                     }
-                    if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-#pragma unroll
-                        for (int c0 = 0; c0 < D; c0 += 16) {
-                            uint32_t o[16];
-                            q4t::ld16(to + c0, o);
-                            q4t::ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-                            q4t::st16(to + c0, o);
-                        }
-                    }
                     const float sub = kTcShift - (m == -INFINITY ? 0.f : m);
                     const float2 ss = make_float2(sub, sub);
                     float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
+                    const auto exp_half = [&](int h) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        float2 v = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, ss);
-                        v.x = ex2(v.x);
-                        v.y = ex2(v.y);
-                        if (e & 1) sum2 = __fadd2_rn(sum2, v);
-                        else sum = __fadd2_rn(sum, v);
-                        s[e] = pack2(v.x, v.y);
-                    }
+                        for (int e = 0; e < 32; ++e) {
+                            float2 v = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, ss);
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            if (e & 1) sum2 = __fadd2_rn(sum2, v);
+                            else sum = __fadd2_rn(sum, v);
+                            s[e] = pack2(v.x, v.y);
+                        }
+                        st32(ts + 32 * h, s);
+                    };
+                    exp_half(0);
+                    load_half(1);
+                    exp_half(1);
                     l = fmaf(l, corr, (sum.x + sum2.x) + (sum.y + sum2.y));
+                    if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 16) q4t::st16(ts + c, s + c);
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            ld32(to + c0, s);
+                            q4t::ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * corr);
+                            st32(to + c0, s);
+                        }
+                    }
                     // A new row's value reaches only the rows that see it, and
                     // what lies behind the sequence nobody: this thread clears
                     // its row of the value tile there, or its infinities and
