@@ -49,9 +49,12 @@ struct Args {
     uint16_t* out;
     long long ldq, ldo;
     int G;       // query heads per kv head
+    q4p::PageDiv by_g;  // division by G
     float c;     // scale * log2(e)
     int ctas;    // CTAs that share the line
-    int BM, KT;  // rows of a job, positions of a tile
+    int BM, KT;  // rows of a job, positions of a tile (1 << KT_log2)
+    int KT_log2;
+    int cost_full, cost_half;  // units of a tile for a row block with more than BM / 2 rows, and for others
     float* po;   // workspace: [2 CTAs][BM][D] outputs
     float2* pml; // [2 CTAs][BM] (m, l)
 };
@@ -66,24 +69,31 @@ __device__ __forceinline__ float2* part_ml(const Args& a, int slot) { return a.p
 // Tiles of a sequence's row block `rb`: with a mask every row may see every
 // new row; causally the block's last token is the last key.
 __device__ __forceinline__ int block_tiles(const Args& a, const Seq& q, int rb) {
-    const int last = min(((rb + 1) * a.BM - 1) / a.G, q.n - 1);
+    const int last = min((int)q4p::page_of(a.by_g, (rb + 1) * a.BM - 1), q.n - 1);
     const int keys = q.ctx + (a.mask ? q.n : last + 1);
-    return (keys + a.KT - 1) / a.KT;
+    return (keys + a.KT - 1) >> a.KT_log2;
 }
 
-// Tiles of one head of a sequence (all row blocks).
-__device__ __forceinline__ long long head_tiles(const Args& a, const Seq& q) {
+// A tile's units of the line: what it costs.
+__device__ __forceinline__ int tile_cost(const Args& a, const Seq& q, int rb) {
+    return q.n * a.G - rb * a.BM > a.BM / 2 ? a.cost_full : a.cost_half;
+}
+
+// Units of one head of a sequence (all row blocks).
+__device__ __forceinline__ long long head_units(const Args& a, const Seq& q) {
     if (q.n <= 0) return 0;
-    const int blocks = (int)(((long long)q.n * a.G + a.BM - 1) / a.BM);
-    if (a.mask || blocks == 1) return (long long)blocks * block_tiles(a, q, blocks - 1);
-    long long t = 0;
-    for (int b = 0; b < blocks; ++b) t += block_tiles(a, q, b);
+    const int blocks = (int)((unsigned)(q.n * a.G + a.BM - 1) / (unsigned)a.BM);
+    const int tiles = block_tiles(a, q, blocks - 1);
+    long long t = (long long)tiles * tile_cost(a, q, blocks - 1);
+    if (a.mask) return t + (long long)(blocks - 1) * tiles * a.cost_full;
+    for (int b = 0; b < blocks - 1; ++b) t += block_tiles(a, q, b) * a.cost_full;
     return t;
 }
 
-// A place in the line of tiles.
+// A job's tiles tile .. tiles - 1; tile t stands at unit start + t * cost of the line.
 struct Place {
-    int s, h, rb, tile, tiles;  // tile of the job's `tiles`
+    int s, h, rb, tile, tiles, cost;
+    long long start;
     Seq q;
 };
 
@@ -97,7 +107,7 @@ __device__ __forceinline__ long long line_scan(const Args& a, long long* sums, i
         bool bad;
         const Seq q = q4p::seq_of(a.w, s, bad);
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
-        t += head_tiles(a, q);
+        t += head_units(a, q);
     }
     t *= a.w.H;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -115,13 +125,16 @@ __device__ __forceinline__ long long line_scan(const Args& a, long long* sums, i
     return sums[threads - 1];
 }
 
-// A CTA's share of the line: as even as whole tiles allow.
+// A CTA's share of the line (CTA c: units c * share ..): a tile belongs to the
+// CTA in whose share its first unit lies.  At least a tile, so that a CTA
+// between two others of a job has a part of it.
 __device__ __forceinline__ long long line_share(const Args& a, long long line) {
-    if (line < (1ll << 31)) return ((unsigned)line + (unsigned)a.ctas - 1) / (unsigned)a.ctas;
-    return (line + a.ctas - 1) / a.ctas;
+    const long long s = line < (1ll << 31) ? (long long)(((unsigned)line + (unsigned)a.ctas - 1) / (unsigned)a.ctas)
+                                           : (line + a.ctas - 1) / a.ctas;
+    return max(s, (long long)a.cost_full);
 }
 
-// Place of tile x (x < the line's length).
+// The job that holds unit x (x < the line's length), from its first tile on.
 __device__ __forceinline__ Place line_find(const Args& a, const long long* sums, int threads, long long x) {
     int lo = 0, hi = threads - 1;  // first thread whose running sum exceeds x
     while (lo < hi) {
@@ -129,32 +142,35 @@ __device__ __forceinline__ Place line_find(const Args& a, const long long* sums,
         if (sums[mid] > x) hi = mid;
         else lo = mid + 1;
     }
-    if (lo > 0) x -= sums[lo - 1];
+    long long rest = lo > 0 ? x - sums[lo - 1] : x;
     const int per = (a.w.S + threads - 1) / threads;
     Place p;
     bool bad;
     long long head = 0;
     for (p.s = lo * per;; ++p.s) {
         p.q = q4p::seq_of(a.w, p.s, bad);
-        head = head_tiles(a, p.q);
-        if (x < head * a.w.H) break;
-        x -= head * a.w.H;
+        head = head_units(a, p.q);
+        if (rest < head * a.w.H) break;
+        rest -= head * a.w.H;
     }
-    p.h = x < (1ll << 31) && head < (1ll << 31) ? (int)((unsigned)x / (unsigned)head) : (int)(x / head);
-    x -= p.h * head;
+    p.h = rest < (1ll << 31) && head < (1ll << 31) ? (int)((unsigned)rest / (unsigned)head) : (int)(rest / head);
+    rest -= p.h * head;
     for (p.rb = 0;; ++p.rb) {
         p.tiles = block_tiles(a, p.q, p.rb);
-        if (x < p.tiles) break;
-        x -= p.tiles;
+        p.cost = tile_cost(a, p.q, p.rb);
+        if (rest < (long long)p.tiles * p.cost) break;
+        rest -= (long long)p.tiles * p.cost;
     }
-    p.tile = (int)x;
+    p.start = x - rest;
+    p.tile = 0;
     return p;
 }
 
-// The next job's first tile (there is one).
+// The next job (there is one).
 __device__ __forceinline__ void next_job(const Args& a, Place& p) {
+    p.start += (long long)p.tiles * p.cost;
     p.tile = 0;
-    if ((long long)++p.rb * a.BM >= (long long)p.q.n * a.G) {
+    if (++p.rb * a.BM >= p.q.n * a.G) {
         p.rb = 0;
         if (++p.h == a.w.H) {
             p.h = 0;
@@ -165,12 +181,44 @@ __device__ __forceinline__ void next_job(const Args& a, Place& p) {
         }
     }
     p.tiles = block_tiles(a, p.q, p.rb);
+    p.cost = tile_cost(a, p.q, p.rb);
 }
 
-// The next tile's place (there is one).
-__device__ __forceinline__ void step(const Args& a, Place& p) {
-    if (++p.tile == p.tiles) next_job(a, p);
+// First tile of the job at or behind unit x: 0 .. tiles.
+__device__ __forceinline__ int tile_at(const Place& p, long long x) {
+    const long long d = x - p.start;
+    if (d <= 0) return 0;
+    if (d >= (long long)p.tiles * p.cost) return p.tiles;
+    return (int)(((unsigned)d + (unsigned)p.cost - 1) / (unsigned)p.cost);
 }
+
+// A CTA's part x0 .. x1 of the line as segments, each a run of one job's
+// tiles p.tile .. end - 1.
+struct Walk {
+    Place p;
+    int end;
+    long long x1, line;
+    // false: the CTA has no tiles
+    __device__ __forceinline__ bool begin(const Args& a, const long long* sums, int threads, long long line_) {
+        line = line_;
+        const long long share = line_share(a, line), x0 = share * blockIdx.x;
+        x1 = min(line, x0 + share);
+        if (x0 >= x1) return false;
+        p = line_find(a, sums, threads, x0);
+        p.tile = tile_at(p, x0);
+        if (p.tile == p.tiles) {  // x0 lies in the last tile's units
+            if (p.start + (long long)p.tiles * p.cost >= x1) return false;
+            next_job(a, p);
+        }
+        end = tile_at(p, x1);
+        return true;
+    }
+    __device__ __forceinline__ bool more() const { return p.start + (long long)p.tiles * p.cost < x1; }
+    __device__ __forceinline__ void next(const Args& a) {
+        next_job(a, p);
+        end = tile_at(p, x1);
+    }
+};
 
 // ----------------------------------------------------------------- devices ---
 template <int D>
@@ -235,12 +283,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
     constexpr uint32_t TB = kKeys * D * 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, u = lane & 3;
     const int wm = warp / WN, wn = warp % WN;
-    const long long line = line_scan(a, sums, kThreads);
-    const long long share = line_share(a, line), x0 = share * blockIdx.x, x1 = min(line, x0 + share);
+    Walk cur;
+    const bool any = cur.begin(a, sums, kThreads, line_scan(a, sums, kThreads));
     q4d::pdl_trigger();  // the joining kernel's blocks may start; they wait for this grid's end
-    if (x0 >= x1) return;
-    Place cur = line_find(a, sums, kThreads, x0);
-    Place ld = cur;
+    if (!any) return;
+    Walk ld = cur;
     const uint32_t sm0 = q4d::smem_addr(smem);
 
     // Tile `ld` into stage st: a thread takes one 16-byte chunk column of
@@ -249,14 +296,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
     auto load = [&](int st) {
         const uint32_t kb = sm0 + (uint32_t)st * 2u * TB, vb = kb + TB;
         const int c = tid % NCH, r0 = tid / NCH;
-        const int len = ld.q.ctx + ld.q.n;
+        const int len = ld.p.q.ctx + ld.p.q.n;
 #pragma unroll
         for (int i = 0; i < kKeys * NCH / kThreads; ++i) {
             const int r = r0 + i * (kThreads / NCH);
-            const int key = ld.tile * kKeys + r;
+            const int key = ld.p.tile * kKeys + r;
             long long at = -1;
             if (key < len) {
-                at = q4p::row_at(a.w, ld.s, key, ld.h, D);
+                at = q4p::row_at(a.w, ld.p.s, key, ld.p.h, D);
                 if (at < 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
             }
             const bool live = at >= 0;
@@ -265,38 +312,39 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             cp16(vb + swz<D>(r, c), a.w.v + off, live);
         }
     };
-    long long loaded = x0;
+    bool more = true;  // tiles to load
+    const auto load_next = [&](int st) {
+        if (!more) return;
+        load(st);
+        if (++ld.p.tile == ld.end) {
+            more = ld.more();
+            if (more) ld.next(a);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-        if (loaded < x1) {
-            load(i);
-            if (++loaded < x1) step(a, ld);
-        }
+        load_next(i);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
 
     uint32_t qf[KS][4];
     float o[DN][4], m[2], l[2];
     bool fresh = true;   // the job's first tile in this CTA
-    bool begun = cur.tile == 0;  // ... and in the line
+    bool begun = cur.p.tile == 0;  // ... and in the line
     const int row0 = wm * 16 + g;  // this thread's rows of the job: row0, row0 + 8
-    for (long long x = x0; x < x1; ++x) {
-        const int st = (int)((x - x0) % kStages);
+    for (int st = 0;; st = st + 1 == kStages ? 0 : st + 1) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncthreads();
-        if (loaded < x1) {
-            load((int)((loaded - x0) % kStages));
-            if (++loaded < x1) step(a, ld);
-        }
+        load_next(st == 0 ? kStages - 1 : st - 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
         const uint32_t kb = sm0 + (uint32_t)st * 2u * TB, vb = kb + TB;
-        const int R = min(BM, (int)min((long long)BM, (long long)cur.q.n * a.G - (long long)cur.rb * BM));
+        const int R = min(BM, cur.p.q.n * a.G - cur.p.rb * BM);
         if (fresh) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = row0 + 8 * e, rr = cur.rb * BM + r;
-                const int tok = rr / a.G, head = cur.h * a.G + rr % a.G;
-                const uint16_t* src = a.q + (cur.q.start + tok) * a.ldq + (long long)head * D + 2 * u;
+                const int r = row0 + 8 * e, rr = cur.p.rb * BM + r;
+                const int tok = (int)q4p::page_of(a.by_g, rr), head = cur.p.h * a.G + rr - tok * a.G;
+                const uint16_t* src = a.q + (cur.p.q.start + tok) * a.ldq + (long long)head * D + 2 * u;
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
                     qf[kk][e] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
@@ -309,9 +357,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             for (int dn = 0; dn < DN; ++dn) o[dn][0] = o[dn][1] = o[dn][2] = o[dn][3] = 0.f;
             fresh = false;
         }
-        const int key0 = cur.tile * kKeys;
-        const bool tail = key0 + kKeys > cur.q.ctx;  // the tile holds new rows, or the end
-        const int tok[2] = {(cur.rb * BM + row0) / a.G, (cur.rb * BM + row0 + 8) / a.G};
+        const int key0 = cur.p.tile * kKeys;
+        const bool tail = key0 + kKeys > cur.p.q.ctx;  // the tile holds new rows, or the end
+        const int tok[2] = {(int)q4p::page_of(a.by_g, cur.p.rb * BM + row0), (int)q4p::page_of(a.by_g, cur.p.rb * BM + row0 + 8)};
         if (tail) {
             // A new row's value reaches only the rows that see it: infinities
             // and NaN of the tile are added to those by hand and then
@@ -319,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             bool odd = false;
             for (int y = tid; y < kKeys * NCH; y += kThreads) {
                 const int r = y / NCH, c = y % NCH;
-                if (key0 + r < cur.q.ctx) continue;
+                if (key0 + r < cur.p.q.ctx) continue;
                 const uint4 w = *reinterpret_cast<const uint4*>(smem + (vb - sm0) + swz<D>(r, c));
                 const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -327,11 +375,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             }
             if (__syncthreads_or(odd)) {
                 for (int j = 0; j < KW; ++j) {
-                    const int r = wn * KW + j, nj = key0 + r - cur.q.ctx;
-                    if (nj < 0 || nj >= cur.q.n) continue;
+                    const int r = wn * KW + j, nj = key0 + r - cur.p.q.ctx;
+                    if (nj < 0 || nj >= cur.p.q.n) continue;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        if (row0 + 8 * e >= R || !sees(a, cur.q.start, tok[e], nj)) continue;
+                        if (row0 + 8 * e >= R || !sees(a, cur.p.q.start, tok[e], nj)) continue;
 #pragma unroll
                         for (int dn = 0; dn < DN; ++dn) {
                             const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + (vb - sm0) + swz<D>(r, dn) + 4 * u);
@@ -344,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
                 __syncthreads();
                 for (int y = tid; y < kKeys * D; y += kThreads) {
                     const int r = y / D, d = y % D;
-                    if (key0 + r < cur.q.ctx) continue;
+                    if (key0 + r < cur.p.q.ctx) continue;
                     uint16_t* v = reinterpret_cast<uint16_t*>(smem + (vb - sm0) + swz<D>(r, d / 8)) + d % 8;
                     if (!finite16(*v)) *v = 0;
                 }
@@ -370,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int nj = key0 + wn * KW + nt * 8 + 2 * u + (e & 1) - cur.q.ctx;
-                    if (nj >= 0 && (nj >= cur.q.n || row0 + 8 * (e >> 1) >= R || !sees(a, cur.q.start, tok[e >> 1], nj)))
+                    const int nj = key0 + wn * KW + nt * 8 + 2 * u + (e & 1) - cur.p.q.ctx;
+                    if (nj >= 0 && (nj >= cur.p.q.n || row0 + 8 * (e >> 1) >= R || !sees(a, cur.p.q.start, tok[e >> 1], nj)))
                         sc[nt][e] = -INFINITY;
                 }
         }
@@ -414,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
                 mma(o[dn + 1], pa[kj], b[2], b[3]);
             }
 
-        const bool job_end = cur.tile + 1 == cur.tiles;
-        if (job_end || x + 1 == x1) {
+        const bool job_end = cur.p.tile + 1 == cur.p.tiles;
+        if (cur.p.tile + 1 == cur.end) {
             // the row sums over the quad's columns, then over the WN warps
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -472,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
                 if (begun && job_end) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = row0 + 8 * e, rr = cur.rb * BM + r;
+                        const int r = row0 + 8 * e, rr = cur.p.rb * BM + r;
                         if (r >= R) continue;
                         const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-                        uint16_t* dst = a.out + (long long)(cur.q.start + rr / a.G) * a.ldo +
-                                        (long long)(cur.h * a.G + rr % a.G) * D + 2 * u;
+                        uint16_t* dst = a.out + (long long)(cur.p.q.start + rr / a.G) * a.ldo +
+                                        (long long)(cur.p.h * a.G + rr % a.G) * D + 2 * u;
 #pragma unroll
                         for (int dn = 0; dn < DN; ++dn)
                             *reinterpret_cast<uint32_t*>(dst + 8 * dn) = pack2(o[dn][2 * e] * inv, o[dn][2 * e + 1] * inv);
@@ -500,13 +548,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             fresh = true;
             begun = true;
         }
-        if (x + 1 < x1) step(a, cur);
+        if (++cur.p.tile == cur.end) {
+            if (!cur.more()) break;
+            cur.next(a);
+        }
     }
 }
 
 // Joins the parts of the jobs that several CTAs shared.  Block b looks at the
-// border between CTAs b and b + 1; it works if that is the first border inside
-// its job.  A warp per row; a lane holds (m, l) of every 32nd part, so the
+// border between CTAs b and b + 1; it works if its job has begun in CTA b.  A warp per row; a lane holds (m, l) of every 32nd part, so the
 // loads are in flight together.
 constexpr int kJoinThreads = 256;
 
@@ -518,12 +568,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Args a) {
     const int b = blockIdx.x;
     const long long xb = share * b, x = xb + share;
     Place p;
-    long long j0 = 0;  // the job's first tile
+    long long last_at = 0;  // the job's last tile's place
     bool work = x < line;
     if (work) {
         p = line_find(a, sums, kJoinThreads, x);
-        j0 = x - p.tile;
-        work = p.tile != 0 && xb <= j0;  // a job across this border, and no earlier border in it
+        last_at = p.start + (long long)(p.tiles - 1) * p.cost;
+        work = p.start >= xb && p.start < x && last_at >= x;  // begun in CTA b, not ended there
     }
     // the parts are written (and no grid that follows this one starts before
     // the attention's end, so blocks without work wait as well)
@@ -532,50 +582,75 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Args a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM);
     // CTA b has the job's beginning (slot 2 b + 1), later CTAs their slot 2 c
-    const int last = (int)((j0 + p.tiles - 1) / share);  // CTA of the job's last tile
+    const int last = (int)(last_at / share);  // CTA of the job's last tile
     const auto slot_of = [&](int c) { return 2 * c + (c == b); };
-    for (int r = blockIdx.y * (kJoinThreads / 32) + warp; r < rows; r += gridDim.y * (kJoinThreads / 32)) {
-        const long long rr = (long long)p.rb * a.BM + r;
-        float m = -INFINITY;
-        for (int c = b + lane; c <= last; c += 32) m = fmaxf(m, part_ml(a, slot_of(c))[r].x);
+    // kIlp rows of a warp at a time: their loads are in flight together
+    constexpr int E = D / 32, kIlp = 4;
+    for (int r0 = (blockIdx.y * (kJoinThreads / 32) + warp) * kIlp; r0 < rows; r0 += gridDim.y * (kJoinThreads / 32) * kIlp) {
+        float m[kIlp], l[kIlp], f[kIlp], o[kIlp][E];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float ms = m == -INFINITY ? 0.f : m;
-        constexpr int E = D / 32;
-        float l = 0.f, o[E] = {};
+        for (int i = 0; i < kIlp; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[i][e] = 0.f;
+        }
+        for (int c = b + lane; c <= last; c += 32)
+#pragma unroll
+            for (int i = 0; i < kIlp; ++i)
+                if (r0 + i < rows) m[i] = fmaxf(m[i], part_ml(a, slot_of(c))[r0 + i].x);
+#pragma unroll
+        for (int i = 0; i < kIlp; ++i) {
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
+            if (m[i] == -INFINITY) m[i] = 0.f;
+        }
         for (int c0 = b; c0 <= last; c0 += 32) {
-            float f = 0.f;
-            if (c0 + lane <= last) {
-                const float2 t = part_ml(a, slot_of(c0 + lane))[r];
-                f = exp2f(t.x - ms);
-                l = fmaf(t.y, f, l);
+#pragma unroll
+            for (int i = 0; i < kIlp; ++i) {
+                f[i] = 0.f;
+                if (c0 + lane <= last && r0 + i < rows) {
+                    const float2 t = part_ml(a, slot_of(c0 + lane))[r0 + i];
+                    f[i] = exp2f(t.x - m[i]);
+                    l[i] = fmaf(t.y, f[i], l[i]);
+                }
             }
             const int n = min(32, last - c0 + 1);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                const float* src = part_o<D>(a, slot_of(c0 + i)) + (size_t)r * D + E * lane;
-                float v[E];
-                if constexpr (E == 4) {
-                    const float4 t = *reinterpret_cast<const float4*>(src);
-                    v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-                } else {
-                    const float2 t = *reinterpret_cast<const float2*>(src);
-                    v[0] = t.x, v[1] = t.y;
-                }
+#pragma unroll 2
+            for (int k = 0; k < n; ++k) {
+                const float* src = part_o<D>(a, slot_of(c0 + k)) + (size_t)r0 * D + E * lane;
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(v[e], fi, o[e]);
+                for (int i = 0; i < kIlp; ++i) {
+                    if (r0 + i >= rows) break;
+                    const float fi = __shfl_sync(0xffffffffu, f[i], k);
+                    if constexpr (E == 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(src + i * D);
+                        o[i][0] = fmaf(t.x, fi, o[i][0]);
+                        o[i][1] = fmaf(t.y, fi, o[i][1]);
+                        o[i][2] = fmaf(t.z, fi, o[i][2]);
+                        o[i][3] = fmaf(t.w, fi, o[i][3]);
+                    } else {
+                        const float2 t = *reinterpret_cast<const float2*>(src + i * D);
+                        o[i][0] = fmaf(t.x, fi, o[i][0]);
+                        o[i][1] = fmaf(t.y, fi, o[i][1]);
+                    }
+                }
             }
         }
 #pragma unroll
-        for (int o2 = 16; o2 > 0; o2 >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o2);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* dst = a.out + (p.q.start + rr / a.G) * a.ldo + (p.h * a.G + rr % a.G) * D + E * lane;
-        uint32_t w[E / 2];
+        for (int i = 0; i < kIlp; ++i) {
+            if (r0 + i >= rows) break;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) w[e / 2] = pack2(o[e] * inv, o[e + 1] * inv);
-        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(dst) = w[0];
+            for (int s = 16; s > 0; s >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+            const int rr = p.rb * a.BM + r0 + i, tok = (int)q4p::page_of(a.by_g, rr);
+            uint16_t* dst = a.out + (size_t)(p.q.start + tok) * a.ldo + (size_t)(p.h * a.G + rr - tok * a.G) * D + E * lane;
+            uint32_t w[E / 2];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) w[e / 2] = pack2(o[i][e] * inv, o[i][e + 1] * inv);
+            if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(dst) = w[0];
+        }
     }
 }
 
@@ -600,7 +675,7 @@ size_t workspace_bytes() {
 template <int D>
 cudaError_t launch_join(const Args& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.ctas - 1, (unsigned)(a.BM <= 32 ? 1 : a.BM <= 64 ? 2 : 4));
+    cfg.gridDim = dim3((unsigned)a.ctas - 1, (unsigned)(a.BM / 32 > 1 ? a.BM / 32 : 1));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -619,6 +694,8 @@ cudaError_t launch(Args& a, void* workspace, int sms, cudaStream_t s) {
     a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
     a.BM = 16 * WM;
     a.KT = kKeys;
+    a.KT_log2 = 6;
+    a.cost_full = a.cost_half = 1;
     place_parts<D>(a, workspace);
     tree_attn_kernel<D, WM><<<a.ctas, kThreads, attn_smem<D>(), s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -634,10 +711,11 @@ cudaError_t launch(Args& a, void* workspace, int sms, cudaStream_t s) {
 //   else: both streams have the same rows and alternate tiles, and their
 //     (m, l, O) are joined at the end.
 // Per stream a warpgroup computes the softmax (thread = row = TMEM lane) while
-// the tensor cores work for the other stream, and one thread issues, in order,
-//   S(0) | P V(0) S(1) | P V(1) S(2) | ...
+// the tensor cores work for the other stream, and one warp issues, in order,
+//   S(0) | PVa(0) PVb(0) S(1) | PVa(1) PVb(1) S(2) | ...
 // S = Q K^T (128 x 128, Q and K from shared memory) and O += P V (P, fp16,
-// from tensor memory over the scores it came from, V read MN-major).  MMAs of
+// from tensor memory over the scores it came from, V read MN-major; a, b: the
+// positions 0 .. 63 and 64 .. 127, each as soon as its P is there).  MMAs of
 // one thread run in order, so S(k + 1) may overwrite what P V(k) reads, and
 // the commit behind S(k + 1) tells the softmax that O holds step k's product.
 // Tensor memory (512 columns): S 0 and 1 (128 each), O 0 and 1.
@@ -650,18 +728,21 @@ cudaError_t launch(Args& a, void* workspace, int sms, cudaStream_t s) {
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1
 constexpr float kTcShift = 7.f;
+constexpr int kTcCostFull = 4, kTcCostHalf = 3;  // of a tile, with two row streams and with alternate tiles
 
 template <int D>
 struct TcShape {
     static constexpr uint32_t kTile = 128 * D * 2;      // a 128 x D fp16 tile: D / 64 swizzled slabs of 16 KB
     static constexpr int kStages = D == 128 ? 2 : 4;    // of keys, and of values
-    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * (size_t)kTile + 512;
+    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * (size_t)kTile + 512 + 8 * 2048;  // tiles, barriers, staging
 };
 
 struct TcBars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t v_clean[4];  // two row streams: stream 0 has cleared what stream 1's products must not meet
-    uint64_t s_full[2], p_full[2], q_full, o_full, x_full, x_empty, drain[2];
+    // per stream: a step's scores; its P, positions 0 .. 63 and 64 .. 127; its turn
+    uint64_t s_full[2], pa_full[2], pb_full[2], turn[2], drain[2];
+    uint64_t q_full, o_full, x_full, x_done;
     uint32_t tmem_base;
     volatile int abort;
     volatile int odd[2];  // last segment (by parity) that met infinities or NaN among its new rows' values
@@ -734,6 +815,56 @@ __device__ __forceinline__ uint32_t sees_word(const Args& a, const Seq& q, int t
     return j0 < 0 ? (bits << -j0) | ((1u << -j0) - 1u) : bits;
 }
 
+// New rows that every row of the job sees.
+__device__ __forceinline__ int all_see(const Args& a, const Place& p) {
+    return a.mask ? 0 : (int)q4p::page_of(a.by_g, p.rb * a.BM) + 1;
+}
+
+// Clears row `row` of a value tile, or only its infinities and NaN; whether there were any.
+template <int D>
+__device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
+    bool found = false;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+        uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + sw_off(row, c & 7));
+        if (all) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 w = *at;
+        uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!finite16((uint16_t)ws[e])) ws[e] &= 0xffff0000u, bad = true;
+            if (!finite16((uint16_t)(ws[e] >> 16))) ws[e] &= 0x0000ffffu, bad = true;
+        }
+        if (bad) *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+        found |= bad;
+    }
+    return found;
+}
+
+// Adds to columns c0 .. c1 - 1 of a written row (fp16 `out`, else fp32 `part`)
+// the infinities and NaN of the new rows it sees in the segment's T tiles.
+template <int D>
+__device__ __noinline__ void add_odd(const Args& a, const Place& p, int T, int tok, int c0, int c1, uint16_t* out,
+                                     float* part) {
+    const int n0 = max(0, p.tile * a.KT - p.q.ctx), n1 = min(p.q.n, (p.tile + T) * a.KT - p.q.ctx);
+    for (int nj = n0; nj < n1; ++nj) {
+        if (!sees(a, p.q.start, tok, nj)) continue;
+        const long long at = q4p::row_at(a.w, p.s, p.q.ctx + nj, p.h, D);
+        if (at < 0) continue;
+        for (int c = c0; c < c1; ++c) {
+            const uint16_t v = a.w.v[at + c];
+            if (finite16(v)) continue;
+            const float f = __half2float(__ushort_as_half(v));
+            if (out) out[c] = __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(out[c])) + f));
+            else part[c] += f;
+        }
+    }
+}
+
 struct TcArgs {
     Args a;
     int box;            // rows per TMA box
@@ -768,14 +899,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             q4d::mbar_init(q4d::smem_addr(&B.s_full[i]), 1);
-            q4d::mbar_init(q4d::smem_addr(&B.p_full[i]), 4);
+            q4d::mbar_init(q4d::smem_addr(&B.pa_full[i]), 4);
+            q4d::mbar_init(q4d::smem_addr(&B.pb_full[i]), 4);
+            q4d::mbar_init(q4d::smem_addr(&B.turn[i]), 4);
             q4d::mbar_init(q4d::smem_addr(&B.drain[i]), 1);
             B.odd[i] = 0;
         }
         q4d::mbar_init(q4d::smem_addr(&B.q_full), 8);
         q4d::mbar_init(q4d::smem_addr(&B.o_full), 2);
-        q4d::mbar_init(q4d::smem_addr(&B.x_full), 4);
-        q4d::mbar_init(q4d::smem_addr(&B.x_empty), 4);
+        q4d::mbar_init(q4d::smem_addr(&B.x_full), 8);
+        q4d::mbar_init(q4d::smem_addr(&B.x_done), 8);
         B.abort = 0;
         q4d::fence_mbar_init();
     }
@@ -786,18 +919,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     const long long line = line_scan(a, sums, kTcThreads);
-    const long long share = line_share(a, line), x0 = share * blockIdx.x, x1 = min(line, x0 + share);
     q4t::fence_before();
     __syncthreads();
     q4t::fence_after();
     q4d::pdl_trigger();
     const uint32_t tmem = B.tmem_base;
 
-    if (x0 < x1) {
-        // Every role walks the same segments: the part of each job that lies
-        // in x0 .. x1 - 1.
-        Place p = line_find(a, sums, kTcThreads, x0);
-        long long x = x0;
+    Walk w;
+    if (w.begin(a, sums, kTcThreads, line)) {
+        // Every role walks the same segments.
+        Place& p = w.p;
+        bool rest = true;     // segments to do
         uint32_t seg = 0;   // segments done
         uint32_t tiles0 = 0;  // tiles before this segment
 
@@ -811,8 +943,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int boxes = kTcKeys / t.box;
             bool ok = true;
             uint32_t kt = 0;
-            while (x < x1 && ok) {
-                const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
+            while (rest && ok) {
+                const int T = w.end - p.tile;
                 const int len = p.q.ctx + p.q.n;
                 for (int j = 0; j < T && ok; ++j, ++kt) {
                     const uint32_t st = kt % NST;
@@ -834,8 +966,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int sl = 0; sl < SLABS; ++sl) q4t::tma_load_2d(dst + sl * 16384, map, 64 * sl, y, fb);
                     }
                 }
-                x += T;
-                if (x < x1 && ok) next_job(a, p);
+                rest = w.more();
+                if (rest && ok) w.next(a);
             }
             if (!ok) {  // copies still in flight land before the CTA can exit
                 for (uint32_t i = kt > (uint32_t)NST ? kt - NST : 0; i < kt; ++i)
@@ -854,15 +986,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint64_t dv = q4t::sw128_desc(q4d::smem_addr(v_s), 16384, 1024);
             const uint32_t sd = tmem + kColS + 128 * i, od = tmem + kColO + 128 * i;
             bool ok = true;
-            uint32_t n_p = 0;    // p_full phases passed
+            uint32_t n_p = 0;     // steps done: the phases of pa_full and pb_full
             uint32_t cleans = 0;  // parity of the v_clean phases passed, a bit per stage
-            while (x < x1 && ok) {
-                const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
-                const bool two = (long long)p.q.n * a.G - (long long)p.rb * a.BM > 128;
+            while (rest && ok) {
+                const int T = w.end - p.tile;
+                const bool two = p.q.n * a.G - p.rb * a.BM > 128;
                 const int steps = two ? T : (T - i + 1) / 2;
                 const uint64_t ad = dq + (uint64_t)((two ? i : 0) * (kTile / 16));
                 const auto tile_of = [&](int k) { return tiles0 + (two ? k : 2 * k + i); };
-                // S of step k (its keys have landed)
+                // the scores of step k (its keys have landed)
                 const auto issue_s = [&](int k) {
                     const uint32_t st = tile_of(k) % NST;
                     const uint64_t bd = dk + (uint64_t)(st * (kTile / 16));
@@ -874,7 +1006,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         q4t::commit(q4d::smem_addr(&B.s_full[i]));
                         q4t::commit(q4d::smem_addr(&B.k_empty[st]));
-                        if (!two) q4t::commit(q4d::smem_addr(&B.k_empty[st]));  // the other stream's share
+                        if (!two) q4t::commit(q4d::smem_addr(&B.k_empty[st]));  // the barrier counts both streams
+                    }
+                    __syncwarp();
+                };
+                // half h of O += P V of step k: its positions 64 h ..
+                const auto issue_pv = [&](int k, int h) {
+                    const uint64_t bd = dv + (uint64_t)((tile_of(k) % NST) * (kTile / 16));
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            q4t::mma_ts(od, sd + 8 * kk, bd + (uint64_t)(kk * 2048 / 16), id_o, (k > 0 || kk > 0) ? 1u : 0u);
                     }
                     __syncwarp();
                 };
@@ -892,21 +1034,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t kt = tile_of(k), st = kt % NST;
                     const bool more = k + 1 < steps;
                     ok = tc_wait(B, B.v_full[st], (kt / NST) & 1, err) && (!more || wait_k(k + 1)) &&
-                         tc_wait(B, B.p_full[i], n_p & 1, err);
-                    if (ok && two && i == 1 && (p.tile + k + 1) * kTcKeys > p.q.ctx + (a.mask ? 0 : p.rb * a.BM / a.G + 1)) {
+                         tc_wait(B, B.pa_full[i], n_p & 1, err);
+                    if (ok && two && i == 1 && (p.tile + k + 1) * kTcKeys > p.q.ctx + all_see(a, p)) {
                         ok = tc_wait(B, B.v_clean[st], cleans >> st & 1, err);
                         cleans ^= 1u << st;
                     }
                     if (!ok) break;
-                    ++n_p;
                     q4t::fence_after();
-                    const uint64_t bd = dv + (uint64_t)(st * (kTile / 16));
-                    if (leader) {
-#pragma unroll
-                        for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                            q4t::mma_ts(od, sd + 8 * kk, bd + (uint64_t)(kk * 2048 / 16), id_o, (k > 0 || kk > 0) ? 1u : 0u);
-                    }
-                    __syncwarp();
+                    issue_pv(k, 0);
+                    if (!(ok = tc_wait(B, B.pb_full[i], n_p & 1, err))) break;
+                    q4t::fence_after();
+                    issue_pv(k, 1);
+                    ++n_p;
                     if (more) issue_s(k + 1);
                     if (leader) {
                         q4t::commit(q4d::smem_addr(&B.v_empty[st]));
@@ -918,8 +1057,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (steps == 0 && leader) q4d::mbar_arrive(q4d::smem_addr(&B.o_full));
                 tiles0 += T;
                 ++seg;
-                x += T;
-                if (x < x1 && ok) next_job(a, p);
+                rest = w.more();
+                if (rest && ok) w.next(a);
             }
             if (!ok) B.abort = 1;
             // every MMA this warp issued has finished before the CTA winds down
@@ -933,52 +1072,77 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint32_t lt = tmem + ((uint32_t)(wr * 32) << 16);
             const uint32_t ts = lt + kColS + 128 * i, to = lt + kColO + 128 * i;
             const float2 cc = make_float2(a.c, a.c);
-            uint32_t n_s = 0;      // s_full phases passed
-            uint32_t joins = 0;    // joined segments so far
+            float* ml_x = reinterpret_cast<float*>(sums);  // [2 streams][128] (m, l), for joins
+            uint32_t n_s = 0;    // steps done: the phases of s_full
+            uint32_t turns = 0;  // turns taken
+            uint32_t joins = 0;  // joined segments so far
+            bool joined = false;  // the last segment was one
             bool ok = true;
-            while (x < x1) {
-                const int T = (int)min((long long)(p.tiles - p.tile), x1 - x);
-                const int R = (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM);
-                const bool two = R > 128;
-                const int r = (two ? 128 * i : 0) + row;  // row of the job
-                const bool live = r < R;  // the others run along with queries of zero
-                const int rr = p.rb * a.BM + (live ? r : 0), tok = rr / a.G;
-                const size_t q_row = (size_t)(p.q.start + tok), q_col = (size_t)(p.h * a.G + rr % a.G) * D;
-                const int steps = two ? T : (T - i + 1) / 2;
-                const bool join = !two && T > 1;
-                // new rows that every row of the job sees
-                const int all_see = a.mask ? 0 : p.rb * a.BM / a.G + 1;
-                // the row's query into the stream's tile (both streams share stream
-                // 0's), once every warp of stream 0 has read the last join's part there
-                if (joins > 0) ok = __all_sync(0xffffffffu, ok && tc_wait(B, B.x_empty, (joins - 1) & 1, err));
-                if (!ok) break;
+            // The job's row of this thread (none: -1), as token and head, and
+            // its query into the stream's tile.  Both streams share stream 0's
+            // tile where the job has 128 rows or fewer.
+            const auto job_row = [&](const Place& w) {
+                const int R = min(a.BM, w.q.n * a.G - w.rb * a.BM);
+                const int r = (R > 128 ? 128 * i : 0) + row;
+                return r < R ? r : -1;
+            };
+            const auto put_query = [&](const Place& w) {
+                const bool two = w.q.n * a.G - w.rb * a.BM > 128;
                 if (two || i == 0) {
+                    // this warp's 32 rows, whole rows at a time
+                    const int R = min(a.BM, w.q.n * a.G - w.rb * a.BM);
                     uint8_t* dst = q_s + (two ? i : 0) * kTile;
-                    const uint4* src = reinterpret_cast<const uint4*>(a.q + q_row * a.ldq + q_col);
+                    constexpr int NC = D / 8, PER = 32 / NC;  // chunks of a row, rows per load
+                    const int c = lane % NC;
+                    uint4 v[NC];
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 w = live ? src[c] : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw_off(row, c & 7)) = w;
+                    for (int e = 0; e < NC; ++e) {
+                        const int r = (two ? 128 * i : 0) + wr * 32 + e * PER + lane / NC;
+                        const int rr = w.rb * a.BM + r, tk = (int)q4p::page_of(a.by_g, rr);
+                        v[e] = make_uint4(0, 0, 0, 0);
+                        if (r < R)
+                            v[e] = *reinterpret_cast<const uint4*>(a.q + (size_t)(w.q.start + tk) * a.ldq +
+                                                                   (size_t)(w.h * a.G + rr - tk * a.G) * D + 8 * c);
                     }
+#pragma unroll
+                    for (int e = 0; e < NC; ++e)
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw_off(wr * 32 + e * PER + lane / NC, c & 7)) = v[e];
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 __syncwarp();
                 if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.q_full));
-
+            };
+            // The streams take turns at the exponentials: one computes them
+            // while the tensor cores work for the other.  Left alone they fall
+            // into step and both wait for each other's MMAs.
+            const auto take_turn = [&]() {
+                const bool open = i == 0 && turns == 0;  // stream 0 begins
+                const bool go = open || tc_wait(B, B.turn[i], (turns - (i == 0)) & 1, err);
+                ++turns;
+                return (bool)__all_sync(0xffffffffu, go);
+            };
+            const auto pass_turn = [&]() {
+                __syncwarp();
+                if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.turn[1 - i]));
+            };
+            put_query(p);
+            while (rest) {
+                const int T = w.end - p.tile;
+                const bool two = p.q.n * a.G - p.rb * a.BM > 128;
+                const int r = job_row(p);
+                const int tok = (int)q4p::page_of(a.by_g, p.rb * a.BM + max(r, 0));
+                const int steps = two ? T : (T - i + 1) / 2;
+                const int seen_by_all = p.q.ctx + all_see(a, p);
                 float m = -INFINITY, l = 0.f;
                 for (int j = 0; j < steps; ++j) {
                     const int tj = two ? j : 2 * j + i;  // tile of the segment
                     const int key0 = (p.tile + tj) * kTcKeys;
                     const uint32_t kt = tiles0 + tj, st = kt % NST;
-                    ok = __all_sync(0xffffffffu, tc_wait(B, B.s_full[i], n_s & 1, err));
-                    if (!ok) break;
-                    ++n_s;
-                    q4t::fence_after();
+                    // some row of the job does not see some position of the tile
+                    const bool tail = key0 + kTcKeys > seen_by_all;
                     // The row in halves, so that it fits the registers: the
-                    // second one's maximum, the first one's, P of the first
-                    // (over scores that are read), the second one again.
-                    // Some row of the job does not see some position of the tile:
-                    const bool tail = key0 + kTcKeys > p.q.ctx + all_see;
+                    // maximum of the second, of the first, P of the first, the
+                    // second once more, P of the second.
                     uint32_t s[64];
                     float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     const auto load_half = [&](int h) {
@@ -1003,6 +1167,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             for (int f = 0; f < 4; ++f)
                                 x4[f] = fmaxf(x4[f], fmaxf(__uint_as_float(s[e + f]), __uint_as_float(s[e + 4 + f])));
                     };
+                    ok = __all_sync(0xffffffffu, tc_wait(B, B.s_full[i], n_s & 1, err));
+                    if (!ok) break;
+                    ++n_s;
+                    q4t::fence_after();
                     load_half(1);
                     max_half();
                     load_half(0);
@@ -1028,12 +1196,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         st32(ts + 32 * h, s);
                     };
+                    if (!(ok = take_turn())) break;
                     exp_half(0);
-                    load_half(1);
-                    exp_half(1);
-                    l = fmaf(l, corr, (sum.x + sum2.x) + (sum.y + sum2.y));
+                    // (this step's scores are in, so the step before is in O)
                     if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-#pragma unroll
+#pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             ld32(to + c0, s);
                             q4t::ld_wait();
@@ -1050,29 +1217,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         ok = __all_sync(0xffffffffu, tc_wait(B, B.v_full[st], (kt / NST) & 1, err));
                         if (!ok) break;
                         const int nj = key0 + row - p.q.ctx;
-                        if (nj >= 0) {
-                            uint8_t* vt = v_s + st * kTile;
-                            bool found = false;
-#pragma unroll
-                            for (int c = 0; c < D / 8; ++c) {
-                                uint4* at = reinterpret_cast<uint4*>(vt + (c >> 3) * 16384 + sw_off(row, c & 7));
-                                if (nj >= p.q.n) {
-                                    *at = make_uint4(0, 0, 0, 0);
-                                    continue;
-                                }
-                                uint4 w = *at;
-                                uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                                bool bad = false;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if (!finite16((uint16_t)ws[e])) ws[e] &= 0xffff0000u, bad = true;
-                                    if (!finite16((uint16_t)(ws[e] >> 16))) ws[e] &= 0x0000ffffu, bad = true;
-                                }
-                                if (bad) *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-                                found |= bad;
-                            }
-                            if (found) B.odd[seg & 1] = (int)seg + 1;
-                        }
+                        if (nj >= 0 && clean_row<D>(v_s + st * kTile, row, nj >= p.q.n)) B.odd[seg & 1] = (int)seg + 1;
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         if (two) {
                             __syncwarp();
@@ -1080,110 +1225,122 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     q4t::st_wait();
+                    if (j == 0 && joined) {  // the other stream's threads have read this one's O
+                        ok = __all_sync(0xffffffffu, tc_wait(B, B.x_done, (joins - 1) & 1, err));
+                        if (!ok) break;
+                    }
                     q4t::fence_before();
                     __syncwarp();
-                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.p_full[i]));
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.pa_full[i]));
+                    load_half(1);
+                    exp_half(1);
+                    pass_turn();
+                    l = fmaf(l, corr, (sum.x + sum2.x) + (sum.y + sum2.y));
+                    q4t::st_wait();
+                    q4t::fence_before();
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.pb_full[i]));
+                }
+                if (ok && !two && steps < (T + 1) / 2) {  // the other stream's last step has no partner here
+                    ok = take_turn();
+                    pass_turn();
                 }
                 if (!ok) break;
                 ok = __all_sync(0xffffffffu, tc_wait(B, B.o_full, seg & 1, err));
                 if (!ok) break;
                 q4t::fence_after();
-                const bool job_begin = p.tile == 0, job_end = p.tile + T == p.tiles;
-                const bool odd = B.odd[seg & 1] == (int)seg + 1;
-                if (join && i == 1) {
-                    // stream 1's part, fp32, into the query tiles' place (16-byte
-                    // chunks of a row spread over the banks); (m, l) into sums, done with
-                    float* ob = reinterpret_cast<float*>(q_s);
-                    constexpr int NC = D / 4;
-#pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 16) {
-                        uint32_t o[16];
-                        q4t::ld16(to + c0, o);
-                        q4t::ld_wait();
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            *reinterpret_cast<uint4*>(ob + row * D + (((c0 / 4 + c) ^ (row & (NC - 1))) * 4)) =
-                                make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                    }
-                    sums[2 * row] = __float_as_int(m);
-                    sums[2 * row + 1] = __float_as_int(l);
-                    __syncwarp();
-                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_full));
-                } else if (two || i == 0) {
-                    float f0 = 1.f, f1 = 0.f;
-                    if (join) {
-                        ok = __all_sync(0xffffffffu, tc_wait(B, B.x_full, joins & 1, err));
-                        if (!ok) break;
-                        const float m1 = __int_as_float((int)sums[2 * row]), l1 = __int_as_float((int)sums[2 * row + 1]);
-                        const float mm = fmaxf(m, m1), ms = mm == -INFINITY ? 0.f : mm;
-                        f0 = ex2(m - ms);
-                        f1 = ex2(m1 - ms);
-                        l = l * f0 + l1 * f1;
-                        m = mm;
-                    }
-                    const bool whole = job_begin && job_end;
-                    const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                    const int slot = 2 * blockIdx.x + (job_begin ? 1 : 0);
-                    const float* ob = reinterpret_cast<const float*>(q_s);
-                    constexpr int NC = D / 4;
-                    if (!whole && live) part_ml(a, slot)[r] = make_float2(m, l);
-#pragma unroll
-                    for (int c0 = 0; c0 < D; c0 += 16) {
-                        uint32_t w[16];
-                        float o[16];
-                        q4t::ld16(to + c0, w);
-                        q4t::ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(w[e]);
-                        if (join) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const float4 v = *reinterpret_cast<const float4*>(
-                                    ob + row * D + (((c0 / 4 + c) ^ (row & (NC - 1))) * 4));
-                                o[4 * c] = fmaf(v.x, f1, o[4 * c] * f0);
-                                o[4 * c + 1] = fmaf(v.y, f1, o[4 * c + 1] * f0);
-                                o[4 * c + 2] = fmaf(v.z, f1, o[4 * c + 2] * f0);
-                                o[4 * c + 3] = fmaf(v.w, f1, o[4 * c + 3] * f0);
-                            }
-                        }
-                        if (odd && live) {
-                            const int n0 = max(0, p.tile * kTcKeys - p.q.ctx), n1 = min(p.q.n, (p.tile + T) * kTcKeys - p.q.ctx);
-                            for (int nj = n0; nj < n1; ++nj) {
-                                if (!sees(a, p.q.start, tok, nj)) continue;
-                                const long long at = q4p::row_at(a.w, p.s, p.q.ctx + nj, p.h, D);
-                                if (at < 0) continue;
-                                for (int e = 0; e < 16; ++e) {
-                                    const uint16_t v = a.w.v[at + c0 + e];
-                                    if (!finite16(v)) o[e] += __half2float(__ushort_as_half(v));
-                                }
-                            }
-                        }
-                        if (!live) continue;
-                        if (whole) {
-                            uint32_t y[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
-                            uint4* dst = reinterpret_cast<uint4*>(a.out + q_row * a.ldo + q_col + c0);
-                            dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                            dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-                        } else {
-                            float4* dst = reinterpret_cast<float4*>(part_o<D>(a, slot) + (size_t)r * D + c0);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        }
-                    }
-                    if (join) {
-                        __syncwarp();
-                        if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_empty));
-                    }
-                }
-                q4t::fence_before();  // O is read before the next segment's queries release its MMAs
-                if (join) ++joins;
+                // The next segment's queries go in first: its scores are
+                // computed while this one's results are written.
+                const Place done = p;
+                const uint32_t seg_done = seg;
                 tiles0 += T;
                 ++seg;
-                x += T;
-                if (x < x1) next_job(a, p);
+                rest = w.more();
+                if (rest) {
+                    w.next(a);
+                    put_query(p);
+                }
+                const bool job_begin = done.tile == 0, whole = job_begin && done.tile + T == done.tiles;
+                // Of a job on alternate tiles every thread has half the row's
+                // columns, of both streams' parts.
+                const bool join = !two && T > 1;
+                float f0 = 1.f, f1 = 0.f;
+                if (join) {
+                    *reinterpret_cast<float2*>(ml_x + 2 * (128 * i + row)) = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_full));
+                    ok = __all_sync(0xffffffffu, tc_wait(B, B.x_full, joins & 1, err));
+                    if (!ok) break;
+                    ++joins;
+                    const float2 u = *reinterpret_cast<const float2*>(ml_x + 2 * row);
+                    const float2 v = *reinterpret_cast<const float2*>(ml_x + 2 * (128 + row));
+                    m = fmaxf(u.x, v.x);
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    f0 = ex2(u.x - ms);
+                    f1 = ex2(v.x - ms);
+                    l = u.y * f0 + v.y * f1;
+                }
+                if (join || two || i == 0) {
+                    const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                    const int slot = 2 * blockIdx.x + (job_begin ? 1 : 0);
+                    const int R = min(a.BM, done.q.n * a.G - done.rb * a.BM);
+                    const int rw = (two ? 128 * i : 0) + wr * 32;  // the warp's first row of the job
+                    if (!whole && r >= 0 && (!join || i == 0)) part_ml(a, slot)[r] = make_float2(m, l);
+                    const int c1 = join ? D / 2 * (i + 1) : D;
+                    const uint32_t t0 = join ? lt + kColO : to;
+                    // 16 columns at a time by way of shared memory, so that a
+                    // warp stores whole sectors: 4 lanes per row
+                    float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&B) + 512) + warp * 512;
+#pragma unroll 1
+                    for (int c0 = join ? D / 2 * i : 0; c0 < c1; c0 += 16) {
+                        uint32_t w[16];
+                        float o[16];
+                        q4t::ld16(t0 + c0, w);
+                        q4t::ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(w[e]) * (f0 * inv);
+                        if (join) {
+                            q4t::ld16(t0 + 128 + c0, w);
+                            q4t::ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(w[e]), f1 * inv, o[e]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float4*>(stage + lane * 16 + ((e ^ (lane >> 1 & 3)) * 4)) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int y = e * 8 + (lane >> 2), c = lane & 3;
+                            const float4 v = *reinterpret_cast<const float4*>(stage + y * 16 + ((c ^ (y >> 1 & 3)) * 4));
+                            const int ry = rw + y;
+                            if (ry >= R) continue;
+                            if (whole) {
+                                const int rr = done.rb * a.BM + ry, tk = (int)q4p::page_of(a.by_g, rr);
+                                *reinterpret_cast<uint2*>(a.out + (size_t)(done.q.start + tk) * a.ldo +
+                                                          (size_t)(done.h * a.G + rr - tk * a.G) * D + c0 + 4 * c) =
+                                    make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+                            } else {
+                                *reinterpret_cast<float4*>(part_o<D>(a, slot) + (size_t)ry * D + c0 + 4 * c) = v;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (B.odd[seg_done & 1] == (int)seg_done + 1 && r >= 0) {
+                        const int rr = done.rb * a.BM + r;
+                        add_odd<D>(a, done, T, tok, join ? D / 2 * i : 0, c1,
+                                   whole ? a.out + (size_t)(done.q.start + tok) * a.ldo + (size_t)(done.h * a.G + rr - tok * a.G) * D
+                                         : nullptr,
+                                   part_o<D>(a, slot) + (size_t)r * D);
+                    }
+                }
+                q4t::fence_before();  // O is read before this warp releases the next segment's products
+                joined = join;
+                if (join) {
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_done));
+                }
             }
         }
     }
@@ -1201,6 +1358,9 @@ q4_status launch_tc(Args& a, const q4_paged_cache& c, void* workspace, int sms, 
     a.ctas = sms < kMaxTcCtas ? sms : kMaxTcCtas;
     a.BM = kTcRows;
     a.KT = kTcKeys;
+    a.KT_log2 = 7;
+    a.cost_full = kTcCostFull;
+    a.cost_half = kTcCostHalf;
     place_parts<D>(a, workspace);
     t.a = a;
     t.box = box;
@@ -1269,6 +1429,7 @@ extern "C" q4_status q4_tree_attention(const q4_tree_attention_desc* desc, q4_st
     a.ldq = d.ldq;
     a.ldo = d.ldo;
     a.G = G;
+    a.by_g = q4p::page_div((uint32_t)G);
     // rows per job: the average sequence's, by 16, 32 or 64
     const long long avg = ((long long)d.rows * G + d.cache.n_seqs - 1) / d.cache.n_seqs;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
