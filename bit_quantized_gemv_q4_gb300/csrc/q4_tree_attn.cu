@@ -20,6 +20,7 @@
 // several share, each leaves (m, l, O) in the workspace (at most two per CTA:
 // one job begun by another, one left unfinished), and a second kernel joins
 // them in the order of the CTAs, so the bits do not depend on timing.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -28,11 +29,11 @@
 
 namespace q4x {
 
+namespace cg = cooperative_groups;
 using q4p::Seq;
 using q4p::View;
 
 constexpr int kKeys = 64;      // positions per tile
-constexpr int kThreads = 128;  // 4 warps: WM of them along the rows, 4 / WM along the positions
 constexpr int kStages = 3;
 constexpr int kMaxRows = 64;   // rows of a job
 constexpr int kMaxCtas = 512;
@@ -80,86 +81,94 @@ __device__ __forceinline__ int tile_cost(const Args& a, const Seq& q, int rb) {
 }
 
 // Units of one head of a sequence (all row blocks).
-__device__ __forceinline__ long long head_units(const Args& a, const Seq& q) {
-    if (q.n <= 0) return 0;
-    const int blocks = (int)((unsigned)(q.n * a.G + a.BM - 1) / (unsigned)a.BM);
-    const int tiles = block_tiles(a, q, blocks - 1);
-    long long t = (long long)tiles * tile_cost(a, q, blocks - 1);
-    if (a.mask) return t + (long long)(blocks - 1) * tiles * a.cost_full;
-    for (int b = 0; b < blocks - 1; ++b) t += block_tiles(a, q, b) * a.cost_full;
+__device__ __forceinline__ unsigned head_units(const Args& a, const Seq& q) {
+    unsigned t = 0;
+    if (q.n > 0)
+#pragma unroll 1
+        for (int b = 0; b * a.BM < q.n * a.G; ++b) t += (unsigned)(block_tiles(a, q, b) * tile_cost(a, q, b));
     return t;
 }
 
 // A job's tiles tile .. tiles - 1; tile t stands at unit start + t * cost of the line.
 struct Place {
     int s, h, rb, tile, tiles, cost;
-    long long start;
+    unsigned start;
     Seq q;
 };
 
 // The line's length; `sums` gets the threads' running shares: each thread adds
-// up a contiguous share of the sequences.
-__device__ __forceinline__ long long line_scan(const Args& a, long long* sums, int threads) {
-    const int per = (a.w.S + threads - 1) / threads;
+// up a contiguous share of the sequences.  The line has fewer than 2^31 units:
+// a call beyond that (some 10^16 operations) is left out, with the error
+// latched.
+__device__ __noinline__ unsigned line_scan(const Args& a, unsigned* sums, int threads) {
+    __shared__ unsigned long long wsum[32];
+    const int per = (int)((unsigned)(a.w.S + threads - 1) / (unsigned)threads);
     const int lo = min(a.w.S, (int)threadIdx.x * per), hi = min(a.w.S, lo + per);
-    long long t = 0;
+    unsigned long long t = 0;
+#pragma unroll 1
     for (int s = lo; s < hi; ++s) {
         bool bad;
         const Seq q = q4p::seq_of(a.w, s, bad);
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
-        t += head_units(a, q);
+        t += (unsigned long long)head_units(a, q) * a.w.H;
     }
-    t *= a.w.H;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, t, o);
+        const unsigned long long u = __shfl_up_sync(0xffffffffu, t, o);
         if (lane >= o) t += u;
     }
-    __shared__ long long wsum[32];
     if (lane == 31) wsum[warp] = t;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) t += wsum[i];
-    sums[threadIdx.x] = t;
+    unsigned long long all = 0;
+#pragma unroll 1
+    for (int i = 0; i < threads / 32; ++i) {
+        if (i == warp) t += all;
+        all += wsum[i];
+    }
+    sums[threadIdx.x] = (unsigned)t;
     __syncthreads();
-    return sums[threads - 1];
+    if (all < (1ull << 31)) return (unsigned)all;
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
+    return 0;
 }
 
 // A CTA's share of the line (CTA c: units c * share ..): a tile belongs to the
 // CTA in whose share its first unit lies.  At least a tile, so that a CTA
 // between two others of a job has a part of it.
-__device__ __forceinline__ long long line_share(const Args& a, long long line) {
-    const long long s = line < (1ll << 31) ? (long long)(((unsigned)line + (unsigned)a.ctas - 1) / (unsigned)a.ctas)
-                                           : (line + a.ctas - 1) / a.ctas;
-    return max(s, (long long)a.cost_full);
+__device__ __forceinline__ unsigned line_share(const Args& a, unsigned line) {
+    return max((line + (unsigned)a.ctas - 1) / (unsigned)a.ctas, (unsigned)a.cost_full);
 }
 
 // The job that holds unit x (x < the line's length), from its first tile on.
-__device__ __forceinline__ Place line_find(const Args& a, const long long* sums, int threads, long long x) {
+__device__ __noinline__ Place line_find(const Args& a, const unsigned* sums, int threads, unsigned x) {
     int lo = 0, hi = threads - 1;  // first thread whose running sum exceeds x
     while (lo < hi) {
         const int mid = (lo + hi) / 2;
         if (sums[mid] > x) hi = mid;
         else lo = mid + 1;
     }
-    long long rest = lo > 0 ? x - sums[lo - 1] : x;
-    const int per = (a.w.S + threads - 1) / threads;
+    unsigned rest = lo > 0 ? x - sums[lo - 1] : x;
     Place p;
-    bool bad;
-    long long head = 0;
-    for (p.s = lo * per;; ++p.s) {
+    unsigned head = 0;
+    p.s = lo * (int)((unsigned)(a.w.S + threads - 1) / (unsigned)threads);
+#pragma unroll 1
+    while (true) {
+        bool bad;
         p.q = q4p::seq_of(a.w, p.s, bad);
         head = head_units(a, p.q);
-        if (rest < head * a.w.H) break;
-        rest -= head * a.w.H;
+        if (rest < head * (unsigned)a.w.H) break;  // (below 2^31: the line is)
+        rest -= head * (unsigned)a.w.H;
+        ++p.s;
     }
-    p.h = rest < (1ll << 31) && head < (1ll << 31) ? (int)((unsigned)rest / (unsigned)head) : (int)(rest / head);
-    rest -= p.h * head;
+    p.h = (int)(rest / head);
+    rest -= (unsigned)p.h * head;
+#pragma unroll 1
     for (p.rb = 0;; ++p.rb) {
         p.tiles = block_tiles(a, p.q, p.rb);
         p.cost = tile_cost(a, p.q, p.rb);
-        if (rest < (long long)p.tiles * p.cost) break;
-        rest -= (long long)p.tiles * p.cost;
+        if (rest < (unsigned)(p.tiles * p.cost)) break;
+        rest -= (unsigned)(p.tiles * p.cost);
     }
     p.start = x - rest;
     p.tile = 0;
@@ -168,7 +177,7 @@ __device__ __forceinline__ Place line_find(const Args& a, const long long* sums,
 
 // The next job (there is one).
 __device__ __forceinline__ void next_job(const Args& a, Place& p) {
-    p.start += (long long)p.tiles * p.cost;
+    p.start += (unsigned)(p.tiles * p.cost);
     p.tile = 0;
     if (++p.rb * a.BM >= p.q.n * a.G) {
         p.rb = 0;
@@ -185,11 +194,9 @@ __device__ __forceinline__ void next_job(const Args& a, Place& p) {
 }
 
 // First tile of the job at or behind unit x: 0 .. tiles.
-__device__ __forceinline__ int tile_at(const Place& p, long long x) {
-    const long long d = x - p.start;
-    if (d <= 0) return 0;
-    if (d >= (long long)p.tiles * p.cost) return p.tiles;
-    return (int)(((unsigned)d + (unsigned)p.cost - 1) / (unsigned)p.cost);
+__device__ __forceinline__ int tile_at(const Place& p, unsigned x) {
+    const unsigned d = x - p.start + (unsigned)p.cost - 1;
+    return x <= p.start ? 0 : min(p.tiles, (int)(d / (unsigned)p.cost));
 }
 
 // A CTA's part x0 .. x1 of the line as segments, each a run of one job's
@@ -197,23 +204,22 @@ __device__ __forceinline__ int tile_at(const Place& p, long long x) {
 struct Walk {
     Place p;
     int end;
-    long long x1, line;
+    unsigned x1;
     // false: the CTA has no tiles
-    __device__ __forceinline__ bool begin(const Args& a, const long long* sums, int threads, long long line_) {
-        line = line_;
-        const long long share = line_share(a, line), x0 = share * blockIdx.x;
+    __device__ __forceinline__ bool begin(const Args& a, const unsigned* sums, int threads, unsigned line) {
+        const unsigned share = line_share(a, line), x0 = share * blockIdx.x;  // below 2^31 + 512 * cost
         x1 = min(line, x0 + share);
         if (x0 >= x1) return false;
         p = line_find(a, sums, threads, x0);
         p.tile = tile_at(p, x0);
         if (p.tile == p.tiles) {  // x0 lies in the last tile's units
-            if (p.start + (long long)p.tiles * p.cost >= x1) return false;
+            if (!more()) return false;
             next_job(a, p);
         }
         end = tile_at(p, x1);
         return true;
     }
-    __device__ __forceinline__ bool more() const { return p.start + (long long)p.tiles * p.cost < x1; }
+    __device__ __forceinline__ bool more() const { return p.start + (unsigned)(p.tiles * p.cost) < x1; }
     __device__ __forceinline__ void next(const Args& a) {
         next_job(a, p);
         end = tile_at(p, x1);
@@ -261,94 +267,241 @@ __device__ __forceinline__ bool sees(const Args& a, int start, int i, int j) {
     return word < a.mask_words && (a.mask[(size_t)(start + i) * a.mask_words + word] >> (j & 31) & 1u);
 }
 
-template <int D>
-constexpr size_t attn_smem() {
-    return (size_t)kStages * 2 * kKeys * D * 2;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// ------------------------------------------------------------------ kernel ---
-// WM warps along the job's 16 WM rows, WN = 4 / WM along the tile's
-// positions.  Fragment layouts of mma.m16n8k16 (g = lane / 4, u = lane % 4):
-// A covers rows g, g + 8 and columns 2u, 2u+1, 2u+8, 2u+9; B rows 2u, 2u+1,
-// 2u+8, 2u+9 of column g; an accumulator rows g, g + 8, columns 2u, 2u+1, so
-// two neighbouring score tiles are the A operand of a 16-position step of P V.
-template <int D, int WM>
-__global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long sums[kThreads];
-    __shared__ float2 ml_s[4][16];
-    constexpr int BM = 16 * WM, WN = 4 / WM;
-    constexpr int NCH = D / 8, KS = D / 16, DN = D / 8;
-    constexpr int KW = kKeys / WN, NT = KW / 8;  // a warp's positions of a tile, 8-wide tiles of them
-    constexpr uint32_t TB = kKeys * D * 2;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, u = lane & 3;
-    const int wm = warp / WN, wn = warp % WN;
-    Walk cur;
-    const bool any = cur.begin(a, sums, kThreads, line_scan(a, sums, kThreads));
-    q4d::pdl_trigger();  // the joining kernel's blocks may start; they wait for this grid's end
-    if (!any) return;
-    Walk ld = cur;
-    const uint32_t sm0 = q4d::smem_addr(smem);
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
 
-    // Tile `ld` into stage st: a thread takes one 16-byte chunk column of
-    // every (kThreads / NCH)-th row.  Positions behind the sequence (stale
-    // rows hold anything, and 0 * NaN would reach the sums) become zeros.
-    auto load = [&](int st) {
-        const uint32_t kb = sm0 + (uint32_t)st * 2u * TB, vb = kb + TB;
-        const int c = tid % NCH, r0 = tid / NCH;
-        const int len = ld.p.q.ctx + ld.p.q.n;
+// Adds to columns c0 .. c1 - 1 of a written row (fp16 `out`, else fp32 `part`)
+// the infinities and NaN of the new rows it sees in the segment's T tiles.
+template <int D>
+__device__ __noinline__ void add_odd(const Args& a, const Place& p, int T, int tok, int c0, int c1, uint16_t* out,
+                                     float* part) {
+    const int n0 = max(0, p.tile * a.KT - p.q.ctx), n1 = min(p.q.n, (p.tile + T) * a.KT - p.q.ctx);
+    for (int nj = n0; nj < n1; ++nj) {
+        if (!sees(a, p.q.start, tok, nj)) continue;
+        const long long at = q4p::row_at(a.w, p.s, p.q.ctx + nj, p.h, D);
+        if (at < 0) continue;
+        for (int c = c0; c < c1; ++c) {
+            const uint16_t v = a.w.v[at + c];
+            if (finite16(v)) continue;
+            const float f = __half2float(__ushort_as_half(v));
+            if (out) out[c] = __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(out[c])) + f));
+            else part[c] += f;
+        }
+    }
+}
+
+// ------------------------------------------------- mma.sync: few rows per job ---
+// WM warps along the job's 16 WM rows, WN = 4 / WM along the tile's
+// positions, and a fifth warp that brings the tiles: by TMA where a page is a
+// multiple of 8 rows (boxes of `box` rows, the greatest power of two up to 64
+// that divides the page; a page that does not exist is read outside the map,
+// where TMA fills in zeros), else by 16-byte cp.async from row to row.  The
+// consumers never meet while they walk a job: a stage is handed over by its
+// "full" and "empty" barriers alone.
+// Fragment layouts of mma.m16n8k16 (g = lane / 4, u = lane % 4): A covers rows
+// g, g + 8 and columns 2u, 2u+1, 2u+8, 2u+9; B rows 2u, 2u+1, 2u+8, 2u+9 of
+// column g; an accumulator rows g, g + 8, columns 2u, 2u+1, so two
+// neighbouring score tiles are the A operand of a 16-position step of P V.
+//
+// kCluster: few jobs (one or two users' decoding), where latency counts.  The
+// 16 CTAs of a cluster take a job's tiles together and join their parts
+// through distributed shared memory: one launch, and no line to walk.
+constexpr int kCluster = 16;
+constexpr int kConsumers = 128, kThreads = 160;
+
+template <int D>
+struct Ring {
+    static constexpr uint32_t kTile = kKeys * D * 2;  // keys or values of a tile
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kTile + 256;
+};
+
+struct RingBars {
+    uint64_t full[kStages], empty[kStages];
+    volatile int abort;
+    volatile int odd[2];  // last segment (by parity) that met infinities or NaN among its new rows' values
+};
+
+// Byte offset of row r, 16-byte chunk c in a tile of 64-wide swizzled slabs of 64 rows.
+__device__ __forceinline__ uint32_t ring_off(int r, int c) {
+    return (uint32_t)((c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ bool ring_wait(RingBars& B, uint64_t& bar, uint32_t parity, int* err) {
+    if (B.abort) return false;
+    if (q4d::mbar_wait(q4d::smem_addr(&bar), parity, err)) return true;
+    B.abort = 1;
+    return false;
+}
+
+struct MapArgs {
+    Args a;
+    int box;       // rows per TMA box
+    int zero_row;  // a row outside the maps
+    int blocks;    // kCluster: row blocks per sequence (at most)
+};
+
+template <int D, int WM, bool kTma, bool kClustered>
+__global__ void __launch_bounds__(kThreads, 2)
+    tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ MapArgs t) {
+    constexpr int BM = 16 * WM, WN = 4 / WM;
+    constexpr int NCH = D / 8, KS = D / 16, DN = D / 8, SLABS = D / 64;
+    constexpr int KW = kKeys / WN, NT = KW / 8;  // a warp's positions of a tile, 8-wide tiles of them
+    constexpr uint32_t TB = Ring<D>::kTile;
+    const Args& a = t.a;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ unsigned sums[kThreads];
+    __shared__ float2 ml_s[4 * 16], fin_s[kClustered ? BM : 1];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    RingBars& B = *reinterpret_cast<RingBars*>(smem + kStages * 2 * TB);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            // by cp.async every lane of the producing warp arrives
+            q4d::mbar_init(q4d::smem_addr(&B.full[i]), kTma ? 1 : 32);
+            q4d::mbar_init(q4d::smem_addr(&B.empty[i]), 4);
+        }
+        B.abort = 0;
+        B.odd[0] = B.odd[1] = 0;
+        q4d::fence_mbar_init();
+    }
+    Walk w;
+    bool any;
+    int rank = 0;
+    if constexpr (kClustered) {
+        const int job = blockIdx.x / kCluster;
+        rank = blockIdx.x % kCluster;
+        bool bad;
+        Place& p = w.p;
+        p.s = job / (a.w.H * t.blocks);
+        p.h = job / t.blocks % a.w.H;
+        p.rb = job % t.blocks;
+        p.q = q4p::seq_of(a.w, p.s, bad);
+        if (bad && rank == 0 && tid == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
+        if (p.rb * BM >= p.q.n * a.G) return;  // (the whole cluster)
+        p.tiles = block_tiles(a, p.q, p.rb);
+        p.tile = (int)((unsigned)(p.tiles * rank) / kCluster);  // tiles * 16 stays below 2^31
+        w.end = (int)((unsigned)(p.tiles * (rank + 1)) / kCluster);
+        p.cost = 1;
+        p.start = 0;
+        w.x1 = 0;  // no more segments
+        any = p.tile < w.end;
+        __syncthreads();
+    } else {
+        any = w.begin(a, sums, kThreads, line_scan(a, sums, kThreads));
+        q4d::pdl_trigger();  // the joining kernel's blocks may start; they wait for this grid's end
+        if (!any) return;
+    }
+    Place& p = w.p;
+
+    if (warp == 4) {
+        // ------------------------------------------------- tiles
+        bool ok = true, rest = any;
+        uint32_t kt = 0;
+        while (rest && ok) {
+            const int len = p.q.ctx + p.q.n;
+            for (; p.tile < w.end && ok; ++p.tile, ++kt) {
+                const int st = kt % kStages;
+                const uint32_t fb = q4d::smem_addr(&B.full[st]);
+                uint8_t* kv = smem + st * 2 * TB;
+                if constexpr (kTma) {
+                    // lanes 0 .. 7: boxes of keys, 8 .. 15: of values
+                    const int b = lane & 7, key = p.tile * kKeys + b * t.box;
+                    const bool mine = lane < 16 && b * t.box < kKeys;
+                    int y = t.zero_row;
+                    if (mine && key < len) {
+                        const long long at = q4p::row_at(a.w, p.s, key, p.h, 1);
+                        if (at >= 0) y = (int)at;
+                        else atomicOr(a.w.err, q4d::kErrDeviceCheck);
+                    }
+                    if (kt >= kStages) ok = ring_wait(B, B.empty[st], (kt / kStages - 1) & 1, a.w.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) q4d::mbar_arrive_expect_tx(fb, 2 * TB);
+                    __syncwarp();
+                    if (mine) {
+                        const uint32_t dst = q4d::smem_addr(kv + (lane >> 3) * TB) + (uint32_t)(b * t.box) * 128u;
 #pragma unroll
-        for (int i = 0; i < kKeys * NCH / kThreads; ++i) {
-            const int r = r0 + i * (kThreads / NCH);
-            const int key = ld.p.tile * kKeys + r;
-            long long at = -1;
-            if (key < len) {
-                at = q4p::row_at(a.w, ld.p.s, key, ld.p.h, D);
-                if (at < 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
+                        for (int sl = 0; sl < SLABS; ++sl)
+                            q4t::tma_load_2d(dst + sl * (kKeys * 128), lane < 8 ? &tmK : &tmV, 64 * sl, y, fb);
+                    }
+                } else {
+                    if (kt >= kStages) ok = ring_wait(B, B.empty[st], (kt / kStages - 1) & 1, a.w.err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    // a lane looks two rows up; the lanes of a row share it
+                    const uint32_t kb = q4d::smem_addr(kv);
+                    constexpr int PER = 32 / NCH;
+                    const int c = lane % NCH;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        const int key = p.tile * kKeys + half * 32 + lane;
+                        long long at = -1;
+                        if (key < len) {
+                            at = q4p::row_at(a.w, p.s, key, p.h, D);
+                            if (at < 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
+                        }
+#pragma unroll 4
+                        for (int e = 0; e < 32; e += PER) {
+                            const int r = e + lane / NCH;
+                            const long long row = __shfl_sync(0xffffffffu, at, r);
+                            const long long off = (row < 0 ? 0 : row) + 8 * c;
+                            const uint32_t to = kb + ring_off(half * 32 + r, c);
+                            cp16(to, a.w.k + off, row >= 0);
+                            cp16(to + TB, a.w.v + off, row >= 0);
+                        }
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
+                }
             }
-            const bool live = at >= 0;
-            const long long off = (live ? at : 0) + 8 * c;
-            cp16(kb + swz<D>(r, c), a.w.k + off, live);
-            cp16(vb + swz<D>(r, c), a.w.v + off, live);
+            rest = w.more();
+            if (rest && ok) w.next(a);
         }
-    };
-    bool more = true;  // tiles to load
-    const auto load_next = [&](int st) {
-        if (!more) return;
-        load(st);
-        if (++ld.p.tile == ld.end) {
-            more = ld.more();
-            if (more) ld.next(a);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-        load_next(i);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        if constexpr (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
+        if (kTma && !ok)  // copies still in flight land before the CTA can exit
+            for (uint32_t i = kt > kStages ? kt - kStages : 0; i < kt; ++i)
+                q4d::mbar_wait(q4d::smem_addr(&B.full[i % kStages]), (i / kStages) & 1, nullptr);
+        if constexpr (!kClustered) return;
     }
 
+    // ----------------------------------------------------- scores and values
+    // A failed wait (latched) does not leave the loops: the results are void,
+    // but every warp still comes to the barriers the others wait at.
+    const int g = lane >> 2, u = lane & 3;
+    const int wm = warp / WN, wn = warp % WN;
     uint32_t qf[KS][4];
     float o[DN][4], m[2], l[2];
-    bool fresh = true;   // the job's first tile in this CTA
-    bool begun = cur.p.tile == 0;  // ... and in the line
-    const int row0 = wm * 16 + g;  // this thread's rows of the job: row0, row0 + 8
-    for (int st = 0;; st = st + 1 == kStages ? 0 : st + 1) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncthreads();
-        load_next(st == 0 ? kStages - 1 : st - 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const uint32_t kb = sm0 + (uint32_t)st * 2u * TB, vb = kb + TB;
-        const int R = min(BM, cur.p.q.n * a.G - cur.p.rb * BM);
+    bool fresh = true;              // the job's first tile in this CTA
+    bool begun = p.tile == 0;       // ... and in the line
+    const int row0 = wm * 16 + g;   // this thread's rows of the job: row0, row0 + 8
+    uint32_t seg = 0, kt = 0;
+    int seg_tile = p.tile;          // the segment's first tile
+    const bool consume = warp < 4 && any;
+    while (consume) {
+        const int st = kt % kStages;
+        const int R = min(BM, p.q.n * a.G - p.rb * BM);
+        int tok[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) tok[e] = (int)q4p::page_of(a.by_g, p.rb * BM + min(row0 + 8 * e, R - 1));
         if (fresh) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = row0 + 8 * e, rr = cur.p.rb * BM + r;
-                const int tok = (int)q4p::page_of(a.by_g, rr), head = cur.p.h * a.G + rr - tok * a.G;
-                const uint16_t* src = a.q + (cur.p.q.start + tok) * a.ldq + (long long)head * D + 2 * u;
+                const bool live = row0 + 8 * e < R;
+                const int rr = p.rb * BM + min(row0 + 8 * e, R - 1);
+                const uint16_t* src = a.q + (size_t)(p.q.start + tok[e]) * a.ldq + (size_t)(p.h * a.G + rr - tok[e] * a.G) * D + 2 * u;
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
-                    qf[kk][e] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
-                    qf[kk][2 + e] = r < R ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8) : 0u;
+                    qf[kk][e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
+                    qf[kk][2 + e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8) : 0u;
                 }
                 m[e] = -INFINITY;
                 l[e] = 0.f;
@@ -356,48 +509,40 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
 #pragma unroll
             for (int dn = 0; dn < DN; ++dn) o[dn][0] = o[dn][1] = o[dn][2] = o[dn][3] = 0.f;
             fresh = false;
+            seg_tile = p.tile;
         }
-        const int key0 = cur.p.tile * kKeys;
-        const bool tail = key0 + kKeys > cur.p.q.ctx;  // the tile holds new rows, or the end
-        const int tok[2] = {(int)q4p::page_of(a.by_g, cur.p.rb * BM + row0), (int)q4p::page_of(a.by_g, cur.p.rb * BM + row0 + 8)};
+        const uint32_t kb = q4d::smem_addr(smem + st * 2 * TB), vb = kb + TB;
+        ring_wait(B, B.full[st], (kt / kStages) & 1, a.w.err);
+        __syncwarp();
+        const int key0 = p.tile * kKeys;
+        const bool tail = key0 + kKeys > p.q.ctx;  // the tile holds new rows, or the end
         if (tail) {
-            // A new row's value reaches only the rows that see it: infinities
-            // and NaN of the tile are added to those by hand and then
-            // cleared, as their products with a zero probability would be NaN.
-            bool odd = false;
-            for (int y = tid; y < kKeys * NCH; y += kThreads) {
-                const int r = y / NCH, c = y % NCH;
-                if (key0 + r < cur.p.q.ctx) continue;
-                const uint4 w = *reinterpret_cast<const uint4*>(smem + (vb - sm0) + swz<D>(r, c));
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) odd |= !finite16((uint16_t)ws[e]) || !finite16((uint16_t)(ws[e] >> 16));
-            }
-            if (__syncthreads_or(odd)) {
-                for (int j = 0; j < KW; ++j) {
-                    const int r = wn * KW + j, nj = key0 + r - cur.p.q.ctx;
-                    if (nj < 0 || nj >= cur.p.q.n) continue;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (row0 + 8 * e >= R || !sees(a, cur.p.q.start, tok[e], nj)) continue;
-#pragma unroll
-                        for (int dn = 0; dn < DN; ++dn) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t*>(smem + (vb - sm0) + swz<D>(r, dn) + 4 * u);
-                            const uint16_t lo = (uint16_t)w, hi = (uint16_t)(w >> 16);
-                            if (!finite16(lo)) o[dn][2 * e] += __half2float(__ushort_as_half(lo));
-                            if (!finite16(hi)) o[dn][2 * e + 1] += __half2float(__ushort_as_half(hi));
-                        }
-                    }
+            // A new row's value reaches only the rows that see it, and what
+            // lies behind the sequence nobody: those rows are cleared, or
+            // their infinities and NaN, which are added back at the end where
+            // they are seen.  (Warps of the same positions write the same.)
+            bool found = false;
+            for (int y = lane; y < KW * NCH; y += 32) {
+                const int r = wn * KW + y / NCH, c = y % NCH, nj = key0 + r - p.q.ctx;
+                if (nj < 0) continue;
+                uint4* at = reinterpret_cast<uint4*>(smem + st * 2 * TB + TB + ring_off(r, c));
+                if (nj >= p.q.n) {
+                    *at = make_uint4(0, 0, 0, 0);
+                    continue;
                 }
-                __syncthreads();
-                for (int y = tid; y < kKeys * D; y += kThreads) {
-                    const int r = y / D, d = y % D;
-                    if (key0 + r < cur.p.q.ctx) continue;
-                    uint16_t* v = reinterpret_cast<uint16_t*>(smem + (vb - sm0) + swz<D>(r, d / 8)) + d % 8;
-                    if (!finite16(*v)) *v = 0;
+                const uint4 v = *at;
+                uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!finite16((uint16_t)ws[e])) ws[e] &= 0xffff0000u, bad = true;
+                    if (!finite16((uint16_t)(ws[e] >> 16))) ws[e] &= 0x0000ffffu, bad = true;
                 }
-                __syncthreads();
+                if (bad) *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+                found |= bad;
             }
+            if (found) B.odd[seg & 1] = (int)seg + 1;
+            __syncwarp();
         }
         // scores
         float sc[NT][4];
@@ -408,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 uint32_t b[4];
-                ldsm4(kb + swz<D>(wn * KW + nt * 8 + (lane & 7), 2 * kk + (lane >> 3)), b);
+                ldsm4(kb + ring_off(wn * KW + nt * 8 + (lane & 7), 2 * kk + (lane >> 3)), b);
                 mma(sc[nt], qf[kk], b[0], b[1]);
                 mma(sc[nt], qf[kk + 1], b[2], b[3]);
             }
@@ -418,9 +563,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int nj = key0 + wn * KW + nt * 8 + 2 * u + (e & 1) - cur.p.q.ctx;
-                    if (nj >= 0 && (nj >= cur.p.q.n || row0 + 8 * (e >> 1) >= R || !sees(a, cur.p.q.start, tok[e >> 1], nj)))
-                        sc[nt][e] = -INFINITY;
+                    const int nj = key0 + wn * KW + nt * 8 + 2 * u + (e & 1) - p.q.ctx;
+                    if (nj >= 0 && (nj >= p.q.n || !sees(a, p.q.start, tok[e >> 1], nj))) sc[nt][e] = -INFINITY;
                 }
         }
         uint32_t pa[NT / 2][4];
@@ -431,25 +575,25 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
             for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][2 * e], sc[nt][2 * e + 1]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // a negative scale turns the order round: the greatest of s c
-            // then comes from the smallest s; c > 0 is checked on the host
-            const float mn = fmaxf(m[e], mx * a.c);
+            const float mn = fmaxf(m[e], mx * a.c);  // (c is positive: checked on the host)
             const float ms = mn == -INFINITY ? 0.f : mn;
-            const float f = exp2f(m[e] - ms);
+            const float f = ex2(m[e] - ms);
             m[e] = mn;
             float sum = 0.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = exp2f(fmaf(sc[nt][2 * e], a.c, kShift - ms));
-                const float p1 = exp2f(fmaf(sc[nt][2 * e + 1], a.c, kShift - ms));
+                const float p0 = ex2(fmaf(sc[nt][2 * e], a.c, kShift - ms));
+                const float p1 = ex2(fmaf(sc[nt][2 * e + 1], a.c, kShift - ms));
                 sum += p0 + p1;
                 pa[nt >> 1][(nt & 1) * 2 + e] = pack2(p0, p1);
             }
             l[e] = fmaf(l[e], f, sum);
+            if (__any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-            for (int dn = 0; dn < DN; ++dn) {
-                o[dn][2 * e] *= f;
-                o[dn][2 * e + 1] *= f;
+                for (int dn = 0; dn < DN; ++dn) {
+                    o[dn][2 * e] *= f;
+                    o[dn][2 * e + 1] *= f;
+                }
             }
         }
 #pragma unroll
@@ -457,39 +601,42 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
 #pragma unroll
             for (int dn = 0; dn < DN; dn += 2) {
                 uint32_t b[4];
-                ldsm4_t(vb + swz<D>(wn * KW + kj * 16 + (lane & 15), dn + (lane >> 4)), b);
+                ldsm4_t(vb + ring_off(wn * KW + kj * 16 + (lane & 15), dn + (lane >> 4)), b);
                 mma(o[dn], pa[kj], b[0], b[1]);
                 mma(o[dn + 1], pa[kj], b[2], b[3]);
             }
 
-        const bool job_end = cur.p.tile + 1 == cur.p.tiles;
-        if (cur.p.tile + 1 == cur.end) {
+        const bool job_end = p.tile + 1 == p.tiles, seg_end = p.tile + 1 == w.end;
+        if (seg_end) {
             // the row sums over the quad's columns, then over the WN warps
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
             }
+            // The warps' outputs meet in this tile's stage, [WN][BM][D] fp32
+            // (at most 32 KB), which is still ours; a cluster's CTA has
+            // consumed all it loads, and takes stage 0, so that the others
+            // know the place.
+            float* ob = reinterpret_cast<float*>(smem + (kClustered ? 0 : st * 2 * TB));
+            static_assert((size_t)WN * BM * D * 4 <= 2 * TB, "joining space");
+            if constexpr (WN > 1 || kClustered) q4d::named_bar(1, kConsumers);  // nobody reads the tiles any more
             if constexpr (WN > 1) {
-                // this tile's stage is free until the next iteration's barrier:
-                // the warps' outputs meet there, [WN][BM][D] fp32 (at most 32 KB)
-                static_assert((size_t)WN * BM * D * 4 <= 2 * TB, "joining space");
                 if (u == 0) {
-                    ml_s[warp][g] = make_float2(m[0], l[0]);
-                    ml_s[warp][g + 8] = make_float2(m[1], l[1]);
+                    ml_s[warp * 16 + g] = make_float2(m[0], l[0]);
+                    ml_s[warp * 16 + g + 8] = make_float2(m[1], l[1]);
                 }
-                __syncthreads();
-                float* ob = reinterpret_cast<float*>(smem + (kb - sm0));
+                q4d::named_bar(1, kConsumers);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = g + 8 * e;
                     float mm = -INFINITY, ls = 0.f;
 #pragma unroll
-                    for (int i = 0; i < WN; ++i) mm = fmaxf(mm, ml_s[wm * WN + i][r].x);
+                    for (int i = 0; i < WN; ++i) mm = fmaxf(mm, ml_s[(wm * WN + i) * 16 + r].x);
                     const float ms = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-                    for (int i = 0; i < WN; ++i) ls = fmaf(ml_s[wm * WN + i][r].y, exp2f(ml_s[wm * WN + i][r].x - ms), ls);
-                    const float f = exp2f(m[e] - ms);
+                    for (int i = 0; i < WN; ++i) ls = fmaf(ml_s[(wm * WN + i) * 16 + r].y, ex2(ml_s[(wm * WN + i) * 16 + r].x - ms), ls);
+                    const float f = ex2(m[e] - ms);
                     float* dst = ob + ((size_t)wn * BM + wm * 16 + r) * D + 2 * u;
 #pragma unroll
                     for (int dn = 0; dn < DN; ++dn)
@@ -497,61 +644,142 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
                     m[e] = mm;
                     l[e] = ls;
                 }
-                __syncthreads();
+                q4d::named_bar(1, kConsumers);
                 if (wn == 0) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int dn = 0; dn < DN; ++dn) {
-                            float2 t = make_float2(0.f, 0.f);
+                            float2 v = make_float2(0.f, 0.f);
 #pragma unroll
                             for (int i = 0; i < WN; ++i) {
-                                const float2 v = *reinterpret_cast<const float2*>(
+                                const float2 x = *reinterpret_cast<const float2*>(
                                     ob + ((size_t)i * BM + wm * 16 + g + 8 * e) * D + 2 * u + 8 * dn);
-                                t.x += v.x;
-                                t.y += v.y;
+                                v.x += x.x;
+                                v.y += x.y;
                             }
-                            o[dn][2 * e] = t.x;
-                            o[dn][2 * e + 1] = t.y;
+                            o[dn][2 * e] = v.x;
+                            o[dn][2 * e + 1] = v.y;
                         }
                 }
             }
-            if (wn == 0) {
-                if (begun && job_end) {
+            if (kClustered && wn == 0) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = row0 + 8 * e, rr = cur.p.rb * BM + r;
-                        if (r >= R) continue;
-                        const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
-                        uint16_t* dst = a.out + (long long)(cur.p.q.start + rr / a.G) * a.ldo +
-                                        (long long)(cur.p.h * a.G + rr % a.G) * D + 2 * u;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row0 + 8 * e;
+                    if (u == 0) fin_s[r] = make_float2(m[e], l[e]);
 #pragma unroll
-                        for (int dn = 0; dn < DN; ++dn)
-                            *reinterpret_cast<uint32_t*>(dst + 8 * dn) = pack2(o[dn][2 * e] * inv, o[dn][2 * e + 1] * inv);
+                    for (int dn = 0; dn < DN; ++dn)  // (over this thread's own elements of the warps' outputs)
+                        *reinterpret_cast<float2*>(ob + (size_t)r * D + 2 * u + 8 * dn) = make_float2(o[dn][2 * e], o[dn][2 * e + 1]);
+                }
+            }
+            if (!kClustered && wn == 0) {
+                const bool whole = begun && job_end;
+                const int slot = 2 * blockIdx.x + (begun ? 1 : 0);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = row0 + 8 * e, rr = p.rb * BM + r;
+                    if (r >= R) continue;
+                    const float inv = !whole ? 1.f : l[e] == 0.f ? 0.f : 1.f / l[e];
+                    uint16_t* out = a.out + (size_t)(p.q.start + tok[e]) * a.ldo + (size_t)(p.h * a.G + rr - tok[e] * a.G) * D;
+                    float* part = part_o<D>(a, slot) + (size_t)r * D;
+                    if (!whole && u == 0) part_ml(a, slot)[r] = make_float2(m[e], l[e]);
+#pragma unroll
+                    for (int dn = 0; dn < DN; ++dn) {
+                        const float x = o[dn][2 * e] * inv, y = o[dn][2 * e + 1] * inv;
+                        if (whole) *reinterpret_cast<uint32_t*>(out + 8 * dn + 2 * u) = pack2(x, y);
+                        else *reinterpret_cast<float2*>(part + 8 * dn + 2 * u) = make_float2(x, y);
                     }
-                } else {
-                    const int slot = 2 * blockIdx.x + (begun ? 1 : 0);
-                    float* po = part_o<D>(a, slot);
-                    float2* pm = part_ml(a, slot);
-#pragma unroll
+                }
+                if (B.odd[seg & 1] == (int)seg + 1) {
+                    __syncwarp();  // the rows are written
+                    Place from = p;
+                    from.tile = seg_tile;
                     for (int e = 0; e < 2; ++e) {
-                        const int r = row0 + 8 * e;
-                        if (r >= R) continue;
-                        if (u == 0) pm[r] = make_float2(m[e], l[e]);
-#pragma unroll
-                        for (int dn = 0; dn < DN; ++dn)
-                            *reinterpret_cast<float2*>(po + (size_t)r * D + 8 * dn + 2 * u) =
-                                make_float2(o[dn][2 * e], o[dn][2 * e + 1]);
+                        const int r = row0 + 8 * e, rr = p.rb * BM + r;
+                        if (r >= R || u != 0) continue;
+                        add_odd<D>(a, from, p.tile + 1 - seg_tile, tok[e], 0, D,
+                                   whole ? a.out + (size_t)(p.q.start + tok[e]) * a.ldo + (size_t)(p.h * a.G + rr - tok[e] * a.G) * D : nullptr,
+                                   part_o<D>(a, slot) + (size_t)r * D);
                     }
                 }
             }
             fresh = true;
             begun = true;
+            ++seg;
         }
-        if (++cur.p.tile == cur.end) {
-            if (!cur.more()) break;
-            cur.next(a);
+        // the stage goes back (what this thread did to it stands before the next copy)
+        if (kTma && (tail || seg_end)) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.empty[st]));
+        ++kt;
+        if (++p.tile == w.end) {
+            if (!w.more()) break;
+            w.next(a);
         }
+    }
+    if constexpr (kClustered) {
+        // ------------------------------------------------- the cluster's parts
+        const int R = min(BM, p.q.n * a.G - p.rb * BM);
+        float* ob = reinterpret_cast<float*>(smem);
+        if (!any) {
+            for (int y = tid; y < R * D; y += kThreads) ob[y] = 0.f;
+            for (int r = tid; r < R; r += kThreads) fin_s[r] = make_float2(-INFINITY, 0.f);
+        }
+        __syncwarp();
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();
+        const int r = rank * 4 + warp;  // a warp per row, the rows spread over the CTAs (BM <= 64)
+        if (warp < 4 && r < R) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            bool odd = false;
+            if (lane < kCluster) {
+                ml = *cl.map_shared_rank(&fin_s[r], lane);
+                odd = *cl.map_shared_rank(const_cast<int*>(&B.odd[0]), lane) != 0;
+            }
+            float mm = ml.x;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+            const float f = ex2(ml.x - (mm == -INFINITY ? 0.f : mm));
+            float ls = lane < kCluster ? ml.y * f : 0.f;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+            constexpr int E = D / 32;
+            float v[kCluster][E];
+#pragma unroll
+            for (int i = 0; i < kCluster; ++i) {
+                const float* src = cl.map_shared_rank(ob + (size_t)r * D + E * lane, i);
+                if constexpr (E == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src);
+                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(src);
+                    v[i][0] = x.x, v[i][1] = x.y;
+                }
+            }
+            float acc[E] = {};
+#pragma unroll
+            for (int i = 0; i < kCluster; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], fi, acc[e]);
+            }
+            const float inv = ls == 0.f ? 0.f : 1.f / ls;
+            const int rr = p.rb * BM + r, tok = (int)q4p::page_of(a.by_g, rr);
+            uint16_t* out = a.out + (size_t)(p.q.start + tok) * a.ldo + (size_t)(p.h * a.G + rr - tok * a.G) * D;
+            uint32_t y[E / 2];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) y[e / 2] = pack2(acc[e] * inv, acc[e + 1] * inv);
+            if constexpr (E == 4) *reinterpret_cast<uint2*>(out + E * lane) = make_uint2(y[0], y[1]);
+            else *reinterpret_cast<uint32_t*>(out + E * lane) = y[0];
+            if (__any_sync(0xffffffffu, odd)) {
+                __syncwarp();  // the row is written
+                Place from = p;
+                from.tile = 0;
+                if (lane == 0) add_odd<D>(a, from, p.tiles, tok, 0, D, out, nullptr);
+            }
+        }
+        cl.sync();  // no CTA leaves while another reads its part
     }
 }
 
@@ -561,18 +789,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_attn_kernel(const Args a) {
 constexpr int kJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Args a) {
-    __shared__ long long sums[kJoinThreads];
-    const long long line = line_scan(a, sums, kJoinThreads);
-    const long long share = line_share(a, line);
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ Args a) {
+    __shared__ unsigned sums[kJoinThreads];
+    const unsigned line = line_scan(a, sums, kJoinThreads);
+    const unsigned share = line_share(a, line), xb = share * blockIdx.x, x = xb + share;
     const int b = blockIdx.x;
-    const long long xb = share * b, x = xb + share;
     Place p;
-    long long last_at = 0;  // the job's last tile's place
+    unsigned last_at = 0;  // the job's last tile's place
     bool work = x < line;
     if (work) {
         p = line_find(a, sums, kJoinThreads, x);
-        last_at = p.start + (long long)(p.tiles - 1) * p.cost;
+        last_at = p.start + (unsigned)((p.tiles - 1) * p.cost);
         work = p.start >= xb && p.start < x && last_at >= x;  // begun in CTA b, not ended there
     }
     // the parts are written (and no grid that follows this one starts before
@@ -616,7 +843,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const Args a) {
                 }
             }
             const int n = min(32, last - c0 + 1);
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < n; ++k) {
                 const float* src = part_o<D>(a, slot_of(c0 + k)) + (size_t)r0 * D + E * lane;
 #pragma unroll
@@ -686,20 +913,75 @@ cudaError_t launch_join(const Args& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a);
 }
 
-template <int D, int WM>
-cudaError_t launch(Args& a, void* workspace, int sms, cudaStream_t s) {
-    static std::atomic<int> marks[64];
-    cudaError_t e = q4i::ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_kernel<D, WM>), marks, (int)attn_smem<D>());
+// The pools as 2-D maps [rows][D], boxes of 64 x box elements.
+inline q4_status pool_maps(CUtensorMap* k, CUtensorMap* v, const q4_paged_cache& c, uint32_t box) {
+    const uint64_t rows = (uint64_t)c.n_pages * c.n_kv_heads * c.page_size, D = (uint64_t)c.head_dim;
+    const q4_status st = q4i::make_map(k, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.k, D, rows, D * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != Q4_OK) return st;
+    return q4i::make_map(v, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.v, D, rows, D * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int D, int WM, bool kTma, bool kClustered>
+cudaError_t launch_kernel(const CUtensorMap& k, const CUtensorMap& v, const MapArgs& t, int grid, cudaStream_t s) {
+    static std::atomic<int> marks[64], wide[64];
+    const auto kern = tree_attn_kernel<D, WM, kTma, kClustered>;
+    const void* fn = reinterpret_cast<const void*>(kern);
+    cudaError_t e = q4i::ensure_smem_attr(fn, marks, (int)Ring<D>::kSmem);
     if (e != cudaSuccess) return e;
-    a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<D>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    if (kClustered) {
+        int dev = 0;
+        cudaGetDevice(&dev);
+        if (!wide[dev & 63].load(std::memory_order_acquire)) {
+            if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+            wide[dev & 63].store(1, std::memory_order_release);
+        }
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = kCluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, k, v, t);
+}
+
+// box 0: no TMA.
+template <int D, int WM>
+q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int box, cudaStream_t s) {
+    MapArgs t;
+    CUtensorMap k = {}, v = {};
     a.BM = 16 * WM;
     a.KT = kKeys;
     a.KT_log2 = 6;
     a.cost_full = a.cost_half = 1;
+    a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
     place_parts<D>(a, workspace);
-    tree_attn_kernel<D, WM><<<a.ctas, kThreads, attn_smem<D>(), s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_join<D>(a, s);
+    if (box) {
+        const q4_status st = pool_maps(&k, &v, c, (uint32_t)box);
+        if (st != Q4_OK) return st;
+    }
+    t.box = box;
+    t.zero_row = (int)((long long)c.n_pages * c.n_kv_heads * c.page_size);
+    // Clusters where two CTAs per SM hold all of them.
+    const long long blocks = ((long long)a.w.rows * a.G + a.BM - 1) / a.BM, jobs = blocks * c.n_seqs * c.n_kv_heads;
+    cudaError_t e;
+    if (jobs * kCluster <= 2 * sms) {
+        t.a = a;
+        t.blocks = (int)blocks;
+        e = box ? launch_kernel<D, WM, true, true>(k, v, t, (int)jobs * kCluster, s)
+                : launch_kernel<D, WM, false, true>(k, v, t, (int)jobs * kCluster, s);
+    } else {
+        t.a = a;
+        t.blocks = 0;
+        e = box ? launch_kernel<D, WM, true, false>(k, v, t, a.ctas, s) : launch_kernel<D, WM, false, false>(k, v, t, a.ctas, s);
+        if (e == cudaSuccess) e = launch_join<D>(a, s);
+    }
+    return e == cudaSuccess ? Q4_OK : q4i::cuda_fail(e, "q4_tree_attention launch");
 }
 
 // ------------------------------------------------- tcgen05: many rows per job ---
@@ -761,12 +1043,6 @@ __device__ __forceinline__ uint32_t sw_off(int r, int c) {  // row r, 16-byte ch
     return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
 }
 
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-    return p != 0;
-}
-
 // 32 consecutive 32-bit columns of this thread's tensor-memory lane.
 __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
     asm volatile(
@@ -787,12 +1063,6 @@ __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // Bits 0 .. 31: which of the positions behind new row j0 (negative: cached)
@@ -845,42 +1115,17 @@ __device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
     return found;
 }
 
-// Adds to columns c0 .. c1 - 1 of a written row (fp16 `out`, else fp32 `part`)
-// the infinities and NaN of the new rows it sees in the segment's T tiles.
-template <int D>
-__device__ __noinline__ void add_odd(const Args& a, const Place& p, int T, int tok, int c0, int c1, uint16_t* out,
-                                     float* part) {
-    const int n0 = max(0, p.tile * a.KT - p.q.ctx), n1 = min(p.q.n, (p.tile + T) * a.KT - p.q.ctx);
-    for (int nj = n0; nj < n1; ++nj) {
-        if (!sees(a, p.q.start, tok, nj)) continue;
-        const long long at = q4p::row_at(a.w, p.s, p.q.ctx + nj, p.h, D);
-        if (at < 0) continue;
-        for (int c = c0; c < c1; ++c) {
-            const uint16_t v = a.w.v[at + c];
-            if (finite16(v)) continue;
-            const float f = __half2float(__ushort_as_half(v));
-            if (out) out[c] = __half_as_ushort(__float2half_rn(__half2float(__ushort_as_half(out[c])) + f));
-            else part[c] += f;
-        }
-    }
-}
-
-struct TcArgs {
-    Args a;
-    int box;            // rows per TMA box
-    int zero_row;       // a row outside the maps
-};
-
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const TcArgs t) {
+    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ MapArgs t) {
     using Sh = TcShape<D>;
     constexpr uint32_t kTile = Sh::kTile;
     constexpr int NST = Sh::kStages, SLABS = D / 64;
     constexpr uint32_t kColS = 0, kColO = 256;
     const Args& a = t.a;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ long long sums[kTcThreads];
+    __shared__ unsigned sums[2 * 256];  // kTcThreads running sums; later (m, l) of both streams' rows
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* q_s = base;                              // two tiles; between segments, stream 1's O (fp32)
     uint8_t* k_s = base + 2 * kTile;
@@ -918,7 +1163,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const long long line = line_scan(a, sums, kTcThreads);
+    const unsigned line = line_scan(a, sums, kTcThreads);
     q4t::fence_before();
     __syncthreads();
     q4t::fence_after();
@@ -1094,19 +1339,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     uint8_t* dst = q_s + (two ? i : 0) * kTile;
                     constexpr int NC = D / 8, PER = 32 / NC;  // chunks of a row, rows per load
                     const int c = lane % NC;
-                    uint4 v[NC];
-#pragma unroll
-                    for (int e = 0; e < NC; ++e) {
-                        const int r = (two ? 128 * i : 0) + wr * 32 + e * PER + lane / NC;
-                        const int rr = w.rb * a.BM + r, tk = (int)q4p::page_of(a.by_g, rr);
-                        v[e] = make_uint4(0, 0, 0, 0);
-                        if (r < R)
-                            v[e] = *reinterpret_cast<const uint4*>(a.q + (size_t)(w.q.start + tk) * a.ldq +
-                                                                   (size_t)(w.h * a.G + rr - tk * a.G) * D + 8 * c);
+                    const uint32_t col = q4d::smem_addr(dst) + (uint32_t)(c >> 3) * 16384u;
+                    // (rolled: the loads are asynchronous, and code that runs
+                    // once per segment costs its instruction fetches)
+#pragma unroll 1
+                    for (int e = wr * 32 + lane / NC; e < wr * 32 + 32; e += PER) {
+                        const int r = (two ? 128 * i : 0) + e;
+                        const int rr = w.rb * a.BM + min(r, R - 1), tk = (int)q4p::page_of(a.by_g, rr);
+                        cp16(col + sw_off(e, c & 7),
+                             a.q + (size_t)(w.q.start + tk) * a.ldq + (size_t)(w.h * a.G + rr - tk * a.G) * D + 8 * c, r < R);
                     }
-#pragma unroll
-                    for (int e = 0; e < NC; ++e)
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + sw_off(wr * 32 + e * PER + lane / NC, c & 7)) = v[e];
+                    asm volatile("cp.async.wait_all;" ::: "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 __syncwarp();
@@ -1354,7 +1597,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 template <int D>
 q4_status launch_tc(Args& a, const q4_paged_cache& c, void* workspace, int sms, int box, cudaStream_t s) {
-    TcArgs t;
+    MapArgs t;
     a.ctas = sms < kMaxTcCtas ? sms : kMaxTcCtas;
     a.BM = kTcRows;
     a.KT = kTcKeys;
@@ -1364,14 +1607,11 @@ q4_status launch_tc(Args& a, const q4_paged_cache& c, void* workspace, int sms, 
     place_parts<D>(a, workspace);
     t.a = a;
     t.box = box;
-    const uint64_t rows = (uint64_t)c.n_pages * c.n_kv_heads * c.page_size;
-    t.zero_row = (int)rows;
+    t.zero_row = (int)((long long)c.n_pages * c.n_kv_heads * c.page_size);
+    t.blocks = 0;
     CUtensorMap tmK, tmV;
-    q4_status st;
-    if ((st = q4i::make_map(&tmK, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.k, D, rows, D * 2, 64, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_128B)) != Q4_OK)
-        return st;
-    if ((st = q4i::make_map(&tmV, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.v, D, rows, D * 2, 64, (uint32_t)box, CU_TENSOR_MAP_SWIZZLE_128B)) != Q4_OK)
-        return st;
+    const q4_status st = pool_maps(&tmK, &tmV, c, (uint32_t)box);
+    if (st != Q4_OK) return st;
     static std::atomic<int> marks[64];
     cudaError_t e = q4i::ensure_smem_attr(reinterpret_cast<const void*>(tree_attn_tc_kernel<D>), marks, (int)TcShape<D>::kSmem);
     if (e == cudaSuccess) {
@@ -1433,15 +1673,21 @@ extern "C" q4_status q4_tree_attention(const q4_tree_attention_desc* desc, q4_st
     // rows per job: the average sequence's, by 16, 32 or 64
     const long long avg = ((long long)d.rows * G + d.cache.n_seqs - 1) / d.cache.n_seqs;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int box = d.cache.page_size % 128 == 0 ? 128 : d.cache.page_size & -d.cache.page_size;
+    // TMA boxes: the greatest power of two that divides a page, 8 at least
+    const int even = d.cache.page_size & -d.cache.page_size;
     const long long pool_rows = (long long)d.cache.n_pages * d.cache.n_kv_heads * d.cache.page_size;
-    if (avg > 32 && box >= 8 && pool_rows < (1ll << 31) - 1)
+    const bool tma = even >= 8 && pool_rows < (1ll << 31) - 1;
+    const int ring_box = !tma ? 0 : even < q4x::kKeys ? even : q4x::kKeys;
+    if (avg > 32 && tma) {
+        const int box = even < q4x::kTcKeys ? even : q4x::kTcKeys;
         return D == 128 ? q4x::launch_tc<128>(a, d.cache, d.workspace, dev->sms, box, s)
                         : q4x::launch_tc<64>(a, d.cache, d.workspace, dev->sms, box, s);
-    cudaError_t e;
+    }
     if (D == 128)
-        e = avg <= 16 ? q4x::launch<128, 1>(a, d.workspace, dev->sms, s) : avg <= 32 ? q4x::launch<128, 2>(a, d.workspace, dev->sms, s) : q4x::launch<128, 4>(a, d.workspace, dev->sms, s);
-    else
-        e = avg <= 16 ? q4x::launch<64, 1>(a, d.workspace, dev->sms, s) : avg <= 32 ? q4x::launch<64, 2>(a, d.workspace, dev->sms, s) : q4x::launch<64, 4>(a, d.workspace, dev->sms, s);
-    return e == cudaSuccess ? Q4_OK : cuda_fail(e, "q4_tree_attention launch");
+        return avg <= 16   ? q4x::launch<128, 1>(a, d.cache, d.workspace, dev->sms, ring_box, s)
+               : avg <= 32 ? q4x::launch<128, 2>(a, d.cache, d.workspace, dev->sms, ring_box, s)
+                           : q4x::launch<128, 4>(a, d.cache, d.workspace, dev->sms, ring_box, s);
+    return avg <= 16   ? q4x::launch<64, 1>(a, d.cache, d.workspace, dev->sms, ring_box, s)
+           : avg <= 32 ? q4x::launch<64, 2>(a, d.cache, d.workspace, dev->sms, ring_box, s)
+                       : q4x::launch<64, 4>(a, d.cache, d.workspace, dev->sms, ring_box, s);
 }
