@@ -12,7 +12,7 @@
 // Weights are integers, round(2^44 2^-t) with t = (max - l) log2(e) / T: their
 // sums are exact in any order (2^19 of them stay below 2^63), so neither
 // atomics nor the split of the work can change a token.  A weight carries an
-// error near 2^-31 of itself (t as a float pair, below), where a plain fp32
+// error near 2^-30 of itself (t as a float pair, below), where a plain fp32
 // exponential's 2^-23 would move the borders of the tail's tokens, which are
 // narrower than that.
 //
@@ -25,13 +25,14 @@
 //      t that holds the N-th greatest of the threads' greatest logits (at
 //      least N tokens are as great), N = top_k or kWanted;
 //   3. the tokens above it into lists, and, unless top_k makes it needless,
-//      the weight of all; one CTA sorts the list (a few hundred), scans its
-//      weights and finds every limit in it.
-// What does not end inside the list (a flat distribution, the tail's share of
-// u) goes on: a histogram of counts and weights over 1536 bins of t, then the
-// tokens of the bin that holds the target, sorted as before; and where one
-// bin holds more than the list (thousands of equal logits), eight bits of the
-// key at a time.
+//      the weight of all and a histogram of the weights below it (1536 bins of
+//      t); one CTA sorts the list (a few hundred), scans its weights and finds
+//      in it whatever limit ends there.
+// A target below the list (a flat distribution's nucleus, the tail's share of
+// u) is found in the histogram; the tokens of its bin are collected and
+// sorted as before.  Where one bin holds more than such a list (thousands of
+// equal logits), and where the list itself overflows, the search goes eight
+// bits of the key at a time.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -48,10 +49,13 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 16;
-constexpr int kWanted = 512;         // tokens the list aims at without top_k
+constexpr int kWanted = 256;         // tokens the list aims at without top_k
 constexpr int kMostK = 1024;         // top_k up to which the list is tried
 constexpr int kList = 1024;          // tokens of a CTA's list
 constexpr int kAll = 2048;           // tokens of the joined list
+constexpr int kBinList = 1024;       // tokens of a bin that are sorted together
+constexpr int kCounting = 256;       // up to here a sort counts, per token, the greater ones
+constexpr int kMostPart = 1 << 17;   // tokens of a CTA: sums of 15-bit parts of their weights stay below 2^32
 constexpr int kCut = 512;            // bins of the threshold: 16 per octave
 constexpr int kBins = 1536;          // bins of the histogram: 32 per octave, 48 octaves (weights end at 45)
 constexpr u64 kOne = 1ull << 44;     // the weight of the greatest logit
@@ -69,17 +73,20 @@ struct Args {
 };
 
 struct Shared {
-    u64 xch[2][kMaxCluster][2];  // exchange between the CTAs, double-buffered
-    u64 red[kWarps + 1];
+    u64 xch[2][kMaxCluster][4];  // exchange between the CTAs, double-buffered
+    u64 red[4][kWarps];
     u64 result[4];
-    u64 all[kAll];    // the joined list, sorted
-    u64 pre[kAll];    // its running weights
+    u64 all[kAll];         // the joined list, sorted
+    u64 pre[kAll];         // its running weights
+    u64 bin_all[kBinList];  // likewise a bin's tokens
+    u64 bin_pre[kBinList];
     u64 list[kList];  // this CTA's tokens: key << 32 | ~index
     u64 mw[kBins];    // the cluster's histogram, then its running sums
     uint32_t mc[kBins];
-    uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's histogram; cnt is also the threshold's
-    uint32_t pow64[64];
-    uint32_t count;  // of list
+    uint32_t h0[kBins], h1[kBins], h2[kBins];  // this CTA's histogram: 15-bit parts of weights, or (count, low, high)
+    uint32_t cut_count[kCut];                  // the threads' greatest logits
+    float2 pow64[64];  // 2^(-j/64) in units of 2^-29: the integer's bits, and as a float
+    uint32_t count;    // of list
     int cut;
 };
 
@@ -101,30 +108,32 @@ struct Scale {
 // t in fp32, as the bins see it: monotone in the logit.
 __device__ __forceinline__ float coarse_t(float l, const Scale& c) { return l == c.max ? 0.f : (c.max - l) * c.hi; }
 
-__device__ __forceinline__ u64 weight_of(float l, const Scale& c, const uint32_t* pow64) {
+// round(2^44 2^-t).  Adding 1.5 2^23 rounds a float to an integer in its low
+// mantissa bits, which keeps conversions off the slow pipe.
+__device__ __forceinline__ u64 weight_of(float l, const Scale& c, const float2* pow64) {
+    constexpr float kMagic = 12582912.f;
     if (l == c.max) return kOne;
     // d + de = max - l exactly (the error of a difference is a float)
     const float d = c.max - l;
-    // t + te = (d + de) (hi + lo) to about 2^-46 of it
-    const float t = d * c.hi;
-    if (!(t < 46.f)) return 0;
+    if (!(d * c.hi < 46.f)) return 0;
     const float b = d - c.max;
     const float de = (c.max - (d - b)) + (-l - b);
-    const float te = fmaf(d, c.hi, -t) + fmaf(d, c.lo, de * c.hi);
-    const float n = floorf(t);
-    const float f = t - n;                    // exact
-    const int j = (int)(f * 64.f);            // 2^-f = 2^(-j/64) 2^-r
-    const float r = (f - (float)j * 0.015625f) + te;  // the difference is exact; |r| < 2^-6 + a little
-    // 2^-r = 1 - y, y = z - z^2 / 2 + z^3 / 6 - z^4 / 24, z = r ln 2; the next
-    // term is below 2^-39
-    const float z = r * 0.69314718f;
-    const float y = z * (1.f - z * (0.5f - z * (0.16666667f - z * 0.041666668f)));
-    const uint32_t p = pow64[j];
-    const long long m = (long long)p - (long long)__float2int_rn((float)p * y);  // units of 2^-32, about 2^31 .. 2^32
-    // 2^44 2^-n m 2^-32, rounded
-    const int sh = 12 - (int)n;
-    if (sh >= 0) return (u64)(m << sh);
-    return (u64)((m + (1ll << (-sh - 1))) >> -sh);
+    // 64 t = k + r, |r| <= 1/2 and a little: the product less k is one fused
+    // operation, so nothing of it is lost; then its smaller parts
+    const float hi = c.hi * 64.f, lo = c.lo * 64.f;  // exact
+    const float kf = fmaf(d, hi, kMagic);
+    const int k = __float_as_int(kf) - __float_as_int(kMagic);
+    const float r = fmaf(d, hi, -(kf - kMagic)) + fmaf(d, lo, de * hi);
+    // 2^(-r/64) = 1 - y, y = z - z^2 / 2 + z^3 / 6, z = r ln2 / 64 < 0.0055;
+    // the next term is below 2^-34
+    const float z = r * 0.010830425f;
+    const float y = z * (1.f - z * (0.5f - z * 0.16666667f));
+    const float2 p = pow64[k & 63];
+    const int q = __float_as_int(fmaf(p.y, y, kMagic)) - __float_as_int(kMagic);  // |p y| < 2^22
+    const u64 m = (u64)(uint32_t)(__float_as_int(p.x) - q);  // 2^28 .. 2^29
+    // 2^44 2^-(k / 64) m 2^-29, rounded
+    const int sh = 15 - (k >> 6);
+    return sh >= 0 ? m << sh : (m + (1ull << (-sh - 1))) >> -sh;
 }
 
 // This CTA's part of a row: 16-byte vectors v0 .. v1 - 1 behind `head` single
@@ -150,19 +159,19 @@ struct Part {
         if constexpr (HALF) return __half2float(__ushort_as_half(row[i]));
         else return row[i];
     }
-    // f(value, index) for every element of the part, four vectors in flight
-    // per thread; a thread's indices ascend.
-    template <typename F>
+    // f(value, index) for every element of the part, N vectors in flight per
+    // thread; a thread's indices ascend.
+    template <int N, typename F>
     __device__ __forceinline__ void each(F f) const {
         if (rank == 0 && (int)threadIdx.x < head) f(at(threadIdx.x), (int)threadIdx.x);
         const uint4* vec = reinterpret_cast<const uint4*>(row + head);
-        for (int v = v0 + threadIdx.x; v < v1; v += 4 * kThreads) {
-            uint4 w[4];
+        for (int v = v0 + threadIdx.x; v < v1; v += N * kThreads) {
+            uint4 w[N];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < N; ++i)
                 if (v + i * kThreads < v1) w[i] = vec[v + i * kThreads];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < N; ++i) {
                 if (v + i * kThreads >= v1) break;
                 const int at0 = head + (v + i * kThreads) * VE;
                 const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -180,16 +189,25 @@ struct Part {
     }
 };
 
-__device__ __forceinline__ u64 block_sum(u64 x, Shared& s) {
+// Sums of N values over the CTA, to all threads.
+template <int N>
+__device__ __forceinline__ void block_sum(u64 (&x)[N], Shared& s) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    u64 t = 0;
+    for (int i = 0; i < N; ++i)
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) t += s.red[i];
-    return t;
+        for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s.red[i][threadIdx.x >> 5] = x[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        u64 t = threadIdx.x % 32 < kWarps ? s.red[i][threadIdx.x % 32] : 0;
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        x[i] = __shfl_sync(0xffffffffu, t, 0);
+    }
 }
 
 // Inclusive running sum of one value per thread.
@@ -201,14 +219,14 @@ __device__ __forceinline__ u64 block_scan(u64 x, Shared& s) {
         if (lane >= o) x += t;
     }
     __syncthreads();
-    if (lane == 31) s.red[warp] = x;
+    if (lane == 31) s.red[0][warp] = x;
     __syncthreads();
-    for (int i = 0; i < warp; ++i) x += s.red[i];
+    for (int i = 0; i < warp; ++i) x += s.red[0][i];
     return x;
 }
 
-struct Pair {
-    u64 a, b;
+struct Four {
+    u64 v[4];
 };
 
 // What the cluster's CTAs share: `mine` (the same in all threads of a CTA)
@@ -218,70 +236,85 @@ struct Pair {
 struct Cluster {
     cg::cluster_group g;
     int rank, ranks, phase;
-    __device__ const u64 (*exchange(Shared& s, Pair mine))[2] {
-        if ((int)threadIdx.x < ranks) {
-            u64* dst = g.map_shared_rank(&s.xch[phase][rank][0], threadIdx.x);
-            dst[0] = mine.a;
-            dst[1] = mine.b;
+    __device__ const u64 (*exchange(Shared& s, Four mine))[4] {
+        if ((int)threadIdx.x < 4 * ranks) {
+            u64* dst = g.map_shared_rank(&s.xch[phase][rank][0], threadIdx.x / 4);
+            const int i = threadIdx.x % 4;
+            dst[i] = i == 0 ? mine.v[0] : i == 1 ? mine.v[1] : i == 2 ? mine.v[2] : mine.v[3];
         }
-        g.sync();
-        const u64(*r)[2] = s.xch[phase];
+        sync();
+        const u64(*r)[4] = s.xch[phase];
         phase ^= 1;
         return r;
     }
+    __device__ void sync() {
+        if (ranks > 1) g.sync();
+        else __syncthreads();
+    }
 };
 
-// Sorts all[0 .. n) descending (bitonic, padded with zeros to a power of two)
-// and leaves the running weights in pre[].
-__device__ void sort_and_scan(Shared& s, int n, const Scale& c) {
-    int m = 2;
-    while (m < n) m *= 2;
-    for (int i = n + threadIdx.x; i < m; i += kThreads) s.all[i] = 0;
-    __syncthreads();
-    for (int size = 2; size <= m; size *= 2)
-        for (int step = size / 2; step > 0; step /= 2) {
-            for (int i = threadIdx.x; i < m / 2; i += kThreads) {
-                const int a = 2 * i - (i & (step - 1)), b = a + step;
-                const u64 x = s.all[a], y = s.all[b];
-                if ((x < y) == ((a & size) == 0)) {
-                    s.all[a] = y;
-                    s.all[b] = x;
+// Sorts all[0 .. n) descending and leaves the running weights in pre[].
+__device__ void sort_and_scan(Shared& s, u64* all, u64* pre, int n, const Scale& c) {
+    if (n <= kCounting) {
+        // every token's place is the number of greater ones (no two are
+        // equal): two threads per token look at half of them each
+        const int i = threadIdx.x >> 1, part = threadIdx.x & 1;
+        const u64 x = i < n ? all[i] : 0;
+        int place = 0;
+        if (i < n)
+            for (int j = part; j < n; j += 2) place += all[j] > x;
+        place += __shfl_xor_sync(0xffffffffu, place, 1);
+        __syncthreads();
+        if (i < n && part == 0) all[place] = x;
+        __syncthreads();
+    } else {
+        // bitonic, padded with zeros to a power of two
+        int m = 2 * kCounting;
+        while (m < n) m *= 2;
+        for (int i = n + threadIdx.x; i < m; i += kThreads) all[i] = 0;
+        __syncthreads();
+        for (int size = 2; size <= m; size *= 2)
+            for (int step = size / 2; step > 0; step /= 2) {
+                for (int i = threadIdx.x; i < m / 2; i += kThreads) {
+                    const int a = 2 * i - (i & (step - 1)), b = a + step;
+                    const u64 x = all[a], y = all[b];
+                    if ((x < y) == ((a & size) == 0)) {
+                        all[a] = y;
+                        all[b] = x;
+                    }
                 }
+                __syncthreads();
             }
-            __syncthreads();
-        }
-    constexpr int P = kAll / kThreads;
-    u64 w[P], t = 0;
-#pragma unroll
-    for (int e = 0; e < P; ++e) {
-        const int i = P * threadIdx.x + e;
-        if (i < n) t += weight_of(key_value((uint32_t)(s.all[i] >> 32)), c, s.pow64);
-        w[e] = t;
     }
-    const u64 before = block_scan(t, s) - t;
-#pragma unroll
-    for (int e = 0; e < P; ++e)
-        if (P * (int)threadIdx.x + e < n) s.pre[P * threadIdx.x + e] = before + w[e];
+    u64 before = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const u64 w = i < n ? weight_of(key_value((uint32_t)(all[i] >> 32)), c, s.pow64) : 0;
+        const u64 run = before + block_scan(w, s);
+        if (i < n) pre[i] = run;
+        __syncthreads();
+        before = pre[min(n, i0 + kThreads) - 1];
+    }
     __syncthreads();
 }
 
 // First place of pre[0 .. n) that reaches target (there is one), to all threads.
-__device__ int reach(Shared& s, int n, u64 target) {
+__device__ int reach(Shared& s, const u64* pre, int n, u64 target) {
     for (int i = threadIdx.x; i < n; i += kThreads)
-        if (s.pre[i] >= target && (i == 0 || s.pre[i - 1] < target)) s.result[3] = i;
+        if (pre[i] >= target && (i == 0 || pre[i - 1] < target)) s.result[3] = i;
     __syncthreads();
     const int i = (int)s.result[3];
     __syncthreads();
     return i;
 }
 
-// The joined list into rank 0's all[], from every CTA's list.
-__device__ void gather(Shared& s, Cluster& cl, const u64 (*counts)[2]) {
+// The joined list into rank 0's `all`, from every CTA's list.
+__device__ void gather(Shared& s, Cluster& cl, const u64 (*counts)[4], u64* all) {
     int at = 0;
     for (int r = 0; r < cl.ranks; ++r) {
         const u64* src = cl.g.map_shared_rank(&s.list[0], r);
         const int n = (int)counts[r][0];
-        for (int i = threadIdx.x; i < n; i += kThreads) s.all[at + i] = src[i];
+        for (int i = threadIdx.x; i < n; i += kThreads) all[at + i] = src[i];
         at += n;
     }
     __syncthreads();
@@ -301,11 +334,11 @@ struct Tally {
     u64 w = 0;
     __device__ __forceinline__ void flush(Shared& s) {
         if (n == 0) return;
-        atomicAdd(&s.cnt[bin], n);
+        atomicAdd(&s.h0[bin], n);
         const uint32_t l = (uint32_t)w;
-        const uint32_t old = atomicAdd(&s.lo[bin], l);
+        const uint32_t old = atomicAdd(&s.h1[bin], l);
         const uint32_t h = (uint32_t)(w >> 32) + (old + l < old ? 1u : 0u);
-        if (h) atomicAdd(&s.hi[bin], h);
+        if (h) atomicAdd(&s.h2[bin], h);
         n = 0;
         w = 0;
     }
@@ -319,24 +352,34 @@ struct Tally {
     }
 };
 
+// A weight's 15-bit parts into the tail's histogram (no result is waited for).
+__device__ __forceinline__ void add_parts(Shared& s, int bin, u64 w) {
+    const uint32_t lo = (uint32_t)w & 0x7fffu, mid = (uint32_t)(w >> 15) & 0x7fffu, hi = (uint32_t)(w >> 30);
+    atomicAdd(&s.h0[bin], lo);
+    if (mid) atomicAdd(&s.h1[bin], mid);
+    if (hi) atomicAdd(&s.h2[bin], hi);
+}
+
 // Every CTA's histogram of `bins` bins (descending logits), joined and summed
-// up from the front, into every CTA's mc[], mw[] (at offset `at`).
-__device__ void join_histogram(Shared& s, Cluster& cl, int bins) {
-    cl.g.sync();  // all histograms done
+// up from the front, into every CTA's mc[] (with counts) and mw[].
+__device__ void join_histogram(Shared& s, Cluster& cl, int bins, bool counts) {
+    cl.sync();  // all histograms done
     const int b0 = bins * cl.rank / cl.ranks, b1 = bins * (cl.rank + 1) / cl.ranks;
     for (int b = b0 + threadIdx.x; b < b1; b += kThreads) {
         uint32_t n = 0;
         u64 w = 0;
         for (int r = 0; r < cl.ranks; ++r) {
-            n += *cl.g.map_shared_rank(&s.cnt[b], r);
-            w += (u64)*cl.g.map_shared_rank(&s.lo[b], r) + ((u64)*cl.g.map_shared_rank(&s.hi[b], r) << 32);
+            const u64 x = *cl.g.map_shared_rank(&s.h0[b], r), y = *cl.g.map_shared_rank(&s.h1[b], r),
+                      z = *cl.g.map_shared_rank(&s.h2[b], r);
+            n += (uint32_t)x;
+            w += counts ? y + (z << 32) : x + (y << 15) + (z << 30);
         }
         for (int r = 0; r < cl.ranks; ++r) {
             *cl.g.map_shared_rank(&s.mc[b], r) = n;
             *cl.g.map_shared_rank(&s.mw[b], r) = w;
         }
     }
-    cl.g.sync();
+    cl.sync();
     constexpr int P = kBins / kThreads;
     u64 n[P], w[P], tn = 0, tw = 0;
 #pragma unroll
@@ -349,7 +392,7 @@ __device__ void join_histogram(Shared& s, Cluster& cl, int bins) {
         n[e] = tn;
         w[e] = tw;
     }
-    const u64 bn = block_scan(tn, s) - tn, bw = block_scan(tw, s) - tw;
+    const u64 bn = counts ? block_scan(tn, s) - tn : 0, bw = block_scan(tw, s) - tw;
 #pragma unroll
     for (int e = 0; e < P; ++e) {
         const int b = P * threadIdx.x + e;
@@ -376,7 +419,7 @@ __device__ int reach_bin(Shared& s, int bins, bool by_count, u64 target) {
 
 __device__ __forceinline__ void clear_histogram(Shared& s, int bins) {
     __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += kThreads) s.cnt[b] = s.lo[b] = s.hi[b] = 0;
+    for (int b = threadIdx.x; b < bins; b += kThreads) s.h0[b] = s.h1[b] = s.h2[b] = 0;
     __syncthreads();
 }
 
@@ -388,6 +431,7 @@ struct Hit {
     u64 weight;  // of everything up to the place, and of the token there
     u64 own;
     int token;
+    bool by_digits;  // the search used the histogram's arrays
 };
 
 // The place where the count or weight of the tokens of `bin` reaches target
@@ -399,12 +443,11 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     __syncthreads();
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    row.each([&](float l, int i) {
-        const uint32_t k = key_of(l);
-        if (k != kLeast && bin_of(l, c) == bin) append(s, k, i);
+    row.template each<4>([&](float l, int i) {
+        if (l > -INFINITY && bin_of(l, c) == bin) append(s, key_of(l), i);
     });
     __syncthreads();
-    const u64(*n)[2] = cl.exchange(s, {s.count, 0});
+    const u64(*n)[4] = cl.exchange(s, {{s.count, 0, 0, 0}});
     u64 total = 0;
     bool fits = true;
     for (int r = 0; r < cl.ranks; ++r) {
@@ -412,21 +455,21 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
         fits = fits && n[r][0] <= kList;
     }
     Hit h;
-    if (fits && total <= kAll) {
+    h.by_digits = !(fits && total <= kBinList);
+    if (!h.by_digits) {
         u64 place = 0, pre = 0, own = 0;
         if (cl.rank == 0) {
-            gather(s, cl, n);
-            sort_and_scan(s, (int)total, c);
-            place = by_count ? target - 1 : reach(s, (int)total, target);
-            pre = s.pre[place];
-            own = pre - (place ? s.pre[place - 1] : 0);
-            place = (uint32_t)~(uint32_t)s.all[place];
+            gather(s, cl, n, s.bin_all);
+            sort_and_scan(s, s.bin_all, s.bin_pre, (int)total, c);
+            place = by_count ? target - 1 : reach(s, s.bin_pre, (int)total, target);
+            pre = s.bin_pre[place];
+            own = pre - (place ? s.bin_pre[place - 1] : 0);
+            place = (uint32_t)~(uint32_t)s.bin_all[place];
         }
-        const u64(*x)[2] = cl.exchange(s, {pre, place});
+        const u64(*x)[4] = cl.exchange(s, {{pre, place, own, 0}});
         h.weight = x[0][0];
         h.token = (int)x[0][1];
-        const u64(*y)[2] = cl.exchange(s, {own, 0});
-        h.own = y[0][0];
+        h.own = x[0][2];
         return h;
     }
     // eight bits of the key at a time, the greatest first
@@ -435,13 +478,13 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     for (int shift = 24; shift >= 0; shift -= 8) {
         clear_histogram(s, 256);
         Tally t;
-        row.each([&](float l, int i) {
+        row.template each<4>([&](float l, int) {
             const uint32_t k = key_of(l);
             if (k == kLeast || bin_of(l, c) != bin || (shift < 24 && k >> (shift + 8) != prefix >> (shift + 8))) return;
             t.add(s, 255 - (int)(k >> shift & 255u), weight_of(key_value(k), c, s.pow64));
         });
         t.flush(s);
-        join_histogram(s, cl, 256);
+        join_histogram(s, cl, 256, true);
         const int b = reach_bin(s, 256, by_count, target - (by_count ? nb : wb));
         const u64 n0 = b ? s.mc[b - 1] : 0, w0 = b ? s.mw[b - 1] : 0;
         equal = s.mc[b] - n0;
@@ -454,10 +497,11 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     if (place >= equal) place = equal - 1;
     h.weight = wb + (place + 1) * h.own;
     // its index: the parts are in index order, and a CTA walks its part so
-    u64 mine = 0;
-    row.each([&](float l, int) { mine += key_of(l) == prefix; });
-    mine = block_sum(mine, s);
-    const u64(*x)[2] = cl.exchange(s, {mine, 0});
+    u64 same[1] = {0};
+    row.template each<4>([&](float l, int) { same[0] += key_of(l) == prefix; });
+    block_sum(same, s);
+    const u64 mine = same[0];
+    const u64(*x)[4] = cl.exchange(s, {{mine, 0, 0, 0}});
     u64 before = 0;
     for (int r = 0; r < cl.rank; ++r) before += x[r][0];
     u64 found = 0;
@@ -476,7 +520,7 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
         }
         found = s.result[1];
     }
-    const u64(*y)[2] = cl.exchange(s, {found, 0});
+    const u64(*y)[4] = cl.exchange(s, {{found, 0, 0, 0}});
     h.token = -1;
     for (int r = 0; r < cl.ranks; ++r)
         if (y[r][0]) h.token = (int)y[r][0] - 1;
@@ -489,16 +533,13 @@ __device__ __forceinline__ u64 share_target(double share, u64 W) {  // least int
 }
 
 template <bool HALF>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared& s = *reinterpret_cast<Shared*>(smem);
     Cluster cl{cg::this_cluster(), 0, a.cluster, 0};
     cl.rank = (int)cl.g.block_rank();
     const int r = blockIdx.x / a.cluster, tid = threadIdx.x;
     const Part<HALF> row(a, r, cl.rank);
-    if (tid < 64) s.pow64[tid] = (uint32_t)fmin(4294967295.0, rint(exp2(-tid / 64.0) * 4294967296.0));
-    for (int b = tid; b < kCut; b += kThreads) s.cnt[b] = 0;
-    if (tid == 0) s.count = 0;
     const auto finish = [&](int token, double prob) {
         if (cl.rank == 0 && tid == 0) {
             a.tokens[r] = token;
@@ -509,13 +550,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     // 1. the greatest logit, at its lowest index
     float best = -INFINITY;
     int best_at = 0;
-    row.each([&](float l, int i) {
+    row.template each<8>([&](float l, int i) {
         if (l > best) {
             best = l;
             best_at = i;
         }
     });
     const bool any = best > -INFINITY;
+    // (while the loads are on their way: the tables)
+    if (tid < 64) {
+        const double p = rint(exp2(-tid / 64.0) * 536870912.0);
+        s.pow64[tid] = make_float2(__int_as_float((int)p), (float)p);
+    }
+    for (int b = tid; b < kCut; b += kThreads) s.cut_count[b] = 0;
+    for (int b = tid; b < kBins; b += kThreads) s.h0[b] = s.h1[b] = s.h2[b] = 0;
+    if (tid == 0) {
+        s.count = 0;
+        s.cut = kCut - 1;
+    }
     {
         u64 m = any ? (u64)key_of(best) << 32 | (uint32_t)~best_at : 0;
 #pragma unroll
@@ -523,14 +575,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
             const u64 t = __shfl_xor_sync(0xffffffffu, m, o);
             m = t > m ? t : m;
         }
-        if ((tid & 31) == 0) s.red[tid >> 5] = m;
-        __syncthreads();
+        if ((tid & 31) == 0) s.red[0][tid >> 5] = m;
     }
+    cl.sync();  // every CTA of the cluster runs: its shared memory can be written
     u64 top = 0;
-    for (int i = 0; i < kWarps; ++i) top = s.red[i] > top ? s.red[i] : top;
-    cl.g.sync();  // every CTA of the cluster runs: its shared memory can be written
-    {
-        const u64(*x)[2] = cl.exchange(s, {top, 0});
+    for (int i = 0; i < kWarps; ++i) top = s.red[0][i] > top ? s.red[0][i] : top;
+    if (cl.ranks > 1) {
+        const u64(*x)[4] = cl.exchange(s, {{top, 0, 0, 0}});
         for (int i = 0; i < cl.ranks; ++i) top = x[i][0] > top ? x[i][0] : top;
     }
     const float T = a.temperature ? a.temperature[r] : 1.f;
@@ -538,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     if (top == 0 || !a.u || !(T > 0.f) || k == 1) {
         if (top == 0) finish(-1, 0.0);
         else finish((int)(uint32_t)~(uint32_t)top, 1.0);
-        cl.g.sync();  // no CTA leaves while another may still write to it
+        cl.sync();  // no CTA leaves while another may still write to it
         return;
     }
     Scale c;
@@ -552,158 +603,204 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const Args a) {
     const float p = a.top_p ? a.top_p[r] : 1.f;
     const float mp = a.min_p ? a.min_p[r] : 0.f;
     const double least = mp > 0.f ? (double)fminf(mp, 1.f) * (double)kOne : 0.0;
+    const u64 least_w = (u64)ceil(least);
     const double u = fmin(fmax((double)a.u[r], 0.0), 1.0);
 
     // 2. the threshold
-    if (any) atomicAdd(&s.cnt[(int)fminf(coarse_t(best, c) * 16.f, (float)(kCut - 1))], 1u);
-    cl.g.sync();
+    if (any) atomicAdd(&s.cut_count[(int)fminf(coarse_t(best, c) * 16.f, (float)(kCut - 1))], 1u);
+    cl.sync();
     {
+        static_assert(kCut == kThreads, "a bin per thread");
         uint32_t n = 0;
-        for (int i = 0; i < cl.ranks; ++i) n += *cl.g.map_shared_rank(&s.cnt[tid], i);
+        if (cl.ranks > 1) {
+            for (int i = 0; i < cl.ranks; ++i) n += *cl.g.map_shared_rank(&s.cut_count[tid], i);
+        } else {
+            n = s.cut_count[tid];
+        }
         const u64 wanted = with_k && k <= kMostK ? k : kWanted;
         const u64 run = block_scan(n, s);
-        if (tid == 0) s.cut = kCut - 1;
-        __syncthreads();
         if (run >= wanted && run - n < wanted) s.cut = tid;
         __syncthreads();
     }
-    static_assert(kCut == kThreads, "a bin per thread");
     const float cut = (float)(s.cut + 1);
 
-    // 3. the list, and the weight of all
-    u64 all = 0, rest = 0;
-    row.each([&](float l, int i) {
-        const float t = coarse_t(l, c) * 16.f;
-        if (t < cut) {
-            append(s, key_of(l), i);
-        } else if (l > -INFINITY) {
-            ++rest;
-        }
-        if (!with_k && l > -INFINITY) all += weight_of(l, c, s.pow64);
-    });
-    all = block_sum(all, s);
-    rest = block_sum(rest, s);
-    u64 n_list = 0, W = 0;
-    bool fits = true, done = false;
-    const u64(*n)[2] = cl.exchange(s, {s.count, rest});
-    rest = 0;
+    // 3. the list; without top_k the weight of all, of those that min_p keeps,
+    // and the histogram of what is not in the list
+    u64 sums[3] = {0, 0, 0};  // rest, all, some
+    if (with_k) {
+        row.template each<4>([&](float l, int i) {
+            if (coarse_t(l, c) * 16.f < cut) append(s, key_of(l), i);
+            else sums[0] += l > -INFINITY;
+        });
+    } else {
+        row.template each<2>([&](float l, int i) {
+            if (!(l > -INFINITY)) return;
+            const u64 w = weight_of(l, c, s.pow64);
+            sums[1] += w;
+            if (w >= least_w) sums[2] += w;
+            const float t = coarse_t(l, c);
+            if (t * 16.f < cut) {
+                append(s, key_of(l), i);
+            } else {
+                ++sums[0];
+                if (w) add_parts(s, (int)(t * 32.f), w);
+            }
+        });
+    }
+    block_sum(sums, s);
+    u64 n_list = 0, rest = 0, W = 0, some = 0;
+    bool fits = true;
+    const u64(*n)[4] = cl.exchange(s, {{s.count, sums[0], sums[1], sums[2]}});
     for (int i = 0; i < cl.ranks; ++i) {
         n_list += n[i][0];
         rest += n[i][1];
+        W += n[i][2];
+        some += n[i][3];
         fits = fits && n[i][0] <= kList;
     }
     fits = fits && n_list <= kAll;
-    if (fits && cl.rank == 0) gather(s, cl, n);
-    {
-        const u64(*x)[2] = cl.exchange(s, {all, 0});
-        for (int i = 0; i < cl.ranks; ++i) W += x[i][0];
-    }
+
+    // What rank 0 finds in the list: 0 everything; 1 the nucleus ends below
+    // it; 2 the token stands below it; 3 the list does not do
+    enum : u64 { kDone, kNucleus, kToken, kNoList };
+    u64 state = kNoList, target = 0, W_list = 0;
+    const auto in_list = [&](u64 t) {
+        const int i = reach(s, s.pre, (int)n_list, t);
+        finish((int)(uint32_t)~(uint32_t)s.all[i], (double)(s.pre[i] - (i ? s.pre[i - 1] : 0)) / (double)W);
+    };
     if (fits && cl.rank == 0) {
         const int N = (int)n_list;
-        sort_and_scan(s, N, c);
-        const u64 W_list = s.pre[N - 1];
-        bool ok = true;
-        if (with_k) {
-            ok = k <= N || rest == 0;
-            W = s.pre[min(k, N) - 1];
-        }
-        if (ok && p < 1.f) {
-            const u64 target = share_target((double)p, W);
-            ok = target <= W_list;
-            if (ok) W = s.pre[reach(s, N, target)];
-        }
-        if (ok && least > 0.0) {
-            int m = 0;  // the ones that min_p keeps
-            for (int i0 = 0; i0 < N; i0 += kThreads) {
-                const int i = i0 + tid;
-                m += __syncthreads_count(i < N && (double)(s.pre[i] - (i ? s.pre[i - 1] : 0)) >= least);
+        gather(s, cl, n, s.all);
+        sort_and_scan(s, s.all, s.pre, N, c);
+        W_list = s.pre[N - 1];
+        if (!with_k || k <= N || rest == 0) {
+            state = kDone;
+            if (with_k) W = s.pre[min(k, N) - 1];
+            if (p < 1.f) {
+                target = share_target((double)p, W);
+                if (target <= W_list) W = s.pre[reach(s, s.pre, N, target)];
+                else state = kNucleus;
             }
-            if (m < N || rest == 0) W = min(W, s.pre[m - 1]);
-            else ok = W <= W_list;
-        }
-        if (ok) {
-            const u64 target = min(W, (u64)(u * (double)W) + 1);
-            ok = target <= W_list;
-            if (ok) {
-                const int i = reach(s, N, target);
-                finish((int)(uint32_t)~(uint32_t)s.all[i], (double)(s.pre[i] - (i ? s.pre[i - 1] : 0)) / (double)W);
+            if (state == kDone) {
+                if (least_w && with_k) {
+                    some = 0;  // of the list: top_k ends in it
+                    for (int i0 = 0; i0 < N; i0 += kThreads) {
+                        const int i = i0 + tid;
+                        some += __syncthreads_count(i < N && s.pre[i] - (i ? s.pre[i - 1] : 0) >= least_w);
+                    }
+                    some = s.pre[some - 1];
+                }
+                if (least_w) W = min(W, some);
+                target = min(W, (u64)(u * (double)W) + 1);
+                if (target <= W_list) in_list(target);
+                else state = kToken;
             }
         }
-        done = ok;
     }
     {
-        const u64(*x)[2] = cl.exchange(s, {done, 0});
-        done = x[0][0] != 0;
+        const u64(*x)[4] = cl.exchange(s, {{state, target, W_list, W}});
+        state = x[0][0];
+        target = x[0][1];
+        W_list = x[0][2];
+        W = state == kNoList ? W : x[0][3];
     }
-    if (!done) {
-        // what the list does not decide: the histogram over all
-        clear_histogram(s, kBins);
-        u64 some = 0;
-        Tally t;
-        row.each([&](float l, int) {
-            if (!(l > -INFINITY)) return;
-            const u64 w = weight_of(l, c, s.pow64);
-            if (w == 0) return;
-            if ((double)w >= least) some += w;
-            t.add(s, bin_of(l, c), w);
-        });
-        t.flush(s);
-        some = block_sum(some, s);
-        {
-            const u64(*x)[2] = cl.exchange(s, {some, 0});
+    if (state == kNucleus || state == kToken) {
+        // below the list, without top_k: by the histogram
+        const auto below = [&]() {
+            const int b = reach_bin(s, kBins, false, target - W_list);
+            const u64 before = W_list + (b ? s.mw[b - 1] : 0);
+            Hit h = search_bin<HALF>(row, s, cl, c, b, false, target - before);
+            h.weight += before;
+            return h;
+        };
+        join_histogram(s, cl, kBins, false);
+        bool found = false;
+        if (state == kNucleus) {
+            Hit h = below();
+            W = h.weight;
+            if (least_w) W = min(W, some);
+            target = min(W, (u64)(u * (double)W) + 1);
+            if (target <= W_list) {
+                if (cl.rank == 0) in_list(target);
+                found = true;
+            } else if (h.by_digits) {  // the histogram once more
+                clear_histogram(s, kBins);
+                row.template each<2>([&](float l, int) {
+                    if (!(l > -INFINITY)) return;
+                    const float t = coarse_t(l, c);
+                    const u64 w = t * 16.f < cut ? 0 : weight_of(l, c, s.pow64);
+                    if (w) add_parts(s, (int)(t * 32.f), w);
+                });
+                join_histogram(s, cl, kBins, false);
+            }
+        }
+        if (!found) {
+            const Hit h = below();
+            finish(h.token, (double)h.own / (double)W);
+        }
+    } else if (state == kNoList) {
+        // the list has overflowed (a flat top), or top_k is larger than one:
+        // counts and weights of all, by bins
+        const auto histogram = [&]() {
+            clear_histogram(s, kBins);
+            Tally t;
+            row.template each<2>([&](float l, int) {
+                if (!(l > -INFINITY)) return;
+                const u64 w = weight_of(l, c, s.pow64);
+                if (w == 0) return;
+                t.add(s, bin_of(l, c), w);
+            });
+            t.flush(s);
+            join_histogram(s, cl, kBins, true);
+        };
+        histogram();
+        if (with_k && least_w) {
+            sums[0] = 0;
+            row.template each<2>([&](float l, int) {
+                if (!(l > -INFINITY)) return;
+                const u64 w = weight_of(l, c, s.pow64);
+                if (w >= least_w) sums[0] += w;
+            });
+            u64 one[1] = {sums[0]};
+            block_sum(one, s);
+            const u64(*x)[4] = cl.exchange(s, {{one[0], 0, 0, 0}});
             some = 0;
             for (int i = 0; i < cl.ranks; ++i) some += x[i][0];
         }
-        join_histogram(s, cl, kBins);
-        // the running sums are needed for up to three searches, which use the
-        // same arrays where a bin overflows the list: the last one's bin and
-        // target are found before that, the others' leave a sum only
         W = s.mw[kBins - 1];
-        const auto before = [&](int b, bool by_count) -> u64 {
-            return b == 0 ? 0 : by_count ? (u64)s.mc[b - 1] : s.mw[b - 1];
+        const auto at = [&](bool by_count, u64 t) {
+            const int b = reach_bin(s, kBins, by_count, t);
+            const u64 nb = b ? s.mc[b - 1] : 0, wb = b ? s.mw[b - 1] : 0;
+            Hit h = search_bin<HALF>(row, s, cl, c, b, by_count, t - (by_count ? nb : wb));
+            h.weight += wb;
+            return h;
         };
-        const auto again = [&]() {  // the histogram, where a search has used its arrays
-            clear_histogram(s, kBins);
-            Tally t2;
-            row.each([&](float l, int) {
-                if (!(l > -INFINITY)) return;
-                const u64 w = weight_of(l, c, s.pow64);
-                if (w) t2.add(s, bin_of(l, c), w);
-            });
-            t2.flush(s);
-            join_histogram(s, cl, kBins);
-        };
+        bool stale = false;
         if (with_k && (u64)k < s.mc[kBins - 1]) {
-            const int b = reach_bin(s, kBins, true, k);
-            const u64 wb = before(b, false);
-            const u64 nb = before(b, true);
-            const bool big = s.mc[b] - nb > kList;  // may not fit the list
-            W = wb + search_bin<HALF>(row, s, cl, c, b, true, k - nb).weight;
-            if (big) again();
+            const Hit h = at(true, (u64)k);
+            W = h.weight;
+            stale = h.by_digits;
         }
         if (p < 1.f) {
-            const u64 target = share_target((double)p, W);
-            const int b = reach_bin(s, kBins, false, target);
-            const u64 wb = before(b, false);
-            const bool big = s.mc[b] - before(b, true) > kList;
-            W = wb + search_bin<HALF>(row, s, cl, c, b, false, target - wb).weight;
-            if (big) again();
+            if (stale) histogram();
+            const Hit h = at(false, share_target((double)p, W));
+            W = h.weight;
+            stale = h.by_digits;
         }
-        if (least > 0.0) W = min(W, some);
-        const u64 target = min(W, (u64)(u * (double)W) + 1);
-        const int b = reach_bin(s, kBins, false, target);
-        const Hit h = search_bin<HALF>(row, s, cl, c, b, false, target - before(b, false));
+        if (least_w) W = min(W, some);
+        if (stale) histogram();
+        const Hit h = at(false, min(W, (u64)(u * (double)W) + 1));
         finish(h.token, (double)h.own / (double)W);
     }
-    cl.g.sync();  // no CTA leaves while another may still use its shared memory
+    cl.sync();  // no CTA leaves while another may still use its shared memory
 }
 
 template <bool HALF>
 cudaError_t launch(Args& a, int rows, int sms, cudaStream_t stream) {
-    // As many CTAs per row as two per SM allow, each with at least 2048
-    // tokens.  16 CTAs need the non-portable cluster size.
+    // As many CTAs per row as two per SM allow, each with at least 1024 tokens
+    // and at most kMostPart.  16 CTAs need the non-portable cluster size.
     int c = kMaxCluster;
-    while (c > 1 && ((long long)rows * c > 2 * sms || a.vocab < 2048 * c / 2 + 1)) c /= 2;
+    while (c > 1 && ((long long)rows * c > 2 * sms || a.vocab <= 1024 * c) && a.vocab <= kMostPart * (c / 2)) c /= 2;
     a.cluster = c;
     static std::atomic<int> marks[64], wide[64];
     const void* kern = reinterpret_cast<const void*>(sample_kernel<HALF>);
