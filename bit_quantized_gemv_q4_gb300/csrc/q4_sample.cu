@@ -49,7 +49,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 16;
-constexpr int kWanted = 256;         // tokens the list aims at without top_k
+constexpr int kWanted = 160;         // tokens the list aims at without top_k
 constexpr int kMostK = 1024;         // top_k up to which the list is tried
 constexpr int kList = 1024;          // tokens of a CTA's list
 constexpr int kAll = 2048;           // tokens of the joined list
@@ -105,35 +105,86 @@ struct Scale {
     float max, hi, lo;  // log2(e) / T = hi + lo
 };
 
-// t in fp32, as the bins see it: monotone in the logit.
-__device__ __forceinline__ float coarse_t(float l, const Scale& c) { return l == c.max ? 0.f : (c.max - l) * c.hi; }
+// Adding 1.5 2^23 rounds a float below 2^22 to an integer in its low mantissa
+// bits, which keeps conversions off the slow pipe.
+constexpr float kMagic = 12582912.f;
+__device__ __forceinline__ int magic_int(float x) { return __float_as_int(x) - __float_as_int(kMagic); }
 
-// round(2^44 2^-t).  Adding 1.5 2^23 rounds a float to an integer in its low
-// mantissa bits, which keeps conversions off the slow pipe.
+// Bin of a logit: 32 t to the nearest integer, kBins - 1 from t = 46 on (no
+// weight there).  Monotone in the logit.
+constexpr float kEnd = 46.f;
+__device__ __forceinline__ int bin_of(float l, const Scale& c) {
+    const float d = l == c.max ? 0.f : c.max - l;
+    return d * c.hi < kEnd ? magic_int(fmaf(d, c.hi * 32.f, kMagic)) : kBins - 1;
+}
+
+// 2^44 2^(-k/64) (1 - y), rounded; k >= 0, |y| < 0.0056.
+__device__ __forceinline__ u64 weight_from(int k, float y, const float2* pow64) {
+    const float2 p = pow64[k & 63];
+    const int q = magic_int(fmaf(p.y, y, kMagic));       // |p y| < 2^22
+    const uint32_t m = (uint32_t)(__float_as_int(p.x) - q);  // units of 2^-29: 2^28 .. 2^29
+    const int sh = 15 - (k >> 6);
+    return sh >= 0 ? (u64)m << sh : (u64)((m + (1u << (-sh - 1))) >> -sh);
+}
+
+// round(2^44 2^-t).  The passes over a row (two_of below) do the same
+// operations on two logits at a time, so a token has one weight.
+template <bool kExact>
 __device__ __forceinline__ u64 weight_of(float l, const Scale& c, const float2* pow64) {
-    constexpr float kMagic = 12582912.f;
     if (l == c.max) return kOne;
     // d + de = max - l exactly (the error of a difference is a float)
     const float d = c.max - l;
-    if (!(d * c.hi < 46.f)) return 0;
+    if (!(d * c.hi < kEnd)) return 0;
     const float b = d - c.max;
-    const float de = (c.max - (d - b)) + (-l - b);
+    const float de = kExact ? (c.max - (d - b)) + (-l - b) : 0.f;
     // 64 t = k + r, |r| <= 1/2 and a little: the product less k is one fused
     // operation, so nothing of it is lost; then its smaller parts
     const float hi = c.hi * 64.f, lo = c.lo * 64.f;  // exact
     const float kf = fmaf(d, hi, kMagic);
-    const int k = __float_as_int(kf) - __float_as_int(kMagic);
-    const float r = fmaf(d, hi, -(kf - kMagic)) + fmaf(d, lo, de * hi);
+    float r = fmaf(d, hi, -(kf - kMagic));
+    if (kExact) r = fmaf(de, hi, r);
+    r = fmaf(d, lo, r);
     // 2^(-r/64) = 1 - y, y = z - z^2 / 2 + z^3 / 6, z = r ln2 / 64 < 0.0055;
     // the next term is below 2^-34
     const float z = r * 0.010830425f;
-    const float y = z * (1.f - z * (0.5f - z * 0.16666667f));
-    const float2 p = pow64[k & 63];
-    const int q = __float_as_int(fmaf(p.y, y, kMagic)) - __float_as_int(kMagic);  // |p y| < 2^22
-    const u64 m = (u64)(uint32_t)(__float_as_int(p.x) - q);  // 2^28 .. 2^29
-    // 2^44 2^-(k / 64) m 2^-29, rounded
-    const int sh = 15 - (k >> 6);
-    return sh >= 0 ? m << sh : (m + (1ull << (-sh - 1))) >> -sh;
+    const float y = z * fmaf(z, fmaf(z, 0.16666667f, -0.5f), 1.f);
+    return weight_from(magic_int(kf), y, pow64);
+}
+
+// d = max - l, t and y of two logits (max finite).  `exact`: the difference's
+// rounding error counts too; of half-precision logits it does not (it is zero
+// but for logits 2^13 times smaller than the greatest, where it is below 2^-28
+// of a weight).
+struct Two {
+    float2 t, y;
+    int k[2];
+};
+template <bool kExact>
+__device__ __forceinline__ Two two_of(float2 l, const Scale& c) {
+    const float2 mx = make_float2(c.max, c.max), neg = make_float2(-1.f, -1.f);
+    const float2 hi = make_float2(c.hi * 64.f, c.hi * 64.f), lo = make_float2(c.lo * 64.f, c.lo * 64.f);
+    const float2 mg = make_float2(kMagic, kMagic);
+    const float2 d = __ffma2_rn(l, neg, mx);
+    const float2 kf = __ffma2_rn(d, hi, mg);
+    const float2 kr = __fadd2_rn(kf, make_float2(-kMagic, -kMagic));
+    float2 r = __ffma2_rn(d, hi, __ffma2_rn(kr, neg, make_float2(0.f, 0.f)));
+    if (kExact) {
+        const float2 b = __fadd2_rn(d, make_float2(-c.max, -c.max));
+        const float2 db = __ffma2_rn(b, neg, d);                      // d - b
+        const float2 e0 = __ffma2_rn(db, neg, mx);                    // max - (d - b)
+        const float2 e1 = __ffma2_rn(__fadd2_rn(l, b), neg, e0);      // ... + (-l - b)
+        r = __ffma2_rn(e1, hi, r);
+    }
+    r = __ffma2_rn(d, lo, r);
+    const float2 z = __fmul2_rn(r, make_float2(0.010830425f, 0.010830425f));
+    const float2 q = __ffma2_rn(z, __ffma2_rn(z, make_float2(0.16666667f, 0.16666667f), make_float2(-0.5f, -0.5f)),
+                                make_float2(1.f, 1.f));
+    Two o;
+    o.t = __fmul2_rn(d, make_float2(c.hi, c.hi));
+    o.y = __fmul2_rn(z, q);
+    o.k[0] = magic_int(kf.x);
+    o.k[1] = magic_int(kf.y);
+    return o;
 }
 
 // This CTA's part of a row: 16-byte vectors v0 .. v1 - 1 behind `head` single
@@ -159,12 +210,14 @@ struct Part {
         if constexpr (HALF) return __half2float(__ushort_as_half(row[i]));
         else return row[i];
     }
-    // f(value, index) for every element of the part, N vectors in flight per
-    // thread; a thread's indices ascend.
+    // f(two values, index of the first) for the part's elements, N vectors in
+    // flight per thread; a thread's indices ascend.  Single elements come with
+    // a -inf, which takes no part.
     template <int N, typename F>
-    __device__ __forceinline__ void each(F f) const {
-        if (rank == 0 && (int)threadIdx.x < head) f(at(threadIdx.x), (int)threadIdx.x);
+    __device__ __forceinline__ void pairs(F f) const {
+        if (rank == 0 && (int)threadIdx.x < head) f(make_float2(at(threadIdx.x), -INFINITY), (int)threadIdx.x);
         const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+#pragma unroll 1
         for (int v = v0 + threadIdx.x; v < v1; v += N * kThreads) {
             uint4 w[N];
 #pragma unroll
@@ -174,18 +227,27 @@ struct Part {
             for (int i = 0; i < N; ++i) {
                 if (v + i * kThreads >= v1) break;
                 const int at0 = head + (v + i * kThreads) * VE;
-                const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
                 if constexpr (HALF) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f(__half2float(__ushort_as_half((uint16_t)(x[e >> 1] >> (16 * (e & 1))))), at0 + e);
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].x)), at0);
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].y)), at0 + 2);
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].z)), at0 + 4);
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].w)), at0 + 6);
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) f(__uint_as_float(x[e]), at0 + e);
+                    f(make_float2(__uint_as_float(w[i].x), __uint_as_float(w[i].y)), at0);
+                    f(make_float2(__uint_as_float(w[i].z), __uint_as_float(w[i].w)), at0 + 2);
                 }
             }
         }
-        if (rank == ranks - 1 && tail + (int)threadIdx.x < vocab) f(at(tail + threadIdx.x), tail + (int)threadIdx.x);
+        if (rank == ranks - 1 && tail + (int)threadIdx.x < vocab)
+            f(make_float2(at(tail + threadIdx.x), -INFINITY), tail + (int)threadIdx.x);
+    }
+    // f(value, index), one at a time (the added -inf among them).
+    template <int N, typename F>
+    __device__ __forceinline__ void each(F f) const {
+        pairs<N>([&](float2 l, int i) {
+            f(l.x, i);
+            f(l.y, i + 1);
+        });
     }
 };
 
@@ -254,6 +316,7 @@ struct Cluster {
 };
 
 // Sorts all[0 .. n) descending and leaves the running weights in pre[].
+template <bool HALF>
 __device__ void sort_and_scan(Shared& s, u64* all, u64* pre, int n, const Scale& c) {
     if (n <= kCounting) {
         // every token's place is the number of greater ones (no two are
@@ -289,7 +352,7 @@ __device__ void sort_and_scan(Shared& s, u64* all, u64* pre, int n, const Scale&
     u64 before = 0;
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + threadIdx.x;
-        const u64 w = i < n ? weight_of(key_value((uint32_t)(all[i] >> 32)), c, s.pow64) : 0;
+        const u64 w = i < n ? weight_of<!HALF>(key_value((uint32_t)(all[i] >> 32)), c, s.pow64) : 0;
         const u64 run = before + block_scan(w, s);
         if (i < n) pre[i] = run;
         __syncthreads();
@@ -298,8 +361,10 @@ __device__ void sort_and_scan(Shared& s, u64* all, u64* pre, int n, const Scale&
     __syncthreads();
 }
 
-// First place of pre[0 .. n) that reaches target (there is one), to all threads.
+// First place of pre[0 .. n) that reaches target (there is one; else the last), to all threads.
 __device__ int reach(Shared& s, const u64* pre, int n, u64 target) {
+    if (threadIdx.x == 0) s.result[3] = n - 1;
+    __syncthreads();
     for (int i = threadIdx.x; i < n; i += kThreads)
         if (pre[i] >= target && (i == 0 || pre[i - 1] < target)) s.result[3] = i;
     __syncthreads();
@@ -310,12 +375,12 @@ __device__ int reach(Shared& s, const u64* pre, int n, u64 target) {
 
 // The joined list into rank 0's `all`, from every CTA's list.
 __device__ void gather(Shared& s, Cluster& cl, const u64 (*counts)[4], u64* all) {
-    int at = 0;
-    for (int r = 0; r < cl.ranks; ++r) {
-        const u64* src = cl.g.map_shared_rank(&s.list[0], r);
-        const int n = (int)counts[r][0];
-        for (int i = threadIdx.x; i < n; i += kThreads) all[at + i] = src[i];
-        at += n;
+    int total = 0;
+    for (int r = 0; r < cl.ranks; ++r) total += (int)counts[r][0];
+    for (int i = threadIdx.x; i < total; i += kThreads) {  // (a thread per token: the remote loads overlap)
+        int r = 0, j = i;
+        while (j >= (int)counts[r][0]) j -= (int)counts[r++][0];
+        all[i] = *cl.g.map_shared_rank(&s.list[j], r);
     }
     __syncthreads();
 }
@@ -356,7 +421,7 @@ struct Tally {
 __device__ __forceinline__ void add_parts(Shared& s, int bin, u64 w) {
     const uint32_t lo = (uint32_t)w & 0x7fffu, mid = (uint32_t)(w >> 15) & 0x7fffu, hi = (uint32_t)(w >> 30);
     atomicAdd(&s.h0[bin], lo);
-    if (mid) atomicAdd(&s.h1[bin], mid);
+    atomicAdd(&s.h1[bin], mid);
     if (hi) atomicAdd(&s.h2[bin], hi);
 }
 
@@ -404,8 +469,10 @@ __device__ void join_histogram(Shared& s, Cluster& cl, int bins, bool counts) {
     __syncthreads();
 }
 
-// First bin whose running count or weight reaches target (there is one).
+// First bin whose running count or weight reaches target (there is one; else the last).
 __device__ int reach_bin(Shared& s, int bins, bool by_count, u64 target) {
+    if (threadIdx.x == 0) s.result[2] = bins - 1;
+    __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kThreads) {
         const u64 x = by_count ? s.mc[b] : s.mw[b];
         const u64 y = b == 0 ? 0 : by_count ? s.mc[b - 1] : s.mw[b - 1];
@@ -421,10 +488,6 @@ __device__ __forceinline__ void clear_histogram(Shared& s, int bins) {
     __syncthreads();
     for (int b = threadIdx.x; b < bins; b += kThreads) s.h0[b] = s.h1[b] = s.h2[b] = 0;
     __syncthreads();
-}
-
-__device__ __forceinline__ int bin_of(float l, const Scale& c) {
-    return (int)fminf(coarse_t(l, c) * 32.f, (float)(kBins - 1));
 }
 
 struct Hit {
@@ -443,8 +506,14 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     __syncthreads();
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    row.template each<4>([&](float l, int i) {
-        if (l > -INFINITY && bin_of(l, c) == bin) append(s, key_of(l), i);
+    const float b32 = c.hi * 32.f;
+    row.template pairs<2>([&](float2 l, int i) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = e ? l.y : l.x, d = c.max - x;
+            // (a NaN or -inf fails the first test; max itself, even +inf, is bin 0)
+            if (x == c.max ? bin == 0 : d * c.hi < kEnd && magic_int(fmaf(d, b32, kMagic)) == bin) append(s, key_of(x), i + e);
+        }
     });
     __syncthreads();
     const u64(*n)[4] = cl.exchange(s, {{s.count, 0, 0, 0}});
@@ -456,12 +525,17 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     }
     Hit h;
     h.by_digits = !(fits && total <= kBinList);
+    if (total == 0) {  // (no target lies in an empty bin)
+        h.weight = h.own = 0;
+        h.token = -1;
+        return h;
+    }
     if (!h.by_digits) {
         u64 place = 0, pre = 0, own = 0;
         if (cl.rank == 0) {
             gather(s, cl, n, s.bin_all);
-            sort_and_scan(s, s.bin_all, s.bin_pre, (int)total, c);
-            place = by_count ? target - 1 : reach(s, s.bin_pre, (int)total, target);
+            sort_and_scan<HALF>(s, s.bin_all, s.bin_pre, (int)total, c);
+            place = by_count ? min(target - 1, total - 1) : reach(s, s.bin_pre, (int)total, target);
             pre = s.bin_pre[place];
             own = pre - (place ? s.bin_pre[place - 1] : 0);
             place = (uint32_t)~(uint32_t)s.bin_all[place];
@@ -478,10 +552,10 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     for (int shift = 24; shift >= 0; shift -= 8) {
         clear_histogram(s, 256);
         Tally t;
-        row.template each<4>([&](float l, int) {
+        row.template each<1>([&](float l, int) {
             const uint32_t k = key_of(l);
             if (k == kLeast || bin_of(l, c) != bin || (shift < 24 && k >> (shift + 8) != prefix >> (shift + 8))) return;
-            t.add(s, 255 - (int)(k >> shift & 255u), weight_of(key_value(k), c, s.pow64));
+            t.add(s, 255 - (int)(k >> shift & 255u), weight_of<!HALF>(key_value(k), c, s.pow64));
         });
         t.flush(s);
         join_histogram(s, cl, 256, true);
@@ -492,13 +566,13 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
         wb += w0;
         prefix |= (uint32_t)(255 - b) << shift;
     }
-    h.own = weight_of(key_value(prefix), c, s.pow64);
+    h.own = weight_of<!HALF>(key_value(prefix), c, s.pow64);
     u64 place = by_count ? target - nb - 1 : h.own ? (target - wb - 1) / h.own : 0;  // among the equal keys
     if (place >= equal) place = equal - 1;
     h.weight = wb + (place + 1) * h.own;
     // its index: the parts are in index order, and a CTA walks its part so
     u64 same[1] = {0};
-    row.template each<4>([&](float l, int) { same[0] += key_of(l) == prefix; });
+    row.template each<1>([&](float l, int) { same[0] += key_of(l) == prefix; });
     block_sum(same, s);
     const u64 mine = same[0];
     const u64(*x)[4] = cl.exchange(s, {{mine, 0, 0, 0}});
@@ -547,15 +621,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
     };
 
-    // 1. the greatest logit, at its lowest index
+    // 1. the greatest logit
     float best = -INFINITY;
-    int best_at = 0;
-    row.template each<8>([&](float l, int i) {
-        if (l > best) {
-            best = l;
-            best_at = i;
-        }
-    });
+    row.template pairs<HALF ? 4 : 8>([&](float2 l, int) { best = fmaxf(best, fmaxf(l.x, l.y)); });
     const bool any = best > -INFINITY;
     // (while the loads are on their way: the tables)
     if (tid < 64) {
@@ -569,32 +637,41 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         s.cut = kCut - 1;
     }
     {
-        u64 m = any ? (u64)key_of(best) << 32 | (uint32_t)~best_at : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const u64 t = __shfl_xor_sync(0xffffffffu, m, o);
-            m = t > m ? t : m;
-        }
+        const uint32_t m = __reduce_max_sync(0xffffffffu, any ? key_of(best) : 0u);
         if ((tid & 31) == 0) s.red[0][tid >> 5] = m;
     }
     cl.sync();  // every CTA of the cluster runs: its shared memory can be written
-    u64 top = 0;
-    for (int i = 0; i < kWarps; ++i) top = s.red[0][i] > top ? s.red[0][i] : top;
+    uint32_t top = __reduce_max_sync(0xffffffffu, (tid & 31) < kWarps ? (uint32_t)s.red[0][tid & 31] : 0u);
     if (cl.ranks > 1) {
         const u64(*x)[4] = cl.exchange(s, {{top, 0, 0, 0}});
-        for (int i = 0; i < cl.ranks; ++i) top = x[i][0] > top ? x[i][0] : top;
+        for (int i = 0; i < cl.ranks; ++i) top = max(top, (uint32_t)x[i][0]);
     }
     const float T = a.temperature ? a.temperature[r] : 1.f;
     const int k = a.top_k ? a.top_k[r] : 0;
-    if (top == 0 || !a.u || !(T > 0.f) || k == 1) {
-        if (top == 0) finish(-1, 0.0);
-        else finish((int)(uint32_t)~(uint32_t)top, 1.0);
+    if (top == 0) {
+        finish(-1, 0.0);
         cl.sync();  // no CTA leaves while another may still write to it
         return;
     }
     Scale c;
+    c.max = key_value(top);
+    if (!a.u || !(T > 0.f) || k == 1) {
+        // its lowest index: the threads that have met it look once more
+        if (tid == 0) s.cut = 0x7fffffff;
+        __syncthreads();
+        if (any && best == c.max)
+            row.template each<1>([&](float l, int i) {
+                if (l == best) atomicMin(&s.cut, i);
+            });
+        __syncthreads();
+        const u64(*x)[4] = cl.exchange(s, {{(u64)s.cut, 0, 0, 0}});
+        u64 at = x[0][0];
+        for (int i = 1; i < cl.ranks; ++i) at = min(at, x[i][0]);
+        finish((int)at, 1.0);
+        cl.sync();
+        return;
+    }
     {
-        c.max = key_value((uint32_t)(top >> 32));
         const double f = fmin(1.4426950408889634 / (double)T, 1e30);
         c.hi = (float)f;
         c.lo = (float)(f - (double)c.hi);
@@ -607,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const double u = fmin(fmax((double)a.u[r], 0.0), 1.0);
 
     // 2. the threshold
-    if (any) atomicAdd(&s.cut_count[(int)fminf(coarse_t(best, c) * 16.f, (float)(kCut - 1))], 1u);
+    if (any) atomicAdd(&s.cut_count[min(bin_of(best, c) >> 1, kCut - 1)], 1u);
     cl.sync();
     {
         static_assert(kCut == kThreads, "a bin per thread");
@@ -622,28 +699,36 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (run >= wanted && run - n < wanted) s.cut = tid;
         __syncthreads();
     }
-    const float cut = (float)(s.cut + 1);
+    const int cut = 2 * (s.cut + 1);  // the list's bins: 0 .. cut - 1
 
     // 3. the list; without top_k the weight of all, of those that min_p keeps,
     // and the histogram of what is not in the list
-    u64 sums[3] = {0, 0, 0};  // rest, all, some
-    if (with_k) {
-        row.template each<4>([&](float l, int i) {
-            if (coarse_t(l, c) * 16.f < cut) append(s, key_of(l), i);
-            else sums[0] += l > -INFINITY;
+    u64 sums[3] = {0, 0, 0};  // valid tokens outside the list (top_k), all, some
+    const bool top_inf = isinf(c.max);
+    if (with_k || top_inf) {
+        // (any beginning of the order will do: one comparison per token)
+        const float least_l = c.max - (float)cut / (c.hi * 32.f);
+        row.template pairs<2>([&](float2 l, int i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = e ? l.y : l.x;
+                if (x >= least_l && x > -INFINITY) append(s, key_of(x), i + e);
+                else sums[0] += x > -INFINITY;
+            }
         });
     } else {
-        row.template each<2>([&](float l, int i) {
-            if (!(l > -INFINITY)) return;
-            const u64 w = weight_of(l, c, s.pow64);
-            sums[1] += w;
-            if (w >= least_w) sums[2] += w;
-            const float t = coarse_t(l, c);
-            if (t * 16.f < cut) {
-                append(s, key_of(l), i);
-            } else {
-                ++sums[0];
-                if (w) add_parts(s, (int)(t * 32.f), w);
+        row.template pairs<HALF ? 1 : 2>([&](float2 l, int i) {
+            const Two x = two_of<!HALF>(l, c);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float t = e ? x.t.y : x.t.x, v = e ? l.y : l.x;
+                if (!(t < kEnd)) continue;  // no weight (-inf and NaN among them)
+                const u64 w = weight_from(x.k[e], e ? x.y.y : x.y.x, s.pow64);
+                sums[1] += w;
+                if (least_w && w >= least_w) sums[2] += w;
+                const int bin = magic_int(fmaf(c.max - v, c.hi * 32.f, kMagic));
+                if (bin < cut) append(s, key_of(v), i + e);
+                else add_parts(s, bin, w);
             }
         });
     }
@@ -658,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         some += n[i][3];
         fits = fits && n[i][0] <= kList;
     }
-    fits = fits && n_list <= kAll;
+    fits = fits && n_list > 0 && n_list <= kAll && !top_inf;
 
     // What rank 0 finds in the list: 0 everything; 1 the nucleus ends below
     // it; 2 the token stands below it; 3 the list does not do
@@ -671,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (fits && cl.rank == 0) {
         const int N = (int)n_list;
         gather(s, cl, n, s.all);
-        sort_and_scan(s, s.all, s.pre, N, c);
+        sort_and_scan<HALF>(s, s.all, s.pre, N, c);
         W_list = s.pre[N - 1];
         if (!with_k || k <= N || rest == 0) {
             state = kDone;
@@ -725,11 +810,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 found = true;
             } else if (h.by_digits) {  // the histogram once more
                 clear_histogram(s, kBins);
-                row.template each<2>([&](float l, int) {
-                    if (!(l > -INFINITY)) return;
-                    const float t = coarse_t(l, c);
-                    const u64 w = t * 16.f < cut ? 0 : weight_of(l, c, s.pow64);
-                    if (w) add_parts(s, (int)(t * 32.f), w);
+                row.template each<1>([&](float l, int) {
+                    const int bin = bin_of(l, c);
+                    if (bin >= cut && bin < kBins - 1) add_parts(s, bin, weight_of<!HALF>(l, c, s.pow64));
                 });
                 join_histogram(s, cl, kBins, false);
             }
@@ -744,9 +827,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const auto histogram = [&]() {
             clear_histogram(s, kBins);
             Tally t;
-            row.template each<2>([&](float l, int) {
+            row.template each<1>([&](float l, int) {
                 if (!(l > -INFINITY)) return;
-                const u64 w = weight_of(l, c, s.pow64);
+                const u64 w = weight_of<!HALF>(l, c, s.pow64);
                 if (w == 0) return;
                 t.add(s, bin_of(l, c), w);
             });
@@ -754,11 +837,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             join_histogram(s, cl, kBins, true);
         };
         histogram();
-        if (with_k && least_w) {
+        if ((with_k || top_inf) && least_w) {
             sums[0] = 0;
-            row.template each<2>([&](float l, int) {
+            row.template each<1>([&](float l, int) {
                 if (!(l > -INFINITY)) return;
-                const u64 w = weight_of(l, c, s.pow64);
+                const u64 w = weight_of<!HALF>(l, c, s.pow64);
                 if (w >= least_w) sums[0] += w;
             });
             u64 one[1] = {sums[0]};
