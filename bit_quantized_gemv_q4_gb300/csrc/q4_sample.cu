@@ -56,8 +56,8 @@ constexpr int kAll = 2048;           // tokens of the joined list
 constexpr int kBinList = 1024;       // tokens of a bin that are sorted together
 constexpr int kCounting = 256;       // up to here a sort counts, per token, the greater ones
 constexpr int kMostPart = 1 << 17;   // tokens of a CTA: sums of 15-bit parts of their weights stay below 2^32
-constexpr int kCut = 512;            // bins of the threshold: 16 per octave
-constexpr int kBins = 1536;          // bins of the histogram: 32 per octave, 48 octaves (weights end at 45)
+constexpr int kCut = 512;            // bins of the threshold: 16 per octave (4 steps)
+constexpr int kBins = 1536;          // bins of a histogram: a step each from the threshold on, or two steps from t = 0 on
 constexpr u64 kOne = 1ull << 44;     // the weight of the greatest logit
 constexpr uint32_t kLeast = 0x007FFFFFu;  // key of -inf: takes no part
 
@@ -110,13 +110,26 @@ struct Scale {
 constexpr float kMagic = 12582912.f;
 __device__ __forceinline__ int magic_int(float x) { return __float_as_int(x) - __float_as_int(kMagic); }
 
-// Bin of a logit: 32 t to the nearest integer, kBins - 1 from t = 46 on (no
-// weight there).  Monotone in the logit.
+// Steps of a logit: 64 t to the nearest integer, kSteps from t = 46 on (no
+// weight there).  Monotone in the logit; every bin is a range of steps.
 constexpr float kEnd = 46.f;
-__device__ __forceinline__ int bin_of(float l, const Scale& c) {
+constexpr int kSteps = 64 * 46 + 1;
+__device__ __forceinline__ int steps_of(float l, const Scale& c) {
     const float d = l == c.max ? 0.f : c.max - l;
-    return d * c.hi < kEnd ? magic_int(fmaf(d, c.hi * 32.f, kMagic)) : kBins - 1;
+    return d * c.hi < kEnd ? magic_int(fmaf(d, c.hi * 64.f, kMagic)) : kSteps;
 }
+
+// round(2^29 2^(-j/64))
+__constant__ uint32_t kPow64[64] = {
+    536870912u, 531087746u, 525366875u, 519707630u, 514109347u, 508571368u, 503093043u, 497673732u,
+    492312797u, 487009610u, 481763549u, 476573998u, 471440350u, 466362000u, 461338355u, 456368824u,
+    451452825u, 446589781u, 441779122u, 437020283u, 432312707u, 427655840u, 423049137u, 418492057u,
+    413984066u, 409524635u, 405113241u, 400749367u, 396432500u, 392162134u, 387937769u, 383758908u,
+    379625062u, 375535746u, 371490480u, 367488790u, 363530205u, 359614263u, 355740503u, 351908471u,
+    348117717u, 344367798u, 340658272u, 336988706u, 333358668u, 329767733u, 326215479u, 322701490u,
+    319225354u, 315786663u, 312385013u, 309020006u, 305691246u, 302398344u, 299140913u, 295918571u,
+    292730940u, 289577647u, 286458320u, 283372595u, 280320109u, 277300504u, 274313427u, 271358526u,
+};
 
 // 2^44 2^(-k/64) (1 - y), rounded; k >= 0, |y| < 0.0056.
 __device__ __forceinline__ u64 weight_from(int k, float y, const float2* pow64) {
@@ -217,12 +230,19 @@ struct Part {
     __device__ __forceinline__ void pairs(F f) const {
         if (rank == 0 && (int)threadIdx.x < head) f(make_float2(at(threadIdx.x), -INFINITY), (int)threadIdx.x);
         const uint4* vec = reinterpret_cast<const uint4*>(row + head);
+        uint4 next[N];  // the loads of the turn after this one are on their way meanwhile
+        const auto load = [&](int v) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (v + i * kThreads < v1) next[i] = vec[v + i * kThreads];
+        };
+        load(v0 + threadIdx.x);
 #pragma unroll 1
         for (int v = v0 + threadIdx.x; v < v1; v += N * kThreads) {
             uint4 w[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (v + i * kThreads < v1) w[i] = vec[v + i * kThreads];
+            for (int i = 0; i < N; ++i) w[i] = next[i];
+            load(v + N * kThreads);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (v + i * kThreads >= v1) break;
@@ -497,22 +517,23 @@ struct Hit {
     bool by_digits;  // the search used the histogram's arrays
 };
 
-// The place where the count or weight of the tokens of `bin` reaches target
-// (what stands before the bin already taken off): its running weight within
-// the bin and, if asked, its token.
+// The place where the count or weight of the tokens of steps s0 .. s1 - 1
+// reaches target (what stands before them already taken off): its running
+// weight among them and its token.
 template <bool HALF>
-__device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const Scale& c, int bin, bool by_count,
-                          u64 target) {
+__device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const Scale& c, int s0, int s1,
+                          bool by_count, u64 target) {
     __syncthreads();
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    const float b32 = c.hi * 32.f;
+    const float b64 = c.hi * 64.f;
     row.template pairs<2>([&](float2 l, int i) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float x = e ? l.y : l.x, d = c.max - x;
-            // (a NaN or -inf fails the first test; max itself, even +inf, is bin 0)
-            if (x == c.max ? bin == 0 : d * c.hi < kEnd && magic_int(fmaf(d, b32, kMagic)) == bin) append(s, key_of(x), i + e);
+            // (a NaN or -inf fails the first test; max itself, even +inf, has 0 steps)
+            const int k = magic_int(fmaf(d, b64, kMagic));
+            if (x == c.max ? s0 == 0 : d * c.hi < kEnd && k >= s0 && k < s1) append(s, key_of(x), i + e);
         }
     });
     __syncthreads();
@@ -554,7 +575,8 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
         Tally t;
         row.template each<1>([&](float l, int) {
             const uint32_t k = key_of(l);
-            if (k == kLeast || bin_of(l, c) != bin || (shift < 24 && k >> (shift + 8) != prefix >> (shift + 8))) return;
+            const int st = steps_of(l, c);
+            if (k == kLeast || st < s0 || st >= s1 || (shift < 24 && k >> (shift + 8) != prefix >> (shift + 8))) return;
             t.add(s, 255 - (int)(k >> shift & 255u), weight_of<!HALF>(key_value(k), c, s.pow64));
         });
         t.flush(s);
@@ -601,9 +623,33 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     return h;
 }
 
-__device__ __forceinline__ u64 share_target(double share, u64 W) {  // least integer at or above share * W, 1 .. W
-    const double want = ceil(fmax(share, 0.0) * (double)W);
-    return want < 1.0 ? 1 : want > (double)W ? W : (u64)want;
+// floor(x W) and whether anything is left over, for 0 <= x <= 1: a float is a
+// 24-bit integer and a power of two, so the product is exact in 128 bits.
+__device__ __forceinline__ u64 share_floor(float x, u64 W, bool& rest) {
+    if (x >= 1.f) {
+        rest = false;
+        return W;
+    }
+    const uint32_t b = __float_as_uint(x);
+    const int e = (int)(b >> 23);
+    const u64 m = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+    const int sh = 150 - (e ? e : 1);  // x = m 2^-sh; 24 .. 149
+    const u64 lo = W * m, hi = __umul64hi(W, m);  // hi below 2^24
+    if (sh < 64) {
+        rest = (lo & ((1ull << sh) - 1)) != 0;
+        return lo >> sh | hi << (64 - sh);
+    }
+    rest = lo != 0 || (sh < 128 ? (hi & ((1ull << (sh - 64)) - 1)) != 0 : hi != 0);
+    return sh - 64 < 64 ? hi >> (sh - 64) : 0;
+}
+__device__ __forceinline__ u64 nucleus_target(float p, u64 W) {  // least integer at or above p W, at least 1
+    bool rest;
+    const u64 t = share_floor(fmaxf(p, 0.f), W, rest);
+    return max(t + rest, 1ull);
+}
+__device__ __forceinline__ u64 token_target(float u, u64 W) {  // least integer above u W, at most W
+    bool rest;
+    return min(share_floor(u, W, rest) + 1, W);
 }
 
 template <bool HALF>
@@ -614,22 +660,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     cl.rank = (int)cl.g.block_rank();
     const int r = blockIdx.x / a.cluster, tid = threadIdx.x;
     const Part<HALF> row(a, r, cl.rank);
-    const auto finish = [&](int token, double prob) {
+    const auto finish = [&](int token, u64 own, u64 of) {
         if (cl.rank == 0 && tid == 0) {
             a.tokens[r] = token;
-            if (a.probs) a.probs[r] = (float)prob;
+            if (a.probs) a.probs[r] = of ? (float)((double)own / (double)of) : 0.f;
         }
     };
 
     // 1. the greatest logit
     float best = -INFINITY;
-    row.template pairs<HALF ? 4 : 8>([&](float2 l, int) { best = fmaxf(best, fmaxf(l.x, l.y)); });
+    row.template pairs<4>([&](float2 l, int) { best = fmaxf(best, fmaxf(l.x, l.y)); });
     const bool any = best > -INFINITY;
     // (while the loads are on their way: the tables)
-    if (tid < 64) {
-        const double p = rint(exp2(-tid / 64.0) * 536870912.0);
-        s.pow64[tid] = make_float2(__int_as_float((int)p), (float)p);
-    }
+    if (tid < 64) s.pow64[tid] = make_float2(__int_as_float((int)kPow64[tid]), (float)kPow64[tid]);
     for (int b = tid; b < kCut; b += kThreads) s.cut_count[b] = 0;
     for (int b = tid; b < kBins; b += kThreads) s.h0[b] = s.h1[b] = s.h2[b] = 0;
     if (tid == 0) {
@@ -649,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const float T = a.temperature ? a.temperature[r] : 1.f;
     const int k = a.top_k ? a.top_k[r] : 0;
     if (top == 0) {
-        finish(-1, 0.0);
+        finish(-1, 0, 0);
         cl.sync();  // no CTA leaves while another may still write to it
         return;
     }
@@ -667,24 +710,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const u64(*x)[4] = cl.exchange(s, {{(u64)s.cut, 0, 0, 0}});
         u64 at = x[0][0];
         for (int i = 1; i < cl.ranks; ++i) at = min(at, x[i][0]);
-        finish((int)at, 1.0);
+        finish((int)at, 1, 1);
         cl.sync();
         return;
     }
     {
-        const double f = fmin(1.4426950408889634 / (double)T, 1e30);
-        c.hi = (float)f;
-        c.lo = (float)(f - (double)c.hi);
+        // log2(e) / T as a float pair: the quotient, and what it leaves over
+        const float f = 1.44269502f / T;
+        c.hi = fminf(f, 1e30f);
+        const float left = fmaf(-f, T, 1.44269502f) + 1.92596299e-8f;
+        c.lo = f > 1e-30f && f < 1e30f ? left / T : 0.f;
     }
     const bool with_k = k > 0 && k < a.vocab;
     const float p = a.top_p ? a.top_p[r] : 1.f;
     const float mp = a.min_p ? a.min_p[r] : 0.f;
-    const double least = mp > 0.f ? (double)fminf(mp, 1.f) * (double)kOne : 0.0;
-    const u64 least_w = (u64)ceil(least);
-    const double u = fmin(fmax((double)a.u[r], 0.0), 1.0);
+    const u64 least_w = mp > 0.f ? __float2ull_ru(fminf(mp, 1.f) * 17592186044416.f) : 0;  // 2^44 min_p, exact
+    const float u = fminf(fmaxf(a.u[r], 0.f), 1.f);
 
     // 2. the threshold
-    if (any) atomicAdd(&s.cut_count[min(bin_of(best, c) >> 1, kCut - 1)], 1u);
+    if (any) atomicAdd(&s.cut_count[min(steps_of(best, c) >> 2, kCut - 1)], 1u);
     cl.sync();
     {
         static_assert(kCut == kThreads, "a bin per thread");
@@ -699,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (run >= wanted && run - n < wanted) s.cut = tid;
         __syncthreads();
     }
-    const int cut = 2 * (s.cut + 1);  // the list's bins: 0 .. cut - 1
+    const int cut = 4 * (s.cut + 1);  // the list's steps: 0 .. cut - 1
 
     // 3. the list; without top_k the weight of all, of those that min_p keeps,
     // and the histogram of what is not in the list
@@ -707,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const bool top_inf = isinf(c.max);
     if (with_k || top_inf) {
         // (any beginning of the order will do: one comparison per token)
-        const float least_l = c.max - (float)cut / (c.hi * 32.f);
+        const float least_l = c.max - (float)cut / (c.hi * 64.f);
         row.template pairs<2>([&](float2 l, int i) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -726,9 +770,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 const u64 w = weight_from(x.k[e], e ? x.y.y : x.y.x, s.pow64);
                 sums[1] += w;
                 if (least_w && w >= least_w) sums[2] += w;
-                const int bin = magic_int(fmaf(c.max - v, c.hi * 32.f, kMagic));
-                if (bin < cut) append(s, key_of(v), i + e);
-                else add_parts(s, bin, w);
+                if (x.k[e] < cut) append(s, key_of(v), i + e);
+                else add_parts(s, min(x.k[e] - cut, kBins - 1), w);
             }
         });
     }
@@ -751,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u64 state = kNoList, target = 0, W_list = 0;
     const auto in_list = [&](u64 t) {
         const int i = reach(s, s.pre, (int)n_list, t);
-        finish((int)(uint32_t)~(uint32_t)s.all[i], (double)(s.pre[i] - (i ? s.pre[i - 1] : 0)) / (double)W);
+        finish((int)(uint32_t)~(uint32_t)s.all[i], s.pre[i] - (i ? s.pre[i - 1] : 0), W);
     };
     if (fits && cl.rank == 0) {
         const int N = (int)n_list;
@@ -762,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             state = kDone;
             if (with_k) W = s.pre[min(k, N) - 1];
             if (p < 1.f) {
-                target = share_target((double)p, W);
+                target = nucleus_target(p, W);
                 if (target <= W_list) W = s.pre[reach(s, s.pre, N, target)];
                 else state = kNucleus;
             }
@@ -776,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                     some = s.pre[some - 1];
                 }
                 if (least_w) W = min(W, some);
-                target = min(W, (u64)(u * (double)W) + 1);
+                target = token_target(u, W);
                 if (target <= W_list) in_list(target);
                 else state = kToken;
             }
@@ -789,12 +832,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         W_list = x[0][2];
         W = state == kNoList ? W : x[0][3];
     }
+    if (state == kDone) return;  // (every CTA has read what it reads of the others)
     if (state == kNucleus || state == kToken) {
         // below the list, without top_k: by the histogram
         const auto below = [&]() {
             const int b = reach_bin(s, kBins, false, target - W_list);
             const u64 before = W_list + (b ? s.mw[b - 1] : 0);
-            Hit h = search_bin<HALF>(row, s, cl, c, b, false, target - before);
+            Hit h = search_bin<HALF>(row, s, cl, c, cut + b, b < kBins - 1 ? cut + b + 1 : kSteps, false, target - before);
             h.weight += before;
             return h;
         };
@@ -804,22 +848,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             Hit h = below();
             W = h.weight;
             if (least_w) W = min(W, some);
-            target = min(W, (u64)(u * (double)W) + 1);
+            target = token_target(u, W);
             if (target <= W_list) {
                 if (cl.rank == 0) in_list(target);
                 found = true;
             } else if (h.by_digits) {  // the histogram once more
                 clear_histogram(s, kBins);
                 row.template each<1>([&](float l, int) {
-                    const int bin = bin_of(l, c);
-                    if (bin >= cut && bin < kBins - 1) add_parts(s, bin, weight_of<!HALF>(l, c, s.pow64));
+                    const int st = steps_of(l, c);
+                    if (st >= cut && st < kSteps) add_parts(s, min(st - cut, kBins - 1), weight_of<!HALF>(l, c, s.pow64));
                 });
                 join_histogram(s, cl, kBins, false);
             }
         }
         if (!found) {
             const Hit h = below();
-            finish(h.token, (double)h.own / (double)W);
+            finish(h.token, h.own, W);
         }
     } else if (state == kNoList) {
         // the list has overflowed (a flat top), or top_k is larger than one:
@@ -831,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 if (!(l > -INFINITY)) return;
                 const u64 w = weight_of<!HALF>(l, c, s.pow64);
                 if (w == 0) return;
-                t.add(s, bin_of(l, c), w);
+                t.add(s, steps_of(l, c) >> 1, w);
             });
             t.flush(s);
             join_histogram(s, cl, kBins, true);
@@ -854,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const auto at = [&](bool by_count, u64 t) {
             const int b = reach_bin(s, kBins, by_count, t);
             const u64 nb = b ? s.mc[b - 1] : 0, wb = b ? s.mw[b - 1] : 0;
-            Hit h = search_bin<HALF>(row, s, cl, c, b, by_count, t - (by_count ? nb : wb));
+            Hit h = search_bin<HALF>(row, s, cl, c, 2 * b, 2 * b + 2, by_count, t - (by_count ? nb : wb));
             h.weight += wb;
             return h;
         };
@@ -866,14 +910,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         if (p < 1.f) {
             if (stale) histogram();
-            const Hit h = at(false, share_target((double)p, W));
+            const Hit h = at(false, nucleus_target(p, W));
             W = h.weight;
             stale = h.by_digits;
         }
         if (least_w) W = min(W, some);
         if (stale) histogram();
-        const Hit h = at(false, min(W, (u64)(u * (double)W) + 1));
-        finish(h.token, (double)h.own / (double)W);
+        const Hit h = at(false, token_target(u, W));
+        finish(h.token, h.own, W);
     }
     cl.sync();  // no CTA leaves while another may still use its shared memory
 }
