@@ -489,6 +489,26 @@ __device__ void join_histogram(Shared& s, Cluster& cl, int bins, bool counts) {
     __syncthreads();
 }
 
+// The same for the weights alone, by rank 0 for itself (every CTA's histogram
+// is done).
+__device__ void join_tail(Shared& s, Cluster& cl) {
+    constexpr int P = kBins / kThreads;
+    u64 w[P] = {};
+    for (int r = 0; r < cl.ranks; ++r) {
+        const uint32_t* h0 = cl.g.map_shared_rank(&s.h0[P * threadIdx.x], r);
+        const uint32_t* h1 = cl.g.map_shared_rank(&s.h1[P * threadIdx.x], r);
+        const uint32_t* h2 = cl.g.map_shared_rank(&s.h2[P * threadIdx.x], r);
+#pragma unroll
+        for (int e = 0; e < P; ++e) w[e] += (u64)h0[e] + ((u64)h1[e] << 15) + ((u64)h2[e] << 30);
+    }
+#pragma unroll
+    for (int e = 1; e < P; ++e) w[e] += w[e - 1];
+    const u64 before = block_scan(w[P - 1], s) - w[P - 1];
+#pragma unroll
+    for (int e = 0; e < P; ++e) s.mw[P * threadIdx.x + e] = before + w[e];
+    __syncthreads();
+}
+
 // First bin whose running count or weight reaches target (there is one; else the last).
 __device__ int reach_bin(Shared& s, int bins, bool by_count, u64 target) {
     if (threadIdx.x == 0) s.result[2] = bins - 1;
@@ -526,14 +546,19 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     __syncthreads();
     if (threadIdx.x == 0) s.count = 0;
     __syncthreads();
-    const float b64 = c.hi * 64.f;
+    // most tokens are ruled out by two comparisons, a step wider than the range
+    // (without a limit where the scale is zero)
+    const float step = 1.f / (c.hi * 64.f);
+    const float most = s0 > 0 ? c.max - (float)(s0 - 1) * step : INFINITY;
+    const float fewest = c.hi > 0.f ? c.max - (float)(s1 + 1) * step : -INFINITY;
     row.template pairs<2>([&](float2 l, int i) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float x = e ? l.y : l.x, d = c.max - x;
-            // (a NaN or -inf fails the first test; max itself, even +inf, has 0 steps)
-            const int k = magic_int(fmaf(d, b64, kMagic));
-            if (x == c.max ? s0 == 0 : d * c.hi < kEnd && k >= s0 && k < s1) append(s, key_of(x), i + e);
+            const float x = e ? l.y : l.x;
+            if (x <= most && x >= fewest && x > -INFINITY) {
+                const int st = steps_of(x, c);
+                if (st >= s0 && st < s1) append(s, key_of(x), i + e);
+            }
         }
     });
     __syncthreads();
@@ -788,13 +813,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     fits = fits && n_list > 0 && n_list <= kAll && !top_inf;
 
-    // What rank 0 finds in the list: 0 everything; 1 the nucleus ends below
-    // it; 2 the token stands below it; 3 the list does not do
+    // Rank 0 decides: the list holds everything; the nucleus ends below it; the
+    // token stands below it (then in which bin, by the histogram); the list
+    // does not do.
     enum : u64 { kDone, kNucleus, kToken, kNoList };
     u64 state = kNoList, target = 0, W_list = 0;
-    const auto in_list = [&](u64 t) {
-        const int i = reach(s, s.pre, (int)n_list, t);
+    int bin = 0;
+    const auto choose = [&]() {  // the token, W being known
+        if (least_w) W = min(W, some);
+        target = token_target(u, W);
+        if (target > W_list) {
+            state = kToken;
+            return;
+        }
+        state = kDone;
+        const int i = reach(s, s.pre, (int)n_list, target);
         finish((int)(uint32_t)~(uint32_t)s.all[i], s.pre[i] - (i ? s.pre[i - 1] : 0), W);
+    };
+    const auto find_bin = [&]() {  // takes what stands before it off the target
+        target -= W_list;
+        bin = reach_bin(s, kBins, false, target);
+        if (bin) target -= s.mw[bin - 1];
     };
     if (fits && cl.rank == 0) {
         const int N = (int)n_list;
@@ -802,69 +841,62 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         sort_and_scan<HALF>(s, s.all, s.pre, N, c);
         W_list = s.pre[N - 1];
         if (!with_k || k <= N || rest == 0) {
-            state = kDone;
-            if (with_k) W = s.pre[min(k, N) - 1];
-            if (p < 1.f) {
-                target = nucleus_target(p, W);
-                if (target <= W_list) W = s.pre[reach(s, s.pre, N, target)];
-                else state = kNucleus;
-            }
-            if (state == kDone) {
-                if (least_w && with_k) {
-                    some = 0;  // of the list: top_k ends in it
+            if (with_k) {
+                W = s.pre[min(k, N) - 1];
+                if (least_w) {  // top_k ends in the list, so what min_p keeps of it is all that counts
+                    some = 0;
                     for (int i0 = 0; i0 < N; i0 += kThreads) {
                         const int i = i0 + tid;
                         some += __syncthreads_count(i < N && s.pre[i] - (i ? s.pre[i - 1] : 0) >= least_w);
                     }
                     some = s.pre[some - 1];
                 }
-                if (least_w) W = min(W, some);
-                target = token_target(u, W);
-                if (target <= W_list) in_list(target);
-                else state = kToken;
+            }
+            state = kDone;
+            if (p < 1.f) {
+                target = nucleus_target(p, W);
+                if (target <= W_list) W = s.pre[reach(s, s.pre, N, target)];
+                else state = kNucleus;
+            }
+            if (state == kDone) choose();
+            if (state != kDone) {
+                join_tail(s, cl);
+                find_bin();
             }
         }
     }
-    {
-        const u64(*x)[4] = cl.exchange(s, {{state, target, W_list, W}});
+    const auto tell = [&]() {
+        const u64(*x)[4] = cl.exchange(s, {{state, target, (u64)bin, W}});
         state = x[0][0];
         target = x[0][1];
-        W_list = x[0][2];
-        W = state == kNoList ? W : x[0][3];
-    }
+        bin = (int)x[0][2];
+        if (state != kNoList) W = x[0][3];
+    };
+    tell();
     if (state == kDone) return;  // (every CTA has read what it reads of the others)
     if (state == kNucleus || state == kToken) {
-        // below the list, without top_k: by the histogram
-        const auto below = [&]() {
-            const int b = reach_bin(s, kBins, false, target - W_list);
-            const u64 before = W_list + (b ? s.mw[b - 1] : 0);
-            Hit h = search_bin<HALF>(row, s, cl, c, cut + b, b < kBins - 1 ? cut + b + 1 : kSteps, false, target - before);
-            h.weight += before;
-            return h;
-        };
-        join_histogram(s, cl, kBins, false);
-        bool found = false;
+        // below the list, without top_k
+        Hit h = search_bin<HALF>(row, s, cl, c, cut + bin, bin < kBins - 1 ? cut + bin + 1 : kSteps, false, target);
         if (state == kNucleus) {
-            Hit h = below();
-            W = h.weight;
-            if (least_w) W = min(W, some);
-            target = token_target(u, W);
-            if (target <= W_list) {
-                if (cl.rank == 0) in_list(target);
-                found = true;
-            } else if (h.by_digits) {  // the histogram once more
+            if (h.by_digits) {  // the search has used the histogram's arrays
                 clear_histogram(s, kBins);
                 row.template each<1>([&](float l, int) {
                     const int st = steps_of(l, c);
                     if (st >= cut && st < kSteps) add_parts(s, min(st - cut, kBins - 1), weight_of<!HALF>(l, c, s.pow64));
                 });
-                join_histogram(s, cl, kBins, false);
+                cl.sync();
             }
+            if (cl.rank == 0) {
+                if (h.by_digits) join_tail(s, cl);
+                W = W_list + (bin ? s.mw[bin - 1] : 0) + h.weight;
+                choose();
+                if (state == kToken) find_bin();
+            }
+            tell();
+            if (state == kDone) return;
+            h = search_bin<HALF>(row, s, cl, c, cut + bin, bin < kBins - 1 ? cut + bin + 1 : kSteps, false, target);
         }
-        if (!found) {
-            const Hit h = below();
-            finish(h.token, h.own, W);
-        }
+        finish(h.token, h.own, W);
     } else if (state == kNoList) {
         // the list has overflowed (a flat top), or top_k is larger than one:
         // counts and weights of all, by bins
