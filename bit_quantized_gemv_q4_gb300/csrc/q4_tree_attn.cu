@@ -83,9 +83,11 @@ __device__ __forceinline__ int tile_cost(const Args& a, const Seq& q, int rb) {
 // Units of one head of a sequence (all row blocks).
 __device__ __forceinline__ unsigned head_units(const Args& a, const Seq& q) {
     unsigned t = 0;
-    if (q.n > 0)
 #pragma unroll 1
-        for (int b = 0; b * a.BM < q.n * a.G; ++b) t += (unsigned)(block_tiles(a, q, b) * tile_cost(a, q, b));
+    for (int b = 0; b * a.BM < q.n * a.G; b += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((b + e) * a.BM < q.n * a.G) t += (unsigned)(block_tiles(a, q, b + e) * tile_cost(a, q, b + e));
     return t;
 }
 
@@ -148,18 +150,25 @@ __device__ __noinline__ Place line_find(const Args& a, const unsigned* sums, int
         if (sums[mid] > x) hi = mid;
         else lo = mid + 1;
     }
-    unsigned rest = lo > 0 ? x - sums[lo - 1] : x;
+    const unsigned before = lo > 0 ? sums[lo - 1] : 0u;
+    unsigned rest = x - before;
     Place p;
     unsigned head = 0;
-    p.s = lo * (int)((unsigned)(a.w.S + threads - 1) / (unsigned)threads);
-#pragma unroll 1
-    while (true) {
-        bool bad;
+    bool bad;
+    if (a.w.S <= threads) {  // a thread's share was one sequence
+        p.s = lo;
         p.q = q4p::seq_of(a.w, p.s, bad);
-        head = head_units(a, p.q);
-        if (rest < head * (unsigned)a.w.H) break;  // (below 2^31: the line is)
-        rest -= head * (unsigned)a.w.H;
-        ++p.s;
+        head = (sums[lo] - before) / (unsigned)a.w.H;
+    } else {
+        p.s = lo * (int)((unsigned)(a.w.S + threads - 1) / (unsigned)threads);
+#pragma unroll 1
+        while (true) {
+            p.q = q4p::seq_of(a.w, p.s, bad);
+            head = head_units(a, p.q);
+            if (rest < head * (unsigned)a.w.H) break;  // (below 2^31: the line is)
+            rest -= head * (unsigned)a.w.H;
+            ++p.s;
+        }
     }
     p.h = (int)(rest / head);
     rest -= (unsigned)p.h * head;
@@ -812,7 +821,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     const int last = (int)(last_at / share);  // CTA of the job's last tile
     const auto slot_of = [&](int c) { return 2 * c + (c == b); };
     // kIlp rows of a warp at a time: their loads are in flight together
-    constexpr int E = D / 32, kIlp = 4;
+    constexpr int E = D / 32, kIlp = 2;
     for (int r0 = (blockIdx.y * (kJoinThreads / 32) + warp) * kIlp; r0 < rows; r0 += gridDim.y * (kJoinThreads / 32) * kIlp) {
         float m[kIlp], l[kIlp], f[kIlp], o[kIlp][E];
 #pragma unroll
@@ -822,45 +831,63 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
 #pragma unroll
             for (int e = 0; e < E; ++e) o[i][e] = 0.f;
         }
-        for (int c = b + lane; c <= last; c += 32)
+        const int parts = last - b + 1;
+        const auto load_o = [&](int c, float (&v)[kIlp][E]) {
+            const float* src = part_o<D>(a, slot_of(c)) + (size_t)r0 * D + E * lane;
+#pragma unroll
+            for (int i = 0; i < kIlp; ++i) {
+                if (r0 + i >= rows) break;
+                if constexpr (E == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(src + i * D);
+                    v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(src + i * D);
+                    v[i][0] = t.x, v[i][1] = t.y;
+                }
+            }
+        };
+        // (m, l) of the first 32 parts and the first part's rows are on their
+        // way together; further parts' (m, l) are read again when their turn comes
+        float2 ml[kIlp];
+        float v[kIlp][E], next[kIlp][E];
+#pragma unroll
+        for (int i = 0; i < kIlp; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (lane < parts && r0 + i < rows) ml[i] = part_ml(a, slot_of(b + lane))[r0 + i];
+        }
+        load_o(b, v);
+        for (int c = b + 32 + lane; c <= last; c += 32)
 #pragma unroll
             for (int i = 0; i < kIlp; ++i)
                 if (r0 + i < rows) m[i] = fmaxf(m[i], part_ml(a, slot_of(c))[r0 + i].x);
 #pragma unroll
         for (int i = 0; i < kIlp; ++i) {
+            m[i] = fmaxf(m[i], ml[i].x);
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
             if (m[i] == -INFINITY) m[i] = 0.f;
         }
-        for (int c0 = b; c0 <= last; c0 += 32) {
-#pragma unroll
-            for (int i = 0; i < kIlp; ++i) {
-                f[i] = 0.f;
-                if (c0 + lane <= last && r0 + i < rows) {
-                    const float2 t = part_ml(a, slot_of(c0 + lane))[r0 + i];
-                    f[i] = exp2f(t.x - m[i]);
-                    l[i] = fmaf(t.y, f[i], l[i]);
-                }
-            }
-            const int n = min(32, last - c0 + 1);
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const float* src = part_o<D>(a, slot_of(c0 + k)) + (size_t)r0 * D + E * lane;
+        for (int c = b; c <= last; ++c) {
+            const int k = (c - b) & 31;
+            if (c < last) load_o(c + 1, next);
+            if (k == 0) {
 #pragma unroll
                 for (int i = 0; i < kIlp; ++i) {
-                    if (r0 + i >= rows) break;
-                    const float fi = __shfl_sync(0xffffffffu, f[i], k);
-                    if constexpr (E == 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(src + i * D);
-                        o[i][0] = fmaf(t.x, fi, o[i][0]);
-                        o[i][1] = fmaf(t.y, fi, o[i][1]);
-                        o[i][2] = fmaf(t.z, fi, o[i][2]);
-                        o[i][3] = fmaf(t.w, fi, o[i][3]);
-                    } else {
-                        const float2 t = *reinterpret_cast<const float2*>(src + i * D);
-                        o[i][0] = fmaf(t.x, fi, o[i][0]);
-                        o[i][1] = fmaf(t.y, fi, o[i][1]);
+                    if (c > b) {
+                        ml[i] = make_float2(-INFINITY, 0.f);
+                        if (c + lane <= last && r0 + i < rows) ml[i] = part_ml(a, slot_of(c + lane))[r0 + i];
                     }
+                    f[i] = ex2(ml[i].x - m[i]);
+                    l[i] = fmaf(ml[i].y, f[i], l[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kIlp; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f[i], k);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (r0 + i < rows) o[i][e] = fmaf(v[i][e], fi, o[i][e]);
+                    v[i][e] = next[i][e];
                 }
             }
         }
@@ -902,7 +929,7 @@ size_t workspace_bytes() {
 template <int D>
 cudaError_t launch_join(const Args& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.ctas - 1, (unsigned)(a.BM / 32 > 1 ? a.BM / 32 : 1));
+    cfg.gridDim = dim3((unsigned)a.ctas - 1, (unsigned)(a.BM / 64 > 1 ? a.BM / 64 : 1));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1010,7 +1037,7 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1
 constexpr float kTcShift = 7.f;
-constexpr int kTcCostFull = 4, kTcCostHalf = 3;  // of a tile, with two row streams and with alternate tiles
+constexpr int kTcCostFull = 8, kTcCostHalf = 5;  // of a tile, with two row streams and with alternate tiles
 
 template <int D>
 struct TcShape {
@@ -1340,9 +1367,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     constexpr int NC = D / 8, PER = 32 / NC;  // chunks of a row, rows per load
                     const int c = lane % NC;
                     const uint32_t col = q4d::smem_addr(dst) + (uint32_t)(c >> 3) * 16384u;
-                    // (rolled: the loads are asynchronous, and code that runs
-                    // once per segment costs its instruction fetches)
-#pragma unroll 1
+                    // (asynchronous loads in a loop: code that runs once per
+                    // segment costs its instruction fetches)
+#pragma unroll 4
                     for (int e = wr * 32 + lane / NC; e < wr * 32 + 32; e += PER) {
                         const int r = (two ? 128 * i : 0) + e;
                         const int rr = w.rb * a.BM + min(r, R - 1), tk = (int)q4p::page_of(a.by_g, rr);
