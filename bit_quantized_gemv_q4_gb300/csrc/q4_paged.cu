@@ -75,117 +75,151 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // holds whole pairs); 1: the halves of the rotated part are whole chunks, a
 // thread turns a chunk of each; 2: halves of any even length, element by
 // element.
+//
+// What bounds it: the bytes, once the latency of a block is covered.  A block
+// lives for a chain of dependent loads (the row's sequence, its sizes, the
+// page, and beside that the frequencies), so each thread fetches its first
+// kAhead items of data before anything else, one warp looks the row up and
+// two others compute the angles meanwhile.
+constexpr int kAhead = 2;
+
 template <int D, int kPairs>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_constant__ AppendArgs p) {
     __shared__ __align__(16) float2 cs[D / 2];
-    __shared__ int slot_s[2];  // sequence (-1: nobody's row), position
+    __shared__ long long base_s;  // head 0's row in the pools (-1: no memory)
+    __shared__ int slot_s;        // the row's position (-1: nobody's row)
     const int row = blockIdx.x, tid = threadIdx.x;
     constexpr int NC = D / 8;
+    const int half = p.rot / 2, rc = half / 8;          // kPairs 1: chunks of a half
+    const int per = kPairs == 1 ? NC - rc : NC;         // items of a rotated head
+    const int nq = p.Hq * per, nk = p.w.H * per, items = nq + nk + p.w.H * NC;
+    // Item x: a chunk (with its partner, kPairs 1) of a query or key head, or
+    // a chunk of the values.
+    struct Item {
+        int h, c;   // head, chunk
+        int kind;   // 0 query, 1 key, 2 value
+    };
+    const auto item = [&](int x) {
+        Item t;
+        const int y = x < nq ? x : x < nq + nk ? x - nq : x - nq - nk;
+        t.kind = x < nq ? 0 : x < nq + nk ? 1 : 2;
+        const int n = t.kind == 2 ? NC : per;
+        t.h = (int)((unsigned)y / (unsigned)n);
+        t.c = y - t.h * n;
+        return t;
+    };
+    const auto source = [&](const Item& t) {
+        const uint16_t* m = t.kind == 0 ? p.q + row * p.ldq : t.kind == 1 ? p.k + row * p.ldk : p.v + row * p.ldv;
+        return m + (long long)t.h * D;
+    };
+    const auto fetch = [&](const Item& t, uint4& a, uint4& b) {
+        const uint16_t* src = source(t);
+        if (kPairs == 1 && t.kind != 2) {
+            if (t.c < rc) b = *reinterpret_cast<const uint4*>(src + 8 * (t.c + rc));
+            a = *reinterpret_cast<const uint4*>(src + 8 * (t.c < rc ? t.c : t.c + rc));
+        } else if (kPairs != 2 || t.kind == 2) {
+            a = *reinterpret_cast<const uint4*>(src + 8 * t.c);
+        }
+    };
+    uint4 a0[kAhead], b0[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (tid + i * kAppendThreads < items) fetch(item(tid + i * kAppendThreads), a0[i], b0[i]);
+
+    const auto angle = [&](int i, long long pos) {
+        const uint64_t turn = (uint64_t)pos * p.freqs[i];
+        float sn, cn;
+        sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f, &sn, &cn);
+        cs[i] = make_float2(cn * p.amplitude, sn * p.amplitude);
+    };
     if (tid < 32) {
         const int s = seq_of_row(p.w, row, tid);
         if (tid == 0) {
-            int slot = -1, live = -1;
+            int slot = -1;
+            long long base = -1;
             if (s < p.w.S) {
                 bool bad;
                 const Seq q = seq_of(p.w, s, bad);
-                if (bad || row < q.start || row >= q.start + q.n) {
-                    atomicOr(p.w.err, q4d::kErrDeviceCheck);
-                } else {
-                    live = s;
+                if (!bad && row >= q.start && row < q.start + q.n) {
                     slot = q.ctx + (row - q.start);
+                    base = row_at(p.w, s, slot, 0, D);
                 }
+                if (base < 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
             }
-            slot_s[0] = live;
-            slot_s[1] = slot;
+            slot_s = slot;
+            base_s = base;
         }
+    } else if (tid >= 64 && tid < 64 + half && p.positions) {
+        angle(tid - 64, p.positions[row]);
     }
-    const int half = p.rot / 2;
     __syncthreads();
-    const int s = slot_s[0], slot = slot_s[1];
-    if (s < 0) return;
-    {
-        const long long pos = p.positions ? p.positions[row] : slot;
-        for (int i = tid; i < half; i += kAppendThreads) {
-            const uint64_t turn = (uint64_t)pos * p.freqs[i];
-            float sn, cn;
-            sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f, &sn, &cn);
-            cs[i] = make_float2(cn * p.amplitude, sn * p.amplitude);
-        }
+    const int slot = slot_s;
+    if (slot < 0) return;
+    if (!p.positions && half > 0) {
+        if (tid < half) angle(tid, slot);
+        __syncthreads();
     }
-    const long long base = row_at(p.w, s, slot, 0, D);  // head 0's row
-    if (base < 0 && tid == 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
-    __syncthreads();
-    const long long head_step = (long long)p.w.div.d * D;
-    const int rc = half / 8;  // kPairs 1: chunks of a half
-    const int per = kPairs == 1 ? NC - rc : NC;  // items of a rotated head
-    const int nq = p.Hq * per, nk = p.w.H * per, nv = p.w.H * NC;
-    for (int x = tid; x < nq + nk + nv; x += kAppendThreads) {
-        if (x >= nq + nk) {  // values
-            const int y = x - nq - nk, h = y / NC, c = y % NC;
-            if (base >= 0)
-                *reinterpret_cast<uint4*>(p.w.v + base + h * head_step + 8 * c) =
-                    *reinterpret_cast<const uint4*>(p.v + row * p.ldv + (long long)h * D + 8 * c);
-            continue;
+    const long long base = base_s, head_step = (long long)p.w.div.d * D;
+    const auto finish = [&](const Item& t, uint4 a, const uint4& b) {
+        uint16_t* dst = t.kind == 0   ? p.q_out + row * p.ldqo + (long long)t.h * D
+                        : t.kind == 1 ? p.w.k + base + t.h * head_step
+                                      : p.w.v + base + t.h * head_step;
+        if (t.kind != 0 && base < 0) return;
+        if (t.kind == 2) {
+            *reinterpret_cast<uint4*>(dst + 8 * t.c) = a;
+            return;
         }
-        const bool isq = x < nq;
-        const int y = isq ? x : x - nq;
-        const int h = y / per, c = y - h * per;
-        const uint16_t* src = isq ? p.q + row * p.ldq + (long long)h * D : p.k + row * p.ldk + (long long)h * D;
-        uint16_t* dst = isq ? p.q_out + row * p.ldqo + (long long)h * D : p.w.k + base + h * head_step;
-        const bool store = isq || base >= 0;
+        uint32_t wa[4] = {a.x, a.y, a.z, a.w};
         if constexpr (kPairs == 1) {
-            if (c >= rc) {  // behind the rotated part
-                const int e = c + rc;
-                const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * e);
-                if (store) *reinterpret_cast<uint4*>(dst + 8 * e) = a;
-                continue;
+            if (t.c >= rc) {  // behind the rotated part
+                *reinterpret_cast<uint4*>(dst + 8 * (t.c + rc)) = a;
+                return;
             }
-            const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * c);
-            const uint4 b = *reinterpret_cast<const uint4*>(src + 8 * (c + rc));
-            const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+            const uint32_t wb[4] = {b.x, b.y, b.z, b.w};
             uint32_t oa[4], ob[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float4 t = *reinterpret_cast<const float4*>(&cs[8 * c + 2 * e]);
-                const float a0 = h2f(wa[e], 0), a1 = h2f(wa[e], 1), b0 = h2f(wb[e], 0), b1 = h2f(wb[e], 1);
-                oa[e] = pack2(a0 * t.x - b0 * t.y, a1 * t.z - b1 * t.w);
-                ob[e] = pack2(b0 * t.x + a0 * t.y, b1 * t.z + a1 * t.w);
+                const float4 r = *reinterpret_cast<const float4*>(&cs[8 * t.c + 2 * e]);
+                const float x0 = h2f(wa[e], 0), x1 = h2f(wa[e], 1), y0 = h2f(wb[e], 0), y1 = h2f(wb[e], 1);
+                oa[e] = pack2(x0 * r.x - y0 * r.y, x1 * r.z - y1 * r.w);
+                ob[e] = pack2(y0 * r.x + x0 * r.y, y1 * r.z + x1 * r.w);
             }
-            if (store) {
-                *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-                *reinterpret_cast<uint4*>(dst + 8 * (c + rc)) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
-            }
+            *reinterpret_cast<uint4*>(dst + 8 * t.c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+            *reinterpret_cast<uint4*>(dst + 8 * (t.c + rc)) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
         } else if constexpr (kPairs == 0) {
-            const uint4 a = *reinterpret_cast<const uint4*>(src + 8 * c);
-            uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = 4 * c + e;  // pair
+                const int i = 4 * t.c + e;  // pair
                 if (i < half) {
-                    const float2 t = cs[i];
-                    const float x0 = h2f(w[e], 0), x1 = h2f(w[e], 1);
-                    w[e] = pack2(x0 * t.x - x1 * t.y, x1 * t.x + x0 * t.y);
+                    const float2 r = cs[i];
+                    const float x = h2f(wa[e], 0), y = h2f(wa[e], 1);
+                    wa[e] = pack2(x * r.x - y * r.y, y * r.x + x * r.y);
                 }
             }
-            if (store) *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + 8 * t.c) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
         } else {
             // pairs (i, i + half) cross the chunks; in place (q_out == q) a
-            // thread must own both elements of a pair, so the items are pairs
-            // here: 8 c .. 8 c + 7 of the first half, then the rest copied
-            for (int i = c; i < half; i += NC) {
-                const float a = __half2float(__ushort_as_half(src[i]));
-                const float b = __half2float(__ushort_as_half(src[i + half]));
-                const float2 t = cs[i];
-                if (store) {
-                    dst[i] = __half_as_ushort(__float2half_rn(a * t.x - b * t.y));
-                    dst[i + half] = __half_as_ushort(__float2half_rn(b * t.x + a * t.y));
-                }
+            // thread must own both elements of a pair, so an item is every
+            // NC-th pair here, and every NC-th element behind them
+            const uint16_t* src = source(t);
+            for (int i = t.c; i < half; i += NC) {
+                const float x = __half2float(__ushort_as_half(src[i]));
+                const float y = __half2float(__ushort_as_half(src[i + half]));
+                const float2 r = cs[i];
+                dst[i] = __half_as_ushort(__float2half_rn(x * r.x - y * r.y));
+                dst[i + half] = __half_as_ushort(__float2half_rn(y * r.x + x * r.y));
             }
-            for (int i = p.rot + c; i < D; i += NC) {
-                const uint16_t a = src[i];
-                if (store) dst[i] = a;
-            }
+            for (int i = p.rot + t.c; i < D; i += NC) dst[i] = src[i];
         }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (tid + i * kAppendThreads < items) finish(item(tid + i * kAppendThreads), a0[i], b0[i]);
+    for (int x = tid + kAhead * kAppendThreads; x < items; x += kAppendThreads) {
+        const Item t = item(x);
+        uint4 a = {}, b = {};
+        fetch(t, a, b);
+        finish(t, a, b);
     }
 }
 

@@ -81,8 +81,8 @@ __device__ __forceinline__ int tile_cost(const Args& a, const Seq& q, int rb) {
 }
 
 // Units of one head of a sequence (all row blocks).
-__device__ __forceinline__ unsigned head_units(const Args& a, const Seq& q) {
-    unsigned t = 0;
+__device__ __forceinline__ unsigned long long head_units(const Args& a, const Seq& q) {
+    unsigned long long t = 0;
 #pragma unroll 1
     for (int b = 0; b * a.BM < q.n * a.G; b += 4)
 #pragma unroll
@@ -112,7 +112,7 @@ __device__ __noinline__ unsigned line_scan(const Args& a, unsigned* sums, int th
         bool bad;
         const Seq q = q4p::seq_of(a.w, s, bad);
         if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
-        t += (unsigned long long)head_units(a, q) * a.w.H;
+        t += head_units(a, q) * a.w.H;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll 1
@@ -164,7 +164,7 @@ __device__ __noinline__ Place line_find(const Args& a, const unsigned* sums, int
 #pragma unroll 1
         while (true) {
             p.q = q4p::seq_of(a.w, p.s, bad);
-            head = head_units(a, p.q);
+            head = (unsigned)head_units(a, p.q);
             if (rest < head * (unsigned)a.w.H) break;  // (below 2^31: the line is)
             rest -= head * (unsigned)a.w.H;
             ++p.s;

@@ -660,7 +660,9 @@ q4_status q4_paged_append(const q4_paged_append_desc *desc, q4_stream_t stream);
  * zeros.  What a row does not see never reaches it, NaN and infinities
  * included.  q and out: fp16 [rows][n_q_heads * head_dim], strides as in 7b,
  * 16-byte aligned; they must not overlap.  The workspace is written and read
- * by the call's kernels; calls that can overlap need one each. */
+ * by the call's kernels; calls that can overlap need one each.  A call of
+ * 2^31 or more units of work (eighths of 64 positions by the rows of a job;
+ * some 10^15 operations) computes nothing and latches Q4_ERR_DEVICE_CHECK. */
 typedef struct q4_tree_attention_desc {
     q4_paged_cache cache;
     const int32_t *ctx_len, *row_start;
@@ -730,7 +732,7 @@ q4_status q4_tree_accept(const q4_tree_accept_desc *desc, q4_stream_t stream);
 typedef struct q4_sample_desc {
     const void *logits;       /* [rows][vocab] of `dtype`, rows ld elements apart */
     q4_dtype dtype;
-    int rows, vocab;          /* rows >= 0, 1 <= vocab <= 2^19 */
+    int rows, vocab;          /* 0 <= rows <= 2^26, 1 <= vocab <= 2^19 */
     int ld;                   /* 0 = vocab */
     const float *temperature; /* [rows]; not above 0: the greatest logit; NULL = 1 for every row */
     const int32_t *top_k;     /* [rows]; below 1: no limit; NULL = no limit */
