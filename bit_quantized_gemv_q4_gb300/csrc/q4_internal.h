@@ -50,6 +50,17 @@ inline cudaError_t ensure_smem_attr(const void* kern, std::atomic<int>* marks, i
     return cudaSuccess;
 }
 
+// Likewise the permission to launch clusters of more than 8 CTAs.
+inline cudaError_t ensure_wide_clusters(const void* kern, std::atomic<int>* done) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const bool tracked = dev >= 0 && dev < 64;
+    if (tracked && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && tracked) done[dev].store(1, std::memory_order_release);
+    return e;
+}
+
 // 2-D tensor map (q4_moe_gemm.cu): `inner` x `outer` elements of type dt,
 // rows `row_bytes` apart, copied in boxes of box_inner x box_outer.
 q4_status make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,

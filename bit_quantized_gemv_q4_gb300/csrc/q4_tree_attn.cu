@@ -24,6 +24,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "q4_paged.cuh"
 #include "q4_tc.cuh"
 
@@ -56,6 +58,7 @@ struct Args {
     int BM, KT;  // rows of a job, positions of a tile (1 << KT_log2)
     int KT_log2;
     int cost_full, cost_half;  // units of a tile for a row block with more than BM / 2 rows, and for others
+    int lead;                  // units of a job before its first tile
     float* po;   // workspace: [2 CTAs][BM][D] outputs
     float2* pml; // [2 CTAs][BM] (m, l)
 };
@@ -87,7 +90,7 @@ __device__ __forceinline__ unsigned long long head_units(const Args& a, const Se
     for (int b = 0; b * a.BM < q.n * a.G; b += 4)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if ((b + e) * a.BM < q.n * a.G) t += (unsigned)(block_tiles(a, q, b + e) * tile_cost(a, q, b + e));
+            if ((b + e) * a.BM < q.n * a.G) t += (unsigned)(a.lead + block_tiles(a, q, b + e) * tile_cost(a, q, b + e));
     return t;
 }
 
@@ -136,10 +139,11 @@ __device__ __noinline__ unsigned line_scan(const Args& a, unsigned* sums, int th
 }
 
 // A CTA's share of the line (CTA c: units c * share ..): a tile belongs to the
-// CTA in whose share its first unit lies.  At least a tile, so that a CTA
-// between two others of a job has a part of it.
+// CTA in whose share its first unit lies.  At least two tiles: one, so that a
+// CTA between two others of a job has a part of it, and another, as fewer
+// parts join faster (one user's 2000 positions: 14.3 -> 11.6 us).
 __device__ __forceinline__ unsigned line_share(const Args& a, unsigned line) {
-    return max((line + (unsigned)a.ctas - 1) / (unsigned)a.ctas, (unsigned)a.cost_full);
+    return max((line + (unsigned)a.ctas - 1) / (unsigned)a.ctas, 2u * (unsigned)a.cost_full);
 }
 
 // The job that holds unit x (x < the line's length), from its first tile on.
@@ -176,17 +180,17 @@ __device__ __noinline__ Place line_find(const Args& a, const unsigned* sums, int
     for (p.rb = 0;; ++p.rb) {
         p.tiles = block_tiles(a, p.q, p.rb);
         p.cost = tile_cost(a, p.q, p.rb);
-        if (rest < (unsigned)(p.tiles * p.cost)) break;
-        rest -= (unsigned)(p.tiles * p.cost);
+        if (rest < (unsigned)(a.lead + p.tiles * p.cost)) break;
+        rest -= (unsigned)(a.lead + p.tiles * p.cost);
     }
-    p.start = x - rest;
+    p.start = x - rest + a.lead;
     p.tile = 0;
     return p;
 }
 
 // The next job (there is one).
 __device__ __forceinline__ void next_job(const Args& a, Place& p) {
-    p.start += (unsigned)(p.tiles * p.cost);
+    p.start += (unsigned)(p.tiles * p.cost + a.lead);
     p.tile = 0;
     if (++p.rb * a.BM >= p.q.n * a.G) {
         p.rb = 0;
@@ -222,13 +226,14 @@ struct Walk {
         p = line_find(a, sums, threads, x0);
         p.tile = tile_at(p, x0);
         if (p.tile == p.tiles) {  // x0 lies in the last tile's units
-            if (!more()) return false;
+            if (!more(a)) return false;
             next_job(a, p);
         }
         end = tile_at(p, x1);
-        return true;
+        return p.tile < end;  // (the part may lie in what leads a job)
     }
-    __device__ __forceinline__ bool more() const { return p.start + (unsigned)(p.tiles * p.cost) < x1; }
+    // whether the next job's first tile lies in the part (the line's end has none behind it)
+    __device__ __forceinline__ bool more(const Args& a) const { return p.start + (unsigned)(p.tiles * p.cost + a.lead) < x1; }
     __device__ __forceinline__ void next(const Args& a) {
         next_job(a, p);
         end = tile_at(p, x1);
@@ -321,11 +326,11 @@ __device__ __noinline__ void add_odd(const Args& a, const Place& p, int T, int t
 // column g; an accumulator rows g, g + 8, columns 2u, 2u+1, so two
 // neighbouring score tiles are the A operand of a 16-position step of P V.
 //
-// kCluster: few jobs (one or two users' decoding), where latency counts.  The
-// 16 CTAs of a cluster take a job's tiles together and join their parts
-// through distributed shared memory: one launch, and no line to walk.
-constexpr int kCluster = 16;
+// kClustered: few jobs (a few users' decoding), where latency counts.  The
+// CTAs of a cluster take a job's tiles together and join their parts through
+// distributed shared memory: one launch, and no line to walk.
 constexpr int kConsumers = 128, kThreads = 160;
+constexpr int kRingCost = 4, kRingLead = 16;  // units of a tile, and of a job before its tiles
 
 template <int D>
 struct Ring {
@@ -355,8 +360,50 @@ struct MapArgs {
     Args a;
     int box;       // rows per TMA box
     int zero_row;  // a row outside the maps
-    int blocks;    // kCluster: row blocks per sequence (at most)
+    int cluster, cluster_log2;  // CTAs per job: 4, 8 or 16 (0: the line)
 };
+
+// Sequence and row block of the call's block-th row block, false if there are
+// fewer: a warp looks through 32 sequences at a time.
+__device__ __forceinline__ bool find_block(const Args& a, int block, Place& p) {
+    const int lane = threadIdx.x & 31;
+    if (a.w.S == 1) {  // (one user's token: 0.3 us)
+        bool bad;
+        p.s = 0;
+        p.rb = block;
+        p.q = q4p::seq_of(a.w, 0, bad);
+        if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
+        return block * a.BM < p.q.n * a.G;
+    }
+#pragma unroll 1
+    for (int s0 = 0; s0 < a.w.S; s0 += 32) {
+        Seq q = {0, 0, 0};
+        if (s0 + lane < a.w.S) {
+            bool bad;
+            q = q4p::seq_of(a.w, s0 + lane, bad);
+            if (bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(a.w.err, q4d::kErrDeviceCheck);
+        }
+        const int own = q.n > 0 ? (q.n * a.G + a.BM - 1) / a.BM : 0;
+        int sum = own;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, x);
+            if (lane >= x) sum += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, block < sum);
+        if (past) {
+            const int from = __ffs((int)past) - 1;
+            p.s = s0 + from;
+            p.rb = block - __shfl_sync(0xffffffffu, sum - own, from);
+            p.q.start = __shfl_sync(0xffffffffu, q.start, from);
+            p.q.n = __shfl_sync(0xffffffffu, q.n, from);
+            p.q.ctx = __shfl_sync(0xffffffffu, q.ctx, from);
+            return true;
+        }
+        block -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return false;
+}
 
 template <int D, int WM, bool kTma, bool kClustered>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -387,19 +434,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool any;
     int rank = 0;
     if constexpr (kClustered) {
-        const int job = blockIdx.x / kCluster;
-        rank = blockIdx.x % kCluster;
-        bool bad;
+        const int job = (int)(blockIdx.x >> t.cluster_log2);
+        rank = (int)blockIdx.x & (t.cluster - 1);
         Place& p = w.p;
-        p.s = job / (a.w.H * t.blocks);
-        p.h = job / t.blocks % a.w.H;
-        p.rb = job % t.blocks;
-        p.q = q4p::seq_of(a.w, p.s, bad);
-        if (bad && rank == 0 && tid == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
-        if (p.rb * BM >= p.q.n * a.G) return;  // (the whole cluster)
+        p.h = job % a.w.H;
+        if (!find_block(a, job / a.w.H, p)) return;  // (the whole cluster)
         p.tiles = block_tiles(a, p.q, p.rb);
-        p.tile = (int)((unsigned)(p.tiles * rank) / kCluster);  // tiles * 16 stays below 2^31
-        w.end = (int)((unsigned)(p.tiles * (rank + 1)) / kCluster);
+        p.tile = (int)((unsigned)(p.tiles * rank) >> t.cluster_log2);  // tiles * 16 stays below 2^31
+        w.end = (int)((unsigned)(p.tiles * (rank + 1)) >> t.cluster_log2);
         p.cost = 1;
         p.start = 0;
         w.x1 = 0;  // no more segments
@@ -472,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
                 }
             }
-            rest = w.more();
+            rest = w.more(a);
             if (rest && ok) w.next(a);
         }
         if constexpr (!kTma) asm volatile("cp.async.wait_all;" ::: "memory");
@@ -723,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.empty[st]));
         ++kt;
         if (++p.tile == w.end) {
-            if (!w.more()) break;
+            if (!w.more(a)) break;
             w.next(a);
         }
     }
@@ -738,11 +780,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         __syncwarp();
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();
-        const int r = rank * 4 + warp;  // a warp per row, the rows spread over the CTAs (BM <= 64)
-        if (warp < 4 && r < R) {
+        // a warp per row, the rows spread over the CTAs
+        for (int r = rank * 4 + warp; warp < 4 && r < R; r += 4 * t.cluster) {
             float2 ml = make_float2(-INFINITY, 0.f);
             bool odd = false;
-            if (lane < kCluster) {
+            if (lane < t.cluster) {
                 ml = *cl.map_shared_rank(&fin_s[r], lane);
                 odd = *cl.map_shared_rank(const_cast<int*>(&B.odd[0]), lane) != 0;
             }
@@ -750,29 +792,35 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
             const float f = ex2(ml.x - (mm == -INFINITY ? 0.f : mm));
-            float ls = lane < kCluster ? ml.y * f : 0.f;
+            float ls = lane < t.cluster ? ml.y * f : 0.f;
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
             constexpr int E = D / 32;
-            float v[kCluster][E];
-#pragma unroll
-            for (int i = 0; i < kCluster; ++i) {
-                const float* src = cl.map_shared_rank(ob + (size_t)r * D + E * lane, i);
-                if constexpr (E == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(src);
-                    v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2*>(src);
-                    v[i][0] = x.x, v[i][1] = x.y;
-                }
-            }
             float acc[E] = {};
+            const auto add = [&](auto size) {  // (all parts' loads in flight together)
+                constexpr int N = decltype(size)::value;
+                float v[N][E];
 #pragma unroll
-            for (int i = 0; i < kCluster; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
+                for (int i = 0; i < N; ++i) {
+                    const float* src = cl.map_shared_rank(ob + (size_t)r * D + E * lane, i);
+                    if constexpr (E == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(src);
+                        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(src);
+                        v[i][0] = x.x, v[i][1] = x.y;
+                    }
+                }
 #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], fi, acc[e]);
-            }
+                for (int i = 0; i < N; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(v[i][e], fi, acc[e]);
+                }
+            };
+            if (t.cluster == 16) add(std::integral_constant<int, 16>{});
+            else if (t.cluster == 8) add(std::integral_constant<int, 8>{});
+            else add(std::integral_constant<int, 4>{});
             const float inv = ls == 0.f ? 0.f : 1.f / ls;
             const int rr = p.rb * BM + r, tok = (int)q4p::page_of(a.by_g, rr);
             uint16_t* out = a.out + (size_t)(p.q.start + tok) * a.ldo + (size_t)(p.h * a.G + rr - tok * a.G) * D;
@@ -793,12 +841,99 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the parts of the jobs that several CTAs shared.  Block b looks at the
-// border between CTAs b and b + 1; it works if its job has begun in CTA b.  A warp per row; a lane holds (m, l) of every 32nd part, so the
-// loads are in flight together.
+// border between CTAs b and b + 1; it works if its job has begun in CTA b.  A
+// warp takes kRows rows and kParts parts at a time, whose loads are in flight
+// together; a lane holds (m, l) of every 32nd part.
 constexpr int kJoinThreads = 256;
 
+template <int D, int kRows, int kParts>
+__device__ __forceinline__ void join_rows(const Args& a, const Place& p, int b, int last) {
+    static_assert(32 % kParts == 0, "");
+    constexpr int E = D / 32, kWarps = kJoinThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM);
+    // CTA b has the job's beginning (slot 2 b + 1), later CTAs their slot 2 c
+    const auto slot_of = [&](int c) { return 2 * c + (c == b); };
+    for (int r0 = (blockIdx.y * kWarps + warp) * kRows; r0 < rows; r0 += gridDim.y * kWarps * kRows) {
+        float m[kRows], l[kRows], f[kRows], o[kRows][E];
+        float2 ml[kRows];
+        const auto load_ml = [&](int c, int i) {  // of this lane's part
+            return c + lane <= last && r0 + i < rows ? part_ml(a, slot_of(c + lane))[r0 + i] : make_float2(-INFINITY, 0.f);
+        };
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            ml[i] = load_ml(b, i);
+            m[i] = ml[i].x;
+            l[i] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[i][e] = 0.f;
+        }
+        for (int c = b; c <= last; c += kParts) {
+            float v[kParts][kRows][E];
+#pragma unroll
+            for (int j = 0; j < kParts; ++j) {
+                const float* src = part_o<D>(a, slot_of(c + j)) + (size_t)r0 * D + E * lane;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    if (c + j > last || r0 + i >= rows) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) v[j][i][e] = 0.f;
+                    } else if constexpr (E == 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(src + i * D);
+                        v[j][i][0] = t.x, v[j][i][1] = t.y, v[j][i][2] = t.z, v[j][i][3] = t.w;
+                    } else {
+                        const float2 t = *reinterpret_cast<const float2*>(src + i * D);
+                        v[j][i][0] = t.x, v[j][i][1] = t.y;
+                    }
+                }
+            }
+            if (c == b) {  // (with the first parts' rows on their way)
+                for (int y = b + 32; y <= last; y += 32)
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) m[i] = fmaxf(m[i], load_ml(y, i).x);
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+                    for (int s = 16; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
+                    if (m[i] == -INFINITY) m[i] = 0.f;
+                }
+            }
+            if (((c - b) & 31) == 0) {
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    if (c > b) ml[i] = load_ml(c, i);  // (read again)
+                    f[i] = ex2(ml[i].x - m[i]);
+                    l[i] = fmaf(ml[i].y, f[i], l[i]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kParts; ++j)
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f[i], (c - b + j) & 31);  // 0 behind the last part
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[i][e] = fmaf(v[j][i][e], fi, o[i][e]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (r0 + i >= rows) break;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+            const int rr = p.rb * a.BM + r0 + i, tok = (int)q4p::page_of(a.by_g, rr);
+            uint16_t* dst = a.out + (size_t)(p.q.start + tok) * a.ldo + (size_t)(p.h * a.G + rr - tok * a.G) * D + E * lane;
+            uint32_t w[E / 2];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) w[e / 2] = pack2(o[i][e] * inv, o[i][e + 1] * inv);
+            if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(dst) = w[0];
+        }
+    }
+}
+
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ Args a) {
     __shared__ unsigned sums[kJoinThreads];
     const unsigned line = line_scan(a, sums, kJoinThreads);
     const unsigned share = line_share(a, line), xb = share * blockIdx.x, x = xb + share;
@@ -815,97 +950,9 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     // the attention's end, so blocks without work wait as well)
     q4d::pdl_wait();
     if (!work) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM);
-    // CTA b has the job's beginning (slot 2 b + 1), later CTAs their slot 2 c
     const int last = (int)(last_at / share);  // CTA of the job's last tile
-    const auto slot_of = [&](int c) { return 2 * c + (c == b); };
-    // kIlp rows of a warp at a time: their loads are in flight together
-    constexpr int E = D / 32, kIlp = 2;
-    for (int r0 = (blockIdx.y * (kJoinThreads / 32) + warp) * kIlp; r0 < rows; r0 += gridDim.y * (kJoinThreads / 32) * kIlp) {
-        float m[kIlp], l[kIlp], f[kIlp], o[kIlp][E];
-#pragma unroll
-        for (int i = 0; i < kIlp; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[i][e] = 0.f;
-        }
-        const int parts = last - b + 1;
-        const auto load_o = [&](int c, float (&v)[kIlp][E]) {
-            const float* src = part_o<D>(a, slot_of(c)) + (size_t)r0 * D + E * lane;
-#pragma unroll
-            for (int i = 0; i < kIlp; ++i) {
-                if (r0 + i >= rows) break;
-                if constexpr (E == 4) {
-                    const float4 t = *reinterpret_cast<const float4*>(src + i * D);
-                    v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
-                } else {
-                    const float2 t = *reinterpret_cast<const float2*>(src + i * D);
-                    v[i][0] = t.x, v[i][1] = t.y;
-                }
-            }
-        };
-        // (m, l) of the first 32 parts and the first part's rows are on their
-        // way together; further parts' (m, l) are read again when their turn comes
-        float2 ml[kIlp];
-        float v[kIlp][E], next[kIlp][E];
-#pragma unroll
-        for (int i = 0; i < kIlp; ++i) {
-            ml[i] = make_float2(-INFINITY, 0.f);
-            if (lane < parts && r0 + i < rows) ml[i] = part_ml(a, slot_of(b + lane))[r0 + i];
-        }
-        load_o(b, v);
-        for (int c = b + 32 + lane; c <= last; c += 32)
-#pragma unroll
-            for (int i = 0; i < kIlp; ++i)
-                if (r0 + i < rows) m[i] = fmaxf(m[i], part_ml(a, slot_of(c))[r0 + i].x);
-#pragma unroll
-        for (int i = 0; i < kIlp; ++i) {
-            m[i] = fmaxf(m[i], ml[i].x);
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
-            if (m[i] == -INFINITY) m[i] = 0.f;
-        }
-        for (int c = b; c <= last; ++c) {
-            const int k = (c - b) & 31;
-            if (c < last) load_o(c + 1, next);
-            if (k == 0) {
-#pragma unroll
-                for (int i = 0; i < kIlp; ++i) {
-                    if (c > b) {
-                        ml[i] = make_float2(-INFINITY, 0.f);
-                        if (c + lane <= last && r0 + i < rows) ml[i] = part_ml(a, slot_of(c + lane))[r0 + i];
-                    }
-                    f[i] = ex2(ml[i].x - m[i]);
-                    l[i] = fmaf(ml[i].y, f[i], l[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kIlp; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f[i], k);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (r0 + i < rows) o[i][e] = fmaf(v[i][e], fi, o[i][e]);
-                    v[i][e] = next[i][e];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kIlp; ++i) {
-            if (r0 + i >= rows) break;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
-            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-            const int rr = p.rb * a.BM + r0 + i, tok = (int)q4p::page_of(a.by_g, rr);
-            uint16_t* dst = a.out + (size_t)(p.q.start + tok) * a.ldo + (size_t)(p.h * a.G + rr - tok * a.G) * D + E * lane;
-            uint32_t w[E / 2];
-#pragma unroll
-            for (int e = 0; e < E; e += 2) w[e / 2] = pack2(o[i][e] * inv, o[i][e + 1] * inv);
-            if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t*>(dst) = w[0];
-        }
-    }
+    if (last - b < 4) join_rows<D, 2, 2>(a, p, b, last);
+    else join_rows<D, 1, 8>(a, p, b, last);
 }
 
 // The parts' places in the workspace.
@@ -950,7 +997,7 @@ inline q4_status pool_maps(CUtensorMap* k, CUtensorMap* v, const q4_paged_cache&
 
 template <int D, int WM, bool kTma, bool kClustered>
 cudaError_t launch_kernel(const CUtensorMap& k, const CUtensorMap& v, const MapArgs& t, int grid, cudaStream_t s) {
-    static std::atomic<int> marks[64], wide[64];
+    static std::atomic<int> marks[64];
     const auto kern = tree_attn_kernel<D, WM, kTma, kClustered>;
     const void* fn = reinterpret_cast<const void*>(kern);
     cudaError_t e = q4i::ensure_smem_attr(fn, marks, (int)Ring<D>::kSmem);
@@ -962,19 +1009,31 @@ cudaError_t launch_kernel(const CUtensorMap& k, const CUtensorMap& v, const MapA
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     if (kClustered) {
-        int dev = 0;
-        cudaGetDevice(&dev);
-        if (!wide[dev & 63].load(std::memory_order_acquire)) {
-            if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-            wide[dev & 63].store(1, std::memory_order_release);
+        if (t.cluster > 8) {
+            static std::atomic<int> wide[64];
+            if ((e = q4i::ensure_wide_clusters(fn, wide)) != cudaSuccess) return e;
         }
         at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = kCluster;
+        at[0].val.clusterDim.x = (unsigned)t.cluster;
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
     return cudaLaunchKernelEx(&cfg, kern, k, v, t);
+}
+
+// CTAs of a job's cluster, where the GPU holds all clusters at once (a GB300
+// places 14 of 16 CTAs, 36 of 8 and 74 of 4, two per SM); 0: the line.  us of a
+// token's step, 8 kv heads of 128, clusters / line, contexts up to
+//              100        1000       4000       16000      64000
+//   1 user     7.9 / 9.4  8.1 / 11   10 / 15    21 / 26    54 / 52   (16 CTAs; of 8: 7.0, 7.4, 11, 28, 88)
+//   2 users    7.1 / 9.4  8.7 / 11   13 / 16    31 / 33    94 / 69   (8)
+//   8 users    8.4 / 11   11 / 13    22 / 23    63 / 64   209 / 182  (4)
+// The host sees the contexts' bound alone, the table's width.
+inline int cluster_size(long long jobs, long long positions, int sms) {
+    if (jobs * 16 <= 3 * sms / 2) return 16;
+    if (positions > 8192) return 0;
+    return jobs * 8 <= 2 * sms - 16 ? 8 : jobs * 4 <= 2 * sms - 8 ? 4 : 0;
 }
 
 // box 0: no TMA.
@@ -985,7 +1044,8 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
     a.BM = 16 * WM;
     a.KT = kKeys;
     a.KT_log2 = 6;
-    a.cost_full = a.cost_half = 1;
+    a.cost_full = a.cost_half = kRingCost;
+    a.lead = kRingLead;
     a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
     place_parts<D>(a, workspace);
     if (box) {
@@ -994,17 +1054,17 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
     }
     t.box = box;
     t.zero_row = (int)((long long)c.n_pages * c.n_kv_heads * c.page_size);
-    // Clusters where two CTAs per SM hold all of them.
-    const long long blocks = ((long long)a.w.rows * a.G + a.BM - 1) / a.BM, jobs = blocks * c.n_seqs * c.n_kv_heads;
+    // (n rows in S sequences that have some make at most S + (n - S) / BM blocks)
+    const long long seqs = c.n_seqs < a.w.rows ? c.n_seqs : a.w.rows;
+    const long long jobs = (seqs + ((long long)a.w.rows * a.G - seqs) / a.BM) * c.n_kv_heads;
+    t.cluster = cluster_size(jobs, (long long)c.max_pages * c.page_size, sms);
+    t.cluster_log2 = t.cluster == 16 ? 4 : t.cluster == 8 ? 3 : 2;
+    t.a = a;
     cudaError_t e;
-    if (jobs * kCluster <= 2 * sms) {
-        t.a = a;
-        t.blocks = (int)blocks;
-        e = box ? launch_kernel<D, WM, true, true>(k, v, t, (int)jobs * kCluster, s)
-                : launch_kernel<D, WM, false, true>(k, v, t, (int)jobs * kCluster, s);
+    if (t.cluster) {
+        e = box ? launch_kernel<D, WM, true, true>(k, v, t, (int)jobs * t.cluster, s)
+                : launch_kernel<D, WM, false, true>(k, v, t, (int)jobs * t.cluster, s);
     } else {
-        t.a = a;
-        t.blocks = 0;
         e = box ? launch_kernel<D, WM, true, false>(k, v, t, a.ctas, s) : launch_kernel<D, WM, false, false>(k, v, t, a.ctas, s);
         if (e == cudaSuccess) e = launch_join<D>(a, s);
     }
@@ -1037,6 +1097,7 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1
 constexpr float kTcShift = 7.f;
+constexpr int kTcLead = 32;
 constexpr int kTcCostFull = 8, kTcCostHalf = 5;  // of a tile, with two row streams and with alternate tiles
 
 template <int D>
@@ -1238,7 +1299,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int sl = 0; sl < SLABS; ++sl) q4t::tma_load_2d(dst + sl * 16384, map, 64 * sl, y, fb);
                     }
                 }
-                rest = w.more();
+                rest = w.more(a);
                 if (rest && ok) w.next(a);
             }
             if (!ok) {  // copies still in flight land before the CTA can exit
@@ -1329,7 +1390,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (steps == 0 && leader) q4d::mbar_arrive(q4d::smem_addr(&B.o_full));
                 tiles0 += T;
                 ++seg;
-                rest = w.more();
+                rest = w.more(a);
                 if (rest && ok) w.next(a);
             }
             if (!ok) B.abort = 1;
@@ -1525,7 +1586,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t seg_done = seg;
                 tiles0 += T;
                 ++seg;
-                rest = w.more();
+                rest = w.more(a);
                 if (rest) {
                     w.next(a);
                     put_query(p);
@@ -1630,12 +1691,12 @@ q4_status launch_tc(Args& a, const q4_paged_cache& c, void* workspace, int sms, 
     a.KT = kTcKeys;
     a.KT_log2 = 7;
     a.cost_full = kTcCostFull;
+    a.lead = kTcLead;
     a.cost_half = kTcCostHalf;
     place_parts<D>(a, workspace);
     t.a = a;
     t.box = box;
     t.zero_row = (int)((long long)c.n_pages * c.n_kv_heads * c.page_size);
-    t.blocks = 0;
     CUtensorMap tmK, tmV;
     const q4_status st = pool_maps(&tmK, &tmV, c, (uint32_t)box);
     if (st != Q4_OK) return st;

@@ -312,3 +312,24 @@ def test_no_rows():
         q4.q4_tree_attention(c, b.dctx, b.dstart, rows, torch.zeros_like(out), 1, out, ws, n)
         assert q4.q4_device_status() == 0
     assert bool((out == -5.0).all())
+
+
+# jobs (sequence, kv head, block of rows) around the limits of the launch's forms: 14, 36, 74, and many
+@pytest.mark.parametrize("S,Hkv", [(1, 14), (7, 2), (5, 3), (12, 3), (37, 1), (37, 2), (25, 3), (70, 1), (120, 3)])
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("G,most", [(2, 1), (3, 9)])
+def test_numbers_of_jobs(S, Hkv, wide, G, most):
+    g = np.random.default_rng(S * 100 + Hkv * 10 + most)
+    ctx = [int(x) for x in g.integers(0, 400, S)]
+    n = [int(x) for x in g.integers(0, most + 1, S)]
+    n[-1] = most
+    b = Batch(g, ctx, n, Hkv, 64, 16)
+    if wide:  # a table for long contexts: places without a page
+        b.table = np.pad(b.table, ((0, 0), (0, 9000 // 16 - b.max_pages)), constant_values=-1)
+        b.max_pages = b.table.shape[1]
+    q = rand16(g, b.rows, Hkv * G, 64)
+    sees = seen_by(b, "tree", g)
+    a, A = expected(b, q, sees)
+    out = attend(b, b.to_device(q4), q, "tree", sees)
+    assert q4.q4_device_status() == 0
+    check(out, b, q, a, A)
