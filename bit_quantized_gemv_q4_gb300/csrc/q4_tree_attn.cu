@@ -61,6 +61,7 @@ struct Args {
     int lead;                  // units of a job before its first tile
     float* po;   // workspace: [2 CTAs][BM][D] outputs
     float2* pml; // [2 CTAs][BM] (m, l)
+    int4* rec;   // [CTAs] tcgen05: the job that begins in the CTA and ends in a later one
 };
 
 template <int D>
@@ -840,130 +841,195 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-// Joins the parts of the jobs that several CTAs shared.  Block b looks at the
-// border between CTAs b and b + 1; it works if its job has begun in CTA b.  A
-// warp takes kRows rows and kParts parts at a time, whose loads are in flight
-// together; a lane holds (m, l) of every 32nd part.
-constexpr int kJoinThreads = 256;
+// A job that several CTAs share: first row of its sequence, head, row block,
+// rows, and the CTAs it is in, b ..  parts 0: no such job.
+struct Shared {
+    int start, h, rb, rows, b, parts;
+};
+__device__ __forceinline__ Shared shared_job(const Args& a, const Place& p, unsigned share, int b) {
+    const int last = (int)((p.start + (unsigned)((p.tiles - 1) * p.cost)) / share);  // CTA of the last tile
+    return {p.q.start, p.h, p.rb, (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM), b, last - b + 1};
+}
 
+// Joins the parts of kRows rows of a job.  kRows rows and kParts parts are
+// taken at a time, their loads in flight together; a lane holds (m, l) of
+// every 32nd part.
 template <int D, int kRows, int kParts>
-__device__ __forceinline__ void join_rows(const Args& a, const Place& p, int b, int last) {
+__device__ __forceinline__ void join_rows(const Args& a, const Shared& job, int r0) {
     static_assert(32 % kParts == 0, "");
-    constexpr int E = D / 32, kWarps = kJoinThreads / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = (int)min((long long)a.BM, (long long)p.q.n * a.G - (long long)p.rb * a.BM);
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, rows = job.rows, b = job.b, last = b + job.parts - 1;
     // CTA b has the job's beginning (slot 2 b + 1), later CTAs their slot 2 c
     const auto slot_of = [&](int c) { return 2 * c + (c == b); };
-    for (int r0 = (blockIdx.y * kWarps + warp) * kRows; r0 < rows; r0 += gridDim.y * kWarps * kRows) {
-        float m[kRows], l[kRows], f[kRows], o[kRows][E];
-        float2 ml[kRows];
-        const auto load_ml = [&](int c, int i) {  // of this lane's part
-            return c + lane <= last && r0 + i < rows ? part_ml(a, slot_of(c + lane))[r0 + i] : make_float2(-INFINITY, 0.f);
-        };
+    float m[kRows], l[kRows], f[kRows], o[kRows][E];
+    float2 ml[kRows];
+    const auto load_ml = [&](int c, int i) {  // of this lane's part
+        return c + lane <= last && r0 + i < rows ? part_ml(a, slot_of(c + lane))[r0 + i] : make_float2(-INFINITY, 0.f);
+    };
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            ml[i] = load_ml(b, i);
-            m[i] = ml[i].x;
-            l[i] = 0.f;
+    for (int i = 0; i < kRows; ++i) {
+        ml[i] = load_ml(b, i);
+        m[i] = ml[i].x;
+        l[i] = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[i][e] = 0.f;
-        }
-        for (int c = b; c <= last; c += kParts) {
-            float v[kParts][kRows][E];
+        for (int e = 0; e < E; ++e) o[i][e] = 0.f;
+    }
+    for (int c = b; c <= last; c += kParts) {
+        float v[kParts][kRows][E];
 #pragma unroll
-            for (int j = 0; j < kParts; ++j) {
-                const float* src = part_o<D>(a, slot_of(c + j)) + (size_t)r0 * D + E * lane;
+        for (int j = 0; j < kParts; ++j) {
+            const float* src = part_o<D>(a, slot_of(c + j)) + (size_t)r0 * D + E * lane;
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    if (c + j > last || r0 + i >= rows) {
+            for (int i = 0; i < kRows; ++i) {
+                if (c + j > last || r0 + i >= rows) {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) v[j][i][e] = 0.f;
-                    } else if constexpr (E == 4) {
-                        const float4 t = *reinterpret_cast<const float4*>(src + i * D);
-                        v[j][i][0] = t.x, v[j][i][1] = t.y, v[j][i][2] = t.z, v[j][i][3] = t.w;
-                    } else {
-                        const float2 t = *reinterpret_cast<const float2*>(src + i * D);
-                        v[j][i][0] = t.x, v[j][i][1] = t.y;
-                    }
+                    for (int e = 0; e < E; ++e) v[j][i][e] = 0.f;
+                } else if constexpr (E == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(src + i * D);
+                    v[j][i][0] = t.x, v[j][i][1] = t.y, v[j][i][2] = t.z, v[j][i][3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(src + i * D);
+                    v[j][i][0] = t.x, v[j][i][1] = t.y;
                 }
             }
-            if (c == b) {  // (with the first parts' rows on their way)
-                for (int y = b + 32; y <= last; y += 32)
+        }
+        if (c == b) {  // (with the first parts' rows on their way)
+            for (int y = b + 32; y <= last; y += 32)
 #pragma unroll
-                    for (int i = 0; i < kRows; ++i) m[i] = fmaxf(m[i], load_ml(y, i).x);
+                for (int i = 0; i < kRows; ++i) m[i] = fmaxf(m[i], load_ml(y, i).x);
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
+            for (int i = 0; i < kRows; ++i) {
 #pragma unroll
-                    for (int s = 16; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
-                    if (m[i] == -INFINITY) m[i] = 0.f;
-                }
+                for (int s = 16; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
+                if (m[i] == -INFINITY) m[i] = 0.f;
             }
-            if (((c - b) & 31) == 0) {
+        }
+        if (((c - b) & 31) == 0) {
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    if (c > b) ml[i] = load_ml(c, i);  // (read again)
-                    f[i] = ex2(ml[i].x - m[i]);
-                    l[i] = fmaf(ml[i].y, f[i], l[i]);
-                }
+            for (int i = 0; i < kRows; ++i) {
+                if (c > b) ml[i] = load_ml(c, i);  // (read again)
+                f[i] = ex2(ml[i].x - m[i]);
+                l[i] = fmaf(ml[i].y, f[i], l[i]);
             }
-#pragma unroll
-            for (int j = 0; j < kParts; ++j)
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    const float fi = __shfl_sync(0xffffffffu, f[i], (c - b + j) & 31);  // 0 behind the last part
-#pragma unroll
-                    for (int e = 0; e < E; ++e) o[i][e] = fmaf(v[j][i][e], fi, o[i][e]);
-                }
         }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (r0 + i >= rows) break;
+        for (int j = 0; j < kParts; ++j)
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
-            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-            const int rr = p.rb * a.BM + r0 + i, tok = (int)q4p::page_of(a.by_g, rr);
-            uint16_t* dst = a.out + (size_t)(p.q.start + tok) * a.ldo + (size_t)(p.h * a.G + rr - tok * a.G) * D + E * lane;
-            uint32_t w[E / 2];
+            for (int i = 0; i < kRows; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f[i], (c - b + j) & 31);  // 0 behind the last part
 #pragma unroll
-            for (int e = 0; e < E; e += 2) w[e / 2] = pack2(o[i][e] * inv, o[i][e + 1] * inv);
-            if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t*>(dst) = w[0];
-        }
+                for (int e = 0; e < E; ++e) o[i][e] = fmaf(v[j][i][e], fi, o[i][e]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if (r0 + i >= rows) break;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        const int rr = job.rb * a.BM + r0 + i, tok = (int)q4p::page_of(a.by_g, rr);
+        uint16_t* dst = a.out + (size_t)(job.start + tok) * a.ldo + (size_t)(job.h * a.G + rr - tok * a.G) * D + E * lane;
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) w[e / 2] = pack2(o[i][e] * inv, o[i][e + 1] * inv);
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t*>(dst) = w[0];
     }
 }
 
+// Two rows at a time where there are few parts, else one.
+constexpr int kFewParts = 8;
+__device__ __forceinline__ int join_items(const Shared& job) {
+    return job.parts == 0 ? 0 : job.parts <= kFewParts ? (job.rows + 1) / 2 : job.rows;
+}
+template <int D>
+__device__ __forceinline__ void join_item(const Args& a, const Shared& job, int i) {
+    if (job.parts <= kFewParts) join_rows<D, 2, 2>(a, job, 2 * i);
+    else join_rows<D, 1, 8>(a, job, i);
+}
+
+constexpr int kJoinThreads = 256;
+
+// Behind the ring's kernel, where a job has few rows: block b looks at the
+// border behind CTA b, for a job that has begun there, while the attention's
+// last CTAs run.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ Args a) {
     __shared__ unsigned sums[kJoinThreads];
     const unsigned line = line_scan(a, sums, kJoinThreads);
     const unsigned share = line_share(a, line), xb = share * blockIdx.x, x = xb + share;
-    const int b = blockIdx.x;
-    Place p;
-    unsigned last_at = 0;  // the job's last tile's place
-    bool work = x < line;
-    if (work) {
-        p = line_find(a, sums, kJoinThreads, x);
-        last_at = p.start + (unsigned)((p.tiles - 1) * p.cost);
-        work = p.start >= xb && p.start < x && last_at >= x;  // begun in CTA b, not ended there
+    Shared job = {};
+    if (x < line) {
+        const Place p = line_find(a, sums, kJoinThreads, x);
+        // begun in CTA b, not ended there
+        if (p.start >= xb && p.start < x && p.start + (unsigned)((p.tiles - 1) * p.cost) >= x)
+            job = shared_job(a, p, share, blockIdx.x);
     }
     // the parts are written (and no grid that follows this one starts before
     // the attention's end, so blocks without work wait as well)
     q4d::pdl_wait();
-    if (!work) return;
-    const int last = (int)(last_at / share);  // CTA of the job's last tile
-    if (last - b < 4) join_rows<D, 2, 2>(a, p, b, last);
-    else join_rows<D, 1, 8>(a, p, b, last);
+    const int items = join_items(job);
+    for (int i = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); i < items; i += gridDim.y * (kJoinThreads / 32))
+        join_item<D>(a, job, i);
+}
+
+// Behind the tcgen05 kernel, where a job has up to 256 rows: CTAs leave records
+// of the jobs they begin, every block counts all records' items, and the warps
+// of the grid share them.  (One user's 61 x 4 rows, 4000 positions: 29 us, with
+// the other kernel 36; that one's 4 users, tokens, 24 us, with this one 26: the
+// records are read when the attention has ended.)
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads, 4) tree_join_many_kernel(const __grid_constant__ Args a) {
+    constexpr int kWarps = kJoinThreads / 32;
+    static_assert(kMaxTcCtas <= kJoinThreads, "a record per thread");
+    __shared__ int before[kJoinThreads];  // items of the records before
+    __shared__ int wsum[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    q4d::pdl_wait();
+    const auto read = [&](int b) {
+        const int4 r = a.rec[b];
+        return Shared{r.x, r.y, r.z, r.w & 0xffff, b, r.w >> 16};
+    };
+    const int items = tid < a.ctas ? join_items(read(tid)) : 0;
+    int run = items;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, run, x);
+        if (lane >= x) run += y;
+    }
+    if (lane == 31) wsum[warp] = run;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) run += wsum[i];
+        all += wsum[i];
+    }
+    before[tid] = run - items;
+    __syncthreads();
+    for (int i = blockIdx.x * kWarps + warp; i < all; i += gridDim.x * kWarps) {
+        int b = 0;  // the last record with before[b] <= i
+#pragma unroll
+        for (int x = kJoinThreads / 2; x > 0; x >>= 1)
+            if (before[b + x] <= i) b += x;
+        join_item<D>(a, read(b), i - before[b]);
+    }
+}
+__device__ __forceinline__ void write_record(const Args& a, const Place& p, unsigned share) {
+    const Shared j = shared_job(a, p, share, blockIdx.x);
+    a.rec[blockIdx.x] = make_int4(j.start, j.h, j.rb, j.rows | j.parts << 16);
 }
 
 // The parts' places in the workspace.
 template <int D>
 size_t parts_bytes(int ctas, int BM) {
-    return (size_t)2 * ctas * BM * (D + 2) * 4;
+    return (size_t)2 * ctas * BM * (D + 2) * 4 + (size_t)ctas * sizeof(int4);
 }
 template <int D>
 void place_parts(Args& a, void* workspace) {
     a.po = static_cast<float*>(workspace);
     a.pml = reinterpret_cast<float2*>(a.po + (size_t)2 * a.ctas * a.BM * D);
+    a.rec = reinterpret_cast<int4*>(a.pml + (size_t)2 * a.ctas * a.BM);
 }
 template <int D>
 size_t workspace_bytes() {
@@ -972,11 +1038,10 @@ size_t workspace_bytes() {
 }
 
 // The joining kernel starts while the attention's last CTAs run (programmatic
-// dependent launch) and has its place in the line by the time they end.
-template <int D>
-cudaError_t launch_join(const Args& a, cudaStream_t s) {
+// dependent launch).
+inline cudaError_t launch_join(void (*kern)(Args), dim3 grid, const Args& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.ctas - 1, (unsigned)(a.BM / 64 > 1 ? a.BM / 64 : 1));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -984,7 +1049,7 @@ cudaError_t launch_join(const Args& a, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 // The pools as 2-D maps [rows][D], boxes of 64 x box elements.
@@ -1066,7 +1131,7 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
                 : launch_kernel<D, WM, false, true>(k, v, t, (int)jobs * t.cluster, s);
     } else {
         e = box ? launch_kernel<D, WM, true, false>(k, v, t, a.ctas, s) : launch_kernel<D, WM, false, false>(k, v, t, a.ctas, s);
-        if (e == cudaSuccess) e = launch_join<D>(a, s);
+        if (e == cudaSuccess) e = launch_join(tree_join_kernel<D>, dim3((unsigned)a.ctas - 1, (unsigned)WM), a, s);
     }
     return e == cudaSuccess ? Q4_OK : q4i::cuda_fail(e, "q4_tree_attention launch");
 }
@@ -1213,7 +1278,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t kColS = 0, kColO = 256;
     const Args& a = t.a;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    __shared__ unsigned sums[2 * 256];  // kTcThreads running sums; later (m, l) of both streams' rows
+    __shared__ unsigned share_s;
+    __shared__ __align__(16) unsigned sums[2 * 256];  // kTcThreads running sums; later (m, l) of both streams' rows, float2
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* q_s = base;                              // two tiles; between segments, stream 1's O (fp32)
     uint8_t* k_s = base + 2 * kTile;
@@ -1257,6 +1323,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     q4t::fence_after();
     q4d::pdl_trigger();
     const uint32_t tmem = B.tmem_base;
+
+    if (tid == 0) {  // (the thread that may write a record later)
+        a.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
+        share_s = line_share(a, line);
+    }
 
     Walk w;
     if (w.begin(a, sums, kTcThreads, line)) {
@@ -1592,6 +1663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     put_query(p);
                 }
                 const bool job_begin = done.tile == 0, whole = job_begin && done.tile + T == done.tiles;
+                if (tid == 0 && job_begin && !whole) write_record(a, done, share_s);
                 // Of a job on alternate tiles every thread has half the row's
                 // columns, of both streams' parts.
                 const bool join = !two && T > 1;
@@ -1706,7 +1778,7 @@ q4_status launch_tc(Args& a, const q4_paged_cache& c, void* workspace, int sms, 
         tree_attn_tc_kernel<D><<<a.ctas, kTcThreads, TcShape<D>::kSmem, s>>>(tmK, tmV, t);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess) e = launch_join<D>(a, s);
+    if (e == cudaSuccess) e = launch_join(tree_join_many_kernel<D>, dim3((unsigned)(4 * sms)), a, s);
     return e == cudaSuccess ? Q4_OK : q4i::cuda_fail(e, "q4_tree_attention launch");
 }
 
