@@ -16,8 +16,8 @@
 // exponential's 2^-23 would move the borders of the tail's tokens, which are
 // narrower than that.
 //
-// GB300 design: a cluster of up to 16 CTAs per row, so that one row alone
-// still uses 16 SMs; the CTAs' tops, sums and lists meet in distributed shared
+// GB300 design: a cluster of up to 8 CTAs per row, so that one row alone
+// still uses 8 SMs; the CTAs' tops, sums and lists meet in distributed shared
 // memory and the whole call is one launch.  The row comes from memory once and
 // from L2 after that:
 //   1. the greatest logit (and each thread's own greatest);
@@ -48,8 +48,8 @@ using u64 = unsigned long long;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxVocab = 1 << 19;
-constexpr int kMaxCluster = 16;
-constexpr int kWanted = 160;         // tokens the list aims at without top_k
+constexpr int kMaxCluster = 8;
+constexpr int kWanted = 96;          // tokens the list aims at without top_k
 constexpr int kMostK = 1024;         // top_k up to which the list is tried
 constexpr int kList = 1024;          // tokens of a CTA's list
 constexpr int kAll = 2048;           // tokens of the joined list
@@ -956,21 +956,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 template <bool HALF>
 cudaError_t launch(Args& a, int rows, int sms, cudaStream_t stream) {
-    // As many CTAs per row as two per SM allow, each with at least 1024 tokens
-    // and at most kMostPart.  16 CTAs need the non-portable cluster size.
+    // As many CTAs per row as the GPU holds for all rows at once (a GB300
+    // places 36 clusters of 8 CTAs, 74 of 4, 152 of 2), each with at least 2048
+    // tokens and at most kMostPart.  us of rows x 151936 with top_k 50, at 8 / 4 /
+    // 2 CTAs: 1 row 13.6 / 14.8 / -, 36 rows 17.7 / 16.3 / -; of 61 rows with
+    // every setting in turn at 8 / 4 / 2: - / 54 / 63, at 16 rows 34 / 38 / -.
+    // Clusters that wait for others cost more than they bring: 16 rows at 16 CTAs
+    // 44, at 8 34.  One row of 8000 is as fast with 2 (9.0) as with 4 (10.9).
+    const auto held = [&](int x) { return x > 2 ? 2 * sms - 2 * x : 2 * sms; };
     int c = kMaxCluster;
-    while (c > 1 && ((long long)rows * c > 2 * sms || a.vocab <= 1024 * c) && a.vocab <= kMostPart * (c / 2)) c /= 2;
+    while (c > 1 && ((long long)rows * c > held(c) || a.vocab <= 2048 * c) && a.vocab <= kMostPart * (c / 2)) c /= 2;
     a.cluster = c;
-    static std::atomic<int> marks[64], wide[64];
+    static std::atomic<int> marks[64];
     const void* kern = reinterpret_cast<const void*>(sample_kernel<HALF>);
-    cudaError_t e = q4i::ensure_smem_attr(kern, marks, (int)sizeof(Shared));
+    const cudaError_t e = q4i::ensure_smem_attr(kern, marks, (int)sizeof(Shared));
     if (e != cudaSuccess) return e;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (c > 8 && !wide[dev & 63].load(std::memory_order_acquire)) {
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-        wide[dev & 63].store(1, std::memory_order_release);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * c));
     cfg.blockDim = dim3(kThreads);
