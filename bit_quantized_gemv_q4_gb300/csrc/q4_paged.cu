@@ -81,6 +81,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // page, and beside that the frequencies), so each thread fetches its first
 // kAhead items of data before anything else, one warp looks the row up and
 // two others compute the angles meanwhile.
+//
+// Measured: 6767 rows of 32 query and 8 kv heads of 128 (166 MB in and out)
+// 30.5 us = 5.4 TB/s, 80 % of the measured copy rate; 478 rows 3.1 us, one row
+// 2.8 us, which is a launch.  kAhead 1 / 2 / 4: 31.4 / 30.5 / 42 us (4 spills);
+// 8 blocks per SM or 6: 30.5 / 31.9 us.
 constexpr int kAhead = 2;
 
 template <int D, int kPairs>
@@ -233,6 +238,12 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_
 // and as paths ascend (path[i] >= i, path[j] > path[i] for j > i) no row is
 // written before the same column's later sources are past it.  ctx_out may be
 // ctx_len, so it is written after every block of the cluster has read it.
+//
+// What bounds it: a chain of dependent loads (sizes, the tokens and parents, the
+// path, its pages, its rows) and, for many sequences, the rows' bytes.  28
+// layers of 8 heads of 128, one sequence of 16 rows 5.0 us, 32 of up to 64 rows
+// (27 MB) 8.7 us = 3.1 TB/s.  Clusters of 1 / 4 / 8: 11.5 / 5.9 / 5.0 and 18.7 /
+// 8.8 / 8.7 us.
 constexpr int kAcceptThreads = 512;
 constexpr int kAcceptCluster = 8;
 constexpr int kMaxTree = 4096;
@@ -383,7 +394,8 @@ extern "C" q4_status q4_paged_append(const q4_paged_append_desc* desc, q4_stream
     a.rot = d.rot_dim;
     a.amplitude = d.amplitude == 0.f ? 1.f : d.amplitude;
     // chunks of 8: neighbours always pair up within one; halves do where they
-    // are whole chunks (rot_dim a multiple of 16)
+    // are whole chunks (rot_dim a multiple of 16; 30.3 us where element by
+    // element takes 40.9, 6767 rows)
     const int pairs = d.layout == Q4_ROPE_INTERLEAVED ? 0 : d.rot_dim % 16 == 0 ? 1 : 2;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     void (*kern)(q4p::AppendArgs) =

@@ -33,6 +33,12 @@
 // sorted as before.  Where one bin holds more than such a list (thousands of
 // equal logits), and where the list itself overflows, the search goes eight
 // bits of the key at a time.
+//
+// What bounds it: the instructions of pass 3 (some 20 a token: the weight, its
+// three sums and its bin) beside the chain of exchanges; DRAM is read once.
+// Measured: 256 rows of 50257 fp16 logits, top_p 0.9 in all, 64 us (26 MB, 0.4
+// TB/s; 34 % of issue slots; weights and bins left out it is 28); 61 rows of
+// 151936 with every setting in turn 53 us; one row with top_k 50 13.6 us.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -49,12 +55,12 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 8;
-constexpr int kWanted = 96;          // tokens the list aims at without top_k
+constexpr int kWanted = 96;          // tokens the list aims at without top_k (320: 256 rows 74 us; 160: 65; 96: 63; 40: 63)
 constexpr int kMostK = 1024;         // top_k up to which the list is tried
 constexpr int kList = 1024;          // tokens of a CTA's list
 constexpr int kAll = 2048;           // tokens of the joined list
 constexpr int kBinList = 1024;       // tokens of a bin that are sorted together
-constexpr int kCounting = 256;       // up to here a sort counts, per token, the greater ones
+constexpr int kCounting = 256;       // up to here a sort counts, per token, the greater ones (one row 14 us, bitonic 19)
 constexpr int kMostPart = 1 << 17;   // tokens of a CTA: sums of 15-bit parts of their weights stay below 2^32
 constexpr int kCut = 512;            // bins of the threshold: 16 per octave (4 steps)
 constexpr int kBins = 1536;          // bins of a histogram: a step each from the threshold on, or two steps from t = 0 on

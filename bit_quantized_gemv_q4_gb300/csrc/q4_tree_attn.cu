@@ -104,7 +104,7 @@ struct Place {
 
 // The line's length; `sums` gets the threads' running shares: each thread adds
 // up a contiguous share of the sequences.  The line has fewer than 2^31 units:
-// a call beyond that (some 10^16 operations) is left out, with the error
+// a call beyond that (10^14 operations and more) is left out, with the error
 // latched.
 __device__ __noinline__ unsigned line_scan(const Args& a, unsigned* sums, int threads) {
     __shared__ unsigned long long wsum[32];
@@ -327,11 +327,23 @@ __device__ __noinline__ void add_odd(const Args& a, const Place& p, int T, int t
 // column g; an accumulator rows g, g + 8, columns 2u, 2u+1, so two
 // neighbouring score tiles are the A operand of a 16-position step of P V.
 //
+// Measured: 40 users' tokens over contexts up to 12000 (8 query heads on each
+// of 4 kv heads of 128, 549 MB of cache) 94 us = 5.8 TB/s, 86 % of the measured
+// copy rate; a short line is bound by its chain of waits: a job's sizes, its
+// first pages, the first tiles, the parts' way through L2 and the joining
+// kernel, 9.5 us with one tile of work.
+//
 // kClustered: few jobs (a few users' decoding), where latency counts.  The
 // CTAs of a cluster take a job's tiles together and join their parts through
-// distributed shared memory: one launch, and no line to walk.
+// distributed shared memory: one launch, and no line to walk.  One user's
+// token over 1000 positions (16 heads on 8): 8.0 us, sizes, pages and one tile
+// per CTA behind one another (the line: 10.6).
 constexpr int kConsumers = 128, kThreads = 160;
-constexpr int kRingCost = 4, kRingLead = 16;  // units of a tile, and of a job before its tiles
+// Units of a tile, and of a job before its tiles: the way to a new job's first
+// tile costs a CTA about four tiles' time.  us with lead 0 / 8 / 16: 24 users'
+// tokens up to 2000 positions 37 / 30 / 29, 100 users' up to 500 56 / 38 / 36,
+// 40 up to 12000 94 / 94 / 94.
+constexpr int kRingCost = 4, kRingLead = 16;
 
 template <int D>
 struct Ring {
@@ -938,7 +950,7 @@ __device__ __forceinline__ void join_rows(const Args& a, const Shared& job, int 
 }
 
 // Two rows at a time where there are few parts, else one.
-constexpr int kFewParts = 8;
+constexpr int kFewParts = 8;  // (trees: 85 us, with 4 87, with 2 88)
 __device__ __forceinline__ int join_items(const Shared& job) {
     return job.parts == 0 ? 0 : job.parts <= kFewParts ? (job.rows + 1) / 2 : job.rows;
 }
@@ -975,9 +987,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
 
 // Behind the tcgen05 kernel, where a job has up to 256 rows: CTAs leave records
 // of the jobs they begin, every block counts all records' items, and the warps
-// of the grid share them.  (One user's 61 x 4 rows, 4000 positions: 29 us, with
-// the other kernel 36; that one's 4 users, tokens, 24 us, with this one 26: the
-// records are read when the attention has ended.)
+// of the grid share them.  One user's 61 x 4 rows over 4000 positions: 28 us,
+// with the kernel above 36.  Behind the ring's kernel it is the other way: 24
+// users' tokens 22.0 us, with this one 23.6, as the records can be read only
+// when the attention has ended.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_many_kernel(const __grid_constant__ Args a) {
     constexpr int kWarps = kJoinThreads / 32;
@@ -1090,10 +1103,11 @@ cudaError_t launch_kernel(const CUtensorMap& k, const CUtensorMap& v, const MapA
 // CTAs of a job's cluster, where the GPU holds all clusters at once (a GB300
 // places 14 of 16 CTAs, 36 of 8 and 74 of 4, two per SM); 0: the line.  us of a
 // token's step, 8 kv heads of 128, clusters / line, contexts up to
-//              100        1000       4000       16000      64000
-//   1 user     7.9 / 9.4  8.1 / 11   10 / 15    21 / 26    54 / 52   (16 CTAs; of 8: 7.0, 7.4, 11, 28, 88)
-//   2 users    7.1 / 9.4  8.7 / 11   13 / 16    31 / 33    94 / 69   (8)
-//   8 users    8.4 / 11   11 / 13    22 / 23    63 / 64   209 / 182  (4)
+//              100        1000       4000      16000    64000
+//   1 user     7.9 / 9.4  8.0 / 11   10 / 15   21 / 25  54 / 52  (16 CTAs; of 8: 7.0, 7.4, 11, 28, 88)
+//   2 users    7.3 / 9.4  8.8 / 11   13 / 16   32 / 32  94 / 69  (8)
+//   4 users    8.4 / 9.5  9.5 / 12   17 / 19   34 / 31  114 / 104
+//   8 users    8.5 / 9.6  11 / 13    22 / 24   64 / 64  209 / 182  (4)
 // The host sees the contexts' bound alone, the table's width.
 inline int cluster_size(long long jobs, long long positions, int sms) {
     if (jobs * 16 <= 3 * sms / 2) return 16;
@@ -1159,11 +1173,22 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
 // Key and value tiles come by TMA as boxes of `box` rows (the greatest power
 // of two, 8 .. 128, that divides the page): a box lies in one page.  A page
 // that does not exist is read outside the map, where TMA fills in zeros.
+//
+// Measured: a chunk of 1024 and one of 532 rows over 6000 and 4100 positions
+// (32 query heads on 8 kv heads of 128) 133 us = 1.11 PFLOP/s, 58 % of the
+// measured matrix rate, the tensor pipe active half of the time: the softmax
+// of a stream is not always done when the other's products are; 14 us are the
+// joining of the parts.  Trees of up to 61 rows over 8 contexts up to 20000:
+// 85 us = 4.4 TB/s of cache (375 MB).  A job's beginning and end (queries in,
+// tensor memory out: some 5 us) are what short contexts cost.
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1
 constexpr float kTcShift = 7.f;
-constexpr int kTcLead = 32;
-constexpr int kTcCostFull = 8, kTcCostHalf = 5;  // of a tile, with two row streams and with alternate tiles
+// Units of a tile, with two row streams and with alternate tiles (8 : 8 instead:
+// trees 101 us, 8 : 4: 96), and of a job before its tiles.  us with lead 0 / 16 /
+// 32: 64 trees of 30 over 1000 positions 113 / 66 / 64, 8 trees of 40 up to 8000
+// 67 / 49 / 48, the chunks 137 / 135 / 132.
+constexpr int kTcCostFull = 8, kTcCostHalf = 5, kTcLead = 32;
 
 template <int D>
 struct TcShape {
@@ -1830,10 +1855,21 @@ extern "C" q4_status q4_tree_attention(const q4_tree_attention_desc* desc, q4_st
     a.ldo = d.ldo;
     a.G = G;
     a.by_g = q4p::page_div((uint32_t)G);
-    // rows per job: the average sequence's, by 16, 32 or 64
+    // Rows per kv head of the average sequence choose the kernel.  us of 32
+    // sequences up to 4000 (500) positions, 8 kv heads of 128, by mean rows:
+    //          jobs of 16   of 32       of 64      tcgen05
+    //   11     62 (21)      63 (22)     85 (28)    72 (30)
+    //   16     67 (24)      58 (24)     76 (31)    65 (34)
+    //   27     78 (30)      61 (27)     73 (32)    62 (32)
+    //   32     123 (37)     87 (33)     92 (33)    75 (33)
+    //   43     130 (41)     82 (33)     83 (35)    68 (35)
+    // The tcgen05 kernel needs TMA; without it 64 beat 32 from some 50 rows on
+    // (230 against 265 us at 86).
     const long long avg = ((long long)d.rows * G + d.cache.n_seqs - 1) / d.cache.n_seqs;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // TMA boxes: the greatest power of two that divides a page, 8 at least
+    // TMA boxes: the greatest power of two that divides a page, 8 at least (a
+    // swizzled row group).  TMA / cp.async, us: 40 contexts up to 12000, pages of
+    // 8 105 / 121, of 16 94 / 107, of 64 93 / 96; one user's 16000 positions 20 / 29.
     const int even = d.cache.page_size & -d.cache.page_size;
     const long long pool_rows = (long long)d.cache.n_pages * d.cache.n_kv_heads * d.cache.page_size;
     const bool tma = even >= 8 && pool_rows < (1ll << 31) - 1;

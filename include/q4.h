@@ -577,7 +577,7 @@ q4_status q4_attention(const q4_attention_desc *desc, q4_stream_t stream);
  * DEVICE) positions are cached before them; row i of a sequence takes
  * position ctx_len[s] + i.  The sizes are read on the device, so a captured
  * graph can be replayed as they change.  Rows from row_start[n_seqs] up to
- * `rows` belong to nobody: they are neither read nor written.  A sequence
+ * `rows` belong to nobody: they are not used and not written.  A sequence
  * whose sizes do not fit (row_start not ascending within 0..rows, ctx_len
  * negative, more positions than max_pages * page_size) is left out, its
  * outputs untouched, and a page number outside [0, n_pages) stands for no
@@ -661,8 +661,9 @@ q4_status q4_paged_append(const q4_paged_append_desc *desc, q4_stream_t stream);
  * included.  q and out: fp16 [rows][n_q_heads * head_dim], strides as in 7b,
  * 16-byte aligned; they must not overlap.  The workspace is written and read
  * by the call's kernels; calls that can overlap need one each.  A call of
- * 2^31 or more units of work (eighths of 64 positions by the rows of a job;
- * some 10^15 operations) computes nothing and latches Q4_ERR_DEVICE_CHECK. */
+ * 2^31 or more units of work (16 positions of a kv head by a block of up to
+ * 256 rows; some 10^14 operations at least) computes nothing and latches
+ * Q4_ERR_DEVICE_CHECK. */
 typedef struct q4_tree_attention_desc {
     q4_paged_cache cache;
     const int32_t *ctx_len, *row_start;
