@@ -496,7 +496,9 @@ def _get_torch():
 
 def _stream_of(torch, dev: int, stream):
     """_stream without building a torch Stream object, which costs as much as a launch."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+    return _stream(stream)
 
 
 def _arg_other(t, dtype, need: int, dev: int, name: str):
@@ -515,6 +517,12 @@ def _arg_other(t, dtype, need: int, dev: int, name: str):
     if t.numel() < need:
         raise ValueError(f"{name}: holds {t.numel()} elements, the call needs {need}")
     return p
+
+
+def _device(torch) -> int:
+    """The current device; -2, which is no tensor's, where there is none."""
+    cuda = torch.cuda
+    return cuda.current_device() if cuda.is_initialized() or cuda.is_available() else -2
 
 
 def _arg(t, dtype, need: int, dev: int, name: str):
@@ -580,7 +588,7 @@ def q4_rope_frequencies(freqs, rot_dim: int, theta: float = 1.0e6, factor: float
     """freqs: int64 (or uint64) [rot_dim / 2] out, turns per position in units of 2^-64."""
     torch = _get_torch()
     d = q4_rope_desc(rot_dim, orig_len, theta, factor, alpha, beta)
-    dev = torch.cuda.current_device()
+    dev = _device(torch)
     p = _arg(freqs, torch.int64, rot_dim // 2, dev, "freqs")
     _check(lib().q4_rope_frequencies(ctypes.byref(d), p, _stream_of(torch, dev, stream)), "q4_rope_frequencies")
 
@@ -590,7 +598,7 @@ def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=No
                     ldq: int = 0, ldk: int = 0, ldv: int = 0, ldqo: int = 0, stream=None):
     """New rows' keys (rotated) and values into the paged cache, queries (rotated) into q_out."""
     torch = _get_torch()
-    dev = torch.cuda.current_device()
+    dev = _device(torch)
     f16, i32_ = torch.float16, torch.int32
     _, _, heads, hd, n_seqs, _ = cache.sizes
     pk, ldk = _rows(k, f16, rows, heads * hd, ldk, dev, "k")
@@ -614,7 +622,7 @@ def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_h
                       ldo: int = 0, stream=None):
     """Attention of the new rows over the cached positions and, by the mask (None: causal), their own."""
     torch = _get_torch()
-    dev = torch.cuda.current_device()
+    dev = _device(torch)
     f16, i32_ = torch.float16, torch.int32
     w, n_seqs = n_q_heads * cache.sizes[3], cache.sizes[4]
     pq, ldq = _rows(q, f16, rows, w, ldq, dev, "q")
@@ -634,7 +642,7 @@ def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, pare
                    next_token, ctx_out, n_layers: int = 1, layer_stride: int = 0, stream=None):
     """Walks each sequence's drafted tree along the sampled tokens and moves the path's cache rows into place."""
     torch = _get_torch()
-    dev = torch.cuda.current_device()
+    dev = _device(torch)
     i32_, n_seqs = torch.int32, cache.sizes[4]
     elements = (n_layers - 1) * layer_stride + cache.pool if n_layers > 0 else 0
     d = q4_tree_accept_desc(
@@ -651,7 +659,7 @@ def q4_sample(logits, dtype, rows: int, vocab: int, tokens, temperature=None, to
               u=None, probs=None, ld: int = 0, stream=None):
     """One token per row of logits (q4.h section 8); u: fp32 random numbers of [0, 1), None = the greatest logit."""
     torch = _get_torch()
-    dev = torch.cuda.current_device()
+    dev = _device(torch)
     f32, i32_ = torch.float32, torch.int32
     p, ld = _rows(logits, torch.float16 if dtype == Q4_F16 else f32, rows, vocab, ld, dev, "logits")
     d = q4_sample_desc(p, dtype, rows, vocab, ld, _arg(temperature, f32, rows, dev, "temperature"),

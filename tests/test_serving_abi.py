@@ -143,3 +143,13 @@ def test_binding_checks_its_tensors(L):
         q4.q4_sample(host, q4.Q4_F32, 1, 64, host)
     with pytest.raises(ValueError, match="CUDA device memory"):
         q4.q4_tree_accept(q4.PagedCache(FAKE, FAKE, 8, 16, 2, 128, host, 2, 4), FAKE, FAKE, 4, *[FAKE] * 7)
+
+
+def test_binding_without_a_device_gives_the_library_s_error(L):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("there is a device")
+    with pytest.raises(q4.Q4Error, match="NO_DEVICE"):
+        q4.q4_sample(FAKE, q4.Q4_F32, 1, 64, FAKE)
+    with pytest.raises(q4.Q4Error, match="vocab"):
+        q4.q4_sample(FAKE, q4.Q4_F32, 1, 0, FAKE)
