@@ -333,3 +333,158 @@ def test_numbers_of_jobs(S, Hkv, wide, G, most):
     out = attend(b, b.to_device(q4), q, "tree", sees)
     assert q4.q4_device_status() == 0
     check(out, b, q, a, A)
+
+
+# a batch for each form of the launch: clusters, the line of mma.sync jobs, tcgen05
+FORMS = {
+    "clusters": dict(ctx=[120, 3, 250], n=[2, 1, 2], Hkv=2, G=2, d=128, page=16),
+    "line": dict(ctx=[90, 0, 300, 17, 64] * 8, n=[1, 2, 1, 3, 1] * 8, Hkv=2, G=2, d=64, page=24),
+    "tcgen05": dict(ctx=[300, 0, 129], n=[40, 17, 64], Hkv=2, G=4, d=128, page=16),
+}
+
+
+def form(name, seed):
+    f = FORMS[name]
+    g = np.random.default_rng(seed)
+    b = Batch(g, f["ctx"], f["n"], f["Hkv"], f["d"], f["page"])
+    return g, b, rand16(g, b.rows, f["Hkv"] * f["G"], f["d"])
+
+
+@pytest.mark.parametrize("name", FORMS)
+def test_forms_replay_with_other_sizes(name):
+    g, b, q = form(name, 21)
+    T, Hq, d = q.shape
+    c = b.to_device(q4)
+    dq, out = torch_dev(q.reshape(T, -1)), torch.empty(T, Hq * d, dtype=torch.float16, device="cuda")
+    ws, n = workspace(d)
+    run = lambda: q4.q4_tree_attention(c, b.dctx, b.dstart, T, dq, Hq, out, ws, n)  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    end = [x + y for x, y in zip(b.ctx, b.n)]  # positions that exist
+    rng = np.random.default_rng(22)
+    for turn in range(4):
+        if turn == 1:
+            rows = [0] * b.S  # nobody has a row
+        elif turn == 2:
+            rows = [0] * (b.S - 1) + [min(end[-1], T)]  # the last sequence has all it can have
+        else:
+            rows = [int(rng.integers(0, min(e, T // b.S) + 1)) for e in end]
+        ctx = [int(rng.integers(0, e - r + 1)) for e, r in zip(end, rows)]
+        b.ctx, b.n = ctx, rows
+        b.start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        b.dctx.copy_(torch_dev(np.array(ctx, np.int32)))
+        b.dstart.copy_(torch_dev(b.start))
+        out.fill_(-5.0)
+        graph.replay()
+        assert q4.q4_device_status() == 0
+        got, R = out.cpu().numpy(), sum(rows)
+        assert np.all(got[R:] == -5.0)
+        if R:
+            a, A = expected(b, q, seen_by(b, "causal", g))
+            assert close(got[:R].reshape(a.shape), a, A).all(), turn
+
+
+@pytest.mark.parametrize("name", FORMS)
+@pytest.mark.parametrize("what", ["page", "ctx", "room"])
+def test_forms_leave_a_bad_sequence_out(name, what):
+    g, b, q = form(name, 23)
+    sees = seen_by(b, "tree", g)
+    c = b.to_device(q4)
+    bad = b.S - 1
+    if what == "page":
+        b.dtable[bad, 0] = b.n_pages
+    elif what == "ctx":
+        b.dctx[bad] = -1
+    else:
+        b.dctx[bad] = b.page * b.max_pages
+    rows = slice(b.start[bad], b.start[bad + 1])
+    if what == "page":  # its positions read as zeros: keys and values
+        first = min(b.page, b.ctx[bad])
+        page = b.table[bad, 0]
+        b.k[0, page, :, :first] = 0
+        b.v[0, page, :, :first] = 0
+    a, A = expected(b, q, sees)
+    out = attend(b, c, q, "tree", sees)
+    assert q4.q4_device_status() == -7
+    got = out.cpu().numpy()[:b.rows].reshape(a.shape)
+    ok = close(got, a, A)
+    if what != "page":
+        assert np.all(got[rows] == -5.0)
+        ok[rows] = True
+    assert ok.all()
+    assert q4.q4_device_status() == 0
+
+
+def test_calls_side_by_side_and_graphs_that_share_a_workspace():
+    made = {}
+    for name in FORMS:
+        g, b, q = form(name, 25)
+        T, Hq, d = q.shape
+        made[name] = (b, b.to_device(q4), torch_dev(q.reshape(T, -1)), Hq, d, T)
+    ws128, n128 = workspace(128)
+
+    def call(name, out, ws, n):
+        b, c, dq, Hq, d, T = made[name]
+        q4.q4_tree_attention(c, b.dctx, b.dstart, T, dq, Hq, out, ws, n)
+
+    new = lambda name: torch.empty(made[name][5], made[name][3] * made[name][4], dtype=torch.float16, device="cuda")  # noqa: E731
+    alone = {}
+    for name in FORMS:
+        alone[name] = new(name)
+        call(name, alone[name], *workspace(made[name][4]))
+        torch.cuda.synchronize()
+    # a workspace and a stream each, many calls in flight
+    streams = {name: torch.cuda.Stream() for name in FORMS}
+    spaces = {name: workspace(made[name][4]) for name in FORMS}
+    outs = {name: [new(name) for _ in range(20)] for name in FORMS}
+    torch.cuda.synchronize()
+    for i in range(20):
+        for name in FORMS:
+            with torch.cuda.stream(streams[name]):
+                call(name, outs[name][i], *spaces[name])
+    torch.cuda.synchronize()
+    assert q4.q4_device_status() == 0
+    for name in FORMS:
+        for o in outs[name]:
+            assert torch.equal(o.view(torch.int16), alone[name].view(torch.int16)), name
+    # one workspace, graphs one after another
+    graphs, res = [], []
+    for name in ("tcgen05", "clusters", "tcgen05"):
+        out, graph = new(name), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(name, out, ws128, n128)
+        graphs.append(graph)
+        res.append((name, out))
+    for _ in range(5):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for name, out in res:
+        assert torch.equal(out.view(torch.int16), alone[name].view(torch.int16)), name
+
+
+# pools of more than 2^31 elements: the pages in use lie at the far end
+@pytest.mark.parametrize("page,n,G", [(64, [1, 2], 2), (64, [40, 3], 4), (48, [20, 1], 1), (7, [9, 1], 2)])
+def test_pages_past_32_bit_offsets(page, n, G):
+    g = np.random.default_rng(31)
+    ctx, Hkv, d = [200, 77], 2, 128
+    b = Batch(g, ctx, n, Hkv, d, page, spare=0)
+    far = (1 << 31) // (Hkv * page * d) + 5  # pages before them
+    pools = []
+    for pool in (b.k, b.v):
+        t = torch.empty(far + b.n_pages, Hkv, page, d, dtype=torch.float16, device="cuda")
+        t[far:] = torch_dev(pool[0])
+        pools.append(t)
+    table = np.where(b.table >= 0, b.table + far, -1).astype(np.int32)
+    dtable = torch_dev(table)
+    b.dctx, b.dstart = torch_dev(np.array(ctx, np.int32)), torch_dev(b.start)
+    c = q4.PagedCache(pools[0], pools[1], far + b.n_pages, page, Hkv, d, dtable, b.S, b.max_pages)
+    q = rand16(g, b.rows, Hkv * G, d)
+    sees = seen_by(b, "tree", g)
+    a, A = expected(b, q, sees)
+    out = attend(b, c, q, "tree", sees)
+    assert q4.q4_device_status() == 0
+    check(out, b, q, a, A)
