@@ -46,6 +46,7 @@ struct AppendArgs {
     const uint64_t* freqs;
     int rot;
     float amplitude;
+    PageDiv by_per;  // division by a rotated head's items
 };
 
 // Sequence of a row: the number of sequences whose end is at or before it, by
@@ -83,9 +84,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // two others compute the angles meanwhile.
 //
 // Measured: 6767 rows of 32 query and 8 kv heads of 128 (166 MB in and out)
-// 30.5 us = 5.4 TB/s, 80 % of the measured copy rate; 478 rows 3.1 us, one row
+// 29.9 us = 5.6 TB/s, 82 % of the measured copy rate; 478 rows 3.1 us, one row
 // 2.8 us, which is a launch.  kAhead 1 / 2 / 4: 31.4 / 30.5 / 42 us (4 spills);
-// 8 blocks per SM or 6: 30.5 / 31.9 us.
+// 8 blocks per SM or 6: 30.5 / 31.9 us (both before the last 0.5 us).
 constexpr int kAhead = 2;
 
 template <int D, int kPairs>
@@ -108,9 +109,13 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_
         Item t;
         const int y = x < nq ? x : x < nq + nk ? x - nq : x - nq - nk;
         t.kind = x < nq ? 0 : x < nq + nk ? 1 : 2;
-        const int n = t.kind == 2 ? NC : per;
-        t.h = (int)((unsigned)y / (unsigned)n);
-        t.c = y - t.h * n;
+        if (t.kind == 2) {
+            t.h = y / NC;
+            t.c = y % NC;
+        } else {
+            t.h = (int)page_of(p.by_per, y);
+            t.c = y - t.h * per;
+        }
         return t;
     };
     const auto source = [&](const Item& t) {
@@ -401,6 +406,7 @@ extern "C" q4_status q4_paged_append(const q4_paged_append_desc* desc, q4_stream
     void (*kern)(q4p::AppendArgs) =
         D == 128 ? (pairs == 0 ? q4p::append_kernel<128, 0> : pairs == 1 ? q4p::append_kernel<128, 1> : q4p::append_kernel<128, 2>)
                  : (pairs == 0 ? q4p::append_kernel<64, 0> : pairs == 1 ? q4p::append_kernel<64, 1> : q4p::append_kernel<64, 2>);
+    a.by_per = q4p::page_div((uint32_t)(pairs == 1 ? D / 8 - d.rot_dim / 16 : D / 8));
     kern<<<d.rows, q4p::kAppendThreads, 0, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? Q4_OK : cuda_fail(e, "q4_paged_append launch");
