@@ -89,7 +89,7 @@ struct Shared {
     u64 list[kList];  // this CTA's tokens: key << 32 | ~index
     u64 mw[kBins];    // the cluster's histogram, then its running sums
     uint32_t mc[kBins];
-    uint32_t h0[kBins], h1[kBins], h2[kBins];  // this CTA's histogram: 15-bit parts of weights, or (count, low, high)
+    uint32_t h0[kBins], h1[kBins], h2[kBins];  // this CTA's histogram: two parts of short weights, or (count, low, high)
     uint32_t cut_count[kCut];                  // the threads' greatest logits
     float2 pow64[64];  // 2^(-j/64) in units of 2^-29: the integer's bits, and as a float
     uint32_t count;    // of list
@@ -120,6 +120,7 @@ __device__ __forceinline__ int magic_int(float x) { return __float_as_int(x) - _
 // weight there).  Monotone in the logit; every bin is a range of steps.
 constexpr float kEnd = 46.f;
 constexpr int kSteps = 64 * 46 + 1;
+constexpr float kLast = kMagic + 64.f * 46.f;  // (that step's weight rounds to zero)
 __device__ __forceinline__ int steps_of(float l, const Scale& c) {
     const float d = l == c.max ? 0.f : c.max - l;
     return d * c.hi < kEnd ? magic_int(fmaf(d, c.hi * 64.f, kMagic)) : kSteps;
@@ -137,13 +138,15 @@ __constant__ uint32_t kPow64[64] = {
     292730940u, 289577647u, 286458320u, 283372595u, 280320109u, 277300504u, 274313427u, 271358526u,
 };
 
-// 2^44 2^(-k/64) (1 - y), rounded; k >= 0, |y| < 0.0056.
-__device__ __forceinline__ u64 weight_from(int k, float y, const float2* pow64) {
+// A weight 2^44 2^(-k/64) (1 - y), rounded (k >= 0, |y| < 0.0056), is
+// short_weight << left(k), and short_weight is below 2^29 + 2^22.
+__device__ __forceinline__ int left(int k) { return max(15 - (k >> 6), 0); }
+__device__ __forceinline__ uint32_t short_weight(int k, float y, const float2* pow64) {
     const float2 p = pow64[k & 63];
-    const int q = magic_int(fmaf(p.y, y, kMagic));       // |p y| < 2^22
+    const int q = magic_int(fmaf(p.y, y, kMagic));           // |p y| < 2^22
     const uint32_t m = (uint32_t)(__float_as_int(p.x) - q);  // units of 2^-29: 2^28 .. 2^29
-    const int sh = 15 - (k >> 6);
-    return sh >= 0 ? (u64)m << sh : (u64)((m + (1u << (-sh - 1))) >> -sh);
+    const int sh = max((k >> 6) - 15, 0);
+    return (m + ((1u << sh) >> 1)) >> sh;
 }
 
 // round(2^44 2^-t).  The passes over a row (two_of below) do the same
@@ -167,16 +170,15 @@ __device__ __forceinline__ u64 weight_of(float l, const Scale& c, const float2* 
     // the next term is below 2^-34
     const float z = r * 0.010830425f;
     const float y = z * fmaf(z, fmaf(z, 0.16666667f, -0.5f), 1.f);
-    return weight_from(magic_int(kf), y, pow64);
+    return (u64)short_weight(magic_int(kf), y, pow64) << left(magic_int(kf));
 }
 
-// d = max - l, t and y of two logits (max finite).  `exact`: the difference's
+// k (as kMagic + k) and y of two logits (max finite).  `exact`: the difference's
 // rounding error counts too; of half-precision logits it does not (it is zero
 // but for logits 2^13 times smaller than the greatest, where it is below 2^-28
 // of a weight).
 struct Two {
-    float2 t, y;
-    int k[2];
+    float2 kf, y;
 };
 template <bool kExact>
 __device__ __forceinline__ Two two_of(float2 l, const Scale& c) {
@@ -198,12 +200,7 @@ __device__ __forceinline__ Two two_of(float2 l, const Scale& c) {
     const float2 z = __fmul2_rn(r, make_float2(0.010830425f, 0.010830425f));
     const float2 q = __ffma2_rn(z, __ffma2_rn(z, make_float2(0.16666667f, 0.16666667f), make_float2(-0.5f, -0.5f)),
                                 make_float2(1.f, 1.f));
-    Two o;
-    o.t = __fmul2_rn(d, make_float2(c.hi, c.hi));
-    o.y = __fmul2_rn(z, q);
-    o.k[0] = magic_int(kf.x);
-    o.k[1] = magic_int(kf.y);
-    return o;
+    return {kf, __fmul2_rn(z, q)};
 }
 
 // This CTA's part of a row: 16-byte vectors v0 .. v1 - 1 behind `head` single
@@ -443,17 +440,18 @@ struct Tally {
     }
 };
 
-// A weight's 15-bit parts into the tail's histogram (no result is waited for).
-__device__ __forceinline__ void add_parts(Shared& s, int bin, u64 w) {
-    const uint32_t lo = (uint32_t)w & 0x7fffu, mid = (uint32_t)(w >> 15) & 0x7fffu, hi = (uint32_t)(w >> 30);
-    atomicAdd(&s.h0[bin], lo);
-    atomicAdd(&s.h1[bin], mid);
-    if (hi) atomicAdd(&s.h2[bin], hi);
+// A short weight into the tail's histogram, in parts of 15 bits (no result is
+// waited for): the tokens of a bin are of one step, which shifts their sum, and
+// the last bin's, from a step above 16 * 64 on, are not shifted.
+__device__ __forceinline__ void add_tail(Shared& s, int bin, uint32_t w) {
+    atomicAdd(&s.h0[bin], w & 0x7fffu);
+    atomicAdd(&s.h1[bin], w >> 15);
 }
+static_assert(kBins > 16 * 64, "the last bin's shift");
 
 // Every CTA's histogram of `bins` bins (descending logits), joined and summed
-// up from the front, into every CTA's mc[] (with counts) and mw[].
-__device__ void join_histogram(Shared& s, Cluster& cl, int bins, bool counts) {
+// up from the front, into every CTA's mc[] and mw[].
+__device__ void join_histogram(Shared& s, Cluster& cl, int bins) {
     cl.sync();  // all histograms done
     const int b0 = bins * cl.rank / cl.ranks, b1 = bins * (cl.rank + 1) / cl.ranks;
     for (int b = b0 + threadIdx.x; b < b1; b += kThreads) {
@@ -463,7 +461,7 @@ __device__ void join_histogram(Shared& s, Cluster& cl, int bins, bool counts) {
             const u64 x = *cl.g.map_shared_rank(&s.h0[b], r), y = *cl.g.map_shared_rank(&s.h1[b], r),
                       z = *cl.g.map_shared_rank(&s.h2[b], r);
             n += (uint32_t)x;
-            w += counts ? y + (z << 32) : x + (y << 15) + (z << 30);
+            w += y + (z << 32);
         }
         for (int r = 0; r < cl.ranks; ++r) {
             *cl.g.map_shared_rank(&s.mc[b], r) = n;
@@ -483,7 +481,7 @@ __device__ void join_histogram(Shared& s, Cluster& cl, int bins, bool counts) {
         n[e] = tn;
         w[e] = tw;
     }
-    const u64 bn = counts ? block_scan(tn, s) - tn : 0, bw = block_scan(tw, s) - tw;
+    const u64 bn = block_scan(tn, s) - tn, bw = block_scan(tw, s) - tw;
 #pragma unroll
     for (int e = 0; e < P; ++e) {
         const int b = P * threadIdx.x + e;
@@ -495,24 +493,31 @@ __device__ void join_histogram(Shared& s, Cluster& cl, int bins, bool counts) {
     __syncthreads();
 }
 
-// The same for the weights alone, by rank 0 for itself (every CTA's histogram
-// is done).
-__device__ void join_tail(Shared& s, Cluster& cl) {
+// The tail's histogram of all CTAs, by rank 0 for itself (every CTA's is done):
+// running sums of the weights into mw[].
+__device__ void join_tail(Shared& s, Cluster& cl, int cut) {
     constexpr int P = kBins / kThreads;
     u64 w[P] = {};
     for (int r = 0; r < cl.ranks; ++r) {
         const uint32_t* h0 = cl.g.map_shared_rank(&s.h0[P * threadIdx.x], r);
         const uint32_t* h1 = cl.g.map_shared_rank(&s.h1[P * threadIdx.x], r);
-        const uint32_t* h2 = cl.g.map_shared_rank(&s.h2[P * threadIdx.x], r);
 #pragma unroll
-        for (int e = 0; e < P; ++e) w[e] += (u64)h0[e] + ((u64)h1[e] << 15) + ((u64)h2[e] << 30);
+        for (int e = 0; e < P; ++e) w[e] += (u64)h0[e] + ((u64)h1[e] << 15);
     }
+#pragma unroll
+    for (int e = 0; e < P; ++e) w[e] <<= left(cut + P * threadIdx.x + e);
 #pragma unroll
     for (int e = 1; e < P; ++e) w[e] += w[e - 1];
     const u64 before = block_scan(w[P - 1], s) - w[P - 1];
 #pragma unroll
     for (int e = 0; e < P; ++e) s.mw[P * threadIdx.x + e] = before + w[e];
     __syncthreads();
+}
+// The weight of this CTA's tail, a part of it per thread.
+__device__ __forceinline__ u64 tail_weight(const Shared& s, int cut) {
+    u64 w = 0;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) w += ((u64)s.h0[b] + ((u64)s.h1[b] << 15)) << left(cut + b);
+    return w;
 }
 
 // First bin whose running count or weight reaches target (there is one; else the last).
@@ -611,7 +616,7 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
             t.add(s, 255 - (int)(k >> shift & 255u), weight_of<!HALF>(key_value(k), c, s.pow64));
         });
         t.flush(s);
-        join_histogram(s, cl, 256, true);
+        join_histogram(s, cl, 256);
         const int b = reach_bin(s, 256, by_count, target - (by_count ? nb : wb));
         const u64 n0 = b ? s.mc[b - 1] : 0, w0 = b ? s.mw[b - 1] : 0;
         equal = s.mc[b] - n0;
@@ -776,9 +781,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     const int cut = 4 * (s.cut + 1);  // the list's steps: 0 .. cut - 1
 
-    // 3. the list; without top_k the weight of all, of those that min_p keeps,
-    // and the histogram of what is not in the list
-    u64 sums[3] = {0, 0, 0};  // valid tokens outside the list (top_k), all, some
+    // 3. the list; without top_k the histogram and the weight of what is not in
+    // it, and of that the weight that min_p keeps
+    u64 sums[3] = {0, 0, 0};  // outside the list: valid tokens (top_k), weight, kept weight
     const bool top_inf = isinf(c.max);
     if (with_k || top_inf) {
         // (any beginning of the order will do: one comparison per token)
@@ -796,18 +801,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             const Two x = two_of<!HALF>(l, c);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float t = e ? x.t.y : x.t.x, v = e ? l.y : l.x;
-                if (!(t < kEnd)) continue;  // no weight (-inf and NaN among them)
-                const u64 w = weight_from(x.k[e], e ? x.y.y : x.y.x, s.pow64);
-                sums[1] += w;
-                if (least_w && w >= least_w) sums[2] += w;
-                if (x.k[e] < cut) append(s, key_of(v), i + e);
-                else add_parts(s, min(x.k[e] - cut, kBins - 1), w);
+                const float kf = e ? x.kf.y : x.kf.x;
+                if (!(kf <= kLast)) continue;  // no weight (-inf and NaN among them)
+                const int k = magic_int(kf);
+                if (k < cut) {
+                    append(s, key_of(e ? l.y : l.x), i + e);
+                } else {
+                    const uint32_t w = short_weight(k, e ? x.y.y : x.y.x, s.pow64);
+                    add_tail(s, min(k - cut, kBins - 1), w);
+                    if (least_w && (u64)w << left(k) >= least_w) sums[2] += (u64)w << left(k);
+                }
             }
         });
+        __syncthreads();
+        sums[1] = tail_weight(s, cut);
     }
     block_sum(sums, s);
-    u64 n_list = 0, rest = 0, W = 0, some = 0;
+    u64 n_list = 0, rest = 0, W = 0, some = 0;  // W, some: the tail's as yet
     bool fits = true;
     const u64(*n)[4] = cl.exchange(s, {{s.count, sums[0], sums[1], sums[2]}});
     for (int i = 0; i < cl.ranks; ++i) {
@@ -847,16 +857,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         sort_and_scan<HALF>(s, s.all, s.pre, N, c);
         W_list = s.pre[N - 1];
         if (!with_k || k <= N || rest == 0) {
-            if (with_k) {
-                W = s.pre[min(k, N) - 1];
-                if (least_w) {  // top_k ends in the list, so what min_p keeps of it is all that counts
-                    some = 0;
-                    for (int i0 = 0; i0 < N; i0 += kThreads) {
-                        const int i = i0 + tid;
-                        some += __syncthreads_count(i < N && s.pre[i] - (i ? s.pre[i - 1] : 0) >= least_w);
-                    }
-                    some = s.pre[some - 1];
+            if (with_k) W = s.pre[min(k, N) - 1];  // top_k ends in the list
+            else W += W_list;
+            if (least_w) {
+                int kept = 0;
+                for (int i0 = 0; i0 < N; i0 += kThreads) {
+                    const int i = i0 + tid;
+                    kept += __syncthreads_count(i < N && s.pre[i] - (i ? s.pre[i - 1] : 0) >= least_w);
                 }
+                some = (with_k ? 0 : some) + s.pre[kept - 1];  // (the greatest is kept)
             }
             state = kDone;
             if (p < 1.f) {
@@ -866,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             }
             if (state == kDone) choose();
             if (state != kDone) {
-                join_tail(s, cl);
+                join_tail(s, cl, cut);
                 find_bin();
             }
         }
@@ -888,12 +897,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 clear_histogram(s, kBins);
                 row.template each<1>([&](float l, int) {
                     const int st = steps_of(l, c);
-                    if (st >= cut && st < kSteps) add_parts(s, min(st - cut, kBins - 1), weight_of<!HALF>(l, c, s.pow64));
+                    if (st >= cut && st < kSteps)
+                        add_tail(s, min(st - cut, kBins - 1), (uint32_t)(weight_of<!HALF>(l, c, s.pow64) >> left(st)));
                 });
                 cl.sync();
             }
             if (cl.rank == 0) {
-                if (h.by_digits) join_tail(s, cl);
+                if (h.by_digits) join_tail(s, cl, cut);
                 W = W_list + (bin ? s.mw[bin - 1] : 0) + h.weight;
                 choose();
                 if (state == kToken) find_bin();
@@ -916,10 +926,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 t.add(s, steps_of(l, c) >> 1, w);
             });
             t.flush(s);
-            join_histogram(s, cl, kBins, true);
+            join_histogram(s, cl, kBins);
         };
         histogram();
-        if ((with_k || top_inf) && least_w) {
+        if (least_w) {
             sums[0] = 0;
             row.template each<1>([&](float l, int) {
                 if (!(l > -INFINITY)) return;
