@@ -226,12 +226,12 @@ struct Part {
         if constexpr (HALF) return __half2float(__ushort_as_half(row[i]));
         else return row[i];
     }
-    // f(two values, index of the first) for the part's elements, N vectors in
-    // flight per thread; a thread's indices ascend.  Single elements come with
-    // a -inf, which takes no part.
-    template <int N, typename F>
-    __device__ __forceinline__ void pairs(F f) const {
-        if (rank == 0 && (int)threadIdx.x < head) f(make_float2(at(threadIdx.x), -INFINITY), (int)threadIdx.x);
+    // f(vector, index of its first element) for the part's vectors, N in flight
+    // per thread, and one(value, index) for the single elements; a thread's
+    // indices ascend.
+    template <int N, typename F, typename G>
+    __device__ __forceinline__ void vectors(F f, G one) const {
+        if (rank == 0 && (int)threadIdx.x < head) one(at(threadIdx.x), (int)threadIdx.x);
         const uint4* vec = reinterpret_cast<const uint4*>(row + head);
         uint4 next[N];  // the loads of the turn after this one are on their way meanwhile
         const auto load = [&](int v) {
@@ -249,20 +249,47 @@ struct Part {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (v + i * kThreads >= v1) break;
-                const int at0 = head + (v + i * kThreads) * VE;
-                if constexpr (HALF) {
-                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].x)), at0);
-                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].y)), at0 + 2);
-                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].z)), at0 + 4);
-                    f(__half22float2(*reinterpret_cast<const __half2*>(&w[i].w)), at0 + 6);
-                } else {
-                    f(make_float2(__uint_as_float(w[i].x), __uint_as_float(w[i].y)), at0);
-                    f(make_float2(__uint_as_float(w[i].z), __uint_as_float(w[i].w)), at0 + 2);
-                }
+                f(w[i], head + (v + i * kThreads) * VE);
             }
         }
-        if (rank == ranks - 1 && tail + (int)threadIdx.x < vocab)
-            f(make_float2(at(tail + threadIdx.x), -INFINITY), tail + (int)threadIdx.x);
+        if (rank == ranks - 1 && tail + (int)threadIdx.x < vocab) one(at(tail + threadIdx.x), tail + (int)threadIdx.x);
+    }
+    // f(two values, index of the first).  Single elements come with a -inf, which
+    // takes no part.
+    template <int N, typename F>
+    __device__ __forceinline__ void pairs(F f) const {
+        vectors<N>(
+            [&](uint4 w, int i) {
+                if constexpr (HALF) {
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w.x)), i);
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w.y)), i + 2);
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w.z)), i + 4);
+                    f(__half22float2(*reinterpret_cast<const __half2*>(&w.w)), i + 6);
+                } else {
+                    f(make_float2(__uint_as_float(w.x), __uint_as_float(w.y)), i);
+                    f(make_float2(__uint_as_float(w.z), __uint_as_float(w.w)), i + 2);
+                }
+            },
+            [&](float x, int i) { f(make_float2(x, -INFINITY), i); });
+    }
+    // This thread's greatest logit (NaN left out), -inf without any.
+    __device__ __forceinline__ float greatest() const {
+        float best = -INFINITY;
+        __half2 two = __floats2half2_rn(-INFINITY, -INFINITY);  // (a maximum of halves needs no conversion)
+        vectors<4>(
+            [&](uint4 w, int) {
+                if constexpr (HALF) {
+                    const __half2 x = __hmax2(*reinterpret_cast<const __half2*>(&w.x), *reinterpret_cast<const __half2*>(&w.y));
+                    const __half2 y = __hmax2(*reinterpret_cast<const __half2*>(&w.z), *reinterpret_cast<const __half2*>(&w.w));
+                    two = __hmax2(two, __hmax2(x, y));
+                } else {
+                    best = fmaxf(best, fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
+                                             fmaxf(__uint_as_float(w.z), __uint_as_float(w.w))));
+                }
+            },
+            [&](float x, int) { best = fmaxf(best, x); });
+        if constexpr (HALF) best = fmaxf(best, fmaxf(__low2float(two), __high2float(two)));
+        return best;
     }
     // f(value, index), one at a time (the added -inf among them).
     template <int N, typename F>
@@ -704,8 +731,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
 
     // 1. the greatest logit
-    float best = -INFINITY;
-    row.template pairs<4>([&](float2 l, int) { best = fmaxf(best, fmaxf(l.x, l.y)); });
+    const float best = row.greatest();
     const bool any = best > -INFINITY;
     // (while the loads are on their way: the tables)
     if (tid < 64) s.pow64[tid] = make_float2(__int_as_float((int)kPow64[tid]), (float)kPow64[tid]);
@@ -797,7 +823,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             }
         });
     } else {
-        row.template pairs<HALF ? 1 : 2>([&](float2 l, int i) {
+        // (whether min_p keeps any of the tail: by the greatest weight of its first step)
+        const bool keeps = least_w && (u64)short_weight(cut, -0.0055f, s.pow64) << left(cut) >= least_w;
+        row.template pairs<1>([&](float2 l, int i) {
             const Two x = two_of<!HALF>(l, c);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -809,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 } else {
                     const uint32_t w = short_weight(k, e ? x.y.y : x.y.x, s.pow64);
                     add_tail(s, min(k - cut, kBins - 1), w);
-                    if (least_w && (u64)w << left(k) >= least_w) sums[2] += (u64)w << left(k);
+                    if (keeps && (u64)w << left(k) >= least_w) sums[2] += (u64)w << left(k);
                 }
             }
         });
