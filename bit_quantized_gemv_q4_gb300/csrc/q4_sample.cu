@@ -589,16 +589,37 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
     const float step = 1.f / (c.hi * 64.f);
     const float most = s0 > 0 ? c.max - (float)(s0 - 1) * step : INFINITY;
     const float fewest = c.hi > 0.f ? c.max - (float)(s1 + 1) * step : -INFINITY;
-    row.template pairs<2>([&](float2 l, int i) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float x = e ? l.y : l.x;
-            if (x <= most && x >= fewest && x > -INFINITY) {
-                const int st = steps_of(x, c);
-                if (st >= s0 && st < s1) append(s, key_of(x), i + e);
-            }
+    const auto one = [&](float x, int i) {
+        if (x <= most && x >= fewest && x > -INFINITY) {
+            const int st = steps_of(x, c);
+            if (st >= s0 && st < s1) append(s, key_of(x), i);
         }
-    });
+    };
+    const __half2 hi = __half2half2(__float2half_ru(most)), lo = __half2half2(__float2half_rd(fewest));
+    row.template vectors<2>(
+        [&](uint4 w, int i) {
+            uint32_t in;  // a bit per element of the vector
+            if constexpr (HALF) {
+                const auto between = [&](uint32_t x) {
+                    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+                    return __hle2_mask(h, hi) & __hge2_mask(h, lo);
+                };
+                in = (between(w.x) & 0x00010001u) | (between(w.y) & 0x00020002u) | (between(w.z) & 0x00040004u) |
+                     (between(w.w) & 0x00080008u);
+            } else {
+                const auto between = [&](uint32_t x) { return __uint_as_float(x) <= most && __uint_as_float(x) >= fewest; };
+                in = (between(w.x) ? 1u : 0u) | (between(w.y) ? 2u : 0u) | (between(w.z) ? 4u : 0u) | (between(w.w) ? 8u : 0u);
+            }
+#pragma unroll 1
+            while (in) {
+                const int b = __ffs((int)in) - 1, word = b & 15;
+                in &= in - 1;
+                const uint32_t x = word == 0 ? w.x : word == 1 ? w.y : word == 2 ? w.z : w.w;
+                if constexpr (HALF) one(__half2float(__ushort_as_half((uint16_t)(b < 16 ? x : x >> 16))), i + 2 * word + (b >> 4));
+                else one(__uint_as_float(x), i + word);
+            }
+        },
+        one);
     __syncthreads();
     const u64(*n)[4] = cl.exchange(s, {{s.count, 0, 0, 0}});
     u64 total = 0;
