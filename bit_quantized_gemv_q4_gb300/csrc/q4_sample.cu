@@ -34,11 +34,13 @@
 // equal logits), and where the list itself overflows, the search goes eight
 // bits of the key at a time.
 //
-// What bounds it: the instructions of pass 3 (some 20 a token: the weight, its
-// three sums and its bin) beside the chain of exchanges; DRAM is read once.
-// Measured: 256 rows of 50257 fp16 logits, top_p 0.9 in all, 64 us (26 MB, 0.4
-// TB/s; 34 % of issue slots; weights and bins left out it is 28); 61 rows of
-// 151936 with every setting in turn 53 us; one row with top_k 50 13.6 us.
+// What bounds it: the instructions of pass 3 (35 a token: the weight, its step's
+// bin, the list), and behind it a chain of exchanges, barriers and short
+// passes; DRAM is read once.  Measured: 256 rows of 50257 fp16 logits, top_p 0.9
+// in all, 52 us (26 MB, 0.5 TB/s): the greatest logit and the threshold 11, pass
+// 3 23, the list 3, what the tail needs 15; SMs with two rows issue in up to 93 %
+// of their cycles.  61 rows of 151936 with every setting in turn 48 us; one row
+// with top_k 50 13.6 us.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -55,7 +57,7 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kMaxCluster = 8;
-constexpr int kWanted = 96;          // tokens the list aims at without top_k (320: 256 rows 74 us; 160: 65; 96: 63; 40: 63)
+constexpr int kWanted = 96;          // tokens the list aims at without top_k (256 rows, of 63 us: 320 74, 160 65, 40 63)
 constexpr int kMostK = 1024;         // top_k up to which the list is tried
 constexpr int kList = 1024;          // tokens of a CTA's list
 constexpr int kAll = 2048;           // tokens of the joined list
@@ -1023,11 +1025,10 @@ template <bool HALF>
 cudaError_t launch(Args& a, int rows, int sms, cudaStream_t stream) {
     // As many CTAs per row as the GPU holds for all rows at once (a GB300
     // places 36 clusters of 8 CTAs, 74 of 4, 152 of 2), each with at least 2048
-    // tokens and at most kMostPart.  us of rows x 151936 with top_k 50, at 8 / 4 /
-    // 2 CTAs: 1 row 13.6 / 14.8 / -, 36 rows 17.7 / 16.3 / -; of 61 rows with
-    // every setting in turn at 8 / 4 / 2: - / 54 / 63, at 16 rows 34 / 38 / -.
-    // Clusters that wait for others cost more than they bring: 16 rows at 16 CTAs
-    // 44, at 8 34.  One row of 8000 is as fast with 2 (9.0) as with 4 (10.9).
+    // tokens and at most kMostPart.  us of rows of 151936 with top_k 50: 1 row 13.6
+    // at 8 CTAs, 14.8 at 4; 36 rows 17.7 and 16.3.  With every setting in turn: 16
+    // rows 34 at 8, 38 at 4, 44 at 16 (clusters that wait for others); 61 rows 54
+    // at 4, 63 at 2.  One row of 8000: 9.0 at 2, 10.9 at 4.
     const auto held = [&](int x) { return x > 2 ? 2 * sms - 2 * x : 2 * sms; };
     int c = kMaxCluster;
     while (c > 1 && ((long long)rows * c > held(c) || a.vocab <= 2048 * c) && a.vocab <= kMostPart * (c / 2)) c /= 2;
