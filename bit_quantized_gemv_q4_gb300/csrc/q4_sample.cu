@@ -93,7 +93,7 @@ struct Shared {
     uint32_t mc[kBins];
     uint32_t h0[kBins], h1[kBins], h2[kBins];  // this CTA's histogram: two parts of short weights, or (count, low, high)
     uint32_t cut_count[kCut];                  // the threads' greatest logits
-    float2 pow64[64];  // 2^(-j/64) in units of 2^-29: the integer's bits, and as a float
+    float2 pow64[64];  // 2^(-j/64) in units of 2^-29 (short_weight)
     uint32_t count;    // of list
     int cut;
 };
@@ -140,16 +140,21 @@ __constant__ uint32_t kPow64[64] = {
     292730940u, 289577647u, 286458320u, 283372595u, 280320109u, 277300504u, 274313427u, 271358526u,
 };
 
-// A weight 2^44 2^(-k/64) (1 - y), rounded (k >= 0, |y| < 0.0056), is
-// short_weight << left(k), and short_weight is below 2^29 + 2^22.
+// A weight 2^44 2^(-k/64) (1 - y), rounded (kf = kMagic + k, k >= 0, |y| <
+// 0.0056), is short_weight << left(k), and short_weight is below 2^29 + 2^22.
+// The table holds an integer's bits, with those of kMagic added, and a float.
+constexpr uint32_t kMagicBits = 0x4B400000u;  // kMagic; its low six bits are zero
 __device__ __forceinline__ int left(int k) { return max(15 - (k >> 6), 0); }
-__device__ __forceinline__ uint32_t short_weight(int k, float y, const float2* pow64) {
-    const float2 p = pow64[k & 63];
-    const int q = magic_int(fmaf(p.y, y, kMagic));           // |p y| < 2^22
-    const uint32_t m = (uint32_t)(__float_as_int(p.x) - q);  // units of 2^-29: 2^28 .. 2^29
-    const int sh = max((k >> 6) - 15, 0);
+__device__ __forceinline__ uint32_t short_weight(float kf, float y, const float2* pow64) {
+    const uint32_t bits = __float_as_uint(kf);
+    const float2 p = pow64[bits & 63];
+    // units of 2^-29: 2^28 .. 2^29; |p y| < 2^22
+    const uint32_t m = __float_as_uint(p.x) - __float_as_uint(fmaf(p.y, y, kMagic));
+    const int sh = max((int)(bits >> 6) - (int)(kMagicBits >> 6) - 15, 0);
     return (m + ((1u << sh) >> 1)) >> sh;
 }
+
+constexpr float kZ1 = 0.0108304247f, kZ2 = -5.86490495e-05f, kZ3 = 2.11731307e-07f;  // ln2/64, -its square / 2, its cube / 6
 
 // round(2^44 2^-t).  The passes over a row (two_of below) do the same
 // operations on two logits at a time, so a token has one weight.
@@ -170,9 +175,8 @@ __device__ __forceinline__ u64 weight_of(float l, const Scale& c, const float2* 
     r = fmaf(d, lo, r);
     // 2^(-r/64) = 1 - y, y = z - z^2 / 2 + z^3 / 6, z = r ln2 / 64 < 0.0055;
     // the next term is below 2^-34
-    const float z = r * 0.010830425f;
-    const float y = z * fmaf(z, fmaf(z, 0.16666667f, -0.5f), 1.f);
-    return (u64)short_weight(magic_int(kf), y, pow64) << left(magic_int(kf));
+    const float y = r * fmaf(r, fmaf(r, kZ3, kZ2), kZ1);
+    return (u64)short_weight(kf, y, pow64) << left(magic_int(kf));
 }
 
 // k (as kMagic + k) and y of two logits (max finite).  `exact`: the difference's
@@ -189,8 +193,7 @@ __device__ __forceinline__ Two two_of(float2 l, const Scale& c) {
     const float2 mg = make_float2(kMagic, kMagic);
     const float2 d = __ffma2_rn(l, neg, mx);
     const float2 kf = __ffma2_rn(d, hi, mg);
-    const float2 kr = __fadd2_rn(kf, make_float2(-kMagic, -kMagic));
-    float2 r = __ffma2_rn(d, hi, __ffma2_rn(kr, neg, make_float2(0.f, 0.f)));
+    float2 r = __ffma2_rn(d, hi, __ffma2_rn(kf, neg, mg));
     if (kExact) {
         const float2 b = __fadd2_rn(d, make_float2(-c.max, -c.max));
         const float2 db = __ffma2_rn(b, neg, d);                      // d - b
@@ -199,10 +202,8 @@ __device__ __forceinline__ Two two_of(float2 l, const Scale& c) {
         r = __ffma2_rn(e1, hi, r);
     }
     r = __ffma2_rn(d, lo, r);
-    const float2 z = __fmul2_rn(r, make_float2(0.010830425f, 0.010830425f));
-    const float2 q = __ffma2_rn(z, __ffma2_rn(z, make_float2(0.16666667f, 0.16666667f), make_float2(-0.5f, -0.5f)),
-                                make_float2(1.f, 1.f));
-    return {kf, __fmul2_rn(z, q)};
+    const float2 q = __ffma2_rn(r, __ffma2_rn(r, make_float2(kZ3, kZ3), make_float2(kZ2, kZ2)), make_float2(kZ1, kZ1));
+    return {kf, __fmul2_rn(r, q)};
 }
 
 // This CTA's part of a row: 16-byte vectors v0 .. v1 - 1 behind `head` single
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const float best = row.greatest();
     const bool any = best > -INFINITY;
     // (while the loads are on their way: the tables)
-    if (tid < 64) s.pow64[tid] = make_float2(__int_as_float((int)kPow64[tid]), (float)kPow64[tid]);
+    if (tid < 64) s.pow64[tid] = make_float2(__uint_as_float(kPow64[tid] + kMagicBits), (float)kPow64[tid]);
     for (int b = tid; b < kCut; b += kThreads) s.cut_count[b] = 0;
     for (int b = tid; b < kBins; b += kThreads) s.h0[b] = s.h1[b] = s.h2[b] = 0;
     if (tid == 0) {
@@ -847,20 +848,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         });
     } else {
         // (whether min_p keeps any of the tail: by the greatest weight of its first step)
-        const bool keeps = least_w && (u64)short_weight(cut, -0.0055f, s.pow64) << left(cut) >= least_w;
+        const bool keeps = least_w && (u64)short_weight(kMagic + (float)cut, -0.0055f, s.pow64) << left(cut) >= least_w;
         row.template pairs<1>([&](float2 l, int i) {
             const Two x = two_of<!HALF>(l, c);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float kf = e ? x.kf.y : x.kf.x;
                 if (!(kf <= kLast)) continue;  // no weight (-inf and NaN among them)
-                const int k = magic_int(kf);
-                if (k < cut) {
+                if (kf < kMagic + (float)cut) {
                     append(s, key_of(e ? l.y : l.x), i + e);
                 } else {
-                    const uint32_t w = short_weight(k, e ? x.y.y : x.y.x, s.pow64);
-                    add_tail(s, min(k - cut, kBins - 1), w);
-                    if (keeps && (u64)w << left(k) >= least_w) sums[2] += (u64)w << left(k);
+                    const uint32_t w = short_weight(kf, e ? x.y.y : x.y.x, s.pow64);
+                    add_tail(s, min(magic_int(kf) - cut, kBins - 1), w);
+                    if (keeps) {
+                        const u64 all = (u64)w << left(magic_int(kf));
+                        if (all >= least_w) sums[2] += all;
+                    }
                 }
             }
         });
