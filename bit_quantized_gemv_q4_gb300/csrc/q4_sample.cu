@@ -34,12 +34,12 @@
 // equal logits), and where the list itself overflows, the search goes eight
 // bits of the key at a time.
 //
-// What bounds it: the instructions of pass 3 (35 a token: the weight, its step's
-// bin, the list), and behind it a chain of exchanges, barriers and short
-// passes; DRAM is read once.  Measured: 256 rows of 50257 fp16 logits, top_p 0.9
-// in all, 52 us (26 MB, 0.5 TB/s): the greatest logit and the threshold 11, pass
-// 3 23, the list 3, what the tail needs 15; SMs with two rows issue in up to 93 %
-// of their cycles.  61 rows of 151936 with every setting in turn 48 us; one row
+// What bounds it: the passes' instructions (35 a token in pass 3: the weight,
+// its step's bin, the list), and behind them a chain of exchanges, barriers and
+// short passes; DRAM is read once.  Measured: 256 rows of 50257 fp16 logits,
+// top_p 0.9 in all, 52 us (26 MB, 0.5 TB/s): the greatest logit and the
+// threshold 12, pass 3 17 (5 of them the histogram's atomics), the list 3, what
+// the tail needs 19; SMs with two rows issue in up to 93 % of their cycles.  61 rows of 151936 with every setting in turn 48 us; one row
 // with top_k 50 13.6 us.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
