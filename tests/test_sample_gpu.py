@@ -210,3 +210,37 @@ def test_one_call_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert tok.tolist() == [oracle.sample(x[i].cpu().numpy(), u=float(u[i]))[0] for i in range(4)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+@pytest.mark.parametrize("kind", ["normal", "rounded", "equal", "masked", "ramp", "wide", "one peak"])
+def test_all_limits_in_turn_over_kinds_of_rows(kind, dtype):
+    """Every row with settings of its own: flat and peaked rows, the nucleus's end
+    and the token in the list, below it and among equals."""
+    g = np.random.default_rng(len(kind) * 10 + len(dtype))
+    for V in (37, 2500, 9001):
+        R = 12
+        x = g.standard_normal((R, V)) * np.exp(g.uniform(-4, 3, (R, 1)))
+        if kind == "rounded":
+            x = np.round(x * 4) / 4
+        elif kind == "equal":
+            x[:] = x[:, :1]
+        elif kind == "masked":
+            x[g.random((R, V)) < 0.7] = -np.inf
+        elif kind == "ramp":
+            x += np.linspace(0, 40, V)
+        elif kind == "wide":
+            x *= 100
+        elif kind == "one peak":
+            x[:, V // 3] += 20
+        x = x.astype(np.float16 if dtype == "f16" else np.float32)
+        T = np.where(g.random(R) < 0.5, 1.0, np.exp(g.uniform(-4, 4, R))).astype(np.float32)
+        k = np.where(g.random(R) < 0.5, 0, g.integers(1, V + 5, R)).astype(np.int32)
+        p = np.where(g.random(R) < 0.4, 1.0, g.random(R)).astype(np.float32)
+        m = np.where(g.random(R) < 0.5, 0.0, np.exp(g.uniform(-10, 0, R))).astype(np.float32)
+        u = g.random(R).astype(np.float32)
+        tok, pr = sample(x, temperature=T, top_k=k, top_p=p, min_p=m, u=u)
+        for r in range(R):
+            t, q = oracle.sample(x[r], float(T[r]), int(k[r]), float(p[r]), float(m[r]), float(u[r]))
+            assert tok[r] == t, (V, r, tok[r], t)
+            assert abs(pr[r] - q) <= 2.0 ** -23 * q + 2.0 ** -43, (V, r, pr[r], q)  # (as in check)
