@@ -684,7 +684,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             // know the place.
             float* ob = reinterpret_cast<float*>(smem + (kClustered ? 0 : st * 2 * TB));
             static_assert((size_t)WN * BM * D * 4 <= 2 * TB, "joining space");
-            if constexpr (WN > 1 || kClustered) q4d::named_bar(1, kConsumers);  // nobody reads the tiles any more
+            // Nobody reads the tiles any more, and every warp's note of
+            // infinities or NaN among the values (B.odd) is there: a warp
+            // that finds a row cleared by another one has none of its own.
+            // As no warp is more than a segment ahead, two notes suffice.
+            q4d::named_bar(1, kConsumers);
             if constexpr (WN > 1) {
                 if (u == 0) {
                     ml_s[warp * 16 + g] = make_float2(m[0], l[0]);

@@ -488,3 +488,51 @@ def test_pages_past_32_bit_offsets(page, n, G):
     out = attend(b, c, q, "tree", sees)
     assert q4.q4_device_status() == 0
     check(out, b, q, a, A)
+
+
+# Infinities and NaN among the new rows' values, in every form of the launch:
+# mma.sync jobs of 16, 32 and 64 rows, several to a CTA (a tile each) or shared by
+# several, in pages that come by TMA and, of 7 and 12 rows, row by row; clusters;
+# tcgen05 with one and two row streams.  n, ctx: from, to; wide: a table that
+# rules the clusters out.
+ODD = {
+    "64 rows, short, pages of 7": dict(S=700, Hkv=2, G=4, n=(9, 16), ctx=(0, 40), d=64, page=7),
+    "64 rows, short, pages of 12": dict(S=120, Hkv=1, G=8, n=(24, 30), ctx=(0, 30), d=128, page=12),
+    "64 rows, shared": dict(S=12, Hkv=2, G=4, n=(16, 20), ctx=(300, 1500), d=128, page=7, wide=True),
+    "16 rows, short": dict(S=600, Hkv=1, G=2, n=(1, 6), ctx=(0, 60), d=64, page=16),
+    "16 rows, short, pages of 7": dict(S=600, Hkv=1, G=2, n=(1, 6), ctx=(0, 60), d=128, page=7),
+    "32 rows, short": dict(S=600, Hkv=1, G=4, n=(5, 7), ctx=(0, 60), d=128, page=8),
+    "16 rows, shared": dict(S=20, Hkv=1, G=2, n=(2, 6), ctx=(500, 2000), d=64, page=16, wide=True),
+    "64 rows, clusters": dict(S=5, Hkv=2, G=4, n=(12, 16), ctx=(0, 500), d=64, page=7),
+    "tcgen05, short": dict(S=170, Hkv=1, G=4, n=(9, 30), ctx=(0, 90), d=128, page=16),
+    "tcgen05, two streams": dict(S=30, Hkv=2, G=4, n=(33, 60), ctx=(0, 300), d=64, page=8),
+    "tcgen05, shared": dict(S=5, Hkv=1, G=4, n=(20, 50), ctx=(500, 3000), d=128, page=64),
+}
+
+
+@pytest.mark.parametrize("kind", ["tree", "causal"])
+@pytest.mark.parametrize("name", ODD)
+def test_infinities_and_nan_reach_what_sees_them_in_every_form(name, kind):
+    f = ODD[name]
+    g = np.random.default_rng(40 + len(name))
+    draw = lambda r: [int(x) for x in g.integers(r[0], r[1] + 1, f["S"])]  # noqa: E731
+    b = Batch(g, draw(f["ctx"]), draw(f["n"]), f["Hkv"], f["d"], f["page"])
+    if f.get("wide"):
+        b.table = np.pad(b.table, ((0, 0), (0, 9000 // b.page)), constant_values=-1)
+        b.max_pages = b.table.shape[1]
+    for s in range(b.S):
+        for j in np.flatnonzero(g.random(b.n[s]) < 0.15):
+            p = b.ctx[s] + j
+            for h in range(b.Hkv):
+                b.v[0, b.table[s, p // b.page], h, p % b.page, g.integers(0, b.d, 3)] = g.choice([np.inf, -np.inf, np.nan], 3)
+    q = rand16(g, b.rows, b.Hkv * f["G"], b.d)
+    sees = seen_by(b, kind, g)
+    with np.errstate(all="ignore"):
+        a, A = expected(b, q, sees)
+    got = attend(b, b.to_device(q4), q, kind, sees).cpu().numpy()[:b.rows].reshape(a.shape)
+    assert q4.q4_device_status() == 0
+    odd = ~np.isfinite(a)
+    assert odd.any() and not odd.all(axis=(1, 2)).any()
+    for what in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(what(got), what(a)), (what, np.argwhere(what(got) != what(a))[:5])
+    assert close(got[~odd], a[~odd], A[~odd]).all()
