@@ -385,7 +385,6 @@ __device__ __forceinline__ bool find_block(const Args& a, int block, Place& p) {
         p.s = 0;
         p.rb = block;
         p.q = q4p::seq_of(a.w, 0, bad);
-        if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.w.err, q4d::kErrDeviceCheck);
         return block * a.BM < p.q.n * a.G;
     }
 #pragma unroll 1
@@ -394,7 +393,6 @@ __device__ __forceinline__ bool find_block(const Args& a, int block, Place& p) {
         if (s0 + lane < a.w.S) {
             bool bad;
             q = q4p::seq_of(a.w, s0 + lane, bad);
-            if (bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(a.w.err, q4d::kErrDeviceCheck);
         }
         const int own = q.n > 0 ? (q.n * a.G + a.BM - 1) / a.BM : 0;
         int sum = own;
@@ -416,6 +414,18 @@ __device__ __forceinline__ bool find_block(const Args& a, int block, Place& p) {
         block -= __shfl_sync(0xffffffffu, sum, 31);
     }
     return false;
+}
+
+// Latches sequences whose sizes do not fit.  find_block stops at its own
+// sequence, so the blocks share all of them: a warp of each looks at every
+// gridDim.x-th 32.
+__device__ __forceinline__ void latch_bad(const Args& a) {
+#pragma unroll 1
+    for (int s = 32 * blockIdx.x + (threadIdx.x & 31); s < a.w.S; s += 32 * gridDim.x) {
+        bool bad;
+        q4p::seq_of(a.w, s, bad);
+        if (bad) atomicOr(a.w.err, q4d::kErrDeviceCheck);
+    }
 }
 
 template <int D, int WM, bool kTma, bool kClustered>
@@ -451,7 +461,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         rank = (int)blockIdx.x & (t.cluster - 1);
         Place& p = w.p;
         p.h = job % a.w.H;
-        if (!find_block(a, job / a.w.H, p)) return;  // (the whole cluster)
+        if (!find_block(a, job / a.w.H, p)) {  // (the whole cluster)
+            if (warp == 4) latch_bad(a);
+            return;
+        }
         p.tiles = block_tiles(a, p.q, p.rb);
         p.tile = (int)((unsigned)(p.tiles * rank) >> t.cluster_log2);  // tiles * 16 stays below 2^31
         w.end = (int)((unsigned)(p.tiles * (rank + 1)) >> t.cluster_log2);
@@ -535,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (uint32_t i = kt > kStages ? kt - kStages : 0; i < kt; ++i)
                 q4d::mbar_wait(q4d::smem_addr(&B.full[i % kStages]), (i / kStages) & 1, nullptr);
         if constexpr (!kClustered) return;
+        latch_bad(a);  // (while the others take the last tiles)
     }
 
     // ----------------------------------------------------- scores and values

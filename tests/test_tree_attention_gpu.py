@@ -536,3 +536,34 @@ def test_infinities_and_nan_reach_what_sees_them_in_every_form(name, kind):
     for what in (np.isnan, np.isposinf, np.isneginf):
         assert np.array_equal(what(got), what(a)), (what, np.argwhere(what(got) != what(a))[:5])
     assert close(got[~odd], a[~odd], A[~odd]).all()
+
+
+# Few rows among many places go to clusters, which look no further than their own
+# sequence: a bad one behind it, with and without rows, is latched and left out.
+@pytest.mark.parametrize("S,n,bad", [(1, {0: 1}, 0), (2, {0: 1}, 1), (40, {s: 1 for s in range(40)}, 39),
+                                     (40, {s: 1 for s in range(40)}, 0), (512, {0: 1, 1: 2}, 511),
+                                     (512, {0: 1, 511: 1}, 511), (300, {7: 3}, 290)])
+@pytest.mark.parametrize("what", ["ctx", "room", "end"])
+def test_clusters_latch_a_bad_sequence_wherever_it_stands(S, n, bad, what):
+    g = np.random.default_rng(S + bad)
+    rows = [n.get(s, 0) for s in range(S)]
+    b = Batch(g, [int(x) for x in g.integers(1, 60, S)], rows, 1, 64, 16)
+    q = rand16(g, b.rows, 2, 64)
+    sees = seen_by(b, "causal", g)
+    a, A = expected(b, q, sees)
+    c = b.to_device(q4)
+    if what == "end" and bad == S - 1:
+        b.dstart[S] = b.rows + 5  # more rows than the call has (two among them that belong to nobody)
+    elif what == "room":
+        b.dctx[bad] = 16 * b.max_pages + 1 - rows[bad]
+    else:
+        b.dctx[bad] = -1
+    out = attend(b, c, q, "causal", sees)
+    assert q4.q4_device_status() == -7
+    got = out.cpu().numpy()[:b.rows].reshape(a.shape)
+    mine = slice(b.start[bad], b.start[bad + 1])
+    assert np.all(got[mine] == -5.0)
+    ok = close(got, a, A)
+    ok[mine] = True
+    assert ok.all()
+    assert q4.q4_device_status() == 0
