@@ -153,14 +153,21 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_
                 if (!bad && row >= q.start && row < q.start + q.n) {
                     slot = q.ctx + (row - q.start);
                     base = row_at(p.w, s, slot, 0, D);
+                    if (base < 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
                 }
-                if (base < 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
             }
             slot_s = slot;
             base_s = base;
         }
     } else if (tid >= 64 && tid < 64 + half && p.positions) {
         angle(tid - 64, p.positions[row]);
+    } else if (tid >= 128 && row == 0) {
+        // the first row's block latches the sequences that do not fit
+        for (int s = tid - 128; s < p.w.S; s += kAppendThreads - 128) {
+            bool bad;
+            seq_of(p.w, s, bad);
+            if (bad) atomicOr(p.w.err, q4d::kErrDeviceCheck);
+        }
     }
     __syncthreads();
     const int slot = slot_s;

@@ -279,3 +279,75 @@ def test_accept_bad_sizes_and_pages():
     c = b.to_device(q4)
     acc, *_ = run_accept(b, c, [1] * (n + 2), [i - 1 for i in range(n)] + [-1, 0], [1] * (n + 2), 1)
     assert q4.q4_device_status() == -7 and acc.tolist() == [-9, 2]
+
+
+# ---------------------------------------- which sequences and rows are whose ---
+
+def append_rows(b, c, k, v, rows):
+    """One append of k, v (its queries a copy of k, left as -3 where nobody's); the pools before it, the queries out."""
+    before = b.dk.clone(), b.dv.clone()
+    qo = torch.full((rows, k.shape[1]), -3.0, dtype=torch.float16, device="cuda")
+    q4.q4_paged_append(c, b.dctx, b.dstart, rows, torch_dev(k), torch_dev(v), q=torch_dev(k), q_out=qo, n_q_heads=b.Hkv)
+    return before, qo.cpu().numpy()
+
+
+def check_stored(b, k, v, before, qo, good):
+    """The rows of the sequences in `good` {s: (first row, rows)} are stored, and nothing else."""
+    mine = np.zeros(len(qo), bool)
+    for s, (start, n) in good.items():
+        at, rows = b.ctx[s] + np.arange(n), slice(start, start + n)
+        mine[rows] = True
+        for dev, x in ((b.dk, k), (b.dv, v)):
+            assert np.array_equal(b.rows_of(dev.cpu().numpy()[0], s, at).reshape(n, -1), x[rows]), s
+    assert np.array_equal(qo[mine], k[mine]) and np.all(qo[~mine] == -3.0)
+    for dev, was in ((b.dk, before[0]), (b.dv, before[1])):
+        same = (dev.view(torch.int16) == was.view(torch.int16)).cpu().numpy()
+        for s, (_, n) in good.items():
+            at = b.ctx[s] + np.arange(n)
+            same[0, b.table[s][at // b.page], :, at % b.page] = True
+        assert same.all()
+
+
+def test_rows_before_the_first_sequence_belong_to_nobody():
+    g = np.random.default_rng(41)
+    b = Batch(g, [4, 9, 0], [2, 3, 1], 2, 64, 8)
+    c = b.to_device(q4)
+    b.dstart += 3
+    k, v = rand16(g, 11, 128), rand16(g, 11, 128)
+    before, qo = append_rows(b, c, k, v, 11)
+    assert q4.q4_device_status() == 0
+    check_stored(b, k, v, before, qo, {0: (3, 2), 1: (5, 3), 2: (8, 1)})
+    # the attention and the acceptance take the same rows
+    out = torch.full((11, 128), -3.0, dtype=torch.float16, device="cuda")
+    ws = torch.empty(q4.q4_tree_attention_workspace_bytes(64), dtype=torch.uint8, device="cuda")
+    q4.q4_tree_attention(c, b.dctx, b.dstart, 11, torch_dev(k), 2, out, ws, ws.numel())
+    assert q4.q4_device_status() == 0
+    got = out.cpu().numpy()
+    assert np.all(got[:3] == -3.0) and np.all(got[9:] == -3.0)
+    kc, vc = b.dk.cpu().numpy()[0], b.dv.cpu().numpy()[0]
+    for s, (ctx, n) in enumerate(zip(b.ctx, b.n)):
+        at, rows = np.arange(ctx + n), slice(3 + b.start[s], 3 + b.start[s + 1])
+        a, A = oracle.tree_attention(k[rows].reshape(n, 2, 64), b.rows_of(kc, s, at), b.rows_of(vc, s, at),
+                                     np.tril(np.ones((n, ctx + n), bool), ctx))
+        assert np.all(np.abs(got[rows].reshape(a.shape) - a) <= 5.5e-4 * A + ulp16(a))
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    acc, path, nxt, ctx_out = ints(9, 9, 9), ints(*[9] * 11), ints(9, 9, 9), ints(9, 9, 9)
+    q4.q4_tree_accept(c, b.dctx, b.dstart, 11, ints(*[1] * 11), ints(9, 9, 9, -1, 0, -1, 0, 1, -1, 9, 9), ints(*[1] * 11),
+                      acc, path, nxt, ctx_out)
+    assert q4.q4_device_status() == 0
+    assert acc.tolist() == [2, 3, 1] and path.tolist() == [9, 9, 9, 0, 1, 0, 1, 2, 0, 9, 9]
+
+
+@pytest.mark.parametrize("S,bad", [(3, 1), (40, 39), (700, 650), (2, 0)])
+def test_append_latches_a_bad_sequence_without_rows(S, bad):
+    g = np.random.default_rng(42)
+    n = [1 if s < 2 else 0 for s in range(S)]
+    n[bad] = 0
+    b = Batch(g, [5] * S, n, 1, 64, 8)
+    c = b.to_device(q4)
+    b.dctx[bad] = -2
+    k, v = rand16(g, b.rows, 64), rand16(g, b.rows, 64)
+    before, qo = append_rows(b, c, k, v, b.rows)
+    assert q4.q4_device_status() == -7
+    check_stored(b, k, v, before, qo, {s: (int(b.start[s]), n[s]) for s in range(S) if n[s]})
+    assert q4.q4_device_status() == 0
