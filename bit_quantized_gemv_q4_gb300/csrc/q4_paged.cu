@@ -50,7 +50,8 @@ struct AppendArgs {
 };
 
 // Sequence of a row: the number of sequences whose end is at or before it, by
-// a search 32 ways wide (one load per lane and level).  All lanes get it.
+// a search 32 ways wide (one load per lane and level).  All lanes get it.  Where
+// the starts are not in order it can be another (or none): the caller checks.
 __device__ __forceinline__ int seq_of_row(const View& w, int row, int lane) {
     int lo = 0, len = w.S;
     while (len > 0) {
@@ -62,6 +63,40 @@ __device__ __forceinline__ int seq_of_row(const View& w, int row, int lane) {
         len = min(stride - 1, len - c * stride);
     }
     return lo;
+}
+
+// Where a row goes.
+constexpr int kNobody = 0x7fffffff;
+struct At {
+    long long base;  // head 0's row in the pools (-1: no memory)
+    int slot;        // position
+    int seq;         // sequence (kNobody: nobody's row)
+};
+
+__device__ __forceinline__ bool holds(const View& w, int s, int row, Seq& q) {
+    bool bad;
+    q = seq_of(w, s, bad);
+    return !bad && row >= q.start && row < q.start + q.n;
+}
+__device__ __forceinline__ void place(const View& w, const Seq& q, int row, int D, At& at) {
+    at.slot = q.ctx + (row - q.start);
+    at.base = row_at(w, at.seq, at.slot, 0, D);
+    if (at.base < 0) atomicOr(w.err, q4d::kErrDeviceCheck);
+}
+
+// By the whole block, where the search has found nobody: a row that is nobody's,
+// or a search led astray by a sequence that does not fit.  Takes the first of all
+// sequences that holds the row, false if none does.
+__device__ __noinline__ bool find_holder(const View& w, int row, int D, At& at) {
+    __syncthreads();  // all have seen that it found nobody
+    Seq q;
+    for (int s = threadIdx.x; s < w.S; s += kAppendThreads)
+        if (holds(w, s, row, q)) atomicMin(&at.seq, s);
+    __syncthreads();
+    if (at.seq == kNobody) return false;
+    if (threadIdx.x == 0 && holds(w, at.seq, row, q)) place(w, q, row, D, at);
+    __syncthreads();
+    return true;
 }
 
 __device__ __forceinline__ float h2f(uint32_t w, int hi) {
@@ -92,8 +127,7 @@ constexpr int kAhead = 2;
 template <int D, int kPairs>
 __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_constant__ AppendArgs p) {
     __shared__ __align__(16) float2 cs[D / 2];
-    __shared__ long long base_s;  // head 0's row in the pools (-1: no memory)
-    __shared__ int slot_s;        // the row's position (-1: nobody's row)
+    __shared__ At at_s;
     const int row = blockIdx.x, tid = threadIdx.x;
     constexpr int NC = D / 8;
     const int half = p.rot / 2, rc = half / 8;          // kPairs 1: chunks of a half
@@ -145,19 +179,10 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_
     if (tid < 32) {
         const int s = seq_of_row(p.w, row, tid);
         if (tid == 0) {
-            int slot = -1;
-            long long base = -1;
-            if (s < p.w.S) {
-                bool bad;
-                const Seq q = seq_of(p.w, s, bad);
-                if (!bad && row >= q.start && row < q.start + q.n) {
-                    slot = q.ctx + (row - q.start);
-                    base = row_at(p.w, s, slot, 0, D);
-                    if (base < 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
-                }
-            }
-            slot_s = slot;
-            base_s = base;
+            Seq q;
+            const bool mine = s < p.w.S && holds(p.w, s, row, q);
+            at_s.seq = mine ? s : kNobody;
+            if (mine) place(p.w, q, row, D, at_s);
         }
     } else if (tid >= 64 && tid < 64 + half && p.positions) {
         angle(tid - 64, p.positions[row]);
@@ -170,13 +195,13 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_
         }
     }
     __syncthreads();
-    const int slot = slot_s;
-    if (slot < 0) return;
+    if (at_s.seq == kNobody && !find_holder(p.w, row, D, at_s)) return;
+    const int slot = at_s.slot;
     if (!p.positions && half > 0) {
         if (tid < half) angle(tid, slot);
         __syncthreads();
     }
-    const long long base = base_s, head_step = (long long)p.w.div.d * D;
+    const long long base = at_s.base, head_step = (long long)p.w.div.d * D;
     const auto finish = [&](const Item& t, uint4 a, const uint4& b) {
         uint16_t* dst = t.kind == 0   ? p.q_out + row * p.ldqo + (long long)t.h * D
                         : t.kind == 1 ? p.w.k + base + t.h * head_step

@@ -351,3 +351,25 @@ def test_append_latches_a_bad_sequence_without_rows(S, bad):
     assert q4.q4_device_status() == -7
     check_stored(b, k, v, before, qo, {s: (int(b.start[s]), n[s]) for s in range(S) if n[s]})
     assert q4.q4_device_status() == 0
+
+
+@pytest.mark.parametrize("S", [3, 40, 1200])
+def test_append_stores_good_sequences_around_bad_ones(S):
+    # ends too large, starts out of order: only the sequence concerned is left out
+    g = np.random.default_rng(43)
+    n = [4] * S
+    b = Batch(g, [int(x) for x in g.integers(0, 20, S)], n, 1, 64, 8)
+    c = b.to_device(q4)
+    start = b.start.copy()
+    first = [0] if S == 3 else [int(x) for x in g.choice(S // 2, S // 8, replace=False) * 2]  # (their neighbours stay)
+    good = {s: (int(start[s]), 4) for s in range(S)}
+    for s in first:
+        start[s + 1] = 99999  # s ends behind the rows, s + 1 begins there
+        good.pop(s)
+        good.pop(s + 1, None)
+    b.dstart.copy_(torch_dev(start))
+    k, v = rand16(g, b.rows + 3, 64), rand16(g, b.rows + 3, 64)
+    before, qo = append_rows(b, c, k, v, b.rows + 3)
+    assert q4.q4_device_status() == -7
+    check_stored(b, k, v, before, qo, good)
+    assert q4.q4_device_status() == 0
