@@ -158,20 +158,19 @@ constexpr float kZ1 = 0.0108304247f, kZ2 = -5.86490495e-05f, kZ3 = 2.11731307e-0
 
 // round(2^44 2^-t).  The passes over a row (two_of below) do the same
 // operations on two logits at a time, so a token has one weight.
-template <bool kExact>
 __device__ __forceinline__ u64 weight_of(float l, const Scale& c, const float2* pow64) {
     if (l == c.max) return kOne;
     // d + de = max - l exactly (the error of a difference is a float)
     const float d = c.max - l;
     if (!(d * c.hi < kEnd)) return 0;
     const float b = d - c.max;
-    const float de = kExact ? (c.max - (d - b)) + (-l - b) : 0.f;
+    const float de = (c.max - (d - b)) + (-l - b);
     // 64 t = k + r, |r| <= 1/2 and a little: the product less k is one fused
     // operation, so nothing of it is lost; then its smaller parts
     const float hi = c.hi * 64.f, lo = c.lo * 64.f;  // exact
     const float kf = fmaf(d, hi, kMagic);
     float r = fmaf(d, hi, -(kf - kMagic));
-    if (kExact) r = fmaf(de, hi, r);
+    r = fmaf(de, hi, r);
     r = fmaf(d, lo, r);
     // 2^(-r/64) = 1 - y, y = z - z^2 / 2 + z^3 / 6, z = r ln2 / 64 < 0.0055;
     // the next term is below 2^-34
@@ -179,14 +178,12 @@ __device__ __forceinline__ u64 weight_of(float l, const Scale& c, const float2* 
     return (u64)short_weight(kf, y, pow64) << left(magic_int(kf));
 }
 
-// k (as kMagic + k) and y of two logits (max finite).  `exact`: the difference's
-// rounding error counts too; of half-precision logits it does not (it is zero
-// but for logits 2^13 times smaller than the greatest, where it is below 2^-28
-// of a weight).
+// k (as kMagic + k) and y of two logits (max finite).  The difference's rounding
+// error counts for half-precision logits as well: some 2^13 times smaller than
+// the greatest they lose bits in it, up to 2^-20 of a weight.
 struct Two {
     float2 kf, y;
 };
-template <bool kExact>
 __device__ __forceinline__ Two two_of(float2 l, const Scale& c) {
     const float2 mx = make_float2(c.max, c.max), neg = make_float2(-1.f, -1.f);
     const float2 hi = make_float2(c.hi * 64.f, c.hi * 64.f), lo = make_float2(c.lo * 64.f, c.lo * 64.f);
@@ -194,13 +191,11 @@ __device__ __forceinline__ Two two_of(float2 l, const Scale& c) {
     const float2 d = __ffma2_rn(l, neg, mx);
     const float2 kf = __ffma2_rn(d, hi, mg);
     float2 r = __ffma2_rn(d, hi, __ffma2_rn(kf, neg, mg));
-    if (kExact) {
-        const float2 b = __fadd2_rn(d, make_float2(-c.max, -c.max));
-        const float2 db = __ffma2_rn(b, neg, d);                      // d - b
-        const float2 e0 = __ffma2_rn(db, neg, mx);                    // max - (d - b)
-        const float2 e1 = __ffma2_rn(__fadd2_rn(l, b), neg, e0);      // ... + (-l - b)
-        r = __ffma2_rn(e1, hi, r);
-    }
+    const float2 b = __fadd2_rn(d, make_float2(-c.max, -c.max));
+    const float2 db = __ffma2_rn(b, neg, d);                  // d - b
+    const float2 e0 = __ffma2_rn(db, neg, mx);                // max - (d - b)
+    const float2 e1 = __ffma2_rn(__fadd2_rn(l, b), neg, e0);  // ... + (-l - b)
+    r = __ffma2_rn(e1, hi, r);
     r = __ffma2_rn(d, lo, r);
     const float2 q = __ffma2_rn(r, __ffma2_rn(r, make_float2(kZ3, kZ3), make_float2(kZ2, kZ2)), make_float2(kZ1, kZ1));
     return {kf, __fmul2_rn(r, q)};
@@ -405,7 +400,7 @@ __device__ void sort_and_scan(Shared& s, u64* all, u64* pre, int n, const Scale&
     u64 before = 0;
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + threadIdx.x;
-        const u64 w = i < n ? weight_of<!HALF>(key_value((uint32_t)(all[i] >> 32)), c, s.pow64) : 0;
+        const u64 w = i < n ? weight_of(key_value((uint32_t)(all[i] >> 32)), c, s.pow64) : 0;
         const u64 run = before + block_scan(w, s);
         if (i < n) pre[i] = run;
         __syncthreads();
@@ -664,7 +659,7 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
             const uint32_t k = key_of(l);
             const int st = steps_of(l, c);
             if (k == kLeast || st < s0 || st >= s1 || (shift < 24 && k >> (shift + 8) != prefix >> (shift + 8))) return;
-            t.add(s, 255 - (int)(k >> shift & 255u), weight_of<!HALF>(key_value(k), c, s.pow64));
+            t.add(s, 255 - (int)(k >> shift & 255u), weight_of(key_value(k), c, s.pow64));
         });
         t.flush(s);
         join_histogram(s, cl, 256);
@@ -675,7 +670,7 @@ __device__ Hit search_bin(const Part<HALF>& row, Shared& s, Cluster& cl, const S
         wb += w0;
         prefix |= (uint32_t)(255 - b) << shift;
     }
-    h.own = weight_of<!HALF>(key_value(prefix), c, s.pow64);
+    h.own = weight_of(key_value(prefix), c, s.pow64);
     u64 place = by_count ? target - nb - 1 : h.own ? (target - wb - 1) / h.own : 0;  // among the equal keys
     if (place >= equal) place = equal - 1;
     h.weight = wb + (place + 1) * h.own;
@@ -850,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         // (whether min_p keeps any of the tail: by the greatest weight of its first step)
         const bool keeps = least_w && (u64)short_weight(kMagic + (float)cut, -0.0055f, s.pow64) << left(cut) >= least_w;
         row.template pairs<1>([&](float2 l, int i) {
-            const Two x = two_of<!HALF>(l, c);
+            const Two x = two_of(l, c);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float kf = e ? x.kf.y : x.kf.x;
@@ -952,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
                 row.template each<1>([&](float l, int) {
                     const int st = steps_of(l, c);
                     if (st >= cut && st < kSteps)
-                        add_tail(s, min(st - cut, kBins - 1), (uint32_t)(weight_of<!HALF>(l, c, s.pow64) >> left(st)));
+                        add_tail(s, min(st - cut, kBins - 1), (uint32_t)(weight_of(l, c, s.pow64) >> left(st)));
                 });
                 cl.sync();
             }
@@ -975,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             Tally t;
             row.template each<1>([&](float l, int) {
                 if (!(l > -INFINITY)) return;
-                const u64 w = weight_of<!HALF>(l, c, s.pow64);
+                const u64 w = weight_of(l, c, s.pow64);
                 if (w == 0) return;
                 t.add(s, steps_of(l, c) >> 1, w);
             });
@@ -987,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             sums[0] = 0;
             row.template each<1>([&](float l, int) {
                 if (!(l > -INFINITY)) return;
-                const u64 w = weight_of<!HALF>(l, c, s.pow64);
+                const u64 w = weight_of(l, c, s.pow64);
                 if (w >= least_w) sums[0] += w;
             });
             u64 one[1] = {sums[0]};

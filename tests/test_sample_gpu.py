@@ -244,3 +244,21 @@ def test_all_limits_in_turn_over_kinds_of_rows(kind, dtype):
             t, q = oracle.sample(x[r], float(T[r]), int(k[r]), float(p[r]), float(m[r]), float(u[r]))
             assert tok[r] == t, (V, r, tok[r], t)
             assert abs(pr[r] - q) <= 2.0 ** -23 * q + 2.0 ** -43, (V, r, pr[r], q)  # (as in check)
+
+
+@pytest.mark.parametrize("top", [8.0078125, 12.0, 2.5])
+@pytest.mark.parametrize("V", [3000, 20001])
+def test_half_logits_far_smaller_than_the_greatest(top, V):
+    """Logits whose difference to the greatest no float holds: multiples of 2^-24
+    under a greatest logit of 2.5 to 12.  Left out, the lost bits come to 2^-21 of
+    such a weight; check allows 2^-23."""
+    g = np.random.default_rng(V)
+    for low in (7, -7, 5, None):
+        x = np.empty((6, V), np.float16)
+        x[:] = (np.full((6, V), low) if low else g.integers(-7, 8, (6, V))) * 2.0 ** -24
+        x[:, V // 2] = top
+        u = ((np.arange(6) + 0.5) / 6).astype(np.float32)
+        u[3:] = 1 - (1 - u[3:]) * np.float32(0.02)
+        check(x, u=u)
+        check(x, u=u, top_p=0.9999)
+        check(x, u=u, top_k=2000)
