@@ -63,7 +63,9 @@ constexpr int kList = 1024;          // tokens of a CTA's list
 constexpr int kAll = 2048;           // tokens of the joined list
 constexpr int kBinList = 1024;       // tokens of a bin that are sorted together
 constexpr int kCounting = 256;       // up to here a sort counts, per token, the greater ones (one row 14 us, bitonic 19)
-constexpr int kMostPart = 1 << 17;   // tokens of a CTA: sums of 15-bit parts of their weights stay below 2^32
+// Tokens of a CTA, so that sums of 15-bit parts of their weights stay below 2^32:
+// with its last vector and up to 7 single elements a part has 2^17 - 1 at most.
+constexpr int kMostPart = (1 << 17) - 8;
 constexpr int kCut = 512;            // bins of the threshold: 16 per octave (4 steps)
 constexpr int kBins = 1536;          // bins of a histogram: a step each from the threshold on, or two steps from t = 0 on
 constexpr u64 kOne = 1ull << 44;     // the weight of the greatest logit

@@ -262,3 +262,26 @@ def test_half_logits_far_smaller_than_the_greatest(top, V):
         check(x, u=u)
         check(x, u=u, top_p=0.9999)
         check(x, u=u, top_k=2000)
+
+
+def test_equal_weights_of_the_longest_part_add_up():
+    """Rows that begin one half behind a 16-byte boundary give the last of four
+    CTAs 2^17 + 7 equal logits below the list; at these temperatures (found by
+    evaluating the weight's operations in exact arithmetic) the 15 low bits of their
+    weight are all set, which no 32-bit sum of as many holds."""
+    V, R = 1 << 19, 48  # (as many rows as leave four CTAs to each)
+    temps = [0.7507458329200745, 0.7530942559242249, 0.7561022043228149, 0.7603664398193359, 0.7634600400924683,
+             0.7695407867431641]
+    x = np.full((R, V + 1), -np.inf, np.float16)
+    x[:, 0] = 0.0
+    rows = list(range(7, R, 8))
+    for r in rows:
+        x[r, 1:1601:8] = 0.0
+        x[r, 1 + 8 * ((V // 8 - 1) * 3 // 4):] = -1.0
+    T, u = np.ones(R, np.float32), np.full(R, 0.5, np.float32)
+    T[rows], u[rows] = temps, [0.3, 0.5, 0.9, 0.99, 0.999, 0.99999]
+    tok, pr = sample(x, ld=V + 1, vocab=V, temperature=T, u=u)
+    for r in rows:
+        t, p = oracle.sample(x[r, :V], float(T[r]), u=float(u[r]))
+        assert tok[r] == t, (r, tok[r], t)
+        assert abs(pr[r] - p) <= 2.0 ** -23 * p + 2.0 ** -43
