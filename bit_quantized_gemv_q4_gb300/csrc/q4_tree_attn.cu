@@ -41,8 +41,10 @@ constexpr int kMaxRows = 64;   // rows of a job
 constexpr int kMaxCtas = 512;
 constexpr int kTcRows = 256, kMaxTcCtas = 160;
 // P = 2^(s - m + kShift): fp16 keeps 11 bits of a probability down to 2^-26
-// of the row's greatest, and O / l is the same quotient.
-constexpr float kShift = 12.f;
+// of the row's greatest (below, it is off by 2^-37 of that at most), and O / l
+// is the same quotient.  The tcgen05 kernel lets the greatest score exceed m by
+// kLag, so P reaches 2^15.
+constexpr float kShift = 12.f, kLag = 3.f;
 
 struct Args {
     View w;
@@ -1189,8 +1191,7 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
 // the commit behind S(k + 1) tells the softmax that O holds step k's product.
 // Tensor memory (512 columns): S 0 and 1 (128 each), O 0 and 1.
 // The reference maximum of a row moves only when its maximum exceeds it by
-// more than 8 (a factor 2^8); then O and l are rescaled.  With kTcShift P
-// reaches 2^15 and keeps 11 bits down to 2^-29 of the row's greatest at worst.
+// more than kLag (a factor 2^3); then O and l are rescaled.
 // Key and value tiles come by TMA as boxes of `box` rows (the greatest power
 // of two, 8 .. 128, that divides the page): a box lies in one page.  A page
 // that does not exist is read outside the map, where TMA fills in zeros.
@@ -1204,7 +1205,6 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
 // tensor memory out: some 5 us) are what short contexts cost.
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1
-constexpr float kTcShift = 7.f;
 // Units of a tile, with two row streams and with alternate tiles (8 : 8 instead:
 // trees 101 us, 8 : 4: 96), and of a job before its tiles.  us with lead 0 / 16 /
 // 32: 64 trees of 30 over 1000 positions 113 / 66 / 64, 8 trees of 40 up to 8000
@@ -1625,11 +1625,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     max_half();
                     const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * a.c;
                     float corr = 1.f;
-                    if (mx > m + 8.f) {
+                    if (mx > m + kLag) {
                         corr = m == -INFINITY ? 1.f : ex2(m - mx);  // nothing seen yet: O and l are zero
                         m = mx;
                     }
-                    const float sub = kTcShift - (m == -INFINITY ? 0.f : m);
+                    const float sub = kShift - (m == -INFINITY ? 0.f : m);
                     const float2 ss = make_float2(sub, sub);
                     float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
                     const auto exp_half = [&](int h) {

@@ -656,7 +656,8 @@ q4_status q4_paged_append(const q4_paged_append_desc *desc, q4_stream_t stream);
  * decoding of a batch.  a = sum_j softmax_j(scale q . k_j) v_j with the heads
  * paired as in section 6 (any number of query heads per kv head), fp32
  * scores, statistics and sums; the probabilities enter the value product as
- * fp16 (error below 5e-4 * sum_j p_j |v_j|).  A row that sees nothing gets
+ * fp16, p_j off by 2^-11 p_j at most, or by 2^-37 of the row's greatest where
+ * that is more (p_j below 2^-26 of it).  A row that sees nothing gets
  * zeros.  What a row does not see never reaches it, NaN and infinities
  * included.  q and out: fp16 [rows][n_q_heads * head_dim], strides as in 7b,
  * 16-byte aligned; they must not overlap.  The workspace is written and read

@@ -567,3 +567,21 @@ def test_clusters_latch_a_bad_sequence_wherever_it_stands(S, n, bad, what):
     ok[mine] = True
     assert ok.all()
     assert q4.q4_device_status() == 0
+
+
+@pytest.mark.parametrize("n,G,page", [(1, 1, 64), (3, 4, 16), (20, 1, 7), (40, 2, 7), (40, 1, 64), (200, 1, 16), (9, 8, 128)])
+def test_small_probabilities_beside_dominant_ones_in_every_form(n, G, page):
+    # every 64th position has a score 17.0 above the others' (e^-17 = 2^-24.5) and
+    # no value: what comes out is the small probabilities' share alone
+    g = np.random.default_rng(44)
+    b = Batch(g, [3000], [n], 1, 128, page)
+    at = np.arange(3000 + n)
+    where = b.table[0][at // page], 0, at % page
+    b.k[0][where] = np.where(at[:, None] % 64 == 0, 1.5, 0.0)
+    b.v[0][where] = np.where(at[:, None] % 64 == 0, 0.0, 4096 * (1 + g.random((3000 + n, 128))))
+    q = np.ones((n, G, 128), np.float16)
+    sees = seen_by(b, "causal", g)
+    a, A = expected(b, q, sees)
+    assert np.all(a > 2.0 ** -8)
+    check(attend(b, b.to_device(q4), q, "causal", sees), b, q, a, A)
+    assert q4.q4_device_status() == 0
