@@ -153,3 +153,22 @@ def test_binding_without_a_device_gives_the_library_s_error(L):
         q4.q4_sample(FAKE, q4.Q4_F32, 1, 64, FAKE)
     with pytest.raises(q4.Q4Error, match="vocab"):
         q4.q4_sample(FAKE, q4.Q4_F32, 1, 0, FAKE)
+
+
+def test_positions_leave_room_for_a_tile_below_2_31(L):
+    # the attention rounds a sequence's length up to tiles of 128 positions in 32 bits
+    append = q4.q4_paged_append_desc(cache(), FAKE, FAKE, 0, None, FAKE, FAKE, 0, 0, None, None, 0, 0, 0, None, 0, 0, 1.0)
+    attend = q4.q4_tree_attention_desc(cache(), FAKE, FAKE, 0, None, 0, FAKE, FAKE, 0, 0, 4, 0.0, FAKE,
+                                       L.q4_tree_attention_workspace_bytes(128))
+    accept = q4.q4_tree_accept_desc(cache(), FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, 0)
+    for pages, size in ((4, (1 << 29) - 31), ((1 << 25) - 1, 64), ((1 << 31) - 127, 1), (1, (1 << 31) - 1)):
+        for call, d in ((L.q4_paged_append, append), (L.q4_tree_attention, attend), (L.q4_tree_accept, accept)):
+            d.cache = cache(max_pages=pages, page_size=size)
+            assert call(ctypes.byref(d), None) == -2, (pages, size)
+    for pages, size in ((4, (1 << 29) - 32), ((1 << 25) - 2, 64), ((1 << 31) - 128, 1), (1, (1 << 31) - 128)):
+        # (no rows: with a device the call ends before it reads anything)
+        for call, d in ((L.q4_paged_append, append), (L.q4_tree_attention, attend)):
+            d.cache = cache(max_pages=pages, page_size=size)
+            assert call(ctypes.byref(d), None) in (0, -6), (pages, size, L.q4_last_error())
+            n = pages * size  # the last tile's end
+            assert (n + 127) // 128 * 128 < 1 << 31
