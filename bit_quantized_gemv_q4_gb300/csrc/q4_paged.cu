@@ -401,8 +401,7 @@ extern "C" q4_status q4_paged_append(const q4_paged_append_desc* desc, q4_stream
     const int D = d.cache.head_dim;
     if (!d.k || !d.v || (d.q && !d.q_out) || (d.q_out && !d.q)) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
     if (d.q ? d.n_q_heads < 1 : d.n_q_heads < 0) return fail(Q4_ERR_INVALID_ARG, "n_q_heads=%d", d.n_q_heads);
-    if ((long long)d.n_q_heads * D > (1 << 24) || (long long)d.cache.n_kv_heads * D > (1 << 24))
-        return fail(Q4_ERR_UNSUPPORTED, "%d query and %d kv heads", d.n_q_heads, d.cache.n_kv_heads);
+    if ((long long)d.n_q_heads * D > (1 << 24)) return fail(Q4_ERR_UNSUPPORTED, "%d query heads", d.n_q_heads);
     if (d.rot_dim < 0 || d.rot_dim > D || d.rot_dim % 2) return fail(Q4_ERR_INVALID_ARG, "rot_dim=%d of %d", d.rot_dim, D);
     if ((d.rot_dim > 0) != (d.freqs != nullptr)) return fail(Q4_ERR_INVALID_ARG, "freqs and rot_dim go together");
     if (d.layout != Q4_ROPE_HALF && d.layout != Q4_ROPE_INTERLEAVED) return fail(Q4_ERR_INVALID_ARG, "layout=%d", (int)d.layout);
@@ -459,7 +458,6 @@ extern "C" q4_status q4_tree_accept(const q4_tree_accept_desc* desc, q4_stream_t
         (unsigned long long)d.cache.n_pages * d.cache.page_size * d.cache.n_kv_heads * d.cache.head_dim;
     if (d.n_layers > 1 && d.layer_stride < pool)
         return fail(Q4_ERR_INVALID_ARG, "layer_stride=%zu, a layer's pool has %llu elements", d.layer_stride, pool);
-    if (d.cache.n_seqs > (1 << 27)) return fail(Q4_ERR_UNSUPPORTED, "n_seqs=%d", d.cache.n_seqs);
     const DeviceInfo* dev = nullptr;
     if ((st = current_device(&dev)) != Q4_OK) return st;
     a.w.err = dev->err_word;

@@ -78,6 +78,8 @@ inline q4_status paged_view(const q4_paged_cache& c, const int32_t* ctx_len, con
         return fail(Q4_ERR_INVALID_ARG, "n_pages=%d page_size=%d n_kv_heads=%d n_seqs=%d max_pages=%d rows=%d", c.n_pages,
                     c.page_size, c.n_kv_heads, c.n_seqs, c.max_pages, rows);
     if (c.head_dim != 64 && c.head_dim != 128) return fail(Q4_ERR_UNSUPPORTED, "head_dim=%d (64 or 128)", c.head_dim);
+    if ((long long)c.n_kv_heads * c.head_dim > (1 << 24) || c.n_seqs > (1 << 27))
+        return fail(Q4_ERR_UNSUPPORTED, "%d kv heads of %d, %d sequences", c.n_kv_heads, c.head_dim, c.n_seqs);
     // (the attention's tiles of up to 128 positions then end below 2^31 as well)
     if ((long long)c.max_pages * c.page_size > (1ll << 31) - 128)
         return fail(Q4_ERR_UNSUPPORTED, "max_pages=%d x page_size=%d positions (at most 2^31 - 128)", c.max_pages, c.page_size);

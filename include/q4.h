@@ -582,7 +582,8 @@ q4_status q4_attention(const q4_attention_desc *desc, q4_stream_t stream);
  * negative, more positions than max_pages * page_size) is left out, its
  * outputs untouched, and a page number outside [0, n_pages) stands for no
  * memory: nothing is written there and its rows read as zeros.  Both latch
- * Q4_ERR_DEVICE_CHECK.  max_pages * page_size must not exceed 2^31 - 128.
+ * Q4_ERR_DEVICE_CHECK.  max_pages * page_size must not exceed 2^31 - 128,
+ * n_kv_heads * head_dim (and n_q_heads * head_dim) 2^24, n_seqs 2^27.
  * ------------------------------------------------------------------------ */
 typedef struct q4_paged_cache {
     uint16_t *k;               /* both 16-byte aligned */

@@ -172,3 +172,16 @@ def test_positions_leave_room_for_a_tile_below_2_31(L):
             assert call(ctypes.byref(d), None) in (0, -6), (pages, size, L.q4_last_error())
             n = pages * size  # the last tile's end
             assert (n + 127) // 128 * 128 < 1 << 31
+
+
+def test_heads_and_sequences_that_pass_32_bits_are_refused(L):
+    # (a layer's columns of 16 bytes, the searches over the sequences and the grids are counted in 32 bits)
+    append = q4.q4_paged_append_desc(cache(), FAKE, FAKE, 0, None, FAKE, FAKE, 0, 0, None, None, 0, 0, 0, None, 0, 0, 1.0)
+    attend = q4.q4_tree_attention_desc(cache(), FAKE, FAKE, 0, None, 0, FAKE, FAKE, 0, 0, 1 << 26, 0.0, FAKE,
+                                       L.q4_tree_attention_workspace_bytes(128))
+    accept = q4.q4_tree_accept_desc(cache(), FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1, 0)
+    for bad in (dict(n_kv_heads=(1 << 17) + 1), dict(n_kv_heads=1 << 26), dict(n_seqs=(1 << 27) + 1),
+                dict(n_seqs=(1 << 31) - 1)):
+        for call, d in ((L.q4_paged_append, append), (L.q4_tree_attention, attend), (L.q4_tree_accept, accept)):
+            d.cache = cache(**bad)
+            assert call(ctypes.byref(d), None) == -2, bad
