@@ -50,6 +50,12 @@ inline cudaError_t ensure_smem_attr(const void* kern, std::atomic<int>* marks, i
     return cudaSuccess;
 }
 
+// Arrays of 32-bit numbers read or written on the device (NULL passes).
+template <typename... P>
+inline bool aligned4(const P*... p) {
+    return ((reinterpret_cast<uintptr_t>(p) % 4 == 0) && ...);
+}
+
 // Likewise the permission to launch clusters of more than 8 CTAs.
 inline cudaError_t ensure_wide_clusters(const void* kern, std::atomic<int>* done) {
     int dev = 0;

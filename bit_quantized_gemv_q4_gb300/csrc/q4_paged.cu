@@ -407,6 +407,7 @@ extern "C" q4_status q4_paged_append(const q4_paged_append_desc* desc, q4_stream
     if (d.layout != Q4_ROPE_HALF && d.layout != Q4_ROPE_INTERLEAVED) return fail(Q4_ERR_INVALID_ARG, "layout=%d", (int)d.layout);
     if (!(d.amplitude >= 0.f) || !(d.amplitude < INFINITY)) return fail(Q4_ERR_INVALID_ARG, "amplitude=%g", d.amplitude);
     if (reinterpret_cast<uintptr_t>(d.freqs) & 7u) return fail(Q4_ERR_MISALIGNED, "freqs must be 8-byte aligned");
+    if (!aligned4(d.positions)) return fail(Q4_ERR_MISALIGNED, "positions must be 4-byte aligned");
     const int wk = d.cache.n_kv_heads * D, wq = d.n_q_heads * D;
     if ((st = row_matrix("k", d.k, wk, &d.ldk)) != Q4_OK || (st = row_matrix("v", d.v, wk, &d.ldv)) != Q4_OK) return st;
     if (d.q && ((st = row_matrix("q", d.q, wq, &d.ldq)) != Q4_OK || (st = row_matrix("q_out", d.q_out, wq, &d.ldqo)) != Q4_OK))
@@ -452,6 +453,8 @@ extern "C" q4_status q4_tree_accept(const q4_tree_accept_desc* desc, q4_stream_t
     if (st != Q4_OK) return st;
     if (!d.accepted || !d.next_token || !d.ctx_out || (d.rows > 0 && (!d.draft || !d.parents || !d.sampled || !d.path)))
         return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned4(d.draft, d.parents, d.sampled, d.accepted, d.path, d.next_token, d.ctx_out))
+        return fail(Q4_ERR_MISALIGNED, "the int32 arrays must be 4-byte aligned");
     if (d.n_layers < 0 || d.n_layers > (1 << 16)) return fail(Q4_ERR_INVALID_ARG, "n_layers=%d", d.n_layers);
     if (d.layer_stride % 8) return fail(Q4_ERR_MISALIGNED, "layer_stride must be a multiple of 8");
     const unsigned long long pool =

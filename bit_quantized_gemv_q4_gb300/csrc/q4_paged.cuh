@@ -83,6 +83,8 @@ inline q4_status paged_view(const q4_paged_cache& c, const int32_t* ctx_len, con
     // (the attention's tiles of up to 128 positions then end below 2^31 as well)
     if ((long long)c.max_pages * c.page_size > (1ll << 31) - 128)
         return fail(Q4_ERR_UNSUPPORTED, "max_pages=%d x page_size=%d positions (at most 2^31 - 128)", c.max_pages, c.page_size);
+    if (!aligned4(c.page_table, ctx_len, row_start))
+        return fail(Q4_ERR_MISALIGNED, "page_table, ctx_len and row_start must be aligned to their elements");
     if (!aligned16(c.k) || !aligned16(c.v)) return fail(Q4_ERR_MISALIGNED, "the cache's pools must be 16-byte aligned");
     w->k = c.k;
     w->v = c.v;

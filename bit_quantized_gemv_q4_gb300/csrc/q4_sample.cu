@@ -1067,6 +1067,8 @@ extern "C" q4_status q4_sample(const q4_sample_desc* desc, q4_stream_t stream) {
     if (!d.logits || !d.tokens) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
     if (reinterpret_cast<uintptr_t>(d.logits) & (d.dtype == Q4_F16 ? 1u : 3u))
         return fail(Q4_ERR_MISALIGNED, "logits must be aligned to their elements");
+    if (!aligned4(d.temperature, d.top_k, d.top_p, d.min_p, d.u, d.tokens, d.probs))
+        return fail(Q4_ERR_MISALIGNED, "the rows' arrays must be 4-byte aligned");
     const DeviceInfo* dev = nullptr;
     const q4_status st = current_device(&dev);
     if (st != Q4_OK) return st;

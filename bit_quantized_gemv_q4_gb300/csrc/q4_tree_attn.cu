@@ -1858,7 +1858,7 @@ extern "C" q4_status q4_tree_attention(const q4_tree_attention_desc* desc, q4_st
     if (d.mask && d.mask_words < 1) return fail(Q4_ERR_INVALID_ARG, "mask_words=%d", d.mask_words);
     a.c = (d.scale == 0.f ? 1.f / sqrtf((float)D) : d.scale) * 1.4426950408889634f;
     if (!(a.c >= 1e-30f && a.c <= 1e30f)) return fail(Q4_ERR_INVALID_ARG, "scale=%g", d.scale);
-    if (reinterpret_cast<uintptr_t>(d.mask) & 3u) return fail(Q4_ERR_MISALIGNED, "mask must be 4-byte aligned");
+    if (!aligned4(d.mask)) return fail(Q4_ERR_MISALIGNED, "mask must be 4-byte aligned");
     if ((st = row_matrix("q", d.q, d.n_q_heads * D, &d.ldq)) != Q4_OK) return st;
     if ((st = row_matrix("out", d.out, d.n_q_heads * D, &d.ldo)) != Q4_OK) return st;
     if (reinterpret_cast<uintptr_t>(d.workspace) & 255u) return fail(Q4_ERR_MISALIGNED, "the workspace must be 256-byte aligned");

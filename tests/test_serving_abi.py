@@ -185,3 +185,27 @@ def test_heads_and_sequences_that_pass_32_bits_are_refused(L):
         for call, d in ((L.q4_paged_append, append), (L.q4_tree_attention, attend), (L.q4_tree_accept, accept)):
             d.cache = cache(**bad)
             assert call(ctypes.byref(d), None) == -2, bad
+
+
+def test_misaligned_arrays_are_refused(L):
+    # (a kernel that reads them would fault)
+    need = L.q4_tree_attention_workspace_bytes(128)
+    append = q4.q4_paged_append_desc(cache(), FAKE, FAKE, 4, FAKE, FAKE, FAKE, 0, 0, FAKE, FAKE, 0, 0, 4, FAKE, 128, 0, 1.0)
+    attend = q4.q4_tree_attention_desc(cache(), FAKE, FAKE, 4, FAKE, 1, FAKE, FAKE, 0, 0, 4, 0.0, FAKE, need)
+    accept = q4.q4_tree_accept_desc(cache(), FAKE, FAKE, 4, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 1, 0)
+    sample = q4.q4_sample_desc(FAKE, 0, 3, 1000, 0, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE)
+    for call, base, names in (
+            (L.q4_paged_append, append, ["ctx_len", "row_start", "positions"]),
+            (L.q4_tree_attention, attend, ["ctx_len", "row_start", "mask"]),
+            (L.q4_tree_accept, accept, ["ctx_len", "row_start", "draft", "parents", "sampled", "accepted", "path",
+                                        "next_token", "ctx_out"]),
+            (L.q4_sample, sample, ["temperature", "top_k", "top_p", "min_p", "u", "tokens", "probs"])):
+        for off in (1, 2, 3):
+            for name in names:
+                d = type(base).from_buffer_copy(base)
+                setattr(d, name, FAKE + off)
+                assert call(ctypes.byref(d), None) == -3, name
+            if base is not sample:
+                d = type(base).from_buffer_copy(base)
+                d.cache = cache(page_table=FAKE + off)
+                assert call(ctypes.byref(d), None) == -3
