@@ -1138,7 +1138,7 @@ inline int cluster_size(long long jobs, int seqs, long long positions, int sms) 
     return jobs * 8 <= 2 * sms - 16 ? 8 : jobs * 4 <= 2 * sms - 8 ? 4 : 0;
 }
 
-// box 0: no TMA.
+// box 0: no TMA.  (64 rows a job only without it: with it as many go to tcgen05.)
 template <int D, int WM>
 q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int box, cudaStream_t s) {
     MapArgs t;
@@ -1162,14 +1162,15 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
     t.cluster = cluster_size(jobs, c.n_seqs, (long long)c.max_pages * c.page_size, sms);
     t.cluster_log2 = t.cluster == 16 ? 4 : t.cluster == 8 ? 3 : 2;
     t.a = a;
+    const auto run = [&](auto tma) {
+        constexpr bool T = decltype(tma)::value;
+        return t.cluster ? launch_kernel<D, WM, T, true>(k, v, t, (int)jobs * t.cluster, s)
+                         : launch_kernel<D, WM, T, false>(k, v, t, a.ctas, s);
+    };
     cudaError_t e;
-    if (t.cluster) {
-        e = box ? launch_kernel<D, WM, true, true>(k, v, t, (int)jobs * t.cluster, s)
-                : launch_kernel<D, WM, false, true>(k, v, t, (int)jobs * t.cluster, s);
-    } else {
-        e = box ? launch_kernel<D, WM, true, false>(k, v, t, a.ctas, s) : launch_kernel<D, WM, false, false>(k, v, t, a.ctas, s);
-        if (e == cudaSuccess) e = launch_join(tree_join_kernel<D>, dim3((unsigned)a.ctas - 1, (unsigned)WM), a, s);
-    }
+    if constexpr (WM == 4) e = run(std::false_type{});
+    else e = box ? run(std::true_type{}) : run(std::false_type{});
+    if (!t.cluster && e == cudaSuccess) e = launch_join(tree_join_kernel<D>, dim3((unsigned)a.ctas - 1, (unsigned)WM), a, s);
     return e == cudaSuccess ? Q4_OK : q4i::cuda_fail(e, "q4_tree_attention launch");
 }
 
