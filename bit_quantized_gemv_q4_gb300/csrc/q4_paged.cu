@@ -399,7 +399,7 @@ extern "C" q4_status q4_paged_append(const q4_paged_append_desc* desc, q4_stream
     q4_status st = paged_view(d.cache, d.ctx_len, d.row_start, d.rows, &a.w);
     if (st != Q4_OK) return st;
     const int D = d.cache.head_dim;
-    if (!d.k || !d.v || (d.q && !d.q_out) || (d.q_out && !d.q)) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    if ((d.rows > 0 && (!d.k || !d.v)) || (d.q && !d.q_out) || (d.q_out && !d.q)) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
     if (d.q ? d.n_q_heads < 1 : d.n_q_heads < 0) return fail(Q4_ERR_INVALID_ARG, "n_q_heads=%d", d.n_q_heads);
     if ((long long)d.n_q_heads * D > (1 << 24)) return fail(Q4_ERR_UNSUPPORTED, "%d query heads", d.n_q_heads);
     if (d.rot_dim < 0 || d.rot_dim > D || d.rot_dim % 2) return fail(Q4_ERR_INVALID_ARG, "rot_dim=%d of %d", d.rot_dim, D);

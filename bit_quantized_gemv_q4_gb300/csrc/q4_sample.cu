@@ -1064,7 +1064,7 @@ extern "C" q4_status q4_sample(const q4_sample_desc* desc, q4_stream_t stream) {
     if (d.vocab > q4s::kMaxVocab) return fail(Q4_ERR_UNSUPPORTED, "vocab=%d above %d", d.vocab, q4s::kMaxVocab);
     if (d.ld != 0 && d.ld < d.vocab) return fail(Q4_ERR_INVALID_ARG, "row stride %d, vocab=%d", d.ld, d.vocab);
     if (d.rows > (1 << 26)) return fail(Q4_ERR_UNSUPPORTED, "rows=%d above %d", d.rows, 1 << 26);
-    if (!d.logits || !d.tokens) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (d.rows > 0 && (!d.logits || !d.tokens)) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
     if (reinterpret_cast<uintptr_t>(d.logits) & (d.dtype == Q4_F16 ? 1u : 3u))
         return fail(Q4_ERR_MISALIGNED, "logits must be aligned to their elements");
     if (!aligned4(d.temperature, d.top_k, d.top_p, d.min_p, d.u, d.tokens, d.probs))

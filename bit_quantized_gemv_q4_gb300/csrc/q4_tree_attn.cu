@@ -1850,7 +1850,7 @@ extern "C" q4_status q4_tree_attention(const q4_tree_attention_desc* desc, q4_st
     q4_status st = paged_view(d.cache, d.ctx_len, d.row_start, d.rows, &a.w);
     if (st != Q4_OK) return st;
     const int D = d.cache.head_dim;
-    if (!d.q || !d.out || !d.workspace) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    if ((d.rows > 0 && (!d.q || !d.out)) || !d.workspace) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
     if (d.n_q_heads < d.cache.n_kv_heads || d.n_q_heads % d.cache.n_kv_heads)
         return fail(Q4_ERR_INVALID_ARG, "n_q_heads=%d is not a multiple of n_kv_heads=%d", d.n_q_heads, d.cache.n_kv_heads);
     if ((long long)d.n_q_heads * D > (1 << 24)) return fail(Q4_ERR_UNSUPPORTED, "%d query heads", d.n_q_heads);

@@ -585,7 +585,7 @@ q4_status q4_attention(const q4_attention_desc *desc, q4_stream_t stream);
  * Q4_ERR_DEVICE_CHECK.  max_pages * page_size must not exceed 2^31 - 128,
  * n_kv_heads * head_dim (and n_q_heads * head_dim) 2^24, n_seqs 2^27.  An
  * int32 or fp32 array of this section or the next that is not 4-byte aligned
- * is Q4_ERR_MISALIGNED.
+ * is Q4_ERR_MISALIGNED.  With rows 0 the rows' arrays may be NULL.
  * ------------------------------------------------------------------------ */
 typedef struct q4_paged_cache {
     uint16_t *k;               /* both 16-byte aligned */

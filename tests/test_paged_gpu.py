@@ -373,3 +373,20 @@ def test_append_stores_good_sequences_around_bad_ones(S):
     assert q4.q4_device_status() == -7
     check_stored(b, k, v, before, qo, good)
     assert q4.q4_device_status() == 0
+
+
+def test_calls_without_rows_take_empty_tensors():
+    g = np.random.default_rng(51)
+    b = Batch(g, [5, 6], [0, 0], 2, 64, 16)
+    c = b.to_device(q4)
+    h = lambda n: torch.empty(0, n, dtype=torch.float16, device="cuda")  # noqa: E731
+    i = torch.empty(0, dtype=torch.int32, device="cuda")
+    ws = torch.empty(q4.q4_tree_attention_workspace_bytes(64), dtype=torch.uint8, device="cuda")
+    q4.q4_paged_append(c, b.dctx, b.dstart, 0, h(128), h(128), q=h(256), q_out=h(256), n_q_heads=4, positions=i)
+    q4.q4_tree_attention(c, b.dctx, b.dstart, 0, h(256), 4, h(256), ws, ws.numel(), mask=i, mask_words=1)
+    q4.q4_sample(torch.empty(0, 99, device="cuda"), q4.Q4_F32, 0, 99, i, top_k=i)
+    two = lambda: torch.full((2,), -9, dtype=torch.int32, device="cuda")  # noqa: E731
+    acc, nxt, ctx_out = two(), two(), two()
+    q4.q4_tree_accept(c, b.dctx, b.dstart, 0, i, i, i, acc, i, nxt, ctx_out)
+    assert q4.q4_device_status() == 0
+    assert acc.tolist() == [0, 0] and nxt.tolist() == [-1, -1] and ctx_out.tolist() == [5, 6]

@@ -209,3 +209,15 @@ def test_misaligned_arrays_are_refused(L):
                 d = type(base).from_buffer_copy(base)
                 d.cache = cache(page_table=FAKE + off)
                 assert call(ctypes.byref(d), None) == -3
+
+
+def test_no_rows_need_no_arrays(L):
+    # (what a framework's empty tensor gives as its address)
+    append = q4.q4_paged_append_desc(cache(), FAKE, FAKE, 0, None, None, None, 0, 0, None, None, 0, 0, 4, FAKE, 128, 0, 1.0)
+    attend = q4.q4_tree_attention_desc(cache(), FAKE, FAKE, 0, None, 1, None, None, 0, 0, 4, 0.0, FAKE,
+                                       L.q4_tree_attention_workspace_bytes(128))
+    sample = q4.q4_sample_desc(None, 0, 0, 1000, 0, None, None, None, None, None, None, None)
+    for call, d in ((L.q4_paged_append, append), (L.q4_tree_attention, attend), (L.q4_sample, sample)):
+        assert call(ctypes.byref(d), None) in (0, -6), L.q4_last_error()
+        d.rows = 1
+        assert call(ctypes.byref(d), None) == -1
