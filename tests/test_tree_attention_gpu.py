@@ -585,3 +585,29 @@ def test_small_probabilities_beside_dominant_ones_in_every_form(n, G, page):
     assert np.all(a > 2.0 ** -8)
     check(attend(b, b.to_device(q4), q, "causal", sees), b, q, a, A)
     assert q4.q4_device_status() == 0
+
+
+# Batches of unlike sequences, and tables of which few places are in use: one
+# kernel takes them all.
+MIXED = {
+    "a chunk among single tokens": dict(d=128, Hkv=1, G=4, page=16, n=[1] * 60 + [300] + [1] * 60),
+    "chunks among single tokens": dict(d=64, Hkv=2, G=2, page=64, n=[1, 1, 200, 1, 130, 1, 1, 0, 17]),
+    "a chunk among single tokens, pages of 7": dict(d=64, Hkv=1, G=2, page=7, n=[1] * 30 + [150] + [1] * 5),
+    "trees in a table mostly idle": dict(d=128, Hkv=2, G=4, page=16, n=([0] * 30 + [61]) * 4 + [0] * 90),
+    "single tokens in a table mostly idle": dict(d=64, Hkv=2, G=4, page=16, n=([0] * 60 + [1]) * 9),
+    "a single token behind a chunk": dict(d=128, Hkv=1, G=8, page=32, n=[130, 1]),
+}
+
+
+@pytest.mark.parametrize("kind", ["causal", "random"])
+@pytest.mark.parametrize("name", MIXED)
+def test_unlike_sequences_and_idle_places(name, kind):
+    f = MIXED[name]
+    g = np.random.default_rng(60 + len(name))
+    b = Batch(g, [int(x) for x in g.integers(0, 400, len(f["n"]))], f["n"], f["Hkv"], f["d"], f["page"])
+    q = rand16(g, b.rows, f["Hkv"] * f["G"], f["d"])
+    sees = seen_by(b, kind, g)
+    a, A = expected(b, q, sees)
+    out = attend(b, b.to_device(q4), q, kind, sees)
+    assert q4.q4_device_status() == 0
+    check(out, b, q, a, A)
