@@ -119,7 +119,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // two others compute the angles meanwhile.
 //
 // Measured: 6767 rows of 32 query and 8 kv heads of 128 (166 MB in and out)
-// 29.9 us = 5.6 TB/s, 82 % of the measured copy rate; 478 rows 3.1 us, one row
+// 30.7 us = 5.4 TB/s, 80 % of the measured copy rate; 478 rows 3.6 us, one row
 // 2.8 us, which is a launch.  kAhead 1 / 2 / 4: 31.4 / 30.5 / 42 us (4 spills);
 // 8 blocks per SM or 6: 30.5 / 31.9 us (both before the last 0.5 us).
 constexpr int kAhead = 2;
@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_
 //
 // What bounds it: a chain of dependent loads (sizes, the tokens and parents, the
 // path, its pages, its rows) and, for many sequences, the rows' bytes.  28
-// layers of 8 heads of 128, one sequence of 16 rows 5.0 us, 32 of up to 64 rows
-// (27 MB) 8.7 us = 3.1 TB/s.  Clusters of 1 / 4 / 8: 11.5 / 5.9 / 5.0 and 18.7 /
+// layers of 8 heads of 128, one sequence of 16 rows 5.3 us, 32 of up to 64 rows
+// (27 MB) 10.7 us = 2.5 TB/s, 8.4 us where the rows lie in L2.  Clusters of 1 / 4 / 8: 11.5 / 5.9 / 5.0 and 18.7 /
 // 8.8 / 8.7 us.
 constexpr int kAcceptThreads = 512;
 constexpr int kAcceptCluster = 8;

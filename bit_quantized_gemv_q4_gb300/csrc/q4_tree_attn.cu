@@ -330,7 +330,7 @@ __device__ __noinline__ void add_odd(const Args& a, const Place& p, int T, int t
 // neighbouring score tiles are the A operand of a 16-position step of P V.
 //
 // Measured: 40 users' tokens over contexts up to 12000 (8 query heads on each
-// of 4 kv heads of 128, 549 MB of cache) 94 us = 5.8 TB/s, 86 % of the measured
+// of 4 kv heads of 128, 549 MB of cache) 95 us = 5.8 TB/s, 85 % of the measured
 // copy rate; a short line is bound by its chain of waits: a job's sizes, its
 // first pages, the first tiles, the parts' way through L2 and the joining
 // kernel, 9.5 us with one tile of work.
@@ -338,7 +338,7 @@ __device__ __noinline__ void add_odd(const Args& a, const Place& p, int T, int t
 // kClustered: few jobs (a few users' decoding), where latency counts.  The
 // CTAs of a cluster take a job's tiles together and join their parts through
 // distributed shared memory: one launch, and no line to walk.  One user's
-// token over 1000 positions (16 heads on 8): 8.0 us, sizes, pages and one tile
+// token over 1000 positions (16 heads on 8): 8.1 us, sizes, pages and one tile
 // per CTA behind one another (the line: 10.6).
 constexpr int kConsumers = 128, kThreads = 160;
 // Units of a tile, and of a job before its tiles: the way to a new job's first
@@ -1010,7 +1010,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
 // of the grid share them.  One user's 61 x 4 rows over 4000 positions: 28 us,
 // with the kernel above 36.  Behind the ring's kernel it is the other way: 24
 // users' tokens 22.0 us, with this one 23.6, as the records can be read only
-// when the attention has ended.
+// when the attention has ended.  With heads of 128 it spills (80 bytes stored,
+// 132 loaded, at 64 registers for four blocks per SM).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_many_kernel(const __grid_constant__ Args a) {
     constexpr int kWarps = kJoinThreads / 32;
@@ -1198,11 +1199,11 @@ q4_status launch(Args& a, const q4_paged_cache& c, void* workspace, int sms, int
 // that does not exist is read outside the map, where TMA fills in zeros.
 //
 // Measured: a chunk of 1024 and one of 532 rows over 6000 and 4100 positions
-// (32 query heads on 8 kv heads of 128) 133 us = 1.11 PFLOP/s, 58 % of the
+// (32 query heads on 8 kv heads of 128) 134 us = 1.10 PFLOP/s, 58 % of the
 // measured matrix rate, the tensor pipe active half of the time: the softmax
 // of a stream is not always done when the other's products are; 14 us are the
 // joining of the parts.  Trees of up to 61 rows over 8 contexts up to 20000:
-// 85 us = 4.4 TB/s of cache (375 MB).  A job's beginning and end (queries in,
+// 86 us = 4.4 TB/s of cache (375 MB).  A job's beginning and end (queries in,
 // tensor memory out: some 5 us) are what short contexts cost.
 constexpr int kTcKeys = 128;
 constexpr int kTcThreads = 384;  // warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1

@@ -576,13 +576,16 @@ q4_status q4_attention(const q4_attention_desc *desc, q4_stream_t stream);
  * int32 [n_seqs+1], DEVICE; a sequence may have none), and ctx_len[s] (int32,
  * DEVICE) positions are cached before them; row i of a sequence takes
  * position ctx_len[s] + i.  The sizes are read on the device, so a captured
- * graph can be replayed as they change.  Rows from row_start[n_seqs] up to
- * `rows` belong to nobody: they are not used and not written.  A sequence
+ * graph can be replayed as they change.  Rows before row_start[0], and from
+ * row_start[n_seqs] up to `rows`, belong to nobody: they are not used and not
+ * written.  A sequence
  * whose sizes do not fit (row_start not ascending within 0..rows, ctx_len
  * negative, more positions than max_pages * page_size) is left out, its
  * outputs untouched, and a page number outside [0, n_pages) stands for no
  * memory: nothing is written there and its rows read as zeros.  Both latch
- * Q4_ERR_DEVICE_CHECK.  max_pages * page_size must not exceed 2^31 - 128,
+ * Q4_ERR_DEVICE_CHECK.  Where the starts go back so far that two sequences
+ * hold one row (the one between them is latched), the call's results are not
+ * defined.  max_pages * page_size must not exceed 2^31 - 128,
  * n_kv_heads * head_dim (and n_q_heads * head_dim) 2^24, n_seqs 2^27.  An
  * int32 or fp32 array of this section or the next that is not 4-byte aligned
  * is Q4_ERR_MISALIGNED.  With rows 0 the rows' arrays may be NULL.
@@ -732,7 +735,9 @@ q4_status q4_tree_accept(const q4_tree_accept_desc *desc, q4_stream_t stream);
  * prob = its share of the kept weights.  -inf and NaN logits take no part; if
  * the greatest logit is +inf, the tokens that have it weigh 1 and all others
  * 0; a row without any other logit gives token -1 and prob 0.  Sums are exact
- * 64-bit integers of weights rounded to 2^-44, whatever the order.
+ * 64-bit integers of weights, each off by some 2^-30 of itself and rounded to
+ * 2^-44, whatever the order.  A logit further below the greatest than fp32's
+ * largest number weighs 0, and a temperature below 1.5e-30 counts as that.
  * ------------------------------------------------------------------------ */
 typedef struct q4_sample_desc {
     const void *logits;       /* [rows][vocab] of `dtype`, rows ld elements apart */
