@@ -19,6 +19,8 @@ __all__ = [
     "q4_moe_gather", "q4_moe_gemm", "q4_moe_combine",
     "PagedCache", "q4_rope_frequencies", "q4_paged_append", "q4_tree_attention", "q4_tree_attention_workspace_bytes",
     "q4_tree_accept", "q4_sample", "Q4_ROPE_HALF", "Q4_ROPE_INTERLEAVED",
+    "HeadNorm", "q4_paged_append_norm", "PagedCache8", "q4_paged_append8", "q4_paged_read8", "q4_tree_attention8",
+    "q4_tree_accept8", "Q4_CACHE8_BLOCK",
     "Q4_F32", "Q4_F16", "Q4_GEMV_PLAIN", "Q4_GEMV_GLU", "Q4_DECODE_NO_GRAPH", "Q4_DECODE_NO_PDL",
     "Q4_DECODE_TAGGED",
     "Q4_DECODE_PERSISTENT", "Q4_DECODE_CLUSTERED", "Q4_GEMV_EARLY_WEIGHTS",
@@ -35,6 +37,7 @@ Q4_DECODE_CLUSTERED = 32
 Q4_GEMV_EARLY_WEIGHTS = 1
 Q4_MAX_SEGMENTS = 4
 Q4_ROPE_HALF, Q4_ROPE_INTERLEAVED = 0, 1
+Q4_CACHE8_BLOCK = 16
 
 STATUS = {0: "Q4_OK", -1: "Q4_ERR_INVALID_ARG", -2: "Q4_ERR_UNSUPPORTED", -3: "Q4_ERR_MISALIGNED",
           -4: "Q4_ERR_CUDA", -5: "Q4_ERR_TIMEOUT", -6: "Q4_ERR_NO_DEVICE", -7: "Q4_ERR_DEVICE_CHECK"}
@@ -48,7 +51,8 @@ EXPORTS = ["q4_last_error", "q4_status_string", "q4_version", "q4_device_status"
            "q4_moe_gather", "q4_moe_gemm", "q4_moe_combine", "q4_gemm", "q4_prefill_workspace_bytes",
            "q4_prefill", "q4_attention_workspace_bytes", "q4_attention", "q4_gemm_workspace_bytes",
            "q4_prefill_buffers", "q4_rope_frequencies", "q4_paged_append", "q4_tree_attention_workspace_bytes",
-           "q4_tree_attention", "q4_tree_accept", "q4_sample"]
+           "q4_tree_attention", "q4_tree_accept", "q4_sample", "q4_paged_append_norm", "q4_paged_append8",
+           "q4_paged_read8", "q4_tree_attention8", "q4_tree_accept8"]
 
 
 class Q4Error(RuntimeError):
@@ -147,6 +151,32 @@ class q4_sample_desc(ctypes.Structure):
                 ("top_k", vp), ("top_p", vp), ("min_p", vp), ("u", vp), ("tokens", vp), ("probs", vp)]
 
 
+class q4_head_norm(ctypes.Structure):
+    _fields_ = [("q_rmsnorm", i32), ("k_rmsnorm", i32), ("q_weight", vp), ("k_weight", vp), ("eps", ctypes.c_float)]
+
+
+class q4_paged_cache8(ctypes.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("k_scales", vp), ("v_scales", vp), ("page_table", vp), ("n_pages", i32),
+                ("page_size", i32), ("n_kv_heads", i32), ("head_dim", i32), ("n_seqs", i32), ("max_pages", i32)]
+
+
+class q4_paged_append8_desc(ctypes.Structure):
+    _fields_ = [("cache", q4_paged_cache8)] + q4_paged_append_desc._fields_[1:]
+
+
+class q4_paged_read8_desc(ctypes.Structure):
+    _fields_ = [("cache", q4_paged_cache8), ("first", vp), ("row_start", vp), ("rows", i32), ("k", vp), ("v", vp),
+                ("ldk", i32), ("ldv", i32)]
+
+
+class q4_tree_attention8_desc(ctypes.Structure):
+    _fields_ = [("cache", q4_paged_cache8)] + q4_tree_attention_desc._fields_[1:]
+
+
+class q4_tree_accept8_desc(ctypes.Structure):
+    _fields_ = [("cache", q4_paged_cache8)] + q4_tree_accept_desc._fields_[1:] + [("scale_stride", ctypes.c_size_t)]
+
+
 _lib = None
 
 
@@ -223,6 +253,16 @@ def lib() -> ctypes.CDLL:
         L.q4_tree_accept.argtypes = [ctypes.POINTER(q4_tree_accept_desc), vp]
         L.q4_sample.restype = st
         L.q4_sample.argtypes = [ctypes.POINTER(q4_sample_desc), vp]
+        L.q4_paged_append_norm.restype = st
+        L.q4_paged_append_norm.argtypes = [ctypes.POINTER(q4_paged_append_desc), ctypes.POINTER(q4_head_norm), vp]
+        L.q4_paged_append8.restype = st
+        L.q4_paged_append8.argtypes = [ctypes.POINTER(q4_paged_append8_desc), ctypes.POINTER(q4_head_norm), vp]
+        L.q4_paged_read8.restype = st
+        L.q4_paged_read8.argtypes = [ctypes.POINTER(q4_paged_read8_desc), vp]
+        L.q4_tree_attention8.restype = st
+        L.q4_tree_attention8.argtypes = [ctypes.POINTER(q4_tree_attention8_desc), vp]
+        L.q4_tree_accept8.restype = st
+        L.q4_tree_accept8.argtypes = [ctypes.POINTER(q4_tree_accept8_desc), vp]
         _lib = L
     return _lib
 
@@ -593,36 +633,64 @@ def q4_rope_frequencies(freqs, rot_dim: int, theta: float = 1.0e6, factor: float
     _check(lib().q4_rope_frequencies(ctypes.byref(d), p, _stream_of(torch, dev, stream)), "q4_rope_frequencies")
 
 
-def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=None, q_out=None, n_q_heads: int = 0,
-                    positions=None, freqs=None, rot_dim: int = 0, layout=Q4_ROPE_HALF, amplitude: float = 1.0,
-                    ldq: int = 0, ldk: int = 0, ldv: int = 0, ldqo: int = 0, stream=None):
-    """New rows' keys (rotated) and values into the paged cache, queries (rotated) into q_out."""
-    torch = _get_torch()
-    dev = _device(torch)
+def _append_desc(kind, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs, rot_dim, layout,
+                 amplitude, ldq, ldk, ldv, ldqo, torch, dev):
     f16, i32_ = torch.float16, torch.int32
     _, _, heads, hd, n_seqs, _ = cache.sizes
     pk, ldk = _rows(k, f16, rows, heads * hd, ldk, dev, "k")
     pv, ldv = _rows(v, f16, rows, heads * hd, ldv, dev, "v")
     pq, ldq = _rows(q, f16, rows, n_q_heads * hd, ldq, dev, "q")
     po, ldqo = _rows(q_out, f16, rows, n_q_heads * hd, ldqo, dev, "q_out")
-    d = q4_paged_append_desc(
+    return kind(
         cache._desc(torch, dev, cache.pool), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
         _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(positions, i32_, rows, dev, "positions"), pk, pv,
         ldk, ldv, pq, po, ldq, ldqo, n_q_heads, _arg(freqs, torch.int64, rot_dim // 2, dev, "freqs"), rot_dim, layout,
         amplitude)
+
+
+def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=None, q_out=None, n_q_heads: int = 0,
+                    positions=None, freqs=None, rot_dim: int = 0, layout=Q4_ROPE_HALF, amplitude: float = 1.0,
+                    ldq: int = 0, ldk: int = 0, ldv: int = 0, ldqo: int = 0, stream=None):
+    """New rows' keys (rotated) and values into the paged cache, queries (rotated) into q_out."""
+    torch = _get_torch()
+    dev = _device(torch)
+    d = _append_desc(q4_paged_append_desc, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
+                     rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev)
     _check(lib().q4_paged_append(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_paged_append")
+
+
+class HeadNorm:
+    """Norms of query and key heads (q4.h section 9): fp16 weights [head_dim] (None = ones), `q` / `k` whether
+    queries / keys are normalised; keeps the tensors."""
+
+    __slots__ = ("q_weight", "k_weight", "eps", "q", "k")
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1.0e-6, q: bool = True, k: bool = True):
+        self.q_weight, self.k_weight, self.eps, self.q, self.k = q_weight, k_weight, eps, q, k
+
+    def _desc(self, torch, dev: int, head_dim: int) -> q4_head_norm:
+        return q4_head_norm(int(self.q), int(self.k), _arg(self.q_weight, torch.float16, head_dim, dev, "norm.q_weight"),
+                            _arg(self.k_weight, torch.float16, head_dim, dev, "norm.k_weight"), self.eps)
+
+
+def q4_paged_append_norm(cache: PagedCache, ctx_len, row_start, rows: int, k, v, norm: HeadNorm = None, q=None, q_out=None,
+                         n_q_heads: int = 0, positions=None, freqs=None, rot_dim: int = 0, layout=Q4_ROPE_HALF,
+                         amplitude: float = 1.0, ldq: int = 0, ldk: int = 0, ldv: int = 0, ldqo: int = 0, stream=None):
+    """q4_paged_append with each query and key head normalised before its rotation."""
+    torch = _get_torch()
+    dev = _device(torch)
+    d = _append_desc(q4_paged_append_desc, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
+                     rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev)
+    n = None if norm is None else ctypes.byref(norm._desc(torch, dev, cache.sizes[3]))
+    _check(lib().q4_paged_append_norm(ctypes.byref(d), n, _stream_of(torch, dev, stream)), "q4_paged_append_norm")
 
 
 def q4_tree_attention_workspace_bytes(head_dim: int) -> int:
     return lib().q4_tree_attention_workspace_bytes(head_dim)
 
 
-def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_heads: int, out, workspace,
-                      workspace_bytes: int, mask=None, mask_words: int = 0, scale: float = 0.0, ldq: int = 0,
-                      ldo: int = 0, stream=None):
-    """Attention of the new rows over the cached positions and, by the mask (None: causal), their own."""
-    torch = _get_torch()
-    dev = _device(torch)
+def _attention_desc(kind, cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace, workspace_bytes, mask,
+                    mask_words, scale, ldq, ldo, torch, dev):
     f16, i32_ = torch.float16, torch.int32
     w, n_seqs = n_q_heads * cache.sizes[3], cache.sizes[4]
     pq, ldq = _rows(q, f16, rows, w, ldq, dev, "q")
@@ -631,11 +699,32 @@ def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_h
         if workspace.numel() * workspace.element_size() < workspace_bytes:
             raise ValueError(f"workspace: smaller than {workspace_bytes} bytes")
         workspace = _arg(workspace, workspace.dtype, 0, dev, "workspace")
-    d = q4_tree_attention_desc(
+    return kind(
         cache._desc(torch, dev, cache.pool), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
         _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(mask, i32_, rows * mask_words, dev, "mask"),
         mask_words, pq, po, ldq, ldo, n_q_heads, scale, workspace, workspace_bytes)
+
+
+def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_heads: int, out, workspace,
+                      workspace_bytes: int, mask=None, mask_words: int = 0, scale: float = 0.0, ldq: int = 0,
+                      ldo: int = 0, stream=None):
+    """Attention of the new rows over the cached positions and, by the mask (None: causal), their own."""
+    torch = _get_torch()
+    dev = _device(torch)
+    d = _attention_desc(q4_tree_attention_desc, cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace,
+                        workspace_bytes, mask, mask_words, scale, ldq, ldo, torch, dev)
     _check(lib().q4_tree_attention(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_attention")
+
+
+def _accept_desc(kind, cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path, next_token, ctx_out,
+                 torch, dev, desc, *strides):
+    i32_, n_seqs = torch.int32, cache.sizes[4]
+    return kind(
+        desc, _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"), _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows,
+        _arg(draft, i32_, rows, dev, "draft"), _arg(parents, i32_, rows, dev, "parents"),
+        _arg(sampled, i32_, rows, dev, "sampled"), _arg(accepted, i32_, n_seqs, dev, "accepted"),
+        _arg(path, i32_, rows, dev, "path"), _arg(next_token, i32_, n_seqs, dev, "next_token"),
+        _arg(ctx_out, i32_, n_seqs, dev, "ctx_out"), *strides)
 
 
 def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, parents, sampled, accepted, path,
@@ -643,16 +732,83 @@ def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, pare
     """Walks each sequence's drafted tree along the sampled tokens and moves the path's cache rows into place."""
     torch = _get_torch()
     dev = _device(torch)
-    i32_, n_seqs = torch.int32, cache.sizes[4]
     elements = (n_layers - 1) * layer_stride + cache.pool if n_layers > 0 else 0
-    d = q4_tree_accept_desc(
-        cache._desc(torch, dev, elements), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
-        _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(draft, i32_, rows, dev, "draft"),
-        _arg(parents, i32_, rows, dev, "parents"), _arg(sampled, i32_, rows, dev, "sampled"),
-        _arg(accepted, i32_, n_seqs, dev, "accepted"), _arg(path, i32_, rows, dev, "path"),
-        _arg(next_token, i32_, n_seqs, dev, "next_token"), _arg(ctx_out, i32_, n_seqs, dev, "ctx_out"), n_layers,
-        layer_stride)
+    d = _accept_desc(q4_tree_accept_desc, cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path,
+                     next_token, ctx_out, torch, dev, cache._desc(torch, dev, elements), n_layers, layer_stride)
     _check(lib().q4_tree_accept(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_accept")
+
+
+class PagedCache8:
+    """Key / value pools of e4m3 codes (torch.float8_e4m3fn or uint8) [n_pages][n_kv_heads][page_size][head_dim],
+    their scales fp32 [n_pages][n_kv_heads][ceil(page_size / 16)] (for q4_tree_accept8 one such pool per layer,
+    layer_stride elements and scale_stride scales apart) and the sequences' page table int32 [n_seqs][max_pages];
+    keeps the tensors."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "page_table", "sizes", "pool", "blocks")
+
+    def __init__(self, k, v, k_scales, v_scales, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, page_table,
+                 n_seqs: int, max_pages: int):
+        self.k, self.v, self.k_scales, self.v_scales, self.page_table = k, v, k_scales, v_scales, page_table
+        self.sizes = (n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages)
+        self.pool = n_pages * page_size * n_kv_heads * head_dim  # elements of one layer's keys
+        self.blocks = n_pages * n_kv_heads * -(-page_size // Q4_CACHE8_BLOCK)  # and scales
+
+    def _desc(self, torch, dev: int, elements: int, scales: int = None) -> q4_paged_cache8:
+        s = self.sizes
+        scales = self.blocks if scales is None else scales
+        codes = [_arg(t, torch.uint8 if t.__class__ is not int and t is not None and t.dtype is torch.uint8
+                      else torch.float8_e4m3fn, elements, dev, name) for t, name in ((self.k, "cache.k"), (self.v, "cache.v"))]
+        return q4_paged_cache8(*codes, _arg(self.k_scales, torch.float32, scales, dev, "cache.k_scales"),
+                               _arg(self.v_scales, torch.float32, scales, dev, "cache.v_scales"),
+                               _arg(self.page_table, torch.int32, s[4] * s[5], dev, "cache.page_table"), *s)
+
+
+def q4_paged_append8(cache: PagedCache8, ctx_len, row_start, rows: int, k, v, norm: HeadNorm = None, q=None, q_out=None,
+                     n_q_heads: int = 0, positions=None, freqs=None, rot_dim: int = 0, layout=Q4_ROPE_HALF,
+                     amplitude: float = 1.0, ldq: int = 0, ldk: int = 0, ldv: int = 0, ldqo: int = 0, stream=None):
+    """q4_paged_append_norm into the 8-bit cache: keys and values as e4m3 codes with a scale for 16 positions and head."""
+    torch = _get_torch()
+    dev = _device(torch)
+    d = _append_desc(q4_paged_append8_desc, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
+                     rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev)
+    n = None if norm is None else ctypes.byref(norm._desc(torch, dev, cache.sizes[3]))
+    _check(lib().q4_paged_append8(ctypes.byref(d), n, _stream_of(torch, dev, stream)), "q4_paged_append8")
+
+
+def q4_paged_read8(cache: PagedCache8, first, row_start, rows: int, k=None, v=None, ldk: int = 0, ldv: int = 0, stream=None):
+    """Keys and values of positions first[s] .. of each sequence as fp16 rows [rows][n_kv_heads * head_dim]."""
+    torch = _get_torch()
+    dev = _device(torch)
+    _, _, heads, hd, n_seqs, _ = cache.sizes
+    pk, ldk = _rows(k, torch.float16, rows, heads * hd, ldk, dev, "k")
+    pv, ldv = _rows(v, torch.float16, rows, heads * hd, ldv, dev, "v")
+    d = q4_paged_read8_desc(cache._desc(torch, dev, cache.pool), _arg(first, torch.int32, n_seqs, dev, "first"),
+                            _arg(row_start, torch.int32, n_seqs + 1, dev, "row_start"), rows, pk, pv, ldk, ldv)
+    _check(lib().q4_paged_read8(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_paged_read8")
+
+
+def q4_tree_attention8(cache: PagedCache8, ctx_len, row_start, rows: int, q, n_q_heads: int, out, workspace,
+                       workspace_bytes: int, mask=None, mask_words: int = 0, scale: float = 0.0, ldq: int = 0,
+                       ldo: int = 0, stream=None):
+    """q4_tree_attention over the 8-bit cache (its workspace: q4_tree_attention_workspace_bytes)."""
+    torch = _get_torch()
+    dev = _device(torch)
+    d = _attention_desc(q4_tree_attention8_desc, cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace,
+                        workspace_bytes, mask, mask_words, scale, ldq, ldo, torch, dev)
+    _check(lib().q4_tree_attention8(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_attention8")
+
+
+def q4_tree_accept8(cache: PagedCache8, ctx_len, row_start, rows: int, draft, parents, sampled, accepted, path,
+                    next_token, ctx_out, n_layers: int = 1, layer_stride: int = 0, scale_stride: int = 0, stream=None):
+    """q4_tree_accept over the 8-bit cache."""
+    torch = _get_torch()
+    dev = _device(torch)
+    elements = (n_layers - 1) * layer_stride + cache.pool if n_layers > 0 else 0
+    scales = (n_layers - 1) * scale_stride + cache.blocks if n_layers > 0 else 0
+    d = _accept_desc(q4_tree_accept8_desc, cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path,
+                     next_token, ctx_out, torch, dev, cache._desc(torch, dev, elements, scales), n_layers, layer_stride,
+                     scale_stride)
+    _check(lib().q4_tree_accept8(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_accept8")
 
 
 def q4_sample(logits, dtype, rows: int, vocab: int, tokens, temperature=None, top_k=None, top_p=None, min_p=None,

@@ -49,22 +49,6 @@ struct AppendArgs {
     PageDiv by_per;  // division by a rotated head's items
 };
 
-// Sequence of a row: the number of sequences whose end is at or before it, by
-// a search 32 ways wide (one load per lane and level).  All lanes get it.  Where
-// the starts are not in order it can be another (or none): the caller checks.
-__device__ __forceinline__ int seq_of_row(const View& w, int row, int lane) {
-    int lo = 0, len = w.S;
-    while (len > 0) {
-        const int stride = (len + 31) / 32;
-        const int i = lane * stride + stride - 1;
-        const bool before = i < len && w.row_start[lo + i + 1] <= row;
-        const int c = __popc(__ballot_sync(0xffffffffu, before));
-        lo += c * stride;
-        len = min(stride - 1, len - c * stride);
-    }
-    return lo;
-}
-
 // Where a row goes.
 constexpr int kNobody = 0x7fffffff;
 struct At {
@@ -73,11 +57,6 @@ struct At {
     int seq;         // sequence (kNobody: nobody's row)
 };
 
-__device__ __forceinline__ bool holds(const View& w, int s, int row, Seq& q) {
-    bool bad;
-    q = seq_of(w, s, bad);
-    return !bad && row >= q.start && row < q.start + q.n;
-}
 __device__ __forceinline__ void place(const View& w, const Seq& q, int row, int D, At& at) {
     at.slot = q.ctx + (row - q.start);
     at.base = row_at(w, at.seq, at.slot, 0, D);
@@ -281,9 +260,6 @@ __global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const __grid_
 // layers of 8 heads of 128, one sequence of 16 rows 5.3 us, 32 of up to 64 rows
 // (27 MB) 10.7 us = 2.5 TB/s, 8.4 us where the rows lie in L2.  Clusters of 1 / 4 / 8: 11.5 / 5.9 / 5.0 and 18.7 /
 // 8.8 / 8.7 us.
-constexpr int kAcceptThreads = 512;
-constexpr int kAcceptCluster = 8;
-constexpr int kMaxTree = 4096;
 constexpr int kMoves = 8;  // rows whose addresses are staged, and whose copies are in flight, together
 
 struct AcceptArgs {
@@ -310,22 +286,7 @@ __global__ void __cluster_dims__(kAcceptCluster, 1, 1) __launch_bounds__(kAccept
     }
     if (bad && rank == 0 && tid == 0) atomicOr(p.w.err, q4d::kErrDeviceCheck);
     const int n = q.n;
-    for (int i = tid; i < n; i += kAcceptThreads) next[i] = 0x7fffffff;
-    __syncthreads();
-    for (int i = 1 + tid; i < n; i += kAcceptThreads) {
-        const int up = p.parents[q.start + i];
-        if (up >= 0 && up < i) {
-            const int t = p.sampled[q.start + up];
-            if (t >= 0 && t == p.draft[q.start + i]) atomicMin(&next[up], i);
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int len = 0;
-        for (int at = 0; at < n; at = next[at]) path[len++] = at;  // ascending: next[at] > at
-        len_s = len;
-    }
-    __syncthreads();
+    walk_tree(p.draft + q.start, p.parents + q.start, p.sampled + q.start, n, next, path, &len_s);
     const int len = len_s;
     // what is moved: path[i] -> i for the rows that are not in place
     const int cols = p.D / 8, per_layer = 2 * p.w.H * cols;

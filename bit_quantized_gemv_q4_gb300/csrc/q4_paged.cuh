@@ -66,6 +66,69 @@ __device__ __forceinline__ long long row_at(const View& w, int s, I pos, int h, 
     return (((long long)id * w.H + h) * w.div.d + ((uint32_t)pos - pg * w.div.d)) * D;
 }
 
+// Sequence of a row: the number of sequences whose end is at or before it, by
+// a search 32 ways wide (one load per lane and level).  All lanes get it.  Where
+// the starts are not in order it can be another (or none): the caller checks.
+__device__ __forceinline__ int seq_of_row(const View& w, int row, int lane) {
+    int lo = 0, len = w.S;
+    while (len > 0) {
+        const int stride = (len + 31) / 32;
+        const int i = lane * stride + stride - 1;
+        const bool before = i < len && w.row_start[lo + i + 1] <= row;
+        const int c = __popc(__ballot_sync(0xffffffffu, before));
+        lo += c * stride;
+        len = min(stride - 1, len - c * stride);
+    }
+    return lo;
+}
+
+__device__ __forceinline__ bool holds(const View& w, int s, int row, Seq& q) {
+    bool bad;
+    q = seq_of(w, s, bad);
+    return !bad && row >= q.start && row < q.start + q.n;
+}
+
+// ---- acceptance: blocks of a sequence's cluster, and the path ---------------
+constexpr int kAcceptThreads = 512;
+constexpr int kAcceptCluster = 8;
+constexpr int kMaxTree = 4096;
+
+// By a whole block: the accepted path of a tree of n rows (n <= kMaxTree) into
+// `path`, its length into *len.  Every row in parallel looks whether it
+// continues its parent (its token is the one sampled there), the smallest such
+// row of a parent wins (an integer minimum, the same in any order), then one
+// thread follows the pointers.
+__device__ __forceinline__ void walk_tree(const int32_t* draft, const int32_t* parents, const int32_t* sampled, int n,
+                                          int32_t* next, int32_t* path, int* len) {
+    const int tid = threadIdx.x;
+    for (int i = tid; i < n; i += kAcceptThreads) next[i] = 0x7fffffff;
+    __syncthreads();
+    for (int i = 1 + tid; i < n; i += kAcceptThreads) {
+        const int up = parents[i];
+        if (up >= 0 && up < i) {
+            const int t = sampled[up];
+            if (t >= 0 && t == draft[i]) atomicMin(&next[up], i);
+        }
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int k = 0;
+        for (int at = 0; at < n; at = next[at]) path[k++] = at;  // ascending: next[at] > at
+        *len = k;
+    }
+    __syncthreads();
+}
+
+// ---- the cache in 8 bits (q4.h section 9) -------------------------------------
+constexpr int kBlock = Q4_CACHE8_BLOCK;
+
+struct View8 {
+    View w;  // its pools are not used
+    uint8_t *k, *v;
+    float *ks, *vs;
+    int nb;  // blocks of a page
+};
+
 }  // namespace q4p
 
 namespace q4i {
@@ -98,6 +161,23 @@ inline q4_status paged_view(const q4_paged_cache& c, const int32_t* ctx_len, con
     w->rows = rows;
     w->div = q4p::page_div((uint32_t)c.page_size);
     w->err = nullptr;
+    return Q4_OK;
+}
+
+// Likewise for the cache in 8 bits.
+inline q4_status paged_view8(const q4_paged_cache8& c, const int32_t* ctx_len, const int32_t* row_start, int rows,
+                             q4p::View8* w) {
+    const q4_paged_cache pools = {reinterpret_cast<uint16_t*>(c.k), reinterpret_cast<uint16_t*>(c.v), c.page_table, c.n_pages,
+                                  c.page_size, c.n_kv_heads, c.head_dim, c.n_seqs, c.max_pages};
+    const q4_status st = paged_view(pools, ctx_len, row_start, rows, &w->w);
+    if (st != Q4_OK) return st;
+    if (!c.k_scales || !c.v_scales) return fail(Q4_ERR_INVALID_ARG, "NULL pointer argument");
+    if (!aligned4(c.k_scales, c.v_scales)) return fail(Q4_ERR_MISALIGNED, "the scales must be 4-byte aligned");
+    w->k = c.k;
+    w->v = c.v;
+    w->ks = c.k_scales;
+    w->vs = c.v_scales;
+    w->nb = (c.page_size - 1) / q4p::kBlock + 1;
     return Q4_OK;
 }
 

@@ -1,0 +1,42 @@
+// Conversions of the paged cache in 8 bits (q4.h section 9).
+#pragma once
+
+#include "q4_paged.cuh"
+
+namespace q4p {
+
+// Two e4m3 codes (bits 0 .. 15 of w, the lower one first) as fp16, exact.
+__device__ __forceinline__ uint32_t e4m3_half2(uint32_t w) {
+    uint32_t h;
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }" : "=r"(h) : "r"(w));
+    return h;
+}
+__device__ __forceinline__ float2 e4m3_f32(uint32_t w) {
+    const uint32_t h = e4m3_half2(w);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Two numbers as e4m3 codes, to nearest, ties to even.
+__device__ __forceinline__ uint32_t f32_e4m3(float lo, float hi) {
+    uint32_t r;
+    asm("{ .reg .b16 c; cvt.rn.satfinite.e4m3x2.f32 c, %2, %1; cvt.u32.u16 %0, c; }" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void unpack8(const uint4& a, float* x) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float* x) {
+    return make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+}
+
+}  // namespace q4p

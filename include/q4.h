@@ -756,6 +756,138 @@ typedef struct q4_sample_desc {
 
 q4_status q4_sample(const q4_sample_desc *desc, q4_stream_t stream);
 
+/* ------------------------------------------------------------------------ *
+ * 9. Norms of queries and keys, and the cache of section 7 in 8 bits.
+ *
+ * Normalising each head's query and key before the rotation belongs to the
+ * operator sequences of the attention path that BaseRT §3.3 fuses; a cache in
+ * fewer bits carries its formats per tensor (§3.3, §4.1: 2 to 16 bits) to the
+ * keys and values.  The pages print no formula for either.
+ * ------------------------------------------------------------------------ */
+
+/* A head x of d = head_dim elements becomes x / sqrt(mean(x^2) + eps) * weight
+ * in fp32, unrounded, before its rotation. */
+typedef struct q4_head_norm {
+    int q_rmsnorm, k_rmsnorm;  /* 1: normalise each query / key head */
+    const uint16_t *q_weight;  /* fp16 [head_dim], 2-byte aligned, one for all heads; NULL = ones */
+    const uint16_t *k_weight;
+    float eps;                 /* >= 0, finite; a head of zeros with eps 0 stays zeros */
+} q4_head_norm;
+
+/* 9a. q4_paged_append (7b: its arguments, checks, outputs) with the norms in
+ * the same pass.  norm NULL: none. */
+q4_status q4_paged_append_norm(const q4_paged_append_desc *desc, const q4_head_norm *norm, q4_stream_t stream);
+
+/* The cache of section 7 with keys and values as e4m3 codes.  The positions
+ * of a page are cut into blocks of 16 (the last one of a page may be shorter),
+ * and each block of a kv head has a scale; an element stands for code * scale.
+ * Section 7's rules on pages, sequences, rows, sizes and errors hold as they
+ * stand.  A scale is a power of two from 2^-15 to 2^8, with 2^8 the codes go
+ * up to 240, so that every element is an fp16 number; where a block that a call
+ * reads has it otherwise, the results are not defined. */
+#define Q4_CACHE8_BLOCK 16
+
+typedef struct q4_paged_cache8 {
+    uint8_t *k;                /* e4m3 [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned */
+    uint8_t *v;
+    float *k_scales;           /* [n_pages][n_kv_heads][ceil(page_size / 16)] */
+    float *v_scales;
+    const int32_t *page_table;
+    int n_pages, page_size;
+    int n_kv_heads, head_dim;  /* head_dim 64 or 128 */
+    int n_seqs, max_pages;
+} q4_paged_cache8;
+
+/* 9b. q4_paged_append8 -- 7b (with 9a's norms, NULL = none) into the 8-bit
+ * cache; q_out is fp16 as there.  With t the greatest magnitude among a
+ * block's new elements, limited to 61440 (240 * 2^8, which is within 2^-4 of
+ * any fp16 number above it; infinities count as that), the block needs the
+ * least scale 2^e, e >= -15, with t <= 448 * 2^e.  A block in which no
+ * position before ctx_len lies takes that scale; another one takes the greater
+ * of it and its own, and if that is not its own, the codes of the block's
+ * positions before ctx_len are rewritten for it (which is exact unless a code
+ * falls below e4m3's normal numbers).  Codes are rounded to nearest, ties to
+ * even, once from fp32; NaN stays NaN and does not count in t. */
+typedef struct q4_paged_append8_desc {
+    q4_paged_cache8 cache;
+    const int32_t *ctx_len;    /* from here on as q4_paged_append_desc */
+    const int32_t *row_start;
+    int rows;
+    const int32_t *positions;
+    const uint16_t *k, *v;
+    int ldk, ldv;
+    const uint16_t *q;
+    uint16_t *q_out;
+    int ldq, ldqo;
+    int n_q_heads;
+    const uint64_t *freqs;
+    int rot_dim;
+    q4_rope_layout layout;
+    float amplitude;
+} q4_paged_append8_desc;
+
+q4_status q4_paged_append8(const q4_paged_append8_desc *desc, const q4_head_norm *norm, q4_stream_t stream);
+
+/* 9c. q4_paged_read8 -- what the cache holds, code * scale as fp16: row i of
+ * sequence s (rows row_start[s] .. as in section 7) is its position
+ * first[s] + i, which has to lie in the page table.  The outputs have the
+ * layout of 7b's k and v (so an append without rotation puts them into an fp16
+ * cache): fp16 [rows][n_kv_heads * head_dim], 16-byte aligned, strides
+ * multiples of 8, 0 = packed; either may be NULL. */
+typedef struct q4_paged_read8_desc {
+    q4_paged_cache8 cache;
+    const int32_t *first;      /* [n_seqs], >= 0 */
+    const int32_t *row_start;  /* [n_seqs + 1] */
+    int rows;
+    uint16_t *k, *v;
+    int ldk, ldv;
+} q4_paged_read8_desc;
+
+q4_status q4_paged_read8(const q4_paged_read8_desc *desc, q4_stream_t stream);
+
+/* 9d. q4_tree_attention8 -- 7c over the 8-bit cache: its arguments, masks,
+ * accuracy, workspace (q4_tree_attention_workspace_bytes) and limits.  What a
+ * row does not see never reaches it: the NaN codes of new rows that it does
+ * not see included. */
+typedef struct q4_tree_attention8_desc {
+    q4_paged_cache8 cache;
+    const int32_t *ctx_len, *row_start;
+    int rows;
+    const uint32_t *mask;
+    int mask_words;
+    const uint16_t *q;
+    uint16_t *out;
+    int ldq, ldo;
+    int n_q_heads;
+    float scale;
+    void *workspace;
+    size_t workspace_bytes;
+} q4_tree_attention8_desc;
+
+q4_status q4_tree_attention8(const q4_tree_attention8_desc *desc, q4_stream_t stream);
+
+/* 9e. q4_tree_accept8 -- 7d over the 8-bit cache; layer l's pools start
+ * l * layer_stride elements (a multiple of 16) and its scales l * scale_stride
+ * floats behind the first one's.  A block into which rows move takes the
+ * greatest of its own scale and those of the blocks they come from; if that is
+ * not its own, the codes of its other positions up to the sequence's last new
+ * row are rewritten for it, as in 9b. */
+typedef struct q4_tree_accept8_desc {
+    q4_paged_cache8 cache;
+    const int32_t *ctx_len, *row_start;
+    int rows;
+    const int32_t *draft, *parents, *sampled;
+    int32_t *accepted;
+    int32_t *path;
+    int32_t *next_token;
+    int32_t *ctx_out;
+    int n_layers;
+    size_t layer_stride;
+    size_t scale_stride;
+} q4_tree_accept8_desc;
+
+q4_status q4_tree_accept8(const q4_tree_accept8_desc *desc, q4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -769,3 +769,84 @@ def tree_path(draft, parents, sampled):
             break
         path.append(nxt[0])
     return path
+
+
+# ---------------------------------------------- norms of heads, 8-bit cache ---
+# BaseRT §3.3 fuses the operator sequences of the attention path; the pages
+# print no formula: the readings are the ones of include/q4.h, section 9.
+
+def head_norm(x, weight=None, eps: float = 1e-6) -> np.ndarray:
+    """x [..., d] / sqrt(mean of squares + eps) * weight, fp64; zeros stay zeros."""
+    x = np.asarray(x, np.float64)
+    v = np.mean(x * x, -1, keepdims=True) + eps
+    y = x / np.sqrt(np.where(v == 0, 1.0, v))
+    return y if weight is None else y * np.asarray(weight, np.float64)
+
+
+_E4M3 = np.array([m / 8 * 2.0 ** -6 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7) for e in range(16) for m in range(8)])
+_E4M3[127] = np.nan
+
+
+def e4m3_values(codes) -> np.ndarray:
+    """fp64 values of e4m3 codes: sign, 4 bits of exponent (bias 7, 0 subnormal), 3 of fraction; 0x7f and 0xff NaN."""
+    codes = np.asarray(codes, np.uint8)
+    return np.where(codes & 128, -1.0, 1.0) * _E4M3[codes & 127]
+
+
+def e4m3_codes(x) -> np.ndarray:
+    """Nearest codes, ties to even, at most 448 in magnitude; NaN is 0x7f."""
+    x = np.asarray(x, np.float64)
+    a = np.minimum(np.abs(np.where(np.isnan(x), 0.0, x)), 448.0)
+    step = np.exp2(np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
+    c = np.searchsorted(_E4M3[:127], np.rint(a / step) * step).astype(np.uint8)
+    return np.where(np.isnan(x), 0x7F, c | np.where(np.signbit(x), 128, 0)).astype(np.uint8)
+
+
+CACHE8_BLOCK, CACHE8_GREATEST = 16, 61440.0
+
+
+def cache8_limited(x) -> np.ndarray:
+    """What the cache rounds: at most 240 * 2^8 in magnitude, NaN as it is."""
+    return np.clip(np.asarray(x, np.float64), -CACHE8_GREATEST, CACHE8_GREATEST)
+
+
+def cache8_scale(top) -> np.ndarray:
+    """The least 2^e, e of -15 .. 8, with top <= 448 * 2^e."""
+    top = np.asarray(top, np.float64)
+    s = np.full(top.shape, 2.0 ** -15)
+    for _ in range(23):
+        s = np.where(top > 448 * s, 2 * s, s)
+    return s
+
+
+def cache8_rescale(codes, old, new) -> np.ndarray:
+    """Codes of one scale as codes of another one."""
+    return e4m3_codes(e4m3_values(codes) * (np.asarray(old, np.float64) / np.asarray(new, np.float64)))
+
+
+def cache8_accept(codes, scales, table, ctx: int, n: int, path) -> None:
+    """Moves the rows of a path into place, in codes [layers, pages, heads, size, d] and scales [layers, pages, heads,
+    blocks] of one sequence's page table, block by block."""
+    size = codes.shape[3]
+    where = lambda j: (table[j // size], j % size)
+    dst = [i for i in range(len(path)) if path[i] != i]
+    while dst:
+        page, at = where(ctx + dst[0])
+        lo = at // CACHE8_BLOCK * CACHE8_BLOCK
+        first = ctx + dst[0] - (at - lo)  # the block's first position
+        count = min(CACHE8_BLOCK, size - lo, ctx + n - first)
+        here = [i for i in dst if ctx + i < first + count]
+        come = []
+        for i in here:
+            p, r = where(ctx + path[i])
+            come.append((lo + ctx + i - first, codes[:, p, :, r].copy(), scales[:, p, :, r // CACHE8_BLOCK].copy()))
+        own = scales[:, page, :, lo // CACHE8_BLOCK].copy()
+        new = own.copy()
+        for _, _, s in come:
+            new = np.maximum(new, s)
+        part = codes[:, page, :, lo:lo + count]
+        part[...] = np.where((new != own)[..., None, None], cache8_rescale(part, own[..., None, None], new[..., None, None]), part)
+        for r, x, s in come:
+            codes[:, page, :, r] = np.where((new != s)[..., None], cache8_rescale(x, s[..., None], new[..., None]), x)
+        scales[:, page, :, lo // CACHE8_BLOCK] = new
+        dst = dst[len(here):]

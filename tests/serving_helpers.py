@@ -55,3 +55,43 @@ def mask_words(rows, words):
 
 def random_tree(g, n, fan=4):
     return [-1] + [int(g.integers(max(0, i - 1 - fan * 3), i)) for i in range(1, n)]
+
+
+class Batch8(Batch):
+    """A Batch whose cache is in 8 bits: k8, v8 codes and k_scales, v_scales;
+    k and v are what they stand for.  Magnitudes differ by head, position and
+    element.  Rows that hold no position are NaN, the scales of blocks that
+    hold none as well."""
+
+    def __init__(self, g, ctx, n, Hkv, d, page, spare=2, layers=1, spread=1.0):
+        super().__init__(g, ctx, n, Hkv, d, page, spare, layers)
+        self.nb = -(-page // 16)
+        for name in ("k", "v"):
+            x = getattr(self, name).astype(np.float64)
+            x *= np.exp(g.standard_normal((layers, 1, Hkv, 1, d)) * 0.7 * spread)
+            x *= np.exp(g.standard_normal((layers, self.n_pages, Hkv, page, 1)) * 0.5 * spread)
+            full = np.full(x.shape[:3] + (self.nb * 16, d), np.nan)
+            full[..., :page, :] = x
+            with np.errstate(all="ignore"):
+                top = np.fmax.reduce(np.abs(full).reshape(x.shape[:3] + (self.nb, 16 * d)), -1)
+            scale = np.where(np.isnan(top), np.nan, oracle.cache8_scale(np.nan_to_num(top)))
+            codes = oracle.e4m3_codes(x / np.repeat(scale, 16, -1)[..., :page, None])
+            setattr(self, name + "8", codes)
+            setattr(self, name + "_scales", scale.astype(np.float32))
+        self.set_values()
+
+    def set_values(self):
+        for name in ("k", "v"):
+            setattr(self, name, self.values(getattr(self, name + "8"), getattr(self, name + "_scales")))
+
+    def values(self, codes, scales):
+        return oracle.e4m3_values(codes) * np.repeat(scales.astype(np.float64), 16, -1)[..., :self.page, None]
+
+    def to_device(self, q4):
+        self.d8 = [torch_dev(x) for x in (self.k8, self.v8, self.k_scales, self.v_scales)]
+        self.dtable = torch_dev(self.table)
+        self.dctx, self.dstart = torch_dev(np.array(self.ctx, np.int32)), torch_dev(self.start)
+        return q4.PagedCache8(*self.d8, self.n_pages, self.page, self.Hkv, self.d, self.dtable, self.S, self.max_pages)
+
+    def from_device(self):
+        return [x.cpu().numpy() for x in self.d8]
