@@ -11,6 +11,11 @@ __device__ __forceinline__ uint32_t e4m3_half2(uint32_t w) {
     asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }" : "=r"(h) : "r"(w));
     return h;
 }
+__device__ __forceinline__ uint32_t e4m3_half2_hi(uint32_t w) {  // bits 16 .. 31
+    uint32_t h;
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi; }" : "=r"(h) : "r"(w));
+    return h;
+}
 __device__ __forceinline__ float2 e4m3_f32(uint32_t w) {
     const uint32_t h = e4m3_half2(w);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));

@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     uint32_t b[4];
                     ldsm4(kb + off(wn * KW + nt * 8 + (lane & 7), kk + (lane >> 3)), b);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mma(sc[nt], qf[kk + e], q4p::e4m3_half2(b[e]), q4p::e4m3_half2(b[e] >> 16));
+                    for (int e = 0; e < 4; ++e) mma(sc[nt], qf[kk + e], q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
                 }
             }
             const float* ks = scales_s + st * (Ring<D, k8>::kScales / 4) + wn * KW + 2 * u;
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const uint32_t x = __byte_perm(b[2 * e], 0u, 0x3120), y = __byte_perm(b[2 * e + 1], 0u, 0x3120);
                         const int dn = 2 * (ch + e);
                         mma(o[dn], pa[kj], mul2(q4p::e4m3_half2(x), s0), mul2(q4p::e4m3_half2(y), s1));
-                        mma(o[dn + 1], pa[kj], mul2(q4p::e4m3_half2(x >> 16), s0), mul2(q4p::e4m3_half2(y >> 16), s1));
+                        mma(o[dn + 1], pa[kj], mul2(q4p::e4m3_half2_hi(x), s0), mul2(q4p::e4m3_half2_hi(y), s1));
                     }
                 }
             } else {
@@ -1369,16 +1369,71 @@ inline q4_status attention_args(Args& a, const uint32_t* mask, int mask_words, c
     return Q4_OK;
 }
 
-// ------------------------------------------------------ for the tcgen05 kernels ---
+// ------------------------------------------------- tcgen05: many rows per job ---
+// From a few dozen rows per kv head on the products bound the work, and they
+// belong to the 5th-generation tensor cores.  A CTA takes a job of up to 256
+// rows and 128-position tiles as two streams of 128 rows (the MMA's M):
+//   more than 128 rows: stream i has rows 128 i .. and every tile, so a tile
+//     of keys and values is read once for 256 rows;
+//   else: both streams have the same rows and alternate tiles, and their
+//     (m, l, O) are joined at the end.
+// Per stream a warpgroup computes the softmax (thread = row = TMEM lane) while
+// the tensor cores work for the other stream, and one warp issues, in order,
+//   S(0) | PVa(0) PVb(0) S(1) | PVa(1) PVb(1) S(2) | ...
+// S = Q K^T (128 x 128, Q and K from shared memory) and O += P V (P, fp16,
+// from tensor memory over the scores it came from, V read MN-major; a, b: the
+// positions 0 .. 63 and 64 .. 127, each as soon as its P is there).  MMAs of
+// one thread run in order, so S(k + 1) may overwrite what P V(k) reads, and
+// the commit behind S(k + 1) tells the softmax that O holds step k's product.
+// Tensor memory (512 columns): S 0 and 1 (128 each), O 0 and 1.
+// The reference maximum of a row moves only when its maximum exceeds it by
+// more than kLag (a factor 2^3); then O and l are rescaled.
+// Key and value tiles come by TMA as boxes of `box` rows (the greatest power
+// of two, 8 .. 128, that divides the page): a box lies in one page.  A page
+// that does not exist is read outside the map, where TMA fills in zeros.
+//
+// Measured: a chunk of 1024 and one of 532 rows over 6000 and 4100 positions
+// (32 query heads on 8 kv heads of 128) 134 us = 1.10 PFLOP/s, 58 % of the
+// measured matrix rate, the tensor pipe active half of the time: the softmax
+// of a stream is not always done when the other's products are; 14 us are the
+// joining of the parts.  Trees of up to 61 rows over 8 contexts up to 20000:
+// 86 us = 4.4 TB/s of cache (375 MB).  A job's beginning and end (queries in,
+// tensor memory out: some 5 us) are what short contexts cost.
+constexpr int kTcKeys = 128;
+// warps 0..3, 4..7: softmax of stream 0, 1; 8: keys, 9: values, 10, 11: MMA of stream 0, 1; 8 bits: 12..15: keys and values
+constexpr int kTcThreads = 384, kTc8Threads = 512;
+// Units of a tile, with two row streams and with alternate tiles (8 : 8 instead:
+// trees 101 us, 8 : 4: 96), and of a job before its tiles.  us with lead 0 / 16 /
+// 32: 64 trees of 30 over 1000 positions 113 / 66 / 64, 8 trees of 40 up to 8000
+// 67 / 49 / 48, the chunks 137 / 135 / 132.
+constexpr int kTcCostFull = 8, kTcCostHalf = 5, kTcLead = 32;
+
+template <int D>
+struct TcShape {
+    static constexpr uint32_t kTile = 128 * D * 2;      // a 128 x D fp16 tile: D / 64 swizzled slabs of 16 KB
+    static constexpr int kStages = D == 128 ? 2 : 4;    // of keys, and of values
+    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * (size_t)kTile + 512 + 8 * 2048;  // tiles, barriers, staging
+};
+
+// 8 bits: a slot for 32 positions' codes per converting warp, and staging half as
+// wide to make room for them.
+constexpr int kTcSlots = kTc8Threads / 32 - 11;
+template <int D>
+struct Tc8Shape : TcShape<D> {
+    static constexpr uint32_t kSlot = 32 * D;
+    static constexpr size_t kSmem = 1024 + (2 + 2 * TcShape<D>::kStages) * (size_t)TcShape<D>::kTile + 512 + 8 * 1024 + kTcSlots * kSlot;
+};
+
 struct TcBars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t v_clean[4];  // two row streams: stream 0 has cleared what stream 1's products must not meet
     // per stream: a step's scores; its P, positions 0 .. 63 and 64 .. 127; its turn
     uint64_t s_full[2], pa_full[2], pb_full[2], turn[2], drain[2];
     uint64_t q_full, o_full, x_full, x_done;
+    uint64_t raw_full[kTcSlots];  // 8 bits
     uint32_t tmem_base;
     volatile int abort;
-    volatile int odd[2];  // last segment (by parity) that met infinities or NaN among its new rows' values
+    volatile int odd[8];  // last segment (modulo kOdd) that met infinities or NaN among its new rows' values
 };
 
 __device__ __forceinline__ bool tc_wait(TcBars& B, uint64_t& bar, uint32_t parity, int* err) {
@@ -1404,6 +1459,18 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+// Likewise 8 or 16.
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
+    if constexpr (N == 16) {
+        q4t::ld16(taddr, r);
+    } else {
+        static_assert(N == 8, "");
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    }
 }
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -1439,6 +1506,708 @@ __device__ __forceinline__ uint32_t sees_word(const Args& a, const Seq& q, int t
 // New rows that every row of the job sees.
 __device__ __forceinline__ int all_see(const Args& a, const Place& p) {
     return a.mask ? 0 : (int)q4p::page_of(a.by_g, p.rb * a.BM) + 1;
+}
+
+// Clears row `row` of a value tile, or only its infinities and NaN; whether there were any.
+template <int D>
+__device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
+    bool found = false;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+        uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * 16384 + sw_off(row, c & 7));
+        if (all) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 w = *at;
+        uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!finite16((uint16_t)ws[e])) ws[e] &= 0xffff0000u, bad = true;
+            if (!finite16((uint16_t)(ws[e] >> 16))) ws[e] &= 0x0000ffffu, bad = true;
+        }
+        if (bad) *at = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+        found |= bad;
+    }
+    return found;
+}
+
+//
+// k8: warps 9 and 12 .. 15 bring the codes and make them fp16, 32 positions of a
+// tile at a time, in turn, first the keys', then the values'.  Each has a slot of
+// its own in shared memory: it waits for a copy, takes it into registers, sets
+// the next copy going (bulk copies of the rows that lie together in a page) and,
+// when the tile that the MMA reads is free, stores the rows into it with the
+// scales multiplied in (exact).  It also clears what must not reach every row,
+// so that the softmax has nothing to do with the tiles.
+template <int D, bool k8>
+__global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
+    tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const __grid_constant__ MapArgs t) {
+    using Sh = std::conditional_t<k8, Tc8Shape<D>, TcShape<D>>;
+    static_assert(sizeof(TcBars) <= 512, "barriers");
+    constexpr uint32_t kTile = Sh::kTile;
+    constexpr int NST = Sh::kStages, SLABS = D / 64;
+    constexpr int kThr = k8 ? kTc8Threads : kTcThreads;
+    // Notes of infinities and NaN: the warps that find them run ahead of the
+    // ones that read them by less than so many segments (the softmax by one; the
+    // tiles' warps by the stages as well, 4 at most, of a tile each, and by the
+    // positions in their registers).
+    constexpr uint32_t kOdd = k8 ? 8 : 2;
+    constexpr uint32_t kColS = 0, kColO = 256;
+    const Args& a = t.a;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ unsigned share_s;
+    __shared__ __align__(16) unsigned sums[2 * 256];  // the threads' running sums; later (m, l) of both streams' rows, float2
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* q_s = base;                              // two tiles; between segments, stream 1's O (fp32)
+    uint8_t* k_s = base + 2 * kTile;
+    uint8_t* v_s = k_s + NST * kTile;
+    TcBars& B = *reinterpret_cast<TcBars*>(v_s + NST * kTile);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* err = a.w.err;
+
+    if (tid == 0) {
+        for (int i = 0; i < NST; ++i) {
+            q4d::mbar_init(q4d::smem_addr(&B.k_full[i]), k8 ? 4 : 1);
+            q4d::mbar_init(q4d::smem_addr(&B.k_empty[i]), 2);  // both streams' MMAs
+            q4d::mbar_init(q4d::smem_addr(&B.v_full[i]), k8 ? 4 : 1);
+            q4d::mbar_init(q4d::smem_addr(&B.v_empty[i]), 2);
+            q4d::mbar_init(q4d::smem_addr(&B.v_clean[i]), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            q4d::mbar_init(q4d::smem_addr(&B.s_full[i]), 1);
+            q4d::mbar_init(q4d::smem_addr(&B.pa_full[i]), 4);
+            q4d::mbar_init(q4d::smem_addr(&B.pb_full[i]), 4);
+            q4d::mbar_init(q4d::smem_addr(&B.turn[i]), 4);
+            q4d::mbar_init(q4d::smem_addr(&B.drain[i]), 1);
+        }
+        for (int i = 0; i < (int)kOdd; ++i) B.odd[i] = 0;
+        if constexpr (k8)
+            for (int i = 0; i < kTcSlots; ++i) q4d::mbar_init(q4d::smem_addr(&B.raw_full[i]), 1);
+        q4d::mbar_init(q4d::smem_addr(&B.q_full), 8);
+        q4d::mbar_init(q4d::smem_addr(&B.o_full), 2);
+        q4d::mbar_init(q4d::smem_addr(&B.x_full), 8);
+        q4d::mbar_init(q4d::smem_addr(&B.x_done), 8);
+        B.abort = 0;
+        q4d::fence_mbar_init();
+    }
+    if (warp == 11) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         q4d::smem_addr(&B.tmem_base))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const unsigned line = line_scan(a, sums, kThr);
+    q4t::fence_before();
+    __syncthreads();
+    q4t::fence_after();
+    q4d::pdl_trigger();
+    const uint32_t tmem = B.tmem_base;
+
+    if (tid == 0) {  // (the thread that may write a record later)
+        a.rec[blockIdx.x] = make_int4(0, 0, 0, 0);
+        share_s = line_share(a, line);
+    }
+
+    Walk w;
+    if (w.begin(a, sums, kThr, line)) {
+        // Every role walks the same segments.
+        Place& p = w.p;
+        bool rest = true;     // segments to do
+        uint32_t seg = 0;   // segments done
+        uint32_t tiles0 = 0;  // tiles before this segment
+
+        if (k8 && (warp == 9 || warp >= 12)) {
+            // --------------------------------------------- codes to fp16
+            if constexpr (k8) {
+                constexpr int NC = D / 8, PER = 32 / NC, NL = 32 / PER;  // lanes of a row (8 codes each), rows at a time, loads
+                constexpr uint32_t kConv = kTcSlots;
+                const int c = lane % NC, g = lane / NC, own = warp == 9 ? 0 : warp - 11;
+                uint8_t* const slot = reinterpret_cast<uint8_t*>(&B) + 512 + 8 * 1024 + own * Sh::kSlot;
+                const uint32_t slot_s = q4d::smem_addr(slot) + lane * D, fb = q4d::smem_addr(&B.raw_full[own]);
+                // Quarters of the line's tiles, 4 each; lane = position.  A quarter
+                // is looked up when the one before it is asked into L2 (a slot is
+                // too little for memory's latency), which is while the one before
+                // that is stored.  The cursor p stands at the tile of quarter
+                // `next`, the last one looked up.
+                uint32_t next = own, kt = 0;
+                int id = -1, key = 0;
+                bool live = false;
+                const auto look_up = [&]() {  // (the page number is used later)
+                    key = p.tile * kTcKeys + 32 * (int)(next & 3) + lane;
+                    live = key < p.q.ctx + p.q.n;
+                    if (live) id = a.w.table[(size_t)p.s * a.w.max_pages + q4p::page_of(a.w.div, (uint32_t)key)];
+                };
+                // moves the cursor on, to quarter `next` (false: there is none)
+                const auto advance = [&]() {
+                    while (next >= 4 * kt + 4) {
+                        ++kt;
+                        if (++p.tile < w.end) continue;
+                        ++seg;
+                        if (!w.more(a)) return false;
+                        w.next(a);
+                    }
+                    return true;
+                };
+                // number, segment, rows that exist, first new row (32 and more:
+                // none); this lane's row (offset) and scales
+                struct Quarter {
+                    uint32_t at, seg, there;
+                    int fresh;
+                    long long row;
+                    float ks, vs;
+                };
+                const auto resolve = [&]() {
+                    Quarter x;
+                    const bool mine = live && (uint32_t)id < (uint32_t)a.w.n_pages;
+                    if (live && !mine) atomicOr(err, q4d::kErrDeviceCheck);
+                    const int in_page = (int)((uint32_t)key - q4p::page_of(a.w.div, (uint32_t)key) * a.w.div.d);
+                    const long long head = (long long)id * a.w.H + p.h, at = head * a.nb + in_page / q4p::kBlock;
+                    x.row = (head * a.w.div.d + in_page) * D;
+                    x.ks = mine ? a.ks[at] : 0.f;
+                    x.vs = mine ? a.vs[at] : 0.f;
+                    x.there = __ballot_sync(0xffffffffu, mine);
+                    x.at = next;
+                    x.seg = seg;
+                    x.fresh = p.q.ctx - (key - lane);
+                    return x;
+                };
+                const auto leads = [&](const Quarter& x) { return (x.there >> lane & 1u) && (lane & (t.box - 1)) == 0; };
+                const auto copy = [&](const Quarter& x, const uint16_t* pool) {
+                    const bool mine = leads(x);
+                    const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                    if (lane == 0) q4d::mbar_arrive_expect_tx(fb, (uint32_t)(boxes * t.box * D));
+                    __syncwarp();
+                    if (mine) q4d::bulk_g2s(slot_s, reinterpret_cast<const uint8_t*>(pool) + x.row, (uint32_t)(t.box * D), fb);
+                };
+                bool more = advance();
+                Quarter now = {}, then = {};
+                if (more) {
+                    look_up();
+                    now = resolve();
+                    copy(now, a.w.k);
+                    next += kConv;
+                }
+                bool further = more && advance(), again = false;
+                if (further) look_up();
+                // `turns` copies have been taken: keys and values by turns.  (One
+                // body for both: the code's length costs instruction fetches.)
+                uint32_t turns = 0;
+                bool flying = more;  // a copy is on its way
+#pragma unroll 1
+                while (more) {
+                    const bool values = turns & 1;
+                    const uint32_t tile = now.at >> 2, st = tile % NST;
+                    if (!__all_sync(0xffffffffu, tc_wait(B, B.raw_full[own], turns & 1, err))) break;
+                    ++turns;
+                    uint2 r[NL];
+#pragma unroll
+                    for (int e = 0; e < NL; ++e) r[e] = *reinterpret_cast<const uint2*>(slot + e * 256 + lane * 8);
+                    const float scale = values ? now.vs : now.ks;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next copy may write the slot
+                    __syncwarp();
+                    if (now.there != 0xffffffffu) {
+#pragma unroll
+                        for (int e = 0; e < NL; ++e)
+                            if (!(now.there >> (e * PER + g) & 1u)) r[e] = make_uint2(0u, 0u);
+                    }
+                    if (!values) again = further;
+                    flying = !values || again;
+                    if (flying) copy(values ? then : now, values ? a.w.k : a.w.v);
+                    if (!values) {
+                        if (further) then = resolve();
+                        next += kConv;
+                    } else {
+                        if (further && (further = advance())) look_up();
+                        if (now.fresh < 32) {  // new rows' NaN
+                            bool found = false;
+#pragma unroll
+                            for (int e = 0; e < NL; ++e) {
+                                if (e * PER + g < now.fresh) continue;
+                                const uint2 x = make_uint2(without_nan(r[e].x), without_nan(r[e].y));
+                                found |= x.x != r[e].x || x.y != r[e].y;
+                                r[e] = x;
+                            }
+                            if (found) B.odd[now.seg & (kOdd - 1)] = (int)now.seg + 1;
+                            __syncwarp();
+                        }
+                    }
+                    uint64_t* empty = values ? B.v_empty : B.k_empty;
+                    if (tile >= (uint32_t)NST && !__all_sync(0xffffffffu, tc_wait(B, empty[st], (tile / NST - 1) & 1, err))) break;
+                    // row y = e * PER + g at (y / 8) * 1024 + (y % 8) * 128, chunk c of its slab
+                    uint8_t* const to = (values ? v_s : k_s) + st * kTile + (c >> 3) * 16384 + 4096 * (now.at & 3);
+                    const uint32_t f2 = pack2(scale, scale);
+#pragma unroll
+                    for (int e = 0; e < NL; ++e) {
+                        const uint32_t f = __shfl_sync(0xffffffffu, f2, e * PER + g);
+                        *reinterpret_cast<uint4*>(to + sw_off(e * PER + g, c & 7)) =
+                            make_uint4(mul2(q4p::e4m3_half2(r[e].x), f), mul2(q4p::e4m3_half2_hi(r[e].x), f),
+                                       mul2(q4p::e4m3_half2(r[e].y), f), mul2(q4p::e4m3_half2_hi(r[e].y), f));
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(values ? &B.v_full[st] : &B.k_full[st]));
+                    if (values) {
+                        now = then;
+                        more = again;
+                    }
+                }
+                if (flying) q4d::mbar_wait(fb, turns & 1, nullptr);  // a copy in flight lands before the CTA can exit
+            }
+        } else if (k8 && warp == 8) {
+            // (nothing to do)
+        } else if (!k8 && (warp == 8 || warp == 9)) {
+            // --------------------------------------------- key / value tiles
+            const bool keys = warp == 8;
+            uint64_t* full = keys ? B.k_full : B.v_full;
+            uint64_t* empty = keys ? B.k_empty : B.v_empty;
+            uint8_t* dst0 = keys ? k_s : v_s;
+            const CUtensorMap* map = keys ? &tmK : &tmV;
+            const int boxes = kTcKeys / t.box;
+            bool ok = true;
+            uint32_t kt = 0;
+            while (rest && ok) {
+                const int T = w.end - p.tile;
+                const int len = p.q.ctx + p.q.n;
+                for (int j = 0; j < T && ok; ++j, ++kt) {
+                    const uint32_t st = kt % NST;
+                    if (kt >= (uint32_t)NST) ok = __all_sync(0xffffffffu, tc_wait(B, empty[st], (kt / NST - 1) & 1, err));
+                    if (!ok) break;
+                    const uint32_t fb = q4d::smem_addr(&full[st]);
+                    if (lane == 0) q4d::mbar_arrive_expect_tx(fb, kTile);
+                    __syncwarp();
+                    for (int b = lane; b < boxes; b += 32) {
+                        const int key = (p.tile + j) * kTcKeys + b * t.box;
+                        int y = t.zero_row;
+                        if (key < len) {
+                            const long long at = q4p::row_at(a.w, p.s, key, p.h, 1);
+                            if (at >= 0) y = (int)at;
+                            else atomicOr(err, q4d::kErrDeviceCheck);
+                        }
+                        const uint32_t dst = q4d::smem_addr(dst0 + st * kTile) + (uint32_t)(b * t.box) * 128u;
+#pragma unroll
+                        for (int sl = 0; sl < SLABS; ++sl) q4t::tma_load_2d(dst + sl * 16384, map, 64 * sl, y, fb);
+                    }
+                }
+                rest = w.more(a);
+                if (rest && ok) w.next(a);
+            }
+            if (!ok) {  // copies still in flight land before the CTA can exit
+                for (uint32_t i = kt > (uint32_t)NST ? kt - NST : 0; i < kt; ++i)
+                    q4d::mbar_wait(q4d::smem_addr(&full[i % NST]), (i / NST) & 1, nullptr);
+            }
+        } else if (warp == 10 || warp == 11) {
+            // ------------------------------------------------- MMA issue
+            // One warp per stream (a completed wait costs an issuing thread
+            // about as much as four MMAs, so the streams' waits run side by
+            // side), one elected lane issuing.
+            const int i = warp - 10;
+            const bool leader = elect_one();
+            const uint32_t id_s = q4t::idesc_f16_m128(kTcKeys, 0), id_o = q4t::idesc_f16_m128(D, 1);
+            const uint64_t dq = q4t::sw128_desc(q4d::smem_addr(q_s), 16, 1024);
+            const uint64_t dk = q4t::sw128_desc(q4d::smem_addr(k_s), 16, 1024);
+            const uint64_t dv = q4t::sw128_desc(q4d::smem_addr(v_s), 16384, 1024);
+            const uint32_t sd = tmem + kColS + 128 * i, od = tmem + kColO + 128 * i;
+            bool ok = true;
+            uint32_t n_p = 0;     // steps done: the phases of pa_full and pb_full
+            uint32_t cleans = 0;  // parity of the v_clean phases passed, a bit per stage
+            while (rest && ok) {
+                const int T = w.end - p.tile;
+                const bool two = p.q.n * a.G - p.rb * a.BM > 128;
+                const int steps = two ? T : (T - i + 1) / 2;
+                const uint64_t ad = dq + (uint64_t)((two ? i : 0) * (kTile / 16));
+                const auto tile_of = [&](int k) { return tiles0 + (two ? k : 2 * k + i); };
+                // the scores of step k (its keys have landed)
+                const auto issue_s = [&](int k) {
+                    const uint32_t st = tile_of(k) % NST;
+                    const uint64_t bd = dk + (uint64_t)(st * (kTile / 16));
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) / 16);
+                            q4t::mma_ss(sd, ad + off, bd + off, id_s, kk > 0 ? 1u : 0u);
+                        }
+                        q4t::commit(q4d::smem_addr(&B.s_full[i]));
+                        q4t::commit(q4d::smem_addr(&B.k_empty[st]));
+                        if (!two) q4t::commit(q4d::smem_addr(&B.k_empty[st]));  // the barrier counts both streams
+                    }
+                    __syncwarp();
+                };
+                // half h of O += P V of step k: its positions 64 h ..
+                const auto issue_pv = [&](int k, int h) {
+                    const uint64_t bd = dv + (uint64_t)((tile_of(k) % NST) * (kTile / 16));
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            q4t::mma_ts(od, sd + 8 * kk, bd + (uint64_t)(kk * 2048 / 16), id_o, (k > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    __syncwarp();
+                };
+                const auto wait_k = [&](int k) {
+                    const uint32_t kt = tile_of(k);
+                    return tc_wait(B, B.k_full[kt % NST], (kt / NST) & 1, err);
+                };
+                ok = tc_wait(B, B.q_full, seg & 1, err);
+                if (ok && steps > 0) {
+                    ok = wait_k(0);
+                    q4t::fence_after();
+                    if (ok) issue_s(0);
+                }
+                for (int k = 0; k < steps && ok; ++k) {
+                    const uint32_t kt = tile_of(k), st = kt % NST;
+                    const bool more = k + 1 < steps;
+                    ok = tc_wait(B, B.v_full[st], (kt / NST) & 1, err) && (!more || wait_k(k + 1)) &&
+                         tc_wait(B, B.pa_full[i], n_p & 1, err);
+                    if (!k8 && ok && two && i == 1 && (p.tile + k + 1) * kTcKeys > p.q.ctx + all_see(a, p)) {
+                        ok = tc_wait(B, B.v_clean[st], cleans >> st & 1, err);
+                        cleans ^= 1u << st;
+                    }
+                    if (!ok) break;
+                    q4t::fence_after();
+                    issue_pv(k, 0);
+                    if (!(ok = tc_wait(B, B.pb_full[i], n_p & 1, err))) break;
+                    q4t::fence_after();
+                    issue_pv(k, 1);
+                    ++n_p;
+                    if (more) issue_s(k + 1);
+                    if (leader) {
+                        q4t::commit(q4d::smem_addr(&B.v_empty[st]));
+                        if (!two) q4t::commit(q4d::smem_addr(&B.v_empty[st]));
+                        if (!more) q4t::commit(q4d::smem_addr(&B.o_full));
+                    }
+                    __syncwarp();
+                }
+                if (steps == 0 && leader) q4d::mbar_arrive(q4d::smem_addr(&B.o_full));
+                tiles0 += T;
+                ++seg;
+                rest = w.more(a);
+                if (rest && ok) w.next(a);
+            }
+            if (!ok) B.abort = 1;
+            // every MMA this warp issued has finished before the CTA winds down
+            if (leader) q4t::commit(q4d::smem_addr(&B.drain[i]));
+            __syncwarp();
+            q4d::mbar_wait(q4d::smem_addr(&B.drain[i]), 0, nullptr);
+        } else if (warp < 8) {
+            // ------------------------------------------------- softmax
+            const int i = warp >> 2, wr = warp & 3;  // stream, TMEM lane quarter
+            const int row = wr * 32 + lane;
+            const uint32_t lt = tmem + ((uint32_t)(wr * 32) << 16);
+            const uint32_t ts = lt + kColS + 128 * i, to = lt + kColO + 128 * i;
+            const float2 cc = make_float2(a.c, a.c);
+            float* ml_x = reinterpret_cast<float*>(sums);  // [2 streams][128] (m, l), for joins
+            uint32_t n_s = 0;    // steps done: the phases of s_full
+            uint32_t turns = 0;  // turns taken
+            uint32_t joins = 0;  // joined segments so far
+            bool joined = false;  // the last segment was one
+            bool ok = true;
+            // The job's row of this thread (none: -1), as token and head, and
+            // its query into the stream's tile.  Both streams share stream 0's
+            // tile where the job has 128 rows or fewer.
+            const auto job_row = [&](const Place& w) {
+                const int R = min(a.BM, w.q.n * a.G - w.rb * a.BM);
+                const int r = (R > 128 ? 128 * i : 0) + row;
+                return r < R ? r : -1;
+            };
+            const auto put_query = [&](const Place& w) {
+                const bool two = w.q.n * a.G - w.rb * a.BM > 128;
+                if (two || i == 0) {
+                    // this warp's 32 rows, whole rows at a time
+                    const int R = min(a.BM, w.q.n * a.G - w.rb * a.BM);
+                    uint8_t* dst = q_s + (two ? i : 0) * kTile;
+                    constexpr int NC = D / 8, PER = 32 / NC;  // chunks of a row, rows per load
+                    const int c = lane % NC;
+                    const uint32_t col = q4d::smem_addr(dst) + (uint32_t)(c >> 3) * 16384u;
+                    // (asynchronous loads in a loop: code that runs once per
+                    // segment costs its instruction fetches)
+#pragma unroll 4
+                    for (int e = wr * 32 + lane / NC; e < wr * 32 + 32; e += PER) {
+                        const int r = (two ? 128 * i : 0) + e;
+                        const int rr = w.rb * a.BM + min(r, R - 1), tk = (int)q4p::page_of(a.by_g, rr);
+                        cp16(col + sw_off(e, c & 7),
+                             a.q + (size_t)(w.q.start + tk) * a.ldq + (size_t)(w.h * a.G + rr - tk * a.G) * D + 8 * c, r < R);
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.q_full));
+            };
+            // The streams take turns at the exponentials: one computes them
+            // while the tensor cores work for the other.  Left alone they fall
+            // into step and both wait for each other's MMAs.
+            const auto take_turn = [&]() {
+                const bool open = i == 0 && turns == 0;  // stream 0 begins
+                const bool go = open || tc_wait(B, B.turn[i], (turns - (i == 0)) & 1, err);
+                ++turns;
+                return (bool)__all_sync(0xffffffffu, go);
+            };
+            const auto pass_turn = [&]() {
+                __syncwarp();
+                if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.turn[1 - i]));
+            };
+            put_query(p);
+            while (rest) {
+                const int T = w.end - p.tile;
+                const bool two = p.q.n * a.G - p.rb * a.BM > 128;
+                const int r = job_row(p);
+                const int tok = (int)q4p::page_of(a.by_g, p.rb * a.BM + max(r, 0));
+                const int steps = two ? T : (T - i + 1) / 2;
+                const int seen_by_all = p.q.ctx + all_see(a, p);
+                float m = -INFINITY, l = 0.f;
+                for (int j = 0; j < steps; ++j) {
+                    const int tj = two ? j : 2 * j + i;  // tile of the segment
+                    const int key0 = (p.tile + tj) * kTcKeys;
+                    const uint32_t kt = tiles0 + tj, st = kt % NST;
+                    // some row of the job does not see some position of the tile
+                    const bool tail = key0 + kTcKeys > seen_by_all;
+                    // The row in halves, so that it fits the registers: the
+                    // maximum of the second, of the first, P of the first, the
+                    // second once more, P of the second.
+                    uint32_t s[64];
+                    float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    const auto load_half = [&](int h) {
+                        ld32(ts + 64 * h, s);
+                        ld32(ts + 64 * h + 32, s + 32);
+                        q4t::ld_wait();
+                        if (tail) {
+#pragma unroll
+                            for (int w = 0; w < 2; ++w) {
+                                const uint32_t bits = sees_word(a, p.q, tok, key0 + 64 * h + 32 * w - p.q.ctx);
+                                if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(bits >> e & 1u)) s[32 * w + e] = 0xff800000u;
+                            }
+                        }
+                    };
+                    const auto max_half = [&]() {
+#pragma unroll
+                        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f)
+                                x4[f] = fmaxf(x4[f], fmaxf(__uint_as_float(s[e + f]), __uint_as_float(s[e + 4 + f])));
+                    };
+                    ok = __all_sync(0xffffffffu, tc_wait(B, B.s_full[i], n_s & 1, err));
+                    if (!ok) break;
+                    ++n_s;
+                    q4t::fence_after();
+                    load_half(1);
+                    max_half();
+                    load_half(0);
+                    max_half();
+                    const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * a.c;
+                    float corr = 1.f;
+                    if (mx > m + kLag) {
+                        corr = m == -INFINITY ? 1.f : ex2(m - mx);  // nothing seen yet: O and l are zero
+                        m = mx;
+                    }
+                    const float sub = kShift - (m == -INFINITY ? 0.f : m);
+                    const float2 ss = make_float2(sub, sub);
+                    float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
+                    const auto exp_half = [&](int h) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float2 v = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, ss);
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            if (e & 1) sum2 = __fadd2_rn(sum2, v);
+                            else sum = __fadd2_rn(sum, v);
+                            s[e] = pack2(v.x, v.y);
+                        }
+                        st32(ts + 32 * h, s);
+                    };
+                    if (!(ok = take_turn())) break;
+                    exp_half(0);
+                    // (this step's scores are in, so the step before is in O)
+                    if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            ld32(to + c0, s);
+                            q4t::ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * corr);
+                            st32(to + c0, s);
+                        }
+                    }
+                    // A new row's value reaches only the rows that see it, and
+                    // what lies behind the sequence nobody: this thread clears
+                    // its row of the value tile there, or its infinities and
+                    // NaN, which the epilogue adds back where they are seen.
+                    if (!k8 && tail && !(two && i == 1)) {
+                        ok = __all_sync(0xffffffffu, tc_wait(B, B.v_full[st], (kt / NST) & 1, err));
+                        if (!ok) break;
+                        const int nj = key0 + row - p.q.ctx;
+                        if (nj >= 0 && clean_row<D>(v_s + st * kTile, row, nj >= p.q.n)) B.odd[seg & (kOdd - 1)] = (int)seg + 1;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        if (two) {
+                            __syncwarp();
+                            if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.v_clean[st]));
+                        }
+                    }
+                    q4t::st_wait();
+                    if (j == 0 && joined) {  // the other stream's threads have read this one's O
+                        ok = __all_sync(0xffffffffu, tc_wait(B, B.x_done, (joins - 1) & 1, err));
+                        if (!ok) break;
+                    }
+                    q4t::fence_before();
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.pa_full[i]));
+                    load_half(1);
+                    exp_half(1);
+                    pass_turn();
+                    l = fmaf(l, corr, (sum.x + sum2.x) + (sum.y + sum2.y));
+                    q4t::st_wait();
+                    q4t::fence_before();
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.pb_full[i]));
+                }
+                if (ok && !two && steps < (T + 1) / 2) {  // the other stream's last step has no partner here
+                    ok = take_turn();
+                    pass_turn();
+                }
+                if (!ok) break;
+                ok = __all_sync(0xffffffffu, tc_wait(B, B.o_full, seg & 1, err));
+                if (!ok) break;
+                q4t::fence_after();
+                // The next segment's queries go in first: its scores are
+                // computed while this one's results are written.
+                const Place done = p;
+                const uint32_t seg_done = seg;
+                tiles0 += T;
+                ++seg;
+                rest = w.more(a);
+                if (rest) {
+                    w.next(a);
+                    put_query(p);
+                }
+                const bool job_begin = done.tile == 0, whole = job_begin && done.tile + T == done.tiles;
+                if (tid == 0 && job_begin && !whole) write_record(a, done, share_s);
+                // Of a job on alternate tiles every thread has half the row's
+                // columns, of both streams' parts.
+                const bool join = !two && T > 1;
+                float f0 = 1.f, f1 = 0.f;
+                if (join) {
+                    *reinterpret_cast<float2*>(ml_x + 2 * (128 * i + row)) = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_full));
+                    ok = __all_sync(0xffffffffu, tc_wait(B, B.x_full, joins & 1, err));
+                    if (!ok) break;
+                    ++joins;
+                    const float2 u = *reinterpret_cast<const float2*>(ml_x + 2 * row);
+                    const float2 v = *reinterpret_cast<const float2*>(ml_x + 2 * (128 + row));
+                    m = fmaxf(u.x, v.x);
+                    const float ms = m == -INFINITY ? 0.f : m;
+                    f0 = ex2(u.x - ms);
+                    f1 = ex2(v.x - ms);
+                    l = u.y * f0 + v.y * f1;
+                }
+                if (join || two || i == 0) {
+                    const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                    const int slot = 2 * blockIdx.x + (job_begin ? 1 : 0);
+                    const int R = min(a.BM, done.q.n * a.G - done.rb * a.BM);
+                    const int rw = (two ? 128 * i : 0) + wr * 32;  // the warp's first row of the job
+                    if (!whole && r >= 0 && (!join || i == 0)) part_ml(a, slot)[r] = make_float2(m, l);
+                    const int c1 = join ? D / 2 * (i + 1) : D;
+                    const uint32_t t0 = join ? lt + kColO : to;
+                    // kCols columns at a time by way of shared memory, so that a
+                    // warp stores whole sectors: kCols / 4 lanes per row
+                    constexpr int kCols = k8 ? 8 : 16, kPer = kCols / 4, kMask = kPer - 1;
+                    float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&B) + 512) + warp * 32 * kCols;
+#pragma unroll 1
+                    for (int c0 = join ? D / 2 * i : 0; c0 < c1; c0 += kCols) {
+                        uint32_t w[kCols];
+                        float o[kCols];
+                        ld_cols<kCols>(t0 + c0, w);
+                        q4t::ld_wait();
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e) o[e] = __uint_as_float(w[e]) * (f0 * inv);
+                        if (join) {
+                            ld_cols<kCols>(t0 + 128 + c0, w);
+                            q4t::ld_wait();
+#pragma unroll
+                            for (int e = 0; e < kCols; ++e) o[e] = fmaf(__uint_as_float(w[e]), f1 * inv, o[e]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e)
+                            *reinterpret_cast<float4*>(stage + lane * kCols + ((e ^ (lane * kPer / 8 & kMask)) * 4)) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) {
+                            const int y = (e * 32 + lane) / kPer, c = lane & kMask;
+                            const float4 v = *reinterpret_cast<const float4*>(stage + y * kCols + ((c ^ (y * kPer / 8 & kMask)) * 4));
+                            const int ry = rw + y;
+                            if (ry >= R) continue;
+                            if (whole) {
+                                const int rr = done.rb * a.BM + ry, tk = (int)q4p::page_of(a.by_g, rr);
+                                *reinterpret_cast<uint2*>(a.out + (size_t)(done.q.start + tk) * a.ldo +
+                                                          (size_t)(done.h * a.G + rr - tk * a.G) * D + c0 + 4 * c) =
+                                    make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+                            } else {
+                                *reinterpret_cast<float4*>(part_o<D>(a, slot) + (size_t)ry * D + c0 + 4 * c) = v;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (B.odd[seg_done & (kOdd - 1)] == (int)seg_done + 1 && r >= 0) {
+                        const int rr = done.rb * a.BM + r;
+                        add_odd<D, k8>(a, done, T, tok, join ? D / 2 * i : 0, c1,
+                                       whole ? a.out + (size_t)(done.q.start + tok) * a.ldo + (size_t)(done.h * a.G + rr - tok * a.G) * D
+                                             : nullptr,
+                                       part_o<D>(a, slot) + (size_t)r * D);
+                    }
+                }
+                q4t::fence_before();  // O is read before this warp releases the next segment's products
+                joined = join;
+                if (join) {
+                    __syncwarp();
+                    if (lane == 0) q4d::mbar_arrive(q4d::smem_addr(&B.x_done));
+                }
+            }
+        }
+    }
+    q4t::fence_before();
+    __syncthreads();
+    if (warp == 11) {
+        q4t::fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// box: rows that lie together in a page (8 bits: 1, 2 .. 32).
+template <int D, bool k8>
+q4_status launch_tc(Args& a, const Pools& c, void* workspace, int sms, int box, cudaStream_t s, const char* what) {
+    MapArgs t;
+    a.ctas = sms < kMaxTcCtas ? sms : kMaxTcCtas;
+    a.BM = kTcRows;
+    a.KT = kTcKeys;
+    a.KT_log2 = 7;
+    a.cost_full = kTcCostFull;
+    a.lead = kTcLead;
+    a.cost_half = kTcCostHalf;
+    place_parts<D>(a, workspace);
+    t.a = a;
+    t.box = box;
+    t.zero_row = (int)((long long)c.n_pages * c.n_kv_heads * c.page_size);
+    CUtensorMap tmK = {}, tmV = {};
+    if constexpr (!k8) {
+        const q4_status st = pool_maps<false>(&tmK, &tmV, c, (uint32_t)box);
+        if (st != Q4_OK) return st;
+    }
+    using Sh = std::conditional_t<k8, Tc8Shape<D>, TcShape<D>>;
+    constexpr int kThr = k8 ? kTc8Threads : kTcThreads;
+    const auto kern = tree_attn_tc_kernel<D, k8>;
+    static std::atomic<int> marks[64];
+    cudaError_t e = q4i::ensure_smem_attr(reinterpret_cast<const void*>(kern), marks, (int)Sh::kSmem);
+    if (e == cudaSuccess) {
+        kern<<<a.ctas, kThr, Sh::kSmem, s>>>(tmK, tmV, t);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) e = launch_join(tree_join_many_kernel<D>, dim3((unsigned)(4 * sms)), a, s);
+    return e == cudaSuccess ? Q4_OK : q4i::cuda_fail(e, what);
 }
 
 }  // namespace q4x

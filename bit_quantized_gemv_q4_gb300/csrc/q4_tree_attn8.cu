@@ -35,11 +35,12 @@ extern "C" q4_status q4_tree_attention8(const q4_tree_attention8_desc* desc, q4_
     const long long pool_rows = (long long)d.cache.n_pages * d.cache.n_kv_heads * d.cache.page_size;
     const bool tma = even >= 8 && pool_rows < (1ll << 31) - 1;
     const int box = !tma ? 0 : even < q4x::kKeys ? even : q4x::kKeys;
+    if (avg > 32)
+        return D == 128 ? q4x::launch_tc<128, true>(a, pools, d.workspace, dev->sms, even < 32 ? even : 32, s, what)
+                        : q4x::launch_tc<64, true>(a, pools, d.workspace, dev->sms, even < 32 ? even : 32, s, what);
     if (D == 128)
-        return avg <= 16   ? q4x::launch<128, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
-               : avg <= 32 ? q4x::launch<128, 2, true>(a, pools, d.workspace, dev->sms, box, s, what)
-                           : q4x::launch<128, 4, true>(a, pools, d.workspace, dev->sms, box, s, what);
-    return avg <= 16   ? q4x::launch<64, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
-           : avg <= 32 ? q4x::launch<64, 2, true>(a, pools, d.workspace, dev->sms, box, s, what)
-                       : q4x::launch<64, 4, true>(a, pools, d.workspace, dev->sms, box, s, what);
+        return avg <= 16 ? q4x::launch<128, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
+                         : q4x::launch<128, 2, true>(a, pools, d.workspace, dev->sms, box, s, what);
+    return avg <= 16 ? q4x::launch<64, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
+                     : q4x::launch<64, 2, true>(a, pools, d.workspace, dev->sms, box, s, what);
 }
