@@ -365,13 +365,20 @@ constexpr int kConsumers = 128, kThreads = 160;
 // 40 up to 12000 94 / 94 / 94.
 constexpr int kRingCost = 4, kRingLead = 16;
 
-template <int D, bool k8>
+// Positions of a tile.  8 bits, the line of 16-row jobs: 128, as its fixed cost
+// (waits, statistics) weighs twice as much against half the bytes.
+template <int WM, bool kClustered, bool k8>
+constexpr int ring_keys() {
+    return k8 && WM == 1 && !kClustered ? 128 : kKeys;
+}
+
+template <int D, bool k8, int KEYS>
 struct Ring {
-    static constexpr int kStages = k8 ? 4 : 3;
-    static constexpr uint32_t kTile = kKeys * D * (k8 ? 1 : 2);      // keys or values of a tile
-    static constexpr uint32_t kScales = k8 ? 2 * kKeys * 4 : 0;      // scales of its positions, keys' and values'
-    static constexpr uint32_t kJoin = k8 ? 64 * D * 4 : 0;           // where the warps' outputs meet (fp16: a stage)
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kTile + kScales) + kJoin + 256;
+    static constexpr int kStages = !k8 ? 3 : KEYS == 64 ? 4 : 2;
+    static constexpr uint32_t kTile = KEYS * D * (k8 ? 1 : 2);       // keys or values of a tile
+    static constexpr uint32_t kScales = k8 ? 2 * KEYS * 4 : 0;       // scales of its positions, keys' and values'
+    static constexpr uint32_t kQuery = k8 ? 16 * D * 2 : 0;          // a 16-row job's query
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * (2 * kTile + kScales) + kQuery + 256;
 };
 
 constexpr int kMaxStages = 4;
@@ -479,14 +486,15 @@ __device__ __forceinline__ void latch_bad(const Args& a) {
 // apart they are the B operands of an even and an odd column tile, which take
 // the values' scales (powers of two: exact) before the product.
 template <int D, int WM, bool kTma, bool kClustered, bool k8>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ MapArgs t) {
     constexpr int BM = 16 * WM, WN = 4 / WM;
     constexpr int NCH = k8 ? D / 16 : D / 8, KS = D / 16, DN = D / 8, SLABS = k8 ? 1 : D / 64;  // chunks of a row ...
-    constexpr int KW = kKeys / WN, NT = KW / 8;  // a warp's positions of a tile, 8-wide tiles of them
-    constexpr uint32_t TB = Ring<D, k8>::kTile;
-    constexpr int kStages = Ring<D, k8>::kStages;
+    constexpr int KEYS = ring_keys<WM, kClustered, k8>();
+    constexpr int KW = KEYS / WN, NT = KW / 8;  // a warp's positions of a tile, 8-wide tiles of them
+    constexpr uint32_t TB = Ring<D, k8, KEYS>::kTile;
+    constexpr int kStages = Ring<D, k8, KEYS>::kStages;
     constexpr auto off = ring_off<D, k8>;
     const Args& a = t.a;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -494,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ float2 ml_s[4 * 16], fin_s[kClustered ? BM : 1];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* scales_s = reinterpret_cast<float*>(smem + kStages * 2 * TB);  // [stage][keys, values][position]
-    float* join_s = scales_s + kStages * Ring<D, k8>::kScales / 4;
-    RingBars& B = *reinterpret_cast<RingBars*>(reinterpret_cast<uint8_t*>(join_s) + Ring<D, k8>::kJoin);
+    uint8_t* query_s = reinterpret_cast<uint8_t*>(scales_s + kStages * Ring<D, k8, KEYS>::kScales / 4);
+    RingBars& B = *reinterpret_cast<RingBars*>(query_s + Ring<D, k8, KEYS>::kQuery);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -544,28 +552,29 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int st = kt % kStages;
                 const uint32_t fb = q4d::smem_addr(&B.full[st]);
                 uint8_t* kv = smem + st * 2 * TB;
-                // the scales of positions `lane` and `lane` + 32
-                long long scale_at[2];
+                // the scales of positions lane, lane + 32, ..
+                long long scale_at[KEYS / 32];
                 if constexpr (k8) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = p.tile * kKeys + e * 32 + lane;
+                    for (int e = 0; e < KEYS / 32; ++e) {
+                        const int key = p.tile * KEYS + e * 32 + lane;
                         scale_at[e] = key < len ? scale_of(a, p.s, key, p.h) : -1;
                     }
                 }
                 const auto bring_scales = [&]() {
-                    const uint32_t to = q4d::smem_addr(scales_s) + (uint32_t)(st * Ring<D, k8>::kScales + lane * 4);
+                    const uint32_t to = q4d::smem_addr(scales_s) + (uint32_t)(st * Ring<D, k8, KEYS>::kScales + lane * 4);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < KEYS / 32; ++e) {
                         const long long x = scale_at[e] < 0 ? 0 : scale_at[e];
                         cp4(to + e * 128, a.ks + x, scale_at[e] >= 0);
-                        cp4(to + kKeys * 4 + e * 128, a.vs + x, scale_at[e] >= 0);
+                        cp4(to + KEYS * 4 + e * 128, a.vs + x, scale_at[e] >= 0);
                     }
                 };
                 if constexpr (kTma) {
-                    // lanes 0 .. 7: boxes of keys, 8 .. 15: of values
-                    const int b = lane & 7, key = p.tile * kKeys + b * t.box;
-                    const bool mine = lane < 16 && b * t.box < kKeys;
+                    // the first NB lanes: boxes of keys, the next: of values
+                    constexpr int NB = KEYS / 8;
+                    const int b = lane % NB, key = p.tile * KEYS + b * t.box;
+                    const bool mine = lane < 2 * NB && b * t.box < KEYS;
                     int y = t.zero_row;
                     if (mine && key < len) {
                         const long long at = q4p::row_at(a.w, p.s, key, p.h, 1);
@@ -578,10 +587,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (lane == 0) q4d::mbar_arrive_expect_tx(fb, 2 * TB);
                     __syncwarp();
                     if (mine) {
-                        const uint32_t dst = q4d::smem_addr(kv + (lane >> 3) * TB) + (uint32_t)(b * t.box) * (k8 ? D : 128);
+                        const uint32_t dst = q4d::smem_addr(kv + (lane / NB) * TB) + (uint32_t)(b * t.box) * (k8 ? D : 128);
 #pragma unroll
                         for (int sl = 0; sl < SLABS; ++sl)
-                            q4t::tma_load_2d(dst + sl * (kKeys * 128), lane < 8 ? &tmK : &tmV, 64 * sl, y, fb);
+                            q4t::tma_load_2d(dst + sl * (KEYS * 128), lane < NB ? &tmK : &tmV, 64 * sl, y, fb);
                     }
                     if constexpr (k8) {
                         bring_scales();
@@ -596,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     constexpr int PER = 32 / NCH;
                     const int c = lane % NCH;
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        const int key = p.tile * kKeys + half * 32 + lane;
+                    for (int half = 0; half < KEYS / 32; ++half) {
+                        const int key = p.tile * KEYS + half * 32 + lane;
                         long long at = -1;
                         if (key < len) {
                             at = q4p::row_at(a.w, p.s, key, p.h, D);
@@ -638,7 +647,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // but every warp still comes to the barriers the others wait at.
     const int g = lane >> 2, u = lane & 3;
     const int wm = warp / WN, wn = warp % WN;
-    uint32_t qf[KS][4];
+    // (8 bits, 16 rows: in shared memory, so that three CTAs' registers fit an SM)
+    constexpr bool kQShared = k8 && WM == 1, kTwoChains = k8 && NT == 2;
+    uint32_t qf[kQShared ? 1 : KS][4];
     float o[DN][4], m[2], l[2];
     bool fresh = true;              // the job's first tile in this CTA
     bool begun = p.tile == 0;       // ... and in the line
@@ -654,14 +665,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 2; ++e) tok[e] = (int)q4p::page_of(a.by_g, p.rb * BM + min(row0 + 8 * e, R - 1));
         if (fresh) {
+            if constexpr (kQShared) {
+                // Four rows a warp.  A chunk of 16 elements is laid down in the order
+                // in which the codes' words take them, elements 4u, 4u+1 before all
+                // 4u+2, 4u+3, so that ldmatrix finds the fragments.
+                const int r = 4 * warp + (lane >> 3);
+                const bool live = r < R;
+                const int rr = p.rb * BM + min(r, R - 1), tk = (int)q4p::page_of(a.by_g, rr);
+                const uint16_t* src = a.q + (size_t)(p.q.start + tk) * a.ldq + (size_t)(p.h * a.G + rr - tk * a.G) * D;
+#pragma unroll
+                for (int kk = lane & 7; kk < KS; kk += 8) {
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    const uint4 x = live ? *reinterpret_cast<const uint4*>(src + 16 * kk) : z;
+                    const uint4 y = live ? *reinterpret_cast<const uint4*>(src + 16 * kk + 8) : z;
+                    *reinterpret_cast<uint4*>(query_s + swz<D>(r, 2 * kk)) = make_uint4(x.x, x.z, y.x, y.z);
+                    *reinterpret_cast<uint4*>(query_s + swz<D>(r, 2 * kk + 1)) = make_uint4(x.y, x.w, y.y, y.w);
+                }
+                q4d::named_bar(1, kConsumers);  // (they have met at the last segment's end, behind its last use)
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool live = row0 + 8 * e < R;
+                const bool live = !kQShared && row0 + 8 * e < R;
                 const int rr = p.rb * BM + min(row0 + 8 * e, R - 1);
                 const uint16_t* src = a.q + (size_t)(p.q.start + tok[e]) * a.ldq + (size_t)(p.h * a.G + rr - tok[e] * a.G) * D +
                                       (k8 ? 4 : 2) * u;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
+                for (int kk = 0; kk < (kQShared ? 0 : KS); ++kk) {
                     if constexpr (k8) {
                         const uint2 x = live ? *reinterpret_cast<const uint2*>(src + 16 * kk) : make_uint2(0u, 0u);
                         qf[kk][e] = x.x;
@@ -682,8 +711,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t kb = q4d::smem_addr(smem + st * 2 * TB), vb = kb + TB;
         ring_wait(B, B.full[st], (kt / kStages) & 1, a.w.err);
         __syncwarp();
-        const int key0 = p.tile * kKeys;
-        const bool tail = key0 + kKeys > p.q.ctx;  // the tile holds new rows, or the end
+        const int key0 = p.tile * KEYS;
+        const bool tail = key0 + KEYS > p.q.ctx;  // the tile holds new rows, or the end
         if (tail) {
             // A new row's value reaches only the rows that see it, and what
             // lies behind the sequence nobody: those rows are cleared, or
@@ -723,17 +752,39 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
         if constexpr (k8) {
+            float sd[kTwoChains ? NT : 1][4] = {};  // (two chains of products where there are few tiles)
+            static_assert(!kTwoChains || kQShared, "");
+            const uint32_t qs = q4d::smem_addr(query_s);
 #pragma unroll
             for (int kk = 0; kk < KS; kk += 4) {
+                if constexpr (kQShared) {
+                    uint32_t b[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t b[4];
-                    ldsm4(kb + off(wn * KW + nt * 8 + (lane & 7), kk + (lane >> 3)), b);
+                    for (int nt = 0; nt < NT; ++nt) ldsm4(kb + off(wn * KW + nt * 8 + (lane & 7), kk + (lane >> 3)), b[nt]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mma(sc[nt], qf[kk + e], q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t qa[4];
+                        ldsm4(qs + swz<D>(lane & 15, 2 * (kk + e) + (lane >> 4)), qa);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma(kTwoChains && (e & 1) ? sd[kTwoChains ? nt : 0] : sc[nt], qa, q4p::e4m3_half2(b[nt][e]), q4p::e4m3_half2_hi(b[nt][e]));
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t b[4];
+                        ldsm4(kb + off(wn * KW + nt * 8 + (lane & 7), kk + (lane >> 3)), b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mma(sc[nt], qf[kk + e], q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
+                    }
                 }
             }
-            const float* ks = scales_s + st * (Ring<D, k8>::kScales / 4) + wn * KW + 2 * u;
+            if constexpr (kTwoChains)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nt][e] += sd[nt][e];
+            const float* ks = scales_s + st * (Ring<D, k8, KEYS>::kScales / 4) + wn * KW + 2 * u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float2 f = *reinterpret_cast<const float2*>(ks + nt * 8);
@@ -795,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int kj = 0; kj < KW / 16; ++kj) {
             if constexpr (k8) {
-                const float* vs = scales_s + st * (Ring<D, k8>::kScales / 4) + kKeys + wn * KW + kj * 16 + 2 * u;
+                const float* vs = scales_s + st * (Ring<D, k8, KEYS>::kScales / 4) + KEYS + wn * KW + kj * 16 + 2 * u;
                 const float2 f0 = *reinterpret_cast<const float2*>(vs), f1 = *reinterpret_cast<const float2*>(vs + 8);
                 const uint32_t s0 = pack2(f0.x, f0.y), s1 = pack2(f1.x, f1.y);
 #pragma unroll
@@ -843,9 +894,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             // The warps' outputs meet in this tile's stage, [WN][BM][D] fp32
             // (at most 32 KB), which is still ours; a cluster's CTA has
             // consumed all it loads, and takes stage 0, so that the others
-            // know the place.  (8 bits: a place of its own.)
-            float* ob = k8 ? join_s : reinterpret_cast<float*>(smem + (kClustered ? 0 : st * 2 * TB));
-            static_assert((size_t)WN * BM * D * 4 <= (k8 ? Ring<D, k8>::kJoin : 2 * TB), "joining space");
+            // know the place.  (8 bits: a stage is half as large, so they meet
+            // in pairs.)
+            float* ob = reinterpret_cast<float*>(smem + (kClustered ? 0 : st * 2 * TB));
+            static_assert((size_t)(k8 ? (WN + 1) / 2 : WN) * BM * D * 4 <= 2 * TB, "joining space");
             // Nobody reads the tiles any more, and every warp's note of
             // infinities or NaN among the values (B.odd) is there: a warp
             // that finds a row cleared by another one has none of its own.
@@ -868,14 +920,49 @@ __global__ void __launch_bounds__(kThreads, 2)
                     for (int i = 0; i < WN; ++i) ls = fmaf(ml_s[(wm * WN + i) * 16 + r].y, ex2(ml_s[(wm * WN + i) * 16 + r].x - ms), ls);
                     const float f = ex2(m[e] - ms);
                     float* dst = ob + ((size_t)wn * BM + wm * 16 + r) * D;
+                    if constexpr (k8) {
 #pragma unroll
-                    for (int dn = 0; dn < DN; ++dn)
-                        *reinterpret_cast<float2*>(dst + col(dn)) = make_float2(o[dn][2 * e] * f, o[dn][2 * e + 1] * f);
+                        for (int dn = 0; dn < DN; ++dn) {
+                            o[dn][2 * e] *= f;
+                            o[dn][2 * e + 1] *= f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int dn = 0; dn < DN; ++dn)
+                            *reinterpret_cast<float2*>(dst + col(dn)) = make_float2(o[dn][2 * e] * f, o[dn][2 * e + 1] * f);
+                    }
                     m[e] = mm;
                     l[e] = ls;
                 }
-                q4d::named_bar(1, kConsumers);
-                if (wn == 0) {
+                if constexpr (k8) {
+                    // warps WN / 2 .. give theirs to the others, and so on
+#pragma unroll
+                    for (int half = WN / 2; half >= 1; half /= 2) {
+                        float* at = ob + ((size_t)(wn % half) * BM + wm * 16 + g) * D;
+                        if (wn >= half && wn < 2 * half) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int dn = 0; dn < DN; ++dn)
+                                    *reinterpret_cast<float2*>(at + 8 * e * D + col(dn)) = make_float2(o[dn][2 * e], o[dn][2 * e + 1]);
+                        }
+                        q4d::named_bar(1, kConsumers);
+                        if (wn < half) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                                for (int dn = 0; dn < DN; ++dn) {
+                                    const float2 x = *reinterpret_cast<const float2*>(at + 8 * e * D + col(dn));
+                                    o[dn][2 * e] += x.x;
+                                    o[dn][2 * e + 1] += x.y;
+                                }
+                        }
+                        if (half > 1) q4d::named_bar(1, kConsumers);
+                    }
+                } else {
+                    q4d::named_bar(1, kConsumers);
+                }
+                if (!k8 && wn == 0) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -951,7 +1038,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if constexpr (kClustered) {
         // ------------------------------------------------- the cluster's parts
         const int R = min(BM, p.q.n * a.G - p.rb * BM);
-        float* ob = k8 ? join_s : reinterpret_cast<float*>(smem);
+        float* ob = reinterpret_cast<float*>(smem);
         if (!any) {
             for (int y = tid; y < R * D; y += kThreads) ob[y] = 0.f;
             for (int r = tid; r < R; r += kThreads) fin_s[r] = make_float2(-INFINITY, 0.f);
@@ -1261,13 +1348,14 @@ template <int D, int WM, bool kTma, bool kClustered, bool k8>
 cudaError_t launch_kernel(const CUtensorMap& k, const CUtensorMap& v, const MapArgs& t, int grid, cudaStream_t s) {
     static std::atomic<int> marks[64];
     const auto kern = tree_attn_kernel<D, WM, kTma, kClustered, k8>;
+    using R = Ring<D, k8, ring_keys<WM, kClustered, k8>()>;
     const void* fn = reinterpret_cast<const void*>(kern);
-    cudaError_t e = q4i::ensure_smem_attr(fn, marks, (int)Ring<D, k8>::kSmem);
+    cudaError_t e = q4i::ensure_smem_attr(fn, marks, (int)R::kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Ring<D, k8>::kSmem;
+    cfg.dynamicSmemBytes = R::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     if (kClustered) {
@@ -1308,11 +1396,10 @@ q4_status launch(Args& a, const Pools& c, void* workspace, int sms, int box, cud
     MapArgs t;
     CUtensorMap k = {}, v = {};
     a.BM = 16 * WM;
-    a.KT = kKeys;
-    a.KT_log2 = 6;
     a.cost_full = a.cost_half = kRingCost;
     a.lead = kRingLead;
-    a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    const int resident = k8 && WM == 1 ? 3 * sms : 2 * sms;
+    a.ctas = resident < kMaxCtas ? resident : kMaxCtas;
     place_parts<D>(a, workspace);
     if (box) {
         const q4_status st = pool_maps<k8>(&k, &v, c, (uint32_t)box);
@@ -1325,6 +1412,8 @@ q4_status launch(Args& a, const Pools& c, void* workspace, int sms, int box, cud
     const long long jobs = (seqs + ((long long)a.w.rows * a.G - seqs) / a.BM) * c.n_kv_heads;
     t.cluster = cluster_size(jobs, c.n_seqs, (long long)c.max_pages * c.page_size, sms);
     t.cluster_log2 = t.cluster == 16 ? 4 : t.cluster == 8 ? 3 : 2;
+    a.KT = t.cluster ? ring_keys<WM, true, k8>() : ring_keys<WM, false, k8>();
+    a.KT_log2 = a.KT == 128 ? 7 : 6;
     t.a = a;
     const auto run = [&](auto tma) {
         constexpr bool T = decltype(tma)::value;
