@@ -37,16 +37,15 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 }
 
 // ------------------------------------------------------------------ append ---
-// A block of threads looks after `win` rows: it finds their sequences, and
+// A block of threads looks after a window of rows: it finds their sequences, and
 // takes every run of rows that begins among them - in the 8-bit cache the new
 // rows of one block of 16 positions (they share a scale, so one thread block
 // has to have them all), else single rows.  gridDim.y blocks share a window's
-// heads.  NC = D / 8 lanes hold a head of a row, 8 elements each: its mean of
-// squares is a sum over them, and the partner of an element lies in the same
-// lane (neighbours) or the same element of another lane (halves of whole
-// 16-byte chunks), else it is read once more.
-constexpr int kRowThreads = 256;
-constexpr int kWin = 16;                    // rows of a window at most
+// heads.  D / 16 lanes hold a head of a row, 16 elements each, the halves of
+// rotated pairs together where they are whole 16-byte chunks: its mean of
+// squares is a sum over them.
+constexpr int kRowThreads = 256, kAhead = 2;
+constexpr int kWin = 8;                     // rows of a window
 constexpr int kCover = kWin + kBlock - 1;   // rows that runs beginning in it may have
 
 struct RowsArgs {
@@ -62,8 +61,18 @@ struct RowsArgs {
     const uint16_t *qw, *kw;
     int q_norm, k_norm;
     float eps;
-    int win;
 };
+
+// Places of pair i's angle and of element i's weight in shared memory: lanes of
+// a head that read 16 bytes each find them side by side.
+template <int D>
+__device__ __forceinline__ int angle_at(int i) {
+    return ((i & 7) / 2 * (D / 16) + i / 8) * 2 + (i & 1);
+}
+template <int D>
+__device__ __forceinline__ int weight_at(int i) {
+    return ((i & 7) / 4 * (D / 8) + i / 8) * 4 + (i & 3);
+}
 
 // Rows of one sequence that share a block of positions.
 struct Run {
@@ -87,31 +96,33 @@ __device__ __forceinline__ bool find_row(const View& w, int row, int lane, int& 
 
 template <int D, int kPairs, bool k8>
 __global__ void __launch_bounds__(kRowThreads, 4) append_rows_kernel(const __grid_constant__ RowsArgs p) {
-    constexpr int NC = D / 8, G = kRowThreads / NC;  // lanes of a head, heads at a time
+    constexpr int NJ = D / 16, G = kRowThreads / NJ;  // lanes of a head, heads at a time
     constexpr int kMost = k8 ? kCover : kWin;
-    constexpr int kPass = k8 ? (kCover + G - 1) / G : 1;
+    static_assert(kMost <= G, "a head of all covered rows at a time");
     __shared__ Run run_s[kWin];
     __shared__ int row_run[kMost];                   // run of each covered row ...
-    __shared__ int row_at_run[kMost];                // ... and its place in it
+    __shared__ int row_at_run[kMost];                // ... its place in it ...
+    __shared__ int row_s[kMost];                     // ... and number
     __shared__ int rows_s;
     __shared__ __align__(16) float2 cs[kMost][D / 2];
     __shared__ __align__(16) float wq_s[D], wk_s[D];
-    __shared__ uint32_t top_s[3][kWin];              // greatest magnitudes of the runs, as bits
+    constexpr int kHeads = G / kBlock;
+    __shared__ uint32_t top_s[3][kHeads][kWin];      // greatest magnitudes of the runs, as bits
     const View& w = p.c.w;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int r0 = blockIdx.x * p.win;
+    const int r0 = blockIdx.x * kWin;
 
     if (tid < D) {
-        if (p.q_norm) wq_s[tid] = p.qw ? __half2float(__ushort_as_half(p.qw[tid])) : 1.f;
-        if (p.k_norm) wk_s[tid] = p.kw ? __half2float(__ushort_as_half(p.kw[tid])) : 1.f;
+        if (p.q_norm) wq_s[weight_at<D>(tid)] = p.qw ? __half2float(__ushort_as_half(p.qw[tid])) : 1.f;
+        if (p.k_norm) wk_s[weight_at<D>(tid)] = p.kw ? __half2float(__ushort_as_half(p.kw[tid])) : 1.f;
     }
-    if (tid < 3 * kWin) top_s[tid / kWin][tid % kWin] = 0u;
+    if (tid < 3 * kHeads * kWin) top_s[tid / kWin / kHeads][tid / kWin % kHeads][tid % kWin] = 0u;
     for (int i = warp; i < kWin; i += kRowThreads / 32) {
         const int row = r0 + i;
         Run r = {0, 0, 0, 0, -1, 0};
         int s;
         Seq q;
-        if (i < p.win && row < w.rows && find_row(w, row, lane, s, q)) {
+        if (i < kWin && row < w.rows && find_row(w, row, lane, s, q)) {
             r.row = row;
             r.slot = q.ctx + (row - q.start);
             const uint32_t pg = page_of(w.div, (uint32_t)r.slot);
@@ -154,6 +165,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) append_rows_kernel(const __gri
         for (int j = 0; j < m; ++j) {
             row_run[sum - m + j] = lane;
             row_at_run[sum - m + j] = j;
+            row_s[sum - m + j] = run_s[lane].row + j;
         }
     }
     __syncthreads();
@@ -165,169 +177,244 @@ __global__ void __launch_bounds__(kRowThreads, 4) append_rows_kernel(const __gri
         const Run& r = run_s[row_run[t]];
         const int j = row_at_run[t];
         const long long pos = p.positions ? p.positions[r.row + j] : r.slot + j;
-        const uint64_t turn = (uint64_t)pos * p.freqs[i];
+        // The fraction of a turn in 2^-32, exact in integers: the nearest quarter
+        // and what is left of it, at most an eighth, whose float is off by 2^-28
+        // turns at most.
+        const uint32_t turn = (uint32_t)((uint64_t)pos * p.freqs[i] >> 32), quarter = (turn + 0x20000000u) >> 30;
         float sn, cn;
-        sincospif((float)(int32_t)(uint32_t)(turn >> 32) * 4.656612873077393e-10f, &sn, &cn);
-        cs[t][i] = make_float2(cn * p.amplitude, sn * p.amplitude);
+        sincospif((float)(int32_t)(turn - (quarter << 30)) * 4.656612873077393e-10f, &sn, &cn);
+        const float co = quarter & 1u ? -sn : cn, si = quarter & 1u ? cn : sn, sign = quarter & 2u ? -p.amplitude : p.amplitude;
+        cs[t][angle_at<D>(i)] = make_float2(co * sign, si * sign);
     }
     __syncthreads();
 
-    const int g = tid / NC, c = tid % NC, rc = half / 8;
-    // A head of covered row t, loaded by its NC lanes (all lanes of the warp come
-    // here; those without one pass live = false), normalised and rotated.
-    const auto turned = [&](const uint16_t* src, bool live, int t, bool norm, const float* weight, float (&x)[8]) {
-        const uint4 a = live ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-        unpack8(a, x);
+    // Lane j of a head's NJ holds two 16-byte chunks of it: the two halves of
+    // eight rotated pairs, or neighbours (which hold whole pairs, or none).
+    const int g = tid / NJ, j = tid % NJ, rc = half / 8;
+    const int c0 = kPairs == 1 && j < rc ? j : 2 * j, c1 = kPairs == 1 && j < rc ? j + rc : 2 * j + 1;
+    struct Head {
+        uint4 a, b;
+    };
+    const auto fetch = [&](const uint16_t* src, bool live) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        return Head{live ? *reinterpret_cast<const uint4*>(src + 8 * c0) : z, live ? *reinterpret_cast<const uint4*>(src + 8 * c1) : z};
+    };
+    // A head of covered row t, which its lanes hold, normalised and rotated (all
+    // lanes of the warp come here; those without a head pass live = false).
+    const auto turned = [&](const Head& a, const uint16_t* src, bool live, int t, bool norm, const float* weight, float (&x)[16]) {
+        unpack8(a.a, x);
+        unpack8(a.b, x + 8);
         float inv = 1.f;
         if (norm) {
-            float ss = 0.f;
+            float ss = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(x[e], x[e], ss);
+                s2 = fmaf(x[8 + e], x[8 + e], s2);
+            }
+            ss += s2;
 #pragma unroll
-            for (int o = NC / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float v = ss * (1.f / D) + p.eps;
-            inv = v == 0.f ? 0.f : 1.f / sqrtf(v);
+            for (int o = NJ / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float v = fmaf(ss, 1.f / D, p.eps);
+            inv = v == 0.f ? 0.f : rsqrtf(v);  // (2 ulp; a sixteenth of a step of fp16)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * weight[8 * c + e];
+            for (int e = 0; e < 8; e += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(weight + weight_at<D>(8 * c0 + e));
+                const float4 v = *reinterpret_cast<const float4*>(weight + weight_at<D>(8 * c1 + e));
+                const float us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[e + i] *= inv * us[i];
+                    x[8 + e + i] *= inv * vs[i];
+                }
+            }
         }
         if (half == 0) return;
         if constexpr (kPairs == 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 4 * c + e;
-                if (i < half) {
-                    const float2 r = cs[t][i];
-                    const float u = x[2 * e], v = x[2 * e + 1];
-                    x[2 * e] = u * r.x - v * r.y;
-                    x[2 * e + 1] = v * r.x + u * r.y;
+            for (int e = 0; e < 8; e += 2) {
+                const float4 f = *reinterpret_cast<const float4*>(&cs[t][angle_at<D>(8 * j + e)]);
+                const float2 rs[2] = {{f.x, f.y}, {f.z, f.w}};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 r = 8 * j + e + i < half ? rs[i] : make_float2(1.f, 0.f);
+                    const float u = x[2 * (e + i)], v = x[2 * (e + i) + 1];
+                    x[2 * (e + i)] = u * r.x - v * r.y;
+                    x[2 * (e + i) + 1] = v * r.x + u * r.y;
                 }
             }
         } else if constexpr (kPairs == 1) {
-            const int partner = c < rc ? c + rc : c < 2 * rc ? c - rc : c;
-            const int i0 = 8 * min(c, partner);
-            const float sign = c < rc ? -1.f : 1.f;
+            if (j < rc) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = __shfl_sync(0xffffffffu, x[e], partner, NC);
-                if (partner != c) {
-                    const float2 r = cs[t][i0 + e];
-                    x[e] = x[e] * r.x + sign * y * r.y;
+                for (int e = 0; e < 8; e += 2) {
+                    const float4 f = *reinterpret_cast<const float4*>(&cs[t][angle_at<D>(8 * j + e)]);
+                    const float2 rs[2] = {{f.x, f.y}, {f.z, f.w}};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float u = x[e + i], v = x[8 + e + i];
+                        x[e + i] = u * rs[i].x - v * rs[i].y;
+                        x[8 + e + i] = v * rs[i].x + u * rs[i].y;
+                    }
                 }
             }
         } else {
             // pairs (i, i + half) across the chunks
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = 8 * c + e;
+            for (int e = 0; e < 16; ++e) {
+                const int i = 16 * j + e;
                 if (i < 2 * half && live) {
                     const int o = i < half ? i + half : i - half;
                     float y = __half2float(__ushort_as_half(src[o]));
-                    if (norm) y = y * inv * weight[o];
-                    const float2 r = cs[t][min(i, o)];
+                    if (norm) y *= inv * weight[weight_at<D>(o)];
+                    const float2 r = cs[t][angle_at<D>(min(i, o))];
                     x[e] = i < half ? x[e] * r.x - y * r.y : x[e] * r.x + y * r.y;
                 }
             }
             __syncwarp();  // in place (q_out == q): every partner is read before any is written
         }
     };
+    const auto put = [&](uint16_t* dst, const uint4& a, const uint4& b) {
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = a;
+        *reinterpret_cast<uint4*>(dst + 8 * c1) = b;
+    };
+    // items of `count` heads: row of the window's, head (small numbers: by one product)
+    const auto split = [&](int x, int count, uint32_t by, int& t, int& h) {
+        t = x < 65536 && count < 65536 ? (int)__umulhi((uint32_t)x, by) : x / count;
+        if (count == 1) t = x;
+        h = x - t * count;
+    };
 
     const int part = blockIdx.y, parts = gridDim.y;
-    // queries
-    {
-        const int h0 = (int)((long long)p.Hq * part / parts), nh = (int)((long long)p.Hq * (part + 1) / parts) - h0;
-        const int items = T * nh;
-        for (int x0 = 0; x0 < items; x0 += G) {
-            const int x = x0 + g, t = min(x, items - 1) / nh, h = h0 + min(x, items - 1) - t * nh;
-            const bool live = x < items;
-            const long long row = run_s[row_run[t]].row + row_at_run[t];
-            float y[8];
-            turned(p.q + row * p.ldq + (long long)h * D, live, t, p.q_norm, wq_s, y);
-            if (live) *reinterpret_cast<uint4*>(p.q_out + row * p.ldqo + (long long)h * D + 8 * c) = pack8(y);
+    // queries, kAhead heads of a thread's on their way together
+    const int q0 = (int)((long long)p.Hq * part / parts), nq = (int)((long long)p.Hq * (part + 1) / parts) - q0;
+    if (nq > 0) {
+        const int items = T * nq;
+        const uint32_t by = 0xffffffffu / (uint32_t)nq + 1u;
+        for (int i0 = 0; i0 < items; i0 += G * kAhead) {
+            Head a[kAhead];
+            int t[kAhead], h[kAhead];
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int i = i0 + e * G + g;
+                split(min(i, items - 1), nq, by, t[e], h[e]);
+                a[e] = fetch(p.q + (long long)row_s[t[e]] * p.ldq + (long long)(q0 + h[e]) * D, i < items);
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                if (i0 + e * G >= items) break;
+                const bool live = i0 + e * G + g < items;
+                const long long row = row_s[t[e]], at = (long long)(q0 + h[e]) * D;
+                float y[16];
+                turned(a[e], p.q + row * p.ldq + at, live, t[e], p.q_norm, wq_s, y);
+                if (live) put(p.q_out + row * p.ldqo + at, pack8(y), pack8(y + 8));
+            }
         }
     }
     // keys (heads 0 ..) and values (heads H ..)
     const int x0 = (int)(2ll * w.H * part / parts), x1 = (int)(2ll * w.H * (part + 1) / parts);
+    if (x0 == x1) return;
+    const auto source = [&](int x, int t) {
+        const long long row = row_s[t];
+        return x < w.H ? p.k + row * p.ldk + (long long)x * D : p.v + row * p.ldv + (long long)(x - w.H) * D;
+    };
     if constexpr (!k8) {
-        const int nh = x1 - x0, items = T * nh;
-        for (int i0 = 0; i0 < items; i0 += G) {
-            const int i = i0 + g, t = min(i, items - 1) / nh, x = x0 + min(i, items - 1) - t * nh;
-            const bool live = i < items;
-            const Run& r = run_s[row_run[t]];
-            const int h = x < w.H ? x : x - w.H;
-            const uint16_t* src = x < w.H ? p.k + r.row * p.ldk + (long long)h * D : p.v + r.row * p.ldv + (long long)h * D;
-            // (a warp may hold keys and values at once: the values go through unchanged)
-            float y[8];
-            turned(src, live, t, p.k_norm, wk_s, y);
-            const uint4 a = x < w.H ? pack8(y) : live ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
-            if (live && r.base >= 0)
-                *reinterpret_cast<uint4*>((x < w.H ? w.k : w.v) + r.base + (long long)h * w.div.d * D + 8 * c) = a;
-        }
-    } else {
-        for (int x = x0; x < x1; ++x) {
-            const bool key = x < w.H;
-            const int h = key ? x : x - w.H, n = (x - x0) % 3;
-            uint8_t* pool = key ? p.c.k : p.c.v;
-            float* scales = key ? p.c.ks : p.c.vs;
-            float y[kPass][8], was[kPass];
+        const auto all = [&](int first, int count, bool key) {  // rows of heads first .. of the keys or values
+            if (count <= 0) return;
+            const int items = T * count;
+            const uint32_t by = 0xffffffffu / (uint32_t)count + 1u;
+            for (int i0 = 0; i0 < items; i0 += G * kAhead) {
+                Head a[kAhead];
+                int t[kAhead], h[kAhead];
 #pragma unroll
-            for (int e = 0; e < kPass; ++e) {
-                const int t = e * G + g;
-                const bool live = t < T;
-                const Run& r = run_s[row_run[live ? t : 0]];
-                const long long row = r.row + row_at_run[live ? t : 0];
-                if (key) {
-                    turned(p.k + row * p.ldk + (long long)h * D, live, live ? t : 0, p.k_norm, wk_s, y[e]);
-                } else {
-                    const uint4 a = live ? *reinterpret_cast<const uint4*>(p.v + row * p.ldv + (long long)h * D + 8 * c)
-                                         : make_uint4(0, 0, 0, 0);
-                    unpack8(a, y[e]);
-                }
-                was[e] = live && r.old > 0 && r.base >= 0 ? scales[r.scale + (long long)h * p.c.nb] : 0.f;
-                float top = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[e][i] = limited(y[e][i]);
-                    top = fmaxf(top, fabsf(y[e][i]));  // (NaN loses)
+                for (int e = 0; e < kAhead; ++e) {
+                    const int i = i0 + e * G + g;
+                    split(min(i, items - 1), count, by, t[e], h[e]);
+                    h[e] += first;
+                    a[e] = fetch((key ? p.k + row_s[t[e]] * p.ldk : p.v + row_s[t[e]] * p.ldv) + (long long)h[e] * D, i < items);
                 }
 #pragma unroll
-                for (int o = NC / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                if (live && c == 0) atomicMax(&top_s[n][row_run[t]], __float_as_uint(top));
+                for (int e = 0; e < kAhead; ++e) {
+                    if (i0 + e * G >= items) break;
+                    const bool live = i0 + e * G + g < items;
+                    const long long base = run_s[row_run[t[e]]].base;
+                    uint16_t* const to = (key ? w.k : w.v) + base + (long long)h[e] * w.div.d * D;
+                    if (key) {
+                        float y[16];
+                        turned(a[e], p.k + row_s[t[e]] * p.ldk + (long long)h[e] * D, live, t[e], p.k_norm, wk_s, y);
+                        if (live && base >= 0) put(to, pack8(y), pack8(y + 8));
+                    } else if (live && base >= 0) {
+                        put(to, a[e].a, a[e].b);
+                    }
+                }
             }
-            // Three sets of tops: this head's is read behind the barrier, the next
-            // head's was cleared before it, and the one before may still be read.
-            if (tid < kWin) top_s[(n + 1) % 3][tid] = 0u;
+        };
+        all(x0, min(x1, w.H) - x0, true);
+        all(max(x0 - w.H, 0), x1 - w.H - max(x0 - w.H, 0), false);
+    } else {
+        // a few heads at a time, all their covered rows together; the next heads'
+        // are on their way while these are rounded
+        const int wide = T <= kBlock ? kBlock : G < 2 * kBlock ? G : 2 * kBlock, heads = G / wide;
+        const int mine = g / wide, t = min(g % wide, T - 1);
+        const Run& r = run_s[row_run[t]];
+        const int in_run = row_at_run[t];
+        const bool has = g % wide < T;
+        Head a = fetch(source(min(x0 + mine, x1 - 1), t), has && x0 + mine < x1);
+        for (int xb = x0, n = 0; xb < x1; xb += heads, n = n == 2 ? 0 : n + 1) {
+            const bool live = has && xb + mine < x1;
+            const int x = min(xb + mine, x1 - 1);
+            const bool key = x < w.H;
+            const int h = key ? x : x - w.H;
+            float* const scale_at = (key ? p.c.ks : p.c.vs) + r.scale + (long long)h * p.c.nb;
+            const Head now = a;
+            a = fetch(source(min(x + heads, x1 - 1), t), has && x + heads < x1);
+            const float was = live && r.old > 0 && r.base >= 0 ? *scale_at : 0.f;
+            float y[16];
+            if (__any_sync(0xffffffffu, key)) turned(now, source(x, t), live && key, t, p.k_norm, wk_s, y);
+            if (!key) {
+                unpack8(now.a, y);
+                unpack8(now.b, y + 8);
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                y[i] = limited(y[i]);
+                top = fmaxf(top, fabsf(y[i]));  // (NaN loses)
+            }
+#pragma unroll
+            for (int o = NJ / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (live && j == 0) atomicMax(&top_s[n][mine][row_run[t]], __float_as_uint(top));
+            // Three sets of tops: this step's is read behind the barrier, the next
+            // one's was cleared before it, and the one before may still be read.
+            if (tid < kHeads * kWin) top_s[n == 2 ? 0 : n + 1][tid / kWin][tid % kWin] = 0u;
             __syncthreads();
+            if (!live || r.base < 0) continue;
+            const float scale = fmaxf(scale_for(__uint_as_float(top_s[n][mine][row_run[t]])), was);
+            const float inv = 1.f / scale;
+            uint8_t* const at = (key ? p.c.k : p.c.v) + r.base + (long long)h * w.div.d * D;
+            uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < kPass; ++e) {
-                const int t = e * G + g;
-                if (t >= T) continue;
-                const Run& r = run_s[row_run[t]];
-                if (r.base < 0) continue;
-                const int j = row_at_run[t];
-                const float scale = fmaxf(scale_for(__uint_as_float(top_s[n][row_run[t]])), was[e]);
-                const float inv = 1.f / scale;
-                uint8_t* at = pool + r.base + (long long)h * w.div.d * D + 8 * c;
+            for (int i = 0; i < 4; ++i)
+                o[i] = f32_e4m3(y[4 * i] * inv, y[4 * i + 1] * inv) | f32_e4m3(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16;
+            *reinterpret_cast<uint2*>(at + in_run * D + 8 * c0) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2*>(at + in_run * D + 8 * c1) = make_uint2(o[2], o[3]);
+            if (in_run == 0 && (r.old == 0 || scale != was)) {
+                if (j == 0) *scale_at = scale;
+                const float ratio = was * inv;
+                for (int b = 1; b <= r.old; ++b)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[e][i] *= inv;
-                *reinterpret_cast<uint2*>(at + (long long)j * D) =
-                    make_uint2(f32_e4m3(y[e][0], y[e][1]) | f32_e4m3(y[e][2], y[e][3]) << 16,
-                               f32_e4m3(y[e][4], y[e][5]) | f32_e4m3(y[e][6], y[e][7]) << 16);
-                if (j == 0 && (r.old == 0 || scale != was[e])) {
-                    if (c == 0) scales[r.scale + (long long)h * p.c.nb] = scale;
-                    const float ratio = was[e] * inv;
-                    for (int o = 1; o <= r.old; ++o) {
-                        uint2* const from = reinterpret_cast<uint2*>(at - (long long)o * D);
+                    for (int i = 0; i < 2; ++i) {
+                        uint2* const from = reinterpret_cast<uint2*>(at - b * D + 8 * (i ? c1 : c0));
                         const uint2 v = *from;
                         *from = make_uint2(rescale4(v.x, ratio), rescale4(v.y, ratio));
                     }
-                }
             }
         }
     }
 }
 
 // -------------------------------------------------------------------- read ---
-// A warp per row: 16 codes a lane.  What bounds it: bytes.
+// A warp per row, 8 codes a lane, kAsk of them on their way together.  What
+// bounds it: bytes, once the look-up of a row is covered by other rows'.
 constexpr int kReadThreads = 256;
 
 struct ReadArgs {
@@ -356,36 +443,34 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     const int id = w.table[(size_t)s * w.max_pages + pg];
     const bool there = (uint32_t)id < (uint32_t)w.n_pages;
     if (!there && lane == 0) atomicOr(w.err, q4d::kErrDeviceCheck);
-    constexpr int NC = D / 16;
+    constexpr int NC = D / 8, kAsk = 8;
     const int items = w.H * NC;
-#pragma unroll
+    const long long head0 = (long long)id * w.H;
+#pragma unroll 1
     for (int kv = 0; kv < 2; ++kv) {
         uint16_t* out = kv ? p.v : p.k;
         if (!out) continue;
         out += row * (kv ? p.ldv : p.ldk);
-        const uint8_t* pool = kv ? p.c.v : p.c.k;
-        const float* scales = kv ? p.c.vs : p.c.ks;
-#pragma unroll 4
-        for (int x = lane; x < items; x += 32) {
-            const int h = x / NC, c = x % NC;
-            uint4 a = make_uint4(0, 0, 0, 0);
-            float f = 0.f;
-            if (there) {
-                const long long hd = (long long)id * w.H + h;
-                a = *reinterpret_cast<const uint4*>(pool + (hd * w.div.d + at) * D + 16 * c);
-                f = scales[hd * p.c.nb + at / kBlock];
-            }
-            const uint32_t ws[4] = {a.x, a.y, a.z, a.w};
-            uint32_t o[8];
+        const uint8_t* pool = (kv ? p.c.v : p.c.k) + (head0 * w.div.d + at) * D;
+        const float* scales = (kv ? p.c.vs : p.c.ks) + head0 * p.c.nb + at / kBlock;
+        for (int x0 = lane; x0 < items; x0 += 32 * kAsk) {
+            uint2 a[kAsk];
+            float f[kAsk];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 u = e4m3_f32(ws[e]), v = e4m3_f32(ws[e] >> 16);
-                o[2 * e] = pack_half2(u.x * f, u.y * f);
-                o[2 * e + 1] = pack_half2(v.x * f, v.y * f);
+            for (int e = 0; e < kAsk; ++e) {
+                const int x = x0 + 32 * e, h = x / NC, c = x % NC;
+                const bool live = there && x < items;
+                a[e] = live ? __ldg(reinterpret_cast<const uint2*>(pool + (long long)h * w.div.d * D + 8 * c)) : make_uint2(0u, 0u);
+                f[e] = live ? __ldg(scales + (long long)h * p.c.nb) : 0.f;
             }
-            uint4* dst = reinterpret_cast<uint4*>(out + (long long)h * D + 16 * c);
-            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+            for (int e = 0; e < kAsk; ++e) {
+                const int x = x0 + 32 * e;
+                if (x >= items) break;
+                const uint32_t f2 = pack_half2(f[e], f[e]);  // (a power of two: exact, and so are the products)
+                *reinterpret_cast<uint4*>(out + 8ll * x) = make_uint4(mul2(e4m3_half2(a[e].x), f2), mul2(e4m3_half2_hi(a[e].x), f2),
+                                                                    mul2(e4m3_half2(a[e].y), f2), mul2(e4m3_half2_hi(a[e].y), f2));
+            }
         }
     }
 }
@@ -580,10 +665,12 @@ q4_status launch_rows(q4p::RowsArgs& a, int D, q4_rope_layout layout, const Devi
                  : (pairs == 0   ? q4p::append_rows_kernel<64, 0, k8>
                     : pairs == 1 ? q4p::append_rows_kernel<64, 1, k8>
                                  : q4p::append_rows_kernel<64, 2, k8>);
-    a.win = rows >= 2048 ? q4p::kWin : rows >= 512 ? 4 : 1;
-    const int windows = (rows - 1) / a.win + 1;
+    // As many parts of the heads as give each SM a few blocks.  us, windows of 16 /
+    // 8 / 4 rows: 6767 rows with norms 36.3 / 34.6 / 36, into 8 bits 40.3 / 39.2 / 50,
+    // 40 rows into 8 bits 6.6 / 5.6 / 5.6.
+    const int windows = (rows - 1) / q4p::kWin + 1;
     const int most = 2 * a.c.w.H < 64 ? 2 * a.c.w.H : 64;
-    int parts = (6 * dev->sms + windows - 1) / windows;
+    int parts = (8 * dev->sms + windows - 1) / windows;
     parts = parts < 1 ? 1 : parts > most ? most : parts;
     kern<<<dim3((unsigned)windows, (unsigned)parts), q4p::kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();

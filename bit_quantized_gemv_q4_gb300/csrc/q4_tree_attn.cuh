@@ -405,10 +405,6 @@ __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
     const uint32_t n = live ? 4u : 0u;
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
 
 __device__ __forceinline__ bool ring_wait(RingBars& B, uint64_t& bar, uint32_t parity, int* err) {
     if (B.abort) return false;
@@ -857,8 +853,8 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t x = __byte_perm(b[2 * e], 0u, 0x3120), y = __byte_perm(b[2 * e + 1], 0u, 0x3120);
                         const int dn = 2 * (ch + e);
-                        mma(o[dn], pa[kj], mul2(q4p::e4m3_half2(x), s0), mul2(q4p::e4m3_half2(y), s1));
-                        mma(o[dn + 1], pa[kj], mul2(q4p::e4m3_half2_hi(x), s0), mul2(q4p::e4m3_half2_hi(y), s1));
+                        mma(o[dn], pa[kj], q4p::mul2(q4p::e4m3_half2(x), s0), q4p::mul2(q4p::e4m3_half2(y), s1));
+                        mma(o[dn + 1], pa[kj], q4p::mul2(q4p::e4m3_half2_hi(x), s0), q4p::mul2(q4p::e4m3_half2_hi(y), s1));
                     }
                 }
             } else {
@@ -1832,8 +1828,8 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                     for (int e = 0; e < NL; ++e) {
                         const uint32_t f = __shfl_sync(0xffffffffu, f2, e * PER + g);
                         *reinterpret_cast<uint4*>(to + sw_off(e * PER + g, c & 7)) =
-                            make_uint4(mul2(q4p::e4m3_half2(r[e].x), f), mul2(q4p::e4m3_half2_hi(r[e].x), f),
-                                       mul2(q4p::e4m3_half2(r[e].y), f), mul2(q4p::e4m3_half2_hi(r[e].y), f));
+                            make_uint4(q4p::mul2(q4p::e4m3_half2(r[e].x), f), q4p::mul2(q4p::e4m3_half2_hi(r[e].x), f),
+                                       q4p::mul2(q4p::e4m3_half2(r[e].y), f), q4p::mul2(q4p::e4m3_half2_hi(r[e].y), f));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
