@@ -413,8 +413,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) append_rows_kernel(const __gri
 }
 
 // -------------------------------------------------------------------- read ---
-// A warp per row, 8 codes a lane, kAsk of them on their way together.  What
-// bounds it: bytes, once the look-up of a row is covered by other rows'.
+// A warp per row, 16 codes a lane.  What bounds it: bytes.  Measured: 31982 rows
+// of 8 heads of 128 (197 MB in and out) 38.5 us = 5.1 TB/s, 75 % of the measured
+// copy rate.  8 codes a lane (whole sectors at a store) 41 us, 4 rows a warp
+// that share their look-ups 42.
 constexpr int kReadThreads = 256;
 
 struct ReadArgs {
@@ -443,34 +445,36 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     const int id = w.table[(size_t)s * w.max_pages + pg];
     const bool there = (uint32_t)id < (uint32_t)w.n_pages;
     if (!there && lane == 0) atomicOr(w.err, q4d::kErrDeviceCheck);
-    constexpr int NC = D / 8, kAsk = 8;
+    constexpr int NC = D / 16;
     const int items = w.H * NC;
-    const long long head0 = (long long)id * w.H;
-#pragma unroll 1
+#pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
         uint16_t* out = kv ? p.v : p.k;
         if (!out) continue;
         out += row * (kv ? p.ldv : p.ldk);
-        const uint8_t* pool = (kv ? p.c.v : p.c.k) + (head0 * w.div.d + at) * D;
-        const float* scales = (kv ? p.c.vs : p.c.ks) + head0 * p.c.nb + at / kBlock;
-        for (int x0 = lane; x0 < items; x0 += 32 * kAsk) {
-            uint2 a[kAsk];
-            float f[kAsk];
-#pragma unroll
-            for (int e = 0; e < kAsk; ++e) {
-                const int x = x0 + 32 * e, h = x / NC, c = x % NC;
-                const bool live = there && x < items;
-                a[e] = live ? __ldg(reinterpret_cast<const uint2*>(pool + (long long)h * w.div.d * D + 8 * c)) : make_uint2(0u, 0u);
-                f[e] = live ? __ldg(scales + (long long)h * p.c.nb) : 0.f;
+        const uint8_t* pool = kv ? p.c.v : p.c.k;
+        const float* scales = kv ? p.c.vs : p.c.ks;
+#pragma unroll 4
+        for (int x = lane; x < items; x += 32) {
+            const int h = x / NC, c = x % NC;
+            uint4 a = make_uint4(0, 0, 0, 0);
+            float f = 0.f;
+            if (there) {
+                const long long hd = (long long)id * w.H + h;
+                a = *reinterpret_cast<const uint4*>(pool + (hd * w.div.d + at) * D + 16 * c);
+                f = scales[hd * p.c.nb + at / kBlock];
             }
+            const uint32_t ws[4] = {a.x, a.y, a.z, a.w};
+            const uint32_t f2 = pack_half2(f, f);  // (a power of two: exact, and so are the products)
+            uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < kAsk; ++e) {
-                const int x = x0 + 32 * e;
-                if (x >= items) break;
-                const uint32_t f2 = pack_half2(f[e], f[e]);  // (a power of two: exact, and so are the products)
-                *reinterpret_cast<uint4*>(out + 8ll * x) = make_uint4(mul2(e4m3_half2(a[e].x), f2), mul2(e4m3_half2_hi(a[e].x), f2),
-                                                                    mul2(e4m3_half2(a[e].y), f2), mul2(e4m3_half2_hi(a[e].y), f2));
+            for (int e = 0; e < 4; ++e) {
+                o[2 * e] = mul2(e4m3_half2(ws[e]), f2);
+                o[2 * e + 1] = mul2(e4m3_half2_hi(ws[e]), f2);
             }
+            uint4* dst = reinterpret_cast<uint4*>(out + (long long)h * D + 16 * c);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
     }
 }
