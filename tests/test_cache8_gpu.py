@@ -315,6 +315,58 @@ def test_append8_around_bad_sequences_and_pages():
     assert same[:6].all() and same[10:].all() and bool((qo[6:10] == 9.0).all())
 
 
+def test_append8_many_sequences():
+    # more sequences than one level of the row search, most of them empty
+    g = np.random.default_rng(6)
+    n = [int(x) for x in g.integers(0, 3, 1500)]
+    n[0] = n[-1] = 0
+    b = Batch8(g, [int(x) for x in g.integers(0, 20, 1500)], n, 1, 64, 8)
+    c = b.to_device(q4)
+    before = b.from_device()
+    k, v = rand16(g, b.rows, 64), rand16(g, b.rows, 64)
+    q4.q4_paged_append8(c, b.dctx, b.dstart, b.rows, torch_dev(k), torch_dev(v))
+    assert q4.q4_device_status() == 0
+    y = k.reshape(-1, 1, 64).astype(np.float64)
+    check_append8(b, before, b.from_device(), y, np.zeros_like(y), v.reshape(-1, 1, 64).astype(np.float64))
+    out = torch.empty(b.rows, 64, dtype=torch.float16, device="cuda")
+    q4.q4_paged_read8(c, b.dctx, b.dstart, b.rows, v=out)
+    pool = b.values(b.from_device()[1], b.from_device()[3])[0]
+    want = np.concatenate([b.rows_of(pool, s, b.ctx[s] + np.arange(m)) for s, m in enumerate(b.n)]).reshape(b.rows, 64)
+    assert np.array_equal(out.cpu().numpy().astype(np.float64), want)
+
+
+@pytest.mark.parametrize("rows", [3, 40, 900])
+def test_append8_replays_with_other_sizes(rows):
+    # one captured call; the sizes change on the device, down to nobody having a row
+    g = np.random.default_rng(rows)
+    b = Batch8(g, [40, 40], [rows, rows], 2, 64, 16)  # (pages for every size below)
+    c = b.to_device(q4)
+    k, v = rand16(g, rows, 128), rand16(g, rows, 128)
+    dk, dv = torch_dev(k), torch_dev(v)
+    run = lambda: q4.q4_paged_append8(c, b.dctx, b.dstart, rows, dk, dv)  # noqa: E731
+    b.dstart.copy_(torch_dev(np.array([0, rows, rows], np.int32)))
+    side = torch.cuda.Stream()
+    keep = [x.clone() for x in b.d8]
+    with torch.cuda.stream(side):
+        run()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for ctx, n in (([30, 5], [rows, 0]), ([0, 17], [rows // 3, rows - rows // 3]), ([7, 9], [0, 0]), ([16, 15], [1, rows - 1])):
+        b.ctx, b.n = ctx, n
+        b.start = np.array([0, n[0], sum(n)], np.int32)
+        b.dctx.copy_(torch_dev(np.array(ctx, np.int32)))
+        b.dstart.copy_(torch_dev(b.start))
+        for x, y in zip(b.d8, keep):
+            x.copy_(y)
+        before = b.from_device()
+        graph.replay()
+        assert q4.q4_device_status() == 0
+        y = k.reshape(-1, 2, 64).astype(np.float64)
+        check_append8(b, before, b.from_device(), y, np.zeros_like(y), v.reshape(-1, 2, 64).astype(np.float64))
+
+
 # ------------------------------------------------------------------ read back ---
 
 @pytest.mark.parametrize("d,Hkv,page", [(128, 8, 64), (128, 3, 24), (64, 1, 7), (64, 5, 1), (128, 1, 100)])
