@@ -646,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
     // (8 bits, 16 rows: in shared memory, so that three CTAs' registers fit an SM)
     constexpr bool kQShared = k8 && WM == 1, kTwoChains = k8 && NT == 2;
     uint32_t qf[kQShared ? 1 : KS][4];
+    int tok[2] = {0, 0};             // tokens of this thread's rows
     float o[DN][4], m[2], l[2];
     bool fresh = true;              // the job's first tile in this CTA
     bool begun = p.tile == 0;       // ... and in the line
@@ -657,9 +658,10 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
     while (consume) {
         const int st = kt % kStages;
         const int R = min(BM, p.q.n * a.G - p.rb * BM);
-        int tok[2];
+        if (!kQShared || fresh) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) tok[e] = (int)q4p::page_of(a.by_g, p.rb * BM + min(row0 + 8 * e, R - 1));
+            for (int e = 0; e < 2; ++e) tok[e] = (int)q4p::page_of(a.by_g, p.rb * BM + min(row0 + 8 * e, R - 1));
+        }
         if (fresh) {
             if constexpr (kQShared) {
                 // Four rows a warp.  A chunk of 16 elements is laid down in the order
@@ -751,21 +753,25 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
             float sd[kTwoChains ? NT : 1][4] = {};  // (two chains of products where there are few tiles)
             static_assert(!kTwoChains || kQShared, "");
             const uint32_t qs = q4d::smem_addr(query_s);
+            if constexpr (kQShared) {
 #pragma unroll
-            for (int kk = 0; kk < KS; kk += 4) {
-                if constexpr (kQShared) {
-                    uint32_t b[NT][4];
+                for (int kk = 0; kk < KS; kk += 2) {
+                    uint32_t qa[2][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) ldsm4(kb + off(wn * KW + nt * 8 + (lane & 7), kk + (lane >> 3)), b[nt]);
+                    for (int e = 0; e < 2; ++e) ldsm4(qs + swz<D>(lane & 15, 2 * (kk + e) + (lane >> 4)), qa[e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t qa[4];
-                        ldsm4(qs + swz<D>(lane & 15, 2 * (kk + e) + (lane >> 4)), qa);
+                    for (int nt = 0; nt < NT; nt += 2) {
+                        uint32_t b[4];  // two chunks of two position tiles
+                        ldsm4(kb + off(wn * KW + (nt + (lane >> 4)) * 8 + (lane & 7), kk + (lane >> 3 & 1)), b);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma(kTwoChains && (e & 1) ? sd[kTwoChains ? nt : 0] : sc[nt], qa, q4p::e4m3_half2(b[nt][e]), q4p::e4m3_half2_hi(b[nt][e]));
+                        for (int e = 0; e < 4; ++e)
+                            mma(kTwoChains && (e & 1) ? sd[kTwoChains ? nt + (e >> 1) : 0] : sc[nt + (e >> 1)], qa[e & 1],
+                                q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
                     }
-                } else {
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < KS; kk += 4)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         uint32_t b[4];
@@ -773,7 +779,6 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) mma(sc[nt], qf[kk + e], q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
                     }
-                }
             }
             if constexpr (kTwoChains)
 #pragma unroll
@@ -1500,13 +1505,13 @@ struct TcShape {
     static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * (size_t)kTile + 512 + 8 * 2048;  // tiles, barriers, staging
 };
 
-// 8 bits: a slot for 32 positions' codes per converting warp, and staging half as
-// wide to make room for them.
-constexpr int kTcSlots = kTc8Threads / 32 - 11;
+// 8 bits: a slot for 32 positions' codes per converting warp, instead of the
+// outputs' staging.
+constexpr int kTcSlots = kTc8Threads / 32 - 10;
 template <int D>
 struct Tc8Shape : TcShape<D> {
     static constexpr uint32_t kSlot = 32 * D;
-    static constexpr size_t kSmem = 1024 + (2 + 2 * TcShape<D>::kStages) * (size_t)TcShape<D>::kTile + 512 + 8 * 1024 + kTcSlots * kSlot;
+    static constexpr size_t kSmem = 1024 + (2 + 2 * TcShape<D>::kStages) * (size_t)TcShape<D>::kTile + 512 + kTcSlots * kSlot;
 };
 
 struct TcBars {
@@ -1544,18 +1549,6 @@ __device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
-}
-// Likewise 8 or 16.
-template <int N>
-__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t* r) {
-    if constexpr (N == 16) {
-        q4t::ld16(taddr, r);
-    } else {
-        static_assert(N == 8, "");
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                     : "r"(taddr));
-    }
 }
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -1619,7 +1612,7 @@ __device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
 }
 
 //
-// k8: warps 9 and 12 .. 15 bring the codes and make them fp16, 32 positions of a
+// k8: warps 8, 9 and 12 .. 15 bring the codes and make them fp16, 32 positions of a
 // tile at a time, in turn, first the keys', then the values'.  Each has a slot of
 // its own in shared memory: it waits for a copy, takes it into registers, sets
 // the next copy going (bulk copies of the rows that lie together in a page) and,
@@ -1704,13 +1697,13 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
         uint32_t seg = 0;   // segments done
         uint32_t tiles0 = 0;  // tiles before this segment
 
-        if (k8 && (warp == 9 || warp >= 12)) {
+        if (k8 && (warp == 8 || warp == 9 || warp >= 12)) {
             // --------------------------------------------- codes to fp16
             if constexpr (k8) {
                 constexpr int NC = D / 8, PER = 32 / NC, NL = 32 / PER;  // lanes of a row (8 codes each), rows at a time, loads
                 constexpr uint32_t kConv = kTcSlots;
-                const int c = lane % NC, g = lane / NC, own = warp == 9 ? 0 : warp - 11;
-                uint8_t* const slot = reinterpret_cast<uint8_t*>(&B) + 512 + 8 * 1024 + own * Sh::kSlot;
+                const int c = lane % NC, g = lane / NC, own = warp < 10 ? warp - 8 : warp - 10;
+                uint8_t* const slot = reinterpret_cast<uint8_t*>(&B) + 512 + own * Sh::kSlot;
                 const uint32_t slot_s = q4d::smem_addr(slot) + lane * D, fb = q4d::smem_addr(&B.raw_full[own]);
                 // Quarters of the line's tiles, 4 each; lane = position.  A quarter
                 // is looked up when the one before it is asked into L2 (a slot is
@@ -1841,8 +1834,6 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                 }
                 if (flying) q4d::mbar_wait(fb, turns & 1, nullptr);  // a copy in flight lands before the CTA can exit
             }
-        } else if (k8 && warp == 8) {
-            // (nothing to do)
         } else if (!k8 && (warp == 8 || warp == 9)) {
             // --------------------------------------------- key / value tiles
             const bool keys = warp == 8;
@@ -2197,45 +2188,52 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                     if (!whole && r >= 0 && (!join || i == 0)) part_ml(a, slot)[r] = make_float2(m, l);
                     const int c1 = join ? D / 2 * (i + 1) : D;
                     const uint32_t t0 = join ? lt + kColO : to;
-                    // kCols columns at a time by way of shared memory, so that a
-                    // warp stores whole sectors: kCols / 4 lanes per row
-                    constexpr int kCols = k8 ? 8 : 16, kPer = kCols / 4, kMask = kPer - 1;
-                    float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&B) + 512) + warp * 32 * kCols;
+                    // 16 columns at a time by way of shared memory, so that a
+                    // warp stores whole sectors: 4 lanes per row.  (8 bits: whose
+                    // room the codes' slots take, so every lane stores its row's.)
+                    float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&B) + 512) + warp * 512;
+                    const auto write = [&](int ry, int col, const float4& v) {
+                        if (ry >= R) return;
+                        if (whole) {
+                            const int rr = done.rb * a.BM + ry, tk = (int)q4p::page_of(a.by_g, rr);
+                            *reinterpret_cast<uint2*>(a.out + (size_t)(done.q.start + tk) * a.ldo +
+                                                      (size_t)(done.h * a.G + rr - tk * a.G) * D + col) =
+                                make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+                        } else {
+                            *reinterpret_cast<float4*>(part_o<D>(a, slot) + (size_t)ry * D + col) = v;
+                        }
+                    };
 #pragma unroll 1
-                    for (int c0 = join ? D / 2 * i : 0; c0 < c1; c0 += kCols) {
-                        uint32_t w[kCols];
-                        float o[kCols];
-                        ld_cols<kCols>(t0 + c0, w);
+                    for (int c0 = join ? D / 2 * i : 0; c0 < c1; c0 += 16) {
+                        uint32_t w[16];
+                        float o[16];
+                        q4t::ld16(t0 + c0, w);
                         q4t::ld_wait();
 #pragma unroll
-                        for (int e = 0; e < kCols; ++e) o[e] = __uint_as_float(w[e]) * (f0 * inv);
+                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(w[e]) * (f0 * inv);
                         if (join) {
-                            ld_cols<kCols>(t0 + 128 + c0, w);
+                            q4t::ld16(t0 + 128 + c0, w);
                             q4t::ld_wait();
 #pragma unroll
-                            for (int e = 0; e < kCols; ++e) o[e] = fmaf(__uint_as_float(w[e]), f1 * inv, o[e]);
+                            for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(w[e]), f1 * inv, o[e]);
                         }
+                        if constexpr (k8) {
 #pragma unroll
-                        for (int e = 0; e < kPer; ++e)
-                            *reinterpret_cast<float4*>(stage + lane * kCols + ((e ^ (lane * kPer / 8 & kMask)) * 4)) =
-                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                        __syncwarp();
+                            for (int e = 0; e < 4; ++e)
+                                write(rw + lane, c0 + 4 * e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < kPer; ++e) {
-                            const int y = (e * 32 + lane) / kPer, c = lane & kMask;
-                            const float4 v = *reinterpret_cast<const float4*>(stage + y * kCols + ((c ^ (y * kPer / 8 & kMask)) * 4));
-                            const int ry = rw + y;
-                            if (ry >= R) continue;
-                            if (whole) {
-                                const int rr = done.rb * a.BM + ry, tk = (int)q4p::page_of(a.by_g, rr);
-                                *reinterpret_cast<uint2*>(a.out + (size_t)(done.q.start + tk) * a.ldo +
-                                                          (size_t)(done.h * a.G + rr - tk * a.G) * D + c0 + 4 * c) =
-                                    make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
-                            } else {
-                                *reinterpret_cast<float4*>(part_o<D>(a, slot) + (size_t)ry * D + c0 + 4 * c) = v;
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<float4*>(stage + lane * 16 + ((e ^ (lane >> 1 & 3)) * 4)) =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                            __syncwarp();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int y = e * 8 + (lane >> 2), c = lane & 3;
+                                write(rw + y, c0 + 4 * c, *reinterpret_cast<const float4*>(stage + y * 16 + ((c ^ (y >> 1 & 3)) * 4)));
                             }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                     if (B.odd[seg_done & (kOdd - 1)] == (int)seg_done + 1 && r >= 0) {
                         const int rr = done.rb * a.BM + r;
