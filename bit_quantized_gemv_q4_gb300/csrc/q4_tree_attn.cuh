@@ -365,11 +365,12 @@ constexpr int kConsumers = 128, kThreads = 160;
 // 40 up to 12000 94 / 94 / 94.
 constexpr int kRingCost = 4, kRingLead = 16;
 
-// Positions of a tile.  8 bits, the line of 16-row jobs: 128, as its fixed cost
-// (waits, statistics) weighs twice as much against half the bytes.
-template <int WM, bool kClustered, bool k8>
+// Positions of a tile.  8 bits, the line: 128, as a tile's fixed cost (waits,
+// statistics) weighs twice as much against half the bytes (48 users' tokens up
+// to 14000 positions: 188 us, with 64 200).
+template <bool kClustered, bool k8>
 constexpr int ring_keys() {
-    return k8 && WM == 1 && !kClustered ? 128 : kKeys;
+    return k8 && !kClustered ? 128 : kKeys;
 }
 
 template <int D, bool k8, int KEYS>
@@ -476,18 +477,24 @@ __device__ __forceinline__ void latch_bad(const Args& a) {
 // k8: the tiles hold e4m3 codes, a 16-byte chunk 16 elements, and the scales of
 // their positions come beside them by 4-byte cp.async.  Codes become fp16 in
 // registers: a thread's word of a key chunk holds elements 4u .. 4u+3, which
-// take the places 2u, 2u+1, 2u+8, 2u+9 of the contraction (the query's words
-// are loaded in the same order), and the scores take the keys' scales in fp32.
-// A transposed word of a value chunk holds elements 2g, 2g+1 of two positions;
-// apart they are the B operands of an even and an odd column tile, which take
-// the values' scales (powers of two: exact) before the product.
+// take the places 2u, 2u+1, 2u+8, 2u+9 of the contraction (the query lies in
+// shared memory in the same order), and the scores take the keys' scales in
+// fp32.  A transposed word of a value chunk holds elements 2g, 2g+1 of two
+// positions; apart they are the B operands of an even and an odd column tile,
+// which take the values' scales (powers of two: exact) before the product.
+// Half the bytes for the same products and more instructions: what bounds it
+// is issue and waits as much as the bytes, so three CTAs share an SM.  48
+// users' tokens over contexts up to 14000 (32 query heads on 8 of 128, 911 MB)
+// 175 us = 5.2 TB/s, 77 % of the measured copy rate, with pages of 64 165 us
+// (of 16: more and smaller copies); two CTAs with three stages 232 us (before
+// the last 13).  The pages looked up a tile ahead brought nothing.
 template <int D, int WM, bool kTma, bool kClustered, bool k8>
-__global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, k8 ? 3 : 2)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ MapArgs t) {
     constexpr int BM = 16 * WM, WN = 4 / WM;
     constexpr int NCH = k8 ? D / 16 : D / 8, KS = D / 16, DN = D / 8, SLABS = k8 ? 1 : D / 64;  // chunks of a row ...
-    constexpr int KEYS = ring_keys<WM, kClustered, k8>();
+    constexpr int KEYS = ring_keys<kClustered, k8>();
     constexpr int KW = KEYS / WN, NT = KW / 8;  // a warp's positions of a tile, 8-wide tiles of them
     constexpr uint32_t TB = Ring<D, k8, KEYS>::kTile;
     constexpr int kStages = Ring<D, k8, KEYS>::kStages;
@@ -643,9 +650,9 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
     // but every warp still comes to the barriers the others wait at.
     const int g = lane >> 2, u = lane & 3;
     const int wm = warp / WN, wn = warp % WN;
-    // (8 bits, 16 rows: in shared memory, so that three CTAs' registers fit an SM)
-    constexpr bool kQShared = k8 && WM == 1, kTwoChains = k8 && NT == 2;
-    uint32_t qf[kQShared ? 1 : KS][4];
+    static_assert(!k8 || WM == 1, "jobs of 16 rows");
+    constexpr bool kTwoChains = k8 && NT == 2;
+    uint32_t qf[k8 ? 1 : KS][4];  // (8 bits: in shared memory, so that three CTAs' registers fit an SM)
     int tok[2] = {0, 0};             // tokens of this thread's rows
     float o[DN][4], m[2], l[2];
     bool fresh = true;              // the job's first tile in this CTA
@@ -658,12 +665,12 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
     while (consume) {
         const int st = kt % kStages;
         const int R = min(BM, p.q.n * a.G - p.rb * BM);
-        if (!kQShared || fresh) {
+        if (!k8 || fresh) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) tok[e] = (int)q4p::page_of(a.by_g, p.rb * BM + min(row0 + 8 * e, R - 1));
         }
         if (fresh) {
-            if constexpr (kQShared) {
+            if constexpr (k8) {
                 // Four rows a warp.  A chunk of 16 elements is laid down in the order
                 // in which the codes' words take them, elements 4u, 4u+1 before all
                 // 4u+2, 4u+3, so that ldmatrix finds the fragments.
@@ -683,20 +690,13 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const bool live = !kQShared && row0 + 8 * e < R;
+                const bool live = !k8 && row0 + 8 * e < R;
                 const int rr = p.rb * BM + min(row0 + 8 * e, R - 1);
-                const uint16_t* src = a.q + (size_t)(p.q.start + tok[e]) * a.ldq + (size_t)(p.h * a.G + rr - tok[e] * a.G) * D +
-                                      (k8 ? 4 : 2) * u;
+                const uint16_t* src = a.q + (size_t)(p.q.start + tok[e]) * a.ldq + (size_t)(p.h * a.G + rr - tok[e] * a.G) * D + 2 * u;
 #pragma unroll
-                for (int kk = 0; kk < (kQShared ? 0 : KS); ++kk) {
-                    if constexpr (k8) {
-                        const uint2 x = live ? *reinterpret_cast<const uint2*>(src + 16 * kk) : make_uint2(0u, 0u);
-                        qf[kk][e] = x.x;
-                        qf[kk][2 + e] = x.y;
-                    } else {
-                        qf[kk][e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
-                        qf[kk][2 + e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8) : 0u;
-                    }
+                for (int kk = 0; kk < (k8 ? 0 : KS); ++kk) {
+                    qf[kk][e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk) : 0u;
+                    qf[kk][2 + e] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * kk + 8) : 0u;
                 }
                 m[e] = -INFINITY;
                 l[e] = 0.f;
@@ -751,34 +751,21 @@ __global__ void __launch_bounds__(kThreads, k8 && WM == 1 ? 3 : 2)
         for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
         if constexpr (k8) {
             float sd[kTwoChains ? NT : 1][4] = {};  // (two chains of products where there are few tiles)
-            static_assert(!kTwoChains || kQShared, "");
             const uint32_t qs = q4d::smem_addr(query_s);
-            if constexpr (kQShared) {
 #pragma unroll
-                for (int kk = 0; kk < KS; kk += 2) {
-                    uint32_t qa[2][4];
+            for (int kk = 0; kk < KS; kk += 2) {
+                uint32_t qa[2][4];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) ldsm4(qs + swz<D>(lane & 15, 2 * (kk + e) + (lane >> 4)), qa[e]);
+                for (int e = 0; e < 2; ++e) ldsm4(qs + swz<D>(lane & 15, 2 * (kk + e) + (lane >> 4)), qa[e]);
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt += 2) {
-                        uint32_t b[4];  // two chunks of two position tiles
-                        ldsm4(kb + off(wn * KW + (nt + (lane >> 4)) * 8 + (lane & 7), kk + (lane >> 3 & 1)), b);
+                for (int nt = 0; nt < NT; nt += 2) {
+                    uint32_t b[4];  // two chunks of two position tiles
+                    ldsm4(kb + off(wn * KW + (nt + (lane >> 4)) * 8 + (lane & 7), kk + (lane >> 3 & 1)), b);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mma(kTwoChains && (e & 1) ? sd[kTwoChains ? nt + (e >> 1) : 0] : sc[nt + (e >> 1)], qa[e & 1],
-                                q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        mma(kTwoChains && (e & 1) ? sd[kTwoChains ? nt + (e >> 1) : 0] : sc[nt + (e >> 1)], qa[e & 1],
+                            q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
                 }
-            } else {
-#pragma unroll
-                for (int kk = 0; kk < KS; kk += 4)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t b[4];
-                        ldsm4(kb + off(wn * KW + nt * 8 + (lane & 7), kk + (lane >> 3)), b);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) mma(sc[nt], qf[kk + e], q4p::e4m3_half2(b[e]), q4p::e4m3_half2_hi(b[e]));
-                    }
             }
             if constexpr (kTwoChains)
 #pragma unroll
@@ -1349,7 +1336,7 @@ template <int D, int WM, bool kTma, bool kClustered, bool k8>
 cudaError_t launch_kernel(const CUtensorMap& k, const CUtensorMap& v, const MapArgs& t, int grid, cudaStream_t s) {
     static std::atomic<int> marks[64];
     const auto kern = tree_attn_kernel<D, WM, kTma, kClustered, k8>;
-    using R = Ring<D, k8, ring_keys<WM, kClustered, k8>()>;
+    using R = Ring<D, k8, ring_keys<kClustered, k8>()>;
     const void* fn = reinterpret_cast<const void*>(kern);
     cudaError_t e = q4i::ensure_smem_attr(fn, marks, (int)R::kSmem);
     if (e != cudaSuccess) return e;
@@ -1399,7 +1386,7 @@ q4_status launch(Args& a, const Pools& c, void* workspace, int sms, int box, cud
     a.BM = 16 * WM;
     a.cost_full = a.cost_half = kRingCost;
     a.lead = kRingLead;
-    const int resident = k8 && WM == 1 ? 3 * sms : 2 * sms;
+    const int resident = k8 ? 3 * sms : 2 * sms;
     a.ctas = resident < kMaxCtas ? resident : kMaxCtas;
     place_parts<D>(a, workspace);
     if (box) {
@@ -1413,7 +1400,7 @@ q4_status launch(Args& a, const Pools& c, void* workspace, int sms, int box, cud
     const long long jobs = (seqs + ((long long)a.w.rows * a.G - seqs) / a.BM) * c.n_kv_heads;
     t.cluster = cluster_size(jobs, c.n_seqs, (long long)c.max_pages * c.page_size, sms);
     t.cluster_log2 = t.cluster == 16 ? 4 : t.cluster == 8 ? 3 : 2;
-    a.KT = t.cluster ? ring_keys<WM, true, k8>() : ring_keys<WM, false, k8>();
+    a.KT = t.cluster ? ring_keys<true, k8>() : ring_keys<false, k8>();
     a.KT_log2 = a.KT == 128 ? 7 : 6;
     t.a = a;
     const auto run = [&](auto tma) {

@@ -35,12 +35,22 @@ extern "C" q4_status q4_tree_attention8(const q4_tree_attention8_desc* desc, q4_
     const long long pool_rows = (long long)d.cache.n_pages * d.cache.n_kv_heads * d.cache.page_size;
     const bool tma = even >= 8 && pool_rows < (1ll << 31) - 1;
     const int box = !tma ? 0 : even < q4x::kKeys ? even : q4x::kKeys;
-    if (avg > 32)
-        return D == 128 ? q4x::launch_tc<128, true>(a, pools, d.workspace, dev->sms, even < 32 ? even : 32, s, what)
-                        : q4x::launch_tc<64, true>(a, pools, d.workspace, dev->sms, even < 32 ? even : 32, s, what);
-    if (D == 128)
-        return avg <= 16 ? q4x::launch<128, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
-                         : q4x::launch<128, 2, true>(a, pools, d.workspace, dev->sms, box, s, what);
-    return avg <= 16 ? q4x::launch<64, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
-                     : q4x::launch<64, 2, true>(a, pools, d.workspace, dev->sms, box, s, what);
+    // Rows per kv head of the average sequence choose the kernel.  us of 32
+    // sequences up to 4000 (500) positions, 8 kv heads of 128, by mean rows:
+    //          jobs of 16   tcgen05
+    //   10     51           111
+    //   18     63           103
+    //   26     64           95
+    //   32     86 (34)      115 (35)
+    //   40     92           104
+    //   67     126 (50)     100 (39)
+    //   97     205          117
+    // (jobs of 32 rows, two CTAs per SM: 74, 70, 74, 111 (32), 102, 135 (42), 213)
+    if (avg > 48) {
+        const int rows = even < 32 ? even : 32;
+        return D == 128 ? q4x::launch_tc<128, true>(a, pools, d.workspace, dev->sms, rows, s, what)
+                        : q4x::launch_tc<64, true>(a, pools, d.workspace, dev->sms, rows, s, what);
+    }
+    return D == 128 ? q4x::launch<128, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
+                    : q4x::launch<64, 1, true>(a, pools, d.workspace, dev->sms, box, s, what);
 }
