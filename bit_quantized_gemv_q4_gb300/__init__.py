@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "Q4Error", "lib", "q4_selftest_expired_wait", "q4_gemv", "q4_gemv8", "q4_gemv_ex", "Segment", "q4_device_status",
@@ -265,6 +266,22 @@ def lib() -> ctypes.CDLL:
         L.q4_tree_accept8.argtypes = [ctypes.POINTER(q4_tree_accept8_desc), vp]
         _lib = L
     return _lib
+
+
+_bytes_lib = None
+
+
+def _by_bytes(name: str):
+    """A call whose descriptors are passed as bytes (a handle of its own, so that lib()'s take the structures)."""
+    global _bytes_lib
+    if _bytes_lib is None:
+        lib()
+        L = ctypes.CDLL(LIB_PATH)
+        for f, n in (("q4_paged_append_norm", 3), ("q4_paged_append8", 3), ("q4_paged_read8", 2), ("q4_tree_attention8", 2),
+                     ("q4_tree_accept8", 2)):
+            getattr(L, f).argtypes, getattr(L, f).restype = [vp] * n, i32
+        _bytes_lib = L
+    return getattr(_bytes_lib, name)
 
 
 def _check(status: int, where: str):
@@ -567,7 +584,9 @@ def _device(torch) -> int:
 
 def _arg(t, dtype, need: int, dev: int, name: str):
     """Device pointer of a packed argument of at least `need` elements; ints and None pass as in _ptr."""
-    if t is None or t.__class__ is int:
+    if t is None:
+        return 0
+    if t.__class__ is int:
         return t
     if t.dtype is dtype and t.get_device() == dev and t.numel() >= need and t.is_contiguous():
         return t.data_ptr()
@@ -595,7 +614,9 @@ def _rows_other(t, dtype, rows: int, width: int, ld: int, dev: int, name: str):
 
 def _rows(t, dtype, rows: int, width: int, ld: int, dev: int, name: str):
     """(device pointer, row stride) of a matrix argument; a 2-D tensor's own stride unless one is given."""
-    if t is None or t.__class__ is int:
+    if t is None:
+        return 0, ld
+    if t.__class__ is int:
         return t, ld
     if (not ld and t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.size(-1) == width
             and t.numel() >= rows * width):
@@ -616,11 +637,13 @@ class PagedCache:
         self.sizes = (n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages)
         self.pool = n_pages * page_size * n_kv_heads * head_dim  # elements of one layer's keys
 
-    def _desc(self, torch, dev: int, elements: int) -> q4_paged_cache:
+    def _fields(self, torch, dev: int, elements: int) -> tuple:
         s = self.sizes
-        return q4_paged_cache(_arg(self.k, torch.float16, elements, dev, "cache.k"),
-                              _arg(self.v, torch.float16, elements, dev, "cache.v"),
-                              _arg(self.page_table, torch.int32, s[4] * s[5], dev, "cache.page_table"), *s)
+        return (_arg(self.k, torch.float16, elements, dev, "cache.k"), _arg(self.v, torch.float16, elements, dev, "cache.v"),
+                _arg(self.page_table, torch.int32, s[4] * s[5], dev, "cache.page_table"), *s)
+
+    def _desc(self, torch, dev: int, elements: int) -> q4_paged_cache:
+        return q4_paged_cache(*self._fields(torch, dev, elements))
 
 
 def q4_rope_frequencies(freqs, rot_dim: int, theta: float = 1.0e6, factor: float = 1.0, orig_len: int = 0,
@@ -633,19 +656,29 @@ def q4_rope_frequencies(freqs, rot_dim: int, theta: float = 1.0e6, factor: float
     _check(lib().q4_rope_frequencies(ctypes.byref(d), p, _stream_of(torch, dev, stream)), "q4_rope_frequencies")
 
 
-def _append_desc(kind, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs, rot_dim, layout,
-                 amplitude, ldq, ldk, ldv, ldqo, torch, dev):
+def _append_fields(cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs, rot_dim, layout, amplitude,
+                   ldq, ldk, ldv, ldqo, torch, dev):
+    """The descriptor's fields behind the cache."""
     f16, i32_ = torch.float16, torch.int32
     _, _, heads, hd, n_seqs, _ = cache.sizes
     pk, ldk = _rows(k, f16, rows, heads * hd, ldk, dev, "k")
     pv, ldv = _rows(v, f16, rows, heads * hd, ldv, dev, "v")
     pq, ldq = _rows(q, f16, rows, n_q_heads * hd, ldq, dev, "q")
     po, ldqo = _rows(q_out, f16, rows, n_q_heads * hd, ldqo, dev, "q_out")
-    return kind(
-        cache._desc(torch, dev, cache.pool), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
-        _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(positions, i32_, rows, dev, "positions"), pk, pv,
-        ldk, ldv, pq, po, ldq, ldqo, n_q_heads, _arg(freqs, torch.int64, rot_dim // 2, dev, "freqs"), rot_dim, layout,
-        amplitude)
+    return (_arg(ctx_len, i32_, n_seqs, dev, "ctx_len"), _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows,
+            _arg(positions, i32_, rows, dev, "positions"), pk, pv, ldk, ldv, pq, po, ldq, ldqo, n_q_heads,
+            _arg(freqs, torch.int64, rot_dim // 2, dev, "freqs"), rot_dim, layout, amplitude)
+
+
+# The later calls' descriptors are packed as bytes, the structures' layout field
+# by field: a few microseconds less than building the structures.
+_CACHE, _CACHE8 = "PPP6i0P", "PPPPP6i0P"
+_APPEND_NORM = struct.Struct("@" + _CACHE + "PPiPPPiiPPiiiPiif0P")
+_APPEND8 = struct.Struct("@" + _CACHE8 + "PPiPPPiiPPiiiPiif0P")
+_NORM = struct.Struct("@iiPPf0P")
+_READ8 = struct.Struct("@" + _CACHE8 + "PPiPPii0P")
+_ATTENTION8 = struct.Struct("@" + _CACHE8 + "PPiPiPPiiifPN")
+_ACCEPT8 = struct.Struct("@" + _CACHE8 + "PPiPPPPPPPiNN")
 
 
 def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=None, q_out=None, n_q_heads: int = 0,
@@ -654,8 +687,9 @@ def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=No
     """New rows' keys (rotated) and values into the paged cache, queries (rotated) into q_out."""
     torch = _get_torch()
     dev = _device(torch)
-    d = _append_desc(q4_paged_append_desc, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
-                     rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev)
+    d = q4_paged_append_desc(cache._desc(torch, dev, cache.pool),
+                             *_append_fields(cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
+                                             rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev))
     _check(lib().q4_paged_append(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_paged_append")
 
 
@@ -668,9 +702,9 @@ class HeadNorm:
     def __init__(self, q_weight=None, k_weight=None, eps: float = 1.0e-6, q: bool = True, k: bool = True):
         self.q_weight, self.k_weight, self.eps, self.q, self.k = q_weight, k_weight, eps, q, k
 
-    def _desc(self, torch, dev: int, head_dim: int) -> q4_head_norm:
-        return q4_head_norm(int(self.q), int(self.k), _arg(self.q_weight, torch.float16, head_dim, dev, "norm.q_weight"),
-                            _arg(self.k_weight, torch.float16, head_dim, dev, "norm.k_weight"), self.eps)
+    def _pack(self, torch, dev: int, head_dim: int) -> bytes:
+        return _NORM.pack(bool(self.q), bool(self.k), _arg(self.q_weight, torch.float16, head_dim, dev, "norm.q_weight"),
+                          _arg(self.k_weight, torch.float16, head_dim, dev, "norm.k_weight"), self.eps)
 
 
 def q4_paged_append_norm(cache: PagedCache, ctx_len, row_start, rows: int, k, v, norm: HeadNorm = None, q=None, q_out=None,
@@ -679,18 +713,20 @@ def q4_paged_append_norm(cache: PagedCache, ctx_len, row_start, rows: int, k, v,
     """q4_paged_append with each query and key head normalised before its rotation."""
     torch = _get_torch()
     dev = _device(torch)
-    d = _append_desc(q4_paged_append_desc, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
-                     rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev)
-    n = None if norm is None else ctypes.byref(norm._desc(torch, dev, cache.sizes[3]))
-    _check(lib().q4_paged_append_norm(ctypes.byref(d), n, _stream_of(torch, dev, stream)), "q4_paged_append_norm")
+    d = _APPEND_NORM.pack(*cache._fields(torch, dev, cache.pool),
+                          *_append_fields(cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
+                                          rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev))
+    n = None if norm is None else norm._pack(torch, dev, cache.sizes[3])
+    _check(_by_bytes("q4_paged_append_norm")(d, n, _stream_of(torch, dev, stream)), "q4_paged_append_norm")
 
 
 def q4_tree_attention_workspace_bytes(head_dim: int) -> int:
     return lib().q4_tree_attention_workspace_bytes(head_dim)
 
 
-def _attention_desc(kind, cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace, workspace_bytes, mask,
-                    mask_words, scale, ldq, ldo, torch, dev):
+def _attention_fields(cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace, workspace_bytes, mask, mask_words, scale,
+                      ldq, ldo, torch, dev):
+    """The descriptor's fields behind the cache."""
     f16, i32_ = torch.float16, torch.int32
     w, n_seqs = n_q_heads * cache.sizes[3], cache.sizes[4]
     pq, ldq = _rows(q, f16, rows, w, ldq, dev, "q")
@@ -699,10 +735,9 @@ def _attention_desc(kind, cache, ctx_len, row_start, rows, q, n_q_heads, out, wo
         if workspace.numel() * workspace.element_size() < workspace_bytes:
             raise ValueError(f"workspace: smaller than {workspace_bytes} bytes")
         workspace = _arg(workspace, workspace.dtype, 0, dev, "workspace")
-    return kind(
-        cache._desc(torch, dev, cache.pool), _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"),
-        _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows, _arg(mask, i32_, rows * mask_words, dev, "mask"),
-        mask_words, pq, po, ldq, ldo, n_q_heads, scale, workspace, workspace_bytes)
+    return (_arg(ctx_len, i32_, n_seqs, dev, "ctx_len"), _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows,
+            _arg(mask, i32_, rows * mask_words, dev, "mask"), mask_words, pq, po, ldq, ldo, n_q_heads, scale, workspace or 0,
+            workspace_bytes)
 
 
 def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_heads: int, out, workspace,
@@ -711,20 +746,20 @@ def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_h
     """Attention of the new rows over the cached positions and, by the mask (None: causal), their own."""
     torch = _get_torch()
     dev = _device(torch)
-    d = _attention_desc(q4_tree_attention_desc, cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace,
-                        workspace_bytes, mask, mask_words, scale, ldq, ldo, torch, dev)
+    d = q4_tree_attention_desc(cache._desc(torch, dev, cache.pool),
+                               *_attention_fields(cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace,
+                                                  workspace_bytes, mask, mask_words, scale, ldq, ldo, torch, dev))
     _check(lib().q4_tree_attention(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_attention")
 
 
-def _accept_desc(kind, cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path, next_token, ctx_out,
-                 torch, dev, desc, *strides):
+def _accept_fields(cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path, next_token, ctx_out, torch, dev):
+    """The descriptor's fields between the cache and the layers."""
     i32_, n_seqs = torch.int32, cache.sizes[4]
-    return kind(
-        desc, _arg(ctx_len, i32_, n_seqs, dev, "ctx_len"), _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows,
-        _arg(draft, i32_, rows, dev, "draft"), _arg(parents, i32_, rows, dev, "parents"),
-        _arg(sampled, i32_, rows, dev, "sampled"), _arg(accepted, i32_, n_seqs, dev, "accepted"),
-        _arg(path, i32_, rows, dev, "path"), _arg(next_token, i32_, n_seqs, dev, "next_token"),
-        _arg(ctx_out, i32_, n_seqs, dev, "ctx_out"), *strides)
+    return (_arg(ctx_len, i32_, n_seqs, dev, "ctx_len"), _arg(row_start, i32_, n_seqs + 1, dev, "row_start"), rows,
+            _arg(draft, i32_, rows, dev, "draft"), _arg(parents, i32_, rows, dev, "parents"),
+            _arg(sampled, i32_, rows, dev, "sampled"), _arg(accepted, i32_, n_seqs, dev, "accepted"),
+            _arg(path, i32_, rows, dev, "path"), _arg(next_token, i32_, n_seqs, dev, "next_token"),
+            _arg(ctx_out, i32_, n_seqs, dev, "ctx_out"))
 
 
 def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, parents, sampled, accepted, path,
@@ -733,8 +768,9 @@ def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, pare
     torch = _get_torch()
     dev = _device(torch)
     elements = (n_layers - 1) * layer_stride + cache.pool if n_layers > 0 else 0
-    d = _accept_desc(q4_tree_accept_desc, cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path,
-                     next_token, ctx_out, torch, dev, cache._desc(torch, dev, elements), n_layers, layer_stride)
+    d = q4_tree_accept_desc(cache._desc(torch, dev, elements),
+                            *_accept_fields(cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path,
+                                            next_token, ctx_out, torch, dev), n_layers, layer_stride)
     _check(lib().q4_tree_accept(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_accept")
 
 
@@ -753,14 +789,13 @@ class PagedCache8:
         self.pool = n_pages * page_size * n_kv_heads * head_dim  # elements of one layer's keys
         self.blocks = n_pages * n_kv_heads * -(-page_size // Q4_CACHE8_BLOCK)  # and scales
 
-    def _desc(self, torch, dev: int, elements: int, scales: int = None) -> q4_paged_cache8:
-        s = self.sizes
-        scales = self.blocks if scales is None else scales
-        codes = [_arg(t, torch.uint8 if t.__class__ is not int and t is not None and t.dtype is torch.uint8
-                      else torch.float8_e4m3fn, elements, dev, name) for t, name in ((self.k, "cache.k"), (self.v, "cache.v"))]
-        return q4_paged_cache8(*codes, _arg(self.k_scales, torch.float32, scales, dev, "cache.k_scales"),
-                               _arg(self.v_scales, torch.float32, scales, dev, "cache.v_scales"),
-                               _arg(self.page_table, torch.int32, s[4] * s[5], dev, "cache.page_table"), *s)
+    def _fields(self, torch, dev: int, elements: int, scales: int) -> tuple:
+        s, k, v, f32 = self.sizes, self.k, self.v, torch.float32
+        u8, f8 = torch.uint8, torch.float8_e4m3fn
+        return (_arg(k, u8 if getattr(k, "dtype", None) is u8 else f8, elements, dev, "cache.k"),
+                _arg(v, u8 if getattr(v, "dtype", None) is u8 else f8, elements, dev, "cache.v"),
+                _arg(self.k_scales, f32, scales, dev, "cache.k_scales"), _arg(self.v_scales, f32, scales, dev, "cache.v_scales"),
+                _arg(self.page_table, torch.int32, s[4] * s[5], dev, "cache.page_table"), *s)
 
 
 def q4_paged_append8(cache: PagedCache8, ctx_len, row_start, rows: int, k, v, norm: HeadNorm = None, q=None, q_out=None,
@@ -769,10 +804,11 @@ def q4_paged_append8(cache: PagedCache8, ctx_len, row_start, rows: int, k, v, no
     """q4_paged_append_norm into the 8-bit cache: keys and values as e4m3 codes with a scale for 16 positions and head."""
     torch = _get_torch()
     dev = _device(torch)
-    d = _append_desc(q4_paged_append8_desc, cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
-                     rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev)
-    n = None if norm is None else ctypes.byref(norm._desc(torch, dev, cache.sizes[3]))
-    _check(lib().q4_paged_append8(ctypes.byref(d), n, _stream_of(torch, dev, stream)), "q4_paged_append8")
+    d = _APPEND8.pack(*cache._fields(torch, dev, cache.pool, cache.blocks),
+                      *_append_fields(cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs, rot_dim,
+                                      layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev))
+    n = None if norm is None else norm._pack(torch, dev, cache.sizes[3])
+    _check(_by_bytes("q4_paged_append8")(d, n, _stream_of(torch, dev, stream)), "q4_paged_append8")
 
 
 def q4_paged_read8(cache: PagedCache8, first, row_start, rows: int, k=None, v=None, ldk: int = 0, ldv: int = 0, stream=None):
@@ -782,9 +818,9 @@ def q4_paged_read8(cache: PagedCache8, first, row_start, rows: int, k=None, v=No
     _, _, heads, hd, n_seqs, _ = cache.sizes
     pk, ldk = _rows(k, torch.float16, rows, heads * hd, ldk, dev, "k")
     pv, ldv = _rows(v, torch.float16, rows, heads * hd, ldv, dev, "v")
-    d = q4_paged_read8_desc(cache._desc(torch, dev, cache.pool), _arg(first, torch.int32, n_seqs, dev, "first"),
-                            _arg(row_start, torch.int32, n_seqs + 1, dev, "row_start"), rows, pk, pv, ldk, ldv)
-    _check(lib().q4_paged_read8(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_paged_read8")
+    d = _READ8.pack(*cache._fields(torch, dev, cache.pool, cache.blocks), _arg(first, torch.int32, n_seqs, dev, "first"),
+                    _arg(row_start, torch.int32, n_seqs + 1, dev, "row_start"), rows, pk, pv, ldk, ldv)
+    _check(_by_bytes("q4_paged_read8")(d, _stream_of(torch, dev, stream)), "q4_paged_read8")
 
 
 def q4_tree_attention8(cache: PagedCache8, ctx_len, row_start, rows: int, q, n_q_heads: int, out, workspace,
@@ -793,9 +829,10 @@ def q4_tree_attention8(cache: PagedCache8, ctx_len, row_start, rows: int, q, n_q
     """q4_tree_attention over the 8-bit cache (its workspace: q4_tree_attention_workspace_bytes)."""
     torch = _get_torch()
     dev = _device(torch)
-    d = _attention_desc(q4_tree_attention8_desc, cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace,
-                        workspace_bytes, mask, mask_words, scale, ldq, ldo, torch, dev)
-    _check(lib().q4_tree_attention8(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_attention8")
+    d = _ATTENTION8.pack(*cache._fields(torch, dev, cache.pool, cache.blocks),
+                         *_attention_fields(cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace, workspace_bytes,
+                                            mask, mask_words, scale, ldq, ldo, torch, dev))
+    _check(_by_bytes("q4_tree_attention8")(d, _stream_of(torch, dev, stream)), "q4_tree_attention8")
 
 
 def q4_tree_accept8(cache: PagedCache8, ctx_len, row_start, rows: int, draft, parents, sampled, accepted, path,
@@ -805,10 +842,10 @@ def q4_tree_accept8(cache: PagedCache8, ctx_len, row_start, rows: int, draft, pa
     dev = _device(torch)
     elements = (n_layers - 1) * layer_stride + cache.pool if n_layers > 0 else 0
     scales = (n_layers - 1) * scale_stride + cache.blocks if n_layers > 0 else 0
-    d = _accept_desc(q4_tree_accept8_desc, cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path,
-                     next_token, ctx_out, torch, dev, cache._desc(torch, dev, elements, scales), n_layers, layer_stride,
-                     scale_stride)
-    _check(lib().q4_tree_accept8(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_accept8")
+    d = _ACCEPT8.pack(*cache._fields(torch, dev, elements, scales),
+                      *_accept_fields(cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path, next_token,
+                                      ctx_out, torch, dev), n_layers, layer_stride, scale_stride)
+    _check(_by_bytes("q4_tree_accept8")(d, _stream_of(torch, dev, stream)), "q4_tree_accept8")
 
 
 def q4_sample(logits, dtype, rows: int, vocab: int, tokens, temperature=None, top_k=None, top_p=None, min_p=None,

@@ -38,6 +38,29 @@ def test_struct_layouts_match_c(tmp_path):
         assert got == int(val), key
 
 
+def test_packed_descriptors_are_the_structures():
+    for packed, kind in ((q4._APPEND_NORM, q4.q4_paged_append_desc), (q4._APPEND8, q4.q4_paged_append8_desc),
+                         (q4._NORM, q4.q4_head_norm), (q4._READ8, q4.q4_paged_read8_desc),
+                         (q4._ATTENTION8, q4.q4_tree_attention8_desc), (q4._ACCEPT8, q4.q4_tree_accept8_desc)):
+        values, n = [], 0
+
+        def build(t):
+            nonlocal n
+            out = t()
+            for f, ty in t._fields_:
+                if issubclass(ty, ctypes.Structure):
+                    setattr(out, f, build(ty))
+                    continue
+                n += 1
+                v = 0.5 * n if ty is ctypes.c_float else 1000 * n + 1
+                values.append(v)
+                setattr(out, f, v)
+            return out
+
+        want = build(kind)
+        assert packed.pack(*values) == bytes(want), kind
+
+
 def cache8(**kw):
     c = dict(k=FAKE, v=FAKE, k_scales=FAKE, v_scales=FAKE, page_table=FAKE, n_pages=8, page_size=16, n_kv_heads=2,
              head_dim=128, n_seqs=2, max_pages=4)
