@@ -27,12 +27,26 @@ __device__ __forceinline__ uint32_t f32_e4m3(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t half2_e4m3(uint32_t h) {
+    uint32_t r;
+    asm("{ .reg .b16 c; cvt.rn.satfinite.e4m3x2.f16x2 c, %1; cvt.u32.u16 %0, c; }" : "=r"(r) : "r"(h));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of a number and NaN the number
+    const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ void unpack8(const uint4& a, float* x) {

@@ -54,8 +54,8 @@ extern "C" q4_status q4_tree_attention(const q4_tree_attention_desc* desc, q4_st
     const int ring_box = !tma ? 0 : even < q4x::kKeys ? even : q4x::kKeys;
     if (avg > 32 && tma) {
         const int box = even < q4x::kTcKeys ? even : q4x::kTcKeys;
-        return D == 128 ? q4x::launch_tc<128, false>(a, pools, d.workspace, dev->sms, box, s, what)
-                        : q4x::launch_tc<64, false>(a, pools, d.workspace, dev->sms, box, s, what);
+        return D == 128 ? q4x::launch_tc<128, 0>(a, pools, d.workspace, dev->sms, box, s, what)
+                        : q4x::launch_tc<64, 0>(a, pools, d.workspace, dev->sms, box, s, what);
     }
     if (D == 128)
         return avg <= 16   ? q4x::launch<128, 1>(a, pools, d.workspace, dev->sms, ring_box, s, what)

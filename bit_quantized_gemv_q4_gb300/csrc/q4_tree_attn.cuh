@@ -1494,11 +1494,11 @@ struct TcShape {
 
 // 8 bits: a slot for 32 positions' codes per converting warp, instead of the
 // outputs' staging.
-constexpr int kTcSlots = kTc8Threads / 32 - 10;
+constexpr int kTcSlots = kTc8Threads / 32 - 10;  // (kCache 2: one is not used)
 template <int D>
 struct Tc8Shape : TcShape<D> {
     static constexpr uint32_t kSlot = 32 * D;
-    static constexpr size_t kSmem = 1024 + (2 + 2 * TcShape<D>::kStages) * (size_t)TcShape<D>::kTile + 512 + kTcSlots * kSlot;
+    static constexpr size_t kSmem = 1024 + (2 + 2 * TcShape<D>::kStages) * (size_t)TcShape<D>::kTile + 512 + kTcSlots * kSlot + (32 + 256) * 4;
 };
 
 struct TcBars {
@@ -1573,6 +1573,40 @@ __device__ __forceinline__ int all_see(const Args& a, const Place& p) {
     return a.mask ? 0 : (int)q4p::page_of(a.by_g, p.rb * a.BM) + 1;
 }
 
+// Elements 8 c .. of row e of a stream's query, 16 lanes a row, from fp16 (two
+// slabs of swizzled 128-byte rows) to three e4m3 parts (three, 16 KB apart, the
+// first two in the same place) of the query times a power of two, whose inverse
+// goes to *scale.  A row with an infinity becomes NaN, as its scores would be.
+__device__ __forceinline__ void split_query(uint8_t* dst, int e, int c, float* scale) {
+    const uint4 q = *reinterpret_cast<const uint4*>(dst + (c >> 3) * 16384 + sw_off(e, c & 7));
+    __syncwarp();
+    uint32_t x[4] = {q.x, q.y, q.z, q.w};
+    uint32_t top2 = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top2 = q4p::max2(top2, x[i] & 0x7fff7fffu);  // (NaN loses: it makes its element NaN)
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top2 = q4p::max2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
+    const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    // top = m 2^k, 1 <= m < 2, k >= -14 (a lesser one counts as 2^-14): times
+    // 2^(7 - k) = 2^up 2^(7 - k - up), of which fp16 has both
+    const int k = max((int)(top >> 10), 1) - 15, up = min(7 - k, 15);
+    const uint32_t f0 = (top >> 10) == 31 ? 0x7e007e00u : (uint32_t)(15 + up) * 0x04000400u, f1 = (uint32_t)(15 + 7 - k - up) * 0x04000400u;
+    if (c == 0) *scale = __uint_as_float((uint32_t)(127 - 7 + k) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = q4p::mul2(q4p::mul2(x[i], f0), f1);
+    uint8_t* const to = dst + sw_off(e, c >> 1) + 8 * (c & 1);
+#pragma unroll
+    for (int part = 0; part < 3; ++part) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = q4p::half2_e4m3(x[i]);
+            if (part < 2) x[i] = q4p::sub2(x[i], q4p::e4m3_half2(w[i]));  // exact
+        }
+        *reinterpret_cast<uint2*>(to + part * 16384) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    }
+}
+
 // Clears row `row` of a value tile, or only its infinities and NaN; whether there were any.
 template <int D>
 __device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
@@ -1599,21 +1633,30 @@ __device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
 }
 
 //
-// k8: warps 8, 9 and 12 .. 15 bring the codes and make them fp16, 32 positions of a
-// tile at a time, in turn, first the keys', then the values'.  Each has a slot of
-// its own in shared memory: it waits for a copy, takes it into registers, sets
-// the next copy going (bulk copies of the rows that lie together in a page) and,
-// when the tile that the MMA reads is free, stores the rows into it with the
-// scales multiplied in (exact).  It also clears what must not reach every row,
-// so that the softmax has nothing to do with the tiles.
-template <int D, bool k8>
-__global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
+// kCache 1 (8 bits): warps 8, 9 and 12 .. 15 bring the codes and make them fp16,
+// 32 positions of a tile at a time, in turn, first the keys', then the values'.
+// Each has a slot of its own in shared memory: it waits for a copy, takes it
+// into registers, sets the next copy going (bulk copies of the rows that lie
+// together in a page) and, when the tile that the MMA reads is free, stores the
+// rows into it with the scales multiplied in (exact).  It also clears what must
+// not reach every row, so that the softmax has nothing to do with the tiles.
+// kCache 2 (heads of 128, pages of whole blocks): the keys stay e4m3, tiles that
+// warp 8's TMA brings and the MMA takes as they are, and five converting warps
+// have the values alone.  The query is split: a power of two times it, whose
+// greatest element then lies in 128 .. 256, is the sum of three e4m3 numbers but
+// for 2^-10 (2^-17 of the greatest), S = Q1 K + Q2 K + Q3 K in one accumulator,
+// half as long again as the fp16 product.  The blocks' scales (16 columns of S
+// each) and the row's enter the maximum and the exponent.
+template <int D, int kCache>
+__global__ void __launch_bounds__(kCache ? kTc8Threads : kTcThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ MapArgs t) {
+    constexpr bool k8 = kCache > 0, kRaw = kCache == 2;
     using Sh = std::conditional_t<k8, Tc8Shape<D>, TcShape<D>>;
     static_assert(sizeof(TcBars) <= 512, "barriers");
     constexpr uint32_t kTile = Sh::kTile;
     constexpr int NST = Sh::kStages, SLABS = D / 64;
+    static_assert(!kRaw || (D == 128 && NST == 2), "keys as they are: heads of 128");
     constexpr int kThr = k8 ? kTc8Threads : kTcThreads;
     // Notes of infinities and NaN: the warps that find them run ahead of the
     // ones that read them by less than so many segments (the softmax by one; the
@@ -1626,16 +1669,19 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
     __shared__ unsigned share_s;
     __shared__ __align__(16) unsigned sums[2 * 256];  // the threads' running sums; later (m, l) of both streams' rows, float2
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* q_s = base;                              // two tiles; between segments, stream 1's O (fp32)
-    uint8_t* k_s = base + 2 * kTile;
-    uint8_t* v_s = k_s + NST * kTile;
+    constexpr uint32_t kPart = 128 * 128;             // kRaw: a part of a stream's query, a tile of keys
+    constexpr uint32_t kQuery = kRaw ? 3 * kPart : kTile, kKeyTile = kRaw ? kPart : kTile;
+    uint8_t* q_s = base;                              // two tiles (kRaw: of three parts)
+    uint8_t* k_s = base + 2 * kQuery;
+    uint8_t* v_s = k_s + NST * kKeyTile;
+    static_assert(2 * kQuery + NST * kKeyTile == (2 + NST) * kTile, "the same room");
     TcBars& B = *reinterpret_cast<TcBars*>(v_s + NST * kTile);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int* err = a.w.err;
 
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
-            q4d::mbar_init(q4d::smem_addr(&B.k_full[i]), k8 ? 4 : 1);
+            q4d::mbar_init(q4d::smem_addr(&B.k_full[i]), kRaw ? 33 : k8 ? 4 : 1);  // kRaw: TMA's bytes, every lane's copies
             q4d::mbar_init(q4d::smem_addr(&B.k_empty[i]), 2);  // both streams' MMAs
             q4d::mbar_init(q4d::smem_addr(&B.v_full[i]), k8 ? 4 : 1);
             q4d::mbar_init(q4d::smem_addr(&B.v_empty[i]), 2);
@@ -1684,19 +1730,25 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
         uint32_t seg = 0;   // segments done
         uint32_t tiles0 = 0;  // tiles before this segment
 
-        if (k8 && (warp == 8 || warp == 9 || warp >= 12)) {
+        // kRaw: [4 tiles][8 blocks] key scales, [2 streams][128] what a row's
+        // scores are to be multiplied by.  (Tile kt's scales are written once
+        // the scores of tile kt - 2 are there; those wait until their stream has
+        // read the step before, tile kt - 4 or later, and the first of a segment
+        // until both streams have ended the one before.)
+        float* const key_scales = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&B) + 512 + kTcSlots * Tc8Shape<D>::kSlot);
+        float* const row_scales = key_scales + 32;
+        if (k8 && ((!kRaw && warp == 8) || warp == 9 || warp >= 12)) {
             // --------------------------------------------- codes to fp16
             if constexpr (k8) {
                 constexpr int NC = D / 8, PER = 32 / NC, NL = 32 / PER;  // lanes of a row (8 codes each), rows at a time, loads
-                constexpr uint32_t kConv = kTcSlots;
-                const int c = lane % NC, g = lane / NC, own = warp < 10 ? warp - 8 : warp - 10;
+                constexpr uint32_t kConv = kRaw ? kTcSlots - 1 : kTcSlots;
+                const int c = lane % NC, g = lane / NC, own = (warp < 10 ? warp - 8 : warp - 10) - (kRaw ? 1 : 0);
                 uint8_t* const slot = reinterpret_cast<uint8_t*>(&B) + 512 + own * Sh::kSlot;
                 const uint32_t slot_s = q4d::smem_addr(slot) + lane * D, fb = q4d::smem_addr(&B.raw_full[own]);
                 // Quarters of the line's tiles, 4 each; lane = position.  A quarter
-                // is looked up when the one before it is asked into L2 (a slot is
-                // too little for memory's latency), which is while the one before
-                // that is stored.  The cursor p stands at the tile of quarter
-                // `next`, the last one looked up.
+                // is looked up while the one before it is copied and the one before
+                // that stored.  The cursor p stands at the tile of quarter `next`,
+                // the last one looked up.
                 uint32_t next = own, kt = 0;
                 int id = -1, key = 0;
                 bool live = false;
@@ -1752,7 +1804,7 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                 if (more) {
                     look_up();
                     now = resolve();
-                    copy(now, a.w.k);
+                    copy(now, kRaw ? a.w.v : a.w.k);
                     next += kConv;
                 }
                 bool further = more && advance(), again = false;
@@ -1763,7 +1815,7 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                 bool flying = more;  // a copy is on its way
 #pragma unroll 1
                 while (more) {
-                    const bool values = turns & 1;
+                    const bool values = kRaw || (turns & 1);
                     const uint32_t tile = now.at >> 2, st = tile % NST;
                     if (!__all_sync(0xffffffffu, tc_wait(B, B.raw_full[own], turns & 1, err))) break;
                     ++turns;
@@ -1778,9 +1830,13 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                         for (int e = 0; e < NL; ++e)
                             if (!(now.there >> (e * PER + g) & 1u)) r[e] = make_uint2(0u, 0u);
                     }
-                    if (!values) again = further;
+                    if (kRaw || !values) again = further;
+                    if (kRaw) {
+                        if (further) then = resolve();
+                        next += kConv;
+                    }
                     flying = !values || again;
-                    if (flying) copy(values ? then : now, values ? a.w.k : a.w.v);
+                    if (flying) copy(values ? then : now, values && !kRaw ? a.w.k : a.w.v);
                     if (!values) {
                         if (further) then = resolve();
                         next += kConv;
@@ -1820,6 +1876,43 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                     }
                 }
                 if (flying) q4d::mbar_wait(fb, turns & 1, nullptr);  // a copy in flight lands before the CTA can exit
+            }
+        } else if (kRaw && warp == 8) {
+            // --------------------------------------------- tiles of keys as they are
+            if constexpr (kRaw) {
+                const int boxes = kTcKeys / t.box;
+                bool ok = true;
+                uint32_t kt = 0;
+                while (rest && ok) {
+                    const int len = p.q.ctx + p.q.n;
+                    for (; p.tile < w.end && ok; ++p.tile, ++kt) {
+                        const uint32_t st = kt % NST, fb = q4d::smem_addr(&B.k_full[st]);
+                        // the first lanes a box each, and the first 8 a block's scale
+                        const int key = p.tile * kTcKeys + lane * t.box, block = p.tile * kTcKeys + lane * q4p::kBlock;
+                        int y = t.zero_row;
+                        if (lane < boxes && key < len) {
+                            const long long at = q4p::row_at(a.w, p.s, key, p.h, 1);
+                            if (at >= 0) y = (int)at;
+                            else atomicOr(err, q4d::kErrDeviceCheck);
+                        }
+                        const long long scale = lane < 8 && block < len ? scale_of(a, p.s, block, p.h) : -1;
+                        if (kt >= (uint32_t)NST) ok = __all_sync(0xffffffffu, tc_wait(B, B.k_empty[st], (kt / NST - 1) & 1, err));
+                        if (!ok) break;
+                        if (lane == 0) q4d::mbar_arrive_expect_tx(fb, kPart);
+                        __syncwarp();
+                        if (lane < boxes) q4t::tma_load_2d(q4d::smem_addr(k_s + st * kPart) + lane * t.box * 128, &tmK, 0, y, fb);
+                        if (lane < 8)
+                            cp4(q4d::smem_addr(key_scales + (kt & 3) * 8 + lane), a.ks + (scale < 0 ? 0 : scale), scale >= 0);
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
+                    }
+                    rest = w.more(a);
+                    if (rest && ok) w.next(a);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                if (!ok) {  // copies still in flight land before the CTA can exit
+                    for (uint32_t i = kt > (uint32_t)NST ? kt - NST : 0; i < kt; ++i)
+                        q4d::mbar_wait(q4d::smem_addr(&B.k_full[i % NST]), (i / NST) & 1, nullptr);
+                }
             }
         } else if (!k8 && (warp == 8 || warp == 9)) {
             // --------------------------------------------- key / value tiles
@@ -1880,17 +1973,25 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                 const int T = w.end - p.tile;
                 const bool two = p.q.n * a.G - p.rb * a.BM > 128;
                 const int steps = two ? T : (T - i + 1) / 2;
-                const uint64_t ad = dq + (uint64_t)((two ? i : 0) * (kTile / 16));
+                const uint64_t ad = dq + (uint64_t)((two ? i : 0) * (kQuery / 16));
                 const auto tile_of = [&](int k) { return tiles0 + (two ? k : 2 * k + i); };
                 // the scores of step k (its keys have landed)
                 const auto issue_s = [&](int k) {
                     const uint32_t st = tile_of(k) % NST;
-                    const uint64_t bd = dk + (uint64_t)(st * (kTile / 16));
+                    const uint64_t bd = dk + (uint64_t)(st * (kKeyTile / 16));
                     if (leader) {
+                        if constexpr (kRaw) {
+                            // (the instruction descriptor's types: e4m3 is 0 here as fp16 is there)
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) / 16);
-                            q4t::mma_ss(sd, ad + off, bd + off, id_s, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < 12; ++kk)
+                                q4t::mma_ss_e4m3(sd, ad + (uint64_t)((kk >> 2) * (kPart / 16) + (kk & 3) * 2), bd + (uint64_t)((kk & 3) * 2), id_s,
+                                                 kk > 0 ? 1u : 0u);
+                        } else {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) / 16);
+                                q4t::mma_ss(sd, ad + off, bd + off, id_s, kk > 0 ? 1u : 0u);
+                            }
                         }
                         q4t::commit(q4d::smem_addr(&B.s_full[i]));
                         q4t::commit(q4d::smem_addr(&B.k_empty[st]));
@@ -1979,7 +2080,7 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                 if (two || i == 0) {
                     // this warp's 32 rows, whole rows at a time
                     const int R = min(a.BM, w.q.n * a.G - w.rb * a.BM);
-                    uint8_t* dst = q_s + (two ? i : 0) * kTile;
+                    uint8_t* dst = q_s + (two ? i : 0) * kQuery;
                     constexpr int NC = D / 8, PER = 32 / NC;  // chunks of a row, rows per load
                     const int c = lane % NC;
                     const uint32_t col = q4d::smem_addr(dst) + (uint32_t)(c >> 3) * 16384u;
@@ -1993,6 +2094,11 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                              a.q + (size_t)(w.q.start + tk) * a.ldq + (size_t)(w.h * a.G + rr - tk * a.G) * D + 8 * c, r < R);
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
+                    if constexpr (kRaw) {
+#pragma unroll 4
+                        for (int e = wr * 32 + lane / NC; e < wr * 32 + 32; e += PER)
+                            split_query(dst, e, c, row_scales + (two ? 128 * i : 0) + e);
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 __syncwarp();
@@ -2020,6 +2126,7 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                 const int steps = two ? T : (T - i + 1) / 2;
                 const int seen_by_all = p.q.ctx + all_see(a, p);
                 float m = -INFINITY, l = 0.f;
+                float c_row = 0.f;  // kRaw: scale log2 e times what the row's query was divided by
                 for (int j = 0; j < steps; ++j) {
                     const int tj = two ? j : 2 * j + i;  // tile of the segment
                     const int key0 = (p.tile + tj) * kTcKeys;
@@ -2046,22 +2153,48 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                             }
                         }
                     };
-                    const auto max_half = [&]() {
+                    // kRaw: the scales of half h's four blocks (0, of one that does not
+                    // exist, counts as 1: its scores are ruled out or 0)
+                    float ks[4];
+                    const auto load_scales = [&](int h) {
+                        const float4 f = *reinterpret_cast<const float4*>(key_scales + (kt & 3) * 8 + 4 * h);
+                        ks[0] = f.x == 0.f ? 1.f : f.x;
+                        ks[1] = f.y == 0.f ? 1.f : f.y;
+                        ks[2] = f.z == 0.f ? 1.f : f.z;
+                        ks[3] = f.w == 0.f ? 1.f : f.w;
+                    };
+                    const auto max_half = [&](int h) {
+                        if constexpr (kRaw) {
+                            load_scales(h);
 #pragma unroll
-                        for (int e = 0; e < 64; e += 8)
+                            for (int b = 0; b < 4; ++b) {
+                                float y[4];
 #pragma unroll
-                            for (int f = 0; f < 4; ++f)
-                                x4[f] = fmaxf(x4[f], fmaxf(__uint_as_float(s[e + f]), __uint_as_float(s[e + 4 + f])));
+                                for (int f = 0; f < 4; ++f) {
+                                    const uint32_t* z = s + 16 * b + f;
+                                    y[f] = fmaxf(fmaxf(__uint_as_float(z[0]), __uint_as_float(z[4])),
+                                                 fmaxf(__uint_as_float(z[8]), __uint_as_float(z[12])));
+                                }
+                                x4[b] = fmaxf(x4[b], fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * ks[b]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+                                for (int f = 0; f < 4; ++f)
+                                    x4[f] = fmaxf(x4[f], fmaxf(__uint_as_float(s[e + f]), __uint_as_float(s[e + 4 + f])));
+                        }
                     };
                     ok = __all_sync(0xffffffffu, tc_wait(B, B.s_full[i], n_s & 1, err));
                     if (!ok) break;
                     ++n_s;
                     q4t::fence_after();
+                    if (kRaw && j == 0) c_row = a.c * row_scales[(two ? 128 * i : 0) + row];
                     load_half(1);
-                    max_half();
+                    max_half(1);
                     load_half(0);
-                    max_half();
-                    const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * a.c;
+                    max_half(0);
+                    const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * (kRaw ? c_row : a.c);
                     float corr = 1.f;
                     if (mx > m + kLag) {
                         corr = m == -INFINITY ? 1.f : ex2(m - mx);  // nothing seen yet: O and l are zero
@@ -2071,9 +2204,12 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                     const float2 ss = make_float2(sub, sub);
                     float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
                     const auto exp_half = [&](int h) {
+                        if constexpr (kRaw) load_scales(h);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            float2 v = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), cc, ss);
+                            const float cb = kRaw ? c_row * ks[e >> 3] : 0.f;
+                            float2 v = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                                  kRaw ? make_float2(cb, cb) : cc, ss);
                             v.x = ex2(v.x);
                             v.y = ex2(v.y);
                             if (e & 1) sum2 = __fadd2_rn(sum2, v);
@@ -2177,7 +2313,7 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                     const uint32_t t0 = join ? lt + kColO : to;
                     // 16 columns at a time by way of shared memory, so that a
                     // warp stores whole sectors: 4 lanes per row.  (8 bits: whose
-                    // room the codes' slots take, so every lane stores its row's.)
+                    // room the codes' slots take: by shuffles.)
                     float* stage = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(&B) + 512) + warp * 512;
                     const auto write = [&](int ry, int col, const float4& v) {
                         if (ry >= R) return;
@@ -2205,9 +2341,25 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
                             for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(w[e]), f1 * inv, o[e]);
                         }
                         if constexpr (k8) {
+                            // 4 x 4 chunks of 4 lanes: chunk e of lane x goes to lane e, as chunk x
+#pragma unroll
+                            for (int b = 2; b > 0; b >>= 1) {
+                                const bool up = lane & b;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if (e & b) continue;
+#pragma unroll
+                                    for (int f = 0; f < 4; ++f) {
+                                        const float give = up ? o[4 * e + f] : o[4 * (e + b) + f];
+                                        const float got = __shfl_xor_sync(0xffffffffu, give, b);
+                                        o[4 * e + f] = up ? got : o[4 * e + f];
+                                        o[4 * (e + b) + f] = up ? o[4 * (e + b) + f] : got;
+                                    }
+                                }
+                            }
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                write(rw + lane, c0 + 4 * e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                                write(rw + (lane & ~3) + e, c0 + 4 * (lane & 3), make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
                         } else {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -2248,7 +2400,7 @@ __global__ void __launch_bounds__(k8 ? kTc8Threads : kTcThreads, 1)
 }
 
 // box: rows that lie together in a page (8 bits: 1, 2 .. 32).
-template <int D, bool k8>
+template <int D, int kCache>
 q4_status launch_tc(Args& a, const Pools& c, void* workspace, int sms, int box, cudaStream_t s, const char* what) {
     MapArgs t;
     a.ctas = sms < kMaxTcCtas ? sms : kMaxTcCtas;
@@ -2263,13 +2415,14 @@ q4_status launch_tc(Args& a, const Pools& c, void* workspace, int sms, int box, 
     t.box = box;
     t.zero_row = (int)((long long)c.n_pages * c.n_kv_heads * c.page_size);
     CUtensorMap tmK = {}, tmV = {};
-    if constexpr (!k8) {
-        const q4_status st = pool_maps<false>(&tmK, &tmV, c, (uint32_t)box);
+    constexpr bool k8 = kCache > 0;
+    if constexpr (kCache != 1) {
+        const q4_status st = pool_maps<k8>(&tmK, &tmV, c, (uint32_t)box);
         if (st != Q4_OK) return st;
     }
     using Sh = std::conditional_t<k8, Tc8Shape<D>, TcShape<D>>;
     constexpr int kThr = k8 ? kTc8Threads : kTcThreads;
-    const auto kern = tree_attn_tc_kernel<D, k8>;
+    const auto kern = tree_attn_tc_kernel<D, kCache>;
     static std::atomic<int> marks[64];
     cudaError_t e = q4i::ensure_smem_attr(reinterpret_cast<const void*>(kern), marks, (int)Sh::kSmem);
     if (e == cudaSuccess) {

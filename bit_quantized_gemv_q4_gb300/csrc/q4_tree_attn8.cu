@@ -46,10 +46,24 @@ extern "C" q4_status q4_tree_attention8(const q4_tree_attention8_desc* desc, q4_
     //   67     126 (50)     100 (39)
     //   97     205          117
     // (jobs of 32 rows, two CTAs per SM: 74, 70, 74, 111 (32), 102, 135 (42), 213)
+    // Of the tcgen05 kernel's forms the one whose keys stay e4m3 converts half as
+    // much, and needs more for the products and for each job's query.  us of 16
+    // sequences, the longest 6000 (400) positions, 8 kv heads of 128, by mean rows:
+    //          keys e4m3    keys fp16
+    //   110    100 (31)     118 (26)
+    //   175    111          129
+    //   250    127 (42)     141 (34)
+    //   350    169          179
+    //   490    224 (66)     207 (55)
+    //   700    337          306
+    // so it has up to 384 rows, where the page table holds long contexts.
     if (avg > 48) {
         const int rows = even < 32 ? even : 32;
-        return D == 128 ? q4x::launch_tc<128, true>(a, pools, d.workspace, dev->sms, rows, s, what)
-                        : q4x::launch_tc<64, true>(a, pools, d.workspace, dev->sms, rows, s, what);
+        const bool lengthy = (long long)d.cache.max_pages * d.cache.page_size >= 2048;
+        if (D == 128 && tma && d.cache.page_size % q4p::kBlock == 0 && avg <= 384 && lengthy)
+            return q4x::launch_tc<128, 2>(a, pools, d.workspace, dev->sms, rows, s, what);
+        return D == 128 ? q4x::launch_tc<128, 1>(a, pools, d.workspace, dev->sms, rows, s, what)
+                        : q4x::launch_tc<64, 1>(a, pools, d.workspace, dev->sms, rows, s, what);
     }
     return D == 128 ? q4x::launch<128, 1, true>(a, pools, d.workspace, dev->sms, box, s, what)
                     : q4x::launch<64, 1, true>(a, pools, d.workspace, dev->sms, box, s, what);
