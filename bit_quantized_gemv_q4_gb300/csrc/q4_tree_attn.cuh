@@ -150,7 +150,7 @@ static __device__ __noinline__ unsigned line_scan(const Args& a, unsigned* sums,
 // CTA between two others of a job has a part of it, and another, as fewer
 // parts join faster (one user's 2000 positions: 14.3 -> 11.6 us).
 __device__ __forceinline__ unsigned line_share(const Args& a, unsigned line) {
-    return max((line + (unsigned)a.ctas - 1) / (unsigned)a.ctas, 2u * (unsigned)a.cost_full);
+    return max((line + (unsigned)a.ctas - 1) / (unsigned)a.ctas, 2u * (unsigned)max(a.cost_full, a.cost_half));
 }
 
 // The job that holds unit x (x < the line's length), from its first tile on.
@@ -1484,6 +1484,13 @@ constexpr int kTcThreads = 384, kTc8Threads = 512;
 // 32: 64 trees of 30 over 1000 positions 113 / 66 / 64, 8 trees of 40 up to 8000
 // 67 / 49 / 48, the chunks 137 / 135 / 132.
 constexpr int kTcCostFull = 8, kTcCostHalf = 5, kTcLead = 32;
+// 8 bits, keys made fp16 (kCache 1 below): the conversions of a tile take as long
+// for 128 rows as for 256, and nothing runs beside them (2.9 us against 2.2).  us
+// of the chunks and of 16 sequences up to 256 rows (6000 positions) with half a
+// tile at 5 / 8 / 10 / 11 : 8: 210 / 183 / 179 / 179, 308 / 284 / 280 / 282.
+// Keys as they are (kCache 2): 1.5 us against 2.5; lead 16 / 32 / 48 / 64: 8 trees
+// of 61 up to 20000 positions 113 / 108 / 105 / 107.
+constexpr int kTc8CostHalf = 10, kTc8Lead = 40, kTcE4Lead = 48;
 
 template <int D>
 struct TcShape {
@@ -1647,6 +1654,17 @@ __device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
 // for 2^-10 (2^-17 of the greatest), S = Q1 K + Q2 K + Q3 K in one accumulator,
 // half as long again as the fp16 product.  The blocks' scales (16 columns of S
 // each) and the row's enter the maximum and the exponent.
+//
+// What bounds it: the converting warps (some 2900 cycles for 32 positions: a
+// warp's instructions one after another, fetched anew beside the other roles')
+// where a tile has 128 rows, the softmax and the products where it has 256.
+// Measured, contexts and heads as above: the chunks 179 us (kCache 1), the trees
+// 105 us (kCache 2; 1 takes 119).  Keys and values by turns in one body; tried in
+// kCache 1 (trees / chunks, before the tiles' costs were weighed: 150 / 215): a
+// warp that brings the slots of all 197 / 311, four converting warps 215 / 328,
+// five 148 / 237, pairs of a key and a value quarter 155 / 291, 16 positions at a
+// time 212 / 280.  In kCache 2: keys of 128 rows or fewer alone as they are, by
+// the converting warps themselves, 158 / 260; the tiles asked into L2 ahead 113.
 template <int D, int kCache>
 __global__ void __launch_bounds__(kCache ? kTc8Threads : kTcThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -2408,8 +2426,8 @@ q4_status launch_tc(Args& a, const Pools& c, void* workspace, int sms, int box, 
     a.KT = kTcKeys;
     a.KT_log2 = 7;
     a.cost_full = kTcCostFull;
-    a.lead = kTcLead;
-    a.cost_half = kTcCostHalf;
+    a.lead = kCache == 1 ? kTc8Lead : kCache == 2 ? kTcE4Lead : kTcLead;
+    a.cost_half = kCache == 1 ? kTc8CostHalf : kTcCostHalf;
     place_parts<D>(a, workspace);
     t.a = a;
     t.box = box;

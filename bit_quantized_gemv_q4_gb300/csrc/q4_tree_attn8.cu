@@ -35,32 +35,24 @@ extern "C" q4_status q4_tree_attention8(const q4_tree_attention8_desc* desc, q4_
     const long long pool_rows = (long long)d.cache.n_pages * d.cache.n_kv_heads * d.cache.page_size;
     const bool tma = even >= 8 && pool_rows < (1ll << 31) - 1;
     const int box = !tma ? 0 : even < q4x::kKeys ? even : q4x::kKeys;
-    // Rows per kv head of the average sequence choose the kernel.  us of 32
-    // sequences up to 4000 (500) positions, 8 kv heads of 128, by mean rows:
-    //          jobs of 16   tcgen05
-    //   10     51           111
-    //   18     63           103
-    //   26     64           95
-    //   32     86 (34)      115 (35)
-    //   40     92           104
-    //   67     126 (50)     100 (39)
-    //   97     205          117
-    // (jobs of 32 rows, two CTAs per SM: 74, 70, 74, 111 (32), 102, 135 (42), 213)
-    // Of the tcgen05 kernel's forms the one whose keys stay e4m3 converts half as
-    // much, and needs more for the products and for each job's query.  us of 16
-    // sequences, the longest 6000 (400) positions, 8 kv heads of 128, by mean rows:
-    //          keys e4m3    keys fp16
-    //   110    100 (31)     118 (26)
-    //   175    111          129
-    //   250    127 (42)     141 (34)
-    //   350    169          179
-    //   490    224 (66)     207 (55)
-    //   700    337          306
-    // so it has up to 384 rows, where the page table holds long contexts.
+    // Rows per kv head of the average sequence choose the kernel, and, of the
+    // tcgen05 kernel's forms, with the page table's length whether the keys stay
+    // e4m3: that converts half as much, and needs more for the products of 256 rows
+    // and for a job's query.  us of 16 sequences, 8 kv heads of 128, the longest
+    // 20000 / 6000 / 2000 / 500 positions, by mean rows (which vary by a tenth or
+    // so between the lengths):
+    //         jobs of 16             keys e4m3              keys fp16
+    //   38    176 / 69 / 37 / 22     159 / 73 / 44 / 31     244 / 86 / 46 / 25
+    //   51    241 / 92 / 41 / 27     166 / 78 / 45 / 30     248 / 90 / 42 / 25
+    //   85    326 / 120 / 52 / 35    150 / 74 / 43 / 26     214 / 85 / 42 / 26
+    //   117   436 / 184 / 68 / 40    173 / 96 / 49 / 33     217 / 93 / 47 / 29
+    //   135   528 / 191 / 74 / 48    204 / 97 / 49 / 35     227 / 99 / 47 / 29
+    //   175   698 / 215 / 93 / 53    214 / 104 / 55 / 33    192 / 94 / 50 / 29
+    // (jobs of 32 rows instead of 16, two CTAs per SM, were slower at all sizes)
     if (avg > 48) {
         const int rows = even < 32 ? even : 32;
-        const bool lengthy = (long long)d.cache.max_pages * d.cache.page_size >= 2048;
-        if (D == 128 && tma && d.cache.page_size % q4p::kBlock == 0 && avg <= 384 && lengthy)
+        const bool lengthy = (long long)d.cache.max_pages * d.cache.page_size >= 4096;
+        if (D == 128 && tma && d.cache.page_size % q4p::kBlock == 0 && avg <= 168 && lengthy)
             return q4x::launch_tc<128, 2>(a, pools, d.workspace, dev->sms, rows, s, what);
         return D == 128 ? q4x::launch_tc<128, 1>(a, pools, d.workspace, dev->sms, rows, s, what)
                         : q4x::launch_tc<64, 1>(a, pools, d.workspace, dev->sms, rows, s, what);

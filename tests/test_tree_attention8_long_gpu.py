@@ -1,5 +1,5 @@
 """GPU parity of the attention over the 8-bit paged cache in the form for page
-tables of many positions (heads of 128, pages of whole blocks, 49 .. 384 rows per
+tables of many positions (heads of 128, pages of whole blocks, 49 .. 168 rows per
 kv head): its keys meet the products as the codes they are, its queries in three
 8-bit parts."""
 import numpy as np
@@ -15,7 +15,7 @@ torch = pytest.importorskip("torch")
 import bit_quantized_gemv_q4_gb300 as q4  # noqa: E402
 
 pytestmark = pytest.mark.gpu
-POSITIONS = 2048  # of a page table, from which on the form is taken
+POSITIONS = 4096  # of a page table, from which on the form is taken
 
 make, reckon = short.batch, short.expected
 
@@ -61,10 +61,10 @@ def as_long(monkeypatch):
 CASES = [
     # Hkv, G, page, ctx, n: jobs of up to 128 rows, of more, of both; boxes of 16 and 32 rows
     (2, 4, 16, [500, 130, 0], [13, 14, 15]),
-    (2, 4, 64, [300, 0, 40], [40, 33, 64]),
-    (1, 8, 48, [700], [40]),
-    (2, 2, 32, [5, 129, 1000], [120, 130, 60]),
-    (1, 1, 128, [2100], [300]),
+    (2, 4, 64, [300, 0, 40, 7], [40, 33, 64, 0]),
+    (1, 8, 48, [700, 5], [40, 0]),
+    (2, 2, 32, [5, 129, 1000, 0], [120, 130, 60, 0]),
+    (1, 1, 128, [2100, 0], [300, 0]),
     (1, 16, 16, [127], [9]),
     (3, 7, 16, [0, 1, 64, 3], [9, 0, 17, 30]),
     (1, 2, 240, [1900, 3], [64, 65]),
@@ -86,7 +86,7 @@ def test_attention(case, kind):
     short.check(out, b, q, *want)
 
 
-@pytest.mark.parametrize("page,n", [(16, [50, 40]), (64, [40, 70]), (16, [100, 90])])
+@pytest.mark.parametrize("page,n", [(16, [50, 40]), (64, [40, 70]), (16, [100, 50])])
 def test_blocks_of_unlike_scales(as_long, page, n):
     short.test_blocks_of_unlike_scales(page, n)
 
@@ -104,12 +104,12 @@ def test_calls_side_by_side(as_long):
     short.test_calls_side_by_side_and_graphs_that_share_a_workspace()
 
 
-@pytest.mark.parametrize("n,G,page", [(40, 2, 16), (200, 1, 16), (20, 8, 128)])
+@pytest.mark.parametrize("n,G,page", [(40, 2, 16), (150, 1, 16), (20, 8, 128)])
 def test_small_probabilities_beside_dominant_ones(as_long, n, G, page):
     short.test_small_probabilities_beside_dominant_ones_in_every_form(n, G, page)
 
 
-@pytest.mark.parametrize("n", [20, 50])
+@pytest.mark.parametrize("n", [20, 40])
 def test_queries_of_every_magnitude(n):
     # rows from fp16's least numbers to its greatest, rows of zeros, and rows whose elements lie 2^20 apart
     g = np.random.default_rng(n)
@@ -128,7 +128,7 @@ def test_queries_of_every_magnitude(n):
     short.check(out, b, q, *want)
 
 
-@pytest.mark.parametrize("n", [20, 50])
+@pytest.mark.parametrize("n", [20, 40])
 def test_queries_that_are_no_numbers_stay_in_their_rows(n):
     g = np.random.default_rng(n)
     b = long(g, [300], [n], 1, 128, 16)
@@ -147,7 +147,7 @@ def test_queries_that_are_no_numbers_stay_in_their_rows(n):
 
 
 @pytest.mark.parametrize("what", ["k", "v"])
-@pytest.mark.parametrize("n", [20, 50])
+@pytest.mark.parametrize("n", [20, 40])
 def test_codes_that_are_no_numbers_reach_who_sees_them(n, what):
     g = np.random.default_rng(70 + n)
     b = long(g, [130, 200], [n, n], 2, 128, 32)
