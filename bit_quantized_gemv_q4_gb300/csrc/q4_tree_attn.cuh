@@ -1487,10 +1487,13 @@ constexpr int kTcCostFull = 8, kTcCostHalf = 5, kTcLead = 32;
 // 8 bits, keys made fp16 (kCache 1 below): the conversions of a tile take as long
 // for 128 rows as for 256, and nothing runs beside them (2.9 us against 2.2).  us
 // of the chunks and of 16 sequences up to 256 rows (6000 positions) with half a
-// tile at 5 / 8 / 10 / 11 : 8: 210 / 183 / 179 / 179, 308 / 284 / 280 / 282.
+// tile at 5 / 8 / 10 / 11 : 8: 210 / 183 / 179 / 179, 308 / 284 / 280 / 282.  Heads
+// of 64: 1.5 against 1.8; at 6 / 8 / 10 : 8 137 / 138 / 139, 213 / 219 / 222.
 // Keys as they are (kCache 2): 1.5 us against 2.5; lead 16 / 32 / 48 / 64: 8 trees
 // of 61 up to 20000 positions 113 / 108 / 105 / 107.
-constexpr int kTc8CostHalf = 10, kTc8Lead = 40, kTcE4Lead = 48;
+template <int D>
+constexpr int kTc8CostHalf = D == 64 ? 7 : 10;
+constexpr int kTc8Lead = 40, kTcE4Lead = 48;
 
 template <int D>
 struct TcShape {
@@ -2427,7 +2430,7 @@ q4_status launch_tc(Args& a, const Pools& c, void* workspace, int sms, int box, 
     a.KT_log2 = 7;
     a.cost_full = kTcCostFull;
     a.lead = kCache == 1 ? kTc8Lead : kCache == 2 ? kTcE4Lead : kTcLead;
-    a.cost_half = kCache == 1 ? kTc8CostHalf : kTcCostHalf;
+    a.cost_half = kCache == 1 ? kTc8CostHalf<D> : kTcCostHalf;
     place_parts<D>(a, workspace);
     t.a = a;
     t.box = box;
