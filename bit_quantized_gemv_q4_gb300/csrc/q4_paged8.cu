@@ -168,8 +168,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) append_rows_kernel(const __gri
             const int y = __shfl_up_sync(0xffffffffu, sum, x);
             if (lane >= x) sum += y;
         }
-        if (lane == kWin - 1) rows_s = sum;
-        for (int j = 0; j < m; ++j) {
+        // (runs of one window overlap, and are more than kMost rows, only where the
+        // starts are not in order, which is latched above: what is past it is left out)
+        if (lane == kWin - 1) rows_s = min(sum, kMost);
+        for (int j = 0; j < m && sum - m + j < kMost; ++j) {
             row_run[sum - m + j] = lane;
             row_at_run[sum - m + j] = j;
             row_s[sum - m + j] = run_s[lane].row + j;

@@ -315,6 +315,27 @@ def test_append8_around_bad_sequences_and_pages():
     assert same[:6].all() and same[10:].all() and bool((qo[6:10] == 9.0).all())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_append8_starts_out_of_order_stay_in_their_pages(d):
+    # sequences 0 (rows 0 .. 15) and 2 (rows 3 .. 19) overlap, 1 and 3 end before they begin: what is stored is not
+    # defined, where it is stored is
+    g = np.random.default_rng(10)
+    b = Batch8(g, [0, 0, 0, 0], [16, 16, 17, 16], 2, d, 16, spare=6)
+    c = b.to_device(q4)
+    b.dstart.copy_(torch.tensor([0, 16, 3, 20, 2], dtype=torch.int32))
+    before = b.from_device()
+    k, v, q = torch_dev(rand16(g, b.rows, 2 * d)), torch_dev(rand16(g, b.rows, 2 * d)), torch_dev(rand16(g, b.rows, d))
+    qo = torch.full_like(q, 9.0)
+    q4.q4_paged_append8(c, b.dctx, b.dstart, b.rows, k, v, q=q, q_out=qo, n_q_heads=1)
+    assert q4.q4_device_status() == -7
+    mine = np.zeros(b.n_pages, bool)
+    mine[b.table[0][:1]] = mine[b.table[2][:2]] = True
+    for x, y in zip(before, b.from_device()):
+        assert np.array_equal(x[:, ~mine].view(np.uint8), y[:, ~mine].view(np.uint8))
+    assert bool((qo[20:] == 9.0).all())
+    assert bool(((qo == 9.0) | (qo == q))[:20].all())
+
+
 def test_append8_many_sequences():
     # more sequences than one level of the row search, most of them empty
     g = np.random.default_rng(6)
