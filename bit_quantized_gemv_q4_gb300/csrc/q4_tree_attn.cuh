@@ -364,6 +364,9 @@ constexpr int kConsumers = 128, kThreads = 160;
 // tokens up to 2000 positions 37 / 30 / 29, 100 users' up to 500 56 / 38 / 36,
 // 40 up to 12000 94 / 94 / 94.
 constexpr int kRingCost = 4, kRingLead = 16;
+// 8 bits, whose tiles are twice as long: lead 4 / 8 / 12 / 16 / 24: 48 users' tokens
+// up to 14000 positions 181 / 175 / 176 / 176 / 180, up to 4000 64 / 62 / 63 / 64 / 67.
+constexpr int kRing8Lead = 8;
 
 // Positions of a tile.  8 bits, the line: 128, as a tile's fixed cost (waits,
 // statistics) weighs twice as much against half the bytes (48 users' tokens up
@@ -487,9 +490,12 @@ __device__ __forceinline__ void latch_bad(const Args& a) {
 // users' tokens over contexts up to 14000 (32 query heads on 8 of 128, 911 MB)
 // 175 us = 5.2 TB/s, 77 % of the measured copy rate, with pages of 64 165 us
 // (of 16: more and smaller copies); two CTAs with three stages 232 us (before
-// the last 13).  The pages looked up a tile ahead brought nothing.
+// the last 13).  The pages looked up a tile ahead brought nothing.  Heads of 64
+// leave room for four: 119 us against 139 with three (457 MB).
+template <int D, bool k8>
+constexpr int kRingCtas = !k8 ? 2 : D == 64 ? 4 : 3;
 template <int D, int WM, bool kTma, bool kClustered, bool k8>
-__global__ void __launch_bounds__(kThreads, k8 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, kRingCtas<D, k8>)
     tree_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ MapArgs t) {
     constexpr int BM = 16 * WM, WN = 4 / WM;
@@ -1385,9 +1391,11 @@ q4_status launch(Args& a, const Pools& c, void* workspace, int sms, int box, cud
     CUtensorMap k = {}, v = {};
     a.BM = 16 * WM;
     a.cost_full = a.cost_half = kRingCost;
-    a.lead = kRingLead;
-    const int resident = k8 ? 3 * sms : 2 * sms;
-    a.ctas = resident < kMaxCtas ? resident : kMaxCtas;
+    a.lead = k8 ? kRing8Lead : kRingLead;
+    // (8 bits: jobs of 16 rows, whose parts are smaller)
+    static_assert(2 * 16 < kMaxRows, "the parts of twice as many CTAs fit the workspace");
+    const int resident = kRingCtas<D, k8> * sms, most = k8 ? 2 * kMaxCtas : kMaxCtas;
+    a.ctas = resident < most ? resident : most;
     place_parts<D>(a, workspace);
     if (box) {
         const q4_status st = pool_maps<k8>(&k, &v, c, (uint32_t)box);
