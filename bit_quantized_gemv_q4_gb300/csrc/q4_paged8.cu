@@ -50,7 +50,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 // not quite cover (issue slots 47 .. 54 % busy).  Measured, 32 query and 8 kv heads
 // of 128: one row with norms (16 query heads) 4.8 us, 40 rows into 8 bits 5.5;
 // 6767 rows with norms into fp16 (166 MB in and out) 33.8 us = 4.9 TB/s, 72 % of
-// the measured copy rate, into 8 bits (152 MB) 38.6 = 3.9 TB/s, 58 %.
+// the measured copy rate, into 8 bits (152 MB) 38.6 = 3.9 TB/s, 58 %
+// (with three blocks per SM 38.0 and 39.0, with five 34.4 and 42.9).
 constexpr int kRowThreads = 256, kAhead = 2;
 constexpr int kWin = 8;                     // rows of a window
 constexpr int kCover = kWin + kBlock - 1;   // rows that runs beginning in it may have
@@ -423,9 +424,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) append_rows_kernel(const __gri
 
 // -------------------------------------------------------------------- read ---
 // A warp per row, 16 codes a lane.  What bounds it: bytes.  Measured: 31982 rows
-// of 8 heads of 128 (197 MB in and out) 38.5 us = 5.1 TB/s, 75 % of the measured
-// copy rate.  8 codes a lane (whole sectors at a store) 41 us, 4 rows a warp
-// that share their look-ups 42.
+// of 8 heads of 128 (197 MB in and out) 36.7 us = 5.4 TB/s, 79 % of the measured
+// copy rate, with six blocks per SM (40 registers; five 38.1, eight 36.9).  With
+// five: 8 codes a lane (whole sectors at a store) 41 us, 4 rows a warp that share
+// their look-ups 42, blocks of 128 / 512 threads 37.9 / 43.
 constexpr int kReadThreads = 256;
 
 struct ReadArgs {
@@ -435,7 +437,7 @@ struct ReadArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs p) {
+__global__ void __launch_bounds__(kReadThreads, 6) read_kernel(const __grid_constant__ ReadArgs p) {
     const View& w = p.c.w;
     const int lane = threadIdx.x & 31, row = (int)(blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5));
     if (blockIdx.x == 0) {
