@@ -2403,6 +2403,8 @@ __global__ void __launch_bounds__(kCache ? kTc8Threads : kTcThreads, 1)
                             __syncwarp();
                         }
                     }
+                    // (what comes next is a lane's own row, which others of the warp have written)
+                    if constexpr (k8) __syncwarp();
                     if (B.odd[seg_done & (kOdd - 1)] == (int)seg_done + 1 && r >= 0) {
                         const int rr = done.rb * a.BM + r;
                         add_odd<D, k8>(a, done, T, tok, join ? D / 2 * i : 0, c1,

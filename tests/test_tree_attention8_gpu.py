@@ -439,3 +439,44 @@ def test_no_rows():
         q4.q4_tree_attention8(c, b.dctx, b.dstart, rows, torch.zeros_like(out), 1, out, ws, n)
         assert q4.q4_device_status() == 0
     assert bool((out == -5.0).all())
+
+
+# tcgen05 jobs whose rows end in one CTA, and those that several share, with one softmax stream or two
+NAN_FORMS = {
+    "128 rows": dict(S=40, Hkv=2, G=4, n=(13, 30), ctx=(0, 300), d=128, page=16),
+    "128 rows, heads of 64": dict(S=40, Hkv=2, G=4, n=(13, 30), ctx=(0, 300), d=64, page=16),
+    "256 rows": dict(S=20, Hkv=2, G=4, n=(35, 64), ctx=(0, 300), d=128, page=48),
+    "shared": dict(S=4, Hkv=1, G=4, n=(13, 64), ctx=(1500, 3000), d=128, page=32),
+    "shared, heads of 64": dict(S=4, Hkv=1, G=4, n=(13, 64), ctx=(1500, 3000), d=64, page=32),
+}
+
+
+@pytest.mark.parametrize("name", NAN_FORMS)
+def test_nan_among_every_lanes_columns_stays_in_its_column(name):
+    # the columns of a row are stored by other lanes than the one that adds the NaN its row sees: every new row
+    # has a NaN code in every fourth column, from another one on for each row, and every run gives the same bits
+    f = NAN_FORMS[name]
+    g = np.random.default_rng(50 + len(name))
+    draw = lambda r: [int(x) for x in g.integers(r[0], r[1] + 1, f["S"])]  # noqa: E731
+    b = batch(g, draw(f["ctx"]), draw(f["n"]), f["Hkv"], f["d"], f["page"])
+    for s in range(b.S):
+        for j in range(b.n[s]):
+            p = b.ctx[s] + j
+            b.v8[0, b.table[s, p // b.page], :, p % b.page, (j * 7 + s) % 4::4] = 0x7F if j % 2 else 0xFF
+    b.set_values()
+    q = rand16(g, b.rows, b.Hkv * f["G"], b.d)
+    sees = [np.eye(n, dtype=bool) for n in b.n]  # a row sees itself: one column of four is NaN
+    with np.errstate(all="ignore"):
+        a, A, B = expected(b, q, sees)
+    odd = np.isnan(a)
+    assert odd.mean() == 0.25
+    c = b.to_device(q4)
+    first = None
+    for _ in range(4):
+        out = attend(b, c, q, "tree", sees)
+        assert q4.q4_device_status() == 0
+        first = out if first is None else first
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16))
+    got = first.cpu().numpy()[:b.rows].reshape(a.shape)
+    assert np.array_equal(np.isnan(got), odd), np.argwhere(np.isnan(got) != odd)[:5]
+    assert close(got, a, A, B)[~odd].all()

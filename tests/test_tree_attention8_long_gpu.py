@@ -170,3 +170,8 @@ def test_codes_that_are_no_numbers_reach_who_sees_them(n, what):
     if what == "k":
         fine[n + 4:, 4:] = False
     assert short.close(out, a, A, B)[fine].all()
+
+
+@pytest.mark.parametrize("name", ["128 rows", "shared"])
+def test_nan_among_every_lanes_columns(as_long, name):
+    short.test_nan_among_every_lanes_columns_stays_in_its_column(name)
