@@ -49,6 +49,19 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {  // of a numb
     const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
+
+// Eight fp16 numbers with NaN for infinities (x * 0 + x, which is x where x is finite).
+__device__ __forceinline__ uint4 without_infinities(const uint4& a) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __half2 h = *reinterpret_cast<const __half2*>(&w[e]), y = __hfma2(h, __half2half2(__ushort_as_half(0)), h);
+        r[e] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 __device__ __forceinline__ void unpack8(const uint4& a, float* x) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll

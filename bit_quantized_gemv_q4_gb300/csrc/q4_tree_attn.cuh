@@ -658,6 +658,13 @@ __global__ void __launch_bounds__(kThreads, kRingCtas<D, k8>)
     const int wm = warp / WN, wn = warp % WN;
     static_assert(!k8 || WM == 1, "jobs of 16 rows");
     constexpr bool kTwoChains = k8 && NT == 2;
+    // 8 bits: an infinity in a query counts as NaN.  All its scores can be -inf,
+    // which would look as if the row saw nothing; finite queries have none, as
+    // their sums stay below 2^40.  So a seen score of -inf makes the row NaN (48
+    // users' tokens 171 us, with the infinities taken out of the query 175); with
+    // heads of 64, where that costs registers that the tile loop lacks, the query
+    // goes in with NaN for infinities (95 against 99 us).
+    constexpr bool kInfSeen = k8 && D == 128;
     uint32_t qf[k8 ? 1 : KS][4];  // (8 bits: in shared memory, so that three CTAs' registers fit an SM)
     int tok[2] = {0, 0};             // tokens of this thread's rows
     float o[DN][4], m[2], l[2];
@@ -687,8 +694,9 @@ __global__ void __launch_bounds__(kThreads, kRingCtas<D, k8>)
 #pragma unroll
                 for (int kk = lane & 7; kk < KS; kk += 8) {
                     const uint4 z = make_uint4(0, 0, 0, 0);
-                    const uint4 x = live ? *reinterpret_cast<const uint4*>(src + 16 * kk) : z;
-                    const uint4 y = live ? *reinterpret_cast<const uint4*>(src + 16 * kk + 8) : z;
+                    uint4 x = live ? *reinterpret_cast<const uint4*>(src + 16 * kk) : z;
+                    uint4 y = live ? *reinterpret_cast<const uint4*>(src + 16 * kk + 8) : z;
+                    if constexpr (!kInfSeen) x = q4p::without_infinities(x), y = q4p::without_infinities(y);
                     *reinterpret_cast<uint4*>(query_s + swz<D>(r, 2 * kk)) = make_uint4(x.x, x.z, y.x, y.z);
                     *reinterpret_cast<uint4*>(query_s + swz<D>(r, 2 * kk + 1)) = make_uint4(x.y, x.w, y.y, y.w);
                 }
@@ -806,6 +814,7 @@ __global__ void __launch_bounds__(kThreads, kRingCtas<D, k8>)
                 for (int e = 0; e < 4; ++e) {
                     const int nj = key0 + wn * KW + nt * 8 + 2 * u + (e & 1) - p.q.ctx;
                     if (nj >= 0 && (nj >= p.q.n || !sees(a, p.q.start, tok[e >> 1], nj))) sc[nt][e] = -INFINITY;
+                    else if (kInfSeen && sc[nt][e] == -INFINITY) sc[nt][e] = NAN;
                 }
         }
         uint32_t pa[NT / 2][4];
@@ -816,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, kRingCtas<D, k8>)
             for (int nt = 0; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(sc[nt][2 * e], sc[nt][2 * e + 1]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            if (kInfSeen && !tail && mx == -INFINITY) l[e] = NAN;
             const float mn = fmaxf(m[e], mx * a.c);  // (c is positive: checked on the host)
             const float ms = mn == -INFINITY ? 0.f : mn;
             const float f = ex2(m[e] - ms);
@@ -2165,6 +2175,7 @@ __global__ void __launch_bounds__(kCache ? kTc8Threads : kTcThreads, 1)
                     // The row in halves, so that it fits the registers: the
                     // maximum of the second, of the first, P of the first, the
                     // second once more, P of the second.
+                    uint32_t seen = 0;  // what this row sees of the tile, some bits of it (kCache 1, tail)
                     uint32_t s[64];
                     float x4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     const auto load_half = [&](int h) {
@@ -2175,6 +2186,7 @@ __global__ void __launch_bounds__(kCache ? kTc8Threads : kTcThreads, 1)
 #pragma unroll
                             for (int w = 0; w < 2; ++w) {
                                 const uint32_t bits = sees_word(a, p.q, tok, key0 + 64 * h + 32 * w - p.q.ctx);
+                                if (kCache == 1) seen |= bits;
                                 if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
@@ -2223,7 +2235,11 @@ __global__ void __launch_bounds__(kCache ? kTc8Threads : kTcThreads, 1)
                     max_half(1);
                     load_half(0);
                     max_half(0);
-                    const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * (kRaw ? c_row : a.c);
+                    const float top = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
+                    // an infinity in the query whose products are all of the other sign
+                    // (finite ones stay below 2^40): NaN, not a row that sees nothing
+                    if (kCache == 1 && top == -INFINITY && (!tail || seen)) l = NAN;
+                    const float mx = top * (kRaw ? c_row : a.c);
                     float corr = 1.f;
                     if (mx > m + kLag) {
                         corr = m == -INFINITY ? 1.f : ex2(m - mx);  // nothing seen yet: O and l are zero

@@ -848,9 +848,9 @@ q4_status q4_paged_read8(const q4_paged_read8_desc *desc, q4_stream_t stream);
 /* 9d. q4_tree_attention8 -- 7c over the 8-bit cache: its arguments, masks,
  * accuracy, workspace (q4_tree_attention_workspace_bytes) and limits; an element
  * of a query may lose up to 2^-17 of its head's greatest one (which counts as
- * 2^-14 at least), and a head of a query with an infinity gives NaN.  What a row
- * does not see never reaches it: the NaN codes of new rows that it does not see
- * included. */
+ * 2^-14 at least), and an infinity in a head of a query counts as NaN: the head
+ * gets NaN unless it sees nothing.  What a row does not see never reaches it: the
+ * NaN codes of new rows that it does not see included. */
 typedef struct q4_tree_attention8_desc {
     q4_paged_cache8 cache;
     const int32_t *ctx_len, *row_start;

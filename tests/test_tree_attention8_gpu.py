@@ -480,3 +480,51 @@ def test_nan_among_every_lanes_columns_stays_in_its_column(name):
     got = first.cpu().numpy()[:b.rows].reshape(a.shape)
     assert np.array_equal(np.isnan(got), odd), np.argwhere(np.isnan(got) != odd)[:5]
     assert close(got, a, A, B)[~odd].all()
+
+
+# every form of the launch, with a sequence of one row and no cached positions
+QUERY_FORMS = {
+    "clusters": dict(ctx=[120, 0, 250], n=[2, 1, 2], Hkv=2, G=2, d=128, page=16),
+    "clusters, heads of 64": dict(ctx=[0, 700], n=[1, 3], Hkv=2, G=4, d=64, page=64),
+    "clusters, pages of 7": dict(ctx=[120, 0, 250], n=[2, 1, 2], Hkv=2, G=2, d=128, page=7),
+    "line": dict(ctx=[90, 0, 300, 17, 64] * 8, n=[1, 1, 3, 3, 1] * 8, Hkv=2, G=2, d=128, page=24),
+    "line, heads of 64": dict(ctx=[90, 0, 300, 17, 64] * 8, n=[1, 1, 3, 3, 1] * 8, Hkv=2, G=5, d=64, page=12),
+    "line, shared": dict(ctx=[9000, 0, 4000], n=[9, 1, 9], Hkv=2, G=4, d=128, page=16),
+    "tcgen05": dict(ctx=[300, 0, 129], n=[40, 1, 64], Hkv=2, G=4, d=128, page=16),
+    "tcgen05, heads of 64": dict(ctx=[300, 0, 129], n=[30, 1, 64], Hkv=2, G=4, d=64, page=7),
+    "tcgen05, 256 rows": dict(ctx=[300, 0, 0], n=[140, 1, 200], Hkv=1, G=4, d=128, page=16),
+    "tcgen05, shared": dict(ctx=[3000, 0], n=[40, 1], Hkv=1, G=4, d=128, page=16),
+}
+
+
+@pytest.mark.parametrize("kind", ["causal", "nothing"])
+@pytest.mark.parametrize("name", QUERY_FORMS)
+def test_queries_that_are_no_numbers_give_nan_in_every_form(name, kind):
+    # an infinity whose products are all of the other sign (every score -inf), all of its own, of both signs or none
+    # (a zero in each key), beside a NaN; a row of them that sees nothing gives zeros, and no other row is touched
+    f = QUERY_FORMS[name]
+    g = np.random.default_rng(80 + len(name))
+    b = batch(g, f["ctx"], f["n"], f["Hkv"], f["d"], f["page"])
+    for e, code in ((3, 0xB8), (8, 0x38), (21, 0x00)):  # -1, 1 and 0 in every key's element e
+        b.k8[..., e] = code
+    b.set_values()
+    q = rand16(g, b.rows, f["Hkv"] * f["G"], f["d"])
+    sees = seen_by(b, kind, g)
+    want = expected(b, q, sees)
+    odd = q.copy()
+    bad = np.zeros(odd.shape[:2], bool)
+    kinds = [(3, np.inf), (8, np.inf), (3, -np.inf), (8, -np.inf), (21, np.inf), (40, -np.inf), (63, np.nan), (f["d"] - 1, np.inf)]
+    for i, r in enumerate(range(0, b.rows, 2)):
+        for h in ((i * 3) % odd.shape[1], (i * 3 + 2) % odd.shape[1]):
+            e, x = kinds[(i + h) % len(kinds)]
+            odd[r, h, e], bad[r, h] = x, True
+    one = b.start[b.n.index(1)]  # the sequence of one row
+    odd[one, :, 3], bad[one] = np.inf, True
+    out = attend(b, b.to_device(q4), odd, kind, sees)
+    assert q4.q4_device_status() == 0
+    got = out.cpu().numpy()[:b.rows].reshape(want[0].shape)
+    looks = np.concatenate([m.any(1) | (c > 0) for m, c in zip(sees, b.ctx)])
+    assert looks.any() and (kind == "causal" or not looks.all())
+    assert np.isnan(got[bad & looks[:, None]]).all(), np.argwhere(~np.isnan(got).all(-1) & bad & looks[:, None])[:5]
+    assert not got[~looks].any()
+    assert close(got, *want)[~bad].all()

@@ -175,3 +175,9 @@ def test_codes_that_are_no_numbers_reach_who_sees_them(n, what):
 @pytest.mark.parametrize("name", ["128 rows", "shared"])
 def test_nan_among_every_lanes_columns(as_long, name):
     short.test_nan_among_every_lanes_columns_stays_in_its_column(name)
+
+
+@pytest.mark.parametrize("kind", ["causal", "nothing"])
+@pytest.mark.parametrize("name", ["tcgen05", "tcgen05, shared"])
+def test_queries_that_are_no_numbers(as_long, name, kind):
+    short.test_queries_that_are_no_numbers_give_nan_in_every_form(name, kind)
