@@ -497,3 +497,111 @@ def test_accept8_without_layers_moves_nothing_and_bad_pages_hold_nothing():
     after = b.from_device()
     for x, y in zip(want, after):
         assert np.array_equal(x.view(np.uint8), y.view(np.uint8))
+
+
+# ------------------------------------------------------------- scales that grow ---
+
+@pytest.mark.parametrize("d,page", [(64, 24), (128, 16), (128, 7), (64, 100)])
+def test_append8_twice_as_large_each_time(d, page):
+    # every token is twice the one before: a block that goes on takes twice its scale each time, in every head
+    g = np.random.default_rng(d + page)
+    S, H, steps = 11, 2, 20
+    ctx0 = [int(x) for x in g.integers(0, 60, S)]
+    b = Batch8(g, [0] * S, [c + steps for c in ctx0], H, d, page)  # (pages for all of it)
+    c = b.to_device(q4)
+    b.d8[2].fill_(2.0 ** -15)
+    b.d8[3].fill_(2.0 ** -15)
+    base = [rand16(g, S, H * d) for _ in range(2)]
+    base = [(x * np.float16(2.0 ** -12) + np.float16(2.0 ** -13) * np.sign(x)).astype(np.float16) for x in base]
+    base = [np.where(x == 0, np.float16(2.0 ** -13), x) for x in base]
+    for x in base:
+        assert 2.0 ** 20 * np.abs(x.astype(np.float64)).max() < 61440
+    b.n, b.rows = [1] * S, S
+    b.start = np.arange(S + 1, dtype=np.int32)
+    b.dstart.copy_(torch_dev(b.start))
+    grown = [0, 0]
+    for i in range(steps):
+        b.ctx = [x + i for x in ctx0]
+        b.dctx.copy_(torch_dev(np.array(b.ctx, np.int32)))
+        k, v = ((x.astype(np.float64) * 2.0 ** i).astype(np.float16) for x in base)
+        before = b.from_device()
+        q4.q4_paged_append8(c, b.dctx, b.dstart, S, torch_dev(k), torch_dev(v))
+        after = b.from_device()
+        check_append8(b, before, after, k.reshape(S, H, d).astype(np.float64), np.zeros((S, H, d)),
+                      v.reshape(S, H, d).astype(np.float64))
+        for s in range(S):
+            at = b.ctx[s] % page
+            if i == 0 or at % 16 == 0:
+                continue  # a block's first token, or one behind positions that this test has not stored
+            for j in range(2):
+                was, now = (x[2 + j][0, b.table[s, b.ctx[s] // page], :, at // 16] for x in (before, after))
+                low = now == 2.0 ** -15  # (the least scale holds for the first ones)
+                assert np.array_equal(now[~low], 2 * was[~low])
+                grown[j] += int((~low).sum())
+    assert q4.q4_device_status() == 0
+    assert min(grown) > S * steps  # of 2 S (steps - 1), less the blocks' first tokens and the least scales
+
+
+@pytest.mark.parametrize("d,Hkv,page,layers", [(128, 2, 16, 3), (64, 3, 32, 1), (64, 1, 48, 2)])
+def test_accept8_rows_from_blocks_of_greater_scales(d, Hkv, page, layers):
+    # positions 16 .. of each sequence are 32 times larger: rows that move from there into the first block of the new
+    # ones take it to their scale, and its other rows are rewritten
+    g = np.random.default_rng(7 + d)
+    ctx, n = [3, 10, 0], [40, 30, 64]
+    b = Batch8(g, ctx, n, Hkv, d, page, layers=layers, spread=0.2)
+    for s in range(3):
+        for p in range(16, ctx[s] + n[s], 16):
+            at = (slice(None), b.table[s, p // page], slice(None), p % page // 16)
+            b.k_scales[at] *= 32.0
+            b.v_scales[at] *= 32.0
+    c = b.to_device(q4)
+    draft, parents, sampled, paths = [], [], [], []
+    for s in range(3):
+        far = [20 + j for j in range(4)]  # 0 -> 20 -> 21 -> 22 -> 23: places 1 .. 4
+        p = [-1] + [0] * (n[s] - 1)
+        smp = [-1] * n[s]
+        for a, i in zip([0] + far, far):
+            p[i], smp[a] = a, i
+        draft, parents, sampled = draft + list(range(n[s])), parents + p, sampled + smp
+        paths.append([0] + far)
+    before = b.from_device()
+    acc = accept(b, c, draft, parents, sampled, layers, (b.k8[0].size, b.k_scales[0].size))[0]
+    assert q4.q4_device_status() == 0
+    assert acc.tolist() == [5, 5, 5]
+    want, after = [x.copy() for x in before], b.from_device()
+    for s in range(3):
+        for i in range(2):
+            oracle.cache8_accept(want[i], want[2 + i], b.table[s], ctx[s], n[s], paths[s])
+            block = (slice(None), b.table[s, 0], slice(None), 0)
+            assert np.all(after[2 + i][block] > before[2 + i][block])
+    for x, y in zip(want, after):
+        assert np.array_equal(x.view(np.uint8), y.view(np.uint8))
+
+
+def test_append_norm_past_32_bit_offsets():
+    # pools of more than 2^31 elements: the pages in use lie at the far end
+    d, Hq, Hkv, rot, page = 128, 4, 2, 128, 64
+    g, b, q, k, v, rotary, wq, wk = setup(Batch, (d, Hq, Hkv, rot, False, page), [200, 77, 0], [3, 1, 70], seed=6)
+    far = (1 << 31) // (Hkv * page * d) + 5  # pages before them
+    b.to_device(q4)
+    pools = []
+    for x in (b.k, b.v):
+        t = torch.empty((far + b.n_pages,) + x.shape[2:], dtype=torch.float16, device="cuda")
+        t[far:] = torch_dev(x[0])
+        pools.append(t)
+    table = torch_dev(np.where(b.table >= 0, b.table + far, -1).astype(np.int32))
+    c = q4.PagedCache(*pools, far + b.n_pages, page, Hkv, d, table, b.S, b.max_pages)
+    qo = call(q4.q4_paged_append_norm, b, c, q, k, v, Hq, rot, False, None, q4.HeadNorm(torch_dev(wq), torch_dev(wk), 1e-3))
+    assert q4.q4_device_status() == 0
+    turns = oracle.rope_turns(rot, 1e4)
+    check_q(qo, q, b, Hq, d, rotary, turns, False, True, wq, 1e-3)
+    want, err = wanted(k, Hkv, d, rotary, turns, False, True, wk, 1e-3)
+    got = [x[far:].cpu().numpy() for x in pools]
+    at = [b.ctx[s] + np.arange(m) for s, m in enumerate(b.n)]
+    new_k, new_v = (np.concatenate([b.rows_of(x, s, p) for s, p in enumerate(at)]) for x in got)
+    assert np.all(np.abs(new_k.astype(np.float64) - want) <= ulp16(want) / 2 + err)
+    assert np.array_equal(new_v, v.reshape(new_v.shape))
+    for pool, was in zip(got, (b.k[0], b.v[0])):
+        for s, p in enumerate(at):
+            was[b.table[s][p // page], :, p % page] = pool[b.table[s][p // page], :, p % page]
+        assert np.array_equal(pool.view(np.uint16), was.view(np.uint16))

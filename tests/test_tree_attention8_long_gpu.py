@@ -181,3 +181,17 @@ def test_nan_among_every_lanes_columns(as_long, name):
 @pytest.mark.parametrize("name", ["tcgen05", "tcgen05, shared"])
 def test_queries_that_are_no_numbers(as_long, name, kind):
     short.test_queries_that_are_no_numbers_give_nan_in_every_form(name, kind)
+
+
+@pytest.mark.parametrize("kind", ["causal", "tree"])
+@pytest.mark.parametrize("name", ["tcgen05, short", "tcgen05, shared"])
+def test_nan_reaches_what_sees_it(as_long, name, kind):
+    short.test_nan_reaches_what_sees_it_in_every_form(name, kind)
+
+
+def test_pages_past_32_bit_offsets(as_long):
+    short.test_pages_past_32_bit_offsets(64, [40, 3], 4)
+
+
+def test_bits_do_not_depend_on_the_run(as_long):
+    short.test_bits_do_not_depend_on_the_run()
