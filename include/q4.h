@@ -846,11 +846,14 @@ typedef struct q4_paged_read8_desc {
 q4_status q4_paged_read8(const q4_paged_read8_desc *desc, q4_stream_t stream);
 
 /* 9d. q4_tree_attention8 -- 7c over the 8-bit cache: its arguments, masks,
- * accuracy, workspace (q4_tree_attention_workspace_bytes) and limits; an element
+ * accuracy, workspace (q4_tree_attention_workspace_bytes) and errors; an element
  * of a query may lose up to 2^-17 of its head's greatest one (which counts as
  * 2^-14 at least), and an infinity in a head of a query counts as NaN: the head
  * gets NaN unless it sees nothing.  What a row does not see never reaches it: the
- * NaN codes of new rows that it does not see included. */
+ * NaN codes of new rows that it does not see included.  Here the 2^31 units of
+ * work from which on a call computes nothing and latches Q4_ERR_DEVICE_CHECK are
+ * of 12 positions of a kv head by a block of rows at least, and a block of rows
+ * (16 or 256 of a sequence and kv head) counts up to 48 of them besides. */
 typedef struct q4_tree_attention8_desc {
     q4_paged_cache8 cache;
     const int32_t *ctx_len, *row_start;

@@ -528,3 +528,28 @@ def test_queries_that_are_no_numbers_give_nan_in_every_form(name, kind):
     assert np.isnan(got[bad & looks[:, None]]).all(), np.argwhere(~np.isnan(got).all(-1) & bad & looks[:, None])[:5]
     assert not got[~looks].any()
     assert close(got, *want)[~bad].all()
+
+
+# sequences of 2^31 positions (one page, again and again): 4 units a tile of 128 positions for 16 rows, 10 (heads of
+# 128) and 7 (of 64) for up to 128, 5 with the keys as they are; the first number of sequences that makes 2^31 units
+@pytest.mark.parametrize("S,n,d,page", [(33, 1, 128, 1 << 22), (33, 9, 64, 1 << 22), (13, 64, 128, 8 * 499979), (19, 100, 64, 1 << 22),
+                                        (26, 60, 128, 1 << 22)])
+def test_calls_of_too_many_units_are_left_out(S, n, d, page):
+    pages = ((1 << 31) - 128) // page
+    codes = torch.zeros(1, 1, page, d, dtype=torch.uint8, device="cuda")
+    scales = torch.ones(1, 1, -(-page // 16), device="cuda")
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.zeros(S, pages, dtype=torch.int32, device="cuda")
+    c = q4.PagedCache8(codes, codes, scales, scales, 1, page, 1, d, table, S, pages)
+    q = torch.zeros(S * n, d, dtype=torch.float16, device="cuda")
+    out = torch.full_like(q, -5.0)
+    ws, size = workspace(d)
+    ctx = ints([page * pages - n] * S)
+    q4.q4_tree_attention8(c, ctx, ints([n * i for i in range(S + 1)]), S * n, q, 1, out, ws, size)
+    assert q4.q4_device_status() == -7
+    assert bool((out == -5.0).all())
+    # and the same call over less is computed
+    ctx.fill_(5)
+    q4.q4_tree_attention8(c, ctx, ints([n * i for i in range(S + 1)]), S * n, q, 1, out, ws, size)
+    assert q4.q4_device_status() == 0
+    assert not out.any()
