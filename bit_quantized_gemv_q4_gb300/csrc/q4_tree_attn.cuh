@@ -45,7 +45,11 @@ constexpr int kTcRows = 256, kMaxTcCtas = 160;
 // P = 2^(s - m + kShift): fp16 keeps 11 bits of a probability down to 2^-26
 // of the row's greatest (below, it is off by 2^-37 of that at most), and O / l
 // is the same quotient.  The tcgen05 kernel lets the greatest score exceed m by
-// kLag, so P reaches 2^15.
+// kLag, so P reaches 2^15, over the fp16 cache alone: a P that decides its row is
+// rounded then, but is 2^12 exactly where m is the greatest score.  8 bits with
+// and without a lag, error against 64 bits and time: the trees 2.09e-4 and 104.7
+// us / 2.02e-4 and 105.2 us, the chunks 2.16e-4 and 179 us / 2.05e-4 and 181 us
+// (rounding the outputs alone: 2.00e-4).
 constexpr float kShift = 12.f, kLag = 3.f;
 
 struct Args {
@@ -1482,7 +1486,7 @@ inline q4_status attention_args(Args& a, const uint32_t* mask, int mask_words, c
 // the commit behind S(k + 1) tells the softmax that O holds step k's product.
 // Tensor memory (512 columns): S 0 and 1 (128 each), O 0 and 1.
 // The reference maximum of a row moves only when its maximum exceeds it by
-// more than kLag (a factor 2^3); then O and l are rescaled.
+// more than kLag (a factor 2^3; 8 bits: at all); then O and l are rescaled.
 // Key and value tiles come by TMA as boxes of `box` rows (the greatest power
 // of two, 8 .. 128, that divides the page): a box lies in one page.  A page
 // that does not exist is read outside the map, where TMA fills in zeros.
@@ -2241,7 +2245,7 @@ __global__ void __launch_bounds__(kCache ? kTc8Threads : kTcThreads, 1)
                     if (kCache == 1 && top == -INFINITY && (!tail || seen)) l = NAN;
                     const float mx = top * (kRaw ? c_row : a.c);
                     float corr = 1.f;
-                    if (mx > m + kLag) {
+                    if (mx > (k8 ? m : m + kLag)) {
                         corr = m == -INFINITY ? 1.f : ex2(m - mx);  // nothing seen yet: O and l are zero
                         m = mx;
                     }

@@ -553,3 +553,36 @@ def test_calls_of_too_many_units_are_left_out(S, n, d, page):
     q4.q4_tree_attention8(c, ctx, ints([n * i for i in range(S + 1)]), S * n, q, 1, out, ws, size)
     assert q4.q4_device_status() == 0
     assert not out.any()
+
+
+@pytest.mark.parametrize("top", [2.25, 1.25])
+@pytest.mark.parametrize("n,G,d,page", [(1, 2, 128, 16), (3, 4, 64, 64), (20, 4, 128, 64), (20, 4, 64, 16), (60, 4, 128, 16),
+                                        (70, 4, 64, 24), (40, 2, 128, 7)])
+def test_a_position_that_decides_its_row_late(n, G, d, page, top):
+    # The first positions have scores of 0 (in units of log2) and no value, position 300 has `top` and a value, the others
+    # next to no weight: the probability of position 300, of which 2^top / 2^12 is far from an fp16 number, decides the
+    # row.  It is the row's greatest, so it enters the product as a power of two and is not rounded: what is left of
+    # close()'s bound are exp2, the sums, the scores and the rounding of the output.
+    g = np.random.default_rng(90)
+    S = 9
+    b = batch(g, [400] * S, [n] * S, 2, d, page)
+    at = np.arange(400 + n)
+    for s in range(S):
+        where = 0, b.table[s][at // page], slice(None), at % page
+        k = np.zeros((400 + n, 2, d))
+        k[..., 0] = -30.0
+        for h in range(2):
+            k[:1 + 3 * s + h, h, 0] = 0.0
+        k[300, :, 0] = top
+        b.k8[where] = oracle.e4m3_codes(k)
+        b.v8[where] = oracle.e4m3_codes(np.where((at < 40)[:, None, None], 0.0, 1 + g.random((400 + n, 2, d))))
+    b.k_scales[...] = b.v_scales[...] = 1.0
+    b.set_values()
+    q = np.zeros((b.rows, 2 * G, d), np.float16)
+    q[..., 0] = 1
+    sees = seen_by(b, "causal", g)
+    a, A, B = expected(b, q, sees, scale=np.log(2.0))
+    got = attend(b, b.to_device(q4), q, "causal", sees, scale=float(np.log(2.0))).cpu().numpy()[:b.rows].reshape(a.shape)
+    assert q4.q4_device_status() == 0
+    ok = np.abs(got.astype(np.float64) - a) <= (4e-5 + 2.0 ** -19 * B) * A + ulp16(a) / 2
+    assert ok.all(), (1 - ok.mean(), (np.abs(got - a) / a).max())

@@ -195,3 +195,9 @@ def test_pages_past_32_bit_offsets(as_long):
 
 def test_bits_do_not_depend_on_the_run(as_long):
     short.test_bits_do_not_depend_on_the_run()
+
+
+@pytest.mark.parametrize("top", [2.25, 1.25])
+@pytest.mark.parametrize("n,G,page", [(20, 4, 64), (40, 4, 16)])
+def test_a_position_that_decides_its_row_late(as_long, n, G, page, top):
+    short.test_a_position_that_decides_its_row_late(n, G, 128, page, top)
