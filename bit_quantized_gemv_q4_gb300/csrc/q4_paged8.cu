@@ -48,7 +48,9 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
 // What bounds it: the smallest calls the chain of look-ups (row, sequence, page,
 // cached scale), the largest bytes and that chain, which four blocks per SM do
 // not quite cover (issue slots 47 .. 54 % busy).  Measured, 32 query and 8 kv heads
-// of 128: one row with norms (16 query heads) 4.8 us, 40 rows into 8 bits 5.5;
+// of 128: one row with norms (16 query heads) 4.6 us, 40 rows into 8 bits 5.4
+// (10.2 where every one of their blocks takes a greater scale: up to 15 cached
+// rows rewritten one after another by the lanes of the block's first new row);
 // 6767 rows with norms into fp16 (166 MB in and out) 33.8 us = 4.9 TB/s, 72 % of
 // the measured copy rate, into 8 bits (152 MB) 38.6 = 3.9 TB/s, 58 %
 // (with three blocks per SM 38.0 and 39.0, with five 34.4 and 42.9).
@@ -499,7 +501,8 @@ __global__ void __launch_bounds__(kReadThreads, 6) read_kernel(const __grid_cons
 // gives up moves within that block: no later block reads what an earlier one
 // has written.  What bounds it: dependent loads (tree, path, page, scales, codes)
 // behind one another.  Measured, 28 layers of 8 heads of 128: one sequence of 16
-// rows 7.0 us, 32 sequences (1426 rows) 13.8.
+// rows 6.9 us, 32 sequences (1426 rows) 13.8 (8.0 and 16.6 where the scales of
+// one destination in ten grow, which a repeated call does not see).
 struct Accept8Args {
     View8 c;
     const int32_t *draft, *parents, *sampled;

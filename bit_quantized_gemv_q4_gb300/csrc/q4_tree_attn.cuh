@@ -12,12 +12,12 @@
 // and parts over different keys join the same way.
 //
 // What bounds it: up to a few dozen rows per kv head the bytes of the cache
-// (each read once: 4 D bytes per position and head), beyond that the
-// products.  The positions are the long axis, and there are often fewer
-// (sequence, head) pairs than SMs, so the work is cut by positions: every
-// (sequence, head, block of rows) is a job of 64-position tiles, all jobs'
-// tiles stand in one line, and the CTA c of C takes its C-th part of the
-// line.  A job that lies in one CTA's part is finished there; of a job that
+// (each read once: 4 D bytes per position and head, in 8 bits 2 D and half a
+// byte of scales), beyond that the products.  The positions are the long axis,
+// and there are often fewer (sequence, head) pairs than SMs, so the work is cut
+// by positions: every (sequence, head, block of rows) is a job of tiles (of 64
+// positions, on tcgen05 and on the line in 8 bits of 128), all jobs' tiles stand
+// in one line, and the CTA c of C takes its C-th part of the line.  A job that lies in one CTA's part is finished there; of a job that
 // several share, each leaves (m, l, O) in the workspace (at most two per CTA:
 // one job begun by another, one left unfinished), and a second kernel joins
 // them in the order of the CTAs, so the bits do not depend on timing.
@@ -231,7 +231,7 @@ struct Walk {
     unsigned x1;
     // false: the CTA has no tiles
     __device__ __forceinline__ bool begin(const Args& a, const unsigned* sums, int threads, unsigned line) {
-        const unsigned share = line_share(a, line), x0 = share * blockIdx.x;  // below 2^31 + 512 * cost
+        const unsigned share = line_share(a, line), x0 = share * blockIdx.x;  // below 2^31 + ctas (1024 at most) * 20: two tiles' cost
         x1 = min(line, x0 + share);
         if (x0 >= x1) return false;
         p = line_find(a, sums, threads, x0);
@@ -492,10 +492,15 @@ __device__ __forceinline__ void latch_bad(const Args& a) {
 // Half the bytes for the same products and more instructions: what bounds it
 // is issue and waits as much as the bytes, so three CTAs share an SM.  48
 // users' tokens over contexts up to 14000 (32 query heads on 8 of 128, 911 MB)
-// 175 us = 5.2 TB/s, 77 % of the measured copy rate, with pages of 64 165 us
+// 171 us = 5.3 TB/s, 78 % of the measured copy rate, with pages of 64 164 us
 // (of 16: more and smaller copies); two CTAs with three stages 232 us (before
-// the last 13).  The pages looked up a tile ahead brought nothing.  Heads of 64
-// leave room for four: 119 us against 139 with three (457 MB).
+// the last 17).  The pages looked up a tile ahead brought nothing.  Heads of 64
+// leave room for four: 119 us against 139 with three (457 MB = 3.8 TB/s: a tile
+// is half the bytes for as many waits, look-ups, scores and exponentials).
+// At 128 registers (heads of 64: 96) it spills, 276 bytes stored and 268 loaded
+// (116 / 164; by cp.async 264 / 256 and 152 / 252), in the tile loop too: the
+// five warps of a CTA load 47 and store 28 registers a tile in that batch (34
+// and 22).
 template <int D, bool k8>
 constexpr int kRingCtas = !k8 ? 2 : D == 64 ? 4 : 3;
 template <int D, int WM, bool kTma, bool kClustered, bool k8>
@@ -1511,6 +1516,7 @@ constexpr int kTcCostFull = 8, kTcCostHalf = 5, kTcLead = 32;
 // of the chunks and of 16 sequences up to 256 rows (6000 positions) with half a
 // tile at 5 / 8 / 10 / 11 : 8: 210 / 183 / 179 / 179, 308 / 284 / 280 / 282.  Heads
 // of 64: 1.5 against 1.8; at 6 / 8 / 10 : 8 137 / 138 / 139, 213 / 219 / 222.
+// (With m following at once, kLag above, the chunks are at 180, of heads of 64 at 140.)
 // Keys as they are (kCache 2): 1.5 us against 2.5; lead 16 / 32 / 48 / 64: 8 trees
 // of 61 up to 20000 positions 113 / 108 / 105 / 107.
 template <int D>
@@ -1683,8 +1689,9 @@ __device__ __noinline__ bool clean_row(uint8_t* tile, int row, bool all) {
 // What bounds it: the converting warps (some 2900 cycles for 32 positions: a
 // warp's instructions one after another, fetched anew beside the other roles')
 // where a tile has 128 rows, the softmax and the products where it has 256.
-// Measured, contexts and heads as above: the chunks 179 us (kCache 1), the trees
-// 105 us (kCache 2; 1 takes 119).  Keys and values by turns in one body; tried in
+// Measured, contexts and heads as above: the chunks 180 us (kCache 1), the trees
+// 104 us (kCache 2; 1 takes 119).  It spills 28 .. 44 bytes at 128 registers, outside
+// the loops over tiles (a warp loads 11 registers in the whole of the chunks).  Keys and values by turns in one body; tried in
 // kCache 1 (trees / chunks, before the tiles' costs were weighed: 150 / 215): a
 // warp that brings the slots of all 197 / 311, four converting warps 215 / 328,
 // five 148 / 237, pairs of a key and a value quarter 155 / 291, 16 positions at a

@@ -48,7 +48,17 @@ extern "C" q4_status q4_tree_attention8(const q4_tree_attention8_desc* desc, q4_
     //   117   436 / 184 / 68 / 40    173 / 96 / 49 / 33     217 / 93 / 47 / 29
     //   135   528 / 191 / 74 / 48    204 / 97 / 49 / 35     227 / 99 / 47 / 29
     //   175   698 / 215 / 93 / 53    214 / 104 / 55 / 33    192 / 94 / 50 / 29
-    // (jobs of 32 rows instead of 16, two CTAs per SM, were slower at all sizes)
+    // (jobs of 32 rows instead of 16, two CTAs per SM, were slower at all sizes; at
+    // 38 rows over 20000 positions the border of 48 is the slower side by a tenth)
+    // Heads of 64, jobs of 16 / keys fp16:
+    //   21    79 / 135, 28 / 50, 19 / 33, 14 / 20
+    //   39    105 / 125, 35 / 45, 26 / 31, 16 / 20
+    //   52    109 / 120, 54 / 56, 26 / 31, 18 / 20
+    //   78    164 / 132, 63 / 53, 29 / 31, 22 / 21
+    //   116   298 / 152, 106 / 65, 51 / 39, 26 / 24
+    // Sequences without rows count in the average, as the host does not see the
+    // sizes: 4 sequences of up to 64 rows over 6000 positions 40 us, among 60 idle
+    // places, in jobs of 16 rows, 91.
     if (avg > 48) {
         const int rows = even < 32 ? even : 32;
         const bool lengthy = (long long)d.cache.max_pages * d.cache.page_size >= 4096;

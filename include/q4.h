@@ -775,7 +775,7 @@ typedef struct q4_head_norm {
 } q4_head_norm;
 
 /* 9a. q4_paged_append (7b: its arguments, checks, outputs) with the norms in
- * the same pass.  norm NULL: none. */
+ * the same pass.  norm NULL: none (7b itself is the faster call then). */
 q4_status q4_paged_append_norm(const q4_paged_append_desc *desc, const q4_head_norm *norm, q4_stream_t stream);
 
 /* The cache of section 7 with keys and values as e4m3 codes.  The positions
