@@ -277,8 +277,8 @@ def _by_bytes(name: str):
     if _bytes_lib is None:
         lib()
         L = ctypes.CDLL(LIB_PATH)
-        for f, n in (("q4_paged_append_norm", 3), ("q4_paged_append8", 3), ("q4_paged_read8", 2), ("q4_tree_attention8", 2),
-                     ("q4_tree_accept8", 2)):
+        for f, n in (("q4_paged_append", 2), ("q4_tree_attention", 2), ("q4_tree_accept", 2), ("q4_paged_append_norm", 3),
+                     ("q4_paged_append8", 3), ("q4_paged_read8", 2), ("q4_tree_attention8", 2), ("q4_tree_accept8", 2)):
             getattr(L, f).argtypes, getattr(L, f).restype = [vp] * n, i32
         _bytes_lib = L
     return getattr(_bytes_lib, name)
@@ -642,9 +642,6 @@ class PagedCache:
         return (_arg(self.k, torch.float16, elements, dev, "cache.k"), _arg(self.v, torch.float16, elements, dev, "cache.v"),
                 _arg(self.page_table, torch.int32, s[4] * s[5], dev, "cache.page_table"), *s)
 
-    def _desc(self, torch, dev: int, elements: int) -> q4_paged_cache:
-        return q4_paged_cache(*self._fields(torch, dev, elements))
-
 
 def q4_rope_frequencies(freqs, rot_dim: int, theta: float = 1.0e6, factor: float = 1.0, orig_len: int = 0,
                         alpha: float = 1.0, beta: float = 32.0, stream=None):
@@ -670,12 +667,15 @@ def _append_fields(cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, p
             _arg(freqs, torch.int64, rot_dim // 2, dev, "freqs"), rot_dim, layout, amplitude)
 
 
-# The later calls' descriptors are packed as bytes, the structures' layout field
-# by field: a few microseconds less than building the structures.
+# The descriptors are packed as bytes, the structures' layout field by field: a
+# few microseconds less than building the structures.
 _CACHE, _CACHE8 = "PPP6i0P", "PPPPP6i0P"
-_APPEND_NORM = struct.Struct("@" + _CACHE + "PPiPPPiiPPiiiPiif0P")
+_APPEND = struct.Struct("@" + _CACHE + "PPiPPPiiPPiiiPiif0P")  # (with norms and without)
+_APPEND_NORM = _APPEND
 _APPEND8 = struct.Struct("@" + _CACHE8 + "PPiPPPiiPPiiiPiif0P")
 _NORM = struct.Struct("@iiPPf0P")
+_ATTENTION = struct.Struct("@" + _CACHE + "PPiPiPPiiifPN")
+_ACCEPT = struct.Struct("@" + _CACHE + "PPiPPPPPPPiN")
 _READ8 = struct.Struct("@" + _CACHE8 + "PPiPPii0P")
 _ATTENTION8 = struct.Struct("@" + _CACHE8 + "PPiPiPPiiifPN")
 _ACCEPT8 = struct.Struct("@" + _CACHE8 + "PPiPPPPPPPiNN")
@@ -687,10 +687,10 @@ def q4_paged_append(cache: PagedCache, ctx_len, row_start, rows: int, k, v, q=No
     """New rows' keys (rotated) and values into the paged cache, queries (rotated) into q_out."""
     torch = _get_torch()
     dev = _device(torch)
-    d = q4_paged_append_desc(cache._desc(torch, dev, cache.pool),
-                             *_append_fields(cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
-                                             rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev))
-    _check(lib().q4_paged_append(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_paged_append")
+    d = _APPEND.pack(*cache._fields(torch, dev, cache.pool),
+                     *_append_fields(cache, ctx_len, row_start, rows, k, v, q, q_out, n_q_heads, positions, freqs,
+                                     rot_dim, layout, amplitude, ldq, ldk, ldv, ldqo, torch, dev))
+    _check(_by_bytes("q4_paged_append")(d, _stream_of(torch, dev, stream)), "q4_paged_append")
 
 
 class HeadNorm:
@@ -746,10 +746,10 @@ def q4_tree_attention(cache: PagedCache, ctx_len, row_start, rows: int, q, n_q_h
     """Attention of the new rows over the cached positions and, by the mask (None: causal), their own."""
     torch = _get_torch()
     dev = _device(torch)
-    d = q4_tree_attention_desc(cache._desc(torch, dev, cache.pool),
-                               *_attention_fields(cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace,
-                                                  workspace_bytes, mask, mask_words, scale, ldq, ldo, torch, dev))
-    _check(lib().q4_tree_attention(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_attention")
+    d = _ATTENTION.pack(*cache._fields(torch, dev, cache.pool),
+                        *_attention_fields(cache, ctx_len, row_start, rows, q, n_q_heads, out, workspace, workspace_bytes,
+                                           mask, mask_words, scale, ldq, ldo, torch, dev))
+    _check(_by_bytes("q4_tree_attention")(d, _stream_of(torch, dev, stream)), "q4_tree_attention")
 
 
 def _accept_fields(cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path, next_token, ctx_out, torch, dev):
@@ -768,10 +768,10 @@ def q4_tree_accept(cache: PagedCache, ctx_len, row_start, rows: int, draft, pare
     torch = _get_torch()
     dev = _device(torch)
     elements = (n_layers - 1) * layer_stride + cache.pool if n_layers > 0 else 0
-    d = q4_tree_accept_desc(cache._desc(torch, dev, elements),
-                            *_accept_fields(cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path,
-                                            next_token, ctx_out, torch, dev), n_layers, layer_stride)
-    _check(lib().q4_tree_accept(ctypes.byref(d), _stream_of(torch, dev, stream)), "q4_tree_accept")
+    d = _ACCEPT.pack(*cache._fields(torch, dev, elements),
+                     *_accept_fields(cache, ctx_len, row_start, rows, draft, parents, sampled, accepted, path, next_token,
+                                     ctx_out, torch, dev), n_layers, layer_stride)
+    _check(_by_bytes("q4_tree_accept")(d, _stream_of(torch, dev, stream)), "q4_tree_accept")
 
 
 class PagedCache8:

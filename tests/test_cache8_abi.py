@@ -189,3 +189,40 @@ def test_binding_checks_its_tensors(L):
         q4.q4_paged_append8(c, FAKE, FAKE, 4, FAKE, FAKE, norm=q4.HeadNorm(eps=-1.0))
     with pytest.raises(q4.Q4Error, match="NO_DEVICE"):
         q4.q4_tree_attention8(c, FAKE, FAKE, 4, FAKE, 4, FAKE, FAKE, 1 << 30)
+
+
+@pytest.mark.parametrize("packed,kind", [("_APPEND", "q4_paged_append_desc"), ("_ATTENTION", "q4_tree_attention_desc"),
+                                         ("_ACCEPT", "q4_tree_accept_desc")])
+def test_packed_descriptors_of_the_fp16_cache_are_the_structures(packed, kind):
+    values = []
+
+    def build(t):
+        out = t()
+        for f, ty in t._fields_:
+            if issubclass(ty, ctypes.Structure):
+                setattr(out, f, build(ty))
+                continue
+            values.append(0.5 * len(values) + 0.5 if ty is ctypes.c_float else 1000 * len(values) + 7)
+            setattr(out, f, values[-1])
+        return out
+
+    want = build(getattr(q4, kind))
+    assert getattr(q4, packed).pack(*values) == bytes(want)
+
+
+def test_binding_of_the_fp16_cache_passes_its_arguments_on(L):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        return  # (the addresses below are nobody's)
+    c = q4.PagedCache(FAKE, FAKE, 8, 16, 2, 128, FAKE, 2, 4)
+    append = lambda **kw: q4.q4_paged_append(c, FAKE, FAKE, 4, FAKE, FAKE, **kw)  # noqa: E731
+    for match, call in (("NO_DEVICE", append), ("NULL", lambda: append(q=FAKE)), ("amplitude", lambda: append(amplitude=-1.0)),
+                        ("layout", lambda: append(layout=5)),
+                        ("NO_DEVICE", lambda: q4.q4_tree_attention(c, FAKE, FAKE, 4, FAKE, 4, FAKE, FAKE, 1 << 30)),
+                        ("workspace", lambda: q4.q4_tree_attention(c, FAKE, FAKE, 4, FAKE, 4, FAKE, FAKE, 1 << 10)),
+                        ("multiple", lambda: q4.q4_tree_attention(c, FAKE, FAKE, 4, FAKE, 3, FAKE, FAKE, 1 << 30)),
+                        ("NO_DEVICE", lambda: q4.q4_tree_accept(c, FAKE, FAKE, 4, *[FAKE] * 7)),
+                        ("layer_stride", lambda: q4.q4_tree_accept(c, FAKE, FAKE, 4, *[FAKE] * 7, n_layers=2, layer_stride=8)),
+                        ("n_layers", lambda: q4.q4_tree_accept(c, FAKE, FAKE, 4, *[FAKE] * 7, n_layers=-1))):
+        with pytest.raises(q4.Q4Error, match=match):
+            call()
